@@ -426,6 +426,118 @@ kvq_status attn_train_donor_forward(const kvq_layer* layer, int32_t n_blocks, co
 size_t attn_train_workspace_bytes(const kvq_layer* layer, int32_t n_rows);
 
 /*
+ * attn_train_forward_lse, attn_train_donor_forward_lse -- attn_train_forward
+ * and attn_train_donor_forward that also keep what the backward pass needs of
+ * the softmax: lse[r][h] = log sum_j exp(q_hat[r][h] . k_hat_j) over the keys
+ * the row sees (natural logarithm, summed in fp32 before P is rounded).
+ * Everything else is written as by those calls, bit for bit.
+ *
+ *   lse             device fp32 [n_rows][n_q_heads]
+ *   other arguments as for attn_train_forward / attn_train_donor_forward; a
+ *                   training step keeps q_prepped (q_hat) and out as fp32
+ */
+kvq_status attn_train_forward_lse(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                                  int32_t n_rows, int32_t max_block_rows,
+                                  const uint16_t* q_raw, const uint16_t* q_norm_w,
+                                  const uint16_t* k_hat, const uint16_t* v_hat,
+                                  void* out, int32_t out_is_f32, uint16_t* q_prepped, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+kvq_status attn_train_donor_forward_lse(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                                        int32_t n_rows, int32_t max_block_rows, const uint16_t* q_raw,
+                                        const uint16_t* k_raw, const uint16_t* v_raw,
+                                        const uint16_t* q_norm_w, const uint16_t* k_norm_w,
+                                        uint16_t* k_hat, uint16_t* v_hat,
+                                        void* out, int32_t out_is_f32, uint16_t* q_prepped, float* lse,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_train_backward -- the gradient of the training read (attn_train_forward
+ * as a function of q_hat, k_hat and v_hat) under the same layout.  The
+ * probabilities are recomputed from lse; nothing of size rows x keys is kept
+ * between the passes.  With d_out the gradient of out, over the keys j that
+ * row i sees:
+ *   P_ij  = exp(q_hat_i . k_hat_j - lse_i)
+ *   dS_ij = P_ij (d_out_i . v_hat_j - d_out_i . out_i)     (0 for a row that sees one key)
+ *   dq_hat_i = sum_j dS_ij k_hat_j
+ *   dk_hat_j = sum_i dS_ij q_hat_i,  dv_hat_j = sum_i P_ij d_out_i
+ * the last two over every row i that sees j and every q head of j's kv head.
+ * Sums are fp32 in an order that depends on the arguments alone (the same call
+ * gives the same bits); P and dS enter the products as bf16.
+ *
+ *   max_block_rows   host upper bound of the rows of every block, 1 .. n_rows (a
+ *                    longer block makes the layout invalid, below)
+ *   q_hat            device bf16 [n_rows][n_q_heads][head_dim] (16-byte aligned): the
+ *                    forward's q_prepped
+ *   k_hat, v_hat     device bf16 [n_rows][n_kv_heads][head_dim] (16-byte aligned)
+ *   out              device [n_rows][n_q_heads][head_dim], as the forward wrote it; fp32
+ *                    if out_is_f32, else bf16 (whose rounding, 2^-8 of out, then shows in
+ *                    dS: give fp32 where rows are sharp, d_out . v close to d_out . out)
+ *   lse              device fp32 [n_rows][n_q_heads], from attn_train_forward_lse
+ *   d_out            device bf16 [n_rows][n_q_heads][head_dim] (16-byte aligned)
+ *   dq_hat           device bf16 [n_rows][n_q_heads][head_dim], written
+ *   dk_hat, dv_hat   device [n_rows][n_kv_heads][head_dim]: bf16 when dkv_is_f32 == 0
+ *                    (written), fp32 when 1; with accumulate == 1 (fp32 only) the
+ *                    gradients are added to what is there, so that a donor's buffers
+ *                    collect those of the layers that read its keys and values
+ *   workspace        device scratch of at least attn_train_backward_workspace_bytes(...)
+ *                    bytes; its first 4 bytes receive the status word
+ * All inputs must be finite; the outputs must not overlap the inputs or each other.
+ * A layout that breaks the rules above (or has a block longer than
+ * max_block_rows) leaves every output as it was and sets
+ * KVQ_STATUS_SEQ_SKIPPED.  n_q_heads / n_kv_heads must divide 128.
+ */
+kvq_status attn_train_backward(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                               int32_t n_rows, int32_t max_block_rows,
+                               const uint16_t* q_hat, const uint16_t* k_hat, const uint16_t* v_hat,
+                               const void* out, int32_t out_is_f32, const float* lse, const uint16_t* d_out,
+                               uint16_t* dq_hat, void* dk_hat, void* dv_hat, int32_t dkv_is_f32,
+                               int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* 0 for an invalid layer or count; never less for more rows. */
+size_t attn_train_backward_workspace_bytes(const kvq_layer* layer, int32_t n_blocks, int32_t n_rows,
+                                           int32_t max_block_rows);
+
+/*
+ * kvq_train_prep_backward -- the gradient of the training preps (the q prep of
+ * the read and kvq_train_kv_prep): per head the RMS norm's and, for q and k,
+ * the rotation's, in one pass.  With r = 1 / sqrt(mean(x^2) + eps) of a raw row
+ * x at layout position p, weight w and the prepped row's gradient dz:
+ *   dy = R_p^T dz,  dx = r w dy - x r^3 mean(w dy x),  dw = sum over rows and heads of dy x r
+ * (v: w = 1, no rotation, no dw).  On a layer with k_eq_v, dk_raw is the
+ * gradient of the shared raw rows through both norms.  The forward's roundings
+ * to bf16 pass the gradient through.
+ *
+ *   q_raw, q_norm_w, dq_hat, dq_raw, dq_norm_w   the q side, or all NULL:
+ *       q_raw, dq_hat, dq_raw   device bf16 [n_rows][n_q_heads][head_dim] (16-byte aligned)
+ *       q_norm_w                device bf16 [head_dim];  dq_norm_w  device fp32 [head_dim]
+ *   k_raw, v_raw, k_norm_w, dk_hat, dv_hat, dk_raw, dv_raw, dk_norm_w   the side of a
+ *       donor's keys and values, or all NULL (a KV-sharing layer):
+ *       k_raw, v_raw, dk_raw, dv_raw   device bf16 [n_rows][n_kv_heads][head_dim] (16-byte
+ *                                      aligned); v_raw and dv_raw NULL iff k_eq_v
+ *       dk_hat, dv_hat                 the same shape (16-byte aligned), fp32 if dkv_is_f32
+ *                                      else bf16, as attn_train_backward leaves them
+ *       k_norm_w                       device bf16 [head_dim];  dk_norm_w  device fp32 [head_dim]
+ *   workspace   device scratch of at least kvq_train_prep_backward_workspace_bytes(layer,
+ *               n_rows) bytes; its first 4 bytes receive the status word
+ * dq_norm_w and dk_norm_w are written (not added to), summed in fp32 in an
+ * order that depends on the arguments alone; with n_rows == 0 nothing is
+ * written.  An output may be the buffer of the gradient it comes from (dq_raw
+ * == dq_hat; dk_raw == dk_hat and dv_raw == dv_hat when those are bf16), else
+ * outputs must not overlap inputs or each other.  A layout that breaks the
+ * rules above leaves every output as it was and sets KVQ_STATUS_SEQ_SKIPPED.
+ */
+kvq_status kvq_train_prep_backward(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                                   int32_t n_rows, const uint16_t* q_raw, const uint16_t* q_norm_w,
+                                   const uint16_t* dq_hat, uint16_t* dq_raw, float* dq_norm_w,
+                                   const uint16_t* k_raw, const uint16_t* v_raw, const uint16_t* k_norm_w,
+                                   const void* dk_hat, const void* dv_hat, int32_t dkv_is_f32,
+                                   uint16_t* dk_raw, uint16_t* dv_raw, float* dk_norm_w,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+size_t kvq_train_prep_backward_workspace_bytes(const kvq_layer* layer, int32_t n_rows);
+
+/*
  * attn_decode_static -- attn_decode without a caller-provided workspace, for
  * callers that cannot allocate device memory: code that only receives input
  * and output pointers from a host framework that owns every allocation (a

@@ -535,3 +535,77 @@ def train_attend(layer, q_raw, q_w, k_hat, v_hat, block_offsets, rows=None):
             out[kvh * G:(kvh + 1) * G] = attend(q_hat[r, kvh * G:(kvh + 1) * G], k_hat[vis, kvh], v_hat[vis, kvh])
         outs[r] = out
     return q_hat, outs
+
+
+# ----------------------------------------------------------------------------
+# gradients of the training read and of the preps (a rounding to bf16 in the
+# forward passes its gradient through unchanged)
+# ----------------------------------------------------------------------------
+
+def train_mask(block_offsets, window: int) -> np.ndarray:
+    """[T, T] truth values: packed row r reads packed row j."""
+    block, pos = layout_positions(block_offsets)
+    see = ((block[None, :] == block[:, None]) | (block[None, :] == 0)) & (pos[None, :] <= pos[:, None])
+    if window > 0:
+        see &= pos[None, :] > pos[:, None] - window
+    return see
+
+
+def train_attend_backward(layer, q_hat, k_hat, v_hat, d_out, block_offsets):
+    """The training read of q_hat [T, Hq, D], k_hat and v_hat [T, Hkv, D] and
+    its gradient for the output gradient d_out [T, Hq, D].  Returns a dict:
+    lse [T, Hq], out [T, Hq, D], dq, dk, dv, and per kv head the matrices
+    "p" and "ds" [T, G, T] the sums are made of."""
+    q, k, v, do = (np.asarray(x, dtype=np.float64) for x in (q_hat, k_hat, v_hat, d_out))
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    G = Hq // Hkv
+    see = train_mask(block_offsets, layer.window)
+    r = {"lse": np.zeros((T, Hq)), "out": np.zeros_like(q), "dq": np.zeros_like(q), "dk": np.zeros_like(k),
+         "dv": np.zeros_like(v), "p": [], "ds": []}
+    for kvh in range(Hkv):
+        ps, dss = [], []
+        for h in range(kvh * G, (kvh + 1) * G):
+            s = np.where(see, q[:, h] @ k[:, kvh].T, -np.inf)
+            m = s.max(axis=1, keepdims=True)
+            e = np.exp(s - m)
+            z = e.sum(axis=1, keepdims=True)
+            p = e / z
+            dp = do[:, h] @ v[:, kvh].T
+            ds = p * (dp - (p * dp).sum(axis=1, keepdims=True))
+            r["lse"][:, h] = (m + np.log(z))[:, 0]
+            r["out"][:, h] = p @ v[:, kvh]
+            r["dq"][:, h] = ds @ k[:, kvh]
+            r["dk"][:, kvh] += ds.T @ q[:, h]
+            r["dv"][:, kvh] += p.T @ do[:, h]
+            ps.append(p)
+            dss.append(ds)
+        r["p"].append(np.stack(ps, axis=1))
+        r["ds"].append(np.stack(dss, axis=1))
+    return r
+
+
+def unrope(dz: np.ndarray, pos: np.ndarray, theta: float, rope_dims: int) -> np.ndarray:
+    """The gradient of `rope`'s input: rows dz [T, H, D] turned back by their
+    angles (the transposed rotation), not rounded."""
+    dz = np.asarray(dz, dtype=np.float64)
+    half, R = rope_dims // 2, rope_dims
+    if half == 0:
+        return dz.copy()
+    hi, lo = rope_angle(pos, rope_inv_freq(theta, dz.shape[-1], R))
+    turn = (np.exp(1j * hi) * np.exp(1j * lo))[:, None, :]
+    c, s = turn.real, turn.imag
+    dy = dz.copy()
+    dy[..., :half] = dz[..., :half] * c + dz[..., half:R] * s
+    dy[..., half:R] = dz[..., half:R] * c - dz[..., :half] * s
+    return dy
+
+
+def rms_norm_backward(x: np.ndarray, w: np.ndarray | None, dy: np.ndarray, eps: float):
+    """Gradients of y = x r w, r = 1 / sqrt(mean(x^2) + eps), over the last
+    axis: (dx, dw) with dw summed over every row (not rounded)."""
+    x, dy = np.asarray(x, dtype=np.float64), np.asarray(dy, dtype=np.float64)
+    r = 1.0 / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + float(eps))
+    g = dy if w is None else dy * np.asarray(w, dtype=np.float64)
+    dx = r * g - x * r ** 3 * np.mean(g * x, axis=-1, keepdims=True)
+    return dx, (dy * x * r).reshape(-1, x.shape[-1]).sum(axis=0)

@@ -90,6 +90,20 @@ def _load():
     lib.attn_train_donor_forward.argtypes = [lay, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp,
                                              sz, vp]
     lib.attn_train_donor_forward.restype = ctypes.c_int
+    lib.attn_train_forward_lse.argtypes = [lay, i32, vp, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    lib.attn_train_forward_lse.restype = ctypes.c_int
+    lib.attn_train_donor_forward_lse.argtypes = [lay, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp,
+                                                 vp, sz, vp]
+    lib.attn_train_donor_forward_lse.restype = ctypes.c_int
+    lib.attn_train_backward.argtypes = [lay, i32, vp, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, vp,
+                                        sz, vp]
+    lib.attn_train_backward.restype = ctypes.c_int
+    lib.attn_train_backward_workspace_bytes.argtypes = [lay, i32, i32, i32]
+    lib.attn_train_backward_workspace_bytes.restype = sz
+    lib.kvq_train_prep_backward.argtypes = [lay, i32, vp, i32] + [vp] * 10 + [i32] + [vp] * 4 + [sz, vp]
+    lib.kvq_train_prep_backward.restype = ctypes.c_int
+    lib.kvq_train_prep_backward_workspace_bytes.argtypes = [lay, i32]
+    lib.kvq_train_prep_backward_workspace_bytes.restype = sz
     lib.attn_train_workspace_bytes.argtypes = [lay, i32]
     lib.attn_train_workspace_bytes.restype = sz
     lib.kvq_static_status.argtypes = [vp, vp]
@@ -256,6 +270,58 @@ def attn_train_forward(layer: KvqLayer, n_blocks, block_offsets, n_rows, max_blo
                                   _ptr(q_raw), _ptr(q_norm_w), _ptr(k_hat), _ptr(v_hat), _ptr(out),
                                   int(out_is_f32), _ptr(q_prepped), _ptr(workspace), workspace_bytes,
                                   _stream(stream)))
+
+
+def attn_train_forward_lse(layer: KvqLayer, n_blocks, block_offsets, n_rows, max_block_rows, q_raw, q_norm_w,
+                           k_hat, v_hat, out, out_is_f32, q_prepped, lse, workspace, workspace_bytes, stream=None):
+    """attn_train_forward that also writes each row's log-sum-exp for the
+    backward pass (see include/kvq.h)."""
+    _check(lib.attn_train_forward_lse(ctypes.byref(layer), n_blocks, _ptr(block_offsets), n_rows, max_block_rows,
+                                      _ptr(q_raw), _ptr(q_norm_w), _ptr(k_hat), _ptr(v_hat), _ptr(out),
+                                      int(out_is_f32), _ptr(q_prepped), _ptr(lse), _ptr(workspace), workspace_bytes,
+                                      _stream(stream)))
+
+
+def attn_train_donor_forward_lse(layer: KvqLayer, n_blocks, block_offsets, n_rows, max_block_rows, q_raw, k_raw,
+                                 v_raw, q_norm_w, k_norm_w, k_hat, v_hat, out, out_is_f32, q_prepped, lse, workspace,
+                                 workspace_bytes, stream=None):
+    """attn_train_donor_forward that also writes each row's log-sum-exp (see
+    include/kvq.h)."""
+    _check(lib.attn_train_donor_forward_lse(ctypes.byref(layer), n_blocks, _ptr(block_offsets), n_rows,
+                                            max_block_rows, _ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(q_norm_w),
+                                            _ptr(k_norm_w), _ptr(k_hat), _ptr(v_hat), _ptr(out), int(out_is_f32),
+                                            _ptr(q_prepped), _ptr(lse), _ptr(workspace), workspace_bytes,
+                                            _stream(stream)))
+
+
+def attn_train_backward(layer: KvqLayer, n_blocks, block_offsets, n_rows, max_block_rows, q_hat, k_hat, v_hat, out,
+                        out_is_f32, lse, d_out, dq_hat, dk_hat, dv_hat, dkv_is_f32, accumulate, workspace,
+                        workspace_bytes, stream=None):
+    """The training read's gradient by q_hat, k_hat and v_hat (see include/kvq.h)."""
+    _check(lib.attn_train_backward(ctypes.byref(layer), n_blocks, _ptr(block_offsets), n_rows, max_block_rows,
+                                   _ptr(q_hat), _ptr(k_hat), _ptr(v_hat), _ptr(out), int(out_is_f32), _ptr(lse),
+                                   _ptr(d_out), _ptr(dq_hat), _ptr(dk_hat), _ptr(dv_hat), int(dkv_is_f32),
+                                   int(accumulate), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def attn_train_backward_workspace_bytes(layer: KvqLayer, n_blocks, n_rows, max_block_rows) -> int:
+    return lib.attn_train_backward_workspace_bytes(ctypes.byref(layer), n_blocks, n_rows, max_block_rows)
+
+
+def kvq_train_prep_backward(layer: KvqLayer, n_blocks, block_offsets, n_rows, q_raw, q_norm_w, dq_hat, dq_raw,
+                            dq_norm_w, k_raw, v_raw, k_norm_w, dk_hat, dv_hat, dkv_is_f32, dk_raw, dv_raw, dk_norm_w,
+                            workspace, workspace_bytes, stream=None):
+    """The gradient of the q, k and v preps (norms and rotation); either side's
+    arguments may all be None (see include/kvq.h)."""
+    _check(lib.kvq_train_prep_backward(ctypes.byref(layer), n_blocks, _ptr(block_offsets), n_rows, _ptr(q_raw),
+                                       _ptr(q_norm_w), _ptr(dq_hat), _ptr(dq_raw), _ptr(dq_norm_w), _ptr(k_raw),
+                                       _ptr(v_raw), _ptr(k_norm_w), _ptr(dk_hat), _ptr(dv_hat), int(dkv_is_f32),
+                                       _ptr(dk_raw), _ptr(dv_raw), _ptr(dk_norm_w), _ptr(workspace),
+                                       workspace_bytes, _stream(stream)))
+
+
+def kvq_train_prep_backward_workspace_bytes(layer: KvqLayer, n_rows) -> int:
+    return lib.kvq_train_prep_backward_workspace_bytes(ctypes.byref(layer), n_rows)
 
 
 def attn_train_workspace_bytes(layer: KvqLayer, n_rows) -> int:

@@ -811,49 +811,26 @@ size_t attn_train_workspace_bytes(const kvq_layer* layer, int32_t n_rows) {
   return kvq::train_ws_bytes(n_rows, L);
 }
 
-kvq_status attn_train_forward(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets, int32_t n_rows,
-                              int32_t max_block_rows, const uint16_t* q_raw, const uint16_t* q_norm_w,
-                              const uint16_t* k_hat, const uint16_t* v_hat, void* out, int32_t out_is_f32,
-                              uint16_t* q_prepped, void* workspace, size_t workspace_bytes, void* stream) {
-  kvq::LayerArgs L;
-  kvq_status st = check_train_layer(layer, &L);
-  if (st != KVQ_OK) return st;
-  if (!kvq::train_supported(L))
-    return fail(KVQ_EUNSUPPORTED, "training read: n_q_heads / n_kv_heads = %d must divide 128", L.G);
-  if ((st = check_layout(n_blocks, block_offsets, n_rows)) != KVQ_OK) return st;
-  if (n_rows == 0) return KVQ_OK;
-  if (max_block_rows < 1 || max_block_rows > n_rows)
-    return fail(KVQ_EINVAL, "max_block_rows %d not in [1, n_rows]", max_block_rows);
-  REQUIRE_PTR(q_raw, "q_raw", 16);
-  REQUIRE_PTR(q_norm_w, "q_norm_w", 2);
-  REQUIRE_PTR(k_hat, "k_hat", 16);
-  REQUIRE_PTR(v_hat, "v_hat", 16);
-  REQUIRE_PTR(out, "out", out_is_f32 ? 4 : 2);
-  REQUIRE_PTR(workspace, "workspace", 256);
-  if (q_prepped && !aligned(q_prepped, 2)) return fail(KVQ_EINVAL, "q_prepped is not 2-byte aligned");
-  if (out_is_f32 != 0 && out_is_f32 != 1) return fail(KVQ_EINVAL, "out_is_f32 must be 0 or 1");
-  const size_t need = kvq::train_ws_bytes(n_rows, L);
-  if (workspace_bytes < need) return fail(KVQ_EWORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
-  kvq::TrainArgs t = {};
-  t.L = L;
-  t.n_rows = n_rows;
-  t.n_blocks = n_blocks;
-  t.off = block_offsets;
-  t.out = out;
-  t.out_f32 = out_is_f32;
-  const kvq::RopeFreqs& f = rope_freqs(layer->rope_theta, L.D, L.rope_dims);
-  const cudaError_t e = kvq::launch_train(t, q_raw, q_norm_w, k_hat, v_hat, q_prepped, workspace, max_block_rows, f,
-                                          static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "attn_train_forward launch");
-  return KVQ_OK;
-}
+}  // extern "C"
 
-kvq_status attn_train_donor_forward(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
-                                    int32_t n_rows, int32_t max_block_rows, const uint16_t* q_raw,
-                                    const uint16_t* k_raw, const uint16_t* v_raw, const uint16_t* q_norm_w,
-                                    const uint16_t* k_norm_w, uint16_t* k_hat, uint16_t* v_hat, void* out,
-                                    int32_t out_is_f32, uint16_t* q_prepped, void* workspace,
-                                    size_t workspace_bytes, void* stream) {
+namespace {
+
+// A donor's raw keys and values, prepped in the call.
+struct DonorKv {
+  const uint16_t* k_raw;
+  const uint16_t* v_raw;
+  const uint16_t* k_norm_w;
+  uint16_t* k_hat;
+  uint16_t* v_hat;
+};
+
+// The training read of every entry point: kv non-NULL preps a donor's keys
+// and values first, lse non-NULL receives the rows' log-sum-exp.
+kvq_status train_forward(const char* what, const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                         int32_t n_rows, int32_t max_block_rows, const uint16_t* q_raw, const uint16_t* q_norm_w,
+                         const uint16_t* k_hat, const uint16_t* v_hat, void* out, int32_t out_is_f32,
+                         uint16_t* q_prepped, float* lse, void* workspace, size_t workspace_bytes, void* stream,
+                         const DonorKv* kv) {
   kvq::LayerArgs L;
   kvq_status st = check_train_layer(layer, &L);
   if (st != KVQ_OK) return st;
@@ -865,12 +842,14 @@ kvq_status attn_train_donor_forward(const kvq_layer* layer, int32_t n_blocks, co
     return fail(KVQ_EINVAL, "max_block_rows %d not in [1, n_rows]", max_block_rows);
   REQUIRE_PTR(q_raw, "q_raw", 16);
   REQUIRE_PTR(q_norm_w, "q_norm_w", 2);
-  REQUIRE_PTR(k_raw, "k_raw", 16);
-  REQUIRE_PTR(k_norm_w, "k_norm_w", 2);
-  if (L.k_eq_v) {
-    if (v_raw) return fail(KVQ_EINVAL, "v_raw must be NULL when k_eq_v = 1");
-  } else {
-    REQUIRE_PTR(v_raw, "v_raw", 16);
+  if (kv) {
+    REQUIRE_PTR(kv->k_raw, "k_raw", 16);
+    REQUIRE_PTR(kv->k_norm_w, "k_norm_w", 2);
+    if (L.k_eq_v) {
+      if (kv->v_raw) return fail(KVQ_EINVAL, "v_raw must be NULL when k_eq_v = 1");
+    } else {
+      REQUIRE_PTR(kv->v_raw, "v_raw", 16);
+    }
   }
   REQUIRE_PTR(k_hat, "k_hat", 16);
   REQUIRE_PTR(v_hat, "v_hat", 16);
@@ -881,17 +860,19 @@ kvq_status attn_train_donor_forward(const kvq_layer* layer, int32_t n_blocks, co
   const size_t need = kvq::train_ws_bytes(n_rows, L);
   if (workspace_bytes < need) return fail(KVQ_EWORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
   kvq::AppendArgs ap = {};
-  ap.L = L;
-  ap.seqs = nullptr;
-  ap.n_seqs = n_blocks;
-  ap.row_offsets = block_offsets;
-  ap.start_pos = nullptr;
-  ap.n_rows = n_rows;
-  ap.k_raw = k_raw;
-  ap.v_raw = v_raw;
-  ap.k_w = k_norm_w;
-  ap.out_k = k_hat;
-  ap.out_v = v_hat;
+  if (kv) {
+    ap.L = L;
+    ap.seqs = nullptr;
+    ap.n_seqs = n_blocks;
+    ap.row_offsets = block_offsets;
+    ap.start_pos = nullptr;
+    ap.n_rows = n_rows;
+    ap.k_raw = kv->k_raw;
+    ap.v_raw = kv->v_raw;
+    ap.k_w = kv->k_norm_w;
+    ap.out_k = kv->k_hat;
+    ap.out_v = kv->v_hat;
+  }
   kvq::TrainArgs t = {};
   t.L = L;
   t.n_rows = n_rows;
@@ -899,10 +880,197 @@ kvq_status attn_train_donor_forward(const kvq_layer* layer, int32_t n_blocks, co
   t.off = block_offsets;
   t.out = out;
   t.out_f32 = out_is_f32;
+  t.lse = lse;
   const kvq::RopeFreqs& f = rope_freqs(layer->rope_theta, L.D, L.rope_dims);
   const cudaError_t e = kvq::launch_train(t, q_raw, q_norm_w, k_hat, v_hat, q_prepped, workspace, max_block_rows, f,
-                                          static_cast<cudaStream_t>(stream), &ap);
-  if (e != cudaSuccess) return cuda_fail(e, "attn_train_donor_forward launch");
+                                          static_cast<cudaStream_t>(stream), kv ? &ap : nullptr);
+  if (e != cudaSuccess) {
+    char msg[64];
+    snprintf(msg, sizeof msg, "%s launch", what);
+    return cuda_fail(e, msg);
+  }
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status attn_train_forward(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets, int32_t n_rows,
+                              int32_t max_block_rows, const uint16_t* q_raw, const uint16_t* q_norm_w,
+                              const uint16_t* k_hat, const uint16_t* v_hat, void* out, int32_t out_is_f32,
+                              uint16_t* q_prepped, void* workspace, size_t workspace_bytes, void* stream) {
+  return train_forward("attn_train_forward", layer, n_blocks, block_offsets, n_rows, max_block_rows, q_raw, q_norm_w,
+                       k_hat, v_hat, out, out_is_f32, q_prepped, nullptr, workspace, workspace_bytes, stream, nullptr);
+}
+
+kvq_status attn_train_forward_lse(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                                  int32_t n_rows, int32_t max_block_rows, const uint16_t* q_raw,
+                                  const uint16_t* q_norm_w, const uint16_t* k_hat, const uint16_t* v_hat, void* out,
+                                  int32_t out_is_f32, uint16_t* q_prepped, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (n_rows != 0) REQUIRE_PTR(lse, "lse", 4);
+  return train_forward("attn_train_forward_lse", layer, n_blocks, block_offsets, n_rows, max_block_rows, q_raw,
+                       q_norm_w, k_hat, v_hat, out, out_is_f32, q_prepped, lse, workspace, workspace_bytes, stream,
+                       nullptr);
+}
+
+kvq_status attn_train_donor_forward(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                                    int32_t n_rows, int32_t max_block_rows, const uint16_t* q_raw,
+                                    const uint16_t* k_raw, const uint16_t* v_raw, const uint16_t* q_norm_w,
+                                    const uint16_t* k_norm_w, uint16_t* k_hat, uint16_t* v_hat, void* out,
+                                    int32_t out_is_f32, uint16_t* q_prepped, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  const DonorKv kv = {k_raw, v_raw, k_norm_w, k_hat, v_hat};
+  return train_forward("attn_train_donor_forward", layer, n_blocks, block_offsets, n_rows, max_block_rows, q_raw,
+                       q_norm_w, k_hat, v_hat, out, out_is_f32, q_prepped, nullptr, workspace, workspace_bytes,
+                       stream, &kv);
+}
+
+kvq_status attn_train_donor_forward_lse(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                                        int32_t n_rows, int32_t max_block_rows, const uint16_t* q_raw,
+                                        const uint16_t* k_raw, const uint16_t* v_raw, const uint16_t* q_norm_w,
+                                        const uint16_t* k_norm_w, uint16_t* k_hat, uint16_t* v_hat, void* out,
+                                        int32_t out_is_f32, uint16_t* q_prepped, float* lse, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  if (n_rows != 0) REQUIRE_PTR(lse, "lse", 4);
+  const DonorKv kv = {k_raw, v_raw, k_norm_w, k_hat, v_hat};
+  return train_forward("attn_train_donor_forward_lse", layer, n_blocks, block_offsets, n_rows, max_block_rows, q_raw,
+                       q_norm_w, k_hat, v_hat, out, out_is_f32, q_prepped, lse, workspace, workspace_bytes, stream,
+                       &kv);
+}
+
+size_t attn_train_backward_workspace_bytes(const kvq_layer* layer, int32_t n_blocks, int32_t n_rows,
+                                           int32_t max_block_rows) {
+  kvq::LayerArgs L;
+  if (check_layer(layer, &L) != KVQ_OK || !kvq::train_supported(L) || n_blocks < 1 || n_blocks > 65535 ||
+      n_rows < 0 || n_rows >= (1 << 24))
+    return 0;
+  if (n_rows == 0) return 256;
+  if (max_block_rows < 1 || max_block_rows > n_rows) return 0;
+  return kvq::train_bwd_ws_bytes(L, n_blocks, n_rows, max_block_rows);
+}
+
+kvq_status attn_train_backward(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                               int32_t n_rows, int32_t max_block_rows, const uint16_t* q_hat,
+                               const uint16_t* k_hat, const uint16_t* v_hat, const void* out, int32_t out_is_f32,
+                               const float* lse, const uint16_t* d_out, uint16_t* dq_hat, void* dk_hat,
+                               void* dv_hat, int32_t dkv_is_f32, int32_t accumulate, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  kvq::TrainBwdArgs a = {};
+  kvq_status st = check_train_layer(layer, &a.L);
+  if (st != KVQ_OK) return st;
+  if (!kvq::train_supported(a.L))
+    return fail(KVQ_EUNSUPPORTED, "training read: n_q_heads / n_kv_heads = %d must divide 128", a.L.G);
+  if ((st = check_layout(n_blocks, block_offsets, n_rows)) != KVQ_OK) return st;
+  if (out_is_f32 != 0 && out_is_f32 != 1) return fail(KVQ_EINVAL, "out_is_f32 must be 0 or 1");
+  if (dkv_is_f32 != 0 && dkv_is_f32 != 1) return fail(KVQ_EINVAL, "dkv_is_f32 must be 0 or 1");
+  if (accumulate != 0 && accumulate != 1) return fail(KVQ_EINVAL, "accumulate must be 0 or 1");
+  if (accumulate && !dkv_is_f32) return fail(KVQ_EINVAL, "accumulate = 1 adds to fp32 sums (dkv_is_f32 must be 1)");
+  if (n_rows == 0) return KVQ_OK;
+  if (max_block_rows < 1 || max_block_rows > n_rows)
+    return fail(KVQ_EINVAL, "max_block_rows %d not in [1, n_rows]", max_block_rows);
+  REQUIRE_PTR(q_hat, "q_hat", 16);
+  REQUIRE_PTR(k_hat, "k_hat", 16);
+  REQUIRE_PTR(v_hat, "v_hat", 16);
+  REQUIRE_PTR(out, "out", out_is_f32 ? 4 : 2);
+  REQUIRE_PTR(lse, "lse", 4);
+  REQUIRE_PTR(d_out, "d_out", 16);
+  REQUIRE_PTR(dq_hat, "dq_hat", 2);
+  REQUIRE_PTR(dk_hat, "dk_hat", dkv_is_f32 ? 4 : 2);
+  REQUIRE_PTR(dv_hat, "dv_hat", dkv_is_f32 ? 4 : 2);
+  REQUIRE_PTR(workspace, "workspace", 256);
+  const size_t need = kvq::train_bwd_ws_bytes(a.L, n_blocks, n_rows, max_block_rows);
+  if (workspace_bytes < need) return fail(KVQ_EWORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  a.n_rows = n_rows;
+  a.n_blocks = n_blocks;
+  a.max_block_rows = max_block_rows;
+  a.off = block_offsets;
+  a.q = q_hat;
+  a.k = k_hat;
+  a.v = v_hat;
+  a.out = out;
+  a.out_f32 = out_is_f32;
+  a.lse = lse;
+  a.d_out = d_out;
+  a.dq = dq_hat;
+  a.dk = dk_hat;
+  a.dv = dv_hat;
+  a.dkv_f32 = dkv_is_f32;
+  a.accumulate = accumulate;
+  const cudaError_t e = kvq::launch_train_bwd(a, workspace, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "attn_train_backward launch");
+  return KVQ_OK;
+}
+
+size_t kvq_train_prep_backward_workspace_bytes(const kvq_layer* layer, int32_t n_rows) {
+  kvq::LayerArgs L;
+  if (check_layer(layer, &L) != KVQ_OK || n_rows < 0 || n_rows >= (1 << 24)) return 0;
+  return kvq::prep_bwd_ws_bytes(L);
+}
+
+kvq_status kvq_train_prep_backward(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
+                                   int32_t n_rows, const uint16_t* q_raw, const uint16_t* q_norm_w,
+                                   const uint16_t* dq_hat, uint16_t* dq_raw, float* dq_norm_w,
+                                   const uint16_t* k_raw, const uint16_t* v_raw, const uint16_t* k_norm_w,
+                                   const void* dk_hat, const void* dv_hat, int32_t dkv_is_f32, uint16_t* dk_raw,
+                                   uint16_t* dv_raw, float* dk_norm_w, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  kvq::PrepBwdArgs a = {};
+  kvq_status st = check_train_layer(layer, &a.L);
+  if (st != KVQ_OK) return st;
+  if ((st = check_layout(n_blocks, block_offsets, n_rows)) != KVQ_OK) return st;
+  if (dkv_is_f32 != 0 && dkv_is_f32 != 1) return fail(KVQ_EINVAL, "dkv_is_f32 must be 0 or 1");
+  if (!q_raw && !k_raw) return fail(KVQ_EINVAL, "q_raw and k_raw are both NULL: give one side at least");
+  if (!q_raw && (q_norm_w || dq_hat || dq_raw || dq_norm_w))
+    return fail(KVQ_EINVAL, "q_raw is NULL: every argument of the q side must be");
+  if (!k_raw && (v_raw || k_norm_w || dk_hat || dv_hat || dk_raw || dv_raw || dk_norm_w))
+    return fail(KVQ_EINVAL, "k_raw is NULL: every argument of the k and v side must be");
+  if (n_rows == 0) return KVQ_OK;
+  if (q_raw) {
+    REQUIRE_PTR(q_raw, "q_raw", 16);
+    REQUIRE_PTR(q_norm_w, "q_norm_w", 2);
+    REQUIRE_PTR(dq_hat, "dq_hat", 16);
+    REQUIRE_PTR(dq_raw, "dq_raw", 16);
+    REQUIRE_PTR(dq_norm_w, "dq_norm_w", 4);
+  }
+  if (k_raw) {
+    REQUIRE_PTR(k_raw, "k_raw", 16);
+    REQUIRE_PTR(k_norm_w, "k_norm_w", 2);
+    REQUIRE_PTR(dk_hat, "dk_hat", 16);
+    REQUIRE_PTR(dv_hat, "dv_hat", 16);
+    REQUIRE_PTR(dk_raw, "dk_raw", 16);
+    REQUIRE_PTR(dk_norm_w, "dk_norm_w", 4);
+    if (a.L.k_eq_v) {
+      if (v_raw || dv_raw) return fail(KVQ_EINVAL, "v_raw and dv_raw must be NULL when k_eq_v = 1");
+    } else {
+      REQUIRE_PTR(v_raw, "v_raw", 16);
+      REQUIRE_PTR(dv_raw, "dv_raw", 16);
+    }
+  }
+  REQUIRE_PTR(workspace, "workspace", 256);
+  const size_t need = kvq::prep_bwd_ws_bytes(a.L);
+  if (workspace_bytes < need) return fail(KVQ_EWORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  a.n_rows = n_rows;
+  a.n_blocks = n_blocks;
+  a.off = block_offsets;
+  a.q_raw = q_raw;
+  a.q_w = q_norm_w;
+  a.dq_hat = dq_hat;
+  a.dq_raw = dq_raw;
+  a.dq_w = dq_norm_w;
+  a.k_raw = k_raw;
+  a.v_raw = v_raw;
+  a.k_w = k_norm_w;
+  a.dk_hat = dk_hat;
+  a.dv_hat = dv_hat;
+  a.dkv_f32 = dkv_is_f32;
+  a.dk_raw = dk_raw;
+  a.dv_raw = dv_raw;
+  a.dk_w = dk_norm_w;
+  const kvq::RopeFreqs& f = rope_freqs(layer->rope_theta, a.L.D, a.L.rope_dims);
+  const cudaError_t e = kvq::launch_prep_bwd(a, f, workspace, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_train_prep_backward launch");
   return KVQ_OK;
 }
 

@@ -145,6 +145,7 @@ struct TrainArgs {
   const int32_t* off;   // block offsets [n_blocks + 1]
   void* out;
   int out_f32;
+  float* lse;           // NULL, or [n_rows][n_q]: each row's log-sum-exp
 };
 bool train_supported(const LayerArgs& L);
 size_t train_ws_bytes(int n_rows, const LayerArgs& L);
@@ -153,6 +154,48 @@ size_t train_ws_bytes(int n_rows, const LayerArgs& L);
 cudaError_t launch_train(const TrainArgs& t, const uint16_t* q_raw, const uint16_t* q_w, const uint16_t* k_hat,
                          const uint16_t* v_hat, uint16_t* q_prepped, void* ws, int max_block_rows,
                          const RopeFreqs& f, cudaStream_t st, const AppendArgs* ap = nullptr);
+// The training read's gradient (kvq_train_bwd.cu).
+struct TrainBwdArgs {
+  LayerArgs L;
+  int n_rows, n_blocks, max_block_rows;
+  const int32_t* off;
+  const uint16_t* q;        // q_hat, k_hat, v_hat (bf16)
+  const uint16_t* k;
+  const uint16_t* v;
+  const void* out;
+  int out_f32;
+  const float* lse;
+  const uint16_t* d_out;
+  uint16_t* dq;
+  void* dk;
+  void* dv;
+  int dkv_f32, accumulate;
+};
+size_t train_bwd_ws_bytes(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows);
+cudaError_t launch_train_bwd(const TrainBwdArgs& a, void* ws, cudaStream_t st);
+// The gradient of the preps (kvq_prep_bwd.cu); q_raw or k_raw may be NULL
+// (that side is left out).
+struct PrepBwdArgs {
+  LayerArgs L;
+  int n_rows, n_blocks;
+  const int32_t* off;
+  const uint16_t* q_raw;
+  const uint16_t* q_w;
+  const uint16_t* dq_hat;
+  uint16_t* dq_raw;
+  float* dq_w;
+  const uint16_t* k_raw;
+  const uint16_t* v_raw;
+  const uint16_t* k_w;
+  const void* dk_hat;
+  const void* dv_hat;
+  int dkv_f32;
+  uint16_t* dk_raw;
+  uint16_t* dv_raw;
+  float* dk_w;
+};
+size_t prep_bwd_ws_bytes(const LayerArgs& L);
+cudaError_t launch_prep_bwd(const PrepBwdArgs& a, const RopeFreqs& f, void* ws, cudaStream_t st);
 // One CTA whose bounded wait on an mbarrier that nothing completes gives up
 // after limit_ns and flags the timeout bit in *status.
 cudaError_t launch_wait_selftest(uint32_t* status, unsigned long long limit_ns, cudaStream_t st);

@@ -94,7 +94,9 @@ __device__ __forceinline__ uint32_t bf2_to_h2(uint32_t w) { return pack_h2(bf16l
 // the 16 softmax warps' own barrier (the MMA warp does not take part)
 __device__ __forceinline__ void softmax_sync() { named_bar(1, kThreads); }
 
-template <int D>
+// LSE: also sum the unrounded probabilities and write each row's log-sum-exp
+// (the output's own sum l is that of the rounded P, as PV multiplies them).
+template <int D, bool LSE>
 __global__ void __launch_bounds__(kThreads + 32, 1)
 train_tc_kernel(const TrainArgs a, uint32_t* status, const __grid_constant__ CUtensorMap tmq,
                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
@@ -283,7 +285,7 @@ train_tc_kernel(const TrainArgs a, uint32_t* status, const __grid_constant__ CUt
     const int dd0 = DPT * hf;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     if (T::VSTAGE && tid == 0) issue_v(0);
-    float m_ref = -INFINITY, l_part = 0.f;
+    float m_ref = -INFINITY, l_part = 0.f, z_part = 0.f;
     for (int ti = 0; ti < n_tiles; ++ti) {
       const int slot = ti & 1;
       int pk0, lp0, pk_end;
@@ -331,6 +333,7 @@ train_tc_kernel(const TrainArgs a, uint32_t* status, const __grid_constant__ CUt
       const float alpha = rescale_o ? exp2f((m_ref - (mt + kHead)) * L2E) : 1.f;
       if (renew) {
         l_part *= alpha;
+        if constexpr (LSE) z_part *= alpha;
         m_ref = mt + kHead;
       }
       // PV(ti-1) done: the output is settled, P and V^T are free
@@ -362,6 +365,7 @@ train_tc_kernel(const TrainArgs a, uint32_t* status, const __grid_constant__ CUt
           const __half2 hp = __floats2half2_rn(p0, p1);
           const float2 pf = __half22float2(hp);
           l_part += pf.x + pf.y;
+          if constexpr (LSE) z_part += p0 + p1;
           pw[e] = *reinterpret_cast<const uint32_t*>(&hp);
         }
         tc::st_x8(lane_base + T::C_P + (kKPT / 2) * hf, pw);
@@ -412,6 +416,19 @@ train_tc_kernel(const TrainArgs a, uint32_t* status, const __grid_constant__ CUt
       tc::ld_x4(lane_base + T::C_X, xl);
       tc::wait_ld();
       l_row = (xl[0] + xl[1]) + (xl[2] + xl[3]);
+    }
+    if constexpr (LSE) {
+      softmax_sync();                                     // every share of l is read
+      tc::st_x1(lane_base + T::C_X + hf, z_part);
+      tc::wait_st();
+      tc::fence_before_sync();
+      softmax_sync();
+      tc::fence_after_sync();
+      float xz[4];
+      tc::ld_x4(lane_base + T::C_X, xz);
+      tc::wait_ld();
+      if (hf == 0 && row_valid)
+        a.lse[((size_t)off0 + t) * a.L.n_q + hq] = m_ref + logf((xz[0] + xz[1]) + (xz[2] + xz[3]));
     }
     const float inv = 1.f / l_row;
     const bool out_vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
@@ -484,7 +501,9 @@ cudaError_t launch_train_t(const TrainArgs& t, const uint16_t* q_raw, const uint
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     std::lock_guard<std::mutex> lock(attr_mu);
     if (!attr_set[dev].load(std::memory_order_relaxed)) {
-      e = cudaFuncSetAttribute(train_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      e = cudaFuncSetAttribute(train_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(train_tc_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
       attr_set[dev].store(true, std::memory_order_release);
     }
@@ -516,7 +535,7 @@ cudaError_t launch_train_t(const TrainArgs& t, const uint16_t* q_raw, const uint
   if (t.n_blocks > 65535 || L.n_kv * Tr<D>::NSPLIT > 65535) return cudaErrorInvalidValue;
   const dim3 grid((max_block_rows + TQ - 1) / TQ, t.n_blocks, L.n_kv * Tr<D>::NSPLIT);
   if ((e = prof_before(st)) != cudaSuccess) return e;
-  if ((e = launch_pdl(train_tc_kernel<D>, grid, dim3(kThreads + 32), (size_t)smem, st, t, status, mq, mk, mv)) !=
+  if ((e = launch_pdl(t.lse ? train_tc_kernel<D, true> : train_tc_kernel<D, false>, grid, dim3(kThreads + 32), (size_t)smem, st, t, status, mq, mk, mv)) !=
       cudaSuccess)
     return e;
   return prof_after(st);

@@ -16,8 +16,10 @@ import workloads as W
 
 from . import (KVQ_PHASE_DECODE, KVQ_PHASE_WINDOW, attn_decode, attn_decode_append, attn_decode_workspace_bytes,
                attn_group, attn_mixed, attn_prefill_append, attn_prefill_chunk, attn_prefill_workspace_bytes,
-               attn_train_donor_forward, attn_train_forward, attn_train_workspace_bytes, kv_quant_append,
-               kvq_train_kv_prep, layer as make_layer)
+               attn_train_backward, attn_train_backward_workspace_bytes, attn_train_donor_forward,
+               attn_train_donor_forward_lse, attn_train_forward, attn_train_forward_lse,
+               attn_train_workspace_bytes, kv_quant_append, kvq_train_kv_prep, kvq_train_prep_backward,
+               kvq_train_prep_backward_workspace_bytes, layer as make_layer)
 from .cache import LayerCaches
 
 
@@ -419,3 +421,92 @@ class TrainStackCase:
     def step(self, stream=None, fused=True):
         for _, _, case in self.layers:
             case.step(stream, fused=fused)
+
+
+class TrainGradCase(TrainCase):
+    """A layer's training step: the read with its log-sum-exp, then, for an
+    output gradient d_out (bf16 [T, Hq, D]), the read's gradient and the
+    gradient of the preps, down to the raw rows and the norm weights.
+
+    A KV-sharing layer is given its donor's case: its key and value gradients
+    go to the donor's fp32 buffers, and the donor, whose backward pass comes
+    after those of its sharers, carries the sums through its preps.  `adds`:
+    the layer adds to those buffers (every one but the first to come)."""
+
+    def __init__(self, wl: W.TrainWorkload, d_out, device="cuda", donor_case=None, adds=False, layer_id=0):
+        super().__init__(wl, device, out_f32=True, keep_prepped=True, layer_id=layer_id,
+                         kv=None if donor_case is None else donor_case.kv)
+        spec, T = self.spec, self.n_rows
+        f32 = dict(dtype=torch.float32, device=device)
+        self.d_out = d_out
+        self.lse = torch.empty((T, spec.n_q_heads), **f32)
+        self.dq_hat, self.dq = torch.empty_like(self.q), torch.empty_like(self.q)
+        self.dq_w = torch.empty(spec.head_dim, **f32)
+        self.adds = adds
+        if donor_case is None:
+            kv = (T, spec.n_kv_heads, spec.head_dim)
+            self.dk_hat, self.dv_hat = torch.empty(kv, **f32), torch.empty(kv, **f32)
+            self.dk = torch.empty_like(self.k)
+            self.dv = None if self.v is None else torch.empty_like(self.v)
+            self.dk_w = torch.empty(spec.head_dim, **f32)
+        else:
+            self.dk_hat, self.dv_hat = donor_case.dk_hat, donor_case.dv_hat
+        self.bwd_bytes = attn_train_backward_workspace_bytes(self.lay, self.n_blocks, T, self.max_rows)
+        self.bwd_ws = torch.empty(self.bwd_bytes, dtype=torch.uint8, device=device)
+        self.prep_bytes = kvq_train_prep_backward_workspace_bytes(self.lay, T)
+        self.prep_ws = torch.empty(self.prep_bytes, dtype=torch.uint8, device=device)
+
+    def forward(self, stream=None):
+        if self.donor:
+            attn_train_donor_forward_lse(self.lay, self.n_blocks, self.offs, self.n_rows, self.max_rows, self.q,
+                                         self.k, self.v, self.q_w, self.k_w, self.k_hat, self.v_hat, self.out, True,
+                                         self.q_prepped, self.lse, self.ws, self.ws_bytes, stream)
+        else:
+            attn_train_forward_lse(self.lay, self.n_blocks, self.offs, self.n_rows, self.max_rows, self.q, self.q_w,
+                                   self.k_hat, self.v_hat, self.out, True, self.q_prepped, self.lse, self.ws,
+                                   self.ws_bytes, stream)
+
+    def read_backward(self, stream=None):
+        attn_train_backward(self.lay, self.n_blocks, self.offs, self.n_rows, self.max_rows, self.q_prepped,
+                            self.k_hat, self.v_hat, self.out, True, self.lse, self.d_out, self.dq_hat, self.dk_hat,
+                            self.dv_hat, True, self.adds, self.bwd_ws, self.bwd_bytes, stream)
+
+    def prep_backward(self, stream=None):
+        kv = (self.k, self.v, self.k_w, self.dk_hat, self.dv_hat, True, self.dk, self.dv, self.dk_w) if self.donor \
+            else (None, None, None, None, None, False, None, None, None)
+        kvq_train_prep_backward(self.lay, self.n_blocks, self.offs, self.n_rows, self.q, self.q_w, self.dq_hat,
+                                self.dq, self.dq_w, *kv, self.prep_ws, self.prep_bytes, stream)
+
+    def backward(self, stream=None):
+        self.read_backward(stream)
+        self.prep_backward(stream)
+
+    def grad_status(self) -> int:
+        return int(self.bwd_ws[:4].cpu().numpy().view(np.uint32)[0] |
+                   self.prep_ws[:4].cpu().numpy().view(np.uint32)[0])
+
+
+class TrainGradStackCase:
+    """Forward and backward pass of the training reads over the 42-layer stack
+    (TrainStackCase's layers): the backward pass walks the layers from the last
+    to the first, so that a donor's sums are complete when it comes to it."""
+
+    def __init__(self, blocks, d_outs, seed=1007, device="cuda", n_layers=W.N_LAYERS, name="train-stack"):
+        """d_outs: a function (layer, spec, rows) -> d_out tensor of that layer."""
+        self.layers, donors = [], {}
+        last = {W.stack_cache_layer(i): i for i in range(n_layers)}      # the first to come in the backward pass
+        for i in range(n_layers):
+            spec = W.FULL_KEQV if W.stack_layer_kind(i) == "full" else W.SLIDING
+            wl = W.TrainWorkload(f"{name}-layer{i}", seed, spec, list(blocks))
+            donor = None if i < W.N_DONORS else donors[W.stack_cache_layer(i)]
+            case = TrainGradCase(wl, d_outs(i, spec, wl.n_rows), device, donor, layer_id=i,
+                                 adds=last[W.stack_cache_layer(i)] != i)
+            if donor is None:
+                donors[i] = case
+            self.layers.append(case)
+
+    def step(self, stream=None):
+        for c in self.layers:
+            c.forward(stream)
+        for c in reversed(self.layers):
+            c.backward(stream)
