@@ -998,7 +998,7 @@ kvq_status attn_train_backward(const kvq_layer* layer, int32_t n_blocks, const i
   a.dv = dv_hat;
   a.dkv_f32 = dkv_is_f32;
   a.accumulate = accumulate;
-  const cudaError_t e = kvq::launch_train_bwd(a, workspace, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = kvq::launch_train_bwd(a, workspace, num_sms_current(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "attn_train_backward launch");
   return KVQ_OK;
 }

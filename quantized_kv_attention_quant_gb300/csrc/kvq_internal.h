@@ -172,7 +172,7 @@ struct TrainBwdArgs {
   int dkv_f32, accumulate;
 };
 size_t train_bwd_ws_bytes(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows);
-cudaError_t launch_train_bwd(const TrainBwdArgs& a, void* ws, cudaStream_t st);
+cudaError_t launch_train_bwd(const TrainBwdArgs& a, void* ws, int num_sms, cudaStream_t st);
 // The gradient of the preps (kvq_prep_bwd.cu); q_raw or k_raw may be NULL
 // (that side is left out).
 struct PrepBwdArgs {

@@ -1,196 +1,1068 @@
 // attn_train_backward: the gradient of the training read (kvq_train.cu) by
-// q_hat, k_hat and v_hat under the prefix-shared layout.  With the row's
-// log-sum-exp from the forward,
+// q_hat, k_hat and v_hat under the prefix-shared layout, on the tensor cores.
+// With each row's log-sum-exp from the forward, over the keys j that row i sees,
 //   P = exp(S - lse), S = q k;  dP = dO v;  dS = P (dP - delta), delta = dO . O
 //   dq = dS k,  dk = dS^T q,  dv = P^T dO   (dk, dv over the kv head's q heads)
 // A row that sees one key has P = 1 whatever its score: its dS is 0 exactly.
 //
-// Plain kernels: one warp per (row, head) walks the keys it sees for dq, one
-// warp per (key, kv head) walks the rows that see it for dk and dv, all in
-// fp32 with the head dims spread over the lanes.
+// Five products per (row, head, key), each computed once.  At head_dim 256 and
+// 512 the accumulators of dk and dv fill tensor memory by themselves, so a
+// kernel that keeps S and dP beside them would have to split the head dims and
+// recompute both (8 or 9 products instead of 5).  Instead P and dS go through
+// the workspace as bf16 tiles of 128 rows x 128 keys, in runs short enough for
+// L2 (chunks of the tile list; the workspace does not grow with rows x keys):
+//   prep     delta per (row, head); one block lists the row tiles, key tiles
+//            and chunks of the layout
+//   scores   S and dP of one chunk's tiles (tcgen05, fp32 in tensor memory),
+//            softmax and dS in registers, P and dS tiles out
+//   products dq of the chunk's row tiles, dk and dv of every key tile over the
+//            chunk's row tiles: one kernel, out = sum_t A_t B_t in tensor memory
+//   finish   dk and dv joined over splits (fixed order) into the outputs
+//            (left out when one chunk and one split write them directly)
+//
+// A row tile is 128 (token, head) pairs of one block that share a kv head (128/G
+// tokens times G heads, pair r = token r / G, head r % G), a key tile 128 keys of
+// one block counted from the block's start.  P and dS tiles are stored as 8 x
+// 16-byte core matrices, [16 key groups of 8][128 rows][8 keys]: a warp of the
+// scores kernel (lane = row) writes 512 contiguous bytes per store, and the
+// same image is a K-major operand without swizzle for dq (M = rows, K = keys)
+// and, read transposed, an MN-major one for dk and dv (M = keys, K = rows).  The
+// other operands (k, q, dO) are MN-major too: rows of 64 dims straight from
+// TMA (128-byte swizzle), no transposition anywhere.
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
+#include "kvq_tc.cuh"
+#include "kvq_tma.cuh"
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
 
 namespace kvq {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kT = 128;                     // rows and keys of a tile
+constexpr uint32_t kTileBytes = kT * kT * 2;
+constexpr int kMaxSplits = 8;
+constexpr float kL2E = 1.4426950408889634f;
 
-struct BwdWs {
-  uint32_t* status;     // status word; word 1: 1 when the layout is valid
-  float* delta;         // [n_rows][n_q]
+// A row tile: tokens row0 .. row0 + nt - 1 (packed), the first at position
+// pos0; its P and dS tiles are base .. base + nA + nB - 1 of its kv head's list:
+// the prefix's key tiles a0 .. (keys at positions below kend), then its own
+// block's key tiles b0 .. (block 0's own keys are the prefix).
+struct alignas(16) RowTile {
+  int row0, nt, pos0, base;
+  int a0, nA, b0, nB;
+  int off0, block, kend, pad;
+};
+// A key tile: keys row0 .. row0 + n - 1 (packed), tile idx of its block.
+struct alignas(16) KeyTile { int row0, n, block, idx; };
+
+struct Head {
+  uint32_t status;
+  int ok, nrt, nkt;             // layout valid; row and key tiles of one kv head
+  int ntiles;                   // (row tile, key tile) pairs of one kv head
 };
 
-BwdWs bwd_carve(void* ws) {
-  BwdWs w;
-  w.status = static_cast<uint32_t*>(ws);
-  w.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
+struct Ws {
+  Head* head;
+  int* chunk;                   // [nl + 1]: chunk c is row tiles chunk[c] .. chunk[c + 1] - 1 (kv head major)
+  int* starts;                  // [2][n_blocks + 1]: row and key tiles before each block
+  RowTile* rt;
+  KeyTile* kt;
+  float* delta;                 // [n_rows][n_q]
+  float* acc;                   // [splits][2][n_rows][n_kv][D]: dk, dv
+  uint8_t* p;                   // [cap] tiles
+  uint8_t* ds;
+};
+
+// Sizes of a call, from what the host knows (block offsets are in device memory).
+struct Plan {
+  int nrt, nkt;                 // bounds of row and key tiles of a kv head
+  int cap;                      // tiles of a chunk
+  int nl;                       // chunk launches
+  int splits;                   // of every key tile's row tiles
+  size_t chunk_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
+};
+
+inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+// Output columns per CTA of the products kernel.
+__host__ __device__ constexpr int prod_n(int D) { return D > 256 ? 256 : D; }
+
+// Row tiles of a key tile are shared out to this many CTAs when few key tiles
+// would leave SMs idle.
+int splits_of(const LayerArgs& L, long long n_rows) {
+  const long long items = cdiv(n_rows, kT) * L.n_kv * 2 * (L.D / prod_n(L.D));
+  return items <= 38 ? 8 : items <= 76 ? 4 : items <= 152 ? 2 : 1;
+}
+
+constexpr int kChunkTiles = 1024;
+
+Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows) {
+  Plan p = {};
+  const int TQ = kT / L.G, W = L.window;
+  p.nrt = std::min(n_rows, n_rows / TQ + n_blocks);
+  p.nkt = std::min(n_rows, n_rows / kT + n_blocks);
+  // most key tiles of a row tile: prefix and own block, both at or before it
+  const long long per_block = cdiv(max_block_rows, kT), pfx = n_blocks > 1 ? per_block : 0, n128 = n_rows / kT;
+  long long tmax = std::min(pfx + per_block, n128 + 3);
+  if (W > 0) tmax = std::min(tmax, ((long long)W + TQ) / kT + 4);
+  // all pairs of a kv head: a block's own part grows from 1 tile to per_block
+  // (half of it on average); or, by packed order, half of all keys for the
+  // full row tiles and all of them for each block's last, ragged one
+  const long long by_block = p.nrt * std::min(tmax, pfx + max_block_rows / (2 * kT) + 3);
+  const long long by_order = n_rows / TQ * std::min(tmax, n128 / 2 + 4) + n_blocks * tmax;
+  const long long total = std::min(by_block, by_order) * L.n_kv;
+  const long long cap = std::min<long long>(total, std::max<long long>(kChunkTiles, 2 * tmax));
+  p.cap = (int)cap;
+  // a chunk ends before a row tile that does not fit: more than cap - tmax tiles each
+  p.nl = cap >= total ? 1 : (int)cdiv(total, cap - tmax + 1);
+  p.splits = splits_of(L, n_rows);
+  // partial sums for every smaller call's splits too: the size grows with n_rows
+  size_t acc_rows = (size_t)p.splits * n_rows;
+  const long long per = (long long)L.n_kv * 2 * (L.D / prod_n(L.D));
+  for (int s = 2 * p.splits, items = p.splits == 1 ? 152 : p.splits == 2 ? 76 : 38; s <= kMaxSplits; s *= 2, items /= 2)
+    acc_rows = std::max(acc_rows, (size_t)s * (size_t)std::min<long long>(n_rows, items / per * kT));
+  size_t o = 256;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  p.chunk_o = take(((size_t)p.nl + 1) * 4);
+  p.starts_o = take(((size_t)n_blocks + 1) * 8);
+  p.rt_o = take((size_t)p.nrt * sizeof(RowTile));
+  p.kt_o = take((size_t)p.nkt * sizeof(KeyTile));
+  p.delta_o = take((size_t)n_rows * L.n_q * 4);
+  p.acc_o = take(acc_rows * 2 * L.n_kv * L.D * 4);
+  p.p_o = take((size_t)p.cap * kTileBytes);
+  p.ds_o = take((size_t)p.cap * kTileBytes);
+  p.bytes = o;
+  return p;
+}
+
+Ws carve(void* base, const Plan& p) {
+  uint8_t* b = static_cast<uint8_t*>(base);
+  Ws w;
+  w.head = reinterpret_cast<Head*>(b);
+  w.chunk = reinterpret_cast<int*>(b + p.chunk_o);
+  w.starts = reinterpret_cast<int*>(b + p.starts_o);
+  w.rt = reinterpret_cast<RowTile*>(b + p.rt_o);
+  w.kt = reinterpret_cast<KeyTile*>(b + p.kt_o);
+  w.delta = reinterpret_cast<float*>(b + p.delta_o);
+  w.acc = reinterpret_cast<float*>(b + p.acc_o);
+  w.p = b + p.p_o;
+  w.ds = b + p.ds_o;
   return w;
 }
 
-// One block: the layout rules of include/kvq.h.
-__global__ void __launch_bounds__(256) layout_kernel(const TrainBwdArgs a, BwdWs w) {
-  __shared__ int bad;
-  if (threadIdx.x == 0) bad = 0;
-  __syncthreads();
-  const int P = a.off[1];
-  for (int b = threadIdx.x; b < a.n_blocks; b += blockDim.x) {
-    const int o0 = a.off[b], o1 = a.off[b + 1];
-    const bool ok = o0 >= 0 && o0 <= o1 && o1 <= a.n_rows && P >= 0 && (b == 0 ? o0 == 0 : o0 >= P) &&
-                    (b + 1 < a.n_blocks || o1 == a.n_rows) && o1 - o0 <= a.max_block_rows;
-    if (!ok) atomicOr(&bad, 1);
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    w.status[0] = bad ? 1u << KVQ_DEV_BADSEQ : 0u;
-    w.status[1] = bad ? 0u : 1u;
-  }
-}
+// ---------------------------------------------------------------------------
+// prep: the layout's tiles (block 0) and delta (the other blocks)
+// ---------------------------------------------------------------------------
+constexpr int kPrepThreads = 256;
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Exclusive prefix sum over the block's threads; *total gets the sum.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  return v;
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, s, m);
+    if (lane >= m) s += o;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kPrepThreads / 32; ++w) {
+    const int x = warp_sums[w];
+    before += w < warp ? x : 0;
+    all += x;
+  }
+  *total = all;
+  return before + s - v;
 }
 
-// block of packed row r (largest b with off[b] <= r and a non-empty block)
-__device__ __forceinline__ int find_block(const int32_t* off, int n, int r) {
+// Largest i in [0, n) with a[i] <= x (a[0] <= x, a non-decreasing).
+__device__ __forceinline__ int last_le(const int* a, int n, int x) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(off + mid) <= r) lo = mid; else hi = mid - 1;
+    if (a[mid] <= x) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
 
-template <int E>
-__device__ __forceinline__ void load_row(const uint16_t* p, int lane, float (&v)[E]) {
-#pragma unroll
-  for (int i = 0; i < E; ++i) v[i] = bf16_to_f(__ldg(p + i * 32 + lane));
-}
-template <int E>
-__device__ __forceinline__ float dot(const float (&x)[E], const float (&y)[E]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) s = fmaf(x[i], y[i], s);
-  return warp_sum(s);
-}
-
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) dq_kernel(const TrainBwdArgs a, BwdWs w) {
-  constexpr int E = D / 32;
-  if (w.status[1] == 0) return;
-  const int lane = threadIdx.x & 31;
-  const long long it = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (it >= (long long)a.n_rows * a.L.n_q) return;
-  const int r = (int)(it / a.L.n_q), h = (int)(it % a.L.n_q), kvh = h / a.L.G;
-  const int b = find_block(a.off, a.n_blocks, r), P = a.off[1], o0 = a.off[b];
-  const int pos = b == 0 ? r : P + (r - o0), lo = a.L.window > 0 ? max(0, pos - a.L.window + 1) : 0;
-  float q[E], dO[E], acc[E];
-  load_row<E>(a.q + (size_t)it * D, lane, q);
-  load_row<E>(a.d_out + (size_t)it * D, lane, dO);
-  float dl = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const size_t o = (size_t)it * D + i * 32 + lane;
-    const float ov = a.out_f32 ? static_cast<const float*>(a.out)[o] : bf16_to_f(static_cast<const uint16_t*>(a.out)[o]);
-    dl = fmaf(dO[i], ov, dl);
-    acc[i] = 0.f;
-  }
-  dl = warp_sum(dl);
-  if (lane == 0) w.delta[it] = dl;
-  const float lse = a.lse[it];
-  for (int p = lo; p <= pos && lo != pos; ++p) {
-    const int j = b == 0 || p < P ? p : o0 + (p - P);
-    float k[E], v[E];
-    load_row<E>(a.k + ((size_t)j * a.L.n_kv + kvh) * D, lane, k);
-    load_row<E>(a.v + ((size_t)j * a.L.n_kv + kvh) * D, lane, v);
-    const float ds = expf(dot(q, k) - lse) * (dot(dO, v) - dl);
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = fmaf(ds, k[i], acc[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < E; ++i) a.dq[(size_t)it * D + i * 32 + lane] = f_to_bf16_rn(acc[i]);
-}
-
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) dkv_kernel(const TrainBwdArgs a, BwdWs w) {
-  constexpr int E = D / 32;
-  if (w.status[1] == 0) return;
-  const int lane = threadIdx.x & 31;
-  const long long it = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (it >= (long long)a.n_rows * a.L.n_kv) return;
-  const int j = (int)(it / a.L.n_kv), kvh = (int)(it % a.L.n_kv);
-  const int bj = find_block(a.off, a.n_blocks, j), P = a.off[1];
-  const int pj = bj == 0 ? j : P + (j - a.off[bj]);
-  const int hi = a.L.window > 0 ? pj + a.L.window - 1 : 1 << 30;    // the newest position that sees the key
-  float k[E], v[E], dk[E], dv[E];
-  load_row<E>(a.k + (size_t)it * D, lane, k);
-  load_row<E>(a.v + (size_t)it * D, lane, v);
-#pragma unroll
-  for (int i = 0; i < E; ++i) dk[i] = dv[i] = 0.f;
-  // the key's own block from the key on, then (a prefix key) every branch
-  for (int b = bj; b < (bj == 0 ? a.n_blocks : bj + 1); ++b) {
+__device__ void plan_block(const TrainBwdArgs& a, const Ws& w, int cap, int nl) {
+  __shared__ int sums[kPrepThreads / 32];
+  const int tid = threadIdx.x, nb = a.n_blocks, TQ = kT / a.L.G, W = a.L.window;
+  const int P = a.off[1];
+  bool bad = false;
+  for (int b = tid; b < nb; b += kPrepThreads) {
     const int o0 = a.off[b], o1 = a.off[b + 1];
-    for (int r = b == bj ? j : o0; r < o1; ++r) {
-      const int pos = b == 0 ? r : P + (r - o0);
-      if (pos > hi) break;
-      const bool one = pos == 0 || a.L.window == 1;
-      for (int h = kvh * a.L.G; h < (kvh + 1) * a.L.G; ++h) {
-        const size_t rh = (size_t)r * a.L.n_q + h;
-        float q[E], dO[E];
-        load_row<E>(a.q + rh * D, lane, q);
-        load_row<E>(a.d_out + rh * D, lane, dO);
-        const float p = expf(dot(q, k) - a.lse[rh]);
-        const float ds = one ? 0.f : p * (dot(dO, v) - w.delta[rh]);
+    bad |= !(o0 >= 0 && o0 <= o1 && o1 <= a.n_rows && P >= 0 && (b == 0 ? o0 == 0 : o0 >= P) &&
+             (b + 1 < nb || o1 == a.n_rows) && o1 - o0 <= a.max_block_rows);
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) {                                // no tiles: nothing is written
+    for (int c = tid; c <= nl; c += kPrepThreads) w.chunk[c] = 0;
+    if (tid == 0) *w.head = Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0};
+    return;
+  }
+  int* rs = w.starts;
+  int* ks = w.starts + nb + 1;
+  int nrt = 0, nkt = 0;
+  for (int b0 = 0; b0 < nb; b0 += kPrepThreads) {
+    const int b = b0 + tid, rows = b < nb ? a.off[b + 1] - a.off[b] : 0;
+    int tr, tk;
+    const int r = block_scan((rows + TQ - 1) / TQ, sums, &tr), k = block_scan((rows + kT - 1) / kT, sums, &tk);
+    if (b < nb) {
+      rs[b] = nrt + r;
+      ks[b] = nkt + k;
+    }
+    nrt += tr;
+    nkt += tk;
+  }
+  __syncthreads();
+  for (int i = tid; i < nkt; i += kPrepThreads) {
+    const int b = last_le(ks, nb, i), idx = i - ks[b], o0 = a.off[b];
+    w.kt[i] = KeyTile{o0 + idx * kT, min(kT, a.off[b + 1] - o0 - idx * kT), b, idx};
+  }
+  int ntiles = 0;
+  for (int i0 = 0; i0 < nrt; i0 += kPrepThreads) {
+    const int i = i0 + tid;
+    RowTile t = {};
+    if (i < nrt) {
+      const int b = last_le(rs, nb, i), o0 = a.off[b], rows = a.off[b + 1] - o0, t0 = (i - rs[b]) * TQ;
+      const int first = b == 0 ? 0 : P;
+      t.row0 = o0 + t0;
+      t.nt = min(TQ, rows - t0);
+      t.pos0 = first + t0;
+      t.off0 = o0;
+      t.block = b;
+      t.kend = b == 0 ? 0x7fffffff : P;
+      const int last = t.pos0 + t.nt - 1, lo = W > 0 ? max(0, t.pos0 - W + 1) : 0;
+      const int a_hi = b == 0 ? last : P - 1;
+      if (a_hi >= lo) {
+        t.a0 = lo / kT;
+        t.nA = a_hi / kT - t.a0 + 1;
+      }
+      if (b > 0) {
+        t.b0 = (max(lo, P) - P) / kT;
+        t.nB = (last - P) / kT - t.b0 + 1;
+      }
+    }
+    int tot;
+    t.base = ntiles + block_scan(t.nA + t.nB, sums, &tot);
+    ntiles += tot;
+    if (i < nrt) w.rt[i] = t;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    // chunks: as many whole row tiles as fit in cap tiles
+    const int all = nrt * a.L.n_kv;
+    auto before = [&](int x) -> long long {            // tiles before row tile x (kv head major)
+      return (long long)(x / nrt) * ntiles + (x % nrt ? w.rt[x % nrt].base : 0);
+    };
+    int x = 0, c = 0;
+    w.chunk[0] = 0;
+    while (x < all && c < nl) {
+      const long long room = before(x) + cap;
+      if (before(x + 1) > room) break;
+      int lo = x + 1, hi = all;                        // largest end with before(end) <= room
+      while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (before(mid) <= room) lo = mid; else hi = mid - 1;
+      }
+      x = lo;
+      w.chunk[++c] = x;
+    }
+    // make_plan's bounds hold every valid layout; were one to break them, nothing is written
+    const bool fits = x == all;
+    while (c < nl) w.chunk[++c] = x;
+    if (!fits)
+      for (int i = 0; i <= nl; ++i) w.chunk[i] = 0;
+    *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0};
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrepThreads)
+bwd_prep_kernel(const TrainBwdArgs a, const Ws w, const int cap, const int nl) {
+  pdl_wait();
+  pdl_launch();
+  if (blockIdx.x == 0) {
+    plan_block(a, w, cap, nl);
+    return;
+  }
+  // delta: one warp per (row, head)
+  constexpr int E = D / 32, VEC = E < 8 ? E : 8;
+  const int lane = threadIdx.x & 31;
+  const long long n = (long long)a.n_rows * a.L.n_q, step = (long long)(gridDim.x - 1) * (kPrepThreads / 32);
+  const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+  for (long long it = (long long)(blockIdx.x - 1) * (kPrepThreads / 32) + (threadIdx.x >> 5); it < n; it += step) {
+    float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          dk[i] = fmaf(ds, q[i], dk[i]);
-          dv[i] = fmaf(p, dO[i], dv[i]);
+    for (int c = 0; c < E / VEC; ++c) {
+      const size_t o = (size_t)it * D + (c * 32 + lane) * VEC;
+      float g[VEC], x[VEC];
+      uint32_t u[VEC / 2];
+      if constexpr (VEC == 8) *reinterpret_cast<uint4*>(u) = __ldg(reinterpret_cast<const uint4*>(a.d_out + o));
+      else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(u) = __ldg(reinterpret_cast<const uint2*>(a.d_out + o));
+      else u[0] = __ldg(reinterpret_cast<const uint32_t*>(a.d_out + o));
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        g[2 * i] = bf16lo_to_f(u[i]);
+        g[2 * i + 1] = bf16hi_to_f(u[i]);
+      }
+      if (a.out_f32) {
+        const float* p = static_cast<const float*>(a.out) + o;
+        if (vec && VEC >= 4) {
+#pragma unroll
+          for (int i = 0; i < VEC; i += 4) *reinterpret_cast<float4*>(x + i) = __ldg(reinterpret_cast<const float4*>(p + i));
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) x[i] = __ldg(p + i);
+        }
+      } else {
+        const uint16_t* p = static_cast<const uint16_t*>(a.out) + o;
+        if (vec && VEC == 8) {
+          *reinterpret_cast<uint4*>(u) = __ldg(reinterpret_cast<const uint4*>(p));
+#pragma unroll
+          for (int i = 0; i < VEC / 2; ++i) {
+            x[2 * i] = bf16lo_to_f(u[i]);
+            x[2 * i + 1] = bf16hi_to_f(u[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) x[i] = bf16_to_f(__ldg(p + i));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s = fmaf(g[i], x[i], s);
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (lane == 0) w.delta[it] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// tensor-core pieces
+// ---------------------------------------------------------------------------
+
+// Descriptor of a shared-memory operand without swizzle (8 x 16-byte core
+// matrices) or, with sw128, MN-major rows of 128 swizzled bytes.
+//   K-major, no swizzle:  lbo = next 8 elements of K, sbo = next 8 rows of M
+//   MN-major, no swizzle: lbo = next 8 of K, sbo = next 8 elements of M
+//   MN-major, 128 bytes:  lbo = next 64 elements of N, sbo = next 8 of K
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, bool sw128) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)(sw128 ? 2 : 0) << 61);
+}
+constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;   // instruction descriptor: MN-major operand
+
+__device__ __forceinline__ void ld_x32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+               "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                 "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+                 "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                 "=r"(r[30]), "=r"(r[31])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// A wait that gives up (kvq_common.cuh) flags the status word once and lets
+// the role run on without waiting.
+struct Waiter {
+  uint32_t* status;
+  bool dead = false;
+  __device__ __forceinline__ void operator()(uint64_t* bar, int parity) {
+    if (!dead && !mbar_wait(bar, parity)) {
+      dead = true;
+      flag_error(status, KVQ_DEV_TIMEOUT);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// scores: P and dS of one chunk's tiles
+// ---------------------------------------------------------------------------
+
+template <int D>
+struct Sc {
+  static constexpr int NG = D / 64;
+  static constexpr bool RES = D <= 256;               // q and dO of the row tile stay in shared memory
+  static constexpr int STAGE = RES ? 16384 : 32768;   // a 64-dim slice of k or v (with q's or dO's beside it)
+  static constexpr int NS = D == 256 ? 6 : D == 512 ? 6 : 8;
+  static constexpr int A_OFF = 0;                     // q, then dO: NG blocks each of [128 rows x 128 B]
+  static constexpr int R_OFF = RES ? 2 * NG * 16384 : 0;
+  static constexpr int C_OFF = R_OFF + NS * STAGE;
+  static constexpr int BYTES = C_OFF + 256 + 1024;    // + room to align the base
+};
+constexpr int kScEpi = 8;                             // epilogue warps
+constexpr int kScThreads = (kScEpi + 2) * 32;
+
+// The tiles of a CTA's run in list order.
+struct Walk {
+  int kvh, i, j;                                      // kv head, row tile, its j-th key tile
+  RowTile t;
+};
+// Largest i in [0, n) with rt[i].base <= x, by the whole warp, 32 probes a step.
+__device__ __forceinline__ int find_row_tile(const RowTile* rt, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;                                // the answer is in [lo, lo + len)
+  while (len > 1) {
+    const int step = (len + 31) / 32, at = lo + lane * step;
+    const bool le = lane * step < len && __ldg(&rt[at].base) <= x;
+    const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;   // probes are non-decreasing, probe 0 holds
+    len = min(step, len - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+__device__ __forceinline__ RowTile load_row_tile(const RowTile* rt, int i) {
+  RowTile t;
+  const int4* s = reinterpret_cast<const int4*>(rt + i);
+  int4* d = reinterpret_cast<int4*>(&t);
+  d[0] = __ldg(s);
+  d[1] = __ldg(s + 1);
+  d[2] = __ldg(s + 2);
+  return t;
+}
+// Key tile j of row tile t: its first key's packed row and position.
+__device__ __forceinline__ void key_tile_at(const RowTile& t, int j, int& pk, int& lp) {
+  if (j < t.nA) {
+    pk = lp = (t.a0 + j) * kT;
+  } else {
+    const int o = (t.b0 + j - t.nA) * kT;
+    pk = t.off0 + o;
+    lp = t.kend + o;                                  // a branch: its first row is at position P = kend
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kScThreads, 1)
+bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __grid_constant__ CUtensorMap tmq,
+                  const __grid_constant__ CUtensorMap tmo, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv) {
+  using T = Sc<D>;
+  constexpr int NG = T::NG;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::C_OFF);
+  uint64_t* empty = full + T::NS;
+  uint64_t* a_full = empty + T::NS;                   // q and dO landed
+  uint64_t* a_free = a_full + 1;                      // the row tile's products are done
+  uint64_t* acc_full = a_free + 1;                    // [2] S and dP of a tile done
+  uint64_t* acc_free = acc_full + 2;                  // [2] read by the epilogue
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + 2);
+  if (tid == 0) {
+    for (int s = 0; s < T::NS; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(a_full, 1);
+    mbar_init(a_free, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(acc_full + s, 1);
+      mbar_init(acc_free + s, kScEpi);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(tslot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tslot;
+  pdl_wait();                                         // the plan and delta; the last chunk's tiles are read
+  pdl_launch();
+
+  const int G = a.L.G, nrt = w.head->nrt, ntiles = w.head->ntiles;
+  const int x0 = w.chunk[chunk], x1 = w.chunk[chunk + 1];
+  Waiter wait{&w.head->status};
+  if (x0 < x1) {
+    // this CTA's run of the chunk's tiles
+    const long long c0 = (long long)(x0 / nrt) * ntiles + w.rt[x0 % nrt].base;
+    const long long c1 = (long long)(x1 / nrt) * ntiles + (x1 % nrt ? w.rt[x1 % nrt].base : 0);
+    const int g0 = (int)((c1 - c0) * blockIdx.x / gridDim.x), g1 = (int)((c1 - c0) * (blockIdx.x + 1) / gridDim.x);
+    Walk k;
+    if (g0 < g1) {
+      k.kvh = (int)((c0 + g0) / ntiles);
+      const int rem = (int)((c0 + g0) % ntiles);
+      k.i = find_row_tile(w.rt, nrt, rem);
+      k.t = load_row_tile(w.rt, k.i);
+      k.j = rem - k.t.base;
+    }
+    auto next = [&]() -> bool {                       // to the next tile; true: another row tile
+      if (++k.j < k.t.nA + k.t.nB) return false;
+      k.j = 0;
+      if (++k.i == nrt) {
+        k.i = 0;
+        ++k.kvh;
+      }
+      k.t = load_row_tile(w.rt, k.i);
+      return true;
+    };
+
+    if (warp == kScEpi) {
+      // ================= copies =================
+      int st = 0, ph = 0, rts = 0;                    // ring stage, its phase; row tiles begun
+      bool fresh = true;
+      for (int g = g0; g < g1; ++g) {
+        int pk, lp;
+        key_tile_at(k.t, k.j, pk, lp);
+        if (T::RES && fresh) {
+          if (rts > 0) wait(a_free, (rts - 1) & 1);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(a_full, 2 * NG * 16384);
+            for (int c = 0; c < NG; ++c) {
+              tc::tma_load_3d(sb + T::A_OFF + c * 16384, &tmq, 64 * c, k.kvh * G, k.t.row0, smem_u32(a_full));
+              tc::tma_load_3d(sb + T::A_OFF + (NG + c) * 16384, &tmo, 64 * c, k.kvh * G, k.t.row0, smem_u32(a_full));
+            }
+          }
+          ++rts;
+        }
+        for (int c = 0; c < 2 * NG; ++c) {
+          wait(empty + st, ph ^ 1);
+          if (lane == 0) {
+            const int dim = 64 * (c < NG ? c : c - NG);
+            const uint32_t dst = sb + T::R_OFF + st * T::STAGE, bar = smem_u32(full + st);
+            mbar_arrive_expect_tx(full + st, T::STAGE);
+            tc::tma_load_3d(dst, c < NG ? &tmk : &tmv, dim, k.kvh, pk, bar);
+            if (!T::RES) tc::tma_load_3d(dst + 16384, c < NG ? &tmq : &tmo, dim, k.kvh * G, k.t.row0, bar);
+          }
+          __syncwarp();
+          if (++st == T::NS) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        fresh = g + 1 < g1 && next();
+      }
+    } else if (warp == kScEpi + 1) {
+      // ================= S = q k^T, dP = dO v^T =================
+      constexpr uint32_t ID = tc::idesc_bf16_f32(kT, kT);
+      int st = 0, ph = 0, rts = 0;
+      bool fresh = true;
+      for (int g = g0; g < g1; ++g) {
+        const int n = g - g0, slot = n & 1;
+        if (T::RES && fresh) wait(a_full, rts++ & 1);
+        if (n >= 2) wait(acc_free + slot, ((n >> 1) - 1) & 1);
+        for (int c = 0; c < 2 * NG; ++c) {
+          wait(full + st, ph);
+          tc::fence_after_sync();
+          if (lane == 0) {
+            const uint32_t bs = sb + T::R_OFF + st * T::STAGE;
+            const uint32_t as = T::RES ? sb + T::A_OFF + c * 16384 : bs + 16384;
+            const uint32_t d = tmem + 256 * slot + (c < NG ? 0 : kT);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              tc::mma_f16(d, tc::desc_kmajor_sw128(as + 32 * s, 1024), tc::desc_kmajor_sw128(bs + 32 * s, 1024), ID,
+                          (c != 0 && c != NG) || s != 0);
+            tc::commit(empty + st);
+          }
+          __syncwarp();
+          if (++st == T::NS) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (lane == 0) tc::commit(acc_full + slot);
+        fresh = g + 1 < g1 && next();
+        if (T::RES && fresh && lane == 0) tc::commit(a_free);
+        __syncwarp();
+      }
+    } else {
+      // ================= P and dS: thread = row, half of the tile's keys =================
+      const int r = 32 * (warp & 3) + lane, hf = warp >> 2, W = a.L.window;
+      const int tq = r / G, h = r % G;
+      const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      float lse2 = 0.f, delta = 0.f;
+      int lo = 0, hi = -1, cut = 0;                   // visible positions lo .. hi of the prefix part: hi below kend
+      bool one = false, fresh = true;
+      for (int g = g0; g < g1; ++g) {
+        const int n = g - g0, slot = n & 1;
+        if (fresh) {
+          const bool valid = tq < k.t.nt;
+          const int pos = k.t.pos0 + tq;
+          lo = W > 0 ? max(0, pos - W + 1) : 0;
+          hi = valid ? pos : -1;
+          cut = valid ? min(pos, k.t.kend - 1) : -1;
+          one = lo == pos;
+          if (valid) {
+            const size_t o = (size_t)(k.t.row0 + tq) * a.L.n_q + k.kvh * G + h;
+            lse2 = __ldg(a.lse + o) * kL2E;
+            delta = w.delta[o];
+          }
+        }
+        int pk, lp;
+        key_tile_at(k.t, k.j, pk, lp);
+        const int top = k.j < k.t.nA ? cut : hi;
+        uint8_t* pt = w.p + (size_t)g * kTileBytes + (size_t)hf * 16384 + r * 16;
+        uint8_t* dt = w.ds + (size_t)g * kTileBytes + (size_t)hf * 16384 + r * 16;
+        wait(acc_full + slot, (n >> 1) & 1);
+        tc::fence_after_sync();
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {                 // 32 keys at a time
+          float S[32], dP[32];
+          const uint32_t ta = lane_base + 256 * slot + 64 * hf + 32 * q;
+          ld_x32(ta, S);
+          ld_x32(ta + kT, dP);
+          tc::wait_ld();
+          if (q == 1) {                               // the slot is read
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_free + slot);
+          }
+          const int p0 = lp + 64 * hf + 32 * q;
+          const bool whole = __all_sync(0xffffffffu, p0 >= lo && p0 + 31 <= top);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pw[4], dw[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float p[2], d[2];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int i = 8 * c + 2 * e + u;
+                p[u] = exp2f(fmaf(S[i], kL2E, -lse2));
+                d[u] = one ? 0.f : p[u] * (dP[i] - delta);
+                if (!whole) {
+                  const bool vis = p0 + i >= lo && p0 + i <= top;
+                  p[u] = vis ? p[u] : 0.f;
+                  d[u] = vis ? d[u] : 0.f;
+                }
+              }
+              pw[e] = pack_bf2(p[0], p[1]);
+              dw[e] = pack_bf2(d[0], d[1]);
+            }
+            const int o = (4 * q + c) * 2048;
+            *reinterpret_cast<uint4*>(pt + o) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+            *reinterpret_cast<uint4*>(dt + o) = make_uint4(dw[0], dw[1], dw[2], dw[3]);
+          }
+        }
+        fresh = g + 1 < g1 && next();
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// products: out[128 x N] = sum over steps of A_t (128 x 64) B_t (64 x N)
+// ---------------------------------------------------------------------------
+
+template <int N>
+struct Pr {
+  static constexpr int A_BYTES = 16384;                       // 128 x 64 of P or dS
+  static constexpr int B_BYTES = N * 128;                     // 64 rows of N dims: N/64 blocks of 8 KB
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int NS = 98304 / STAGE;                    // two CTAs per SM
+  static constexpr int C_OFF = NS * STAGE;
+  static constexpr int BYTES = C_OFF + 256 + 1024;
+};
+constexpr int kPrEpi = 4;
+constexpr int kPrThreads = (kPrEpi + 2) * 32;
+
+struct ProdGrid {
+  int n_kt, n_rt;               // bounds: key tiles of a kv head, row tiles of a chunk
+  int splits;
+  int direct;                   // 1: dk and dv go straight to the outputs
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 2)
+bwd_products_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const ProdGrid pg,
+                    const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmo,
+                    const __grid_constant__ CUtensorMap tmk) {
+  constexpr int N = prod_n(D), H = D / N;
+  using T = Pr<N>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::C_OFF);
+  uint64_t* empty = full + T::NS;
+  uint64_t* done = empty + T::NS;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  pdl_wait();
+  pdl_launch();
+  // ---- the CTA's item: dk and dv first (their sums are the longest) ----
+  const Head hd = *w.head;
+  const int G = a.L.G, TQ = kT / G;
+  const int x0 = w.chunk[chunk], x1 = w.chunk[chunk + 1];
+  int id = blockIdx.x;
+  const int n_dkv = pg.n_kt * a.L.n_kv * 2 * H * pg.splits;
+  const bool dkv = id < n_dkv;
+  int half, kvh, kind = 0, split = 0;
+  KeyTile kt = {};
+  RowTile rt = {};
+  if (dkv) {
+    half = id % H;
+    id /= H;
+    kind = id % 2;                                    // 0: dk = dS^T q, 1: dv = P^T dO
+    id /= 2;
+    split = id % pg.splits;
+    id /= pg.splits;
+    kvh = id % a.L.n_kv;
+    id /= a.L.n_kv;
+    if (id >= hd.nkt || (chunk > 0 && x0 == x1)) return;
+    kt = w.kt[id];
+  } else {
+    id -= n_dkv;
+    half = id % H;
+    id = x0 + id / H;
+    if (id >= x1) return;
+    kvh = id / hd.nrt;
+    rt = load_row_tile(w.rt, id % hd.nrt);
+  }
+  const long long c0 = x0 < x1 ? (long long)(x0 / hd.nrt) * hd.ntiles + w.rt[x0 % hd.nrt].base : 0;
+  // the chunk's row tiles of this kv head, and the tile slot of the first tile of its list
+  const int xs = dkv ? max(0, x0 - kvh * hd.nrt) : 0, xe = dkv ? min(hd.nrt, x1 - kvh * hd.nrt) : 0;
+  const long long slot0 = (long long)kvh * hd.ntiles - c0;
+  // slot of the key tile in row tile i's list, or -1
+  auto slot_of = [&](int i) -> int {
+    if (i >= xe) return -1;
+    const RowTile t = load_row_tile(w.rt, i);
+    int j = -1;
+    if (kt.block == 0) {
+      if (kt.idx >= t.a0 && kt.idx < t.a0 + t.nA) j = kt.idx - t.a0;
+    } else if (t.block == kt.block && kt.idx >= t.b0 && kt.idx < t.b0 + t.nB) {
+      j = t.nA + kt.idx - t.b0;
+    }
+    return j < 0 ? -1 : (int)(slot0 + t.base + j);
+  };
+
+  if (tid == 0) {
+    for (int s = 0; s < T::NS; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(tslot, N);
+    tc::tmem_relinquish();
+  }
+  // how many row tiles this split takes: the first and last of the visible ones
+  __shared__ int vis_range[2];
+  if (dkv && warp == kPrEpi) {
+    int n = 0;
+    for (int i = xs; i < xe; i += 32) n += __popc(__ballot_sync(0xffffffffu, slot_of(i + lane) >= 0));
+    if (lane == 0) {
+      vis_range[0] = (int)((long long)n * split / pg.splits);
+      vis_range[1] = (int)((long long)n * (split + 1) / pg.splits);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tslot;
+  const int v0 = dkv ? vis_range[0] : 0, v1 = dkv ? vis_range[1] : rt.nA + rt.nB;
+  const int steps = 2 * (v1 - v0);
+  Waiter wait{&w.head->status};
+
+  if (warp == kPrEpi) {
+    // ================= copies =================
+    int st = 0, ph = 0;
+    auto stage = [&](int slot, int s, int pk, int row0) {     // step s (0, 1) of a tile
+      wait(empty + st, ph ^ 1);
+      const uint32_t dst = sb + st * T::STAGE, bar = smem_u32(full + st);
+      if (lane == 0) mbar_arrive_expect_tx(full + st, T::STAGE);
+      __syncwarp();
+      const uint8_t* img = (dkv && kind == 1 ? w.p : w.ds) + (size_t)slot * kTileBytes;
+      if (dkv) {
+        // rows 64 s .. of every key group: [16][64 rows][16 B]
+        if (lane < 16) bulk_g2s(sm + st * T::STAGE + lane * 1024, img + lane * 2048 + s * 1024, 1024, full + st);
+        if (lane >= 16 && lane - 16 < N / 64) {
+          const int b = lane - 16;
+          tc::tma_load_3d(dst + T::A_BYTES + b * 8192, kind == 0 ? &tmq : &tmo, half * N + 64 * b, kvh * G,
+                          row0 + s * (TQ / 2), bar);
+        }
+      } else {
+        // keys 64 s ..: [8][128 rows][16 B]
+        if (lane == 0) bulk_g2s(sm + st * T::STAGE, img + s * 16384, 16384, full + st);
+        if (lane >= 16 && lane - 16 < N / 64) {
+          const int b = lane - 16;
+          tc::tma_load_3d(dst + T::A_BYTES + b * 8192, &tmk, half * N + 64 * b, kvh, pk + 64 * s, bar);
+        }
+      }
+      __syncwarp();
+      if (++st == T::NS) {
+        st = 0;
+        ph ^= 1;
+      }
+    };
+    if (dkv) {
+      int seen = 0;
+      for (int i = xs; i < xe && seen < v1; i += 32) {
+        const int mine = slot_of(i + lane);
+        const int row = i + lane < xe ? __ldg(&w.rt[i + lane].row0) : 0;
+        uint32_t m = __ballot_sync(0xffffffffu, mine >= 0);
+        for (; m; m &= m - 1, ++seen) {
+          if (seen < v0) continue;
+          if (seen >= v1) break;
+          const int src = __ffs(m) - 1;
+          const int slot = __shfl_sync(0xffffffffu, mine, src), row0 = __shfl_sync(0xffffffffu, row, src);
+          stage(slot, 0, 0, row0);
+          stage(slot, 1, 0, row0);
+        }
+      }
+    } else {
+      const int slot = (int)(slot0 + rt.base);
+      for (int j = 0; j < v1; ++j) {
+        int pk, lp;
+        key_tile_at(rt, j, pk, lp);
+        stage(slot + j, 0, pk, 0);
+        stage(slot + j, 1, pk, 0);
+      }
+    }
+  } else if (warp == kPrEpi + 1) {
+    // ================= products =================
+    const uint32_t ID = tc::idesc_bf16_f32(kT, N) | kTransB | (dkv ? kTransA : 0u);
+    int st = 0, ph = 0;
+    for (int t = 0; t < steps; ++t) {
+      wait(full + st, ph);
+      tc::fence_after_sync();
+      if (lane == 0) {
+        const uint32_t as = sb + st * T::STAGE, bs = as + T::A_BYTES;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          tc::mma_f16(tmem, dkv ? smem_desc(as + 256 * s, 128, 1024, false) : smem_desc(as + 4096 * s, 2048, 128, false),
+                      smem_desc(bs + 2048 * s, 8192, 1024, true), ID, t > 0 || s > 0);
+        tc::commit(empty + st);
+        if (t + 1 == steps) tc::commit(done);
+      }
+      __syncwarp();
+      if (++st == T::NS) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+  } else {
+    // ================= out: thread = row =================
+    const int r = tid;
+    if (steps > 0) {
+      wait(done, 0);
+      tc::fence_after_sync();
+      __syncwarp();
+    }
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
+    size_t o;                                         // element offset of the row's first dim
+    bool valid;
+    if (dkv) {
+      valid = r < kt.n;
+      o = ((size_t)(kt.row0 + r) * a.L.n_kv + kvh) * D + half * N;
+    } else {
+      const int tq = r / G;
+      valid = tq < rt.nt;
+      o = ((size_t)(rt.row0 + tq) * a.L.n_q + kvh * G + r % G) * D + half * N;
+    }
+    const size_t plane = (size_t)a.n_rows * a.L.n_kv * D;
+    float* acc = w.acc + ((size_t)split * 2 + kind) * plane;
+    void* out = dkv ? (kind == 0 ? a.dk : a.dv) : a.dq;
+    const bool f32 = dkv && (!pg.direct || a.dkv_f32), add = dkv && (pg.direct ? a.accumulate != 0 : chunk > 0);
+    const bool vec = f32 ? !pg.direct || (reinterpret_cast<uintptr_t>(out) & 15u) == 0
+                         : (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+    float* of = pg.direct ? static_cast<float*>(out) : acc;
+    for (int c = 0; c < N / 16; ++c) {
+      float v[16];
+      if (steps > 0) {
+        tc::ld_x16(lane_base + 16 * c, v);
+        tc::wait_ld();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+      }
+      if (!valid) continue;
+      const size_t e = o + 16 * c;
+      if (f32) {
+        if (add && steps == 0) continue;
+        if (vec) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float4* p = reinterpret_cast<float4*>(of + e) + i;
+            float4 x = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (add) {
+              const float4 y = *p;
+              x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+            }
+            *p = x;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) of[e + i] = add ? of[e + i] + v[i] : v[i];
+        }
+      } else {
+        uint16_t* p = static_cast<uint16_t*>(out) + e;
+        if (vec) {
+          uint32_t u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] = pack_bf2(v[2 * i], v[2 * i + 1]);
+          reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+          reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = f_to_bf16_rn(v[i]);
         }
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const size_t o = (size_t)it * D + i * 32 + lane;
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, N);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// finish: dk and dv over the splits, in split order
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) bwd_finish_kernel(const TrainBwdArgs a, const Ws w, const int splits) {
+  pdl_wait();
+  pdl_launch();
+  if (!w.head->ok) return;
+  const size_t plane = (size_t)a.n_rows * a.L.n_kv * a.L.D;
+  const int kind = blockIdx.y;
+  void* out = kind == 0 ? a.dk : a.dv;
+  const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+  for (size_t e = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; e < plane; e += (size_t)gridDim.x * 1024) {
+    float4 s = *reinterpret_cast<const float4*>(w.acc + kind * plane + e);
+    for (int i = 1; i < splits; ++i) {
+      const float4 y = *reinterpret_cast<const float4*>(w.acc + ((size_t)i * 2 + kind) * plane + e);
+      s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
     if (a.dkv_f32) {
-      float* pk = static_cast<float*>(a.dk) + o;
-      float* pv = static_cast<float*>(a.dv) + o;
-      *pk = a.accumulate ? *pk + dk[i] : dk[i];
-      *pv = a.accumulate ? *pv + dv[i] : dv[i];
+      float* p = static_cast<float*>(out) + e;
+      if (vec) {
+        float4 x = s;
+        if (a.accumulate) {
+          const float4 y = *reinterpret_cast<float4*>(p);
+          x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+        }
+        *reinterpret_cast<float4*>(p) = x;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = a.accumulate ? p[i] + v[i] : v[i];
+      }
     } else {
-      static_cast<uint16_t*>(a.dk)[o] = f_to_bf16_rn(dk[i]);
-      static_cast<uint16_t*>(a.dv)[o] = f_to_bf16_rn(dv[i]);
+      uint16_t* p = static_cast<uint16_t*>(out) + e;
+      if (vec) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = f_to_bf16_rn(v[i]);
+      }
     }
   }
 }
 
+// ---- host side ----
+
+bool map_bf16(CUtensorMap* m, const void* base, int D, int heads, int rows, int box_h, int box_r) {
+  return rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, D, heads, rows, box_h, box_r);
+}
+
 template <int D>
-cudaError_t launch_t(const TrainBwdArgs& a, BwdWs w, cudaStream_t st) {
-  const long long nq = ((long long)a.n_rows * a.L.n_q + kWarps - 1) / kWarps;
-  const long long nk = ((long long)a.n_rows * a.L.n_kv + kWarps - 1) / kWarps;
-  if (nq > 0x7fffffffLL || nk > 0x7fffffffLL) return cudaErrorInvalidValue;
-  layout_kernel<<<1, 256, 0, st>>>(a, w);
-  dq_kernel<D><<<(unsigned)nq, kWarps * 32, 0, st>>>(a, w);
-  dkv_kernel<D><<<(unsigned)nk, kWarps * 32, 0, st>>>(a, w);
-  return cudaGetLastError();
+cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t st) {
+  constexpr int N = prod_n(D), H = D / N;
+  static_assert(Sc<D>::BYTES <= 227 * 1024 && 2 * Pr<N>::BYTES <= 226 * 1024, "shared memory");
+  cudaError_t e;
+  static std::atomic<bool> attr_set[64];
+  static std::mutex attr_mu;
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(attr_mu);
+    if (!attr_set[dev].load(std::memory_order_relaxed)) {
+      e = cudaFuncSetAttribute(bwd_scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sc<D>::BYTES);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(bwd_products_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Pr<N>::BYTES);
+      if (e != cudaSuccess) return e;
+      attr_set[dev].store(true, std::memory_order_release);
+    }
+  }
+  const LayerArgs& L = a.L;
+  const Plan p = make_plan(L, a.n_blocks, a.n_rows, a.max_block_rows);
+  const Ws w = carve(wsp, p);
+  const int TQ = kT / L.G;
+  // boxes: 128 (token, head) pairs and 128 keys for the scores, 64 for the products
+  // (with one q head per tile row the 64-pair box is half the tokens; TQ >= 8)
+  CUtensorMap q1, o1, k1, v1, q2, o2, k2;
+  if (!map_bf16(&q1, a.q, D, L.n_q, a.n_rows, L.G, TQ) || !map_bf16(&o1, a.d_out, D, L.n_q, a.n_rows, L.G, TQ) ||
+      !map_bf16(&k1, a.k, D, L.n_kv, a.n_rows, 1, kT) || !map_bf16(&v1, a.v, D, L.n_kv, a.n_rows, 1, kT) ||
+      !map_bf16(&q2, a.q, D, L.n_q, a.n_rows, L.G, TQ / 2) || !map_bf16(&o2, a.d_out, D, L.n_q, a.n_rows, L.G, TQ / 2) ||
+      !map_bf16(&k2, a.k, D, L.n_kv, a.n_rows, 1, 64))
+    return cudaErrorInvalidValue;
+  const long long pairs = (long long)a.n_rows * L.n_q;
+  const int prep_blocks = 1 + (int)std::min<long long>(cdiv(pairs, kPrepThreads / 32), 8LL * num_sms);
+  if ((e = launch_pdl(bwd_prep_kernel<D>, dim3(prep_blocks), dim3(kPrepThreads), 0, st, a, w, p.cap, p.nl)) !=
+      cudaSuccess)
+    return e;
+  ProdGrid pg;
+  pg.n_kt = p.nkt;
+  pg.n_rt = (int)std::min<long long>((long long)p.nrt * L.n_kv, p.cap);
+  pg.splits = p.splits;
+  pg.direct = p.nl == 1 && p.splits == 1;
+  const long long items = (long long)pg.n_kt * L.n_kv * 2 * H * pg.splits + (long long)pg.n_rt * H;
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  for (int c = 0; c < p.nl; ++c) {
+    if ((e = launch_pdl(bwd_scores_kernel<D>, dim3(std::min(num_sms, p.cap)), dim3(kScThreads), (size_t)Sc<D>::BYTES, st,
+                        a, w, c, q1, o1, k1, v1)) != cudaSuccess)
+      return e;
+    if ((e = launch_pdl(bwd_products_kernel<D>, dim3((unsigned)items), dim3(kPrThreads), (size_t)Pr<N>::BYTES, st, a, w,
+                        c, pg, q2, o2, k2)) != cudaSuccess)
+      return e;
+  }
+  if (pg.direct) return cudaSuccess;
+  const long long quads = (long long)a.n_rows * L.n_kv * D / 4;
+  return launch_pdl(bwd_finish_kernel, dim3((unsigned)std::min<long long>(cdiv(quads, 256), 4LL * num_sms), 2),
+                    dim3(256), 0, st, a, w, p.splits);
 }
 
 }  // namespace
 
 size_t train_bwd_ws_bytes(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows) {
-  return 256 + (size_t)n_rows * L.n_q * 4;
+  return make_plan(L, n_blocks, n_rows, max_block_rows).bytes;
 }
 
-cudaError_t launch_train_bwd(const TrainBwdArgs& a, void* ws, cudaStream_t st) {
-  const BwdWs w = bwd_carve(ws);
+cudaError_t launch_train_bwd(const TrainBwdArgs& a, void* ws, int num_sms, cudaStream_t st) {
   switch (a.L.D) {
-    case 64: return launch_t<64>(a, w, st);
-    case 128: return launch_t<128>(a, w, st);
-    case 256: return launch_t<256>(a, w, st);
-    case 512: return launch_t<512>(a, w, st);
+    case 64: return launch_t<64>(a, ws, num_sms, st);
+    case 128: return launch_t<128>(a, ws, num_sms, st);
+    case 256: return launch_t<256>(a, ws, num_sms, st);
+    case 512: return launch_t<512>(a, ws, num_sms, st);
     default: return cudaErrorInvalidValue;
   }
 }
