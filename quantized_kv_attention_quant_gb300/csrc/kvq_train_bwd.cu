@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 namespace kvq {
 
@@ -98,7 +99,7 @@ int splits_of(const LayerArgs& L, long long n_rows) {
   return items <= 38 ? 8 : items <= 76 ? 4 : items <= 152 ? 2 : 1;
 }
 
-constexpr int kChunkTiles = 1024;
+constexpr int kChunkTiles = 4096;
 
 Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows) {
   Plan p = {};
@@ -108,7 +109,7 @@ Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows)
   // most key tiles of a row tile: prefix and own block, both at or before it
   const long long per_block = cdiv(max_block_rows, kT), pfx = n_blocks > 1 ? per_block : 0, n128 = n_rows / kT;
   long long tmax = std::min(pfx + per_block, n128 + 3);
-  if (W > 0) tmax = std::min(tmax, ((long long)W + TQ) / kT + 4);
+  if (W > 0) tmax = std::min(tmax, ((long long)W + TQ + kT - 3) / kT + 2);   // a span of W + TQ - 1 positions
   // all pairs of a kv head: a block's own part grows from 1 tile to per_block
   // (half of it on average); or, by packed order, half of all keys for the
   // full row tiles and all of them for each block's last, ragged one
@@ -380,6 +381,13 @@ __device__ __forceinline__ void ld_x32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 2^x; a result below the smallest normal float is 0 (no P that small counts)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -413,7 +421,7 @@ struct Sc {
   static constexpr int C_OFF = R_OFF + NS * STAGE;
   static constexpr int BYTES = C_OFF + 256 + 1024;    // + room to align the base
 };
-constexpr int kScEpi = 8;                             // epilogue warps
+constexpr int kScEpi = 16;                            // epilogue warps
 constexpr int kScThreads = (kScEpi + 2) * 32;
 
 // The tiles of a CTA's run in list order.
@@ -593,13 +601,13 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
         __syncwarp();
       }
     } else {
-      // ================= P and dS: thread = row, half of the tile's keys =================
-      const int r = 32 * (warp & 3) + lane, hf = warp >> 2, W = a.L.window;
+      // ================= P and dS: thread = row, 32 of the tile's keys =================
+      const int r = 32 * (warp & 3) + lane, qt = warp >> 2, W = a.L.window;
       const int tq = r / G, h = r % G;
-      const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32 * qt;
       float lse2 = 0.f, delta = 0.f;
-      int lo = 0, hi = -1, cut = 0;                   // visible positions lo .. hi of the prefix part: hi below kend
-      bool one = false, fresh = true;
+      int lo = 0, hi = -1, cut = -1;                  // visible positions: lo .. hi, in prefix tiles lo .. cut
+      bool fresh = true;
       for (int g = g0; g < g1; ++g) {
         const int n = g - g0, slot = n & 1;
         if (fresh) {
@@ -608,7 +616,6 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
           lo = W > 0 ? max(0, pos - W + 1) : 0;
           hi = valid ? pos : -1;
           cut = valid ? min(pos, k.t.kend - 1) : -1;
-          one = lo == pos;
           if (valid) {
             const size_t o = (size_t)(k.t.row0 + tq) * a.L.n_q + k.kvh * G + h;
             lse2 = __ldg(a.lse + o) * kL2E;
@@ -617,26 +624,21 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
         }
         int pk, lp;
         key_tile_at(k.t, k.j, pk, lp);
-        const int top = k.j < k.t.nA ? cut : hi;
-        uint8_t* pt = w.p + (size_t)g * kTileBytes + (size_t)hf * 16384 + r * 16;
-        uint8_t* dt = w.ds + (size_t)g * kTileBytes + (size_t)hf * 16384 + r * 16;
+        const int p0 = lp + 32 * qt, top = k.j < k.t.nA ? cut : hi;
+        const size_t at = (size_t)g * kTileBytes + (size_t)qt * 8192 + r * 16;
+        uint8_t* pt = w.p + at;
+        uint8_t* dt = w.ds + at;
         wait(acc_full + slot, (n >> 1) & 1);
         tc::fence_after_sync();
         __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {                 // 32 keys at a time
-          float S[32], dP[32];
-          const uint32_t ta = lane_base + 256 * slot + 64 * hf + 32 * q;
-          ld_x32(ta, S);
-          ld_x32(ta + kT, dP);
-          tc::wait_ld();
-          if (q == 1) {                               // the slot is read
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_free + slot);
-          }
-          const int p0 = lp + 64 * hf + 32 * q;
-          const bool whole = __all_sync(0xffffffffu, p0 >= lo && p0 + 31 <= top);
+        float S[32], dP[32];
+        ld_x32(lane_base + 256 * slot, S);
+        ld_x32(lane_base + 256 * slot + kT, dP);
+        tc::wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_free + slot);  // the slot is read
+        auto emit = [&](auto masked) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pw[4], dw[4];
@@ -646,22 +648,24 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
                 const int i = 8 * c + 2 * e + u;
-                p[u] = exp2f(fmaf(S[i], kL2E, -lse2));
-                d[u] = one ? 0.f : p[u] * (dP[i] - delta);
-                if (!whole) {
+                p[u] = ex2(fmaf(S[i], kL2E, -lse2));
+                d[u] = p[u] * (dP[i] - delta);
+                if constexpr (decltype(masked)::value) {
                   const bool vis = p0 + i >= lo && p0 + i <= top;
                   p[u] = vis ? p[u] : 0.f;
-                  d[u] = vis ? d[u] : 0.f;
+                  d[u] = vis && lo < hi ? d[u] : 0.f;  // lo == hi: the row sees one key
                 }
               }
               pw[e] = pack_bf2(p[0], p[1]);
               dw[e] = pack_bf2(d[0], d[1]);
             }
-            const int o = (4 * q + c) * 2048;
-            *reinterpret_cast<uint4*>(pt + o) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-            *reinterpret_cast<uint4*>(dt + o) = make_uint4(dw[0], dw[1], dw[2], dw[3]);
+            *reinterpret_cast<uint4*>(pt + c * 2048) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+            *reinterpret_cast<uint4*>(dt + c * 2048) = make_uint4(dw[0], dw[1], dw[2], dw[3]);
           }
-        }
+        };
+        // (a row that sees one key sees no 32 keys: it always takes the masked form)
+        if (__all_sync(0xffffffffu, p0 >= lo && p0 + 31 <= top)) emit(std::false_type{});
+        else emit(std::true_type{});
         fresh = g + 1 < g1 && next();
       }
     }

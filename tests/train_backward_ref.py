@@ -8,6 +8,7 @@ import oracle as O
 
 BF16 = 2.0 ** -8        # half a step of a bf16 rounding, relative to the value
 F32 = 2.0 ** -24
+TINY = 2.0 ** -126      # the smallest normal float: a smaller P may be taken as 0
 
 
 def bf16_normal(rng, shape, scale=1.0):
@@ -23,7 +24,9 @@ def read_bounds(q, k, v, do, g, out_err=0.0, lse_err=0.0):
     F32 of its size, so S is off by at most D F32 |q||k| (likewise dP, and
     delta with out off by out_err); lse by F32 |lse| + lse_err; the exponential
     by 4 F32 of itself.  P and dS each enter a product rounded to bf16; a sum
-    of n products in fp32 adds n F32 of the sum of their sizes."""
+    of n products in fp32 adds n F32 of the sum of their sizes.  P below the
+    smallest normal float, TINY, may be flushed to 0 by the exponential: P is
+    off by TINY at most beside the relative errors, dS by TINY (|dP| + |delta|)."""
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     G = Hq // Hkv
@@ -36,13 +39,14 @@ def read_bounds(q, k, v, do, g, out_err=0.0, lse_err=0.0):
             e_p = D * F32 * (aq[:, h] @ ak[:, kvh].T) + (F32 * np.abs(g["lse"][:, h]) + lse_err)[:, None] + 4 * F32
             e_dp = D * F32 * (ado[:, h] @ av[:, kvh].T)
             e_delta = D * F32 * (ado[:, h] * aout[:, h]).sum(1) + (ado[:, h] * out_err * aout[:, h]).sum(1)
-            e_ds = ds * (BF16 + e_p) + p * (1 + BF16 + e_p) * (e_dp + e_delta[:, None])
+            size = ado[:, h] @ av[:, kvh].T + (ado[:, h] * aout[:, h]).sum(1)[:, None]     # >= |dP| + |delta|
+            e_ds = ds * (BF16 + e_p) + TINY * (p > 0) * size + p * (1 + BF16 + e_p) * (e_dp + e_delta[:, None])
             one = (p > 0).sum(1) == 1                       # one visible key: dS is 0
             e_ds[one] = 0.0
             n = T * G * F32
             bq[:, h] = (e_ds + n * ds) @ ak[:, kvh]
             bk[:, kvh] += (e_ds + n * ds).T @ aq[:, h]
-            bv[:, kvh] += (p * (BF16 + e_p + n)).T @ ado[:, h]
+            bv[:, kvh] += (p * (BF16 + e_p + n) + TINY * (p > 0)).T @ ado[:, h]
     return bq, bk, bv
 
 
