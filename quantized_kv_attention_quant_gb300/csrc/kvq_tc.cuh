@@ -138,6 +138,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void* map, 
                : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const void* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+               " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+               :: "r"(smem_dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+               : "memory");
+}
+
 // 16-byte chunk `chunk` of row `r` of a K-major 128-byte-swizzled tile whose
 // rows are 128 bytes (byte offset from the tile's 1024-aligned base)
 __host__ __device__ constexpr uint32_t sw128_off(int r, int chunk) {

@@ -45,5 +45,19 @@ inline bool rows_map(CUtensorMap* m, CUtensorMapDataType type, const void* base,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Runs of 1024 contiguous bytes, [n3][n2][n1][1024 bytes] packed, read in
+// boxes of (one run, 1, n2, 1), not swizzled.  The base must be 16-byte aligned.
+inline bool runs_map(CUtensorMap* m, const void* base, int n1, int n2, int n3) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {256, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
+  const cuuint64_t strides[3] = {1024, 1024 * (cuuint64_t)n1, 1024 * (cuuint64_t)n1 * n2};
+  const cuuint32_t box[4] = {256u, 1u, (cuuint32_t)n2, 1u};
+  const cuuint32_t es[4] = {1u, 1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 }  // namespace kvq

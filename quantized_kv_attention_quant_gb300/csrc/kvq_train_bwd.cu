@@ -69,6 +69,8 @@ struct Head {
 struct Ws {
   Head* head;
   int* chunk;                   // [nl + 1]: chunk c is row tiles chunk[c] .. chunk[c + 1] - 1 (kv head major)
+  int* counter;                 // [nl]: items of a chunk's products handed out
+  int* pieces;                  // [key pairs][n_kv]: pieces a key pair's sums are in
   int* starts;                  // [2][n_blocks + 1]: row and key tiles before each block
   RowTile* rt;
   KeyTile* kt;
@@ -83,8 +85,9 @@ struct Plan {
   int nrt, nkt;                 // bounds of row and key tiles of a kv head
   int cap;                      // tiles of a chunk
   int nl;                       // chunk launches
-  int splits;                   // of every key tile's row tiles
-  size_t chunk_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
+  int splits, piece;            // of a key pair's row tiles: most pieces; row tiles of one
+  int direct;                   // one chunk, one split: dk and dv need no sums beside the outputs
+  size_t chunk_o, counter_o, pieces_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
 };
 
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
@@ -92,16 +95,10 @@ inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 // Output columns per CTA of the products kernel.
 __host__ __device__ constexpr int prod_n(int D) { return D > 256 ? 256 : D; }
 
-// Row tiles of a key tile are shared out to this many CTAs when few key tiles
-// would leave SMs idle.
-int splits_of(const LayerArgs& L, long long n_rows) {
-  const long long items = cdiv(n_rows, kT) * L.n_kv * 2 * (L.D / prod_n(L.D));
-  return items <= 38 ? 8 : items <= 76 ? 4 : items <= 152 ? 2 : 1;
-}
-
 constexpr int kChunkTiles = 4096;
+constexpr int kMinPiece = 12;
 
-Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows) {
+Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows, int num_sms) {
   Plan p = {};
   const int TQ = kT / L.G, W = L.window;
   p.nrt = std::min(n_rows, n_rows / TQ + n_blocks);
@@ -120,12 +117,21 @@ Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows)
   p.cap = (int)cap;
   // a chunk ends before a row tile that does not fit: more than cap - tmax tiles each
   p.nl = cap >= total ? 1 : (int)cdiv(total, cap - tmax + 1);
-  p.splits = splits_of(L, n_rows);
-  // partial sums for every smaller call's splits too: the size grows with n_rows
-  size_t acc_rows = (size_t)p.splits * n_rows;
-  const long long per = (long long)L.n_kv * 2 * (L.D / prod_n(L.D));
-  for (int s = 2 * p.splits, items = p.splits == 1 ? 152 : p.splits == 2 ? 76 : 38; s <= kMaxSplits; s *= 2, items /= 2)
-    acc_rows = std::max(acc_rows, (size_t)s * (size_t)std::min<long long>(n_rows, items / per * kT));
+  // Splits: the list of row tiles of a key pair is cut into pieces, so that no
+  // CTA's item is long beside an SM's share of the products (in steps of a pair
+  // of tiles); a piece costs its output once more, so it is not cut short.
+  // With one chunk each list is cut by its own length (`piece` row tiles at
+  // least), with several every list into the same number of pieces.
+  const int H = L.D / prod_n(L.D);
+  const long long share = std::min(total, cap) * 3 * H / 2 / num_sms;
+  p.piece = (int)std::max<long long>(kMinPiece, share / 2);
+  p.splits = p.nl == 1 ? (int)std::min<long long>(kMaxSplits, cdiv(p.nrt, p.piece))
+                       : (int)std::min<long long>(kMaxSplits, std::max(1LL, std::min<long long>(p.nrt, 2 * cap / tmax) / std::max(1LL, share)));
+  // and have room: 256 MB of partial sums, or one set
+  const size_t plane = 2 * (size_t)n_rows * L.n_kv * L.D * 4;
+  const size_t acc = std::max(plane, std::min<size_t>(kMaxSplits * plane, (size_t)256 << 20));
+  p.splits = (int)std::min<size_t>(p.splits, acc / plane);
+  p.direct = p.nl == 1 && p.splits == 1;
   size_t o = 256;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -133,11 +139,13 @@ Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows)
     return at;
   };
   p.chunk_o = take(((size_t)p.nl + 1) * 4);
+  p.counter_o = take((size_t)p.nl * 4);
+  p.pieces_o = take(((size_t)p.nkt + 1) / 2 * L.n_kv * 4);
   p.starts_o = take(((size_t)n_blocks + 1) * 8);
   p.rt_o = take((size_t)p.nrt * sizeof(RowTile));
   p.kt_o = take((size_t)p.nkt * sizeof(KeyTile));
   p.delta_o = take((size_t)n_rows * L.n_q * 4);
-  p.acc_o = take(acc_rows * 2 * L.n_kv * L.D * 4);
+  p.acc_o = take(acc);
   p.p_o = take((size_t)p.cap * kTileBytes);
   p.ds_o = take((size_t)p.cap * kTileBytes);
   p.bytes = o;
@@ -149,6 +157,8 @@ Ws carve(void* base, const Plan& p) {
   Ws w;
   w.head = reinterpret_cast<Head*>(b);
   w.chunk = reinterpret_cast<int*>(b + p.chunk_o);
+  w.counter = reinterpret_cast<int*>(b + p.counter_o);
+  w.pieces = reinterpret_cast<int*>(b + p.pieces_o);
   w.starts = reinterpret_cast<int*>(b + p.starts_o);
   w.rt = reinterpret_cast<RowTile*>(b + p.rt_o);
   w.kt = reinterpret_cast<KeyTile*>(b + p.kt_o);
@@ -201,6 +211,7 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, int cap, int nl) 
   __shared__ int sums[kPrepThreads / 32];
   const int tid = threadIdx.x, nb = a.n_blocks, TQ = kT / a.L.G, W = a.L.window;
   const int P = a.off[1];
+  for (int c = tid; c < nl; c += kPrepThreads) w.counter[c] = 0;
   bool bad = false;
   for (int b = tid; b < nb; b += kPrepThreads) {
     const int o0 = a.off[b], o1 = a.off[b + 1];
@@ -393,13 +404,15 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// A wait that gives up (kvq_common.cuh) flags the status word once and lets
-// the role run on without waiting.
+// A wait by a whole warp.  One that gives up (kvq_common.cuh) flags the status
+// word once and lets the warp run on without waiting, all lanes alike.
 struct Waiter {
   uint32_t* status;
   bool dead = false;
   __device__ __forceinline__ void operator()(uint64_t* bar, int parity) {
-    if (!dead && !mbar_wait(bar, parity)) {
+    if (dead) return;
+    const bool ok = mbar_wait(bar, parity);
+    if (__any_sync(0xffffffffu, !ok)) {
       dead = true;
       flag_error(status, KVQ_DEV_TIMEOUT);
     }
@@ -681,30 +694,46 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
 // ---------------------------------------------------------------------------
 // products: out[128 x N] = sum over steps of A_t (128 x 64) B_t (64 x N)
 // ---------------------------------------------------------------------------
+// An item is a pair of tiles (two row tiles for dq, two key tiles for dk or dv)
+// times N head dims: both tiles' A meet the same B, which halves B's traffic
+// (with one tile per CTA the kernel was bound by what L2 delivers).  The list
+// of row tiles of a key pair is cut into `splits` pieces, each with its own sums.
+// CTAs stay resident, take items from a counter (who computes an item does not
+// change it), and the copies of the next item run under the last one's output.
 
 template <int N>
 struct Pr {
-  static constexpr int A_BYTES = 16384;                       // 128 x 64 of P or dS
+  static constexpr int A_BYTES = 16384;                       // 128 x 64 of P or dS, one per tile of the pair
   static constexpr int B_BYTES = N * 128;                     // 64 rows of N dims: N/64 blocks of 8 KB
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int NS = 98304 / STAGE;                    // two CTAs per SM
-  static constexpr int C_OFF = NS * STAGE;
-  static constexpr int BYTES = C_OFF + 256 + 1024;
+  static constexpr int STAGE = 2 * A_BYTES + B_BYTES;
+  static constexpr int NS = N == 256 ? 3 : 4;
+  static constexpr int NBUF = N == 256 ? 1 : 2;               // accumulator pairs in tensor memory
+  static constexpr int E_OFF = NS * STAGE;                    // 4 KB per output warp
+  static constexpr int C_OFF = E_OFF + 8 * 4096;
+  static constexpr int BYTES = C_OFF + 512 + 1024;
 };
-constexpr int kPrEpi = 4;
+constexpr int kPrEpi = 8;
 constexpr int kPrThreads = (kPrEpi + 2) * 32;
 
-struct ProdGrid {
-  int n_kt, n_rt;               // bounds: key tiles of a kv head, row tiles of a chunk
-  int splits;
+// What the copies tell the MMA warp about a stage.
+enum : int { kTile0 = 1, kTile1 = 2, kFirst = 4, kLast = 8, kKeys = 16, kEnd = 32 };
+
+struct Item {
+  bool dkv;
+  int kind, half, kvh, split;   // kind 0: dk = dS^T q, 1: dv = P^T dO
+  int t0, n;                    // first tile of the pair (key tile, or row tile of the kv head) and tiles (1, 2)
+};
+
+struct ProdArgs {
+  int chunk, splits, piece;     // piece: 0 when every list is cut into `splits` pieces
   int direct;                   // 1: dk and dv go straight to the outputs
 };
 
 template <int D>
-__global__ void __launch_bounds__(kPrThreads, 2)
-bwd_products_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const ProdGrid pg,
-                    const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmo,
-                    const __grid_constant__ CUtensorMap tmk) {
+__global__ void __launch_bounds__(kPrThreads, 1)
+bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const __grid_constant__ CUtensorMap tmq,
+                    const __grid_constant__ CUtensorMap tmo, const __grid_constant__ CUtensorMap tmk,
+                    const __grid_constant__ CUtensorMap tmp, const __grid_constant__ CUtensorMap tmd) {
   constexpr int N = prod_n(D), H = D / N;
   using T = Pr<N>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -714,229 +743,373 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const Pro
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::C_OFF);
   uint64_t* empty = full + T::NS;
-  uint64_t* done = empty + T::NS;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
-  pdl_wait();
-  pdl_launch();
-  // ---- the CTA's item: dk and dv first (their sums are the longest) ----
-  const Head hd = *w.head;
-  const int G = a.L.G, TQ = kT / G;
-  const int x0 = w.chunk[chunk], x1 = w.chunk[chunk + 1];
-  int id = blockIdx.x;
-  const int n_dkv = pg.n_kt * a.L.n_kv * 2 * H * pg.splits;
-  const bool dkv = id < n_dkv;
-  int half, kvh, kind = 0, split = 0;
-  KeyTile kt = {};
-  RowTile rt = {};
-  if (dkv) {
-    half = id % H;
-    id /= H;
-    kind = id % 2;                                    // 0: dk = dS^T q, 1: dv = P^T dO
-    id /= 2;
-    split = id % pg.splits;
-    id /= pg.splits;
-    kvh = id % a.L.n_kv;
-    id /= a.L.n_kv;
-    if (id >= hd.nkt || (chunk > 0 && x0 == x1)) return;
-    kt = w.kt[id];
-  } else {
-    id -= n_dkv;
-    half = id % H;
-    id = x0 + id / H;
-    if (id >= x1) return;
-    kvh = id / hd.nrt;
-    rt = load_row_tile(w.rt, id % hd.nrt);
-  }
-  const long long c0 = x0 < x1 ? (long long)(x0 / hd.nrt) * hd.ntiles + w.rt[x0 % hd.nrt].base : 0;
-  // the chunk's row tiles of this kv head, and the tile slot of the first tile of its list
-  const int xs = dkv ? max(0, x0 - kvh * hd.nrt) : 0, xe = dkv ? min(hd.nrt, x1 - kvh * hd.nrt) : 0;
-  const long long slot0 = (long long)kvh * hd.ntiles - c0;
-  // slot of the key tile in row tile i's list, or -1
-  auto slot_of = [&](int i) -> int {
-    if (i >= xe) return -1;
-    const RowTile t = load_row_tile(w.rt, i);
-    int j = -1;
-    if (kt.block == 0) {
-      if (kt.idx >= t.a0 && kt.idx < t.a0 + t.nA) j = kt.idx - t.a0;
-    } else if (t.block == kt.block && kt.idx >= t.b0 && kt.idx < t.b0 + t.nB) {
-      j = t.nA + kt.idx - t.b0;
-    }
-    return j < 0 ? -1 : (int)(slot0 + t.base + j);
-  };
-
+  uint64_t* done = empty + T::NS;                     // [NBUF] an item's products are in tensor memory
+  uint64_t* acc_free = done + T::NBUF;                // [NBUF] and read from it
+  uint64_t* item_full = acc_free + T::NBUF;           // [2]
+  uint64_t* item_empty = item_full + 2;               // [2]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(item_empty + 2);
+  volatile int* info = reinterpret_cast<volatile int*>(tslot + 1);   // [NS] stage flags
+  volatile int* got = info + T::NS;                   // [NBUF] tiles of the pair with any product
+  volatile int* items = got + T::NBUF;                // [2][2]: item (-1: no more), its steps
   if (tid == 0) {
     for (int s = 0; s < T::NS; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
-    mbar_init(done, 1);
+    for (int s = 0; s < T::NBUF; ++s) {
+      mbar_init(done + s, 2);                         // the MMAs, and the flags in got[]
+      mbar_init(acc_free + s, kPrEpi);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(item_full + s, 1);
+      mbar_init(item_empty + s, kPrEpi);
+    }
     fence_mbar_init();
   }
   if (warp == 0) {
-    tc::tmem_alloc(tslot, N);
+    tc::tmem_alloc(tslot, 512);
     tc::tmem_relinquish();
-  }
-  // how many row tiles this split takes: the first and last of the visible ones
-  __shared__ int vis_range[2];
-  if (dkv && warp == kPrEpi) {
-    int n = 0;
-    for (int i = xs; i < xe; i += 32) n += __popc(__ballot_sync(0xffffffffu, slot_of(i + lane) >= 0));
-    if (lane == 0) {
-      vis_range[0] = (int)((long long)n * split / pg.splits);
-      vis_range[1] = (int)((long long)n * (split + 1) / pg.splits);
-    }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tslot;
-  const int v0 = dkv ? vis_range[0] : 0, v1 = dkv ? vis_range[1] : rt.nA + rt.nB;
-  const int steps = 2 * (v1 - v0);
+  pdl_wait();
+  pdl_launch();
+
+  const Head hd = *w.head;
+  const int G = a.L.G, TQ = kT / G, nkv = a.L.n_kv;
+  const int x0 = w.chunk[pa.chunk], x1 = w.chunk[pa.chunk + 1];
+  // an empty chunk (or layout) has no items; dk and dv come first (the longest sums)
+  const int kp = (hd.nkt + 1) / 2, rp = (hd.nrt + 1) / 2;
+  const int n_dkv = x0 < x1 ? kp * pa.splits * nkv * 2 * H : 0;
+  const int q0 = x0 < x1 ? x0 / hd.nrt * rp + x0 % hd.nrt / 2 : 0;
+  const int n_items = x0 < x1 ? n_dkv + ((x1 - 1) / hd.nrt * rp + (x1 - 1) % hd.nrt / 2 - q0 + 1) * H : 0;
+  const long long c0 = x0 < x1 ? (long long)(x0 / hd.nrt) * hd.ntiles + w.rt[x0 % hd.nrt].base : 0;
+  auto decode = [&](int id) {
+    Item t;
+    t.dkv = id < n_dkv;
+    if (!t.dkv) id -= n_dkv;
+    t.half = id % H;
+    id /= H;
+    t.kind = t.split = 0;
+    if (t.dkv) {
+      t.kind = id % 2;
+      id /= 2;
+      t.kvh = id % nkv;
+      id /= nkv;
+      t.split = id % pa.splits;
+      t.t0 = id / pa.splits * 2;
+      t.n = min(2, hd.nkt - t.t0);
+    } else {
+      id += q0;
+      t.kvh = id / rp;
+      t.t0 = max(id % rp * 2, x0 - t.kvh * hd.nrt);   // a pair at the chunk's edge may be cut
+      t.n = min(min(hd.nrt, x1 - t.kvh * hd.nrt), id % rp * 2 + 2) - t.t0;
+    }
+    return t;
+  };
   Waiter wait{&w.head->status};
 
   if (warp == kPrEpi) {
     // ================= copies =================
-    int st = 0, ph = 0;
-    auto stage = [&](int slot, int s, int pk, int row0) {     // step s (0, 1) of a tile
-      wait(empty + st, ph ^ 1);
-      const uint32_t dst = sb + st * T::STAGE, bar = smem_u32(full + st);
-      if (lane == 0) mbar_arrive_expect_tx(full + st, T::STAGE);
-      __syncwarp();
-      const uint8_t* img = (dkv && kind == 1 ? w.p : w.ds) + (size_t)slot * kTileBytes;
-      if (dkv) {
-        // rows 64 s .. of every key group: [16][64 rows][16 B]
-        if (lane < 16) bulk_g2s(sm + st * T::STAGE + lane * 1024, img + lane * 2048 + s * 1024, 1024, full + st);
-        if (lane >= 16 && lane - 16 < N / 64) {
-          const int b = lane - 16;
-          tc::tma_load_3d(dst + T::A_BYTES + b * 8192, kind == 0 ? &tmq : &tmo, half * N + 64 * b, kvh * G,
-                          row0 + s * (TQ / 2), bar);
-        }
-      } else {
-        // keys 64 s ..: [8][128 rows][16 B]
-        if (lane == 0) bulk_g2s(sm + st * T::STAGE, img + s * 16384, 16384, full + st);
-        if (lane >= 16 && lane - 16 < N / 64) {
-          const int b = lane - 16;
-          tc::tma_load_3d(dst + T::A_BYTES + b * 8192, &tmk, half * N + 64 * b, kvh, pk + 64 * s, bar);
-        }
+    int st = 0, ph = 0, e = 0, eph = 0;
+    auto publish = [&](int id, int n) {
+      wait(item_empty + e, eph ^ 1);
+      if (lane == 0) {
+        items[2 * e] = id;
+        items[2 * e + 1] = n;
+        mbar_arrive(item_full + e);
       }
       __syncwarp();
-      if (++st == T::NS) {
-        st = 0;
-        ph ^= 1;
+      if (++e == 2) {
+        e = 0;
+        eph ^= 1;
       }
     };
-    if (dkv) {
-      int seen = 0;
-      for (int i = xs; i < xe && seen < v1; i += 32) {
-        const int mine = slot_of(i + lane);
-        const int row = i + lane < xe ? __ldg(&w.rt[i + lane].row0) : 0;
-        uint32_t m = __ballot_sync(0xffffffffu, mine >= 0);
-        for (; m; m &= m - 1, ++seen) {
-          if (seen < v0) continue;
-          if (seen >= v1) break;
-          const int src = __ffs(m) - 1;
-          const int slot = __shfl_sync(0xffffffffu, mine, src), row0 = __shfl_sync(0xffffffffu, row, src);
-          stage(slot, 0, 0, row0);
-          stage(slot, 1, 0, row0);
+    for (;;) {
+      int id = 0;
+      if (lane == 0) id = atomicAdd(w.counter + pa.chunk, 1);
+      id = __shfl_sync(0xffffffffu, id, 0);
+      if (id >= n_items) break;
+      const Item it = decode(id);
+      const long long slot0 = (long long)it.kvh * hd.ntiles - c0;    // slot of the kv head's first tile
+      int left = 0;                                   // stages still to come
+      bool first = true;
+      // one tile of each of the pair (slot -1: not there) and the 128 rows of B they meet
+      auto tile = [&](int s0, int s1, int row) {
+        const int mask = (s0 >= 0 ? kTile0 : 0) | (s1 >= 0 ? kTile1 : 0);
+        for (int s = 0; s < 2; ++s) {
+          wait(empty + st, ph ^ 1);
+          const uint32_t dst = sb + st * T::STAGE, bar = smem_u32(full + st);
+          if (lane == 0) {
+            info[st] = mask | (first ? kFirst : 0) | (--left == 0 ? kLast : 0) | (it.dkv ? kKeys : 0);
+            mbar_arrive_expect_tx(full + st, __popc(mask) * T::A_BYTES + T::B_BYTES);
+          }
+          first = false;
+          __syncwarp();
+          // A: lanes 0 and 1, a tile each; B: the next lanes, 64 dims each
+          const int slot = lane == 0 ? s0 : s1, b = lane - 2;
+          if (it.dkv) {
+            // rows 64 s .. of every key group: [16][64 rows][16 B], runs of 1 KB (one copy
+            // for the sixteen: a copy takes the issuing warp some 60 cycles)
+            if (lane < 2 && slot >= 0)
+              tc::tma_load_4d(dst + lane * T::A_BYTES, it.kind == 1 ? &tmp : &tmd, 0, s, 0, slot, bar);
+            if (b >= 0 && b < N / 64)
+              tc::tma_load_3d(dst + 2 * T::A_BYTES + b * 8192, it.kind == 0 ? &tmq : &tmo, it.half * N + 64 * b,
+                              it.kvh * G, row + s * (TQ / 2), bar);
+          } else {
+            // keys 64 s ..: [8][128 rows][16 B]
+            if (lane < 2 && slot >= 0)
+              bulk_g2s(sm + st * T::STAGE + lane * T::A_BYTES, w.ds + (size_t)slot * kTileBytes + s * 16384, 16384,
+                       full + st);
+            if (b >= 0 && b < N / 64)
+              tc::tma_load_3d(dst + 2 * T::A_BYTES + b * 8192, &tmk, it.half * N + 64 * b, it.kvh, row + 64 * s, bar);
+          }
+          __syncwarp();
+          if (++st == T::NS) {
+            st = 0;
+            ph ^= 1;
+          }
         }
+      };
+      if (it.dkv) {
+        // the chunk's row tiles that see either key tile; this split's share of them by count
+        const KeyTile ka = w.kt[it.t0], kb = w.kt[it.t0 + it.n - 1];
+        const int xs = max(0, x0 - it.kvh * hd.nrt), xe = min(hd.nrt, x1 - it.kvh * hd.nrt);
+        auto tile_of = [&](const KeyTile& t, const RowTile& r) -> int {      // its place in the row tile's list
+          if (t.block == 0) return t.idx >= r.a0 && t.idx < r.a0 + r.nA ? t.idx - r.a0 : -1;
+          return t.block == r.block && t.idx >= r.b0 && t.idx < r.b0 + r.nB ? r.nA + t.idx - r.b0 : -1;
+        };
+        int n = 0;
+#pragma unroll 4
+        for (int i = xs; i < xe; i += 32) {
+          bool see = false;
+          if (i + lane < xe) {
+            const RowTile r = load_row_tile(w.rt, i + lane);
+            see = tile_of(ka, r) >= 0 || tile_of(kb, r) >= 0;
+          }
+          n += __popc(__ballot_sync(0xffffffffu, see));
+        }
+        const int cuts = pa.piece ? max(1, min(pa.splits, n / pa.piece)) : pa.splits;
+        if (it.split >= cuts) continue;               // (no item for the others)
+        if (lane == 0 && it.half == 0 && it.kind == 0 && it.split == 0) w.pieces[it.t0 / 2 * nkv + it.kvh] = cuts;
+        const int v0 = (int)((long long)n * it.split / cuts), v1 = (int)((long long)n * (it.split + 1) / cuts);
+        left = 2 * (v1 - v0);
+        publish(id, left);
+        int seen = 0;
+        for (int i = xs; i < xe && seen < v1; i += 32) {
+          int j0 = -1, j1 = -1, row = 0;
+          if (i + lane < xe) {
+            const RowTile r = load_row_tile(w.rt, i + lane);
+            j0 = tile_of(ka, r);
+            j1 = it.n == 2 ? tile_of(kb, r) : -1;
+            const int base = (int)(slot0 + r.base);
+            j0 += j0 >= 0 ? base : 0;
+            j1 += j1 >= 0 ? base : 0;
+            row = r.row0;
+          }
+          uint32_t m = __ballot_sync(0xffffffffu, j0 >= 0 || j1 >= 0);
+          for (; m; m &= m - 1, ++seen) {
+            if (seen < v0) continue;
+            if (seen >= v1) break;
+            const int src = __ffs(m) - 1;
+            tile(__shfl_sync(0xffffffffu, j0, src), __shfl_sync(0xffffffffu, j1, src),
+                 __shfl_sync(0xffffffffu, row, src));
+          }
+        }
+      } else {
+        const RowTile r0 = load_row_tile(w.rt, it.t0);
+        RowTile r1 = load_row_tile(w.rt, it.t0 + it.n - 1);
+        if (it.n == 1) r1.nA = r1.nB = 0;
+        const int base0 = (int)(slot0 + r0.base), base1 = (int)(slot0 + r1.base);
+        // the key tiles either row tile sees: both lists merged, prefix then own block
+        auto walk = [&](auto f) {
+          auto range = [&](int lo0, int n0, int o0, int lo1, int n1, int o1, int row) {
+            const int lo = n0 == 0 ? lo1 : n1 == 0 ? lo0 : min(lo0, lo1), hi = max(n0 ? lo0 + n0 : 0, n1 ? lo1 + n1 : 0);
+            for (int x = lo; x < hi; ++x) {
+              const bool in0 = x >= lo0 && x < lo0 + n0, in1 = x >= lo1 && x < lo1 + n1;
+              if (in0 || in1) f(in0 ? o0 + x - lo0 : -1, in1 ? o1 + x - lo1 : -1, row + x * kT);
+            }
+          };
+          range(r0.a0, r0.nA, base0, r1.a0, r1.nA, base1, 0);
+          if (r0.block == r1.block) {
+            range(r0.b0, r0.nB, base0 + r0.nA, r1.b0, r1.nB, base1 + r1.nA, r0.off0);
+          } else {
+            range(r0.b0, r0.nB, base0 + r0.nA, 0, 0, 0, r0.off0);
+            range(0, 0, 0, r1.b0, r1.nB, base1 + r1.nA, r1.off0);
+          }
+        };
+        walk([&](int, int, int) { left += 2; });
+        publish(id, left);
+        walk(tile);
       }
-    } else {
-      const int slot = (int)(slot0 + rt.base);
-      for (int j = 0; j < v1; ++j) {
-        int pk, lp;
-        key_tile_at(rt, j, pk, lp);
-        stage(slot + j, 0, pk, 0);
-        stage(slot + j, 1, pk, 0);
-      }
+    }
+    publish(-1, 0);
+    wait(empty + st, ph ^ 1);
+    if (lane == 0) {
+      info[st] = kEnd;
+      mbar_arrive(full + st);
     }
   } else if (warp == kPrEpi + 1) {
     // ================= products =================
-    const uint32_t ID = tc::idesc_bf16_f32(kT, N) | kTransB | (dkv ? kTransA : 0u);
-    int st = 0, ph = 0;
-    for (int t = 0; t < steps; ++t) {
+    int st = 0, ph = 0, use = 0, started = 0;
+    for (;;) {
       wait(full + st, ph);
+      const int f = __shfl_sync(0xffffffffu, info[st], 0);   // (every lane is here before lane 0 goes on)
+      if ((f & kEnd) || wait.dead) break;
+      const int buf = use % T::NBUF;
+      if (f & kFirst) {
+        if (use >= T::NBUF) wait(acc_free + buf, (use / T::NBUF - 1) & 1);
+        started = 0;
+      }
       tc::fence_after_sync();
       if (lane == 0) {
-        const uint32_t as = sb + st * T::STAGE, bs = as + T::A_BYTES;
+        const uint32_t ID = tc::idesc_bf16_f32(kT, N) | kTransB | (f & kKeys ? kTransA : 0u);
+        const uint32_t bs = sb + st * T::STAGE + 2 * T::A_BYTES;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          tc::mma_f16(tmem, dkv ? smem_desc(as + 256 * s, 128, 1024, false) : smem_desc(as + 4096 * s, 2048, 128, false),
-                      smem_desc(bs + 2048 * s, 8192, 1024, true), ID, t > 0 || s > 0);
+        for (int t = 0; t < 2; ++t) {
+          if (!(f & (kTile0 << t))) continue;
+          const uint32_t as = sb + st * T::STAGE + t * T::A_BYTES, d = tmem + (buf * 2 + t) * N;
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            tc::mma_f16(d, f & kKeys ? smem_desc(as + 256 * s, 128, 1024, false) : smem_desc(as + 4096 * s, 2048, 128, false),
+                        smem_desc(bs + 2048 * s, 8192, 1024, true), ID, (started >> t & 1) || s > 0);
+        }
         tc::commit(empty + st);
-        if (t + 1 == steps) tc::commit(done);
+        if (f & kLast) {
+          got[buf] = started | (f & (kTile0 | kTile1));
+          tc::commit(done + buf);
+          mbar_arrive(done + buf);
+        }
       }
       __syncwarp();
+      started |= f & (kTile0 | kTile1);
+      if (f & kLast) ++use;
       if (++st == T::NS) {
         st = 0;
         ph ^= 1;
       }
     }
   } else {
-    // ================= out: thread = row =================
-    const int r = tid;
-    if (steps > 0) {
-      wait(done, 0);
-      tc::fence_after_sync();
-      __syncwarp();
-    }
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
-    size_t o;                                         // element offset of the row's first dim
-    bool valid;
-    if (dkv) {
-      valid = r < kt.n;
-      o = ((size_t)(kt.row0 + r) * a.L.n_kv + kvh) * D + half * N;
-    } else {
-      const int tq = r / G;
-      valid = tq < rt.nt;
-      o = ((size_t)(rt.row0 + tq) * a.L.n_q + kvh * G + r % G) * D + half * N;
-    }
-    const size_t plane = (size_t)a.n_rows * a.L.n_kv * D;
-    float* acc = w.acc + ((size_t)split * 2 + kind) * plane;
-    void* out = dkv ? (kind == 0 ? a.dk : a.dv) : a.dq;
-    const bool f32 = dkv && (!pg.direct || a.dkv_f32), add = dkv && (pg.direct ? a.accumulate != 0 : chunk > 0);
-    const bool vec = f32 ? !pg.direct || (reinterpret_cast<uintptr_t>(out) & 15u) == 0
-                         : (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-    float* of = pg.direct ? static_cast<float*>(out) : acc;
-    for (int c = 0; c < N / 16; ++c) {
-      float v[16];
+    // ================= out: warp = 32 rows of one tile of the pair =================
+    const int t = warp >> 2;
+    uint8_t* stg = sm + T::E_OFF + warp * 4096;
+    int e = 0, eph = 0, use = 0;
+    const size_t plane = (size_t)a.n_rows * nkv * D;
+    for (;;) {
+      wait(item_full + e, eph);
+      const int id = items[2 * e], steps = items[2 * e + 1];
+      if (id < 0 || wait.dead) break;
+      const Item it = decode(id);
+      const int buf = use % T::NBUF;
+      bool has = false;
       if (steps > 0) {
-        tc::ld_x16(lane_base + 16 * c, v);
-        tc::wait_ld();
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        wait(done + buf, (use / T::NBUF) & 1);
+        tc::fence_after_sync();
+        has = got[buf] >> t & 1;
       }
-      if (!valid) continue;
-      const size_t e = o + 16 * c;
-      if (f32) {
-        if (add && steps == 0) continue;
-        if (vec) {
+      __syncwarp();
+      // where the tile's rows go: row r at o + (r >> sh) * big + (r & ((1 << sh) - 1)) * D
+      size_t o = 0, big;
+      int rows = 0, sh;
+      if (it.dkv) {
+        sh = 0;
+        big = (size_t)nkv * D;
+        if (t < it.n) {
+          const KeyTile k = w.kt[it.t0 + t];
+          rows = k.n;
+          o = ((size_t)k.row0 * nkv + it.kvh) * D;
+        }
+      } else {
+        sh = 31 - __clz(G);
+        big = (size_t)a.L.n_q * D;
+        if (t < it.n) {
+          const RowTile r = load_row_tile(w.rt, it.t0 + t);
+          rows = r.nt * G;
+          o = ((size_t)r.row0 * a.L.n_q + it.kvh * G) * D;
+        }
+      }
+      o += it.half * N;
+      auto at = [&](int r) { return o + (size_t)(r >> sh) * big + (size_t)(r & ((1 << sh) - 1)) * D; };
+      void* out = it.dkv ? (it.kind == 0 ? a.dk : a.dv) : a.dq;
+      const bool part = it.dkv && !pa.direct, f32 = part || (it.dkv && a.dkv_f32);
+      const bool add = it.dkv && (pa.direct ? a.accumulate != 0 : pa.chunk > 0);
+      if (part) out = w.acc + ((size_t)it.split * 2 + it.kind) * plane;
+      const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+      const int r0 = 32 * (warp & 3);
+      const uint32_t ta = tmem + ((uint32_t)r0 << 16) + (buf * 2 + t) * N;
+      const bool write = rows > r0 && (has || !add);
+      for (int c = 0; c < N && write; c += 32) {
+        float v[32];
+        if (has) {
+          ld_x32(ta + c, v);
+          tc::wait_ld();
+        } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float4* p = reinterpret_cast<float4*>(of + e) + i;
-            float4 x = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            if (add) {
-              const float4 y = *p;
-              x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        if (!vec) {                                   // an output that is only aligned to its elements
+          if (r0 + lane < rows) {
+            const size_t p = at(r0 + lane) + c;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (f32) static_cast<float*>(out)[p + i] = add ? static_cast<float*>(out)[p + i] + v[i] : v[i];
+              else static_cast<uint16_t*>(out)[p + i] = f_to_bf16_rn(v[i]);
             }
-            *p = x;
+          }
+          continue;
+        }
+        // through shared memory, so that 8 (4) lanes write a row's 128 (64) bytes
+        if (f32) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          __syncwarp();
+          const int q = lane & 7;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            float4 x = *reinterpret_cast<const float4*>(stg + r * 128 + ((q ^ (r & 7)) << 4));
+            if (r0 + r < rows) {
+              float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at(r0 + r) + c + 4 * q);
+              if (add) {
+                const float4 y = *p;
+                x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+              }
+              *p = x;
+            }
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) of[e + i] = add ? of[e + i] + v[i] : v[i];
-        }
-      } else {
-        uint16_t* p = static_cast<uint16_t*>(out) + e;
-        if (vec) {
-          uint32_t u[8];
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(stg + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) =
+                make_uint4(pack_bf2(v[8 * q], v[8 * q + 1]), pack_bf2(v[8 * q + 2], v[8 * q + 3]),
+                           pack_bf2(v[8 * q + 4], v[8 * q + 5]), pack_bf2(v[8 * q + 6], v[8 * q + 7]));
+          __syncwarp();
+          const int q = lane & 3;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) u[i] = pack_bf2(v[2 * i], v[2 * i + 1]);
-          reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-          reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = f_to_bf16_rn(v[i]);
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const uint4 x = *reinterpret_cast<const uint4*>(stg + r * 64 + ((q ^ (r >> 1 & 3)) << 4));
+            if (r0 + r < rows) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at(r0 + r) + c + 8 * q) = x;
+          }
         }
+        __syncwarp();
+      }
+      if (steps > 0) {
+        tc::fence_before_sync();
+        ++use;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (steps > 0) mbar_arrive(acc_free + buf);
+        mbar_arrive(item_empty + e);
+      }
+      if (++e == 2) {
+        e = 0;
+        eph ^= 1;
       }
     }
   }
@@ -944,48 +1117,57 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const Pro
   __syncthreads();
   if (warp == 0) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, N);
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
 // ---------------------------------------------------------------------------
 // finish: dk and dv over the splits, in split order
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) bwd_finish_kernel(const TrainBwdArgs a, const Ws w, const int splits) {
+__global__ void __launch_bounds__(256) bwd_finish_kernel(const TrainBwdArgs a, const Ws w) {
   pdl_wait();
   pdl_launch();
-  if (!w.head->ok) return;
+  const int nkt = w.head->nkt;                        // (0 for a layout that breaks the rules)
   const size_t plane = (size_t)a.n_rows * a.L.n_kv * a.L.D;
-  const int kind = blockIdx.y;
+  const int kind = blockIdx.z, D = a.L.D;
   void* out = kind == 0 ? a.dk : a.dv;
   const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-  for (size_t e = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; e < plane; e += (size_t)gridDim.x * 1024) {
-    float4 s = *reinterpret_cast<const float4*>(w.acc + kind * plane + e);
-    for (int i = 1; i < splits; ++i) {
-      const float4 y = *reinterpret_cast<const float4*>(w.acc + ((size_t)i * 2 + kind) * plane + e);
-      s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
-    }
-    const float v[4] = {s.x, s.y, s.z, s.w};
-    if (a.dkv_f32) {
-      float* p = static_cast<float*>(out) + e;
-      if (vec) {
-        float4 x = s;
-        if (a.accumulate) {
-          const float4 y = *reinterpret_cast<float4*>(p);
-          x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
-        }
-        *reinterpret_cast<float4*>(p) = x;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = a.accumulate ? p[i] + v[i] : v[i];
+  // block (x, y): key tiles x, x + grid, ..., a share y of their rows
+  for (int t = blockIdx.x; t < nkt; t += gridDim.x) {
+    const KeyTile k = w.kt[t];
+    const int per = kT / gridDim.y, r0 = blockIdx.y * per, quads = min(per, k.n - r0) * a.L.n_kv * (D / 4);
+    for (int q = threadIdx.x; q < quads; q += 256) {
+      const int col = q % (a.L.n_kv * (D / 4));
+      const int pieces = w.pieces[t / 2 * a.L.n_kv + col / (D / 4)];
+      const size_t e = ((size_t)(k.row0 + r0) * a.L.n_kv * (D / 4) + q) * 4;
+      float4 s = *reinterpret_cast<const float4*>(w.acc + kind * plane + e);
+#pragma unroll 4
+      for (int i = 1; i < pieces; ++i) {
+        const float4 y = *reinterpret_cast<const float4*>(w.acc + ((size_t)i * 2 + kind) * plane + e);
+        s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
       }
-    } else {
-      uint16_t* p = static_cast<uint16_t*>(out) + e;
-      if (vec) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
-      } else {
+      const float v[4] = {s.x, s.y, s.z, s.w};
+      if (a.dkv_f32) {
+        float* p = static_cast<float*>(out) + e;
+        if (vec) {
+          float4 x = s;
+          if (a.accumulate) {
+            const float4 y = *reinterpret_cast<float4*>(p);
+            x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+          }
+          *reinterpret_cast<float4*>(p) = x;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = f_to_bf16_rn(v[i]);
+          for (int i = 0; i < 4; ++i) p[i] = a.accumulate ? p[i] + v[i] : v[i];
+        }
+      } else {
+        uint16_t* p = static_cast<uint16_t*>(out) + e;
+        if (vec) {
+          *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = f_to_bf16_rn(v[i]);
+        }
       }
     }
   }
@@ -1000,7 +1182,7 @@ bool map_bf16(CUtensorMap* m, const void* base, int D, int heads, int rows, int 
 template <int D>
 cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t st) {
   constexpr int N = prod_n(D), H = D / N;
-  static_assert(Sc<D>::BYTES <= 227 * 1024 && 2 * Pr<N>::BYTES <= 226 * 1024, "shared memory");
+  static_assert(Sc<D>::BYTES <= 227 * 1024 && Pr<N>::BYTES <= 227 * 1024, "shared memory");
   cudaError_t e;
   static std::atomic<bool> attr_set[64];
   static std::mutex attr_mu;
@@ -1018,47 +1200,41 @@ cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t
     }
   }
   const LayerArgs& L = a.L;
-  const Plan p = make_plan(L, a.n_blocks, a.n_rows, a.max_block_rows);
+  const Plan p = make_plan(L, a.n_blocks, a.n_rows, a.max_block_rows, num_sms);
   const Ws w = carve(wsp, p);
   const int TQ = kT / L.G;
   // boxes: 128 (token, head) pairs and 128 keys for the scores, 64 for the products
   // (with one q head per tile row the 64-pair box is half the tokens; TQ >= 8)
-  CUtensorMap q1, o1, k1, v1, q2, o2, k2;
+  CUtensorMap q1, o1, k1, v1, q2, o2, k2, pm, dm;
   if (!map_bf16(&q1, a.q, D, L.n_q, a.n_rows, L.G, TQ) || !map_bf16(&o1, a.d_out, D, L.n_q, a.n_rows, L.G, TQ) ||
       !map_bf16(&k1, a.k, D, L.n_kv, a.n_rows, 1, kT) || !map_bf16(&v1, a.v, D, L.n_kv, a.n_rows, 1, kT) ||
       !map_bf16(&q2, a.q, D, L.n_q, a.n_rows, L.G, TQ / 2) || !map_bf16(&o2, a.d_out, D, L.n_q, a.n_rows, L.G, TQ / 2) ||
-      !map_bf16(&k2, a.k, D, L.n_kv, a.n_rows, 1, 64))
+      !map_bf16(&k2, a.k, D, L.n_kv, a.n_rows, 1, 64) || !runs_map(&pm, w.p, 2, kT / 8, p.cap) ||
+      !runs_map(&dm, w.ds, 2, kT / 8, p.cap))
     return cudaErrorInvalidValue;
   const long long pairs = (long long)a.n_rows * L.n_q;
   const int prep_blocks = 1 + (int)std::min<long long>(cdiv(pairs, kPrepThreads / 32), 8LL * num_sms);
   if ((e = launch_pdl(bwd_prep_kernel<D>, dim3(prep_blocks), dim3(kPrepThreads), 0, st, a, w, p.cap, p.nl)) !=
       cudaSuccess)
     return e;
-  ProdGrid pg;
-  pg.n_kt = p.nkt;
-  pg.n_rt = (int)std::min<long long>((long long)p.nrt * L.n_kv, p.cap);
-  pg.splits = p.splits;
-  pg.direct = p.nl == 1 && p.splits == 1;
-  const long long items = (long long)pg.n_kt * L.n_kv * 2 * H * pg.splits + (long long)pg.n_rt * H;
+  const long long items = cdiv(p.nkt, 2) * p.splits * L.n_kv * 2 * H + std::min<long long>((long long)p.nrt * L.n_kv, p.cap) * H;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   for (int c = 0; c < p.nl; ++c) {
     if ((e = launch_pdl(bwd_scores_kernel<D>, dim3(std::min(num_sms, p.cap)), dim3(kScThreads), (size_t)Sc<D>::BYTES, st,
                         a, w, c, q1, o1, k1, v1)) != cudaSuccess)
       return e;
-    if ((e = launch_pdl(bwd_products_kernel<D>, dim3((unsigned)items), dim3(kPrThreads), (size_t)Pr<N>::BYTES, st, a, w,
-                        c, pg, q2, o2, k2)) != cudaSuccess)
+    if ((e = launch_pdl(bwd_products_kernel<D>, dim3((unsigned)std::min<long long>(num_sms, items)), dim3(kPrThreads),
+                        (size_t)Pr<N>::BYTES, st, a, w, ProdArgs{c, p.splits, p.nl == 1 ? p.piece : 0, p.direct}, q2, o2, k2, pm, dm)) != cudaSuccess)
       return e;
   }
-  if (pg.direct) return cudaSuccess;
-  const long long quads = (long long)a.n_rows * L.n_kv * D / 4;
-  return launch_pdl(bwd_finish_kernel, dim3((unsigned)std::min<long long>(cdiv(quads, 256), 4LL * num_sms), 2),
-                    dim3(256), 0, st, a, w, p.splits);
+  if (p.direct) return cudaSuccess;
+  return launch_pdl(bwd_finish_kernel, dim3(std::min(p.nkt, 4 * num_sms), 16, 2), dim3(256), 0, st, a, w);
 }
 
 }  // namespace
 
 size_t train_bwd_ws_bytes(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows) {
-  return make_plan(L, n_blocks, n_rows, max_block_rows).bytes;
+  return make_plan(L, n_blocks, n_rows, max_block_rows, 1).bytes;      // (the SM count sets the splits alone)
 }
 
 cudaError_t launch_train_bwd(const TrainBwdArgs& a, void* ws, int num_sms, cudaStream_t st) {
