@@ -423,19 +423,31 @@ struct Waiter {
 // scores: P and dS of one chunk's tiles
 // ---------------------------------------------------------------------------
 
+// A CTA takes a run of the chunk's tile list and works on units of one or two
+// key tiles of a row tile: an MMA of 256 columns reads 12 KB of shared memory in
+// 128 cycles, one of 128 columns 8 KB in 64, which with the copies' writes is
+// more than shared memory gives (measured: half the rate).  S and dP of a unit
+// fill tensor memory; the two halves alternate: while the epilogue turns S into
+// P, dP is multiplied, and while it turns dP into dS, the next unit's S.
 template <int D>
 struct Sc {
   static constexpr int NG = D / 64;
   static constexpr bool RES = D <= 256;               // q and dO of the row tile stay in shared memory
-  static constexpr int STAGE = RES ? 16384 : 32768;   // a 64-dim slice of k or v (with q's or dO's beside it)
-  static constexpr int NS = D == 256 ? 6 : D == 512 ? 6 : 8;
+  static constexpr int STAGE = RES ? 32768 : 49152;   // 64 dims of k or v, two tiles (with q's or dO's behind)
+  static constexpr int NS = D == 256 ? 3 : 4;
   static constexpr int A_OFF = 0;                     // q, then dO: NG blocks each of [128 rows x 128 B]
   static constexpr int R_OFF = RES ? 2 * NG * 16384 : 0;
   static constexpr int C_OFF = R_OFF + NS * STAGE;
   static constexpr int BYTES = C_OFF + 256 + 1024;    // + room to align the base
 };
-constexpr int kScEpi = 16;                            // epilogue warps
+// Eight epilogue warps, a key tile of the unit per four; a thread's 128 P wait for
+// dP as pairs of f16 times 2^15: 11 bits of every P above 2^-29 (8 times finer
+// than the bf16 dS they end in), in half the registers of fp32.  Nothing may
+// spill here: shared memory leaves so little L1 that a reload goes to L2 (with
+// sixteen warps of 96 registers the epilogue took 10k cycles a unit for that).
+constexpr int kScEpi = 8;
 constexpr int kScThreads = (kScEpi + 2) * 32;
+constexpr float kPScale = 32768.f;
 
 // The tiles of a CTA's run in list order.
 struct Walk {
@@ -491,7 +503,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
   uint64_t* empty = full + T::NS;
   uint64_t* a_full = empty + T::NS;                   // q and dO landed
   uint64_t* a_free = a_full + 1;                      // the row tile's products are done
-  uint64_t* acc_full = a_free + 1;                    // [2] S and dP of a tile done
+  uint64_t* acc_full = a_free + 1;                    // [2] a unit's S, its dP done
   uint64_t* acc_free = acc_full + 2;                  // [2] read by the epilogue
   uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + 2);
   if (tid == 0) {
@@ -534,8 +546,10 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
       k.t = load_row_tile(w.rt, k.i);
       k.j = rem - k.t.base;
     }
-    auto next = [&]() -> bool {                       // to the next tile; true: another row tile
-      if (++k.j < k.t.nA + k.t.nB) return false;
+    // tiles of the unit at list place g, and the step past it (true: another row tile)
+    auto unit = [&](int g) { return g + 1 < g1 && k.j + 1 < k.t.nA + k.t.nB ? 2 : 1; };
+    auto next = [&](int tiles) -> bool {
+      if ((k.j += tiles) < k.t.nA + k.t.nB) return false;
       k.j = 0;
       if (++k.i == nrt) {
         k.i = 0;
@@ -549,9 +563,11 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
       // ================= copies =================
       int st = 0, ph = 0, rts = 0;                    // ring stage, its phase; row tiles begun
       bool fresh = true;
-      for (int g = g0; g < g1; ++g) {
-        int pk, lp;
-        key_tile_at(k.t, k.j, pk, lp);
+      for (int g = g0; g < g1;) {
+        const int tiles = unit(g);
+        int pk[2], lp;
+        key_tile_at(k.t, k.j, pk[0], lp);
+        if (tiles == 2) key_tile_at(k.t, k.j + 1, pk[1], lp);
         if (T::RES && fresh) {
           if (rts > 0) wait(a_free, (rts - 1) & 1);
           if (lane == 0) {
@@ -568,9 +584,10 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
           if (lane == 0) {
             const int dim = 64 * (c < NG ? c : c - NG);
             const uint32_t dst = sb + T::R_OFF + st * T::STAGE, bar = smem_u32(full + st);
-            mbar_arrive_expect_tx(full + st, T::STAGE);
-            tc::tma_load_3d(dst, c < NG ? &tmk : &tmv, dim, k.kvh, pk, bar);
-            if (!T::RES) tc::tma_load_3d(dst + 16384, c < NG ? &tmq : &tmo, dim, k.kvh * G, k.t.row0, bar);
+            mbar_arrive_expect_tx(full + st, (tiles + (T::RES ? 0 : 1)) * 16384);
+            if (!T::RES) tc::tma_load_3d(dst + 32768, c < NG ? &tmq : &tmo, dim, k.kvh * G, k.t.row0, bar);
+            tc::tma_load_3d(dst, c < NG ? &tmk : &tmv, dim, k.kvh, pk[0], bar);
+            if (tiles == 2) tc::tma_load_3d(dst + 16384, c < NG ? &tmk : &tmv, dim, k.kvh, pk[1], bar);
           }
           __syncwarp();
           if (++st == T::NS) {
@@ -578,29 +595,31 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
             ph ^= 1;
           }
         }
-        fresh = g + 1 < g1 && next();
+        g += tiles;
+        fresh = g < g1 && next(tiles);
       }
     } else if (warp == kScEpi + 1) {
       // ================= S = q k^T, dP = dO v^T =================
-      constexpr uint32_t ID = tc::idesc_bf16_f32(kT, kT);
-      int st = 0, ph = 0, rts = 0;
+      int st = 0, ph = 0, rts = 0, n = 0;
       bool fresh = true;
-      for (int g = g0; g < g1; ++g) {
-        const int n = g - g0, slot = n & 1;
+      for (int g = g0; g < g1; ++n) {
+        const int tiles = unit(g);
+        const uint32_t ID = tc::idesc_bf16_f32(kT, kT) + (tiles == 2 ? tc::idesc_bf16_f32(kT, 2 * kT) - tc::idesc_bf16_f32(kT, kT) : 0u);
         if (T::RES && fresh) wait(a_full, rts++ & 1);
-        if (n >= 2) wait(acc_free + slot, ((n >> 1) - 1) & 1);
         for (int c = 0; c < 2 * NG; ++c) {
+          const int half = c >= NG;
+          if (n > 0 && (c == 0 || c == NG)) wait(acc_free + half, (n - 1) & 1);
           wait(full + st, ph);
           tc::fence_after_sync();
           if (lane == 0) {
             const uint32_t bs = sb + T::R_OFF + st * T::STAGE;
-            const uint32_t as = T::RES ? sb + T::A_OFF + c * 16384 : bs + 16384;
-            const uint32_t d = tmem + 256 * slot + (c < NG ? 0 : kT);
+            const uint32_t as = T::RES ? sb + T::A_OFF + c * 16384 : bs + 32768;
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              tc::mma_f16(d, tc::desc_kmajor_sw128(as + 32 * s, 1024), tc::desc_kmajor_sw128(bs + 32 * s, 1024), ID,
-                          (c != 0 && c != NG) || s != 0);
+              tc::mma_f16(tmem + 256 * half, tc::desc_kmajor_sw128(as + 32 * s, 1024),
+                          tc::desc_kmajor_sw128(bs + 32 * s, 1024), ID, (c != 0 && c != NG) || s != 0);
             tc::commit(empty + st);
+            if (c == NG - 1 || c == 2 * NG - 1) tc::commit(acc_full + half);
           }
           __syncwarp();
           if (++st == T::NS) {
@@ -608,21 +627,22 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
             ph ^= 1;
           }
         }
-        if (lane == 0) tc::commit(acc_full + slot);
-        fresh = g + 1 < g1 && next();
+        g += tiles;
+        fresh = g < g1 && next(tiles);
         if (T::RES && fresh && lane == 0) tc::commit(a_free);
         __syncwarp();
       }
     } else {
-      // ================= P and dS: thread = row, 32 of the tile's keys =================
-      const int r = 32 * (warp & 3) + lane, qt = warp >> 2, W = a.L.window;
+      // ================= P and dS: thread = row, one key tile of the unit =================
+      const int r = 32 * (warp & 3) + lane, mine = warp >> 2, W = a.L.window;
       const int tq = r / G, h = r % G;
-      const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32 * qt;
-      float lse2 = 0.f, delta = 0.f;
+      const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kT * mine;
+      float lse2 = 0.f, delta = 0.f;                  // log2(e) lse, delta / 2^15
       int lo = 0, hi = -1, cut = -1;                  // visible positions: lo .. hi, in prefix tiles lo .. cut
       bool fresh = true;
-      for (int g = g0; g < g1; ++g) {
-        const int n = g - g0, slot = n & 1;
+      int n = 0;
+      for (int g = g0; g < g1; ++n) {
+        const int tiles = unit(g);
         if (fresh) {
           const bool valid = tq < k.t.nt;
           const int pos = k.t.pos0 + tq;
@@ -632,54 +652,83 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
           if (valid) {
             const size_t o = (size_t)(k.t.row0 + tq) * a.L.n_q + k.kvh * G + h;
             lse2 = __ldg(a.lse + o) * kL2E;
-            delta = w.delta[o];
+            delta = w.delta[o] * (1.f / kPScale);
           }
         }
+        const bool busy = mine < tiles;
         int pk, lp;
-        key_tile_at(k.t, k.j, pk, lp);
-        const int p0 = lp + 32 * qt, top = k.j < k.t.nA ? cut : hi;
-        const size_t at = (size_t)g * kTileBytes + (size_t)qt * 8192 + r * 16;
-        uint8_t* pt = w.p + at;
-        uint8_t* dt = w.ds + at;
-        wait(acc_full + slot, (n >> 1) & 1);
+        key_tile_at(k.t, k.j + mine, pk, lp);
+        const int top = k.j + mine < k.t.nA ? cut : hi;
+        // (a row that sees one key does not see 128: it always takes the masked form)
+        const bool whole = __all_sync(0xffffffffu, lp >= lo && lp + kT - 1 <= top);
+        const size_t at = (size_t)(g + mine) * kTileBytes + r * 16;
+        uint32_t ph[kT / 2];
+        wait(acc_full, n & 1);
         tc::fence_after_sync();
         __syncwarp();
-        float S[32], dP[32];
-        ld_x32(lane_base + 256 * slot, S);
-        ld_x32(lane_base + 256 * slot + kT, dP);
-        tc::wait_ld();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_free + slot);  // the slot is read
-        auto emit = [&](auto masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pw[4], dw[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float p[2], d[2];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int i = 8 * c + 2 * e + u;
-                p[u] = ex2(fmaf(S[i], kL2E, -lse2));
-                d[u] = p[u] * (dP[i] - delta);
-                if constexpr (decltype(masked)::value) {
-                  const bool vis = p0 + i >= lo && p0 + i <= top;
-                  p[u] = vis ? p[u] : 0.f;
-                  d[u] = vis && lo < hi ? d[u] : 0.f;  // lo == hi: the row sees one key
-                }
-              }
-              pw[e] = pack_bf2(p[0], p[1]);
-              dw[e] = pack_bf2(d[0], d[1]);
-            }
-            *reinterpret_cast<uint4*>(pt + c * 2048) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-            *reinterpret_cast<uint4*>(dt + c * 2048) = make_uint4(dw[0], dw[1], dw[2], dw[3]);
+        for (int q = 0; q < kT / 16; ++q) {
+          float p[16];
+          if (busy) {
+            tc::ld_x16(ts + 16 * q, p);
+            tc::wait_ld();
           }
-        };
-        // (a row that sees one key sees no 32 keys: it always takes the masked form)
-        if (__all_sync(0xffffffffu, p0 >= lo && p0 + 31 <= top)) emit(std::false_type{});
-        else emit(std::true_type{});
-        fresh = g + 1 < g1 && next();
+          if (q == kT / 16 - 1) {                               // S is read
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_free);
+          }
+          if (busy) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] = ex2(fmaf(p[i], kL2E, -lse2));
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) p[i] = lp + 16 * q + i >= lo && lp + 16 * q + i <= top ? p[i] : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<uint4*>(w.p + at + (2 * q + c) * 2048) =
+                  make_uint4(pack_bf2(p[8 * c], p[8 * c + 1]), pack_bf2(p[8 * c + 2], p[8 * c + 3]),
+                             pack_bf2(p[8 * c + 4], p[8 * c + 5]), pack_bf2(p[8 * c + 6], p[8 * c + 7]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ph[8 * q + i] = pack_h2(p[2 * i] * kPScale, p[2 * i + 1] * kPScale);
+          }
+        }
+        if (!whole && lo >= hi) {                     // one key: dS = 0
+#pragma unroll
+          for (int i = 0; i < kT / 2; ++i) ph[i] = 0u;
+        }
+        wait(acc_full + 1, n & 1);
+        tc::fence_after_sync();
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < kT / 16; ++q) {
+          float d[16];
+          if (busy) {
+            tc::ld_x16(ts + 256 + 16 * q, d);
+            tc::wait_ld();
+          }
+          if (q == kT / 16 - 1) {                               // dP is read
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_free + 1);
+          }
+          if (busy) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&ph[8 * q + i]));
+              d[2 * i] = p.x * fmaf(d[2 * i], 1.f / kPScale, -delta);
+              d[2 * i + 1] = p.y * fmaf(d[2 * i + 1], 1.f / kPScale, -delta);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<uint4*>(w.ds + at + (2 * q + c) * 2048) =
+                  make_uint4(pack_bf2(d[8 * c], d[8 * c + 1]), pack_bf2(d[8 * c + 2], d[8 * c + 3]),
+                             pack_bf2(d[8 * c + 4], d[8 * c + 5]), pack_bf2(d[8 * c + 6], d[8 * c + 7]));
+          }
+        }
+        g += tiles;
+        fresh = g < g1 && next(tiles);
       }
     }
   }

@@ -6,6 +6,7 @@ import numpy as np
 
 import oracle as O
 
+F16 = 2.0 ** -11        # of an f16 rounding
 BF16 = 2.0 ** -8        # half a step of a bf16 rounding, relative to the value
 F32 = 2.0 ** -24
 TINY = 2.0 ** -126      # the smallest normal float: a smaller P may be taken as 0
@@ -26,7 +27,10 @@ def read_bounds(q, k, v, do, g, out_err=0.0, lse_err=0.0):
     by 4 F32 of itself.  P and dS each enter a product rounded to bf16; a sum
     of n products in fp32 adds n F32 of the sum of their sizes.  P below the
     smallest normal float, TINY, may be flushed to 0 by the exponential: P is
-    off by TINY at most beside the relative errors, dS by TINY (|dP| + |delta|)."""
+    off by TINY at most beside the relative errors, dS by TINY (|dP| + |delta|).
+    For dS, P is rounded to f16 times 2^15 first: off by F16 of itself, or by
+    half the smallest f16 step, 2^-25, over 2^15 where it is subnormal there
+    (2^-40, which holds TINY too)."""
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     G = Hq // Hkv
@@ -40,7 +44,7 @@ def read_bounds(q, k, v, do, g, out_err=0.0, lse_err=0.0):
             e_dp = D * F32 * (ado[:, h] @ av[:, kvh].T)
             e_delta = D * F32 * (ado[:, h] * aout[:, h]).sum(1) + (ado[:, h] * out_err * aout[:, h]).sum(1)
             size = ado[:, h] @ av[:, kvh].T + (ado[:, h] * aout[:, h]).sum(1)[:, None]     # >= |dP| + |delta|
-            e_ds = ds * (BF16 + e_p) + TINY * (p > 0) * size + p * (1 + BF16 + e_p) * (e_dp + e_delta[:, None])
+            e_ds = ds * (BF16 + F16 + e_p) + 2.0 ** -40 * (p > 0) * size + p * (1 + BF16 + F16 + e_p) * (e_dp + e_delta[:, None])
             one = (p > 0).sum(1) == 1                       # one visible key: dS is 0
             e_ds[one] = 0.0
             n = T * G * F32
