@@ -1069,7 +1069,7 @@ kvq_status kvq_train_prep_backward(const kvq_layer* layer, int32_t n_blocks, con
   a.dv_raw = dv_raw;
   a.dk_w = dk_norm_w;
   const kvq::RopeFreqs& f = rope_freqs(layer->rope_theta, a.L.D, a.L.rope_dims);
-  const cudaError_t e = kvq::launch_prep_bwd(a, f, workspace, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = kvq::launch_prep_bwd(a, f, workspace, num_sms_current(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kvq_train_prep_backward launch");
   return KVQ_OK;
 }

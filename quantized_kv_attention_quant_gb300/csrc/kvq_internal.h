@@ -195,7 +195,7 @@ struct PrepBwdArgs {
   float* dk_w;
 };
 size_t prep_bwd_ws_bytes(const LayerArgs& L);
-cudaError_t launch_prep_bwd(const PrepBwdArgs& a, const RopeFreqs& f, void* ws, cudaStream_t st);
+cudaError_t launch_prep_bwd(const PrepBwdArgs& a, const RopeFreqs& f, void* ws, int num_sms, cudaStream_t st);
 // One CTA whose bounded wait on an mbarrier that nothing completes gives up
 // after limit_ns and flags the timeout bit in *status.
 cudaError_t launch_wait_selftest(uint32_t* status, unsigned long long limit_ns, cudaStream_t st);

@@ -8,13 +8,16 @@
 // row and their dx are added before the one rounding to bf16.  The forward's
 // roundings pass the gradient through.
 //
-// One pass over memory: x, dz in, dx out (6 bytes an element with bf16 dz).
-// A block takes `rb` rows at a time: it evaluates the rows' rotation angles
-// once for all heads into shared memory, then each warp takes one (row, head)
-// at a time, VEC consecutive dims of a lane per 16-byte access.  The rotation's
-// partner of a dim sits a fixed number of lanes away (one shuffle).  dw stays
-// in registers over all rows of a warp, goes to one partial row per block and
-// is summed over the blocks in block order by a second small kernel.
+// One pass over memory: x, dz in, dx out (6 bytes an element with bf16 dz); that
+// traffic bounds it, so the layout is for loads in flight and few instructions.
+// Every warp works alone: it takes units of one row and a run of its heads (q
+// heads on some of a block's warps, a donor's keys and values on the others),
+// evaluates the row's angles once, keeps the (cos, sin) of its own dims in
+// registers for all heads, and holds the next heads' x and dz in flight.  VEC
+// consecutive dims of a lane per 16-byte access; the rotation's partner of a dim
+// sits a fixed number of lanes away (one shuffle).  dw stays in registers over
+// all rows of a warp, goes to one partial row per block and is summed over the
+// blocks in block order by a second small kernel.
 #include <algorithm>
 
 #include "kvq_common.cuh"
@@ -25,12 +28,11 @@ namespace kvq {
 namespace {
 
 constexpr int kPbWarps = 8;
-constexpr int kPbMaxRows = 16;          // rows of a block per step
 
 // cos and sin of p f (f the exact sum of three floats, 0 <= p < 2^24) to
-// about 1e-7: p f and its distance to the nearest multiple of pi/2 in
-// float-float (two_prod exact, pi/2 in three floats), then the library's
-// sine and cosine of the remainder.
+// about 1e-7: p f and its distance r to the nearest multiple of pi/2 in
+// float-float (two_prod exact, pi/2 in three floats), then the Taylor series of
+// sine and cosine (|r| <= pi/4: the terms left out are below 2e-9 and 6e-10).
 __device__ __forceinline__ float2 rope_cos_sin_f32(int p, float f1, float f2, float f3) {
   const float P = (float)p;
   const ff a1 = two_prod(P, f1), a2 = two_prod(P, f2);
@@ -41,9 +43,11 @@ __device__ __forceinline__ float2 rope_cos_sin_f32(int p, float f1, float f2, fl
   ff_accum(r, -b1.lo);
   ff_accum(r, a2.hi);
   ff_accum(r, -b2.hi);
-  const float rr = r.hi + (r.lo + (fmaf(P, f3, a2.lo) - fmaf(k, KVQ_PIO2_3, b2.lo)));
-  float s, c;
-  sincosf(rr, &s, &c);
+  const float x = r.hi + (r.lo + (fmaf(P, f3, a2.lo) - fmaf(k, KVQ_PIO2_3, b2.lo)));
+  const float z = x * x;
+  const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f),
+                               -0.5f), 1.f);
   const int q = (int)k & 3;
   const float cc = q & 1 ? s : c, ss = q & 1 ? c : s;
   return make_float2(q == 1 || q == 2 ? -cc : cc, q >= 2 ? -ss : ss);
@@ -57,28 +61,31 @@ struct Pb {
   __host__ __device__ static constexpr int dim(int c, int lane) { return (c * 32 + lane) * VEC; }
 };
 
+// a lane's E bf16 of a row as they are stored, two to a word
 template <int D>
-__device__ __forceinline__ void load_bf16(const uint16_t* row, int lane, float (&v)[D / 32]) {
+__device__ __forceinline__ void load_raw(const uint16_t* row, int lane, uint32_t (&w)[D / 64]) {
   using T = Pb<D>;
 #pragma unroll
   for (int c = 0; c < T::NC; ++c) {
     const uint16_t* p = row + (c * 32 + lane) * T::VEC;
-    uint32_t w[T::VEC / 2];
-    if constexpr (T::VEC == 8) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-    } else if constexpr (T::VEC == 4) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = u.x; w[1] = u.y;
-    } else {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    }
-#pragma unroll
-    for (int i = 0; i < T::VEC / 2; ++i) {
-      v[c * T::VEC + 2 * i] = bf16lo_to_f(w[i]);
-      v[c * T::VEC + 2 * i + 1] = bf16hi_to_f(w[i]);
-    }
+    if constexpr (T::VEC == 8) *reinterpret_cast<uint4*>(w + 4 * c) = *reinterpret_cast<const uint4*>(p);
+    else if constexpr (T::VEC == 4) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    else w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
+}
+template <int D>
+__device__ __forceinline__ void unpack(const uint32_t (&w)[D / 64], float (&v)[D / 32]) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    v[2 * i] = bf16lo_to_f(w[i]);
+    v[2 * i + 1] = bf16hi_to_f(w[i]);
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_bf16(const uint16_t* row, int lane, float (&v)[D / 32]) {
+  uint32_t w[D / 64];
+  load_raw<D>(row, lane, w);
+  unpack<D>(w, v);
 }
 template <int D>
 __device__ __forceinline__ void load_f32(const float* row, int lane, float (&v)[D / 32]) {
@@ -99,6 +106,10 @@ __device__ __forceinline__ void load_f32(const float* row, int lane, float (&v)[
     }
   }
 }
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
 template <int D>
 __device__ __forceinline__ void store_bf16(uint16_t* row, int lane, const float (&v)[D / 32]) {
   using T = Pb<D>;
@@ -107,7 +118,7 @@ __device__ __forceinline__ void store_bf16(uint16_t* row, int lane, const float 
     uint32_t w[T::VEC / 2];
 #pragma unroll
     for (int i = 0; i < T::VEC / 2; ++i)
-      w[i] = (uint32_t)f_to_bf16_rn(v[c * T::VEC + 2 * i]) | ((uint32_t)f_to_bf16_rn(v[c * T::VEC + 2 * i + 1]) << 16);
+      w[i] = bf16_pair(v[c * T::VEC + 2 * i], v[c * T::VEC + 2 * i + 1]);
     uint16_t* p = row + (c * 32 + lane) * T::VEC;
     if constexpr (T::VEC == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     else if constexpr (T::VEC == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
@@ -115,37 +126,42 @@ __device__ __forceinline__ void store_bf16(uint16_t* row, int lane, const float 
   }
 }
 
+// How a lane finds the partners of its dims in the rotation of `rope` dims.
+enum : int { kNoRope, kLanes, kChunks, kAny };   // none; whole lanes apart in chunk 0; chunk 0 with chunk 1; else
+
+template <int D>
+__device__ __forceinline__ int rope_kind(int rope) {
+  using T = Pb<D>;
+  const int half = rope >> 1;
+  if (half == 0) return kNoRope;
+  if (half % T::VEC == 0 && 2 * (half / T::VEC) <= 32) return kLanes;
+  if (T::NC == 2 && half == 32 * T::VEC) return kChunks;
+  return kAny;
+}
+
 // dz -> R^T dz in place: of a pair (j, j + half) at angle (c, s),
 //   dy_j = dz_j c + dz_(j+half) s,  dy_(j+half) = dz_(j+half) c - dz_j s.
-// cs: the row's half (cos, sin) pairs; scratch: D floats of this warp, used
-// when the pairs do not sit whole lanes apart inside one chunk.
+// cs: the (c, s) of this lane's dims, s with its sign (kLanes, kChunks);
+// table, scratch: the row's pairs and D floats of this warp (kAny).
 template <int D>
-__device__ __forceinline__ void unrotate(float (&z)[D / 32], int lane, int rope, const float2* cs, float* scratch) {
+__device__ __forceinline__ void unrotate(float (&z)[D / 32], int lane, int rope, int kind,
+                                         const float2 (&cs)[Pb<D>::VEC], const float2* table, float* scratch) {
   using T = Pb<D>;
-  const int half = rope >> 1, s = half / T::VEC;
-  if (half % T::VEC == 0 && 2 * s <= 32) {            // pairs s lanes apart in chunk 0
-    const bool in = lane < 2 * s, lo = lane < s;
-    const int other = !in ? lane : lo ? lane + s : lane - s;
-    const int j0 = (lo ? lane : lane - s) * T::VEC;
+  if (kind == kLanes) {                               // (lanes past the rotated dims hold c = 1, s = 0)
+    const int s = (rope >> 1) / T::VEC, other = lane < s ? lane + s : lane < 2 * s ? lane - s : lane;
 #pragma unroll
-    for (int i = 0; i < T::VEC; ++i) {
-      const float y = __shfl_sync(0xffffffffu, z[i], other);
-      if (in) {
-        const float2 t = cs[j0 + i];
-        z[i] = fmaf(z[i], t.x, lo ? y * t.y : -y * t.y);
-      }
-    }
-  } else if (T::NC == 2 && s == 32) {                 // chunk 0 with chunk 1, in the lane
+    for (int i = 0; i < T::VEC; ++i) z[i] = fmaf(z[i], cs[i].x, __shfl_sync(0xffffffffu, z[i], other) * cs[i].y);
+  } else if (kind == kChunks) {
     if constexpr (T::NC == 2) {
 #pragma unroll
       for (int i = 0; i < T::VEC; ++i) {
-        const float2 t = cs[lane * T::VEC + i];
         const float a = z[i], b = z[T::VEC + i];
-        z[i] = fmaf(a, t.x, b * t.y);
-        z[T::VEC + i] = fmaf(b, t.x, -a * t.y);
+        z[i] = fmaf(a, cs[i].x, b * cs[i].y);
+        z[T::VEC + i] = fmaf(b, cs[i].x, -a * cs[i].y);
       }
     }
-  } else {                                            // any other even rope_dims
+  } else if (kind == kAny) {
+    const int half = rope >> 1;
 #pragma unroll
     for (int i = 0; i < T::E; ++i) scratch[T::dim(i / T::VEC, lane) + i % T::VEC] = z[i];
     __syncwarp();
@@ -155,7 +171,7 @@ __device__ __forceinline__ void unrotate(float (&z)[D / 32], int lane, int rope,
       if (e < rope) {
         const bool lo = e < half;
         const float y = scratch[lo ? e + half : e - half];
-        const float2 t = cs[lo ? e : e - half];
+        const float2 t = table[lo ? e : e - half];
         z[i] = fmaf(z[i], t.x, lo ? y * t.y : -y * t.y);
       }
     }
@@ -163,29 +179,35 @@ __device__ __forceinline__ void unrotate(float (&z)[D / 32], int lane, int rope,
   }
 }
 
+template <int NW>
+__device__ __forceinline__ float weight(const uint32_t (&w)[NW], int i) {
+  return i & 1 ? bf16hi_to_f(w[i / 2]) : bf16lo_to_f(w[i / 2]);
+}
+
 // dx of one row from x and dy; adds the row's part of dw.
 template <int D, bool WEIGHT>
 __device__ __forceinline__ void norm_backward(const float (&x)[D / 32], const float (&dy)[D / 32],
-                                              const float (&w)[D / 32], float eps, float (&dx)[D / 32],
+                                              const uint32_t (&w)[D / 64], float eps, float (&dx)[D / 32],
                                               float (&dw)[D / 32]) {
   constexpr int E = D / 32;
   float ss = 0.f, gx = 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     ss = fmaf(x[i], x[i], ss);
-    gx = fmaf(WEIGHT ? dy[i] * w[i] : dy[i], x[i], gx);
+    gx = fmaf(WEIGHT ? dy[i] * weight(w, i) : dy[i], x[i], gx);
   }
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) {
     ss += __shfl_xor_sync(0xffffffffu, ss, m);
     gx += __shfl_xor_sync(0xffffffffu, gx, m);
   }
-  const float r = 1.f / sqrtf(ss * (1.f / D) + eps);
+  const float ms = fmaf(ss, 1.f / D, eps), r0 = rsqrtf(ms);
+  const float r = r0 * fmaf(-0.5f * ms * r0, r0, 1.5f);     // one Newton step: within 2^-23
   // r^3 gx / D as r (r (r gx / D)): no intermediate of r^3's size
   const float back = r * (r * (r * gx * (1.f / D)));
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    const float g = WEIGHT ? dy[i] * w[i] : dy[i];
+    const float g = WEIGHT ? dy[i] * weight(w, i) : dy[i];
     dx[i] = fmaf(r, g, -x[i] * back);
     if (WEIGHT) dw[i] = fmaf(dy[i], x[i] * r, dw[i]);
   }
@@ -196,17 +218,22 @@ struct PbWs {
   float* part;          // [blocks][2][D]: q and k weight gradients
 };
 
+// The share of a call's work: qw of a block's warps take q heads, the others
+// keys and values; a unit is one row and 1/q_cut of its q heads (1/kv_cut of its
+// kv heads).
+struct PbShare { int qw, q_cut, kv_cut; };
+
 template <int D>
-__global__ void __launch_bounds__(kPbWarps * 32)
-prep_bwd_kernel(const PrepBwdArgs a, const RopeFreqs freqs, const PbWs ws, const int rb) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(kPbWarps * 32, 2)
+prep_bwd_kernel(const PrepBwdArgs a, const RopeFreqs freqs, const PbWs ws, const PbShare sh) {
+  using T = Pb<D>;
+  constexpr int E = T::E, NW = D / 64;
   extern __shared__ __align__(16) uint8_t pb_smem[];
-  __shared__ int rpos[kPbMaxRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int R = a.L.rope_dims, half = R >> 1, Hq = a.L.n_q, Hkv = a.L.n_kv;
-  float2* cs = reinterpret_cast<float2*>(pb_smem);                              // [rb][half]
-  float (*freq)[3] = reinterpret_cast<float (*)[3]>(pb_smem + ((size_t)rb * half * 8 + 15) / 16 * 16);
-  float* rows = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(freq) + 16 * ((3 * half + 3) / 4));   // [warps][D]
+  float (*freq)[3] = reinterpret_cast<float (*)[3]>(pb_smem);
+  float* rows = reinterpret_cast<float*>(pb_smem + 16 * ((3 * half + 3) / 4));                  // [warps][D]
+  float2* table = reinterpret_cast<float2*>(rows + kPbWarps * D) + warp * half;                 // [warps][half]
   if (R > 0) stage_freqs(freqs.f, half, freq);
   pdl_wait();
   pdl_launch();
@@ -223,64 +250,128 @@ prep_bwd_kernel(const PrepBwdArgs a, const RopeFreqs freqs, const PbWs ws, const
   if (blockIdx.x == 0 && tid == 0) *ws.status = bad ? 1u << KVQ_DEV_BADSEQ : 0u;
   if (bad) return;
 
-  float wq[E], wk[E], dwq[E], dwk[E];
+  const bool is_q = warp < sh.qw;
+  const int heads = is_q ? Hq : Hkv, cut = is_q ? sh.q_cut : sh.kv_cut;
+  const int n_warps = (is_q ? sh.qw : kPbWarps - sh.qw) * gridDim.x;
+  const int me = is_q ? (int)blockIdx.x * sh.qw + warp : (int)blockIdx.x * (kPbWarps - sh.qw) + warp - sh.qw;
+  const int kind = rope_kind<D>(R);
+  float dw[E];
+  uint32_t w[NW];                                     // the weights (only 2-byte aligned), two to a word
+  {
+    const uint16_t* src = is_q ? a.q_w : a.k_w;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int e = Pb<D>::dim(i / Pb<D>::VEC, lane) + i % Pb<D>::VEC;
-    wq[i] = a.q_raw ? bf16_to_f(__ldg(a.q_w + e)) : 0.f;
-    wk[i] = a.k_raw ? bf16_to_f(__ldg(a.k_w + e)) : 0.f;
-    dwq[i] = dwk[i] = 0.f;
-  }
-  const int nq = a.q_raw ? Hq : 0, per_row = nq + (a.k_raw ? Hkv : 0);
-  for (long long row0 = (long long)blockIdx.x * rb; row0 < a.n_rows; row0 += (long long)gridDim.x * rb) {
-    const int n = (int)min((long long)rb, a.n_rows - row0);
-    __syncthreads();                                  // the last step's angles are read
-    if (R > 0) {
-      if (tid < n) {
-        const int row = (int)row0 + tid;
-        int lo = 0, hi = a.n_blocks - 1;              // largest block starting at or before the row
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (__ldg(a.off + mid) <= row) lo = mid; else hi = mid - 1;
-        }
-        rpos[tid] = lo == 0 ? row : P + (row - __ldg(a.off + lo));
-      }
-      __syncthreads();
-      for (int i = tid; i < n * half; i += kPbWarps * 32) {
-        const int j = i % half;
-        cs[i] = rope_cos_sin_f32(rpos[i / half], freq[j][0], freq[j][1], freq[j][2]);
-      }
-      __syncthreads();
+    for (int i = 0; i < E; i += 2) {
+      const int e = T::dim(i / T::VEC, lane) + i % T::VEC;
+      w[i / 2] = (uint32_t)__ldg(src + e) | ((uint32_t)__ldg(src + e + 1) << 16);
+      dw[i] = dw[i + 1] = 0.f;
     }
-    for (int it = warp; it < n * per_row; it += kPbWarps) {
-      const int rl = it / per_row, h = it % per_row;
-      const size_t row = (size_t)row0 + rl;
-      float x[E], z[E], dx[E];
-      if (h < nq) {
-        const size_t o = (row * Hq + h) * D;
-        load_bf16<D>(a.q_raw + o, lane, x);
-        load_bf16<D>(a.dq_hat + o, lane, z);
-        if (R > 0) unrotate<D>(z, lane, R, cs + rl * half, rows + warp * D);
-        norm_backward<D, true>(x, z, wq, a.L.eps, dx, dwq);
-        store_bf16<D>(a.dq_raw + o, lane, dx);
-      } else {
-        const size_t o = (row * Hkv + (h - nq)) * D;
-        float y[E], dv[E];
-        load_bf16<D>(a.k_raw + o, lane, x);
-        if (a.dkv_f32) {
-          load_f32<D>(static_cast<const float*>(a.dk_hat) + o, lane, z);
-          load_f32<D>(static_cast<const float*>(a.dv_hat) + o, lane, y);
-        } else {
-          load_bf16<D>(static_cast<const uint16_t*>(a.dk_hat) + o, lane, z);
-          load_bf16<D>(static_cast<const uint16_t*>(a.dv_hat) + o, lane, y);
+  }
+  // units me, me + n_warps, ...: row and share of its heads
+  struct At { int row, c, h, end; };
+  const int d_row = n_warps / cut, d_c = n_warps % cut;
+  auto heads_of = [&](At& p) {
+    p.h = p.c * heads / cut;
+    p.end = (p.c + 1) * heads / cut;
+  };
+  auto next_unit = [&](At& p) {
+    p.row += d_row;
+    if ((p.c += d_c) >= cut) {
+      p.c -= cut;
+      ++p.row;
+    }
+    heads_of(p);
+  };
+  At at = {me / cut, me % cut, 0, 0};
+  heads_of(at);
+  float2 cs[T::VEC];
+  int at_row = -1;
+  auto angles = [&](int row) {                        // the row's rotation: table, and this lane's part of it
+    if (R == 0 || row == at_row) return;
+    at_row = row;
+    int lo = 0, hi = a.n_blocks - 1;                  // largest block starting at or before the row
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(a.off + mid) <= row) lo = mid; else hi = mid - 1;
+    }
+    const int pos = lo == 0 ? row : P + (row - __ldg(a.off + lo));
+    __syncwarp();
+    for (int j = lane; j < half; j += 32) table[j] = rope_cos_sin_f32(pos, freq[j][0], freq[j][1], freq[j][2]);
+    __syncwarp();
+    if (kind == kLanes) {
+      const int s = half / T::VEC, j0 = (lane < s ? lane : lane - s) * T::VEC;
+#pragma unroll
+      for (int i = 0; i < T::VEC; ++i) {
+        cs[i] = lane < 2 * s ? table[j0 + i] : make_float2(1.f, 0.f);
+        if (lane >= s) cs[i].y = -cs[i].y;
+      }
+    } else if (kind == kChunks) {
+#pragma unroll
+      for (int i = 0; i < T::VEC; ++i) cs[i] = table[lane * T::VEC + i];
+    }
+  };
+  if (is_q) {
+    // (row, head) in unit order, x and dz of the next AHEAD in flight
+    auto step = [&](At& p) {
+      if (++p.h == p.end) next_unit(p);
+    };
+    constexpr int AHEAD = D <= 256 ? 2 : 0;           // (head_dim 512: no registers for it)
+    uint32_t xr[AHEAD + 1][NW], zr[AHEAD + 1][NW];
+    At ahead = at;
+    auto fetch = [&](uint32_t (&x)[NW], uint32_t (&z)[NW]) {
+      if (ahead.row >= a.n_rows) return;
+      const size_t o = ((size_t)ahead.row * heads + ahead.h) * D;
+      load_raw<D>(a.q_raw + o, lane, x);
+      load_raw<D>(a.dq_hat + o, lane, z);
+      step(ahead);
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(xr[i], zr[i]);
+    while (at.row < a.n_rows) {
+#pragma unroll
+      for (int b = 0; b < AHEAD + 1; ++b) {
+        if (at.row >= a.n_rows) break;
+        fetch(xr[(b + AHEAD) % (AHEAD + 1)], zr[(b + AHEAD) % (AHEAD + 1)]);
+        angles(at.row);
+        float x[E], z[E], dx[E];
+        unpack<D>(xr[b], x);
+        unpack<D>(zr[b], z);
+        unrotate<D>(z, lane, R, kind, cs, table, rows + warp * D);
+        norm_backward<D, true>(x, z, w, a.L.eps, dx, dw);
+        store_bf16<D>(a.dq_raw + ((size_t)at.row * heads + at.h) * D, lane, dx);
+        step(at);
+      }
+    }
+  } else {
+    auto gradient = [&](const void* g, size_t o, float (&z)[E]) {
+      if (a.dkv_f32) load_f32<D>(static_cast<const float*>(g) + o, lane, z);
+      else load_bf16<D>(static_cast<const uint16_t*>(g) + o, lane, z);
+    };
+    for (; at.row < a.n_rows; next_unit(at)) {
+      for (int h = at.h; h < at.end; ++h) {
+        const size_t o = ((size_t)at.row * heads + h) * D;
+        // all four rows in flight at once; at head_dim 512 v's after k's
+        constexpr bool EARLY = D <= 256;
+        float z[E], y[E], dx[E];
+        uint32_t xr[NW], vr[NW];
+        auto load_v = [&]() {
+          if (!a.L.k_eq_v) load_raw<D>(a.v_raw + o, lane, vr);
+          gradient(a.dv_hat, o, y);
+        };
+        load_raw<D>(a.k_raw + o, lane, xr);
+        gradient(a.dk_hat, o, z);
+        if (EARLY) load_v();
+        angles(at.row);
+        {
+          float x[E];
+          unpack<D>(xr, x);
+          unrotate<D>(z, lane, R, kind, cs, table, rows + warp * D);
+          norm_backward<D, true>(x, z, w, a.L.eps, dx, dw);
         }
-        if (R > 0) unrotate<D>(z, lane, R, cs + rl * half, rows + warp * D);
-        norm_backward<D, true>(x, z, wk, a.L.eps, dx, dwk);
-        if (!a.L.k_eq_v) {
-          store_bf16<D>(a.dk_raw + o, lane, dx);
-          load_bf16<D>(a.v_raw + o, lane, x);
-        }
-        norm_backward<D, false>(x, y, wk, a.L.eps, dv, dwk);
+        if (!a.L.k_eq_v) store_bf16<D>(a.dk_raw + o, lane, dx);
+        if (!EARLY) load_v();
+        float x[E], dv[E];
+        unpack<D>(a.L.k_eq_v ? xr : vr, x);
+        norm_backward<D, false>(x, y, w, a.L.eps, dv, dw);
         if (a.L.k_eq_v) {
 #pragma unroll
           for (int i = 0; i < E; ++i) dx[i] += dv[i];
@@ -292,28 +383,26 @@ prep_bwd_kernel(const PrepBwdArgs a, const RopeFreqs freqs, const PbWs ws, const
     }
   }
   // the block's weight gradients: over its warps in warp order
-  for (int kind = 0; kind < 2; ++kind) {
-    if (kind == 0 ? !a.q_raw : !a.k_raw) continue;
-    __syncthreads();
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      rows[warp * D + Pb<D>::dim(i / Pb<D>::VEC, lane) + i % Pb<D>::VEC] = kind == 0 ? dwq[i] : dwk[i];
-    __syncthreads();
-    for (int e = tid; e < D; e += kPbWarps * 32) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < kPbWarps; ++w) s += rows[w * D + e];
-      if (gridDim.x == 1) (kind == 0 ? a.dq_w : a.dk_w)[e] = s;
-      else ws.part[((size_t)blockIdx.x * 2 + kind) * D + e] = s;
-    }
+  for (int i = 0; i < E; ++i) rows[warp * D + T::dim(i / T::VEC, lane) + i % T::VEC] = dw[i];
+  __syncthreads();
+  for (int i = tid; i < 2 * D; i += kPbWarps * 32) {
+    const int kv = i / D, e = i % D, w0 = kv ? sh.qw : 0, w1 = kv ? kPbWarps : sh.qw;
+    if (w0 == w1) continue;
+    float s = 0.f;
+    for (int x = w0; x < w1; ++x) s += rows[x * D + e];
+    if (gridDim.x == 1) (kv ? a.dk_w : a.dq_w)[e] = s;
+    else ws.part[((size_t)blockIdx.x * 2 + kv) * D + e] = s;
   }
 }
 
 // Sums the blocks' weight gradients: block x takes 32 columns of one kind,
-// warp w the partial rows w, w + 8, ...; the eight sums join in warp order.
-__global__ void __launch_bounds__(kPbWarps * 32)
+// warp w the partial rows w, w + 32, ...; the sums join in warp order.
+constexpr int kPbSumWarps = 32;
+__global__ void __launch_bounds__(kPbSumWarps * 32)
 prep_bwd_weights_kernel(const PrepBwdArgs a, const PbWs ws, const int blocks, const int D) {
-  __shared__ float sums[kPbWarps][32];
+  __shared__ float sums[kPbSumWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch();
@@ -321,48 +410,63 @@ prep_bwd_weights_kernel(const PrepBwdArgs a, const PbWs ws, const int blocks, co
   float* dst = kind == 0 ? a.dq_w : a.dk_w;
   if (*ws.status != 0 || !dst) return;
   float s = 0.f;
-  for (int b = warp; b < blocks; b += kPbWarps) s += ws.part[((size_t)b * 2 + kind) * D + e];
+#pragma unroll 10
+  for (int b = warp; b < blocks; b += kPbSumWarps) s += ws.part[((size_t)b * 2 + kind) * D + e];
   sums[warp][lane] = s;
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < kPbWarps; ++w) s += sums[w][lane];
+    for (int w = 1; w < kPbSumWarps; ++w) s += sums[w][lane];
     dst[e] = s;
   }
 }
 
-// Blocks of the grid: two per SM's worth of work at most, so that a call's
-// partial rows stay few.
-constexpr int kPbMaxBlocks = 608;
+// Most blocks of a grid (their partial rows are kept): two per SM, as many as are resident.
+constexpr int kPbMaxBlocks = 304;
 
 template <int D>
-cudaError_t launch_t(const PrepBwdArgs& a, const RopeFreqs& f, void* wsp, cudaStream_t st) {
+cudaError_t launch_t(const PrepBwdArgs& a, const RopeFreqs& f, void* wsp, int num_sms, cudaStream_t st) {
   PbWs ws;
   ws.status = static_cast<uint32_t*>(wsp);
   ws.part = reinterpret_cast<float*>(static_cast<uint8_t*>(wsp) + 256);
-  const int per_row = (a.q_raw ? a.L.n_q : 0) + (a.k_raw ? a.L.n_kv : 0), half = a.L.rope_dims / 2;
-  // four items a warp per step; angle tables of at most 16 KB
-  int rb = std::max(1, std::min(kPbMaxRows, 4 * kPbWarps / per_row));
-  if (half > 0) rb = std::max(1, std::min(rb, 2048 / half));
-  const size_t smem = ((size_t)rb * half * 8 + 15) / 16 * 16 + 16 * ((3 * half + 3) / 4) + (size_t)kPbWarps * D * 4;
-  const int blocks = std::min(kPbMaxBlocks, (a.n_rows + rb - 1) / rb);
+  const int half = a.L.rope_dims / 2, nq = a.q_raw ? a.L.n_q : 0, nkv = a.k_raw ? a.L.n_kv : 0;
+  // warps in proportion to the bytes of a row
+  const long long q_bytes = 6LL * nq, kv_bytes = (long long)nkv * ((a.L.k_eq_v ? 4 : 8) + (a.dkv_f32 ? 8 : 4));
+  PbShare sh;
+  sh.qw = nkv == 0 ? kPbWarps
+          : nq == 0 ? 0
+                    : (int)std::max<long long>(1, std::min<long long>(kPbWarps - 1, (kPbWarps * q_bytes + (q_bytes + kv_bytes) / 2) / (q_bytes + kv_bytes)));
+  // blocks: enough that no warp has more than one head, two per SM at most;
+  // then units small enough that every warp gets about two
+  const int kw = kPbWarps - sh.qw;
+  const long long want = std::max(sh.qw ? ((long long)a.n_rows * nq + sh.qw - 1) / sh.qw : 0,
+                                  kw ? ((long long)a.n_rows * nkv + kw - 1) / kw : 0);
+  // (a handful of heads goes to one block, which needs no second kernel)
+  const int blocks = want <= 3 ? 1 : (int)std::min<long long>(std::min(kPbMaxBlocks, 2 * num_sms), want);
+  auto cuts = [&](int warps, int heads) {
+    const long long c = warps ? (2LL * warps * blocks + a.n_rows - 1) / a.n_rows : 1;
+    return (int)std::max<long long>(1, std::min<long long>(heads, c));
+  };
+  sh.q_cut = cuts(sh.qw, nq);
+  sh.kv_cut = cuts(kw, nkv);
+  const size_t smem = 16 * ((3 * half + 3) / 4) + (size_t)kPbWarps * (D * 4 + half * 8);      // at most 35 KB
   cudaError_t e;
-  if ((e = launch_pdl(prep_bwd_kernel<D>, dim3(blocks), dim3(kPbWarps * 32), smem, st, a, f, ws, rb)) != cudaSuccess)
+  if ((e = launch_pdl(prep_bwd_kernel<D>, dim3(blocks), dim3(kPbWarps * 32), smem, st, a, f, ws, sh)) != cudaSuccess)
     return e;
   if (blocks == 1) return cudaSuccess;
-  return launch_pdl(prep_bwd_weights_kernel, dim3(D / 32, 2), dim3(kPbWarps * 32), 0, st, a, ws, blocks, D);
+  return launch_pdl(prep_bwd_weights_kernel, dim3(D / 32, 2), dim3(kPbSumWarps * 32), 0, st, a, ws, blocks, D);
 }
 
 }  // namespace
 
 size_t prep_bwd_ws_bytes(const LayerArgs& L) { return 256 + (size_t)kPbMaxBlocks * 2 * L.D * 4; }
 
-cudaError_t launch_prep_bwd(const PrepBwdArgs& a, const RopeFreqs& f, void* ws, cudaStream_t st) {
+cudaError_t launch_prep_bwd(const PrepBwdArgs& a, const RopeFreqs& f, void* ws, int num_sms, cudaStream_t st) {
   switch (a.L.D) {
-    case 64: return launch_t<64>(a, f, ws, st);
-    case 128: return launch_t<128>(a, f, ws, st);
-    case 256: return launch_t<256>(a, f, ws, st);
-    case 512: return launch_t<512>(a, f, ws, st);
+    case 64: return launch_t<64>(a, f, ws, num_sms, st);
+    case 128: return launch_t<128>(a, f, ws, num_sms, st);
+    case 256: return launch_t<256>(a, f, ws, num_sms, st);
+    case 512: return launch_t<512>(a, f, ws, num_sms, st);
     default: return cudaErrorInvalidValue;
   }
 }
