@@ -138,18 +138,69 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void* map, 
                : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const void* map, int x, int y, int z, int w,
-                                            uint32_t bar) {
-  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-               " [%0], [%1, {%2, %3, %4, %5}], [%6];"
-               :: "r"(smem_dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-               : "memory");
-}
-
 // 16-byte chunk `chunk` of row `r` of a K-major 128-byte-swizzled tile whose
 // rows are 128 bytes (byte offset from the tile's 1024-aligned base)
 __host__ __device__ constexpr uint32_t sw128_off(int r, int chunk) {
   return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4));
+}
+
+// ---- a pair of CTAs (cluster of two) working on one MMA ----
+// M = 256: CTA r holds rows 128 r .. of A and of the accumulator and half r of
+// B's N rows, each at the same shared-memory and tensor-memory addresses; one
+// thread of CTA 0 issues for both.
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of CTA 0's copy of a shared-memory object
+__device__ __forceinline__ uint32_t in_cta0(const void* p) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+               : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))));
+  return r;
+}
+__device__ __forceinline__ void arrive_cta0(uint64_t* mbar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(in_cta0(mbar)) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc2(uint32_t* smem_dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+               :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem_dst))), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma2_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         bool accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u) : "memory");
+}
+// the barrier at this address in both CTAs receives one arrival when every MMA
+// issued so far by this thread is complete
+__device__ __forceinline__ void commit2(uint64_t* mbar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mbar))), "h"((uint16_t)3) : "memory");
+}
+// copies into this CTA's shared memory that count on a barrier of either CTA
+__device__ __forceinline__ void tma2_load_3d(uint32_t smem_dst, const void* map, int x, int y, int z, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+               " [%0], [%1, {%2, %3, %4}], [%5];"
+               :: "r"(smem_dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tma2_load_4d(uint32_t smem_dst, const void* map, int x, int y, int z, int w,
+                                             uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+               " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+               :: "r"(smem_dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+               : "memory");
 }
 
 }  // namespace tc

@@ -64,19 +64,20 @@ struct Head {
   uint32_t status;
   int ok, nrt, nkt;             // layout valid; row and key tiles of one kv head
   int ntiles;                   // (row tile, key tile) pairs of one kv head
+  int npieces;                  // entries of the piece list
 };
 
 struct Ws {
   Head* head;
   int* chunk;                   // [nl + 1]: chunk c is row tiles chunk[c] .. chunk[c + 1] - 1 (kv head major)
-  int* counter;                 // [nl]: items of a chunk's products handed out
-  int* pieces;                  // [key pairs][n_kv]: pieces a key pair's sums are in
+  int* counts;                  // [nkt]: row tiles that see a key tile; then [key pairs]: pieces of its lists
+  int* list;                    // the (key pair, piece) of every dk and dv item: pair * kMaxSplits + piece
   int* starts;                  // [2][n_blocks + 1]: row and key tiles before each block
   RowTile* rt;
   KeyTile* kt;
   float* delta;                 // [n_rows][n_q]
   float* acc;                   // [splits][2][n_rows][n_kv][D]: dk, dv
-  uint8_t* p;                   // [cap] tiles
+  uint8_t* p;                   // [cap + 1] tiles, the last of zeros
   uint8_t* ds;
 };
 
@@ -87,7 +88,7 @@ struct Plan {
   int nl;                       // chunk launches
   int splits, piece;            // of a key pair's row tiles: most pieces; row tiles of one
   int direct;                   // one chunk, one split: dk and dv need no sums beside the outputs
-  size_t chunk_o, counter_o, pieces_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
+  size_t chunk_o, counts_o, list_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
 };
 
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
@@ -139,15 +140,15 @@ Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows,
     return at;
   };
   p.chunk_o = take(((size_t)p.nl + 1) * 4);
-  p.counter_o = take((size_t)p.nl * 4);
-  p.pieces_o = take(((size_t)p.nkt + 1) / 2 * L.n_kv * 4);
+  p.counts_o = take(((size_t)p.nkt + (p.nkt + 1) / 2) * 4);
+  p.list_o = take(((size_t)p.nkt + 1) / 2 * kMaxSplits * 4);
   p.starts_o = take(((size_t)n_blocks + 1) * 8);
   p.rt_o = take((size_t)p.nrt * sizeof(RowTile));
   p.kt_o = take((size_t)p.nkt * sizeof(KeyTile));
   p.delta_o = take((size_t)n_rows * L.n_q * 4);
   p.acc_o = take(acc);
-  p.p_o = take((size_t)p.cap * kTileBytes);
-  p.ds_o = take((size_t)p.cap * kTileBytes);
+  p.p_o = take(((size_t)p.cap + 1) * kTileBytes);      // the last tile holds zeros
+  p.ds_o = take(((size_t)p.cap + 1) * kTileBytes);
   p.bytes = o;
   return p;
 }
@@ -157,8 +158,8 @@ Ws carve(void* base, const Plan& p) {
   Ws w;
   w.head = reinterpret_cast<Head*>(b);
   w.chunk = reinterpret_cast<int*>(b + p.chunk_o);
-  w.counter = reinterpret_cast<int*>(b + p.counter_o);
-  w.pieces = reinterpret_cast<int*>(b + p.pieces_o);
+  w.counts = reinterpret_cast<int*>(b + p.counts_o);
+  w.list = reinterpret_cast<int*>(b + p.list_o);
   w.starts = reinterpret_cast<int*>(b + p.starts_o);
   w.rt = reinterpret_cast<RowTile*>(b + p.rt_o);
   w.kt = reinterpret_cast<KeyTile*>(b + p.kt_o);
@@ -207,11 +208,13 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
   return lo;
 }
 
-__device__ void plan_block(const TrainBwdArgs& a, const Ws& w, int cap, int nl) {
+// What the plan needs of the host's: tiles of a chunk, chunks, and how lists are cut.
+struct PlanArgs { int cap, nl, splits, piece; };
+
+__device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl) {
   __shared__ int sums[kPrepThreads / 32];
-  const int tid = threadIdx.x, nb = a.n_blocks, TQ = kT / a.L.G, W = a.L.window;
+  const int tid = threadIdx.x, nb = a.n_blocks, TQ = kT / a.L.G, W = a.L.window, cap = pl.cap, nl = pl.nl;
   const int P = a.off[1];
-  for (int c = tid; c < nl; c += kPrepThreads) w.counter[c] = 0;
   bool bad = false;
   for (int b = tid; b < nb; b += kPrepThreads) {
     const int o0 = a.off[b], o1 = a.off[b + 1];
@@ -221,7 +224,7 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, int cap, int nl) 
   bad = __syncthreads_or(bad);
   if (bad) {                                // no tiles: nothing is written
     for (int c = tid; c <= nl; c += kPrepThreads) w.chunk[c] = 0;
-    if (tid == 0) *w.head = Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0};
+    if (tid == 0) *w.head = Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0};
     return;
   }
   int* rs = w.starts;
@@ -242,7 +245,9 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, int cap, int nl) 
   for (int i = tid; i < nkt; i += kPrepThreads) {
     const int b = last_le(ks, nb, i), idx = i - ks[b], o0 = a.off[b];
     w.kt[i] = KeyTile{o0 + idx * kT, min(kT, a.off[b + 1] - o0 - idx * kT), b, idx};
+    w.counts[i] = 0;
   }
+  __syncthreads();
   int ntiles = 0;
   for (int i0 = 0; i0 < nrt; i0 += kPrepThreads) {
     const int i = i0 + tid;
@@ -270,9 +275,32 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, int cap, int nl) 
     int tot;
     t.base = ntiles + block_scan(t.nA + t.nB, sums, &tot);
     ntiles += tot;
-    if (i < nrt) w.rt[i] = t;
+    if (i < nrt) {
+      w.rt[i] = t;
+      if (nl == 1) {                                   // (whole numbers: their order does not matter)
+        for (int j = 0; j < t.nA; ++j) atomicAdd(w.counts + t.a0 + j, 1);
+        for (int j = 0; j < t.nB; ++j) atomicAdd(w.counts + ks[t.block] + t.b0 + j, 1);
+      }
+    }
   }
   __syncthreads();
+  // the pieces of every key pair's list: `piece` row tiles or more each with one
+  // chunk (by the longer of the two tiles' lists), `splits` with several
+  const int nkp = (nkt + 1) / 2;
+  int npieces = 0;
+  for (int i0 = 0; i0 < nkp; i0 += kPrepThreads) {
+    const int i = i0 + tid;
+    int cuts = 0;
+    if (i < nkp) {
+      const int n = max(__ldcg(w.counts + 2 * i), 2 * i + 1 < nkt ? __ldcg(w.counts + 2 * i + 1) : 0);
+      cuts = nl == 1 ? max(1, min(pl.splits, n / pl.piece)) : pl.splits;
+      w.counts[nkt + i] = cuts;
+    }
+    int tot;
+    const int at = npieces + block_scan(cuts, sums, &tot);
+    npieces += tot;
+    for (int c = 0; c < cuts; ++c) w.list[at + c] = i * kMaxSplits + c;
+  }
   if (tid == 0) {
     // chunks: as many whole row tiles as fit in cap tiles
     const int all = nrt * a.L.n_kv;
@@ -297,18 +325,23 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, int cap, int nl) 
     while (c < nl) w.chunk[++c] = x;
     if (!fits)
       for (int i = 0; i <= nl; ++i) w.chunk[i] = 0;
-    *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0};
+    *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles, npieces} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0};
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads)
-bwd_prep_kernel(const TrainBwdArgs a, const Ws w, const int cap, const int nl) {
+bwd_prep_kernel(const TrainBwdArgs a, const Ws w, const PlanArgs pl) {
   pdl_wait();
   pdl_launch();
   if (blockIdx.x == 0) {
-    plan_block(a, w, cap, nl);
+    plan_block(a, w, pl);
     return;
+  }
+  // the tiles of zeros, 4 KB a block
+  for (int i = blockIdx.x - 1; i < (int)(2 * kTileBytes / 4096); i += gridDim.x - 1) {
+    uint8_t* z = (i & 1 ? w.ds : w.p) + (size_t)pl.cap * kTileBytes + (i >> 1) * 4096;
+    reinterpret_cast<uint4*>(z)[threadIdx.x] = make_uint4(0, 0, 0, 0);
   }
   // delta: one warp per (row, head)
   constexpr int E = D / 32, VEC = E < 8 ? E : 8;
@@ -367,13 +400,14 @@ bwd_prep_kernel(const TrainBwdArgs a, const Ws w, const int cap, const int nl) {
 // ---------------------------------------------------------------------------
 
 // Descriptor of a shared-memory operand without swizzle (8 x 16-byte core
-// matrices) or, with sw128, MN-major rows of 128 swizzled bytes.
+// matrices) or MN-major with rows of 128 or 64 swizzled bytes.
 //   K-major, no swizzle:  lbo = next 8 elements of K, sbo = next 8 rows of M
 //   MN-major, no swizzle: lbo = next 8 of K, sbo = next 8 elements of M
-//   MN-major, 128 bytes:  lbo = next 64 elements of N, sbo = next 8 of K
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, bool sw128) {
+//   MN-major, swizzled:   lbo = next row's worth of elements of N, sbo = next 8 of K
+constexpr int kPlain = 0, kSw128 = 2, kSw64 = 4;
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, int swizzle) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)(sw128 ? 2 : 0) << 61);
+         ((uint64_t)1 << 46) | ((uint64_t)swizzle << 61);
 }
 constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;   // instruction descriptor: MN-major operand
 
@@ -410,9 +444,15 @@ struct Waiter {
   uint32_t* status;
   bool dead = false;
   __device__ __forceinline__ void operator()(uint64_t* bar, int parity) {
-    if (dead) return;
-    const bool ok = mbar_wait(bar, parity);
+    const bool ok = !dead && mbar_wait(bar, parity);
     if (__any_sync(0xffffffffu, !ok)) {
+      if (!dead) flag_error(status, KVQ_DEV_TIMEOUT);
+      dead = true;
+    }
+  }
+  // by one thread alone
+  __device__ __forceinline__ void one(uint64_t* bar, int parity) {
+    if (!dead && !mbar_wait(bar, parity)) {
       dead = true;
       flag_error(status, KVQ_DEV_TIMEOUT);
     }
@@ -744,28 +784,36 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
 // products: out[128 x N] = sum over steps of A_t (128 x 64) B_t (64 x N)
 // ---------------------------------------------------------------------------
 // An item is a pair of tiles (two row tiles for dq, two key tiles for dk or dv)
-// times N head dims: both tiles' A meet the same B, which halves B's traffic
-// (with one tile per CTA the kernel was bound by what L2 delivers).  The list
-// of row tiles of a key pair is cut into `splits` pieces, each with its own sums.
-// CTAs stay resident, take items from a counter (who computes an item does not
-// change it), and the copies of the next item run under the last one's output.
+// times N head dims, and a pair of CTAs (a cluster of two) works on it with
+// MMAs of 256 rows: each CTA brings its own tile's A and half of B, so that
+// shared memory is read at half the rate one CTA's MMA needs (bound by that and
+// by what L2 delivers, a CTA alone reached 0.6 of the rate) and the accumulators
+// fit tensor memory twice: an item's output runs under the next item's products.
+// The list of row tiles of a key pair is cut into pieces, each with its own
+// sums.  A tile that a step's other tile sees alone is a tile of zeros.  The CTA
+// pairs stay resident and take the items in turn, the longest first.
 
+// A step is a whole tile: 128 rows (or keys) of K in one stage, three copies (a
+// copy takes the issuing thread some 150 cycles; with stages of 64 the copies
+// took longer than their MMAs).
 template <int N>
 struct Pr {
-  static constexpr int A_BYTES = 16384;                       // 128 x 64 of P or dS, one per tile of the pair
-  static constexpr int B_BYTES = N * 128;                     // 64 rows of N dims: N/64 blocks of 8 KB
-  static constexpr int STAGE = 2 * A_BYTES + B_BYTES;
+  static constexpr int A_BYTES = kTileBytes;                  // 128 x 128 of P or dS
+  static constexpr int DIMS = N / 2;                          // of B per CTA
+  static constexpr int BOX = DIMS < 64 ? DIMS : 64;           // per copy
+  static constexpr int B_BYTES = DIMS * 256;                  // 128 rows
+  static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int NS = N == 256 ? 3 : 4;
-  static constexpr int NBUF = N == 256 ? 1 : 2;               // accumulator pairs in tensor memory
   static constexpr int E_OFF = NS * STAGE;                    // 4 KB per output warp
-  static constexpr int C_OFF = E_OFF + 8 * 4096;
+  static constexpr int L_OFF = E_OFF + 8 * 4096;              // 32 steps of the copies' list
+  static constexpr int C_OFF = L_OFF + 512;
   static constexpr int BYTES = C_OFF + 512 + 1024;
 };
 constexpr int kPrEpi = 8;
 constexpr int kPrThreads = (kPrEpi + 2) * 32;
 
 // What the copies tell the MMA warp about a stage.
-enum : int { kTile0 = 1, kTile1 = 2, kFirst = 4, kLast = 8, kKeys = 16, kEnd = 32 };
+enum : int { kFirst = 1, kLast = 2, kKeys = 4, kEnd = 8 };
 
 struct Item {
   bool dkv;
@@ -774,12 +822,13 @@ struct Item {
 };
 
 struct ProdArgs {
-  int chunk, splits, piece;     // piece: 0 when every list is cut into `splits` pieces
+  int chunk;
+  int zero;                     // slot of a tile of zeros
   int direct;                   // 1: dk and dv go straight to the outputs
 };
 
 template <int D>
-__global__ void __launch_bounds__(kPrThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
 bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const __grid_constant__ CUtensorMap tmq,
                     const __grid_constant__ CUtensorMap tmo, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmp, const __grid_constant__ CUtensorMap tmd) {
@@ -790,48 +839,47 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::C_OFF);
+  const int rank = (int)tc::cta_rank();
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::C_OFF);      // CTA 0's: both CTAs' copies landed
   uint64_t* empty = full + T::NS;
-  uint64_t* done = empty + T::NS;                     // [NBUF] an item's products are in tensor memory
-  uint64_t* acc_free = done + T::NBUF;                // [NBUF] and read from it
-  uint64_t* item_full = acc_free + T::NBUF;           // [2]
+  uint64_t* done = empty + T::NS;                     // [2] an item's products are in tensor memory
+  uint64_t* acc_free = done + 2;                      // [2] CTA 0's: and read from it, in both CTAs
+  uint64_t* item_full = acc_free + 2;                 // [2]
   uint64_t* item_empty = item_full + 2;               // [2]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(item_empty + 2);
-  volatile int* info = reinterpret_cast<volatile int*>(tslot + 1);   // [NS] stage flags
-  volatile int* got = info + T::NS;                   // [NBUF] tiles of the pair with any product
-  volatile int* items = got + T::NBUF;                // [2][2]: item (-1: no more), its steps
+  volatile int* info = reinterpret_cast<volatile int*>(tslot + 1);   // [NS] stage flags (CTA 0)
+  volatile int* items = info + T::NS;                 // [2][2]: item (-1: no more), its steps
   if (tid == 0) {
     for (int s = 0; s < T::NS; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
-    for (int s = 0; s < T::NBUF; ++s) {
-      mbar_init(done + s, 2);                         // the MMAs, and the flags in got[]
-      mbar_init(acc_free + s, kPrEpi);
-    }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(done + s, 1);
+      mbar_init(acc_free + s, 2 * kPrEpi);
       mbar_init(item_full + s, 1);
       mbar_init(item_empty + s, kPrEpi);
     }
     fence_mbar_init();
   }
   if (warp == 0) {
-    tc::tmem_alloc(tslot, 512);
-    tc::tmem_relinquish();
+    tc::tmem_alloc2(tslot, 512);
+    tc::tmem_relinquish2();
   }
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();                                 // both CTAs' barriers and tensor memory are there
   tc::fence_after_sync();
   const uint32_t tmem = *tslot;
   pdl_wait();
   pdl_launch();
 
   const Head hd = *w.head;
-  const int G = a.L.G, TQ = kT / G, nkv = a.L.n_kv;
+  const int G = a.L.G, nkv = a.L.n_kv;
   const int x0 = w.chunk[pa.chunk], x1 = w.chunk[pa.chunk + 1];
   // an empty chunk (or layout) has no items; dk and dv come first (the longest sums)
-  const int kp = (hd.nkt + 1) / 2, rp = (hd.nrt + 1) / 2;
-  const int n_dkv = x0 < x1 ? kp * pa.splits * nkv * 2 * H : 0;
+  const int rp = (hd.nrt + 1) / 2;
+  const int n_dkv = x0 < x1 ? hd.npieces * nkv * 2 * H : 0;
   const int q0 = x0 < x1 ? x0 / hd.nrt * rp + x0 % hd.nrt / 2 : 0;
   const int n_items = x0 < x1 ? n_dkv + ((x1 - 1) / hd.nrt * rp + (x1 - 1) % hd.nrt / 2 - q0 + 1) * H : 0;
   const long long c0 = x0 < x1 ? (long long)(x0 / hd.nrt) * hd.ntiles + w.rt[x0 % hd.nrt].base : 0;
@@ -847,8 +895,9 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
       id /= 2;
       t.kvh = id % nkv;
       id /= nkv;
-      t.split = id % pa.splits;
-      t.t0 = id / pa.splits * 2;
+      id = __ldg(w.list + id);
+      t.split = id % kMaxSplits;
+      t.t0 = id / kMaxSplits * 2;
       t.n = min(2, hd.nkt - t.t0);
     } else {
       id += q0;
@@ -861,8 +910,10 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   Waiter wait{&w.head->status};
 
   if (warp == kPrEpi) {
-    // ================= copies =================
+    // ================= copies: this CTA's tile of A and half of B =================
     int st = 0, ph = 0, e = 0, eph = 0;
+    const uint32_t bar0 = tc::in_cta0(full);
+    int4* steps = reinterpret_cast<int4*>(sm + T::L_OFF);
     auto publish = [&](int id, int n) {
       wait(item_empty + e, eph ^ 1);
       if (lane == 0) {
@@ -876,55 +927,38 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         eph ^= 1;
       }
     };
-    for (;;) {
-      int id = 0;
-      if (lane == 0) id = atomicAdd(w.counter + pa.chunk, 1);
-      id = __shfl_sync(0xffffffffu, id, 0);
-      if (id >= n_items) break;
+    for (int id = blockIdx.x / 2; id < n_items; id += gridDim.x / 2) {
       const Item it = decode(id);
       const long long slot0 = (long long)it.kvh * hd.ntiles - c0;    // slot of the kv head's first tile
+      const int dim = it.half * N + rank * T::DIMS;
       int left = 0;                                   // stages still to come
       bool first = true;
-      // one tile of each of the pair (slot -1: not there) and the 128 rows of B they meet
+      // one tile of each of the pair (slot -1: not there) and the 128 rows of B they
+      // meet: one thread
       auto tile = [&](int s0, int s1, int row) {
-        const int mask = (s0 >= 0 ? kTile0 : 0) | (s1 >= 0 ? kTile1 : 0);
-        for (int s = 0; s < 2; ++s) {
-          wait(empty + st, ph ^ 1);
-          const uint32_t dst = sb + st * T::STAGE, bar = smem_u32(full + st);
-          if (lane == 0) {
-            info[st] = mask | (first ? kFirst : 0) | (--left == 0 ? kLast : 0) | (it.dkv ? kKeys : 0);
-            mbar_arrive_expect_tx(full + st, __popc(mask) * T::A_BYTES + T::B_BYTES);
-          }
-          first = false;
-          __syncwarp();
-          // A: lanes 0 and 1, a tile each; B: the next lanes, 64 dims each
-          const int slot = lane == 0 ? s0 : s1, b = lane - 2;
-          if (it.dkv) {
-            // rows 64 s .. of every key group: [16][64 rows][16 B], runs of 1 KB (one copy
-            // for the sixteen: a copy takes the issuing warp some 60 cycles)
-            if (lane < 2 && slot >= 0)
-              tc::tma_load_4d(dst + lane * T::A_BYTES, it.kind == 1 ? &tmp : &tmd, 0, s, 0, slot, bar);
-            if (b >= 0 && b < N / 64)
-              tc::tma_load_3d(dst + 2 * T::A_BYTES + b * 8192, it.kind == 0 ? &tmq : &tmo, it.half * N + 64 * b,
-                              it.kvh * G, row + s * (TQ / 2), bar);
-          } else {
-            // keys 64 s ..: [8][128 rows][16 B]
-            if (lane < 2 && slot >= 0)
-              bulk_g2s(sm + st * T::STAGE + lane * T::A_BYTES, w.ds + (size_t)slot * kTileBytes + s * 16384, 16384,
-                       full + st);
-            if (b >= 0 && b < N / 64)
-              tc::tma_load_3d(dst + 2 * T::A_BYTES + b * 8192, &tmk, it.half * N + 64 * b, it.kvh, row + 64 * s, bar);
-          }
-          __syncwarp();
-          if (++st == T::NS) {
-            st = 0;
-            ph ^= 1;
-          }
+        const int mine = rank == 0 ? s0 : s1, slot = mine >= 0 ? mine : pa.zero;
+        wait.one(empty + st, ph ^ 1);
+        const uint32_t dst = sb + st * T::STAGE, bar = bar0 + 8 * st;
+        if (rank == 0) {
+          info[st] = (first ? kFirst : 0) | (--left == 0 ? kLast : 0) | (it.dkv ? kKeys : 0);
+          mbar_arrive_expect_tx(full + st, 2 * T::STAGE);
+        }
+        first = false;
+        tc::tma2_load_4d(dst, it.dkv && it.kind == 1 ? &tmp : &tmd, 0, 0, 0, slot, bar);
+#pragma unroll
+        for (int b = 0; b < T::DIMS / T::BOX; ++b) {
+          if (it.dkv) tc::tma2_load_3d(dst + T::A_BYTES + b * 16384, it.kind == 0 ? &tmq : &tmo, dim + T::BOX * b, it.kvh * G, row, bar);
+          else tc::tma2_load_3d(dst + T::A_BYTES + b * 16384, &tmk, dim + T::BOX * b, it.kvh, row, bar);
+        }
+        if (++st == T::NS) {
+          st = 0;
+          ph ^= 1;
         }
       };
       if (it.dkv) {
-        // the chunk's row tiles that see either key tile; this split's share of them by count
+        // the chunk's row tiles that see either key tile; this piece's share of them by count
         const KeyTile ka = w.kt[it.t0], kb = w.kt[it.t0 + it.n - 1];
+        const int cuts = w.counts[hd.nkt + it.t0 / 2];
         const int xs = max(0, x0 - it.kvh * hd.nrt), xe = min(hd.nrt, x1 - it.kvh * hd.nrt);
         auto tile_of = [&](const KeyTile& t, const RowTile& r) -> int {      // its place in the row tile's list
           if (t.block == 0) return t.idx >= r.a0 && t.idx < r.a0 + r.nA ? t.idx - r.a0 : -1;
@@ -940,11 +974,8 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
           }
           n += __popc(__ballot_sync(0xffffffffu, see));
         }
-        const int cuts = pa.piece ? max(1, min(pa.splits, n / pa.piece)) : pa.splits;
-        if (it.split >= cuts) continue;               // (no item for the others)
-        if (lane == 0 && it.half == 0 && it.kind == 0 && it.split == 0) w.pieces[it.t0 / 2 * nkv + it.kvh] = cuts;
         const int v0 = (int)((long long)n * it.split / cuts), v1 = (int)((long long)n * (it.split + 1) / cuts);
-        left = 2 * (v1 - v0);
+        left = v1 - v0;
         publish(id, left);
         int seen = 0;
         for (int i = xs; i < xe && seen < v1; i += 32) {
@@ -958,14 +989,14 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
             j1 += j1 >= 0 ? base : 0;
             row = r.row0;
           }
-          uint32_t m = __ballot_sync(0xffffffffu, j0 >= 0 || j1 >= 0);
-          for (; m; m &= m - 1, ++seen) {
-            if (seen < v0) continue;
-            if (seen >= v1) break;
-            const int src = __ffs(m) - 1;
-            tile(__shfl_sync(0xffffffffu, j0, src), __shfl_sync(0xffffffffu, j1, src),
-                 __shfl_sync(0xffffffffu, row, src));
-          }
+          const uint32_t m = __ballot_sync(0xffffffffu, j0 >= 0 || j1 >= 0);
+          const int mine = seen + __popc(m & ((1u << lane) - 1)), from = max(v0, seen), upto = min(v1, seen + __popc(m));
+          if ((m >> lane & 1) && mine >= from && mine < upto) steps[mine - from] = make_int4(j0, j1, row, 0);
+          __syncwarp();
+          if (lane == 0)
+            for (int x = 0; x < upto - from; ++x) tile(steps[x].x, steps[x].y, steps[x].z);
+          __syncwarp();
+          seen += __popc(m);
         }
       } else {
         const RowTile r0 = load_row_tile(w.rt, it.t0);
@@ -989,51 +1020,57 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
             range(0, 0, 0, r1.b0, r1.nB, base1 + r1.nA, r1.off0);
           }
         };
-        walk([&](int, int, int) { left += 2; });
+        walk([&](int, int, int) { ++left; });
         publish(id, left);
-        walk(tile);
+        if (lane == 0) walk(tile);
+        __syncwarp();
       }
     }
     publish(-1, 0);
-    wait(empty + st, ph ^ 1);
+    // every stage consumed, in both CTAs, before either may leave
     if (lane == 0) {
-      info[st] = kEnd;
-      mbar_arrive(full + st);
+      const int st1 = st;
+      for (int i = 0; i < T::NS; ++i) {
+        wait.one(empty + st, ph ^ 1);
+        if (++st == T::NS) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+      if (rank == 0) {
+        info[st1] = kEnd;
+        mbar_arrive(full + st1);
+      }
     }
+    __syncwarp();
   } else if (warp == kPrEpi + 1) {
-    // ================= products =================
-    int st = 0, ph = 0, use = 0, started = 0;
-    for (;;) {
+    // ================= products (CTA 0, for both) =================
+    int st = 0, ph = 0, use = 0;
+    bool started = false;
+    while (rank == 0) {
       wait(full + st, ph);
       const int f = __shfl_sync(0xffffffffu, info[st], 0);   // (every lane is here before lane 0 goes on)
       if ((f & kEnd) || wait.dead) break;
-      const int buf = use % T::NBUF;
+      const int buf = use & 1;
       if (f & kFirst) {
-        if (use >= T::NBUF) wait(acc_free + buf, (use / T::NBUF - 1) & 1);
-        started = 0;
+        if (use >= 2) wait(acc_free + buf, ((use >> 1) - 1) & 1);
+        started = false;
       }
       tc::fence_after_sync();
       if (lane == 0) {
-        const uint32_t ID = tc::idesc_bf16_f32(kT, N) | kTransB | (f & kKeys ? kTransA : 0u);
-        const uint32_t bs = sb + st * T::STAGE + 2 * T::A_BYTES;
+        const uint32_t ID = tc::idesc_bf16_f32(2 * kT, N) | kTransB | (f & kKeys ? kTransA : 0u);
+        const uint32_t as = sb + st * T::STAGE, bs = as + T::A_BYTES;
+        constexpr uint32_t ROW = T::BOX * 2;          // bytes of a row of B
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!(f & (kTile0 << t))) continue;
-          const uint32_t as = sb + st * T::STAGE + t * T::A_BYTES, d = tmem + (buf * 2 + t) * N;
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            tc::mma_f16(d, f & kKeys ? smem_desc(as + 256 * s, 128, 1024, false) : smem_desc(as + 4096 * s, 2048, 128, false),
-                        smem_desc(bs + 2048 * s, 8192, 1024, true), ID, (started >> t & 1) || s > 0);
-        }
-        tc::commit(empty + st);
-        if (f & kLast) {
-          got[buf] = started | (f & (kTile0 | kTile1));
-          tc::commit(done + buf);
-          mbar_arrive(done + buf);
-        }
+        for (int s = 0; s < 8; ++s)
+          tc::mma2_f16(tmem + buf * N,
+                       f & kKeys ? smem_desc(as + 256 * s, 128, 2048, kPlain) : smem_desc(as + 4096 * s, 2048, 128, kPlain),
+                       smem_desc(bs + 16 * ROW * s, 16384, 8 * ROW, T::BOX == 64 ? kSw128 : kSw64), ID, started || s > 0);
+        tc::commit2(empty + st);
+        if (f & kLast) tc::commit2(done + buf);
       }
       __syncwarp();
-      started |= f & (kTile0 | kTile1);
+      started = true;
       if (f & kLast) ++use;
       if (++st == T::NS) {
         st = 0;
@@ -1041,8 +1078,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
       }
     }
   } else {
-    // ================= out: warp = 32 rows of one tile of the pair =================
-    const int t = warp >> 2;
+    // ================= out: warp = 32 rows of this CTA's tile, half of the columns =================
     uint8_t* stg = sm + T::E_OFF + warp * 4096;
     int e = 0, eph = 0, use = 0;
     const size_t plane = (size_t)a.n_rows * nkv * D;
@@ -1051,12 +1087,11 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
       const int id = items[2 * e], steps = items[2 * e + 1];
       if (id < 0 || wait.dead) break;
       const Item it = decode(id);
-      const int buf = use % T::NBUF;
-      bool has = false;
-      if (steps > 0) {
-        wait(done + buf, (use / T::NBUF) & 1);
+      const int buf = use & 1;
+      const bool has = steps > 0;
+      if (has) {
+        wait(done + buf, (use >> 1) & 1);
         tc::fence_after_sync();
-        has = got[buf] >> t & 1;
       }
       __syncwarp();
       // where the tile's rows go: row r at o + (r >> sh) * big + (r & ((1 << sh) - 1)) * D
@@ -1065,16 +1100,16 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
       if (it.dkv) {
         sh = 0;
         big = (size_t)nkv * D;
-        if (t < it.n) {
-          const KeyTile k = w.kt[it.t0 + t];
+        if (rank < it.n) {
+          const KeyTile k = w.kt[it.t0 + rank];
           rows = k.n;
           o = ((size_t)k.row0 * nkv + it.kvh) * D;
         }
       } else {
         sh = 31 - __clz(G);
         big = (size_t)a.L.n_q * D;
-        if (t < it.n) {
-          const RowTile r = load_row_tile(w.rt, it.t0 + t);
+        if (rank < it.n) {
+          const RowTile r = load_row_tile(w.rt, it.t0 + rank);
           rows = r.nt * G;
           o = ((size_t)r.row0 * a.L.n_q + it.kvh * G) * D;
         }
@@ -1086,10 +1121,10 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
       const bool add = it.dkv && (pa.direct ? a.accumulate != 0 : pa.chunk > 0);
       if (part) out = w.acc + ((size_t)it.split * 2 + it.kind) * plane;
       const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-      const int r0 = 32 * (warp & 3);
-      const uint32_t ta = tmem + ((uint32_t)r0 << 16) + (buf * 2 + t) * N;
+      const int r0 = 32 * (warp & 3), n0 = (warp >> 2) * (N / 2);
+      const uint32_t ta = tmem + ((uint32_t)r0 << 16) + buf * N;
       const bool write = rows > r0 && (has || !add);
-      for (int c = 0; c < N && write; c += 32) {
+      for (int c = n0; c < n0 + N / 2 && write; c += 32) {
         float v[32];
         if (has) {
           ld_x32(ta + c, v);
@@ -1147,13 +1182,13 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         }
         __syncwarp();
       }
-      if (steps > 0) {
+      if (has) {
         tc::fence_before_sync();
         ++use;
       }
       __syncwarp();
       if (lane == 0) {
-        if (steps > 0) mbar_arrive(acc_free + buf);
+        if (has) tc::arrive_cta0(acc_free + buf);
         mbar_arrive(item_empty + e);
       }
       if (++e == 2) {
@@ -1164,9 +1199,10 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   }
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();                                 // neither CTA's memory is written or read any more
   if (warp == 0) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc2(tmem, 512);
   }
 }
 
@@ -1184,10 +1220,9 @@ __global__ void __launch_bounds__(256) bwd_finish_kernel(const TrainBwdArgs a, c
   // block (x, y): key tiles x, x + grid, ..., a share y of their rows
   for (int t = blockIdx.x; t < nkt; t += gridDim.x) {
     const KeyTile k = w.kt[t];
+    const int pieces = w.counts[nkt + t / 2];
     const int per = kT / gridDim.y, r0 = blockIdx.y * per, quads = min(per, k.n - r0) * a.L.n_kv * (D / 4);
     for (int q = threadIdx.x; q < quads; q += 256) {
-      const int col = q % (a.L.n_kv * (D / 4));
-      const int pieces = w.pieces[t / 2 * a.L.n_kv + col / (D / 4)];
       const size_t e = ((size_t)(k.row0 + r0) * a.L.n_kv * (D / 4) + q) * 4;
       float4 s = *reinterpret_cast<const float4*>(w.acc + kind * plane + e);
 #pragma unroll 4
@@ -1224,8 +1259,8 @@ __global__ void __launch_bounds__(256) bwd_finish_kernel(const TrainBwdArgs a, c
 
 // ---- host side ----
 
-bool map_bf16(CUtensorMap* m, const void* base, int D, int heads, int rows, int box_h, int box_r) {
-  return rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, D, heads, rows, box_h, box_r);
+bool map_bf16(CUtensorMap* m, const void* base, int D, int heads, int rows, int box_h, int box_r, int box_d = 64) {
+  return rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, D, heads, rows, box_h, box_r, box_d);
 }
 
 template <int D>
@@ -1252,18 +1287,19 @@ cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t
   const Plan p = make_plan(L, a.n_blocks, a.n_rows, a.max_block_rows, num_sms);
   const Ws w = carve(wsp, p);
   const int TQ = kT / L.G;
-  // boxes: 128 (token, head) pairs and 128 keys for the scores, 64 for the products
-  // (with one q head per tile row the 64-pair box is half the tokens; TQ >= 8)
+  // boxes of 128 (token, head) pairs or keys
   CUtensorMap q1, o1, k1, v1, q2, o2, k2, pm, dm;
+  constexpr int BOX = Pr<N>::BOX;
   if (!map_bf16(&q1, a.q, D, L.n_q, a.n_rows, L.G, TQ) || !map_bf16(&o1, a.d_out, D, L.n_q, a.n_rows, L.G, TQ) ||
       !map_bf16(&k1, a.k, D, L.n_kv, a.n_rows, 1, kT) || !map_bf16(&v1, a.v, D, L.n_kv, a.n_rows, 1, kT) ||
-      !map_bf16(&q2, a.q, D, L.n_q, a.n_rows, L.G, TQ / 2) || !map_bf16(&o2, a.d_out, D, L.n_q, a.n_rows, L.G, TQ / 2) ||
-      !map_bf16(&k2, a.k, D, L.n_kv, a.n_rows, 1, 64) || !runs_map(&pm, w.p, 2, kT / 8, p.cap) ||
-      !runs_map(&dm, w.ds, 2, kT / 8, p.cap))
+      !map_bf16(&q2, a.q, D, L.n_q, a.n_rows, L.G, TQ, BOX) || !map_bf16(&o2, a.d_out, D, L.n_q, a.n_rows, L.G, TQ, BOX) ||
+      !map_bf16(&k2, a.k, D, L.n_kv, a.n_rows, 1, kT, BOX) ||
+      !runs_map(&pm, w.p, 2, kT / 8, p.cap + 1, 2, kT / 8) || !runs_map(&dm, w.ds, 2, kT / 8, p.cap + 1, 2, kT / 8))
     return cudaErrorInvalidValue;
   const long long pairs = (long long)a.n_rows * L.n_q;
   const int prep_blocks = 1 + (int)std::min<long long>(cdiv(pairs, kPrepThreads / 32), 8LL * num_sms);
-  if ((e = launch_pdl(bwd_prep_kernel<D>, dim3(prep_blocks), dim3(kPrepThreads), 0, st, a, w, p.cap, p.nl)) !=
+  if ((e = launch_pdl(bwd_prep_kernel<D>, dim3(prep_blocks), dim3(kPrepThreads), 0, st, a, w,
+                      PlanArgs{p.cap, p.nl, p.splits, p.piece})) !=
       cudaSuccess)
     return e;
   const long long items = cdiv(p.nkt, 2) * p.splits * L.n_kv * 2 * H + std::min<long long>((long long)p.nrt * L.n_kv, p.cap) * H;
@@ -1272,8 +1308,8 @@ cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t
     if ((e = launch_pdl(bwd_scores_kernel<D>, dim3(std::min(num_sms, p.cap)), dim3(kScThreads), (size_t)Sc<D>::BYTES, st,
                         a, w, c, q1, o1, k1, v1)) != cudaSuccess)
       return e;
-    if ((e = launch_pdl(bwd_products_kernel<D>, dim3((unsigned)std::min<long long>(num_sms, items)), dim3(kPrThreads),
-                        (size_t)Pr<N>::BYTES, st, a, w, ProdArgs{c, p.splits, p.nl == 1 ? p.piece : 0, p.direct}, q2, o2, k2, pm, dm)) != cudaSuccess)
+    if ((e = launch_pdl(bwd_products_kernel<D>, dim3(2 * (unsigned)std::min<long long>(num_sms / 2, items)), dim3(kPrThreads),
+                        (size_t)Pr<N>::BYTES, st, a, w, ProdArgs{c, p.cap, p.direct}, q2, o2, k2, pm, dm)) != cudaSuccess)
       return e;
   }
   if (p.direct) return cudaSuccess;
