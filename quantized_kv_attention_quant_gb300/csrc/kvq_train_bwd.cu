@@ -60,16 +60,70 @@ struct alignas(16) RowTile {
 // A key tile: keys row0 .. row0 + n - 1 (packed), tile idx of its block.
 struct alignas(16) KeyTile { int row0, n, block, idx; };
 
+// The key tiles that either of two row tiles sees: prefix tiles a0 .., own-block
+// tiles b0 .. of both (one block) or of the first and then c0 .. of the second.
+struct Merged {
+  int a0, nA, b0, nB, c0, nC;
+  __device__ __forceinline__ int n() const { return nA + nB + nC; }
+};
+__device__ __forceinline__ Merged merged(const RowTile& r0, const RowTile& r1, bool two) {
+  Merged u = {r0.a0, r0.nA, r0.b0, r0.nB, 0, 0};
+  if (!two) return u;
+  auto hull = [](int& lo, int& n, int lo1, int n1) {
+    if (n1 == 0) return;
+    const int l = n ? min(lo, lo1) : lo1, h = n ? max(lo + n, lo1 + n1) : lo1 + n1;
+    lo = l;
+    n = h - l;
+  };
+  hull(u.a0, u.nA, r1.a0, r1.nA);
+  if (r0.block == r1.block) {
+    hull(u.b0, u.nB, r1.b0, r1.nB);
+  } else {
+    u.c0 = r1.b0;
+    u.nC = r1.nB;
+  }
+  return u;
+}
+// Key tile j of a merged list: its first key's packed row and position, and its
+// place in each row tile's own list (-1: not there).
+struct MergedTile { int pk, lp, j0, j1; bool prefix; };
+__device__ __forceinline__ MergedTile merged_at(const Merged& u, const RowTile& r0, const RowTile& r1, bool two, int j) {
+  MergedTile t;
+  auto in = [](int x, int lo, int n, int base) { return x >= lo && x < lo + n ? base + x - lo : -1; };
+  t.prefix = j < u.nA;
+  if (t.prefix) {
+    const int x = u.a0 + j;
+    t.pk = t.lp = x * kT;
+    t.j0 = in(x, r0.a0, r0.nA, 0);
+    t.j1 = two ? in(x, r1.a0, r1.nA, 0) : -1;
+  } else if (j < u.nA + u.nB) {
+    const int x = u.b0 + j - u.nA;
+    t.pk = r0.off0 + x * kT;
+    t.lp = r0.kend + x * kT;                          // a branch: its first row is at position P = kend
+    t.j0 = in(x, r0.b0, r0.nB, r0.nA);
+    t.j1 = two && r1.block == r0.block ? in(x, r1.b0, r1.nB, r1.nA) : -1;
+  } else {
+    const int x = u.c0 + j - u.nA - u.nB;
+    t.pk = r1.off0 + x * kT;
+    t.lp = r1.kend + x * kT;
+    t.j0 = -1;
+    t.j1 = r1.nA + x - r1.b0;
+  }
+  return t;
+}
+
 struct Head {
   uint32_t status;
   int ok, nrt, nkt;             // layout valid; row and key tiles of one kv head
   int ntiles;                   // (row tile, key tile) pairs of one kv head
   int npieces;                  // entries of the piece list
+  int nunits;                   // units of the scores kernel, of one kv head
 };
 
 struct Ws {
   Head* head;
-  int* chunk;                   // [nl + 1]: chunk c is row tiles chunk[c] .. chunk[c + 1] - 1 (kv head major)
+  int* chunk;                   // [nl + 1]: chunk c is pairs of row tiles chunk[c] .. chunk[c + 1] - 1 (kv head major)
+  int* units;                   // [pairs of row tiles]: units of the scores kernel before each
   int* counts;                  // [nkt]: row tiles that see a key tile; then [key pairs]: pieces of its lists
   int* list;                    // the (key pair, piece) of every dk and dv item: pair * kMaxSplits + piece
   int* starts;                  // [2][n_blocks + 1]: row and key tiles before each block
@@ -88,7 +142,7 @@ struct Plan {
   int nl;                       // chunk launches
   int splits, piece;            // of a key pair's row tiles: most pieces; row tiles of one
   int direct;                   // one chunk, one split: dk and dv need no sums beside the outputs
-  size_t chunk_o, counts_o, list_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
+  size_t chunk_o, units_o, counts_o, list_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
 };
 
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
@@ -96,7 +150,10 @@ inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 // Output columns per CTA of the products kernel.
 __host__ __device__ constexpr int prod_n(int D) { return D > 256 ? 256 : D; }
 
-constexpr int kChunkTiles = 4096;
+// Tiles of a chunk (1 GB of workspace at most).  Larger is faster: 4096 rows of 16
+// heads of 512 took 1016 us in chunks of 1024 (64 MB, within L2), 751 of 2048, 612
+// in one: longer sums for each output beat L2 hits.
+constexpr int kChunkTiles = 16384;
 constexpr int kMinPiece = 12;
 
 Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows, int num_sms) {
@@ -114,10 +171,10 @@ Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows,
   const long long by_block = p.nrt * std::min(tmax, pfx + max_block_rows / (2 * kT) + 3);
   const long long by_order = n_rows / TQ * std::min(tmax, n128 / 2 + 4) + n_blocks * tmax;
   const long long total = std::min(by_block, by_order) * L.n_kv;
-  const long long cap = std::min<long long>(total, std::max<long long>(kChunkTiles, 2 * tmax));
+  const long long cap = std::min<long long>(total, std::max<long long>(kChunkTiles, 4 * tmax));
   p.cap = (int)cap;
-  // a chunk ends before a row tile that does not fit: more than cap - tmax tiles each
-  p.nl = cap >= total ? 1 : (int)cdiv(total, cap - tmax + 1);
+  // a chunk ends before a pair of row tiles that does not fit: more than cap - 2 tmax tiles each
+  p.nl = cap >= total ? 1 : (int)cdiv(total, cap - 2 * tmax + 1);
   // Splits: the list of row tiles of a key pair is cut into pieces, so that no
   // CTA's item is long beside an SM's share of the products (in steps of a pair
   // of tiles); a piece costs its output once more, so it is not cut short.
@@ -140,6 +197,7 @@ Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows,
     return at;
   };
   p.chunk_o = take(((size_t)p.nl + 1) * 4);
+  p.units_o = take(((size_t)p.nrt + 1) / 2 * 4);
   p.counts_o = take(((size_t)p.nkt + (p.nkt + 1) / 2) * 4);
   p.list_o = take(((size_t)p.nkt + 1) / 2 * kMaxSplits * 4);
   p.starts_o = take(((size_t)n_blocks + 1) * 8);
@@ -160,6 +218,7 @@ Ws carve(void* base, const Plan& p) {
   w.chunk = reinterpret_cast<int*>(b + p.chunk_o);
   w.counts = reinterpret_cast<int*>(b + p.counts_o);
   w.list = reinterpret_cast<int*>(b + p.list_o);
+  w.units = reinterpret_cast<int*>(b + p.units_o);
   w.starts = reinterpret_cast<int*>(b + p.starts_o);
   w.rt = reinterpret_cast<RowTile*>(b + p.rt_o);
   w.kt = reinterpret_cast<KeyTile*>(b + p.kt_o);
@@ -224,7 +283,7 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
   bad = __syncthreads_or(bad);
   if (bad) {                                // no tiles: nothing is written
     for (int c = tid; c <= nl; c += kPrepThreads) w.chunk[c] = 0;
-    if (tid == 0) *w.head = Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0};
+    if (tid == 0) *w.head = Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0};
     return;
   }
   int* rs = w.starts;
@@ -301,11 +360,23 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     npieces += tot;
     for (int c = 0; c < cuts; ++c) w.list[at + c] = i * kMaxSplits + c;
   }
+  // the units of every pair of row tiles
+  const int rp = (nrt + 1) / 2;
+  int nunits = 0;
+  for (int m0 = 0; m0 < rp; m0 += kPrepThreads) {
+    const int m = m0 + tid;
+    int n = 0;
+    if (m < rp) n = (merged(w.rt[2 * m], w.rt[min(2 * m + 1, nrt - 1)], 2 * m + 1 < nrt).n() + 1) / 2;
+    int tot;
+    const int at = nunits + block_scan(n, sums, &tot);
+    nunits += tot;
+    if (m < rp) w.units[m] = at;
+  }
   if (tid == 0) {
-    // chunks: as many whole row tiles as fit in cap tiles
-    const int all = nrt * a.L.n_kv;
-    auto before = [&](int x) -> long long {            // tiles before row tile x (kv head major)
-      return (long long)(x / nrt) * ntiles + (x % nrt ? w.rt[x % nrt].base : 0);
+    // chunks: as many whole pairs of row tiles as fit in cap tiles
+    const int all = rp * a.L.n_kv;
+    auto before = [&](int x) -> long long {            // tiles before pair x (kv head major)
+      return (long long)(x / rp) * ntiles + (x % rp ? w.rt[x % rp * 2].base : 0);
     };
     int x = 0, c = 0;
     w.chunk[0] = 0;
@@ -325,7 +396,7 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     while (c < nl) w.chunk[++c] = x;
     if (!fits)
       for (int i = 0; i <= nl; ++i) w.chunk[i] = 0;
-    *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles, npieces} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0};
+    *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles, npieces, nunits} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0};
   }
 }
 
@@ -463,22 +534,24 @@ struct Waiter {
 // scores: P and dS of one chunk's tiles
 // ---------------------------------------------------------------------------
 
-// A CTA takes a run of the chunk's tile list and works on units of one or two
-// key tiles of a row tile: an MMA of 256 columns reads 12 KB of shared memory in
-// 128 cycles, one of 128 columns 8 KB in 64, which with the copies' writes is
-// more than shared memory gives (measured: half the rate).  S and dP of a unit
-// fill tensor memory; the two halves alternate: while the epilogue turns S into
-// P, dP is multiplied, and while it turns dP into dS, the next unit's S.
+// A pair of CTAs (a cluster of two) works on a pair of row tiles, one each, with
+// MMAs of 256 rows x 256 keys: a unit is two of the key tiles that either row
+// tile sees, each CTA bringing one of them and its own q and dO.  Shared memory
+// is then read and written at 128 bytes a cycle for MMAs at their full rate (a
+// CTA alone needs 256 for 128 x 128 and 192 for 128 x 256 and ran at 0.5 and 0.67
+// of the rate), and L2 delivers half as much.  S and dP of a unit fill tensor
+// memory; the two halves alternate: while the epilogue turns S into P, dP is
+// multiplied, and while it turns dP into dS, the next unit's S.
 template <int D>
 struct Sc {
   static constexpr int NG = D / 64;
   static constexpr bool RES = D <= 256;               // q and dO of the row tile stay in shared memory
-  static constexpr int STAGE = RES ? 32768 : 49152;   // 64 dims of k or v, two tiles (with q's or dO's behind)
-  static constexpr int NS = D == 256 ? 3 : 4;
+  static constexpr int STAGE = RES ? 16384 : 32768;   // 64 dims of k or v, a tile (with q's or dO's behind)
+  static constexpr int NS = D <= 128 ? 8 : 6;
   static constexpr int A_OFF = 0;                     // q, then dO: NG blocks each of [128 rows x 128 B]
   static constexpr int R_OFF = RES ? 2 * NG * 16384 : 0;
   static constexpr int C_OFF = R_OFF + NS * STAGE;
-  static constexpr int BYTES = C_OFF + 256 + 1024;    // + room to align the base
+  static constexpr int BYTES = C_OFF + 512 + 1024;    // + room to align the base
 };
 // Eight epilogue warps, a key tile of the unit per four; a thread's 128 P wait for
 // dP as pairs of f16 times 2^15: 11 bits of every P above 2^-29 (8 times finer
@@ -489,18 +562,22 @@ constexpr int kScEpi = 8;
 constexpr int kScThreads = (kScEpi + 2) * 32;
 constexpr float kPScale = 32768.f;
 
-// The tiles of a CTA's run in list order.
-struct Walk {
-  int kvh, i, j;                                      // kv head, row tile, its j-th key tile
-  RowTile t;
+// What the copies tell the other warps of their CTA about a unit.
+enum : int { kUnitFresh = 1, kUnitEnd = 2 };          // another pair of row tiles; no more
+constexpr int kUnits = 4;                             // units told ahead
+struct alignas(16) Unit {
+  int flags, slot[2], lp[2];                          // this CTA's tile slots (-1: not in its list), first positions
+  int prefix;                                         // bit t: tile t holds keys of the prefix
+  int row0, nt, pos0, kend, kvh, pad;                 // this CTA's row tile
 };
-// Largest i in [0, n) with rt[i].base <= x, by the whole warp, 32 probes a step.
-__device__ __forceinline__ int find_row_tile(const RowTile* rt, int n, int x) {
+
+// Largest i in [0, n) with a[i] <= x, by the whole warp, 32 probes a step.
+__device__ __forceinline__ int find_last_le(const int* a, int n, int x) {
   const int lane = threadIdx.x & 31;
   int lo = 0, len = n;                                // the answer is in [lo, lo + len)
   while (len > 1) {
-    const int step = (len + 31) / 32, at = lo + lane * step;
-    const bool le = lane * step < len && __ldg(&rt[at].base) <= x;
+    const int step = (len + 31) / 32;
+    const bool le = lane * step < len && __ldg(a + lo + lane * step) <= x;
     const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;   // probes are non-decreasing, probe 0 holds
     len = min(step, len - k * step);
     lo += k * step;
@@ -516,36 +593,30 @@ __device__ __forceinline__ RowTile load_row_tile(const RowTile* rt, int i) {
   d[2] = __ldg(s + 2);
   return t;
 }
-// Key tile j of row tile t: its first key's packed row and position.
-__device__ __forceinline__ void key_tile_at(const RowTile& t, int j, int& pk, int& lp) {
-  if (j < t.nA) {
-    pk = lp = (t.a0 + j) * kT;
-  } else {
-    const int o = (t.b0 + j - t.nA) * kT;
-    pk = t.off0 + o;
-    lp = t.kend + o;                                  // a branch: its first row is at position P = kend
-  }
-}
 
 template <int D>
-__global__ void __launch_bounds__(kScThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
 bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __grid_constant__ CUtensorMap tmq,
                   const __grid_constant__ CUtensorMap tmo, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv) {
   using T = Sc<D>;
   constexpr int NG = T::NG;
   extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ Unit units[kUnits];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::C_OFF);
+  const int rank = (int)tc::cta_rank();
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::C_OFF);      // CTA 0's: both CTAs' copies landed
   uint64_t* empty = full + T::NS;
-  uint64_t* a_full = empty + T::NS;                   // q and dO landed
-  uint64_t* a_free = a_full + 1;                      // the row tile's products are done
+  uint64_t* a_full = empty + T::NS;                   // CTA 0's: q and dO landed
+  uint64_t* a_free = a_full + 1;                      // the row tiles' products are done
   uint64_t* acc_full = a_free + 1;                    // [2] a unit's S, its dP done
-  uint64_t* acc_free = acc_full + 2;                  // [2] read by the epilogue
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + 2);
+  uint64_t* acc_free = acc_full + 2;                  // [2] CTA 0's: read by both epilogues
+  uint64_t* unit_full = acc_free + 2;                 // [kUnits]
+  uint64_t* unit_empty = unit_full + kUnits;          // [kUnits]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(unit_empty + kUnits);
   if (tid == 0) {
     for (int s = 0; s < T::NS; ++s) {
       mbar_init(full + s, 1);
@@ -555,228 +626,265 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
     mbar_init(a_free, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(acc_full + s, 1);
-      mbar_init(acc_free + s, kScEpi);
+      mbar_init(acc_free + s, 2 * kScEpi);
+    }
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(unit_full + s, 1);
+      mbar_init(unit_empty + s, kScEpi + (rank == 0 ? 1 : 0));      // the epilogue, and CTA 0's MMA warp
     }
     fence_mbar_init();
   }
   if (warp == 0) {
-    tc::tmem_alloc(tslot, 512);
-    tc::tmem_relinquish();
+    tc::tmem_alloc2(tslot, 512);
+    tc::tmem_relinquish2();
   }
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();                                 // both CTAs' barriers and tensor memory are there
   tc::fence_after_sync();
   const uint32_t tmem = *tslot;
   pdl_wait();                                         // the plan and delta; the last chunk's tiles are read
   pdl_launch();
 
-  const int G = a.L.G, nrt = w.head->nrt, ntiles = w.head->ntiles;
-  const int x0 = w.chunk[chunk], x1 = w.chunk[chunk + 1];
+  const int G = a.L.G;
   Waiter wait{&w.head->status};
-  if (x0 < x1) {
-    // this CTA's run of the chunk's tiles
-    const long long c0 = (long long)(x0 / nrt) * ntiles + w.rt[x0 % nrt].base;
-    const long long c1 = (long long)(x1 / nrt) * ntiles + (x1 % nrt ? w.rt[x1 % nrt].base : 0);
-    const int g0 = (int)((c1 - c0) * blockIdx.x / gridDim.x), g1 = (int)((c1 - c0) * (blockIdx.x + 1) / gridDim.x);
-    Walk k;
-    if (g0 < g1) {
-      k.kvh = (int)((c0 + g0) / ntiles);
-      const int rem = (int)((c0 + g0) % ntiles);
-      k.i = find_row_tile(w.rt, nrt, rem);
-      k.t = load_row_tile(w.rt, k.i);
-      k.j = rem - k.t.base;
+  if (warp == kScEpi) {
+    // ================= the walk, and copies: this CTA's row tile and one key tile of a unit =================
+    const Head hd = *w.head;
+    const int x0 = w.chunk[chunk], x1 = w.chunk[chunk + 1], rp = (hd.nrt + 1) / 2;
+    long long u0 = 0, u1 = 0, c0 = 0;                 // this pair's units of the chunk; tiles before the chunk
+    if (x0 < x1) {
+      auto before = [&](int x) { return (long long)(x / rp) * hd.nunits + (x % rp ? __ldg(w.units + x % rp) : 0); };
+      const long long b0 = before(x0), n = before(x1) - b0;
+      u0 = b0 + n * (blockIdx.x / 2) / (gridDim.x / 2);
+      u1 = b0 + n * (blockIdx.x / 2 + 1) / (gridDim.x / 2);
+      c0 = (long long)(x0 / rp) * hd.ntiles + (x0 % rp ? __ldg(&w.rt[x0 % rp * 2].base) : 0);
     }
-    // tiles of the unit at list place g, and the step past it (true: another row tile)
-    auto unit = [&](int g) { return g + 1 < g1 && k.j + 1 < k.t.nA + k.t.nB ? 2 : 1; };
-    auto next = [&](int tiles) -> bool {
-      if ((k.j += tiles) < k.t.nA + k.t.nB) return false;
-      k.j = 0;
-      if (++k.i == nrt) {
-        k.i = 0;
-        ++k.kvh;
-      }
-      k.t = load_row_tile(w.rt, k.i);
-      return true;
-    };
-
-    if (warp == kScEpi) {
-      // ================= copies =================
-      int st = 0, ph = 0, rts = 0;                    // ring stage, its phase; row tiles begun
-      bool fresh = true;
-      for (int g = g0; g < g1;) {
-        const int tiles = unit(g);
-        int pk[2], lp;
-        key_tile_at(k.t, k.j, pk[0], lp);
-        if (tiles == 2) key_tile_at(k.t, k.j + 1, pk[1], lp);
-        if (T::RES && fresh) {
-          if (rts > 0) wait(a_free, (rts - 1) & 1);
-          if (lane == 0) {
-            mbar_arrive_expect_tx(a_full, 2 * NG * 16384);
-            for (int c = 0; c < NG; ++c) {
-              tc::tma_load_3d(sb + T::A_OFF + c * 16384, &tmq, 64 * c, k.kvh * G, k.t.row0, smem_u32(a_full));
-              tc::tma_load_3d(sb + T::A_OFF + (NG + c) * 16384, &tmo, 64 * c, k.kvh * G, k.t.row0, smem_u32(a_full));
-            }
-          }
-          ++rts;
-        }
-        for (int c = 0; c < 2 * NG; ++c) {
-          wait(empty + st, ph ^ 1);
-          if (lane == 0) {
-            const int dim = 64 * (c < NG ? c : c - NG);
-            const uint32_t dst = sb + T::R_OFF + st * T::STAGE, bar = smem_u32(full + st);
-            mbar_arrive_expect_tx(full + st, (tiles + (T::RES ? 0 : 1)) * 16384);
-            if (!T::RES) tc::tma_load_3d(dst + 32768, c < NG ? &tmq : &tmo, dim, k.kvh * G, k.t.row0, bar);
-            tc::tma_load_3d(dst, c < NG ? &tmk : &tmv, dim, k.kvh, pk[0], bar);
-            if (tiles == 2) tc::tma_load_3d(dst + 16384, c < NG ? &tmk : &tmv, dim, k.kvh, pk[1], bar);
-          }
-          __syncwarp();
-          if (++st == T::NS) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
-        g += tiles;
-        fresh = g < g1 && next(tiles);
-      }
-    } else if (warp == kScEpi + 1) {
-      // ================= S = q k^T, dP = dO v^T =================
-      int st = 0, ph = 0, rts = 0, n = 0;
-      bool fresh = true;
-      for (int g = g0; g < g1; ++n) {
-        const int tiles = unit(g);
-        const uint32_t ID = tc::idesc_bf16_f32(kT, kT) + (tiles == 2 ? tc::idesc_bf16_f32(kT, 2 * kT) - tc::idesc_bf16_f32(kT, kT) : 0u);
-        if (T::RES && fresh) wait(a_full, rts++ & 1);
-        for (int c = 0; c < 2 * NG; ++c) {
-          const int half = c >= NG;
-          if (n > 0 && (c == 0 || c == NG)) wait(acc_free + half, (n - 1) & 1);
-          wait(full + st, ph);
-          tc::fence_after_sync();
-          if (lane == 0) {
-            const uint32_t bs = sb + T::R_OFF + st * T::STAGE;
-            const uint32_t as = T::RES ? sb + T::A_OFF + c * 16384 : bs + 32768;
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              tc::mma_f16(tmem + 256 * half, tc::desc_kmajor_sw128(as + 32 * s, 1024),
-                          tc::desc_kmajor_sw128(bs + 32 * s, 1024), ID, (c != 0 && c != NG) || s != 0);
-            tc::commit(empty + st);
-            if (c == NG - 1 || c == 2 * NG - 1) tc::commit(acc_full + half);
-          }
-          __syncwarp();
-          if (++st == T::NS) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
-        g += tiles;
-        fresh = g < g1 && next(tiles);
-        if (T::RES && fresh && lane == 0) tc::commit(a_free);
-        __syncwarp();
-      }
-    } else {
-      // ================= P and dS: thread = row, one key tile of the unit =================
-      const int r = 32 * (warp & 3) + lane, mine = warp >> 2, W = a.L.window;
-      const int tq = r / G, h = r % G;
-      const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kT * mine;
-      float lse2 = 0.f, delta = 0.f;                  // log2(e) lse, delta / 2^15
-      int lo = 0, hi = -1, cut = -1;                  // visible positions: lo .. hi, in prefix tiles lo .. cut
-      bool fresh = true;
-      int n = 0;
-      for (int g = g0; g < g1; ++n) {
-        const int tiles = unit(g);
+    int kvh = 0, m = 0, j = 0;                        // kv head, pair of row tiles, next key tile of its list
+    if (u0 < u1) {
+      kvh = (int)(u0 / hd.nunits);
+      const int rem = (int)(u0 % hd.nunits);
+      m = find_last_le(w.units, rp, rem);
+      j = 2 * (rem - __ldg(w.units + m));
+    }
+    if (lane == 0) {
+      const uint32_t full0 = tc::in_cta0(full), a_full0 = tc::in_cta0(a_full);
+      int st = 0, ph = 0, pairs = 0, n = 0;
+      bool fresh = true, two = false;
+      RowTile r0 = {}, r1 = {};
+      Merged u = {};
+      for (long long g = u0; g < u1; ++g, ++n) {
         if (fresh) {
-          const bool valid = tq < k.t.nt;
-          const int pos = k.t.pos0 + tq;
-          lo = W > 0 ? max(0, pos - W + 1) : 0;
-          hi = valid ? pos : -1;
-          cut = valid ? min(pos, k.t.kend - 1) : -1;
-          if (valid) {
-            const size_t o = (size_t)(k.t.row0 + tq) * a.L.n_q + k.kvh * G + h;
-            lse2 = __ldg(a.lse + o) * kL2E;
-            delta = w.delta[o] * (1.f / kPScale);
+          r0 = load_row_tile(w.rt, 2 * m);
+          two = 2 * m + 1 < hd.nrt;
+          r1 = load_row_tile(w.rt, two ? 2 * m + 1 : 2 * m);
+          u = merged(r0, r1, two);
+        }
+        const bool more = j + 1 < u.n();
+        const MergedTile t0 = merged_at(u, r0, r1, two, j), t1 = merged_at(u, r0, r1, two, more ? j + 1 : j);
+        const int k0 = rank == 0 ? t0.j0 : t0.j1, k1 = !more ? -1 : rank == 0 ? t1.j0 : t1.j1;
+        const int base = (int)((long long)kvh * hd.ntiles - c0 + (rank == 0 ? r0.base : r1.base));
+        const int row0 = rank == 0 ? r0.row0 : r1.row0, pk = rank == 0 ? t0.pk : t1.pk, e = n % kUnits;
+        wait.one(unit_empty + e, (n / kUnits & 1) ^ 1);
+        Unit& un = units[e];
+        un.flags = fresh ? kUnitFresh : 0;
+        un.slot[0] = k0 < 0 ? -1 : base + k0;
+        un.slot[1] = k1 < 0 ? -1 : base + k1;
+        un.lp[0] = t0.lp;
+        un.lp[1] = t1.lp;
+        un.prefix = (t0.prefix ? 1 : 0) | (t1.prefix ? 2 : 0);
+        un.row0 = row0;
+        un.nt = rank == 0 ? r0.nt : two ? r1.nt : 0;
+        un.pos0 = rank == 0 ? r0.pos0 : r1.pos0;
+        un.kend = rank == 0 ? r0.kend : r1.kend;
+        un.kvh = kvh;
+        mbar_arrive(unit_full + e);
+        if (T::RES && fresh) {                        // (told before: on it the MMA warp frees the last row tiles)
+          if (pairs > 0) wait.one(a_free, (pairs - 1) & 1);
+          if (rank == 0) mbar_arrive_expect_tx(a_full, 4 * NG * 16384);
+          for (int c = 0; c < NG; ++c) {
+            tc::tma2_load_3d(sb + T::A_OFF + c * 16384, &tmq, 64 * c, kvh * G, row0, a_full0);
+            tc::tma2_load_3d(sb + T::A_OFF + (NG + c) * 16384, &tmo, 64 * c, kvh * G, row0, a_full0);
+          }
+          ++pairs;
+        }
+        for (int c = 0; c < 2 * NG; ++c) {
+          wait.one(empty + st, ph ^ 1);
+          const int dim = 64 * (c < NG ? c : c - NG);
+          const uint32_t dst = sb + T::R_OFF + st * T::STAGE, bar = full0 + 8 * st;
+          if (rank == 0) mbar_arrive_expect_tx(full + st, 2 * T::STAGE);
+          tc::tma2_load_3d(dst, c < NG ? &tmk : &tmv, dim, kvh, pk, bar);
+          if (!T::RES) tc::tma2_load_3d(dst + 16384, c < NG ? &tmq : &tmo, dim, kvh * G, row0, bar);
+          if (++st == T::NS) {
+            st = 0;
+            ph ^= 1;
           }
         }
-        const bool busy = mine < tiles;
-        int pk, lp;
-        key_tile_at(k.t, k.j + mine, pk, lp);
-        const int top = k.j + mine < k.t.nA ? cut : hi;
-        // (a row that sees one key does not see 128: it always takes the masked form)
-        const bool whole = __all_sync(0xffffffffu, lp >= lo && lp + kT - 1 <= top);
-        const size_t at = (size_t)(g + mine) * kTileBytes + r * 16;
-        uint32_t ph[kT / 2];
-        wait(acc_full, n & 1);
-        tc::fence_after_sync();
+        j += 2;
+        fresh = j >= u.n();
+        if (fresh) {
+          j = 0;
+          if (++m == rp) {
+            m = 0;
+            ++kvh;
+          }
+        }
+      }
+      wait.one(unit_empty + n % kUnits, (n / kUnits & 1) ^ 1);
+      units[n % kUnits].flags = kUnitEnd;
+      mbar_arrive(unit_full + n % kUnits);
+      // every stage consumed, in both CTAs, before either may leave
+      for (int i = 0; i < T::NS; ++i) {
+        wait.one(empty + st, ph ^ 1);
+        if (++st == T::NS) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kScEpi + 1) {
+    // ================= S = q k^T, dP = dO v^T (CTA 0, for both) =================
+    constexpr uint32_t ID = tc::idesc_bf16_f32(2 * kT, 2 * kT);
+    int st = 0, ph = 0, pairs = 0;
+    for (int n = 0; rank == 0; ++n) {
+      const int e = n % kUnits;
+      wait(unit_full + e, n / kUnits & 1);
+      const int flags = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&units[e].flags), 0);
+      if (lane == 0) mbar_arrive(unit_empty + e);
+      if ((flags & kUnitEnd) || wait.dead) break;
+      if (T::RES && (flags & kUnitFresh)) {
+        if (pairs > 0 && lane == 0) tc::commit2(a_free);
         __syncwarp();
-#pragma unroll
-        for (int q = 0; q < kT / 16; ++q) {
-          float p[16];
-          if (busy) {
-            tc::ld_x16(ts + 16 * q, p);
-            tc::wait_ld();
-          }
-          if (q == kT / 16 - 1) {                               // S is read
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_free);
-          }
-          if (busy) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] = ex2(fmaf(p[i], kL2E, -lse2));
-            if (!whole) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) p[i] = lp + 16 * q + i >= lo && lp + 16 * q + i <= top ? p[i] : 0.f;
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              *reinterpret_cast<uint4*>(w.p + at + (2 * q + c) * 2048) =
-                  make_uint4(pack_bf2(p[8 * c], p[8 * c + 1]), pack_bf2(p[8 * c + 2], p[8 * c + 3]),
-                             pack_bf2(p[8 * c + 4], p[8 * c + 5]), pack_bf2(p[8 * c + 6], p[8 * c + 7]));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ph[8 * q + i] = pack_h2(p[2 * i] * kPScale, p[2 * i + 1] * kPScale);
-          }
-        }
-        if (!whole && lo >= hi) {                     // one key: dS = 0
-#pragma unroll
-          for (int i = 0; i < kT / 2; ++i) ph[i] = 0u;
-        }
-        wait(acc_full + 1, n & 1);
+        wait(a_full, pairs++ & 1);
+      }
+      for (int c = 0; c < 2 * NG; ++c) {
+        const int half = c >= NG;
+        if (n > 0 && (c == 0 || c == NG)) wait(acc_free + half, (n - 1) & 1);
+        wait(full + st, ph);
         tc::fence_after_sync();
-        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bs = sb + T::R_OFF + st * T::STAGE;
+          const uint32_t as = T::RES ? sb + T::A_OFF + c * 16384 : bs + 16384;
 #pragma unroll
-        for (int q = 0; q < kT / 16; ++q) {
-          float d[16];
-          if (busy) {
-            tc::ld_x16(ts + 256 + 16 * q, d);
-            tc::wait_ld();
-          }
-          if (q == kT / 16 - 1) {                               // dP is read
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_free + 1);
-          }
-          if (busy) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&ph[8 * q + i]));
-              d[2 * i] = p.x * fmaf(d[2 * i], 1.f / kPScale, -delta);
-              d[2 * i + 1] = p.y * fmaf(d[2 * i + 1], 1.f / kPScale, -delta);
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              *reinterpret_cast<uint4*>(w.ds + at + (2 * q + c) * 2048) =
-                  make_uint4(pack_bf2(d[8 * c], d[8 * c + 1]), pack_bf2(d[8 * c + 2], d[8 * c + 3]),
-                             pack_bf2(d[8 * c + 4], d[8 * c + 5]), pack_bf2(d[8 * c + 6], d[8 * c + 7]));
-          }
+          for (int s = 0; s < 4; ++s)
+            tc::mma2_f16(tmem + 256 * half, tc::desc_kmajor_sw128(as + 32 * s, 1024),
+                         tc::desc_kmajor_sw128(bs + 32 * s, 1024), ID, (c != 0 && c != NG) || s != 0);
+          tc::commit2(empty + st);
+          if (c == NG - 1 || c == 2 * NG - 1) tc::commit2(acc_full + half);
         }
-        g += tiles;
-        fresh = g < g1 && next(tiles);
+        __syncwarp();
+        if (++st == T::NS) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+  } else {
+    // ================= P and dS: thread = row, one key tile of the unit =================
+    const int r = 32 * (warp & 3) + lane, mine = warp >> 2, W = a.L.window;
+    const int tq = r / G, h = r % G;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kT * mine;
+    float lse2 = 0.f, delta = 0.f;                    // log2(e) lse, delta / 2^15
+    int lo = 0, hi = -1, cut = -1;                    // visible positions: lo .. hi, in prefix tiles lo .. cut
+    for (int n = 0;; ++n) {
+      const int e = n % kUnits;
+      wait(unit_full + e, n / kUnits & 1);
+      const Unit un = units[e];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(unit_empty + e);
+      if ((un.flags & kUnitEnd) || wait.dead) break;
+      if (un.flags & kUnitFresh) {
+        const bool valid = tq < un.nt;
+        const int pos = un.pos0 + tq;
+        lo = W > 0 ? max(0, pos - W + 1) : 0;
+        hi = valid ? pos : -1;
+        cut = valid ? min(pos, un.kend - 1) : -1;
+        if (valid) {
+          const size_t o = (size_t)(un.row0 + tq) * a.L.n_q + un.kvh * G + h;
+          lse2 = __ldg(a.lse + o) * kL2E;
+          delta = w.delta[o] * (1.f / kPScale);
+        }
+      }
+      const int slot = mine ? un.slot[1] : un.slot[0], lp = mine ? un.lp[1] : un.lp[0];
+      const bool busy = slot >= 0;
+      const int top = un.prefix >> mine & 1 ? cut : hi;
+      // (a row that sees one key does not see 128: it always takes the masked form)
+      const bool whole = __all_sync(0xffffffffu, lp >= lo && lp + kT - 1 <= top);
+      const size_t at = (size_t)(busy ? slot : 0) * kTileBytes + r * 16;
+      uint32_t ph[kT / 2];
+      wait(acc_full, n & 1);
+      tc::fence_after_sync();
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kT / 16; ++q) {
+        float p[16];
+        if (busy) {
+          tc::ld_x16(ts + 16 * q, p);
+          tc::wait_ld();
+        }
+        if (q == kT / 16 - 1) {                       // S is read
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::arrive_cta0(acc_free);
+        }
+        if (busy) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = ex2(fmaf(p[i], kL2E, -lse2));
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] = lp + 16 * q + i >= lo && lp + 16 * q + i <= top ? p[i] : 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(w.p + at + (2 * q + c) * 2048) =
+                make_uint4(pack_bf2(p[8 * c], p[8 * c + 1]), pack_bf2(p[8 * c + 2], p[8 * c + 3]),
+                           pack_bf2(p[8 * c + 4], p[8 * c + 5]), pack_bf2(p[8 * c + 6], p[8 * c + 7]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ph[8 * q + i] = pack_h2(p[2 * i] * kPScale, p[2 * i + 1] * kPScale);
+        }
+      }
+      if (!whole && lo >= hi) {                       // one key: dS = 0
+#pragma unroll
+        for (int i = 0; i < kT / 2; ++i) ph[i] = 0u;
+      }
+      wait(acc_full + 1, n & 1);
+      tc::fence_after_sync();
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kT / 16; ++q) {
+        float d[16];
+        if (busy) {
+          tc::ld_x16(ts + 256 + 16 * q, d);
+          tc::wait_ld();
+        }
+        if (q == kT / 16 - 1) {                       // dP is read
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::arrive_cta0(acc_free + 1);
+        }
+        if (busy) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&ph[8 * q + i]));
+            d[2 * i] = p.x * fmaf(d[2 * i], 1.f / kPScale, -delta);
+            d[2 * i + 1] = p.y * fmaf(d[2 * i + 1], 1.f / kPScale, -delta);
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(w.ds + at + (2 * q + c) * 2048) =
+                make_uint4(pack_bf2(d[8 * c], d[8 * c + 1]), pack_bf2(d[8 * c + 2], d[8 * c + 3]),
+                           pack_bf2(d[8 * c + 4], d[8 * c + 5]), pack_bf2(d[8 * c + 6], d[8 * c + 7]));
+        }
       }
     }
   }
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();                                 // neither CTA's memory is written or read any more
   if (warp == 0) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc2(tmem, 512);
   }
 }
 
@@ -880,9 +988,8 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   // an empty chunk (or layout) has no items; dk and dv come first (the longest sums)
   const int rp = (hd.nrt + 1) / 2;
   const int n_dkv = x0 < x1 ? hd.npieces * nkv * 2 * H : 0;
-  const int q0 = x0 < x1 ? x0 / hd.nrt * rp + x0 % hd.nrt / 2 : 0;
-  const int n_items = x0 < x1 ? n_dkv + ((x1 - 1) / hd.nrt * rp + (x1 - 1) % hd.nrt / 2 - q0 + 1) * H : 0;
-  const long long c0 = x0 < x1 ? (long long)(x0 / hd.nrt) * hd.ntiles + w.rt[x0 % hd.nrt].base : 0;
+  const int n_items = n_dkv + (x1 - x0) * H;
+  const long long c0 = x0 < x1 ? (long long)(x0 / rp) * hd.ntiles + w.rt[x0 % rp * 2].base : 0;
   auto decode = [&](int id) {
     Item t;
     t.dkv = id < n_dkv;
@@ -900,10 +1007,10 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
       t.t0 = id / kMaxSplits * 2;
       t.n = min(2, hd.nkt - t.t0);
     } else {
-      id += q0;
+      id += x0;
       t.kvh = id / rp;
-      t.t0 = max(id % rp * 2, x0 - t.kvh * hd.nrt);   // a pair at the chunk's edge may be cut
-      t.n = min(min(hd.nrt, x1 - t.kvh * hd.nrt), id % rp * 2 + 2) - t.t0;
+      t.t0 = id % rp * 2;
+      t.n = min(2, hd.nrt - t.t0);
     }
     return t;
   };
@@ -959,7 +1066,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         // the chunk's row tiles that see either key tile; this piece's share of them by count
         const KeyTile ka = w.kt[it.t0], kb = w.kt[it.t0 + it.n - 1];
         const int cuts = w.counts[hd.nkt + it.t0 / 2];
-        const int xs = max(0, x0 - it.kvh * hd.nrt), xe = min(hd.nrt, x1 - it.kvh * hd.nrt);
+        const int xs = 2 * max(0, x0 - it.kvh * rp), xe = min(hd.nrt, 2 * (x1 - it.kvh * rp));
         auto tile_of = [&](const KeyTile& t, const RowTile& r) -> int {      // its place in the row tile's list
           if (t.block == 0) return t.idx >= r.a0 && t.idx < r.a0 + r.nA ? t.idx - r.a0 : -1;
           return t.block == r.block && t.idx >= r.b0 && t.idx < r.b0 + r.nB ? r.nA + t.idx - r.b0 : -1;
@@ -999,25 +1106,14 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
           seen += __popc(m);
         }
       } else {
-        const RowTile r0 = load_row_tile(w.rt, it.t0);
-        RowTile r1 = load_row_tile(w.rt, it.t0 + it.n - 1);
-        if (it.n == 1) r1.nA = r1.nB = 0;
+        const bool two = it.n == 2;
+        const RowTile r0 = load_row_tile(w.rt, it.t0), r1 = load_row_tile(w.rt, it.t0 + it.n - 1);
+        const Merged u = merged(r0, r1, two);
         const int base0 = (int)(slot0 + r0.base), base1 = (int)(slot0 + r1.base);
-        // the key tiles either row tile sees: both lists merged, prefix then own block
-        auto walk = [&](auto f) {
-          auto range = [&](int lo0, int n0, int o0, int lo1, int n1, int o1, int row) {
-            const int lo = n0 == 0 ? lo1 : n1 == 0 ? lo0 : min(lo0, lo1), hi = max(n0 ? lo0 + n0 : 0, n1 ? lo1 + n1 : 0);
-            for (int x = lo; x < hi; ++x) {
-              const bool in0 = x >= lo0 && x < lo0 + n0, in1 = x >= lo1 && x < lo1 + n1;
-              if (in0 || in1) f(in0 ? o0 + x - lo0 : -1, in1 ? o1 + x - lo1 : -1, row + x * kT);
-            }
-          };
-          range(r0.a0, r0.nA, base0, r1.a0, r1.nA, base1, 0);
-          if (r0.block == r1.block) {
-            range(r0.b0, r0.nB, base0 + r0.nA, r1.b0, r1.nB, base1 + r1.nA, r0.off0);
-          } else {
-            range(r0.b0, r0.nB, base0 + r0.nA, 0, 0, 0, r0.off0);
-            range(0, 0, 0, r1.b0, r1.nB, base1 + r1.nA, r1.off0);
+        auto walk = [&](auto f) {                     // the key tiles either row tile sees
+          for (int j = 0; j < u.n(); ++j) {
+            const MergedTile t = merged_at(u, r0, r1, two, j);
+            if (t.j0 >= 0 || t.j1 >= 0) f(t.j0 < 0 ? -1 : base0 + t.j0, t.j1 < 0 ? -1 : base1 + t.j1, t.pk);
           }
         };
         walk([&](int, int, int) { ++left; });
@@ -1305,7 +1401,7 @@ cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t
   const long long items = cdiv(p.nkt, 2) * p.splits * L.n_kv * 2 * H + std::min<long long>((long long)p.nrt * L.n_kv, p.cap) * H;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   for (int c = 0; c < p.nl; ++c) {
-    if ((e = launch_pdl(bwd_scores_kernel<D>, dim3(std::min(num_sms, p.cap)), dim3(kScThreads), (size_t)Sc<D>::BYTES, st,
+    if ((e = launch_pdl(bwd_scores_kernel<D>, dim3(2 * std::min(num_sms / 2, p.cap)), dim3(kScThreads), (size_t)Sc<D>::BYTES, st,
                         a, w, c, q1, o1, k1, v1)) != cudaSuccess)
       return e;
     if ((e = launch_pdl(bwd_products_kernel<D>, dim3(2 * (unsigned)std::min<long long>(num_sms / 2, items)), dim3(kPrThreads),
