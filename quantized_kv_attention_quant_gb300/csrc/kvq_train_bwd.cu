@@ -46,6 +46,7 @@ namespace {
 constexpr int kT = 128;                     // rows and keys of a tile
 constexpr uint32_t kTileBytes = kT * kT * 2;
 constexpr int kMaxSplits = 8;
+constexpr int kMaxPairs = 128;              // CTA pairs of a grid
 constexpr float kL2E = 1.4426950408889634f;
 
 // A row tile: tokens row0 .. row0 + nt - 1 (packed), the first at position
@@ -126,6 +127,7 @@ struct Ws {
   int* units;                   // [pairs of row tiles]: units of the scores kernel before each
   int* counts;                  // [nkt]: row tiles that see a key tile; then [key pairs]: pieces of its lists
   int* list;                    // the (key pair, piece) of every dk and dv item: pair * kMaxSplits + piece
+  int4* begin;                  // [pairs]: a CTA pair's units, and the kv head, row tile pair and key tile of its first
   int* starts;                  // [2][n_blocks + 1]: row and key tiles before each block
   RowTile* rt;
   KeyTile* kt;
@@ -142,7 +144,7 @@ struct Plan {
   int nl;                       // chunk launches
   int splits, piece;            // of a key pair's row tiles: most pieces; row tiles of one
   int direct;                   // one chunk, one split: dk and dv need no sums beside the outputs
-  size_t chunk_o, units_o, counts_o, list_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
+  size_t chunk_o, begin_o, units_o, counts_o, list_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
 };
 
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
@@ -197,6 +199,7 @@ Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows,
     return at;
   };
   p.chunk_o = take(((size_t)p.nl + 1) * 4);
+  p.begin_o = take(kMaxPairs * sizeof(int4));
   p.units_o = take(((size_t)p.nrt + 1) / 2 * 4);
   p.counts_o = take(((size_t)p.nkt + (p.nkt + 1) / 2) * 4);
   p.list_o = take(((size_t)p.nkt + 1) / 2 * kMaxSplits * 4);
@@ -219,6 +222,7 @@ Ws carve(void* base, const Plan& p) {
   w.counts = reinterpret_cast<int*>(b + p.counts_o);
   w.list = reinterpret_cast<int*>(b + p.list_o);
   w.units = reinterpret_cast<int*>(b + p.units_o);
+  w.begin = reinterpret_cast<int4*>(b + p.begin_o);
   w.starts = reinterpret_cast<int*>(b + p.starts_o);
   w.rt = reinterpret_cast<RowTile*>(b + p.rt_o);
   w.kt = reinterpret_cast<KeyTile*>(b + p.kt_o);
@@ -268,15 +272,25 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
 }
 
 // What the plan needs of the host's: tiles of a chunk, chunks, and how lists are cut.
-struct PlanArgs { int cap, nl, splits, piece; };
+struct PlanArgs { int cap, nl, splits, piece, pairs; };       // pairs: CTA pairs of the scores kernel
 
 __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl) {
-  __shared__ int sums[kPrepThreads / 32];
+  // what later steps look up again stays in shared memory where it is small (the
+  // chain of dependent loads is the whole time of a short call)
+  constexpr int kS = kPrepThreads;
+  __shared__ int sums[kPrepThreads / 32], s_off[kS + 1], s_rs[kS], s_ks[kS], s_counts[kS], s_units[kS];
+  __shared__ RowTile s_rt[kS];
   const int tid = threadIdx.x, nb = a.n_blocks, TQ = kT / a.L.G, W = a.L.window, cap = pl.cap, nl = pl.nl;
-  const int P = a.off[1];
+  const int32_t* off = a.off;
+  if (nb <= kS) {
+    for (int b = tid; b <= nb; b += kPrepThreads) s_off[b] = a.off[b];
+    __syncthreads();
+    off = s_off;
+  }
+  const int P = off[1];
   bool bad = false;
   for (int b = tid; b < nb; b += kPrepThreads) {
-    const int o0 = a.off[b], o1 = a.off[b + 1];
+    const int o0 = off[b], o1 = off[b + 1];
     bad |= !(o0 >= 0 && o0 <= o1 && o1 <= a.n_rows && P >= 0 && (b == 0 ? o0 == 0 : o0 >= P) &&
              (b + 1 < nb || o1 == a.n_rows) && o1 - o0 <= a.max_block_rows);
   }
@@ -286,11 +300,11 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     if (tid == 0) *w.head = Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0};
     return;
   }
-  int* rs = w.starts;
-  int* ks = w.starts + nb + 1;
+  int* rs = nb <= kS ? s_rs : w.starts;
+  int* ks = nb <= kS ? s_ks : w.starts + nb + 1;
   int nrt = 0, nkt = 0;
   for (int b0 = 0; b0 < nb; b0 += kPrepThreads) {
-    const int b = b0 + tid, rows = b < nb ? a.off[b + 1] - a.off[b] : 0;
+    const int b = b0 + tid, rows = b < nb ? off[b + 1] - off[b] : 0;
     int tr, tk;
     const int r = block_scan((rows + TQ - 1) / TQ, sums, &tr), k = block_scan((rows + kT - 1) / kT, sums, &tk);
     if (b < nb) {
@@ -300,11 +314,13 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     nrt += tr;
     nkt += tk;
   }
+  int* counts = nkt <= kS ? s_counts : w.counts;
+  RowTile* rt = nrt <= kS ? s_rt : w.rt;
   __syncthreads();
   for (int i = tid; i < nkt; i += kPrepThreads) {
-    const int b = last_le(ks, nb, i), idx = i - ks[b], o0 = a.off[b];
-    w.kt[i] = KeyTile{o0 + idx * kT, min(kT, a.off[b + 1] - o0 - idx * kT), b, idx};
-    w.counts[i] = 0;
+    const int b = last_le(ks, nb, i), idx = i - ks[b], o0 = off[b];
+    w.kt[i] = KeyTile{o0 + idx * kT, min(kT, off[b + 1] - o0 - idx * kT), b, idx};
+    counts[i] = 0;
   }
   __syncthreads();
   int ntiles = 0;
@@ -312,7 +328,7 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     const int i = i0 + tid;
     RowTile t = {};
     if (i < nrt) {
-      const int b = last_le(rs, nb, i), o0 = a.off[b], rows = a.off[b + 1] - o0, t0 = (i - rs[b]) * TQ;
+      const int b = last_le(rs, nb, i), o0 = off[b], rows = off[b + 1] - o0, t0 = (i - rs[b]) * TQ;
       const int first = b == 0 ? 0 : P;
       t.row0 = o0 + t0;
       t.nt = min(TQ, rows - t0);
@@ -336,9 +352,10 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     ntiles += tot;
     if (i < nrt) {
       w.rt[i] = t;
-      if (nl == 1) {                                   // (whole numbers: their order does not matter)
-        for (int j = 0; j < t.nA; ++j) atomicAdd(w.counts + t.a0 + j, 1);
-        for (int j = 0; j < t.nB; ++j) atomicAdd(w.counts + ks[t.block] + t.b0 + j, 1);
+      if (nrt <= kS) s_rt[i] = t;
+      if (pl.splits > 1 && nl == 1) {                  // (whole numbers: their order does not matter)
+        for (int j = 0; j < t.nA; ++j) atomicAdd(counts + t.a0 + j, 1);
+        for (int j = 0; j < t.nB; ++j) atomicAdd(counts + ks[t.block] + t.b0 + j, 1);
       }
     }
   }
@@ -351,7 +368,8 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     const int i = i0 + tid;
     int cuts = 0;
     if (i < nkp) {
-      const int n = max(__ldcg(w.counts + 2 * i), 2 * i + 1 < nkt ? __ldcg(w.counts + 2 * i + 1) : 0);
+      const volatile int* c = counts;
+      const int n = max(c[2 * i], 2 * i + 1 < nkt ? c[2 * i + 1] : 0);
       cuts = nl == 1 ? max(1, min(pl.splits, n / pl.piece)) : pl.splits;
       w.counts[nkt + i] = cuts;
     }
@@ -362,19 +380,40 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
   }
   // the units of every pair of row tiles
   const int rp = (nrt + 1) / 2;
+  int* units = rp <= kS ? s_units : w.units;
   int nunits = 0;
   for (int m0 = 0; m0 < rp; m0 += kPrepThreads) {
     const int m = m0 + tid;
     int n = 0;
-    if (m < rp) n = (merged(w.rt[2 * m], w.rt[min(2 * m + 1, nrt - 1)], 2 * m + 1 < nrt).n() + 1) / 2;
+    if (m < rp) n = (merged(rt[2 * m], rt[min(2 * m + 1, nrt - 1)], 2 * m + 1 < nrt).n() + 1) / 2;
     int tot;
     const int at = nunits + block_scan(n, sums, &tot);
     nunits += tot;
-    if (m < rp) w.units[m] = at;
+    if (m < rp) {
+      w.units[m] = at;
+      if (rp <= kS) s_units[m] = at;
+    }
+  }
+  const int all = rp * a.L.n_kv;
+  if (nl == 1) {
+    // one chunk, which make_plan's bound holds (were it not to, nothing is written);
+    // where each CTA pair of the scores kernel begins
+    const bool fits = (long long)ntiles * a.L.n_kv <= cap;
+    __syncthreads();
+    for (int c = tid; c < pl.pairs && fits; c += kPrepThreads) {
+      const long long n = (long long)nunits * a.L.n_kv, u0 = n * c / pl.pairs, u1 = n * (c + 1) / pl.pairs;
+      const int rem = (int)(u0 % nunits), m = last_le(units, rp, rem);
+      w.begin[c] = make_int4((int)(u1 - u0), (int)(u0 / nunits), m, 2 * (rem - units[m]));
+    }
+    if (tid == 0) {
+      w.chunk[0] = 0;
+      w.chunk[1] = fits ? all : 0;
+      *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles, npieces, nunits} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0};
+    }
+    return;
   }
   if (tid == 0) {
     // chunks: as many whole pairs of row tiles as fit in cap tiles
-    const int all = rp * a.L.n_kv;
     auto before = [&](int x) -> long long {            // tiles before pair x (kv head major)
       return (long long)(x / rp) * ntiles + (x % rp ? w.rt[x % rp * 2].base : 0);
     };
@@ -596,7 +635,7 @@ __device__ __forceinline__ RowTile load_row_tile(const RowTile* rt, int i) {
 
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScThreads, 1)
-bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __grid_constant__ CUtensorMap tmq,
+bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int one_chunk, const __grid_constant__ CUtensorMap tmq,
                   const __grid_constant__ CUtensorMap tmo, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv) {
   using T = Sc<D>;
@@ -643,7 +682,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
   tc::cluster_sync();                                 // both CTAs' barriers and tensor memory are there
   tc::fence_after_sync();
   const uint32_t tmem = *tslot;
-  pdl_wait();                                         // the plan and delta; the last chunk's tiles are read
+  if (warp >= kScEpi) pdl_wait();                     // the plan and delta; the last chunk's tiles are read
   pdl_launch();
 
   const int G = a.L.G;
@@ -652,20 +691,26 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
     // ================= the walk, and copies: this CTA's row tile and one key tile of a unit =================
     const Head hd = *w.head;
     const int x0 = w.chunk[chunk], x1 = w.chunk[chunk + 1], rp = (hd.nrt + 1) / 2;
-    long long u0 = 0, u1 = 0, c0 = 0;                 // this pair's units of the chunk; tiles before the chunk
-    if (x0 < x1) {
+    int count = 0, kvh = 0, m = 0, j = 0;             // this pair's units; kv head, pair of row tiles, next key tile of its list
+    long long c0 = 0;                                 // tiles before the chunk
+    if (one_chunk) {                                  // (one round of loads: the chain below counts in a short call)
+      const int4 b = w.begin[blockIdx.x / 2];
+      count = x0 < x1 ? b.x : 0;
+      kvh = b.y;
+      m = b.z;
+      j = b.w;
+    } else if (x0 < x1) {
       auto before = [&](int x) { return (long long)(x / rp) * hd.nunits + (x % rp ? __ldg(w.units + x % rp) : 0); };
       const long long b0 = before(x0), n = before(x1) - b0;
-      u0 = b0 + n * (blockIdx.x / 2) / (gridDim.x / 2);
-      u1 = b0 + n * (blockIdx.x / 2 + 1) / (gridDim.x / 2);
+      const long long u0 = b0 + n * (blockIdx.x / 2) / (gridDim.x / 2), u1 = b0 + n * (blockIdx.x / 2 + 1) / (gridDim.x / 2);
+      count = (int)(u1 - u0);
       c0 = (long long)(x0 / rp) * hd.ntiles + (x0 % rp ? __ldg(&w.rt[x0 % rp * 2].base) : 0);
-    }
-    int kvh = 0, m = 0, j = 0;                        // kv head, pair of row tiles, next key tile of its list
-    if (u0 < u1) {
       kvh = (int)(u0 / hd.nunits);
       const int rem = (int)(u0 % hd.nunits);
-      m = find_last_le(w.units, rp, rem);
-      j = 2 * (rem - __ldg(w.units + m));
+      if (count > 0) {
+        m = find_last_le(w.units, rp, rem);
+        j = 2 * (rem - __ldg(w.units + m));
+      }
     }
     if (lane == 0) {
       const uint32_t full0 = tc::in_cta0(full), a_full0 = tc::in_cta0(a_full);
@@ -673,7 +718,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
       bool fresh = true, two = false;
       RowTile r0 = {}, r1 = {};
       Merged u = {};
-      for (long long g = u0; g < u1; ++g, ++n) {
+      for (; n < count; ++n) {
         if (fresh) {
           r0 = load_row_tile(w.rt, 2 * m);
           two = 2 * m + 1 < hd.nrt;
@@ -787,13 +832,22 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
     const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kT * mine;
     float lse2 = 0.f, delta = 0.f;                    // log2(e) lse, delta / 2^15
     int lo = 0, hi = -1, cut = -1;                    // visible positions: lo .. hi, in prefix tiles lo .. cut
-    for (int n = 0;; ++n) {
-      const int e = n % kUnits;
-      wait(unit_full + e, n / kUnits & 1);
-      const Unit un = units[e];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(unit_empty + e);
-      if ((un.flags & kUnitEnd) || wait.dead) break;
+    // Round -1 is a rehearsal on whatever tensor memory holds, with nothing waited
+    // for, told or stored: the straight-line code below (30 KB) then comes from the
+    // instruction cache, while the plan and the first copies are still on their way
+    // (a first unit took 10k cycles instead of 5k).
+    for (int n = -1;; ++n) {
+      const bool real = n >= 0;
+      if (n == 0) pdl_wait();                         // delta; the last chunk's tiles are read
+      Unit un = {};
+      if (real) {
+        const int e = n % kUnits;
+        wait(unit_full + e, n / kUnits & 1);
+        un = units[e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(unit_empty + e);
+        if ((un.flags & kUnitEnd) || wait.dead) break;
+      }
       if (un.flags & kUnitFresh) {
         const bool valid = tq < un.nt;
         const int pos = un.pos0 + tq;
@@ -813,7 +867,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
       const bool whole = __all_sync(0xffffffffu, lp >= lo && lp + kT - 1 <= top);
       const size_t at = (size_t)(busy ? slot : 0) * kTileBytes + r * 16;
       uint32_t ph[kT / 2];
-      wait(acc_full, n & 1);
+      if (real) wait(acc_full, n & 1);
       tc::fence_after_sync();
       __syncwarp();
 #pragma unroll
@@ -826,7 +880,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
         if (q == kT / 16 - 1) {                       // S is read
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::arrive_cta0(acc_free);
+          if (real && lane == 0) tc::arrive_cta0(acc_free);
         }
         if (busy) {
 #pragma unroll
@@ -837,7 +891,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<uint4*>(w.p + at + (2 * q + c) * 2048) =
+            if (real) *reinterpret_cast<uint4*>(w.p + at + (2 * q + c) * 2048) =
                 make_uint4(pack_bf2(p[8 * c], p[8 * c + 1]), pack_bf2(p[8 * c + 2], p[8 * c + 3]),
                            pack_bf2(p[8 * c + 4], p[8 * c + 5]), pack_bf2(p[8 * c + 6], p[8 * c + 7]));
 #pragma unroll
@@ -848,7 +902,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
 #pragma unroll
         for (int i = 0; i < kT / 2; ++i) ph[i] = 0u;
       }
-      wait(acc_full + 1, n & 1);
+      if (real) wait(acc_full + 1, n & 1);
       tc::fence_after_sync();
       __syncwarp();
 #pragma unroll
@@ -861,7 +915,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
         if (q == kT / 16 - 1) {                       // dP is read
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::arrive_cta0(acc_free + 1);
+          if (real && lane == 0) tc::arrive_cta0(acc_free + 1);
         }
         if (busy) {
 #pragma unroll
@@ -872,7 +926,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const __gri
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<uint4*>(w.ds + at + (2 * q + c) * 2048) =
+            if (real) *reinterpret_cast<uint4*>(w.ds + at + (2 * q + c) * 2048) =
                 make_uint4(pack_bf2(d[8 * c], d[8 * c + 1]), pack_bf2(d[8 * c + 2], d[8 * c + 3]),
                            pack_bf2(d[8 * c + 4], d[8 * c + 5]), pack_bf2(d[8 * c + 6], d[8 * c + 7]));
         }
@@ -1392,19 +1446,19 @@ cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t
       !map_bf16(&k2, a.k, D, L.n_kv, a.n_rows, 1, kT, BOX) ||
       !runs_map(&pm, w.p, 2, kT / 8, p.cap + 1, 2, kT / 8) || !runs_map(&dm, w.ds, 2, kT / 8, p.cap + 1, 2, kT / 8))
     return cudaErrorInvalidValue;
-  const long long pairs = (long long)a.n_rows * L.n_q;
-  const int prep_blocks = 1 + (int)std::min<long long>(cdiv(pairs, kPrepThreads / 32), 8LL * num_sms);
+  const int pairs = std::max(1, std::min({num_sms / 2, kMaxPairs, p.cap}));
+  const int prep_blocks = 1 + (int)std::min<long long>(cdiv((long long)a.n_rows * L.n_q, kPrepThreads / 32), 8LL * num_sms);
   if ((e = launch_pdl(bwd_prep_kernel<D>, dim3(prep_blocks), dim3(kPrepThreads), 0, st, a, w,
-                      PlanArgs{p.cap, p.nl, p.splits, p.piece})) !=
+                      PlanArgs{p.cap, p.nl, p.splits, p.piece, pairs})) !=
       cudaSuccess)
     return e;
   const long long items = cdiv(p.nkt, 2) * p.splits * L.n_kv * 2 * H + std::min<long long>((long long)p.nrt * L.n_kv, p.cap) * H;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   for (int c = 0; c < p.nl; ++c) {
-    if ((e = launch_pdl(bwd_scores_kernel<D>, dim3(2 * std::min(num_sms / 2, p.cap)), dim3(kScThreads), (size_t)Sc<D>::BYTES, st,
-                        a, w, c, q1, o1, k1, v1)) != cudaSuccess)
+    if ((e = launch_pdl(bwd_scores_kernel<D>, dim3(2 * pairs), dim3(kScThreads), (size_t)Sc<D>::BYTES, st,
+                        a, w, c, (int)(p.nl == 1), q1, o1, k1, v1)) != cudaSuccess)
       return e;
-    if ((e = launch_pdl(bwd_products_kernel<D>, dim3(2 * (unsigned)std::min<long long>(num_sms / 2, items)), dim3(kPrThreads),
+    if ((e = launch_pdl(bwd_products_kernel<D>, dim3(2 * (unsigned)std::min<long long>(std::max(1, num_sms / 2), items)), dim3(kPrThreads),
                         (size_t)Pr<N>::BYTES, st, a, w, ProdArgs{c, p.cap, p.direct}, q2, o2, k2, pm, dm)) != cudaSuccess)
       return e;
   }
