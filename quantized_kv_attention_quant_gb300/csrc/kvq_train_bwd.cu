@@ -156,7 +156,7 @@ __host__ __device__ constexpr int prod_n(int D) { return D > 256 ? 256 : D; }
 // heads of 512 took 1016 us in chunks of 1024 (64 MB, within L2), 751 of 2048, 612
 // in one: longer sums for each output beat L2 hits.
 constexpr int kChunkTiles = 16384;
-constexpr int kMinPiece = 12;
+constexpr int kMinPiece = 8;
 
 Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows, int num_sms) {
   Plan p = {};
@@ -592,12 +592,13 @@ struct Sc {
   static constexpr int C_OFF = R_OFF + NS * STAGE;
   static constexpr int BYTES = C_OFF + 512 + 1024;    // + room to align the base
 };
-// Eight epilogue warps, a key tile of the unit per four; a thread's 128 P wait for
-// dP as pairs of f16 times 2^15: 11 bits of every P above 2^-29 (8 times finer
-// than the bf16 dS they end in), in half the registers of fp32.  Nothing may
-// spill here: shared memory leaves so little L1 that a reload goes to L2 (with
-// sixteen warps of 96 registers the epilogue took 10k cycles a unit for that).
-constexpr int kScEpi = 8;
+// Sixteen epilogue warps, a key tile of the unit per eight; a thread's 64 P wait
+// for dP as pairs of f16 times 2^15: 11 bits of every P above 2^-29 (8 times finer
+// than the bf16 dS they end in), in half the registers of fp32.  Columns come 16
+// at a time, so that next to nothing spills: shared memory leaves so little L1
+// that reloads go to L2 (with P in fp32 and 32 columns at a time the epilogue took
+// 10k cycles a unit for them, now 3k).
+constexpr int kScEpi = 16;
 constexpr int kScThreads = (kScEpi + 2) * 32;
 constexpr float kPScale = 32768.f;
 
@@ -826,14 +827,14 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
       }
     }
   } else {
-    // ================= P and dS: thread = row, one key tile of the unit =================
-    const int r = 32 * (warp & 3) + lane, mine = warp >> 2, W = a.L.window;
+    // ================= P and dS: thread = row, half hh of one key tile of the unit =================
+    const int r = 32 * (warp & 3) + lane, mine = warp >> 3, hh = warp >> 2 & 1, W = a.L.window;
     const int tq = r / G, h = r % G;
-    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kT * mine;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kT * mine + 64 * hh;
     float lse2 = 0.f, delta = 0.f;                    // log2(e) lse, delta / 2^15
     int lo = 0, hi = -1, cut = -1;                    // visible positions: lo .. hi, in prefix tiles lo .. cut
     // Round -1 is a rehearsal on whatever tensor memory holds, with nothing waited
-    // for, told or stored: the straight-line code below (30 KB) then comes from the
+    // for, told or stored: the straight-line code below (15 KB) then comes from the
     // instruction cache, while the plan and the first copies are still on their way
     // (a first unit took 10k cycles instead of 5k).
     for (int n = -1;; ++n) {
@@ -860,24 +861,24 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
           delta = w.delta[o] * (1.f / kPScale);
         }
       }
-      const int slot = mine ? un.slot[1] : un.slot[0], lp = mine ? un.lp[1] : un.lp[0];
+      const int slot = mine ? un.slot[1] : un.slot[0], lp = (mine ? un.lp[1] : un.lp[0]) + 64 * hh;
       const bool busy = slot >= 0;
       const int top = un.prefix >> mine & 1 ? cut : hi;
-      // (a row that sees one key does not see 128: it always takes the masked form)
-      const bool whole = __all_sync(0xffffffffu, lp >= lo && lp + kT - 1 <= top);
-      const size_t at = (size_t)(busy ? slot : 0) * kTileBytes + r * 16;
-      uint32_t ph[kT / 2];
+      // (a row that sees one key does not see 64: it always takes the masked form)
+      const bool whole = __all_sync(0xffffffffu, lp >= lo && lp + 63 <= top);
+      const size_t at = (size_t)(busy ? slot : 0) * kTileBytes + hh * 16384 + r * 16;
+      uint32_t ph[32];
       if (real) wait(acc_full, n & 1);
       tc::fence_after_sync();
       __syncwarp();
 #pragma unroll
-      for (int q = 0; q < kT / 16; ++q) {
+      for (int q = 0; q < 4; ++q) {
         float p[16];
         if (busy) {
           tc::ld_x16(ts + 16 * q, p);
           tc::wait_ld();
         }
-        if (q == kT / 16 - 1) {                       // S is read
+        if (q == 3) {                       // S is read
           tc::fence_before_sync();
           __syncwarp();
           if (real && lane == 0) tc::arrive_cta0(acc_free);
@@ -900,19 +901,19 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
       }
       if (!whole && lo >= hi) {                       // one key: dS = 0
 #pragma unroll
-        for (int i = 0; i < kT / 2; ++i) ph[i] = 0u;
+        for (int i = 0; i < 32; ++i) ph[i] = 0u;
       }
       if (real) wait(acc_full + 1, n & 1);
       tc::fence_after_sync();
       __syncwarp();
 #pragma unroll
-      for (int q = 0; q < kT / 16; ++q) {
+      for (int q = 0; q < 4; ++q) {
         float d[16];
         if (busy) {
           tc::ld_x16(ts + 256 + 16 * q, d);
           tc::wait_ld();
         }
-        if (q == kT / 16 - 1) {                       // dP is read
+        if (q == 3) {                       // dP is read
           tc::fence_before_sync();
           __syncwarp();
           if (real && lane == 0) tc::arrive_cta0(acc_free + 1);

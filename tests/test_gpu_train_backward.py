@@ -509,3 +509,62 @@ def test_training_step_of_the_stack_runs(m):
         assert c.status_word() == 0 and c.grad_status() == 0
         for t in (c.dq, c.dq_w) + ((c.dk, c.dk_w) if c.donor else ()):
             assert np.isfinite(values(t)).all() and values(t).any()
+
+
+# ---------------------------------------------------------------------------
+# passes whose P and dS tiles do not fit one chunk of the workspace
+# ---------------------------------------------------------------------------
+
+def dense_gradient(q, k, v, do, see):
+    """The definition in 64 bits on the GPU, head by head: dq, dk, dv, out, lse."""
+    G = q.shape[1] // k.shape[1]
+    dq, dk, dv, out = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v), torch.zeros_like(q)
+    lse = torch.zeros(q.shape[:2], dtype=torch.float64, device="cuda")
+    for h in range(q.shape[1]):
+        s = (q[:, h] @ k[:, h // G].T).masked_fill_(~see, -float("inf"))
+        lse[:, h] = torch.logsumexp(s, 1)
+        p = (s - lse[:, h, None]).exp_()
+        dp = do[:, h] @ v[:, h // G].T
+        ds = p * (dp - (p * dp).sum(1, keepdim=True))
+        dq[:, h], out[:, h] = ds @ k[:, h // G], p @ v[:, h // G]
+        dk[:, h // G] += ds.T @ q[:, h]
+        dv[:, h // G] += p.T @ do[:, h]
+    return dq, dk, dv, out, lse
+
+
+@pytest.mark.parametrize("D,n_q,n_kv,window,blocks,f32_sums", [
+    (64, 128, 8, 0, [2100], True),                       # one causal block
+    (64, 128, 8, 700, [900, 700, 600, 500], False),      # branches, a window into the prefix
+    (256, 64, 4, 0, [1500, 40, 1500], True),
+])
+def test_read_backward_in_several_chunks(m, D, n_q, n_kv, window, blocks, f32_sums):
+    """More than 16384 tiles: dk and dv are summed over chunks, accumulated to
+    what was there; against the definition in 64 bits (2-norms)."""
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    T = sum(blocks)
+
+    def rows(heads, scale):
+        x = torch.randn(T, heads, D, generator=gen, device="cuda") * scale
+        return x.bfloat16()
+
+    q, k, v, do = rows(n_q, 0.4), rows(n_kv, 1.0), rows(n_kv, 1.0), rows(n_q, 0.01)
+    see = torch.from_numpy(O.train_mask(np.concatenate([[0], np.cumsum(blocks)]), window)).cuda()
+    want = dense_gradient(*(x.double() for x in (q, k, v, do)), see)
+    out, lse = want[3].float(), want[4].float()
+    lay = m.layer(n_q, n_kv, D, window, 0, 1e4)
+    ws_bytes = m.attn_train_backward_workspace_bytes(lay, len(blocks), T, max(blocks))
+    assert ws_bytes > (1 << 30)                          # a full chunk: 16384 tiles of 64 KB
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device="cuda")
+    kind = torch.float32 if f32_sums else torch.bfloat16
+    dq = torch.empty_like(q)
+    start = torch.randn(2, T, n_kv, D, generator=gen, device="cuda").to(kind) if f32_sums else None
+    dk, dv = (start[0].clone(), start[1].clone()) if f32_sums else (torch.empty_like(k), torch.empty_like(v))
+    m.attn_train_backward(lay, len(blocks), offsets(blocks), T, max(blocks), q, k, v, out, 1, lse, do, dq, dk, dv,
+                          f32_sums, f32_sums, ws, ws_bytes)
+    torch.cuda.synchronize()
+    assert int(ws[:4].cpu().numpy().view(np.uint32)[0]) == 0
+    for name, got, w, s in (("dq", dq, want[0], None), ("dk", dk, want[1], 0), ("dv", dv, want[2], 1)):
+        got = got.double() - (start[s].double() if f32_sums and s is not None else 0.0)
+        # (the fp32 addition to `start`, of size 1, rounds by 2^-24 of it)
+        room = 5e-3 * w.norm() + (2.0 ** -24 * start[s].double().norm() if f32_sums and s is not None else 0.0)
+        assert (got - w).norm() <= room, (name, float((got - w).norm() / w.norm()))
