@@ -144,15 +144,30 @@ def _ptr(x):
     raise TypeError(f"cannot pass {type(x)} as a device pointer")
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """The address of the current torch stream as a function.  torch's raw query
+    where it has one: building a Stream object takes some 3 us of every call."""
+    try:
+        import torch
+    except ImportError:
+        return lambda: None
+    if not torch.cuda.is_available():
+        return None                       # (asked again: the caller may be early)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(torch.cuda.current_device())
+
+
 def _stream(stream):
+    global _current_stream
     if stream is None:
-        try:
-            import torch
-            if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:
-            pass
-        return None
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return None if _current_stream is None else _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
