@@ -163,8 +163,11 @@ __device__ __forceinline__ uint32_t in_cta0(const void* p) {
                : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))));
   return r;
 }
+// An arrival that tells CTA 0's MMA thread that this warp's tcgen05 loads are
+// complete (wait::ld returned before it is issued).  Relaxed: no memory is passed
+// on, and a release would wait for the warp's global stores.
 __device__ __forceinline__ void arrive_cta0(uint64_t* mbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(in_cta0(mbar)) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(in_cta0(mbar)) : "memory");
 }
 __device__ __forceinline__ void tmem_alloc2(uint32_t* smem_dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
