@@ -458,7 +458,7 @@ bwd_prep_kernel(const TrainBwdArgs a, const Ws w, const PlanArgs pl) {
   const int lane = threadIdx.x & 31;
   const long long n = (long long)a.n_rows * a.L.n_q, step = (long long)(gridDim.x - 1) * (kPrepThreads / 32);
   const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
-  for (long long it = (long long)(blockIdx.x - 1) * (kPrepThreads / 32) + (threadIdx.x >> 5); it < n; it += step) {
+  auto partial = [&](long long it) {                  // this lane's part of dO . O
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < E / VEC; ++c) {
@@ -499,9 +499,21 @@ bwd_prep_kernel(const TrainBwdArgs a, const Ws w, const PlanArgs pl) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) s = fmaf(g[i], x[i], s);
     }
+    return s;
+  };
+  // two of them at a time, for twice the loads in flight
+  for (long long it = (long long)(blockIdx.x - 1) * (kPrepThreads / 32) + (threadIdx.x >> 5); it < n; it += 2 * step) {
+    const bool both = it + step < n;
+    float s0 = partial(it), s1 = both ? partial(it + step) : 0.f;
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    if (lane == 0) w.delta[it] = s;
+    for (int m = 16; m >= 1; m >>= 1) {
+      s0 += __shfl_xor_sync(0xffffffffu, s0, m);
+      s1 += __shfl_xor_sync(0xffffffffu, s1, m);
+    }
+    if (lane == 0) {
+      w.delta[it] = s0;
+      if (both) w.delta[it + step] = s1;
+    }
   }
 }
 
