@@ -1388,7 +1388,7 @@ __global__ void __launch_bounds__(256) bwd_finish_kernel(const TrainBwdArgs a, c
     for (int q = threadIdx.x; q < quads; q += 256) {
       const size_t e = ((size_t)(k.row0 + r0) * a.L.n_kv * (D / 4) + q) * 4;
       float4 s = *reinterpret_cast<const float4*>(w.acc + kind * plane + e);
-#pragma unroll 4
+#pragma unroll 7
       for (int i = 1; i < pieces; ++i) {
         const float4 y = *reinterpret_cast<const float4*>(w.acc + ((size_t)i * 2 + kind) * plane + e);
         s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
@@ -1476,7 +1476,7 @@ cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t
       return e;
   }
   if (p.direct) return cudaSuccess;
-  return launch_pdl(bwd_finish_kernel, dim3(std::min(p.nkt, 4 * num_sms), 16, 2), dim3(256), 0, st, a, w);
+  return launch_pdl(bwd_finish_kernel, dim3(std::min(p.nkt, 4 * num_sms), 32, 2), dim3(256), 0, st, a, w);
 }
 
 }  // namespace
