@@ -981,6 +981,7 @@ kvq_status attn_train_backward(const kvq_layer* layer, int32_t n_blocks, const i
   REQUIRE_PTR(dv_hat, "dv_hat", dkv_is_f32 ? 4 : 2);
   REQUIRE_PTR(workspace, "workspace", 256);
   const size_t need = kvq::train_bwd_ws_bytes(a.L, n_blocks, n_rows, max_block_rows);
+  if (need == 0) return fail(KVQ_EUNSUPPORTED, "too many tiles of 128 rows x 128 keys (2^31), or n_kv_heads > 65535");
   if (workspace_bytes < need) return fail(KVQ_EWORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
   a.n_rows = n_rows;
   a.n_blocks = n_blocks;

@@ -58,8 +58,9 @@ struct alignas(16) RowTile {
   int a0, nA, b0, nB;
   int off0, block, kend, pad;
 };
-// A key tile: keys row0 .. row0 + n - 1 (packed), tile idx of its block.
-struct alignas(16) KeyTile { int row0, n, block, idx; };
+// A key tile: keys row0 .. row0 + n - 1 (packed), tile idx of its block; the row
+// tiles that may see it are lo .. hi - 1 (a branch's: its own, from there on).
+struct alignas(16) KeyTile { int row0, n, block, idx, lo, hi, pad[2]; };
 
 // The key tiles that either of two row tiles sees: prefix tiles a0 .., own-block
 // tiles b0 .. of both (one block) or of the first and then c0 .. of the second.
@@ -144,6 +145,7 @@ struct Plan {
   int nl;                       // chunk launches
   int splits, piece;            // of a key pair's row tiles: most pieces; row tiles of one
   int direct;                   // one chunk, one split: dk and dv need no sums beside the outputs
+  bool fits;                    // tile counts fit 32 bits (else nothing else is set)
   size_t chunk_o, begin_o, units_o, counts_o, list_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
 };
 
@@ -173,6 +175,8 @@ Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows,
   const long long by_block = p.nrt * std::min(tmax, pfx + max_block_rows / (2 * kT) + 3);
   const long long by_order = n_rows / TQ * std::min(tmax, n128 / 2 + 4) + n_blocks * tmax;
   const long long total = std::min(by_block, by_order) * L.n_kv;
+  if (total > 0x7fffffffLL || L.n_kv > 0xffff) return Plan{};
+  p.fits = true;
   const long long cap = std::min<long long>(total, std::max<long long>(kChunkTiles, 4 * tmax));
   p.cap = (int)cap;
   // a chunk ends before a pair of row tiles that does not fit: more than cap - 2 tmax tiles each
@@ -319,7 +323,8 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
   __syncthreads();
   for (int i = tid; i < nkt; i += kPrepThreads) {
     const int b = last_le(ks, nb, i), idx = i - ks[b], o0 = off[b];
-    w.kt[i] = KeyTile{o0 + idx * kT, min(kT, off[b + 1] - o0 - idx * kT), b, idx};
+    const int lo = rs[b] + idx * kT / TQ, hi = b == 0 || b + 1 == nb ? nrt : rs[b + 1];
+    w.kt[i] = KeyTile{o0 + idx * kT, min(kT, off[b + 1] - o0 - idx * kT), b, idx, lo, hi, {0, 0}};
     counts[i] = 0;
   }
   __syncthreads();
@@ -558,6 +563,14 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Two f16, finite: where scores are so large (10^6) that their own rounding takes
+// P = exp(S - lse) past 2, it stays below 2 instead of becoming an infinity.
+__device__ __forceinline__ uint32_t pack_h2_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // A wait by a whole warp.  One that gives up (kvq_common.cuh) flags the status
@@ -908,7 +921,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
                 make_uint4(pack_bf2(p[8 * c], p[8 * c + 1]), pack_bf2(p[8 * c + 2], p[8 * c + 3]),
                            pack_bf2(p[8 * c + 4], p[8 * c + 5]), pack_bf2(p[8 * c + 6], p[8 * c + 7]));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ph[8 * q + i] = pack_h2(p[2 * i] * kPScale, p[2 * i + 1] * kPScale);
+          for (int i = 0; i < 8; ++i) ph[8 * q + i] = pack_h2_sat(p[2 * i] * kPScale, p[2 * i + 1] * kPScale);
         }
       }
       if (!whole && lo >= hi) {                       // one key: dS = 0
@@ -971,6 +984,8 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
 // A step is a whole tile: 128 rows (or keys) of K in one stage, three copies (a
 // copy takes the issuing thread some 150 cycles; with stages of 64 the copies
 // took longer than their MMAs).
+constexpr int kBatches = 3;                                   // of 32 steps listed ahead
+constexpr int kItems = 4;                                     // items told to the epilogue ahead
 template <int N>
 struct Pr {
   static constexpr int A_BYTES = kTileBytes;                  // 128 x 128 of P or dS
@@ -980,15 +995,15 @@ struct Pr {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int NS = N == 256 ? 3 : 4;
   static constexpr int E_OFF = NS * STAGE;                    // 4 KB per output warp
-  static constexpr int L_OFF = E_OFF + 8 * 4096;              // 32 steps of the copies' list
-  static constexpr int C_OFF = L_OFF + 512;
+  static constexpr int L_OFF = E_OFF + 8 * 4096;              // kBatches x 32 steps for the copies
+  static constexpr int C_OFF = L_OFF + kBatches * 512;
   static constexpr int BYTES = C_OFF + 512 + 1024;
 };
 constexpr int kPrEpi = 8;
-constexpr int kPrThreads = (kPrEpi + 2) * 32;
+constexpr int kPrThreads = (kPrEpi + 3) * 32;
 
 // What the copies tell the MMA warp about a stage.
-enum : int { kFirst = 1, kLast = 2, kKeys = 4, kEnd = 8 };
+enum : int { kFirst = 1, kLast = 2, kKeys = 4, kEnd = 8, kQ = 16 };   // kKeys: dk or dv, with kQ dk
 
 struct Item {
   bool dkv;
@@ -1019,11 +1034,15 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   uint64_t* empty = full + T::NS;
   uint64_t* done = empty + T::NS;                     // [2] an item's products are in tensor memory
   uint64_t* acc_free = done + 2;                      // [2] CTA 0's: and read from it, in both CTAs
-  uint64_t* item_full = acc_free + 2;                 // [2]
-  uint64_t* item_empty = item_full + 2;               // [2]
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(item_empty + 2);
+  uint64_t* item_full = acc_free + 2;                 // [kItems]
+  uint64_t* item_empty = item_full + kItems;          // [kItems]
+  uint64_t* list_full = item_empty + kItems;          // [kBatches]
+  uint64_t* list_empty = list_full + kBatches;        // [kBatches]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(list_empty + kBatches);
   volatile int* info = reinterpret_cast<volatile int*>(tslot + 1);   // [NS] stage flags (CTA 0)
-  volatile int* items = info + T::NS;                 // [2][2]: item (-1: no more), its steps
+  volatile int* items = info + T::NS;                 // [kItems][2]: item (-1: no more), its steps
+  volatile int* list_n = items + 2 * kItems;          // [kBatches] steps of a batch (0: no more)
+  int4* list = reinterpret_cast<int4*>(sm + T::L_OFF);
   if (tid == 0) {
     for (int s = 0; s < T::NS; ++s) {
       mbar_init(full + s, 1);
@@ -1032,8 +1051,14 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
     for (int s = 0; s < 2; ++s) {
       mbar_init(done + s, 1);
       mbar_init(acc_free + s, 2 * kPrEpi);
+    }
+    for (int s = 0; s < kItems; ++s) {
       mbar_init(item_full + s, 1);
       mbar_init(item_empty + s, kPrEpi);
+    }
+    for (int s = 0; s < kBatches; ++s) {
+      mbar_init(list_full + s, 1);
+      mbar_init(list_empty + s, 1);
     }
     fence_mbar_init();
   }
@@ -1083,11 +1108,10 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   };
   Waiter wait{&w.head->status};
 
-  if (warp == kPrEpi) {
-    // ================= copies: this CTA's tile of A and half of B =================
-    int st = 0, ph = 0, e = 0, eph = 0;
-    const uint32_t bar0 = tc::in_cta0(full);
-    int4* steps = reinterpret_cast<int4*>(sm + T::L_OFF);
+  if (warp == kPrEpi + 2) {
+    // ================= the items' steps, listed ahead for the copies =================
+    // (a list costs several dependent loads, as long as a few steps' products)
+    int e = 0, eph = 0, b = 0, bph = 0;
     auto publish = [&](int id, int n) {
       wait(item_empty + e, eph ^ 1);
       if (lane == 0) {
@@ -1096,66 +1120,81 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         mbar_arrive(item_full + e);
       }
       __syncwarp();
-      if (++e == 2) {
+      if (++e == kItems) {
         e = 0;
         eph ^= 1;
+      }
+    };
+    auto hand_over = [&](int n) {
+      __syncwarp();
+      if (lane == 0) {
+        list_n[b] = n;
+        mbar_arrive(list_full + b);
+      }
+      __syncwarp();
+      if (++b == kBatches) {
+        b = 0;
+        bph ^= 1;
       }
     };
     for (int id = blockIdx.x / 2; id < n_items; id += gridDim.x / 2) {
       const Item it = decode(id);
       const long long slot0 = (long long)it.kvh * hd.ntiles - c0;    // slot of the kv head's first tile
-      const int dim = it.half * N + rank * T::DIMS;
-      int left = 0;                                   // stages still to come
-      bool first = true;
-      // one tile of each of the pair (slot -1: not there) and the 128 rows of B they
-      // meet: one thread
-      auto tile = [&](int s0, int s1, int row) {
-        const int mine = rank == 0 ? s0 : s1, slot = mine >= 0 ? mine : pa.zero;
-        wait.one(empty + st, ph ^ 1);
-        const uint32_t dst = sb + st * T::STAGE, bar = bar0 + 8 * st;
-        if (rank == 0) {
-          info[st] = (first ? kFirst : 0) | (--left == 0 ? kLast : 0) | (it.dkv ? kKeys : 0);
-          mbar_arrive_expect_tx(full + st, 2 * T::STAGE);
-        }
-        first = false;
-        tc::tma2_load_4d(dst, it.dkv && it.kind == 1 ? &tmp : &tmd, 0, 0, 0, slot, bar);
-#pragma unroll
-        for (int b = 0; b < T::DIMS / T::BOX; ++b) {
-          if (it.dkv) tc::tma2_load_3d(dst + T::A_BYTES + b * 16384, it.kind == 0 ? &tmq : &tmo, dim + T::BOX * b, it.kvh * G, row, bar);
-          else tc::tma2_load_3d(dst + T::A_BYTES + b * 16384, &tmk, dim + T::BOX * b, it.kvh, row, bar);
-        }
-        if (++st == T::NS) {
-          st = 0;
-          ph ^= 1;
-        }
+      const int place = it.kvh << 10 | (it.half * N + rank * T::DIMS), kind = it.dkv ? kKeys | (it.kind == 0 ? kQ : 0) : 0;
+      int at = 0, n = 0;                              // steps listed, steps of the item
+      // up to 32 steps, one a lane where `see`: s0 and s1 (-1: not there) are the tiles
+      // of the pair, `row` the first of the 128 rows of B that they meet
+      auto batch = [&](bool see, int s0, int s1, int row) {
+        const uint32_t m = __ballot_sync(0xffffffffu, see);
+        if (m == 0) return;
+        wait(list_empty + b, bph ^ 1);
+        const int x = __popc(m & ((1u << lane) - 1)), mine = rank == 0 ? s0 : s1;
+        if (see)
+          list[32 * b + x] = make_int4(mine >= 0 ? mine : pa.zero, row, place,
+                                       kind | (at + x == 0 ? kFirst : 0) | (at + x == n - 1 ? kLast : 0));
+        at += __popc(m);
+        hand_over(__popc(m));
       };
       if (it.dkv) {
         // the chunk's row tiles that see either key tile; this piece's share of them by count
         const KeyTile ka = w.kt[it.t0], kb = w.kt[it.t0 + it.n - 1];
         const int cuts = w.counts[hd.nkt + it.t0 / 2];
-        const int xs = 2 * max(0, x0 - it.kvh * rp), xe = min(hd.nrt, 2 * (x1 - it.kvh * rp));
+        const int xs = max(2 * (x0 - it.kvh * rp), min(ka.lo, kb.lo));
+        const int xe = min(2 * (x1 - it.kvh * rp), max(ka.hi, kb.hi));
         auto tile_of = [&](const KeyTile& t, const RowTile& r) -> int {      // its place in the row tile's list
           if (t.block == 0) return t.idx >= r.a0 && t.idx < r.a0 + r.nA ? t.idx - r.a0 : -1;
           return t.block == r.block && t.idx >= r.b0 && t.idx < r.b0 + r.nB ? r.nA + t.idx - r.b0 : -1;
         };
-        int n = 0;
+        int all = 0, count = 0;                       // lane g: of the g-th 32 row tiles
+        RowTile r = {}, head = {};                    // (the first 32 are kept: in a short call they are all)
 #pragma unroll 4
         for (int i = xs; i < xe; i += 32) {
           bool see = false;
           if (i + lane < xe) {
-            const RowTile r = load_row_tile(w.rt, i + lane);
+            r = load_row_tile(w.rt, i + lane);
             see = tile_of(ka, r) >= 0 || tile_of(kb, r) >= 0;
+            if (i == xs) head = r;
           }
-          n += __popc(__ballot_sync(0xffffffffu, see));
+          const int c = __popc(__ballot_sync(0xffffffffu, see));
+          if ((i - xs) / 32 == lane) count = c;
+          all += c;
         }
-        const int v0 = (int)((long long)n * it.split / cuts), v1 = (int)((long long)n * (it.split + 1) / cuts);
-        left = v1 - v0;
-        publish(id, left);
+        const int v0 = (int)((long long)all * it.split / cuts), v1 = (int)((long long)all * (it.split + 1) / cuts);
+        n = v1 - v0;
+        publish(id, n);
         int seen = 0;
-        for (int i = xs; i < xe && seen < v1; i += 32) {
+        for (int i = xs, g = 0; i < xe && seen < v1; i += 32, ++g) {
+          if (g < 32) {                               // all of another piece
+            const int c = __shfl_sync(0xffffffffu, count, g);
+            if (seen + c <= v0) {
+              seen += c;
+              continue;
+            }
+          }
           int j0 = -1, j1 = -1, row = 0;
           if (i + lane < xe) {
-            const RowTile r = load_row_tile(w.rt, i + lane);
+            if (g == 0) r = head;
+            else r = load_row_tile(w.rt, i + lane);
             j0 = tile_of(ka, r);
             j1 = it.n == 2 ? tile_of(kb, r) : -1;
             const int base = (int)(slot0 + r.base);
@@ -1164,34 +1203,69 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
             row = r.row0;
           }
           const uint32_t m = __ballot_sync(0xffffffffu, j0 >= 0 || j1 >= 0);
-          const int mine = seen + __popc(m & ((1u << lane) - 1)), from = max(v0, seen), upto = min(v1, seen + __popc(m));
-          if ((m >> lane & 1) && mine >= from && mine < upto) steps[mine - from] = make_int4(j0, j1, row, 0);
-          __syncwarp();
-          if (lane == 0)
-            for (int x = 0; x < upto - from; ++x) tile(steps[x].x, steps[x].y, steps[x].z);
-          __syncwarp();
+          const int mine = seen + __popc(m & ((1u << lane) - 1));
+          batch((m >> lane & 1) && mine >= v0 && mine < v1, j0, j1, row);
           seen += __popc(m);
         }
       } else {
+        // the key tiles that either row tile sees
         const bool two = it.n == 2;
         const RowTile r0 = load_row_tile(w.rt, it.t0), r1 = load_row_tile(w.rt, it.t0 + it.n - 1);
         const Merged u = merged(r0, r1, two);
         const int base0 = (int)(slot0 + r0.base), base1 = (int)(slot0 + r1.base);
-        auto walk = [&](auto f) {                     // the key tiles either row tile sees
-          for (int j = 0; j < u.n(); ++j) {
-            const MergedTile t = merged_at(u, r0, r1, two, j);
-            if (t.j0 >= 0 || t.j1 >= 0) f(t.j0 < 0 ? -1 : base0 + t.j0, t.j1 < 0 ? -1 : base1 + t.j1, t.pk);
-          }
+        auto sees = [&](int j, MergedTile& t) {
+          if (j >= u.n()) return false;
+          t = merged_at(u, r0, r1, two, j);
+          return t.j0 >= 0 || t.j1 >= 0;
         };
-        walk([&](int, int, int) { ++left; });
-        publish(id, left);
-        if (lane == 0) walk(tile);
-        __syncwarp();
+        MergedTile t = {};
+        for (int j = 0; j < u.n(); j += 32) n += __popc(__ballot_sync(0xffffffffu, sees(j + lane, t)));
+        publish(id, n);
+        for (int j = 0; j < u.n(); j += 32) {
+          const bool see = sees(j + lane, t);
+          batch(see, t.j0 < 0 ? -1 : base0 + t.j0, t.j1 < 0 ? -1 : base1 + t.j1, t.pk);
+        }
       }
     }
     publish(-1, 0);
-    // every stage consumed, in both CTAs, before either may leave
+    wait(list_empty + b, bph ^ 1);
+    hand_over(0);
+  } else if (warp == kPrEpi) {
+    // ================= copies: this CTA's tile of A and half of B =================
     if (lane == 0) {
+      int st = 0, ph = 0;
+      const uint32_t bar0 = tc::in_cta0(full);
+      for (int b = 0, bph = 0;;) {
+        wait.one(list_full + b, bph);
+        const int n = wait.dead ? 0 : list_n[b];
+        if (n == 0) break;
+        for (int x = 0; x < n; ++x) {
+          const int4 s = list[32 * b + x];            // tile, first row of B, kv head and dims, flags
+          wait.one(empty + st, ph ^ 1);
+          const uint32_t dst = sb + st * T::STAGE, bar = bar0 + 8 * st;
+          if (rank == 0) {
+            info[st] = s.w;
+            mbar_arrive_expect_tx(full + st, 2 * T::STAGE);
+          }
+          const bool keys = s.w & kKeys, of_q = s.w & kQ;
+          const int kvh = s.z >> 10, dim = s.z & 1023;
+          tc::tma2_load_4d(dst, keys && !of_q ? &tmp : &tmd, 0, 0, 0, s.x, bar);
+#pragma unroll
+          for (int i = 0; i < T::DIMS / T::BOX; ++i)
+            tc::tma2_load_3d(dst + T::A_BYTES + i * 16384, !keys ? &tmk : of_q ? &tmq : &tmo, dim + T::BOX * i,
+                             keys ? kvh * G : kvh, s.y, bar);
+          if (++st == T::NS) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        mbar_arrive(list_empty + b);
+        if (++b == kBatches) {
+          b = 0;
+          bph ^= 1;
+        }
+      }
+      // every stage consumed, in both CTAs, before either may leave
       const int st1 = st;
       for (int i = 0; i < T::NS; ++i) {
         wait.one(empty + st, ph ^ 1);
@@ -1354,7 +1428,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         if (has) tc::arrive_cta0(acc_free + buf);
         mbar_arrive(item_empty + e);
       }
-      if (++e == 2) {
+      if (++e == kItems) {
         e = 0;
         eph ^= 1;
       }
@@ -1448,6 +1522,7 @@ cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t
   }
   const LayerArgs& L = a.L;
   const Plan p = make_plan(L, a.n_blocks, a.n_rows, a.max_block_rows, num_sms);
+  if (!p.fits) return cudaErrorInvalidValue;
   const Ws w = carve(wsp, p);
   const int TQ = kT / L.G;
   // boxes of 128 (token, head) pairs or keys
@@ -1482,7 +1557,7 @@ cudaError_t launch_t(const TrainBwdArgs& a, void* wsp, int num_sms, cudaStream_t
 }  // namespace
 
 size_t train_bwd_ws_bytes(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows) {
-  return make_plan(L, n_blocks, n_rows, max_block_rows, 1).bytes;      // (the SM count sets the splits alone)
+  return make_plan(L, n_blocks, n_rows, max_block_rows, 1).bytes;      // (the SM count sets the splits alone; 0: too large)
 }
 
 cudaError_t launch_train_bwd(const TrainBwdArgs& a, void* ws, int num_sms, cudaStream_t st) {

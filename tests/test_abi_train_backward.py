@@ -66,10 +66,23 @@ def test_read_backward_workspace_grows(m, D, n_q, n_kv):
     lay = layer(m, head_dim=D, n_q_heads=n_q, n_kv_heads=n_kv, window=0, rope_dims=0)
     f = m.attn_train_backward_workspace_bytes
     last = 0
-    for n in list(range(1, 400)) + [1000, 4097, 20000, 100001, (1 << 24) - 1]:
+    for n in list(range(1, 400)) + [1000, 4097, 20000, 100001, 500001]:
         b = f(lay, 1, n, n)
         assert b >= last
         last = b
+
+
+def test_read_backward_too_many_tiles(m):
+    """Tiles are counted in 32 bits: a pass that may have more is refused, one
+    of as many rows in short blocks is not."""
+    lay = layer(m, head_dim=512, n_q_heads=16, n_kv_heads=1, window=0, rope_dims=0)
+    f = m.attn_train_backward_workspace_bytes
+    rows = (1 << 24) - 1
+    assert f(lay, 1, rows, rows) == 0
+    assert read(m, lay, n_rows=rows, max_rows=rows) == 2 and b"tiles" in m.lib.kvq_last_error()
+    assert f(lay, 65535, rows, 300) > 0
+    windowed = layer(m, head_dim=512, n_q_heads=16, n_kv_heads=1, window=1024, rope_dims=0)
+    assert f(windowed, 1, rows, rows) > 0
 
 
 def test_lse_refusals(m):

@@ -202,6 +202,59 @@ def test_bf16_gradients_are_the_rounded_sums(m):
     assert torch.equal(a.dq.t, b.dq.t)
 
 
+@pytest.mark.parametrize("D,window", [(64, 0), (256, 40)])
+def test_hundreds_of_branches(m, D, window):
+    """More blocks, tiles and pairs of tiles than the plan keeps on chip; a few
+    blocks are empty."""
+    c = ReadCase(m, spec(1, 1, D, window), [130] + [1] * 300 + [0] * 7 + [2] * 220 + [257])
+    c.run()
+    c.verify()
+
+
+@pytest.mark.parametrize("D,n_q,n_kv,f32_sums", [(64, 4, 2, False), (128, 2, 2, True), (512, 16, 1, True), (256, 8, 2, False)])
+def test_outputs_and_out_aligned_to_their_elements(m, D, n_q, n_kv, f32_sums):
+    """dq, dk, dv and out one element past a 16-byte boundary: the same bits,
+    with and without pieces to join (a sum of one piece, several)."""
+    for blocks in ([70, 30], [1100, 300] if D <= 128 else [300, 60]):
+        c = ReadCase(m, spec(n_q, n_kv, D, 0), blocks, dkv_f32=f32_sums)
+        c.run()
+        want = [o.t.clone() for o in (c.dq, c.dk, c.dv)]
+        off = []
+        for o in (c.dq, c.dk, c.dv):
+            n = o.t.numel()
+            whole = torch.full((n + 9,), 77, dtype=o.t.dtype, device="cuda")
+            off.append((whole, whole[1:1 + n].view(o.t.shape)))
+        flat = torch.empty(c.dev["out"].numel() + 1, dtype=c.dev["out"].dtype, device="cuda")
+        flat[1:].copy_(c.dev["out"].reshape(-1))
+        c.dev["out"] = flat[1:].view(c.dev["out"].shape)
+        c.run(dq=off[0][1], dk=off[1][1], dv=off[2][1])
+        torch.cuda.synchronize()
+        assert c.status() == 0
+        for (whole, t), w in zip(off, want):
+            assert torch.equal(t, w)
+            assert int(whole[0]) == 77 and bool((whole[1 + t.numel():] == 77).all())
+        if f32_sums:                                     # x + x is exact
+            c.run(accumulate=True, dq=off[0][1], dk=off[1][1], dv=off[2][1])
+            torch.cuda.synchronize()
+            assert torch.equal(off[1][1], 2 * want[1]) and torch.equal(off[2][1], 2 * want[2])
+
+
+def test_scores_of_millions_stay_finite(m):
+    """Norm weights of 256 allow scores of 10^7, which fp32 holds to steps of 1:
+    P = exp(S - lse) is then off by a factor, the gradients stay finite."""
+    c = ReadCase(m, spec(4, 2, 512, 0), [90, 40], q_scale=256.0)
+    c.dev["k"] = bits(c.k * 256.0)
+    s = np.einsum("ihd,jhd->hij", c.q, np.repeat(c.k, 2, axis=1) * 256.0)
+    see = O.train_mask(np.array([0, 90, 130]), 0)
+    top = np.where(see[None], s, -np.inf).max(2).T       # the log-sum-exp of scores this far apart
+    c.dev["lse"] = f32(top)
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    for o in (c.dq, c.dk, c.dv):
+        assert np.isfinite(o.check()).all()
+
+
 def test_same_call_same_bits_and_max_block_rows(m):
     """Twice the same bits, on another stream, and with a looser bound of the
     block rows (another workspace and grid)."""
