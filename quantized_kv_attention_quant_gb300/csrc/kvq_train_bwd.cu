@@ -114,12 +114,13 @@ __device__ __forceinline__ MergedTile merged_at(const Merged& u, const RowTile& 
   return t;
 }
 
-struct Head {
+struct alignas(16) Head {
   uint32_t status;
   int ok, nrt, nkt;             // layout valid; row and key tiles of one kv head
   int ntiles;                   // (row tile, key tile) pairs of one kv head
   int npieces;                  // entries of the piece list
   int nunits;                   // units of the scores kernel, of one kv head
+  int pad;
 };
 
 struct Ws {
@@ -301,7 +302,7 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
   bad = __syncthreads_or(bad);
   if (bad) {                                // no tiles: nothing is written
     for (int c = tid; c <= nl; c += kPrepThreads) w.chunk[c] = 0;
-    if (tid == 0) *w.head = Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0};
+    if (tid == 0) *w.head = Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0, 0};
     return;
   }
   int* rs = nb <= kS ? s_rs : w.starts;
@@ -413,7 +414,7 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     if (tid == 0) {
       w.chunk[0] = 0;
       w.chunk[1] = fits ? all : 0;
-      *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles, npieces, nunits} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0};
+      *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles, npieces, nunits, 0} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0, 0};
     }
     return;
   }
@@ -440,7 +441,7 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     while (c < nl) w.chunk[++c] = x;
     if (!fits)
       for (int i = 0; i <= nl; ++i) w.chunk[i] = 0;
-    *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles, npieces, nunits} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0};
+    *w.head = fits ? Head{0u, 1, nrt, nkt, ntiles, npieces, nunits, 0} : Head{1u << KVQ_DEV_BADSEQ, 0, 0, 0, 0, 0, 0, 0};
   }
 }
 
@@ -649,13 +650,15 @@ __device__ __forceinline__ int find_last_le(const int* a, int n, int x) {
   }
   return lo;
 }
-__device__ __forceinline__ RowTile load_row_tile(const RowTile* rt, int i) {
-  RowTile t;
-  const int4* s = reinterpret_cast<const int4*>(rt + i);
+// The plan's records, from L2 (they may be read before the grid below has waited).
+template <typename R>
+__device__ __forceinline__ R load_plan(const R* src) {
+  static_assert(sizeof(R) % 16 == 0 && alignof(R) == 16, "whole 16-byte words");
+  R t;
+  const int4* s = reinterpret_cast<const int4*>(src);
   int4* d = reinterpret_cast<int4*>(&t);
-  d[0] = __ldg(s);
-  d[1] = __ldg(s + 1);
-  d[2] = __ldg(s + 2);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(R) / 16); ++i) d[i] = __ldcg(s + i);
   return t;
 }
 
@@ -708,8 +711,12 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
   tc::cluster_sync();                                 // both CTAs' barriers and tensor memory are there
   tc::fence_after_sync();
   const uint32_t tmem = *tslot;
-  if (warp >= kScEpi) pdl_wait();                     // the plan and delta; the last chunk's tiles are read
-  pdl_launch();
+  // the plan and delta; the last chunk's tiles are read.  The next kernel is let
+  // go only then, so that it may read the plan before it waits.
+  if (warp >= kScEpi) {
+    pdl_wait();
+    pdl_launch();
+  }
 
   const int G = a.L.G;
   Waiter wait{&w.head->status};
@@ -746,9 +753,9 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
       Merged u = {};
       for (; n < count; ++n) {
         if (fresh) {
-          r0 = load_row_tile(w.rt, 2 * m);
+          r0 = load_plan(w.rt + 2 * m);
           two = 2 * m + 1 < hd.nrt;
-          r1 = load_row_tile(w.rt, two ? 2 * m + 1 : 2 * m);
+          r1 = load_plan(w.rt + (two ? 2 * m + 1 : 2 * m));
           u = merged(r0, r1, two);
         }
         const bool more = j + 1 < u.n();
@@ -864,7 +871,10 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
     // (a first unit took 10k cycles instead of 5k).
     for (int n = -1;; ++n) {
       const bool real = n >= 0;
-      if (n == 0) pdl_wait();                         // delta; the last chunk's tiles are read
+      if (n == 0) {                                   // delta; the last chunk's tiles are read
+        pdl_wait();
+        pdl_launch();
+      }
       Unit un = {};
       if (real) {
         const int e = n % kUnits;
@@ -1071,17 +1081,20 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   tc::cluster_sync();                                 // both CTAs' barriers and tensor memory are there
   tc::fence_after_sync();
   const uint32_t tmem = *tslot;
-  pdl_wait();
+  // (the warp that lists the items needs the plan alone, which the scores kernel
+  // has waited for before this one could start: the lists of a CTA's first items
+  // are there when P and dS are, 4 to 7 us sooner)
+  if (warp != kPrEpi + 2) pdl_wait();
   pdl_launch();
 
-  const Head hd = *w.head;
+  const Head hd = load_plan(w.head);
   const int G = a.L.G, nkv = a.L.n_kv;
-  const int x0 = w.chunk[pa.chunk], x1 = w.chunk[pa.chunk + 1];
+  const int x0 = __ldcg(w.chunk + pa.chunk), x1 = __ldcg(w.chunk + pa.chunk + 1);
   // an empty chunk (or layout) has no items; dk and dv come first (the longest sums)
   const int rp = (hd.nrt + 1) / 2;
   const int n_dkv = x0 < x1 ? hd.npieces * nkv * 2 * H : 0;
   const int n_items = n_dkv + (x1 - x0) * H;
-  const long long c0 = x0 < x1 ? (long long)(x0 / rp) * hd.ntiles + w.rt[x0 % rp * 2].base : 0;
+  const long long c0 = x0 < x1 ? (long long)(x0 / rp) * hd.ntiles + __ldcg(&w.rt[x0 % rp * 2].base) : 0;
   auto decode = [&](int id) {
     Item t;
     t.dkv = id < n_dkv;
@@ -1094,7 +1107,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
       id /= 2;
       t.kvh = id % nkv;
       id /= nkv;
-      id = __ldg(w.list + id);
+      id = __ldcg(w.list + id);
       t.split = id % kMaxSplits;
       t.t0 = id / kMaxSplits * 2;
       t.n = min(2, hd.nkt - t.t0);
@@ -1137,7 +1150,10 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         bph ^= 1;
       }
     };
-    for (int id = blockIdx.x / 2; id < n_items; id += gridDim.x / 2) {
+    // (there and back: the lists grow shorter, so every pair gets long and short ones)
+    for (int id0 = 0, back = 0; id0 < n_items; id0 += gridDim.x / 2, back ^= 1) {
+      const int id = id0 + (int)(back ? gridDim.x / 2 - 1 - blockIdx.x / 2 : blockIdx.x / 2);
+      if (id >= n_items) continue;
       const Item it = decode(id);
       const long long slot0 = (long long)it.kvh * hd.ntiles - c0;    // slot of the kv head's first tile
       const int place = it.kvh << 10 | (it.half * N + rank * T::DIMS), kind = it.dkv ? kKeys | (it.kind == 0 ? kQ : 0) : 0;
@@ -1157,8 +1173,8 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
       };
       if (it.dkv) {
         // the chunk's row tiles that see either key tile; this piece's share of them by count
-        const KeyTile ka = w.kt[it.t0], kb = w.kt[it.t0 + it.n - 1];
-        const int cuts = w.counts[hd.nkt + it.t0 / 2];
+        const KeyTile ka = load_plan(w.kt + it.t0), kb = load_plan(w.kt + it.t0 + it.n - 1);
+        const int cuts = __ldcg(w.counts + hd.nkt + it.t0 / 2);
         const int xs = max(2 * (x0 - it.kvh * rp), min(ka.lo, kb.lo));
         const int xe = min(2 * (x1 - it.kvh * rp), max(ka.hi, kb.hi));
         auto tile_of = [&](const KeyTile& t, const RowTile& r) -> int {      // its place in the row tile's list
@@ -1171,7 +1187,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         for (int i = xs; i < xe; i += 32) {
           bool see = false;
           if (i + lane < xe) {
-            r = load_row_tile(w.rt, i + lane);
+            r = load_plan(w.rt + i + lane);
             see = tile_of(ka, r) >= 0 || tile_of(kb, r) >= 0;
             if (i == xs) head = r;
           }
@@ -1194,7 +1210,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
           int j0 = -1, j1 = -1, row = 0;
           if (i + lane < xe) {
             if (g == 0) r = head;
-            else r = load_row_tile(w.rt, i + lane);
+            else r = load_plan(w.rt + i + lane);
             j0 = tile_of(ka, r);
             j1 = it.n == 2 ? tile_of(kb, r) : -1;
             const int base = (int)(slot0 + r.base);
@@ -1210,7 +1226,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
       } else {
         // the key tiles that either row tile sees
         const bool two = it.n == 2;
-        const RowTile r0 = load_row_tile(w.rt, it.t0), r1 = load_row_tile(w.rt, it.t0 + it.n - 1);
+        const RowTile r0 = load_plan(w.rt + it.t0), r1 = load_plan(w.rt + it.t0 + it.n - 1);
         const Merged u = merged(r0, r1, two);
         const int base0 = (int)(slot0 + r0.base), base1 = (int)(slot0 + r1.base);
         auto sees = [&](int j, MergedTile& t) {
@@ -1338,7 +1354,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         sh = 0;
         big = (size_t)nkv * D;
         if (rank < it.n) {
-          const KeyTile k = w.kt[it.t0 + rank];
+          const KeyTile k = load_plan(w.kt + it.t0 + rank);
           rows = k.n;
           o = ((size_t)k.row0 * nkv + it.kvh) * D;
         }
@@ -1346,7 +1362,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         sh = 31 - __clz(G);
         big = (size_t)a.L.n_q * D;
         if (rank < it.n) {
-          const RowTile r = load_row_tile(w.rt, it.t0 + rank);
+          const RowTile r = load_plan(w.rt + it.t0 + rank);
           rows = r.nt * G;
           o = ((size_t)r.row0 * a.L.n_q + it.kvh * G) * D;
         }
