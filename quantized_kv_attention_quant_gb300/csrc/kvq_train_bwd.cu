@@ -574,6 +574,10 @@ __device__ __forceinline__ uint32_t pack_h2_sat(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 // A wait by a whole warp.  One that gives up (kvq_common.cuh) flags the status
 // word once and lets the warp run on without waiting, all lanes alike.
 struct Waiter {
@@ -629,7 +633,7 @@ constexpr int kScThreads = (kScEpi + 2) * 32;
 constexpr float kPScale = 32768.f;
 
 // What the copies tell the other warps of their CTA about a unit.
-enum : int { kUnitFresh = 1, kUnitEnd = 2 };          // another pair of row tiles; no more
+enum : int { kUnitFresh = 1, kUnitEnd = 2, kUnitLast = 4 };      // another pair of row tiles; no more; another pair follows
 constexpr int kUnits = 4;                             // units told ahead
 struct alignas(16) Unit {
   int flags, slot[2], lp[2];                          // this CTA's tile slots (-1: not in its list), first positions
@@ -678,9 +682,9 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
   const int rank = (int)tc::cta_rank();
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::C_OFF);      // CTA 0's: both CTAs' copies landed
   uint64_t* empty = full + T::NS;
-  uint64_t* a_full = empty + T::NS;                   // CTA 0's: q and dO landed
-  uint64_t* a_free = a_full + 1;                      // the row tiles' products are done
-  uint64_t* acc_full = a_free + 1;                    // [2] a unit's S, its dP done
+  uint64_t* a_full = empty + T::NS;                   // [2] CTA 0's: q, dO landed
+  uint64_t* a_free = a_full + 2;                      // [2] the row tiles' S, dP are done
+  uint64_t* acc_full = a_free + 2;                    // [2] a unit's S, its dP done
   uint64_t* acc_free = acc_full + 2;                  // [2] CTA 0's: read by both epilogues
   uint64_t* unit_full = acc_free + 2;                 // [kUnits]
   uint64_t* unit_empty = unit_full + kUnits;          // [kUnits]
@@ -690,9 +694,9 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
-    mbar_init(a_full, 1);
-    mbar_init(a_free, 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(a_full + s, 1);
+      mbar_init(a_free + s, 1);
       mbar_init(acc_full + s, 1);
       mbar_init(acc_free + s, 2 * kScEpi);
     }
@@ -713,6 +717,8 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
   const uint32_t tmem = *tslot;
   // the plan and delta; the last chunk's tiles are read.  The next kernel is let
   // go only then, so that it may read the plan before it waits.
+  if (warp == kScEpi && lane == 0)
+    for (const CUtensorMap* m : {&tmq, &tmo, &tmk, &tmv}) prefetch_map(m);
   if (warp >= kScEpi) {
     pdl_wait();
     pdl_launch();
@@ -765,7 +771,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
         const int row0 = rank == 0 ? r0.row0 : r1.row0, pk = rank == 0 ? t0.pk : t1.pk, e = n % kUnits;
         wait.one(unit_empty + e, (n / kUnits & 1) ^ 1);
         Unit& un = units[e];
-        un.flags = fresh ? kUnitFresh : 0;
+        un.flags = (fresh ? kUnitFresh : 0) | (j + 2 >= u.n() && n + 1 < count ? kUnitLast : 0);
         un.slot[0] = k0 < 0 ? -1 : base + k0;
         un.slot[1] = k1 < 0 ? -1 : base + k1;
         un.lp[0] = t0.lp;
@@ -777,16 +783,15 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
         un.kend = rank == 0 ? r0.kend : r1.kend;
         un.kvh = kvh;
         mbar_arrive(unit_full + e);
-        if (T::RES && fresh) {                        // (told before: on it the MMA warp frees the last row tiles)
-          if (pairs > 0) wait.one(a_free, (pairs - 1) & 1);
-          if (rank == 0) mbar_arrive_expect_tx(a_full, 4 * NG * 16384);
-          for (int c = 0; c < NG; ++c) {
-            tc::tma2_load_3d(sb + T::A_OFF + c * 16384, &tmq, 64 * c, kvh * G, row0, a_full0);
-            tc::tma2_load_3d(sb + T::A_OFF + (NG + c) * 16384, &tmo, 64 * c, kvh * G, row0, a_full0);
-          }
-          ++pairs;
-        }
         for (int c = 0; c < 2 * NG; ++c) {
+          if (T::RES && fresh && c % NG == 0) {       // q before k, dO before v
+            const int half = c / NG;
+            if (pairs > 0) wait.one(a_free + half, (pairs - 1) & 1);
+            if (rank == 0) mbar_arrive_expect_tx(a_full + half, 2 * NG * 16384);
+            for (int b = 0; b < NG; ++b)
+              tc::tma2_load_3d(sb + T::A_OFF + (c + b) * 16384, half ? &tmo : &tmq, 64 * b, kvh * G, row0, a_full0 + 8 * half);
+            pairs += half;
+          }
           wait.one(empty + st, ph ^ 1);
           const int dim = 64 * (c < NG ? c : c - NG);
           const uint32_t dst = sb + T::R_OFF + st * T::STAGE, bar = full0 + 8 * st;
@@ -831,13 +836,12 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
       const int flags = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&units[e].flags), 0);
       if (lane == 0) mbar_arrive(unit_empty + e);
       if ((flags & kUnitEnd) || wait.dead) break;
-      if (T::RES && (flags & kUnitFresh)) {
-        if (pairs > 0 && lane == 0) tc::commit2(a_free);
-        __syncwarp();
-        wait(a_full, pairs++ & 1);
-      }
       for (int c = 0; c < 2 * NG; ++c) {
         const int half = c >= NG;
+        if (T::RES && (flags & kUnitFresh) && c % NG == 0) {
+          wait(a_full + half, pairs & 1);
+          pairs += half;
+        }
         if (n > 0 && (c == 0 || c == NG)) wait(acc_free + half, (n - 1) & 1);
         wait(full + st, ph);
         tc::fence_after_sync();
@@ -849,7 +853,10 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
             tc::mma2_f16(tmem + 256 * half, tc::desc_kmajor_sw128(as + 32 * s, 1024),
                          tc::desc_kmajor_sw128(bs + 32 * s, 1024), ID, (c != 0 && c != NG) || s != 0);
           tc::commit2(empty + st);
-          if (c == NG - 1 || c == 2 * NG - 1) tc::commit2(acc_full + half);
+          if (c == NG - 1 || c == 2 * NG - 1) {
+            if (T::RES && (flags & kUnitLast)) tc::commit2(a_free + half);
+            tc::commit2(acc_full + half);
+          }
         }
         __syncwarp();
         if (++st == T::NS) {
@@ -1084,6 +1091,8 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   // (the warp that lists the items needs the plan alone, which the scores kernel
   // has waited for before this one could start: the lists of a CTA's first items
   // are there when P and dS are, 4 to 7 us sooner)
+  if (warp == kPrEpi && lane == 0)
+    for (const CUtensorMap* m : {&tmq, &tmo, &tmk, &tmp, &tmd}) prefetch_map(m);
   if (warp != kPrEpi + 2) pdl_wait();
   pdl_launch();
 
