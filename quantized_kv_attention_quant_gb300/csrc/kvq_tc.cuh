@@ -169,6 +169,20 @@ __device__ __forceinline__ uint32_t in_cta0(const void* p) {
 __device__ __forceinline__ void arrive_cta0(uint64_t* mbar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(in_cta0(mbar)) : "memory");
 }
+// An arrival at CTA 0's barrier after reads that the other side may then overwrite.
+__device__ __forceinline__ void arrive_cta0_release(uint64_t* mbar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(in_cta0(mbar)) : "memory");
+}
+// A word into CTA 1's shared memory, its 4 bytes counted on CTA 1's barrier.
+__device__ __forceinline__ void send_cta1(const void* dst, int value, const void* mbar) {
+  uint32_t d, m;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 1;"
+               : "=r"(d) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 1;"
+               : "=r"(m) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mbar))));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+               :: "r"(d), "r"(value), "r"(m) : "memory");
+}
 __device__ __forceinline__ void tmem_alloc2(uint32_t* smem_dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem_dst))), "r"(ncols) : "memory");

@@ -128,6 +128,7 @@ struct Ws {
   int* chunk;                   // [nl + 1]: chunk c is pairs of row tiles chunk[c] .. chunk[c + 1] - 1 (kv head major)
   int* units;                   // [pairs of row tiles]: units of the scores kernel before each
   int* counts;                  // [nkt]: row tiles that see a key tile; then [key pairs]: pieces of its lists
+  int* next;                    // [nl]: the products' items drawn so far
   int* list;                    // the (key pair, piece) of every dk and dv item: pair * kMaxSplits + piece
   int4* begin;                  // [pairs]: a CTA pair's units, and the kv head, row tile pair and key tile of its first
   int* starts;                  // [2][n_blocks + 1]: row and key tiles before each block
@@ -147,7 +148,7 @@ struct Plan {
   int splits, piece;            // of a key pair's row tiles: most pieces; row tiles of one
   int direct;                   // one chunk, one split: dk and dv need no sums beside the outputs
   bool fits;                    // tile counts fit 32 bits (else nothing else is set)
-  size_t chunk_o, begin_o, units_o, counts_o, list_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
+  size_t chunk_o, next_o, begin_o, units_o, counts_o, list_o, starts_o, rt_o, kt_o, delta_o, acc_o, p_o, ds_o, bytes;
 };
 
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
@@ -204,6 +205,7 @@ Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows,
     return at;
   };
   p.chunk_o = take(((size_t)p.nl + 1) * 4);
+  p.next_o = take((size_t)p.nl * 4);
   p.begin_o = take(kMaxPairs * sizeof(int4));
   p.units_o = take(((size_t)p.nrt + 1) / 2 * 4);
   p.counts_o = take(((size_t)p.nkt + (p.nkt + 1) / 2) * 4);
@@ -224,6 +226,7 @@ Ws carve(void* base, const Plan& p) {
   Ws w;
   w.head = reinterpret_cast<Head*>(b);
   w.chunk = reinterpret_cast<int*>(b + p.chunk_o);
+  w.next = reinterpret_cast<int*>(b + p.next_o);
   w.counts = reinterpret_cast<int*>(b + p.counts_o);
   w.list = reinterpret_cast<int*>(b + p.list_o);
   w.units = reinterpret_cast<int*>(b + p.units_o);
@@ -292,6 +295,7 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
     __syncthreads();
     off = s_off;
   }
+  for (int c = tid; c < nl; c += kPrepThreads) w.next[c] = 0;
   const int P = off[1];
   bool bad = false;
   for (int b = tid; b < nb; b += kPrepThreads) {
@@ -1001,7 +1005,7 @@ bwd_scores_kernel(const TrainBwdArgs a, const Ws w, const int chunk, const int o
 // A step is a whole tile: 128 rows (or keys) of K in one stage, three copies (a
 // copy takes the issuing thread some 150 cycles; with stages of 64 the copies
 // took longer than their MMAs).
-constexpr int kBatches = 3;                                   // of 32 steps listed ahead
+constexpr int kBatches = 2, kBatch = 4;                       // of steps listed ahead, and steps of one
 constexpr int kItems = 4;                                     // items told to the epilogue ahead
 template <int N>
 struct Pr {
@@ -1012,8 +1016,8 @@ struct Pr {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int NS = N == 256 ? 3 : 4;
   static constexpr int E_OFF = NS * STAGE;                    // 4 KB per output warp
-  static constexpr int L_OFF = E_OFF + 8 * 4096;              // kBatches x 32 steps for the copies
-  static constexpr int C_OFF = L_OFF + kBatches * 512;
+  static constexpr int L_OFF = E_OFF + 8 * 4096;              // the copies' list
+  static constexpr int C_OFF = L_OFF + kBatches * kBatch * 16;
   static constexpr int BYTES = C_OFF + 512 + 1024;
 };
 constexpr int kPrEpi = 8;
@@ -1055,10 +1059,13 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   uint64_t* item_empty = item_full + kItems;          // [kItems]
   uint64_t* list_full = item_empty + kItems;          // [kBatches]
   uint64_t* list_empty = list_full + kBatches;        // [kBatches]
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(list_empty + kBatches);
+  uint64_t* mail_full = list_empty + kBatches;        // [2] CTA 1's: the next item's number
+  uint64_t* mail_empty = mail_full + 2;               // [2] CTA 0's
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(mail_empty + 2);
   volatile int* info = reinterpret_cast<volatile int*>(tslot + 1);   // [NS] stage flags (CTA 0)
   volatile int* items = info + T::NS;                 // [kItems][2]: item (-1: no more), its steps
   volatile int* list_n = items + 2 * kItems;          // [kBatches] steps of a batch (0: no more)
+  volatile int* mail = list_n + kBatches;             // [2] (CTA 1)
   int4* list = reinterpret_cast<int4*>(sm + T::L_OFF);
   if (tid == 0) {
     for (int s = 0; s < T::NS; ++s) {
@@ -1068,6 +1075,8 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
     for (int s = 0; s < 2; ++s) {
       mbar_init(done + s, 1);
       mbar_init(acc_free + s, 2 * kPrEpi);
+      mbar_init(mail_full + s, 1);
+      mbar_init(mail_empty + s, 1);
     }
     for (int s = 0; s < kItems; ++s) {
       mbar_init(item_full + s, 1);
@@ -1159,26 +1168,47 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         bph ^= 1;
       }
     };
-    // (there and back: the lists grow shorter, so every pair gets long and short ones)
-    for (int id0 = 0, back = 0; id0 < n_items; id0 += gridDim.x / 2, back ^= 1) {
-      const int id = id0 + (int)(back ? gridDim.x / 2 - 1 - blockIdx.x / 2 : blockIdx.x / 2);
-      if (id >= n_items) continue;
+    // The items are taken from a counter, the longest first: CTA 0 draws one as soon
+    // as the last's final steps are listed (four to eight of them still to copy) and
+    // sends its number to CTA 1.  Who takes an item does not show in the results.
+    auto draw = [&](int k) {
+      const int slot = k & 1, parity = k >> 1 & 1;
+      int id = 0;
+      if (rank == 0) {
+        wait(mail_empty + slot, parity ^ 1);
+        if (lane == 0) {
+          id = (int)(gridDim.x / 2) + atomicAdd(w.next + pa.chunk, 1);
+          tc::send_cta1(const_cast<int*>(mail + slot), id, mail_full + slot);
+        }
+        id = __shfl_sync(0xffffffffu, id, 0);
+      } else {
+        if (lane == 0) mbar_arrive_expect_tx(mail_full + slot, 4);
+        __syncwarp();
+        wait(mail_full + slot, parity);
+        id = mail[slot];
+        __syncwarp();
+        if (lane == 0) tc::arrive_cta0_release(mail_empty + slot);
+      }
+      return wait.dead ? n_items : id;
+    };
+    for (int id = blockIdx.x / 2, k = 0; id < n_items; id = draw(k++)) {
       const Item it = decode(id);
       const long long slot0 = (long long)it.kvh * hd.ntiles - c0;    // slot of the kv head's first tile
       const int place = it.kvh << 10 | (it.half * N + rank * T::DIMS), kind = it.dkv ? kKeys | (it.kind == 0 ? kQ : 0) : 0;
       int at = 0, n = 0;                              // steps listed, steps of the item
-      // up to 32 steps, one a lane where `see`: s0 and s1 (-1: not there) are the tiles
+      // steps, one a lane where `see`: s0 and s1 (-1: not there) are the tiles
       // of the pair, `row` the first of the 128 rows of B that they meet
       auto batch = [&](bool see, int s0, int s1, int row) {
         const uint32_t m = __ballot_sync(0xffffffffu, see);
-        if (m == 0) return;
-        wait(list_empty + b, bph ^ 1);
-        const int x = __popc(m & ((1u << lane) - 1)), mine = rank == 0 ? s0 : s1;
-        if (see)
-          list[32 * b + x] = make_int4(mine >= 0 ? mine : pa.zero, row, place,
-                                       kind | (at + x == 0 ? kFirst : 0) | (at + x == n - 1 ? kLast : 0));
-        at += __popc(m);
-        hand_over(__popc(m));
+        const int x = __popc(m & ((1u << lane) - 1)), mine = rank == 0 ? s0 : s1, steps = __popc(m);
+        for (int from = 0; from < steps; from += kBatch) {
+          wait(list_empty + b, bph ^ 1);
+          if (see && x >= from && x < from + kBatch)
+            list[kBatch * b + x - from] = make_int4(mine >= 0 ? mine : pa.zero, row, place,
+                                                    kind | (at + x == 0 ? kFirst : 0) | (at + x == n - 1 ? kLast : 0));
+          hand_over(min(kBatch, steps - from));
+        }
+        at += steps;
       };
       if (it.dkv) {
         // the chunk's row tiles that see either key tile; this piece's share of them by count
@@ -1265,7 +1295,7 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
         const int n = wait.dead ? 0 : list_n[b];
         if (n == 0) break;
         for (int x = 0; x < n; ++x) {
-          const int4 s = list[32 * b + x];            // tile, first row of B, kv head and dims, flags
+          const int4 s = list[kBatch * b + x];            // tile, first row of B, kv head and dims, flags
           wait.one(empty + st, ph ^ 1);
           const uint32_t dst = sb + st * T::STAGE, bar = bar0 + 8 * st;
           if (rank == 0) {
