@@ -160,7 +160,9 @@ __host__ __device__ constexpr int prod_n(int D) { return D > 256 ? 256 : D; }
 // heads of 512 took 1016 us in chunks of 1024 (64 MB, within L2), 751 of 2048, 612
 // in one: longer sums for each output beat L2 hits.
 constexpr int kChunkTiles = 16384;
-constexpr int kMinPiece = 8;
+// Least row tiles of a piece: 6 and 8 took 27.4 and 30.3 us on 900 rows in ragged
+// blocks, 54.8 and 53.5 on 2048 rows with a window of 512 (head_dim 256, 8 heads).
+constexpr int kMinPiece = 6;
 
 Plan make_plan(const LayerArgs& L, int n_blocks, int n_rows, int max_block_rows, int num_sms) {
   Plan p = {};
@@ -1108,13 +1110,22 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
   const Head hd = load_plan(w.head);
   const int G = a.L.G, nkv = a.L.n_kv;
   const int x0 = __ldcg(w.chunk + pa.chunk), x1 = __ldcg(w.chunk + pa.chunk + 1);
-  // an empty chunk (or layout) has no items; dk and dv come first (the longest sums)
-  const int rp = (hd.nrt + 1) / 2;
-  const int n_dkv = x0 < x1 ? hd.npieces * nkv * 2 * H : 0;
-  const int n_items = n_dkv + (x1 - x0) * H;
+  // Items kv head by kv head, the last first: its tiles are the newest in L2, and dq
+  // meets the dS that dk has just read.  Of a head dk and dv come first (the longest
+  // sums).  An empty chunk (or layout) has no items.
+  const int rp = (hd.nrt + 1) / 2, n_dkv = hd.npieces * 2 * H;       // (of one kv head)
+  const int n_items = x0 < x1 ? n_dkv * nkv + (x1 - x0) * H : 0;
   const long long c0 = x0 < x1 ? (long long)(x0 / rp) * hd.ntiles + __ldcg(&w.rt[x0 % rp * 2].base) : 0;
   auto decode = [&](int id) {
     Item t;
+    auto above = [&](int h) { return n_dkv * (nkv - 1 - h) + H * max(0, x1 - max(x0, (h + 1) * rp)); };
+    int lo = 0, hi = nkv - 1;                         // the least head with no more items above it than id
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (above(mid) <= id) hi = mid; else lo = mid + 1;
+    }
+    id -= above(lo);
+    t.kvh = lo;
     t.dkv = id < n_dkv;
     if (!t.dkv) id -= n_dkv;
     t.half = id % H;
@@ -1122,17 +1133,12 @@ bwd_products_kernel(const TrainBwdArgs a, const Ws w, const ProdArgs pa, const _
     t.kind = t.split = 0;
     if (t.dkv) {
       t.kind = id % 2;
-      id /= 2;
-      t.kvh = id % nkv;
-      id /= nkv;
-      id = __ldcg(w.list + id);
+      id = __ldcg(w.list + id / 2);
       t.split = id % kMaxSplits;
       t.t0 = id / kMaxSplits * 2;
       t.n = min(2, hd.nkt - t.t0);
     } else {
-      id += x0;
-      t.kvh = id / rp;
-      t.t0 = id % rp * 2;
+      t.t0 = (max(x0 - lo * rp, 0) + id) * 2;
       t.n = min(2, hd.nrt - t.t0);
     }
     return t;
