@@ -462,8 +462,9 @@ kvq_status attn_train_donor_forward_lse(const kvq_layer* layer, int32_t n_blocks
  *   dq_hat_i = sum_j dS_ij k_hat_j
  *   dk_hat_j = sum_i dS_ij q_hat_i,  dv_hat_j = sum_i P_ij d_out_i
  * the last two over every row i that sees j and every q head of j's kv head.
- * Sums are fp32 in an order that depends on the arguments alone (the same call
- * gives the same bits); P and dS enter the products as bf16.
+ * Sums are fp32 in an order that depends on the arguments and the GPU alone (the
+ * same call gives the same bits); P and dS enter the products as bf16 (dS from P
+ * rounded to 11 bits).
  *
  *   max_block_rows   host upper bound of the rows of every block, 1 .. n_rows (a
  *                    longer block makes the layout invalid, below)
@@ -481,11 +482,16 @@ kvq_status attn_train_donor_forward_lse(const kvq_layer* layer, int32_t n_blocks
  *                    gradients are added to what is there, so that a donor's buffers
  *                    collect those of the layers that read its keys and values
  *   workspace        device scratch of at least attn_train_backward_workspace_bytes(...)
- *                    bytes; its first 4 bytes receive the status word
+ *                    bytes (up to about 1 GB, then some more for sums of fp32: 256 MB
+ *                    or 8 bytes per element of dk_hat, what is larger); its first 4
+ *                    bytes receive the status word
  * All inputs must be finite; the outputs must not overlap the inputs or each other.
  * A layout that breaks the rules above (or has a block longer than
  * max_block_rows) leaves every output as it was and sets
- * KVQ_STATUS_SEQ_SKIPPED.  n_q_heads / n_kv_heads must divide 128.
+ * KVQ_STATUS_SEQ_SKIPPED.  n_q_heads / n_kv_heads must divide 128, n_kv_heads be at
+ * most 65535, and the tiles of 128 (row, head) x 128 keys that max_block_rows and
+ * the window allow fewer than 2^31 (a causal pass of some 2 million rows with 16
+ * q heads per kv head), else the call is KVQ_EUNSUPPORTED.
  */
 kvq_status attn_train_backward(const kvq_layer* layer, int32_t n_blocks, const int32_t* block_offsets,
                                int32_t n_rows, int32_t max_block_rows,
@@ -494,7 +500,8 @@ kvq_status attn_train_backward(const kvq_layer* layer, int32_t n_blocks, const i
                                uint16_t* dq_hat, void* dk_hat, void* dv_hat, int32_t dkv_is_f32,
                                int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
-/* 0 for an invalid layer or count; never less for more rows. */
+/* 0 for an invalid layer or count, or a pass of too many tiles; otherwise never
+ * less for more rows. */
 size_t attn_train_backward_workspace_bytes(const kvq_layer* layer, int32_t n_blocks, int32_t n_rows,
                                            int32_t max_block_rows);
 
@@ -520,8 +527,10 @@ size_t attn_train_backward_workspace_bytes(const kvq_layer* layer, int32_t n_blo
  *       k_norm_w                       device bf16 [head_dim];  dk_norm_w  device fp32 [head_dim]
  *   workspace   device scratch of at least kvq_train_prep_backward_workspace_bytes(layer,
  *               n_rows) bytes; its first 4 bytes receive the status word
+ * All inputs must be finite, and the sum of a raw row's squares, plus eps, neither
+ * zero nor past the range of fp32 (|x| < 10^17 with eps > 0).
  * dq_norm_w and dk_norm_w are written (not added to), summed in fp32 in an
- * order that depends on the arguments alone; with n_rows == 0 nothing is
+ * order that depends on the arguments and the GPU alone; with n_rows == 0 nothing is
  * written.  An output may be the buffer of the gradient it comes from (dq_raw
  * == dq_hat; dk_raw == dk_hat and dv_raw == dv_hat when those are bf16), else
  * outputs must not overlap inputs or each other.  A layout that breaks the

@@ -1096,6 +1096,6 @@ const char* kvq_status_string(kvq_status s) {
 
 const char* kvq_last_error(void) { return g_last_error.c_str(); }
 
-int32_t kvq_version(void) { return 130; }
+int32_t kvq_version(void) { return 140; }
 
 }  // extern "C"
