@@ -12,13 +12,13 @@
 // calls are bound by the latency of those loads at 16 warps an SM (16384 rows of 8 +
 // 2 + 2 heads of 256, fp32 gradients of keys and values: 84 us, 0.59 of the measured
 // copy rate), short ones by the angles and the chain of shuffles of a row (2048 such
-// rows in 20 us, 0.27; issue slots 47 % busy): the layout is for loads in flight and
+// rows in 18 us, 0.31; issue slots 47 % busy): the layout is for loads in flight and
 // few instructions.  80 registers, for 24 warps an SM, spilled (125 us); a block
 // barrier and a shared table of angles per row took 182.
-// Every warp works alone: it takes units of one row and a run of its heads (q
-// heads on some of a block's warps, a donor's keys and values on the others),
-// evaluates the row's angles once, keeps the (cos, sin) of its own dims in
-// registers for all heads, and holds the next heads' x and dz in flight.  VEC
+// Every warp works alone on runs of (row, head) pairs, a row's heads as a rule (q
+// heads on some of a block's warps, a donor's keys and values on the others): it
+// evaluates a row's angles once, keeps the (cos, sin) of its own dims in registers for all
+// heads, and holds the next heads' x and dz in flight.  VEC
 // consecutive dims of a lane per 16-byte access; the rotation's partner of a dim
 // sits a fixed number of lanes away (one shuffle).  dw stays in registers over
 // all rows of a warp, goes to one partial row per block and is summed over the
@@ -223,10 +223,9 @@ struct PbWs {
   float* part;          // [blocks][2][D]: q and k weight gradients
 };
 
-// The share of a call's work: qw of a block's warps take q heads, the others
-// keys and values; a unit is one row and 1/q_cut of its q heads (1/kv_cut of its
-// kv heads).
-struct PbShare { int qw, q_cut, kv_cut; };
+// The share of a call's work: qw of a block's warps take q heads, the others keys
+// and values, in runs of q_run or kv_run consecutive (row, head) pairs.
+struct PbShare { int qw, q_run, kv_run; };
 
 template <int D>
 __global__ void __launch_bounds__(kPbWarps * 32, 2)
@@ -255,10 +254,10 @@ prep_bwd_kernel(const PrepBwdArgs a, const RopeFreqs freqs, const PbWs ws, const
   if (blockIdx.x == 0 && tid == 0) *ws.status = bad ? 1u << KVQ_DEV_BADSEQ : 0u;
   if (bad) return;
 
-  const bool is_q = warp < sh.qw;
-  const int heads = is_q ? Hq : Hkv, cut = is_q ? sh.q_cut : sh.kv_cut;
-  const int n_warps = (is_q ? sh.qw : kPbWarps - sh.qw) * gridDim.x;
-  const int me = is_q ? (int)blockIdx.x * sh.qw + warp : (int)blockIdx.x * (kPbWarps - sh.qw) + warp - sh.qw;
+  const int qw = sh.qw;
+  const bool is_q = warp < qw;
+  const int heads = is_q ? Hq : Hkv, n_warps = (is_q ? qw : kPbWarps - qw) * gridDim.x, run = is_q ? sh.q_run : sh.kv_run;
+  const int me = is_q ? (int)blockIdx.x * qw + warp : (int)blockIdx.x * (kPbWarps - qw) + warp - qw;
   const int kind = rope_kind<D>(R);
   float dw[E];
   uint32_t w[NW];                                     // the weights (only 2-byte aligned), two to a word
@@ -271,23 +270,26 @@ prep_bwd_kernel(const PrepBwdArgs a, const RopeFreqs freqs, const PbWs ws, const
       dw[i] = dw[i + 1] = 0.f;
     }
   }
-  // units me, me + n_warps, ...: row and share of its heads
-  struct At { int row, c, h, end; };
-  const int d_row = n_warps / cut, d_c = n_warps % cut;
-  auto heads_of = [&](At& p) {
-    p.h = p.c * heads / cut;
-    p.end = (p.c + 1) * heads / cut;
-  };
-  auto next_unit = [&](At& p) {
-    p.row += d_row;
-    if ((p.c += d_c) >= cut) {
-      p.c -= cut;
+  // this warp's runs me, me + n_warps, ... of the (row, head) pairs
+  struct At { int row, h, left; };
+  const long long first = (long long)me * run, jump = (long long)(n_warps - 1) * run;
+  const int jump_rows = (int)(jump / heads), jump_heads = (int)(jump % heads);
+  At at = {(int)min((long long)a.n_rows, first / heads), (int)(first % heads), run};
+  auto step = [&](At& p) {
+    if (--p.left == 0) {
+      p.left = run;
+      p.row += jump_rows;
+      p.h += jump_heads;
+      if (p.h >= heads) {
+        p.h -= heads;
+        ++p.row;
+      }
+    }
+    if (++p.h == heads) {
+      p.h = 0;
       ++p.row;
     }
-    heads_of(p);
   };
-  At at = {me / cut, me % cut, 0, 0};
-  heads_of(at);
   float2 cs[T::VEC];
   int at_row = -1;
   auto angles = [&](int row) {                        // the row's rotation: table, and this lane's part of it
@@ -315,10 +317,7 @@ prep_bwd_kernel(const PrepBwdArgs a, const RopeFreqs freqs, const PbWs ws, const
     }
   };
   if (is_q) {
-    // (row, head) in unit order, x and dz of the next AHEAD in flight
-    auto step = [&](At& p) {
-      if (++p.h == p.end) next_unit(p);
-    };
+    // x and dz of the next AHEAD heads in flight
     constexpr int AHEAD = D <= 256 ? 2 : 0;           // (head_dim 512: no registers for it)
     uint32_t xr[AHEAD + 1][NW], zr[AHEAD + 1][NW];
     At ahead = at;
@@ -351,39 +350,37 @@ prep_bwd_kernel(const PrepBwdArgs a, const RopeFreqs freqs, const PbWs ws, const
       if (a.dkv_f32) load_f32<D>(static_cast<const float*>(g) + o, lane, z);
       else load_bf16<D>(static_cast<const uint16_t*>(g) + o, lane, z);
     };
-    for (; at.row < a.n_rows; next_unit(at)) {
-      for (int h = at.h; h < at.end; ++h) {
-        const size_t o = ((size_t)at.row * heads + h) * D;
-        // all four rows in flight at once; at head_dim 512 v's after k's
-        constexpr bool EARLY = D <= 256;
-        float z[E], y[E], dx[E];
-        uint32_t xr[NW], vr[NW];
-        auto load_v = [&]() {
-          if (!a.L.k_eq_v) load_raw<D>(a.v_raw + o, lane, vr);
-          gradient(a.dv_hat, o, y);
-        };
-        load_raw<D>(a.k_raw + o, lane, xr);
-        gradient(a.dk_hat, o, z);
-        if (EARLY) load_v();
-        angles(at.row);
-        {
-          float x[E];
-          unpack<D>(xr, x);
-          unrotate<D>(z, lane, R, kind, cs, table, rows + warp * D);
-          norm_backward<D, true>(x, z, w, a.L.eps, dx, dw);
-        }
-        if (!a.L.k_eq_v) store_bf16<D>(a.dk_raw + o, lane, dx);
-        if (!EARLY) load_v();
-        float x[E], dv[E];
-        unpack<D>(a.L.k_eq_v ? xr : vr, x);
-        norm_backward<D, false>(x, y, w, a.L.eps, dv, dw);
-        if (a.L.k_eq_v) {
+    for (; at.row < a.n_rows; step(at)) {
+      const size_t o = ((size_t)at.row * heads + at.h) * D;
+      // all four rows in flight at once; at head_dim 512 v's after k's
+      constexpr bool EARLY = D <= 256;
+      float z[E], y[E], dx[E];
+      uint32_t xr[NW], vr[NW];
+      auto load_v = [&]() {
+        if (!a.L.k_eq_v) load_raw<D>(a.v_raw + o, lane, vr);
+        gradient(a.dv_hat, o, y);
+      };
+      load_raw<D>(a.k_raw + o, lane, xr);
+      gradient(a.dk_hat, o, z);
+      if (EARLY) load_v();
+      angles(at.row);
+      {
+        float x[E];
+        unpack<D>(xr, x);
+        unrotate<D>(z, lane, R, kind, cs, table, rows + warp * D);
+        norm_backward<D, true>(x, z, w, a.L.eps, dx, dw);
+      }
+      if (!a.L.k_eq_v) store_bf16<D>(a.dk_raw + o, lane, dx);
+      if (!EARLY) load_v();
+      float x[E], dv[E];
+      unpack<D>(a.L.k_eq_v ? xr : vr, x);
+      norm_backward<D, false>(x, y, w, a.L.eps, dv, dw);
+      if (a.L.k_eq_v) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) dx[i] += dv[i];
-          store_bf16<D>(a.dk_raw + o, lane, dx);
-        } else {
-          store_bf16<D>(a.dv_raw + o, lane, dv);
-        }
+        for (int i = 0; i < E; ++i) dx[i] += dv[i];
+        store_bf16<D>(a.dk_raw + o, lane, dx);
+      } else {
+        store_bf16<D>(a.dv_raw + o, lane, dv);
       }
     }
   }
@@ -393,7 +390,7 @@ prep_bwd_kernel(const PrepBwdArgs a, const RopeFreqs freqs, const PbWs ws, const
   for (int i = 0; i < E; ++i) rows[warp * D + T::dim(i / T::VEC, lane) + i % T::VEC] = dw[i];
   __syncthreads();
   for (int i = tid; i < 2 * D; i += kPbWarps * 32) {
-    const int kv = i / D, e = i % D, w0 = kv ? sh.qw : 0, w1 = kv ? kPbWarps : sh.qw;
+    const int kv = i / D, e = i % D, w0 = kv ? qw : 0, w1 = kv ? kPbWarps : qw;
     if (w0 == w1) continue;
     float s = 0.f;
     for (int x = w0; x < w1; ++x) s += rows[x * D + e];
@@ -437,23 +434,23 @@ cudaError_t launch_t(const PrepBwdArgs& a, const RopeFreqs& f, void* wsp, int nu
   const int half = a.L.rope_dims / 2, nq = a.q_raw ? a.L.n_q : 0, nkv = a.k_raw ? a.L.n_kv : 0;
   // warps in proportion to the bytes of a row
   const long long q_bytes = 6LL * nq, kv_bytes = (long long)nkv * ((a.L.k_eq_v ? 4 : 8) + (a.dkv_f32 ? 8 : 4));
-  PbShare sh;
-  sh.qw = nkv == 0 ? kPbWarps
-          : nq == 0 ? 0
-                    : (int)std::max<long long>(1, std::min<long long>(kPbWarps - 1, (kPbWarps * q_bytes + (q_bytes + kv_bytes) / 2) / (q_bytes + kv_bytes)));
-  // blocks: enough that no warp has more than one head, two per SM at most;
-  // then units small enough that every warp gets about two
-  const int kw = kPbWarps - sh.qw;
-  const long long want = std::max(sh.qw ? ((long long)a.n_rows * nq + sh.qw - 1) / sh.qw : 0,
+  const int qw = nkv == 0 ? kPbWarps
+                 : nq == 0 ? 0
+                           : (int)std::max<long long>(1, std::min<long long>(kPbWarps - 1, (kPbWarps * q_bytes + (q_bytes + kv_bytes) / 2) / (q_bytes + kv_bytes)));
+  // blocks: enough that no warp has more than one head, two per SM at most
+  const int kw = kPbWarps - qw;
+  const long long want = std::max(qw ? ((long long)a.n_rows * nq + qw - 1) / qw : 0,
                                   kw ? ((long long)a.n_rows * nkv + kw - 1) / kw : 0);
   // (a handful of heads goes to one block, which needs no second kernel)
   const int blocks = want <= 3 ? 1 : (int)std::min<long long>(std::min(kPbMaxBlocks, 2 * num_sms), want);
-  auto cuts = [&](int warps, int heads) {
-    const long long c = warps ? (2LL * warps * blocks + a.n_rows - 1) / a.n_rows : 1;
-    return (int)std::max<long long>(1, std::min<long long>(heads, c));
+  // a row's heads in one run (its angles are evaluated once: 2048 rows of 8 heads of
+  // 256 took 18.2 us so, 20.3 in runs of 4, 22.9 in one run per warp, 16384 rows 84.7,
+  // 107 and 111), fewer where there are not as many pairs for every warp
+  auto run_of = [&](int warps, int heads) {
+    const long long all = (long long)a.n_rows * heads, n = std::max(1LL, (long long)warps * blocks);
+    return (int)std::max(1LL, std::min<long long>(heads, (all + n - 1) / n));
   };
-  sh.q_cut = cuts(sh.qw, nq);
-  sh.kv_cut = cuts(kw, nkv);
+  const PbShare sh = {qw, run_of(qw, nq), run_of(kw, nkv)};
   const size_t smem = 16 * ((3 * half + 3) / 4) + (size_t)kPbWarps * (D * 4 + half * 8);      // at most 35 KB
   cudaError_t e;
   if ((e = launch_pdl(prep_bwd_kernel<D>, dim3(blocks), dim3(kPbWarps * 32), smem, st, a, f, ws, sh)) != cudaSuccess)
