@@ -334,6 +334,47 @@ def test_two_streams_with_their_own_workspaces(m):
         c.verify()
 
 
+@pytest.mark.parametrize("D,n_q,n_kv,window,blocks", [(512, 16, 1, 0, [512, 300, 301]), (128, 8, 8, 0, [1501])])
+def test_same_bits_beside_another_stream(m, D, n_q, n_kv, window, blocks):
+    """CTAs draw their sums' pieces from a counter: with calls on two streams at
+    once they draw them in another order each time, and the bits stay."""
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    T = sum(blocks)
+    lay, offs = m.layer(n_q, n_kv, D, window, 0, 1e4), offsets(blocks)
+    ws_bytes = m.attn_train_backward_workspace_bytes(lay, len(blocks), T, max(blocks))
+
+    def case():
+        q, do, out = (torch.randn(T, n_q, D, generator=gen, device="cuda") * x for x in (0.2, 0.01, 0.5))
+        k, v = (torch.randn(T, n_kv, D, generator=gen, device="cuda") * x for x in (0.2, 1.0))
+        lse = torch.full((T, n_q), 8.0, device="cuda")    # (any finite statistics will do)
+        got = [torch.empty(T, h, D, dtype=torch.bfloat16, device="cuda") for h in (n_q, n_kv, n_kv)]
+        return [x.bfloat16() for x in (q, k, v)], out, lse, do.bfloat16(), got, torch.empty(ws_bytes, dtype=torch.uint8, device="cuda")
+
+    def run(c, stream):
+        (q, k, v), out, lse, do, got, ws = c
+        m.attn_train_backward(lay, len(blocks), offs, T, max(blocks), q, k, v, out, 1, lse, do, *got, 0, 0, ws, ws_bytes,
+                              stream)
+
+    cases, streams = [case(), case()], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    first = []
+    for c in cases:
+        run(c, streams[0])
+        torch.cuda.synchronize()
+        first.append([t.clone() for t in c[4]])
+    for _ in range(10):
+        for c in cases:
+            for t in c[4]:
+                t.zero_()
+        torch.cuda.synchronize()
+        for c, st in zip(cases, streams):
+            run(c, st)
+        torch.cuda.synchronize()
+        for c, f in zip(cases, first):
+            assert all(torch.equal(x, y) for x, y in zip(c[4], f))
+            assert int(c[5][:4].view(torch.int32)[0]) == 0
+
+
 @pytest.mark.parametrize("kind", ["sliding", "full"])
 def test_read_backward_of_the_stack(m, kind):
     """The 42-layer stack's layer shapes over its training pass (prefix 1024,
