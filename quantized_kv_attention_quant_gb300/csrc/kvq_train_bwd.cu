@@ -64,7 +64,9 @@ struct alignas(16) RowTile {
   int off0, block, kend, pad;
 };
 // A key tile: keys row0 .. row0 + n - 1 (packed), tile idx of its block; the row
-// tiles that may see it are lo .. hi - 1 (a branch's: its own, from there on).
+// tiles that may see it are lo .. hi - 1 (a branch's: its own, from there on; with a
+// window, up to the last whose window reaches back to it.  The products' lists look
+// at each of them, for every item: without that end the listing grew with rows x rows).
 struct alignas(16) KeyTile { int row0, n, block, idx, lo, hi, pad[2]; };
 
 // The key tiles that either of two row tiles sees: prefix tiles a0 .., own-block
@@ -338,8 +340,15 @@ __device__ void plan_block(const TrainBwdArgs& a, const Ws& w, const PlanArgs pl
   __syncthreads();
   for (int i = tid; i < nkt; i += kPrepThreads) {
     const int b = last_le(ks, nb, i), idx = i - ks[b], o0 = off[b];
-    const int lo = rs[b] + idx * kT / TQ, hi = b == 0 || b + 1 == nb ? nrt : rs[b + 1];
-    w.kt[i] = KeyTile{o0 + idx * kT, min(kT, off[b + 1] - o0 - idx * kT), b, idx, lo, hi, {0, 0}};
+    const int n = min(kT, off[b + 1] - o0 - idx * kT), lo = rs[b] + idx * kT / TQ;
+    int hi = b == 0 || b + 1 == nb ? nrt : rs[b + 1];
+    if (W > 0) {
+      // the last row of its block, from the block's start, whose window holds the tile's
+      // last key; a prefix tile is seen by branches (from position P on) only if that is P or later
+      const long long last = (long long)idx * kT + n - 1 + W - 1;
+      if (b > 0 || last < P) hi = (int)min((long long)(b == 0 && nb > 1 ? rs[1] : hi), rs[b] + last / TQ + 1);
+    }
+    w.kt[i] = KeyTile{o0 + idx * kT, n, b, idx, lo, hi, {0, 0}};
     counts[i] = 0;
   }
   __syncthreads();
