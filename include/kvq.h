@@ -482,9 +482,12 @@ kvq_status attn_train_donor_forward_lse(const kvq_layer* layer, int32_t n_blocks
  *                    gradients are added to what is there, so that a donor's buffers
  *                    collect those of the layers that read its keys and values
  *   workspace        device scratch of at least attn_train_backward_workspace_bytes(...)
- *                    bytes (up to about 1 GB, then some more for sums of fp32: 256 MB
- *                    or 8 bytes per element of dk_hat, what is larger); its first 4
- *                    bytes receive the status word
+ *                    bytes, at most the sum of 1 GiB, or where rows may see more than
+ *                    some 524,000 keys 2 KiB per key that a row may see (all at or
+ *                    before it, or the window); of fp32 sums 256 MiB, or 8 bytes per
+ *                    element of dk_hat where that is more; 4 bytes per element of lse;
+ *                    104 bytes per row; 8 bytes per block; 4 MiB.  Its first 4 bytes
+ *                    receive the status word
  * All inputs must be finite; the outputs must not overlap the inputs or each other.
  * A layout that breaks the rules above (or has a block longer than
  * max_block_rows) leaves every output as it was and sets

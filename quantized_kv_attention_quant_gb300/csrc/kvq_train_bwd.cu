@@ -10,7 +10,8 @@
 // kernel that keeps S and dP beside them would have to split the head dims and
 // recompute both (8 or 9 products instead of 5).  Instead P and dS go through
 // the workspace as bf16 tiles of 128 rows x 128 keys, a chunk of the tile list at
-// a time (1 GB at most; the workspace does not grow with rows x keys):
+// a time (1 GB, or four row tiles' whole lists where that is more: it does not grow
+// with rows x keys, past some 524,000 visible keys it does with the keys):
 //   prep     delta per (row, head); one block lists the row tiles, key tiles
 //            and chunks of the layout
 //   scores   S and dP of one chunk's tiles (tcgen05, fp32 in tensor memory),
@@ -163,7 +164,8 @@ inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 // Output columns per CTA of the products kernel.
 __host__ __device__ constexpr int prod_n(int D) { return D > 256 ? 256 : D; }
 
-// Tiles of a chunk (1 GB of workspace at most).  Larger is faster: 4096 rows of 16
+// Tiles of a chunk (1 GB of workspace; more only where a row tile sees over 4096 key
+// tiles, as a chunk ends before a pair of row tiles that does not fit).  Larger is faster: 4096 rows of 16
 // heads of 512 took 1016 us in chunks of 1024 (64 MB, within L2), 751 of 2048, 612
 // in one: longer sums for each output beat L2 hits.
 constexpr int kChunkTiles = 16384;
