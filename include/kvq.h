@@ -616,8 +616,8 @@ const char* kvq_status_string(kvq_status status);
 /*
  * kvq_profile_next_read -- profiling: the calling host thread's next call
  * that reads attention (attn_decode, attn_decode_append, attn_prefill_chunk,
- * attn_prefill_append, attn_train_forward, attn_train_donor_forward; not
- * attn_mixed) records start_event on its stream right before launching its
+ * attn_prefill_append, attn_train_forward and attn_train_donor_forward, with
+ * or without _lse; not attn_mixed nor attn_train_backward) records start_event on its stream right before launching its
  * attention kernel and stop_event right after, so that
  * cudaEventElapsedTime gives that kernel's time alone.  Both are
  * cudaEvent_t created with timing enabled, or both NULL (clears).  Inside a
