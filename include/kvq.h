@@ -491,8 +491,8 @@ kvq_status attn_train_donor_forward_lse(const kvq_layer* layer, int32_t n_blocks
  * All inputs must be finite; the outputs must not overlap the inputs or each other.
  * A layout that breaks the rules above (or has a block longer than
  * max_block_rows) leaves every output as it was and sets
- * KVQ_STATUS_SEQ_SKIPPED.  n_q_heads / n_kv_heads must divide 128, n_kv_heads be at
- * most 65535, and the tiles of 128 (row, head) x 128 keys that max_block_rows and
+ * KVQ_STATUS_SEQ_SKIPPED.  n_q_heads / n_kv_heads must divide 128 (1, 2, 4, 8 or 16:
+ * a layer has 16 at most), n_kv_heads be at most 65535, and the tiles of 128 (row, head) x 128 keys that max_block_rows and
  * the window allow fewer than 2^31 (a causal pass of some 2 million rows with 16
  * q heads per kv head), else the call is KVQ_EUNSUPPORTED.
  */
@@ -617,8 +617,9 @@ const char* kvq_status_string(kvq_status status);
  * kvq_profile_next_read -- profiling: the calling host thread's next call
  * that reads attention (attn_decode, attn_decode_append, attn_prefill_chunk,
  * attn_prefill_append, attn_train_forward and attn_train_donor_forward, with
- * or without _lse; not attn_mixed nor attn_train_backward) records start_event on its stream right before launching its
- * attention kernel and stop_event right after, so that
+ * or without _lse; not attn_mixed nor attn_train_backward) records
+ * start_event on its stream right before launching its attention kernel and
+ * stop_event right after, so that
  * cudaEventElapsedTime gives that kernel's time alone.  Both are
  * cudaEvent_t created with timing enabled, or both NULL (clears).  Inside a
  * stream capture they are recorded as external event nodes.  Recording an

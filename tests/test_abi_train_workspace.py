@@ -47,3 +47,18 @@ def test_workspace_of_long_passes(m):
     b = f(m.layer(16, 1, 512, 0, 0, 1e4), 1, n, n)
     assert 3.8 * (1 << 30) <= b - 8 * n * 512 and b <= 2048 * n + rest
     assert f(m.layer(16, 1, 512, 1024, 0, 1e4), 1, n, n) <= (1 << 30) + rest
+
+
+@pytest.mark.parametrize("ratio", [3, 12, 17, 32, 64, 128])
+def test_ratios_a_layer_or_a_tile_does_not_take(m, ratio):
+    """q heads per kv head: 1, 2, 4, 8 or 16."""
+    import ctypes
+    lay = m.layer(ratio, 1, 256, 0, 0, 1e4)
+    p = 1 << 20                                                       # a fake address: never dereferenced
+    read = (1, p, 4, 4, p, p, p, p, 1, p, p, p, p, p, 0, 0, p, 1 << 40, None)
+    assert m.lib.attn_train_backward(ctypes.byref(lay), *read) == 2
+    assert m.attn_train_backward_workspace_bytes(lay, 1, 4, 4) == 0
+    if ratio > 16:
+        prep = (1, p, 4) + (p,) * 5 + (None,) * 5 + (0,) + (None,) * 3 + (p, 1 << 40, None)
+        assert m.lib.kvq_train_prep_backward(ctypes.byref(lay), *prep) == 2
+        assert m.kvq_train_prep_backward_workspace_bytes(lay, 4) == 0
