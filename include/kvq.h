@@ -464,7 +464,8 @@ kvq_status attn_train_donor_forward_lse(const kvq_layer* layer, int32_t n_blocks
  * the last two over every row i that sees j and every q head of j's kv head.
  * Sums are fp32 in an order that depends on the arguments and the GPU alone (the
  * same call gives the same bits); P and dS enter the products as bf16 (dS from P
- * rounded to 11 bits).
+ * rounded to 11 bits, or to steps of 2^-39 where that is coarser; a P below 2^-126
+ * may count as 0).
  *
  *   max_block_rows   host upper bound of the rows of every block, 1 .. n_rows (a
  *                    longer block makes the layout invalid, below)

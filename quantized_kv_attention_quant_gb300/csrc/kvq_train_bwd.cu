@@ -24,7 +24,8 @@
 // prefix of 1024 and four branches of 256, 16 heads of 512 on one kv head: 168 us,
 // 0.44 of the measured bf16 rate (one by one: prep 20 us, scores 63, products 78,
 // finish 13);
-// on 4096 rows of a prefix of 2048 and eight branches 515 us, 0.63.
+// on 4096 rows of a prefix of 2048 and two branches of 1024 508 us, 0.63; on 8192
+// rows of twice those blocks, in several chunks, 1.84 ms, 0.70.
 //
 // A row tile is 128 (token, head) pairs of one block that share a kv head (128/G
 // tokens times G heads, pair r = token r / G, head r % G), a key tile 128 keys of
@@ -67,7 +68,8 @@ struct alignas(16) RowTile {
 // A key tile: keys row0 .. row0 + n - 1 (packed), tile idx of its block; the row
 // tiles that may see it are lo .. hi - 1 (a branch's: its own, from there on; with a
 // window, up to the last whose window reaches back to it.  The products' lists look
-// at each of them, for every item: without that end the listing grew with rows x rows).
+// at each of them, for every item: without that end the listing grew with rows x rows,
+// 19.3 instead of 11.5 ms on 524288 rows with a window of 512, 8 heads of 256).
 struct alignas(16) KeyTile { int row0, n, block, idx, lo, hi, pad[2]; };
 
 // The key tiles that either of two row tiles sees: prefix tiles a0 .., own-block
@@ -169,7 +171,7 @@ __host__ __device__ constexpr int prod_n(int D) { return D > 256 ? 256 : D; }
 // heads of 512 took 1016 us in chunks of 1024 (64 MB, within L2), 751 of 2048, 612
 // in one: longer sums for each output beat L2 hits.
 constexpr int kChunkTiles = 16384;
-// Least row tiles of a piece: 6 and 8 took 27.4 and 30.3 us on 900 rows in ragged
+// Least row tiles of a piece: 6 and 8 took 27.4 and 30.3 us on 739 rows in ragged
 // blocks, 54.8 and 53.5 on 2048 rows with a window of 512 (head_dim 256, 8 heads).
 constexpr int kMinPiece = 6;
 
