@@ -551,6 +551,214 @@ kvq_status kvq_train_prep_backward(const kvq_layer* layer, int32_t n_blocks, con
 size_t kvq_train_prep_backward_workspace_bytes(const kvq_layer* layer, int32_t n_rows);
 
 /*
+ * The paged 8-bit cache.  Instead of one contiguous cache per sequence, the
+ * rows of all sequences live in a pool of pages of page_tokens positions each;
+ * a sequence's row of a page table names the pages of its positions in order
+ * (position p is slot p % page_tokens of page tables[s][p / page_tokens]).
+ * Keys and values are held in 8 bits with one scale for each (page, kv head):
+ * a row reads as code * scale.
+ *
+ *   k_codes, v_codes    [n_pages][n_kv_heads][page_tokens][head_dim], one byte an
+ *                       element: int8 codes -127 .. 127 (KVQ_CODE_I8) or e4m3
+ *                       values (KVQ_CODE_E4M3)
+ *   k_scales, v_scales  fp32 [n_pages][n_kv_heads], 0 (all rows read as zeros)
+ *                       or from 2^-40 to 2^40
+ *
+ * Writing the rows of a call into a page (kvq_paged_append), per kv head, with
+ * a the largest magnitude of the call's rows in that page, in IEEE fp32:
+ *   s_new = a / 127 (int8) or a / 448 (e4m3); 0 when that is below 2^-40
+ *   s     = max(s_new, s_old) when the page already holds older positions of
+ *           the sequence (the call's first row in it is not at slot 0), else s_new
+ *   code  = round(x / s), half to even, within +-127 or +-448; 0 when s is 0
+ * and where s > s_old the older rows' codes become round(code * s_old / s): a
+ * row is within half a step of s of its value when it is written, and moves by
+ * at most another half step at each growth.  Slots behind the newest position
+ * are neither read nor kept.
+ *
+ * The tables, positions and row offsets live in device memory and are checked
+ * by the kernels: a position counts only below max_pages * page_tokens (and
+ * 2^24), and a table entry names a page only within 0 .. n_pages - 1.  Two
+ * sequences may share pages that both only read; a page that is written must
+ * belong to one sequence alone (kvq_pages_reserve sees to it).
+ */
+enum { KVQ_CODE_I8 = 0, KVQ_CODE_E4M3 = 1 };
+
+/* One layer's pages (host memory, read during the call). */
+typedef struct {
+  uint8_t* k_codes;      /* device, 16-byte aligned */
+  uint8_t* v_codes;
+  float* k_scales;       /* device */
+  float* v_scales;
+  int32_t n_pages;
+  int32_t page_tokens;   /* 16, 32, 64 or 128 */
+  int32_t n_kv_heads;    /* the layer's */
+  int32_t head_dim;
+  int32_t code_type;     /* KVQ_CODE_I8 or KVQ_CODE_E4M3 */
+} kvq_paged_cache;
+
+/*
+ * kvq_paged_append -- prep and quantize new K/V rows into their pages: the
+ * rows of kv_quant_append (k: norm, RoPE; v: un-scaled norm; K = V layers),
+ * quantized as above.  The layer's rot_signs must be NULL (KVQ_EUNSUPPORTED);
+ * its window does not matter.
+ *
+ *   tables         device int32[n_seqs][max_pages]
+ *   row_offsets, start_pos, n_rows, k_raw, v_raw, k_norm_w, kv_prepped
+ *                  as for kv_quant_append, with n_seqs and n_rows below 2^24; a
+ *                  sequence with a negative start_pos is idle
+ * Rows of idle sequences, past the table, or whose page the table does not
+ * name are not written (to kv_prepped neither).  All inputs must be finite.
+ */
+kvq_status kvq_paged_append(const kvq_layer* layer, const kvq_paged_cache* cache, const int32_t* tables,
+                            int32_t max_pages, int32_t n_seqs, const int32_t* row_offsets, const int32_t* start_pos,
+                            int32_t n_rows, const uint16_t* k_raw, const uint16_t* v_raw, const uint16_t* k_norm_w,
+                            uint16_t* kv_prepped, void* stream);
+
+/*
+ * kvq_paged_gather -- rows of the cache as bf16 values code * scale: row t of
+ * sequence s is its position start_pos[s] + (t - row_offsets[s]).
+ *
+ *   k_rows, v_rows   device bf16 [n_rows][n_kv_heads][head_dim] (16-byte aligned)
+ * Rows without a page (as above) are NaN.
+ */
+kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t* tables, int32_t max_pages, int32_t n_seqs,
+                            const int32_t* row_offsets, const int32_t* start_pos, int32_t n_rows, uint16_t* k_rows,
+                            uint16_t* v_rows, void* stream);
+
+/*
+ * attn_paged_decode -- attn_decode over pages: one query row per sequence
+ * attends positions max(0, p-window+1) .. p of its sequence, with
+ * k_hat_j, v_hat_j = code * scale.  The same call on the same GPU gives the
+ * same bits.
+ *
+ *   pos         device int32[n_seqs]; a negative position is an idle slot of the
+ *               batch, whose output is zeros
+ *   max_pos     host upper bound of pos[], 0 <= max_pos < 2^24 (sizes the
+ *               workspace and the shares of the work)
+ *   q_raw, q_norm_w, out, out_is_f32, q_prepped   as for attn_decode
+ *   workspace   at least attn_paged_decode_workspace_bytes(...) bytes; its first
+ *               4 bytes receive the status word
+ * A row whose position is above max_pos or past the table, or one of whose
+ * pages the table does not name, is NaN and sets KVQ_STATUS_SEQ_SKIPPED.
+ */
+kvq_status attn_paged_decode(const kvq_layer* layer, const kvq_paged_cache* cache, const int32_t* tables,
+                             int32_t max_pages, int32_t n_seqs, const int32_t* pos, int32_t max_pos,
+                             const uint16_t* q_raw, const uint16_t* q_norm_w, void* out, int32_t out_is_f32,
+                             uint16_t* q_prepped, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t attn_paged_decode_workspace_bytes(const kvq_layer* layer, const kvq_paged_cache* cache, int32_t n_seqs,
+                                         int32_t max_pos);
+
+/*
+ * attn_paged_prefill -- attn_prefill_chunk over pages: whole prompts (start_pos
+ * 0), later chunks of prompts and verify windows, after kvq_paged_append stored
+ * the rows' keys and values.  Arguments as for attn_prefill_chunk and
+ * attn_paged_decode; max_pos bounds the position of every row.  A sequence
+ * with a negative start_pos is idle: its rows are zeros.
+ */
+kvq_status attn_paged_prefill(const kvq_layer* layer, const kvq_paged_cache* cache, const int32_t* tables,
+                              int32_t max_pages, int32_t n_seqs, const int32_t* row_offsets, const int32_t* start_pos,
+                              int32_t n_rows, int32_t max_rows_per_seq, int32_t max_pos, const uint16_t* q_raw,
+                              const uint16_t* q_norm_w, void* out, int32_t out_is_f32, uint16_t* q_prepped,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+size_t attn_paged_prefill_workspace_bytes(const kvq_layer* layer, const kvq_paged_cache* cache, int32_t n_seqs,
+                                          int32_t n_rows, int32_t max_rows_per_seq, int32_t max_pos);
+
+/*
+ * The pool: which sequence holds which pages.  Its state is device memory
+ * alone, and every call below works on it in stream order without a host
+ * synchronization (all can be captured).  One pool may serve many layers'
+ * caches: a page number then means the same page of each.
+ *
+ * A page is free when refs is 0.  The calls keep: tables[s][i] for i below
+ * ceil(lens[s] / page_tokens) names a page, later entries are -1, and refs
+ * counts the table entries that name a page.  References that a program adds
+ * for itself (a cached prefix that no sequence holds) keep a page from being
+ * taken; kvq_pages_compact tells their new numbers.  An empty pool is tables
+ * of -1 and zero lens and refs.
+ */
+typedef struct {
+  int32_t* tables;       /* device int32[n_seqs][max_pages] */
+  int32_t* lens;         /* device int32[n_seqs]: tokens of each sequence */
+  int32_t* refs;         /* device int32[n_pages] */
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t n_pages;
+  int32_t page_tokens;   /* 16, 32, 64 or 128 */
+} kvq_page_pool;
+
+#define KVQ_MAX_PAGED_CACHES 128
+
+/*
+ * kvq_pages_free -- gives pages back: sequence seqs[i] keeps its first
+ * keep_tokens[i] tokens (0 below that; all it has where that is more), and the
+ * pages behind them lose a reference.  keep_tokens NULL frees whole
+ * sequences.  Numbers that are no sequence are passed over; of a sequence
+ * listed twice the first entry counts.
+ *
+ *   seqs          device int32[n]
+ *   keep_tokens   NULL or device int32[n]
+ */
+kvq_status kvq_pages_free(const kvq_page_pool* pool, const int32_t* seqs, const int32_t* keep_tokens, int32_t n,
+                          void* stream);
+
+/*
+ * kvq_pages_fork -- sequence children[i] becomes a copy of parents[i] by
+ * sharing all of its pages (one more reference each; nothing is copied).  The
+ * child must be empty.  Refused (granted[i] = 0, the child left as it was):
+ * numbers that are no sequence, a child that is not empty or was listed
+ * before, a parent that is a child of the same call.
+ *
+ *   parents, children   device int32[n]
+ *   granted             NULL or device int32[n]: 1, or 0 where refused
+ */
+kvq_status kvq_pages_fork(const kvq_page_pool* pool, const int32_t* parents, const int32_t* children, int32_t n,
+                          int32_t* granted, void* stream);
+
+/*
+ * kvq_pages_reserve -- room for n_new[s] more tokens of every sequence: new
+ * pages are taken and lens grows, so that the rows can be appended at
+ * start_pos.  A partly filled last page that the new rows would be written to
+ * and that has other references at the start of the call is first replaced by
+ * a copy of its own (codes and scales of every cache), in every sequence that
+ * shares it.
+ *
+ * Sequences are served in order, each taking the lowest-numbered pages that
+ * were free at the start of the call and are left (the copy's page first,
+ * then its new pages in order).  The first sequence that asks for more than is
+ * left, and every later one that asks for any, gets nothing (granted 0, its
+ * state unchanged), as does one whose tokens would pass max_pages pages or
+ * 2^24; a sequence that needs no page is granted always.
+ *
+ *   caches      host array of the n_caches caches whose pages this pool manages,
+ *               1 .. KVQ_MAX_PAGED_CACHES, each with the pool's n_pages and page_tokens
+ *   n_new       device int32[n_seqs] (negative: 0)
+ *   start_pos   device int32[n_seqs]: lens before the call
+ *   granted     device int32[n_seqs]
+ *   workspace   at least kvq_pages_workspace_bytes(pool) bytes
+ */
+kvq_status kvq_pages_reserve(const kvq_page_pool* pool, const kvq_paged_cache* caches, int32_t n_caches,
+                             const int32_t* n_new, int32_t* start_pos, int32_t* granted, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * kvq_pages_compact -- moves the fewest pages so that the pool's L live pages
+ * are pages 0 .. L - 1: the k-th live page numbered L or more goes to the k-th
+ * free page below L (ascending both), with its references; the tables follow.
+ *
+ *   page_map   NULL or device int32[n_pages]: each page's new number, -1 for a
+ *              page that was free
+ *   n_live     device int32[1]: L
+ *   others as for kvq_pages_reserve
+ */
+kvq_status kvq_pages_compact(const kvq_page_pool* pool, const kvq_paged_cache* caches, int32_t n_caches,
+                             int32_t* page_map, int32_t* n_live, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+size_t kvq_pages_workspace_bytes(const kvq_page_pool* pool);
+
+/*
  * attn_decode_static -- attn_decode without a caller-provided workspace, for
  * callers that cannot allocate device memory: code that only receives input
  * and output pointers from a host framework that owns every allocation (a
@@ -617,8 +825,9 @@ const char* kvq_status_string(kvq_status status);
 /*
  * kvq_profile_next_read -- profiling: the calling host thread's next call
  * that reads attention (attn_decode, attn_decode_append, attn_prefill_chunk,
- * attn_prefill_append, attn_train_forward and attn_train_donor_forward, with
- * or without _lse; not attn_mixed nor attn_train_backward) records
+ * attn_prefill_append, attn_paged_decode, attn_paged_prefill, attn_train_forward
+ * and attn_train_donor_forward, with or without _lse; not attn_mixed nor
+ * attn_train_backward) records
  * start_event on its stream right before launching its attention kernel and
  * stop_event right after, so that
  * cudaEventElapsedTime gives that kernel's time alone.  Both are

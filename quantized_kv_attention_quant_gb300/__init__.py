@@ -49,6 +49,23 @@ class KvqAttnGroup(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+KVQ_CODE_I8, KVQ_CODE_E4M3 = 0, 1
+KVQ_MAX_PAGED_CACHES = 128
+
+
+class KvqPagedCache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("code_type", ctypes.c_int32)]
+
+
+class KvqPagePool(ctypes.Structure):
+    _fields_ = [("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32)]
+
+
 class KvqError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"kvq status {status}: {message}")
@@ -106,6 +123,29 @@ def _load():
     lib.kvq_train_prep_backward_workspace_bytes.restype = sz
     lib.attn_train_workspace_bytes.argtypes = [lay, i32]
     lib.attn_train_workspace_bytes.restype = sz
+    pc, pool = ctypes.POINTER(KvqPagedCache), ctypes.POINTER(KvqPagePool)
+    lib.kvq_paged_append.argtypes = [lay, pc, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp]
+    lib.kvq_paged_append.restype = ctypes.c_int
+    lib.kvq_paged_gather.argtypes = [pc, vp, i32, i32, vp, vp, i32, vp, vp, vp]
+    lib.kvq_paged_gather.restype = ctypes.c_int
+    lib.attn_paged_decode.argtypes = [lay, pc, vp, i32, i32, vp, i32, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.attn_paged_decode.restype = ctypes.c_int
+    lib.attn_paged_decode_workspace_bytes.argtypes = [lay, pc, i32, i32]
+    lib.attn_paged_decode_workspace_bytes.restype = sz
+    lib.attn_paged_prefill.argtypes = [lay, pc, vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.attn_paged_prefill.restype = ctypes.c_int
+    lib.attn_paged_prefill_workspace_bytes.argtypes = [lay, pc, i32, i32, i32, i32]
+    lib.attn_paged_prefill_workspace_bytes.restype = sz
+    lib.kvq_pages_free.argtypes = [pool, vp, vp, i32, vp]
+    lib.kvq_pages_free.restype = ctypes.c_int
+    lib.kvq_pages_fork.argtypes = [pool, vp, vp, i32, vp, vp]
+    lib.kvq_pages_fork.restype = ctypes.c_int
+    lib.kvq_pages_reserve.argtypes = [pool, pc, i32, vp, vp, vp, vp, sz, vp]
+    lib.kvq_pages_reserve.restype = ctypes.c_int
+    lib.kvq_pages_compact.argtypes = [pool, pc, i32, vp, vp, vp, sz, vp]
+    lib.kvq_pages_compact.restype = ctypes.c_int
+    lib.kvq_pages_workspace_bytes.argtypes = [pool]
+    lib.kvq_pages_workspace_bytes.restype = sz
     lib.kvq_static_status.argtypes = [vp, vp]
     lib.kvq_static_status.restype = ctypes.c_int
     lib.kvq_selftest_wait_timeout.argtypes = [vp, ctypes.c_uint64, vp]
@@ -341,6 +381,93 @@ def kvq_train_prep_backward_workspace_bytes(layer: KvqLayer, n_rows) -> int:
 
 def attn_train_workspace_bytes(layer: KvqLayer, n_rows) -> int:
     return lib.attn_train_workspace_bytes(ctypes.byref(layer), n_rows)
+
+
+def paged_cache(k_codes, v_codes, k_scales, v_scales, n_pages, page_tokens, n_kv_heads, head_dim,
+                code_type) -> KvqPagedCache:
+    """One layer's 8-bit pages (see include/kvq.h, "The paged 8-bit cache")."""
+    return KvqPagedCache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), int(n_pages), int(page_tokens),
+                         int(n_kv_heads), int(head_dim), int(code_type))
+
+
+def paged_caches(caches):
+    """The caches whose pages one pool manages, as the pool calls take them."""
+    return (KvqPagedCache * len(caches))(*caches)
+
+
+def page_pool(tables, lens, refs, n_seqs, max_pages, n_pages, page_tokens) -> KvqPagePool:
+    """The state of a pool of pages (see include/kvq.h)."""
+    return KvqPagePool(_ptr(tables), _ptr(lens), _ptr(refs), int(n_seqs), int(max_pages), int(n_pages),
+                       int(page_tokens))
+
+
+def kvq_paged_append(layer: KvqLayer, cache: KvqPagedCache, tables, max_pages, n_seqs, row_offsets, start_pos, n_rows,
+                     k_raw, v_raw, k_norm_w, kv_prepped=None, stream=None):
+    """New K/V rows into 8-bit pages (see include/kvq.h)."""
+    _check(lib.kvq_paged_append(ctypes.byref(layer), ctypes.byref(cache), _ptr(tables), max_pages, n_seqs,
+                                _ptr(row_offsets), _ptr(start_pos), n_rows, _ptr(k_raw), _ptr(v_raw), _ptr(k_norm_w),
+                                _ptr(kv_prepped), _stream(stream)))
+
+
+def kvq_paged_gather(cache: KvqPagedCache, tables, max_pages, n_seqs, row_offsets, start_pos, n_rows, k_rows, v_rows,
+                     stream=None):
+    """Rows of the pages as bf16 values (see include/kvq.h)."""
+    _check(lib.kvq_paged_gather(ctypes.byref(cache), _ptr(tables), max_pages, n_seqs, _ptr(row_offsets),
+                                _ptr(start_pos), n_rows, _ptr(k_rows), _ptr(v_rows), _stream(stream)))
+
+
+def attn_paged_decode(layer: KvqLayer, cache: KvqPagedCache, tables, max_pages, n_seqs, pos, max_pos, q_raw, q_norm_w,
+                      out, out_is_f32, q_prepped, workspace, workspace_bytes, stream=None):
+    """attn_decode over 8-bit pages (see include/kvq.h)."""
+    _check(lib.attn_paged_decode(ctypes.byref(layer), ctypes.byref(cache), _ptr(tables), max_pages, n_seqs, _ptr(pos),
+                                 max_pos, _ptr(q_raw), _ptr(q_norm_w), _ptr(out), int(out_is_f32), _ptr(q_prepped),
+                                 _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def attn_paged_decode_workspace_bytes(layer: KvqLayer, cache: KvqPagedCache, n_seqs, max_pos) -> int:
+    return lib.attn_paged_decode_workspace_bytes(ctypes.byref(layer), ctypes.byref(cache), n_seqs, max_pos)
+
+
+def attn_paged_prefill(layer: KvqLayer, cache: KvqPagedCache, tables, max_pages, n_seqs, row_offsets, start_pos,
+                       n_rows, max_rows_per_seq, max_pos, q_raw, q_norm_w, out, out_is_f32, q_prepped, workspace,
+                       workspace_bytes, stream=None):
+    """attn_prefill_chunk over 8-bit pages (see include/kvq.h)."""
+    _check(lib.attn_paged_prefill(ctypes.byref(layer), ctypes.byref(cache), _ptr(tables), max_pages, n_seqs,
+                                  _ptr(row_offsets), _ptr(start_pos), n_rows, max_rows_per_seq, max_pos, _ptr(q_raw),
+                                  _ptr(q_norm_w), _ptr(out), int(out_is_f32), _ptr(q_prepped), _ptr(workspace),
+                                  workspace_bytes, _stream(stream)))
+
+
+def attn_paged_prefill_workspace_bytes(layer: KvqLayer, cache: KvqPagedCache, n_seqs, n_rows, max_rows_per_seq,
+                                       max_pos) -> int:
+    return lib.attn_paged_prefill_workspace_bytes(ctypes.byref(layer), ctypes.byref(cache), n_seqs, n_rows,
+                                                  max_rows_per_seq, max_pos)
+
+
+def kvq_pages_free(pool: KvqPagePool, seqs, keep_tokens, n, stream=None):
+    """Pages of sequences given back (see include/kvq.h)."""
+    _check(lib.kvq_pages_free(ctypes.byref(pool), _ptr(seqs), _ptr(keep_tokens), n, _stream(stream)))
+
+
+def kvq_pages_fork(pool: KvqPagePool, parents, children, n, granted=None, stream=None):
+    """Empty sequences made copies of others by sharing pages (see include/kvq.h)."""
+    _check(lib.kvq_pages_fork(ctypes.byref(pool), _ptr(parents), _ptr(children), n, _ptr(granted), _stream(stream)))
+
+
+def kvq_pages_reserve(pool: KvqPagePool, caches, n_new, start_pos, granted, workspace, workspace_bytes, stream=None):
+    """Room for n_new tokens of every sequence; caches as from paged_caches (see include/kvq.h)."""
+    _check(lib.kvq_pages_reserve(ctypes.byref(pool), caches, len(caches), _ptr(n_new), _ptr(start_pos), _ptr(granted),
+                                 _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def kvq_pages_compact(pool: KvqPagePool, caches, page_map, n_live, workspace, workspace_bytes, stream=None):
+    """Live pages moved to the lowest numbers; caches as from paged_caches (see include/kvq.h)."""
+    _check(lib.kvq_pages_compact(ctypes.byref(pool), caches, len(caches), _ptr(page_map), _ptr(n_live),
+                                 _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def kvq_pages_workspace_bytes(pool: KvqPagePool) -> int:
+    return lib.kvq_pages_workspace_bytes(ctypes.byref(pool))
 
 
 def attn_group(phase, seqs, n_seqs, row_offsets, pos, n_rows, max_pos, max_rows_per_seq, q_raw, out,

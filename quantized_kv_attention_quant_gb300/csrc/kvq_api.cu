@@ -12,6 +12,7 @@
 #include <tuple>
 
 #include "kvq_internal.h"
+#include "kvq_paged.h"
 #include "kvq_prompt.h"
 
 namespace {
@@ -1073,6 +1074,326 @@ kvq_status kvq_train_prep_backward(const kvq_layer* layer, int32_t n_blocks, con
   const cudaError_t e = kvq::launch_prep_bwd(a, f, workspace, num_sms_current(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kvq_train_prep_backward launch");
   return KVQ_OK;
+}
+
+// ---------------------------------------------------------------------------
+// The paged 8-bit cache: append, read-back, attention over pages, the pool.
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+bool page_tokens_ok(int32_t n) { return n == 16 || n == 32 || n == 64 || n == 128; }
+
+kvq_status check_paged_cache(const kvq_paged_cache* c, kvq::PagedArgs* out) {
+  if (!c) return fail(KVQ_EINVAL, "cache is NULL");
+  if (c->code_type != KVQ_CODE_I8 && c->code_type != KVQ_CODE_E4M3)
+    return fail(KVQ_EINVAL, "code_type %d is neither KVQ_CODE_I8 nor KVQ_CODE_E4M3", c->code_type);
+  if (!page_tokens_ok(c->page_tokens))
+    return fail(KVQ_EUNSUPPORTED, "page_tokens %d not in {16, 32, 64, 128}", c->page_tokens);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256 && c->head_dim != 512)
+    return fail(KVQ_EUNSUPPORTED, "head_dim %d not in {64, 128, 256, 512}", c->head_dim);
+  if (c->n_pages < 1) return fail(KVQ_EINVAL, "n_pages %d < 1", c->n_pages);
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 65535)
+    return fail(KVQ_EINVAL, "n_kv_heads %d not in [1, 65535]", c->n_kv_heads);
+  // a page's codes are addressed in 32 bits
+  if ((long long)c->n_kv_heads * c->page_tokens * c->head_dim > 0x7fffffffLL)
+    return fail(KVQ_EUNSUPPORTED, "a page of more than 2^31 codes");
+  REQUIRE_PTR(c->k_codes, "k_codes", 16);
+  REQUIRE_PTR(c->v_codes, "v_codes", 16);
+  REQUIRE_PTR(c->k_scales, "k_scales", 4);
+  REQUIRE_PTR(c->v_scales, "v_scales", 4);
+  *out = kvq::PagedArgs{};
+  out->k_codes = c->k_codes;
+  out->v_codes = c->v_codes;
+  out->k_scales = c->k_scales;
+  out->v_scales = c->v_scales;
+  out->n_pages = c->n_pages;
+  out->P = c->page_tokens;
+  out->p_shift = __builtin_ctz((unsigned)c->page_tokens);
+  out->e4m3 = c->code_type == KVQ_CODE_E4M3;
+  return KVQ_OK;
+}
+
+// A cache with the layer that reads or writes it.
+kvq_status check_paged(const kvq_layer* layer, const kvq_paged_cache* cache, kvq::LayerArgs* L, kvq::PagedArgs* pg) {
+  kvq_status st = check_layer(layer, L);
+  if (st != KVQ_OK) return st;
+  if (L->rot) return fail(KVQ_EUNSUPPORTED, "a paged cache keeps plain keys and values (rot_signs must be NULL)");
+  if ((st = check_paged_cache(cache, pg)) != KVQ_OK) return st;
+  if (cache->n_kv_heads != L->n_kv || cache->head_dim != L->D)
+    return fail(KVQ_EINVAL, "the cache's n_kv_heads (%d) and head_dim (%d) are not the layer's (%d, %d)",
+                cache->n_kv_heads, cache->head_dim, L->n_kv, L->D);
+  return KVQ_OK;
+}
+
+kvq_status check_paged_rows(const int32_t* tables, int32_t max_pages, int32_t n_seqs, const int32_t* row_offsets,
+                            const int32_t* start_pos, int32_t n_rows, int32_t max_pos, kvq::PagedArgs* pg,
+                            kvq::PagedRows* r) {
+  if (n_seqs == 0) return fail(KVQ_EINVAL, "n_rows > 0 with n_seqs == 0");
+  if (max_pages < 1) return fail(KVQ_EINVAL, "max_pages %d < 1", max_pages);
+  REQUIRE_PTR(tables, "tables", 4);
+  REQUIRE_PTR(start_pos, "pos/start_pos", 4);
+  pg->tables = tables;
+  pg->max_pages = max_pages;
+  pg->limit = (int)std::min<long long>((long long)max_pages << pg->p_shift, (long long)max_pos + 1);
+  *r = kvq::PagedRows{row_offsets, start_pos, n_seqs, n_rows};
+  return KVQ_OK;
+}
+
+kvq_status paged_read(bool window, const kvq_layer* layer, const kvq_paged_cache* cache, const int32_t* tables,
+                      int32_t max_pages, int32_t n_seqs, const int32_t* row_offsets, const int32_t* pos,
+                      int32_t n_rows, int32_t max_rows_per_seq, int32_t max_pos, const uint16_t* q_raw,
+                      const uint16_t* q_norm_w, void* out, int32_t out_is_f32, uint16_t* q_prepped, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  kvq::PagedReadArgs a = {};
+  kvq_status st = check_paged(layer, cache, &a.L, &a.pg);
+  if (st != KVQ_OK) return st;
+  if (n_seqs < 0 || n_rows < 0) return fail(KVQ_EINVAL, "negative n_seqs or n_rows");
+  if (!max_pos_ok(max_pos)) return fail(KVQ_EINVAL, "max_pos %d not in [0, 2^24)", max_pos);
+  if (n_rows == 0) return KVQ_OK;
+  if (n_rows >= (1 << 24) || n_seqs >= (1 << 24)) return fail(KVQ_EINVAL, "n_rows or n_seqs not below 2^24");
+  if ((st = check_paged_rows(tables, max_pages, n_seqs, row_offsets, pos, n_rows, max_pos, &a.pg, &a.r)) != KVQ_OK)
+    return st;
+  if (window) {
+    REQUIRE_PTR(row_offsets, "row_offsets", 4);
+    if (max_rows_per_seq < 1) return fail(KVQ_EINVAL, "max_rows_per_seq < 1");
+  }
+  REQUIRE_PTR(q_raw, "q_raw", 16);
+  REQUIRE_PTR(q_norm_w, "q_norm_w", 2);
+  if (out_is_f32 != 0 && out_is_f32 != 1) return fail(KVQ_EINVAL, "out_is_f32 must be 0 or 1");
+  REQUIRE_PTR(out, "out", out_is_f32 ? 4 : 2);
+  if (q_prepped && !aligned(q_prepped, 2)) return fail(KVQ_EINVAL, "q_prepped is not 2-byte aligned");
+  REQUIRE_PTR(workspace, "workspace", 256);
+  const int sms = num_sms_current();
+  const size_t need = kvq::paged_decode_ws_bytes(a.L, n_seqs, n_rows, max_pos, sms);
+  if (workspace_bytes < need)
+    return fail(KVQ_EWORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  a.q_raw = q_raw;
+  a.q_w = q_norm_w;
+  a.out = out;
+  a.out_f32 = out_is_f32;
+  a.q_prepped = q_prepped;
+  const kvq::RopeFreqs& f = rope_freqs(layer->rope_theta, a.L.D, a.L.rope_dims);
+  const cudaError_t e = kvq::launch_paged_decode(a, f, max_pos, workspace, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, window ? "attn_paged_prefill launch" : "attn_paged_decode launch");
+  return KVQ_OK;
+}
+
+kvq_status check_pool(const kvq_page_pool* pool, kvq::PoolArgs* p) {
+  if (!pool) return fail(KVQ_EINVAL, "pool is NULL");
+  if (!page_tokens_ok(pool->page_tokens))
+    return fail(KVQ_EUNSUPPORTED, "page_tokens %d not in {16, 32, 64, 128}", pool->page_tokens);
+  if (pool->n_seqs < 1 || pool->max_pages < 1 || pool->n_pages < 1)
+    return fail(KVQ_EINVAL, "n_seqs, max_pages and n_pages must be positive");
+  if ((long long)pool->n_seqs * pool->max_pages > 0x7fffffffLL)
+    return fail(KVQ_EUNSUPPORTED, "tables of more than 2^31 - 1 entries");
+  REQUIRE_PTR(pool->tables, "tables", 4);
+  REQUIRE_PTR(pool->lens, "lens", 4);
+  REQUIRE_PTR(pool->refs, "refs", 4);
+  p->tables = pool->tables;
+  p->lens = pool->lens;
+  p->refs = pool->refs;
+  p->n_seqs = pool->n_seqs;
+  p->max_pages = pool->max_pages;
+  p->n_pages = pool->n_pages;
+  p->P = pool->page_tokens;
+  p->p_shift = __builtin_ctz((unsigned)pool->page_tokens);
+  return KVQ_OK;
+}
+
+kvq_status check_pool_caches(const kvq_page_pool* pool, const kvq_paged_cache* caches, int32_t n_caches,
+                             kvq::PoolCaches* c) {
+  if (n_caches < 1 || n_caches > KVQ_MAX_PAGED_CACHES)
+    return fail(KVQ_EINVAL, "n_caches %d not in [1, %d]", n_caches, KVQ_MAX_PAGED_CACHES);
+  if (!caches) return fail(KVQ_EINVAL, "caches is NULL");
+  c->n = n_caches;
+  long long runs = 0;
+  for (int i = 0; i < n_caches; ++i) {
+    kvq::PagedArgs pg;
+    const kvq_status st = check_paged_cache(caches + i, &pg);
+    if (st != KVQ_OK) return st;
+    if (caches[i].page_tokens != pool->page_tokens || caches[i].n_pages != pool->n_pages)
+      return fail(KVQ_EINVAL, "cache %d has other pages (%d of %d tokens) than the pool (%d of %d)", i,
+                  caches[i].n_pages, caches[i].page_tokens, pool->n_pages, pool->page_tokens);
+    const long long bytes = (long long)caches[i].n_kv_heads * caches[i].page_tokens * caches[i].head_dim;
+    c->c[i] = {pg.k_codes, pg.v_codes, pg.k_scales, pg.v_scales, caches[i].n_kv_heads, (uint32_t)bytes};
+    runs += bytes / 4096 + 2;
+  }
+  if (runs > 0x7fffffffLL) return fail(KVQ_EUNSUPPORTED, "pages of all caches together are too large");
+  return KVQ_OK;
+}
+
+kvq_status check_pages_ws(const kvq::PoolArgs& p, const void* workspace, size_t workspace_bytes) {
+  REQUIRE_PTR(workspace, "workspace", 256);
+  const size_t need = kvq::pages_ws_bytes(p);
+  if (workspace_bytes < need)
+    return fail(KVQ_EWORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_paged_append(const kvq_layer* layer, const kvq_paged_cache* cache, const int32_t* tables,
+                            int32_t max_pages, int32_t n_seqs, const int32_t* row_offsets, const int32_t* start_pos,
+                            int32_t n_rows, const uint16_t* k_raw, const uint16_t* v_raw, const uint16_t* k_norm_w,
+                            uint16_t* kv_prepped, void* stream) {
+  kvq::PagedAppendArgs a = {};
+  kvq_status st = check_paged(layer, cache, &a.L, &a.pg);
+  if (st != KVQ_OK) return st;
+  if (n_seqs < 0 || n_rows < 0) return fail(KVQ_EINVAL, "negative n_seqs or n_rows");
+  if (n_rows == 0) return KVQ_OK;
+  if (n_rows >= (1 << 24) || n_seqs >= (1 << 24)) return fail(KVQ_EINVAL, "n_rows or n_seqs not below 2^24");
+  if ((st = check_paged_rows(tables, max_pages, n_seqs, row_offsets, start_pos, n_rows, (1 << 24) - 1, &a.pg,
+                             &a.r)) != KVQ_OK)
+    return st;
+  REQUIRE_PTR(row_offsets, "row_offsets", 4);
+  REQUIRE_PTR(k_raw, "k_raw", 16);
+  REQUIRE_PTR(k_norm_w, "k_norm_w", 2);
+  if (a.L.k_eq_v) {
+    if (v_raw) return fail(KVQ_EINVAL, "v_raw must be NULL when k_eq_v = 1");
+  } else {
+    REQUIRE_PTR(v_raw, "v_raw", 16);
+  }
+  if (kv_prepped && !aligned(kv_prepped, 2)) return fail(KVQ_EINVAL, "kv_prepped is not 2-byte aligned");
+  a.k_raw = k_raw;
+  a.v_raw = v_raw;
+  a.k_w = k_norm_w;
+  a.prepped = kv_prepped;
+  const kvq::RopeFreqs& f = rope_freqs(layer->rope_theta, a.L.D, a.L.rope_dims);
+  const cudaError_t e = kvq::launch_paged_append(a, f, num_sms_current(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_paged_append launch");
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t* tables, int32_t max_pages, int32_t n_seqs,
+                            const int32_t* row_offsets, const int32_t* start_pos, int32_t n_rows, uint16_t* k_rows,
+                            uint16_t* v_rows, void* stream) {
+  kvq::PagedGatherArgs a = {};
+  kvq_status st = check_paged_cache(cache, &a.pg);
+  if (st != KVQ_OK) return st;
+  if (n_seqs < 0 || n_rows < 0) return fail(KVQ_EINVAL, "negative n_seqs or n_rows");
+  if (n_rows == 0) return KVQ_OK;
+  if ((st = check_paged_rows(tables, max_pages, n_seqs, row_offsets, start_pos, n_rows, (1 << 24) - 1, &a.pg,
+                             &a.r)) != KVQ_OK)
+    return st;
+  REQUIRE_PTR(row_offsets, "row_offsets", 4);
+  REQUIRE_PTR(k_rows, "k_rows", 16);
+  REQUIRE_PTR(v_rows, "v_rows", 16);
+  a.n_kv = cache->n_kv_heads;
+  a.D = cache->head_dim;
+  a.k_rows = k_rows;
+  a.v_rows = v_rows;
+  const cudaError_t e = kvq::launch_paged_gather(a, num_sms_current(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_paged_gather launch");
+  return KVQ_OK;
+}
+
+kvq_status attn_paged_decode(const kvq_layer* layer, const kvq_paged_cache* cache, const int32_t* tables,
+                             int32_t max_pages, int32_t n_seqs, const int32_t* pos, int32_t max_pos,
+                             const uint16_t* q_raw, const uint16_t* q_norm_w, void* out, int32_t out_is_f32,
+                             uint16_t* q_prepped, void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_read(false, layer, cache, tables, max_pages, n_seqs, nullptr, pos, n_seqs, 1, max_pos, q_raw, q_norm_w,
+                    out, out_is_f32, q_prepped, workspace, workspace_bytes, stream);
+}
+
+size_t attn_paged_decode_workspace_bytes(const kvq_layer* layer, const kvq_paged_cache* cache, int32_t n_seqs,
+                                         int32_t max_pos) {
+  kvq::LayerArgs L;
+  kvq::PagedArgs pg;
+  if (check_paged(layer, cache, &L, &pg) != KVQ_OK || n_seqs < 0 || n_seqs >= (1 << 24) || !max_pos_ok(max_pos)) return 0;
+  return kvq::paged_decode_ws_bytes(L, n_seqs, n_seqs, max_pos, num_sms_current());
+}
+
+kvq_status attn_paged_prefill(const kvq_layer* layer, const kvq_paged_cache* cache, const int32_t* tables,
+                              int32_t max_pages, int32_t n_seqs, const int32_t* row_offsets, const int32_t* start_pos,
+                              int32_t n_rows, int32_t max_rows_per_seq, int32_t max_pos, const uint16_t* q_raw,
+                              const uint16_t* q_norm_w, void* out, int32_t out_is_f32, uint16_t* q_prepped,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_read(true, layer, cache, tables, max_pages, n_seqs, row_offsets, start_pos, n_rows, max_rows_per_seq,
+                    max_pos, q_raw, q_norm_w, out, out_is_f32, q_prepped, workspace, workspace_bytes, stream);
+}
+
+size_t attn_paged_prefill_workspace_bytes(const kvq_layer* layer, const kvq_paged_cache* cache, int32_t n_seqs,
+                                          int32_t n_rows, int32_t max_rows_per_seq, int32_t max_pos) {
+  kvq::LayerArgs L;
+  kvq::PagedArgs pg;
+  if (check_paged(layer, cache, &L, &pg) != KVQ_OK || n_seqs < 0 || n_seqs >= (1 << 24) || n_rows < 0 ||
+      n_rows >= (1 << 24) || max_rows_per_seq < 0 || !max_pos_ok(max_pos))
+    return 0;
+  return kvq::paged_decode_ws_bytes(L, n_seqs, n_rows, max_pos, num_sms_current());
+}
+
+kvq_status kvq_pages_free(const kvq_page_pool* pool, const int32_t* seqs, const int32_t* keep_tokens, int32_t n,
+                          void* stream) {
+  kvq::PoolArgs p;
+  const kvq_status st = check_pool(pool, &p);
+  if (st != KVQ_OK) return st;
+  if (n < 0) return fail(KVQ_EINVAL, "n %d < 0", n);
+  if (n == 0) return KVQ_OK;
+  REQUIRE_PTR(seqs, "seqs", 4);
+  if (keep_tokens && !aligned(keep_tokens, 4)) return fail(KVQ_EINVAL, "keep_tokens is not 4-byte aligned");
+  const cudaError_t e = kvq::launch_pages_free(p, seqs, keep_tokens, n, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_pages_free launch");
+  return KVQ_OK;
+}
+
+kvq_status kvq_pages_fork(const kvq_page_pool* pool, const int32_t* parents, const int32_t* children, int32_t n,
+                          int32_t* granted, void* stream) {
+  kvq::PoolArgs p;
+  const kvq_status st = check_pool(pool, &p);
+  if (st != KVQ_OK) return st;
+  if (n < 0) return fail(KVQ_EINVAL, "n %d < 0", n);
+  if (n == 0) return KVQ_OK;
+  REQUIRE_PTR(parents, "parents", 4);
+  REQUIRE_PTR(children, "children", 4);
+  if (granted && !aligned(granted, 4)) return fail(KVQ_EINVAL, "granted is not 4-byte aligned");
+  const cudaError_t e = kvq::launch_pages_fork(p, parents, children, n, granted, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_pages_fork launch");
+  return KVQ_OK;
+}
+
+kvq_status kvq_pages_reserve(const kvq_page_pool* pool, const kvq_paged_cache* caches, int32_t n_caches,
+                             const int32_t* n_new, int32_t* start_pos, int32_t* granted, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  kvq::PoolArgs p;
+  kvq::PoolCaches c;
+  kvq_status st = check_pool(pool, &p);
+  if (st != KVQ_OK) return st;
+  if ((st = check_pool_caches(pool, caches, n_caches, &c)) != KVQ_OK) return st;
+  REQUIRE_PTR(n_new, "n_new", 4);
+  REQUIRE_PTR(start_pos, "start_pos", 4);
+  REQUIRE_PTR(granted, "granted", 4);
+  if ((st = check_pages_ws(p, workspace, workspace_bytes)) != KVQ_OK) return st;
+  const cudaError_t e = kvq::launch_pages_reserve(p, c, n_new, start_pos, granted, workspace, num_sms_current(),
+                                                  static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_pages_reserve launch");
+  return KVQ_OK;
+}
+
+kvq_status kvq_pages_compact(const kvq_page_pool* pool, const kvq_paged_cache* caches, int32_t n_caches,
+                             int32_t* page_map, int32_t* n_live, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  kvq::PoolArgs p;
+  kvq::PoolCaches c;
+  kvq_status st = check_pool(pool, &p);
+  if (st != KVQ_OK) return st;
+  if ((st = check_pool_caches(pool, caches, n_caches, &c)) != KVQ_OK) return st;
+  if (page_map && !aligned(page_map, 4)) return fail(KVQ_EINVAL, "page_map is not 4-byte aligned");
+  REQUIRE_PTR(n_live, "n_live", 4);
+  if ((st = check_pages_ws(p, workspace, workspace_bytes)) != KVQ_OK) return st;
+  const cudaError_t e = kvq::launch_pages_compact(p, c, page_map, n_live, workspace, num_sms_current(),
+                                                  static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_pages_compact launch");
+  return KVQ_OK;
+}
+
+size_t kvq_pages_workspace_bytes(const kvq_page_pool* pool) {
+  kvq::PoolArgs p;
+  if (check_pool(pool, &p) != KVQ_OK) return 0;
+  return kvq::pages_ws_bytes(p);
 }
 
 kvq_status kvq_profile_next_read(void* start_event, void* stop_event) {

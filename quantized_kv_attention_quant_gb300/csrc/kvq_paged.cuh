@@ -1,0 +1,87 @@
+// Device helpers of the paged 8-bit cache kernels: where a position's row
+// lives, and codes as pairs of f16.
+//
+// A page holds page_tokens (P, a power of two from 16 to 128) consecutive
+// positions of one sequence for every kv head, K and V apart; each (page, kv
+// head) has one fp32 scale for its K codes and one for its V codes, and a row
+// reads as code * scale.  P >= 16, so 16 positions that start at a multiple
+// of 16 lie in one page, under one scale.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "kvq_common.cuh"
+#include "kvq_paged.h"
+
+namespace kvq {
+namespace {
+
+// A page's scale below this is stored as 0 (all codes 0); readers may take
+// log2 and the reciprocal of every other scale.
+constexpr float kSmallestScale = 9.094947017729282e-13f;   // 2^-40
+
+// The sequence of a packed row: the largest s with off[s] <= row.
+__device__ __forceinline__ int paged_seq_of(const PagedRows& r, int row) {
+  if (r.row_offsets == nullptr) return row;
+  int lo = 0, hi = r.n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(r.row_offsets + mid) <= row) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+struct SeqRows { int s, off, rows, start; };
+__device__ __forceinline__ SeqRows paged_seq_rows(const PagedRows& r, int s) {
+  if (r.row_offsets == nullptr) return {s, s, 1, __ldg(r.start + s)};
+  const int o = __ldg(r.row_offsets + s);
+  return {s, o, __ldg(r.row_offsets + s + 1) - o, __ldg(r.start + s)};
+}
+
+// The page of position p of sequence s, or -1 when the table names none.
+__device__ __forceinline__ int paged_page(const PagedArgs& pg, int s, int p) {
+  const int id = __ldg(pg.tables + (size_t)s * pg.max_pages + (p >> pg.p_shift));
+  return (unsigned)id < (unsigned)pg.n_pages ? id : -1;
+}
+
+// Two f16 values from two int8 codes (bytes of x with the sign bit flipped,
+// i.e. code + 128): the byte under the exponent of 1024 is 1024 + 128 + code,
+// and the subtraction of 1152 is exact.
+__device__ __forceinline__ uint32_t i8_pair(uint32_t flipped, uint32_t sel) {
+  const uint32_t h = prmt(flipped, 0x64646464u, sel);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
+  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)r.x | ((uint32_t)r.y << 16);
+}
+// Four codes (bytes 0..3 of w) as two pairs: (0, 1) and (2, 3).
+template <bool E4M3>
+__device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (E4M3) {
+    lo = e4m3_pair(w & 0xFFFFu);
+    hi = e4m3_pair(w >> 16);
+  } else {
+    w ^= 0x80808080u;
+    lo = i8_pair(w, 0x4140u);
+    hi = i8_pair(w, 0x4342u);
+  }
+}
+
+// x / s as a code byte, rounded half to even: fl32(x / s) for s > 0.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t encode_q(float q) {
+  if constexpr (E4M3) return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+  return (uint32_t)min(max(__float2int_rn(q), -127), 127) & 0xFFu;
+}
+template <bool E4M3>
+__device__ __forceinline__ float decode_byte(uint32_t b) {
+  if constexpr (E4M3) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3);
+    return __half2float(__half(h));
+  }
+  return (float)(int)(int8_t)b;
+}
+
+}  // namespace
+}  // namespace kvq

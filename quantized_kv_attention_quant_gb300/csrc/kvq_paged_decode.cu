@@ -1,0 +1,657 @@
+// attn_paged_decode (and few-row windows of attn_paged_prefill): attention of
+// single tokens over pages of 8-bit codes, on mma.sync.
+//
+// A unit is one kv head of a group of up to 16 / G rows of one sequence: its
+// 16 (token, q head) rows are the M rows of m16n8k16 (row r = token r / G, head
+// r % G), so a window of drafted rows reads its keys once.  The key tiles (64
+// positions) of all units, in (group, kv head, tile) order, are cut into equal
+// contiguous shares, one per CTA (long and short sequences mixed leave no CTA
+// idle); a share that holds part of a unit leaves its softmax state and sums
+// in the workspace and paged_merge_kernel joins the parts in order.
+//
+// Mathematics, per key j of a page with scales sk, sv and codes ck_j, cv_j:
+//   y_j = (q . ck_j) sk log2 e          (products of f16 q and codes are exact)
+//   t_j = y_j + log2 sv
+//   p_j = 2^(t_j - ref)                 rounded to f16 for the product with cv
+//   O += p_j cv_j,   l += p_j / sv      out = O / l
+// The value scale goes into the probability, not the codes, so both products
+// take codes as exact f16 values, and ref follows the largest t_j, so p_j <=
+// 2^15 whatever the scales are (renewed when a tile exceeds it by 2^8).  A
+// scale of 0 (all codes 0) counts as 1.
+//
+// A CTA is four warps.  Warp w scores keys 16 w .. of a tile over all dims.
+// With D >= 256, WD = D / 128 warps share the output: each keeps 128 dims of O
+// (64 registers) for the keys of all of them, and they exchange P and the row
+// maxima through shared memory, one barrier a tile: the next tile's scores are
+// formed before it, so it also publishes their maxima.  Codes come by 16-byte
+// asynchronous copies into a ring that no other thread reads (thread i's
+// copies are thread i's fragments: the order of dims inside an MMA's k range
+// and of output columns is free, so a lane takes 16 consecutive bytes), which
+// needs no barrier and has no bank conflicts; positions that no row of the
+// group sees are filled with zeros and never read.  Page numbers are looked up
+// a tile ahead of the copies.
+#include <algorithm>
+
+#include "kvq_paged.cuh"
+#include "kvq_paged_rows.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kPdThreads = 128;
+constexpr int kPdMinTiles = 2;           // shortest share of a CTA, key tiles
+
+template <int D>
+struct Pd {
+  static constexpr int WD = D >= 128 ? D / 128 : 1;     // warps that share a tile's output dims
+  static constexpr int TEAMS = 4 / WD;
+  static constexpr int DS = D / WD;                     // output dims per warp
+  static constexpr int NT = DS / 8;                     // 8-dim MMA columns per warp
+  static constexpr int VB = DS / 8;                     // V bytes of a key per lane (8 or 16)
+  static constexpr int KB = D / 64;                     // 16-byte K chunks of a key per lane
+  static constexpr int KS = D / 16;                     // MMA steps of QK
+  static constexpr bool QREG = D <= 128;                // q fragments in registers
+  // ring: K chunks [2 KB][128 threads][16 B], V chunks [4 WD][128][VB], scales [4 warps][2]
+  static constexpr int V_OFF = 2 * KB * kPdThreads * 16;
+  static constexpr int S_OFF = V_OFF + 4 * WD * kPdThreads * VB;
+  static constexpr int STAGE = S_OFF + 64;
+  static constexpr int NS = D <= 128 ? 4 : 3;           // stages
+  static constexpr int CPS = D == 64 ? 4 : D == 128 ? 3 : D == 256 ? 2 : 1;   // CTAs per SM
+  static constexpr int RING = NS * STAGE;
+  static constexpr int Q_OFF = RING;                    // q fragments [KS][32] x 16 B
+  static constexpr int P_OFF = Q_OFF + (QREG ? 0 : KS * 512);      // P fragments [2][4 warps][32] x 16 B
+  static constexpr int M_OFF = P_OFF + (WD > 1 ? 4096 : 0);        // row maxima [2][4 warps][16]
+  static constexpr int BYTES = M_OFF + 512;
+  static constexpr int OSTR = D + 4;                    // floats of a merged row (a row's start moves by 4 banks)
+  static_assert(TEAMS * 16 * OSTR * 4 + 4 * 16 * 8 <= RING, "the merge of a CTA's warps reuses the ring");
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// The shares of a call: T tiles over nc CTAs, CTA c taking [T c / nc, T (c+1) / nc).
+struct PdShares {
+  long long T;
+  int nc;
+  __device__ long long begin(int c) const { return T * c / nc; }
+  __device__ int cta_of(long long x) const { return (int)(((x + 1) * nc - 1) / T); }
+};
+__device__ __forceinline__ PdShares pd_shares(long long T, int ctas) {
+  return {T, (int)max(1ll, min((long long)ctas, T / kPdMinTiles))};
+}
+
+// part_o [2 ctas][16][D], part_ml [2 ctas][2][16]: slot 2 c of CTA c is the
+// piece that begins its share, 2 c + 1 the piece that ends it.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kPdThreads, Pd<D>::CPS)
+paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, const uint16_t* q16,
+                    const long long* prefix, float* part_o, float* part_ml, uint32_t* status) {
+  using S = Pd<D>;
+  constexpr int WD = S::WD, KB = S::KB, NT = S::NT, VB = S::VB, NS = S::NS, KS = S::KS;
+  constexpr float L2E = 1.4426950408889634f;
+  constexpr float kSlack = 8.f;      // how far a tile may exceed ref, log2
+  constexpr float kTop = 7.f;        // p of a key at ref is 2^kTop
+  extern __shared__ __align__(128) uint8_t sm[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rr = lane >> 2, cc = lane & 3;
+  const int team = warp / WD, wd = warp % WD;
+  const int G = a.L.G, n_kv = a.L.n_kv, P = a.pg.P, sh = a.pg.p_shift, W = a.L.window;
+  const uint32_t sbase = smem_u32(sm);
+  pdl_launch();
+  pdl_wait();                                             // q16, the plan and the status word are written
+  const PdShares shares = pd_shares(__ldg(prefix + n_groups) * n_kv, gridDim.x);
+  if (shares.T == 0 || (int)blockIdx.x >= shares.nc) return;
+  long long x = shares.begin(blockIdx.x);
+  const long long x_begin = x, x_end = shares.begin(blockIdx.x + 1);
+
+  while (x < x_end) {
+    // ---- the unit of tile x: group u, kv head h, tiles [t_a, t_b) of its `tiles` ----
+    int u;
+    {
+      int lo = 0, hi = n_groups - 1;                      // the largest u with prefix[u] n_kv <= x
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(prefix + mid) * n_kv <= x) lo = mid; else hi = mid - 1;
+      }
+      u = lo;
+    }
+    const PagedGroup g = paged_group(a.r, a.pg, W, TG, u);
+    const long long in_u = x - __ldg(prefix + u) * n_kv;
+    const int h = (int)(in_u / g.tiles), t_a = (int)(in_u - (long long)h * g.tiles);
+    const int n = (int)min((long long)(g.tiles - t_a), x_end - x);
+    const int k0 = g.kt0 + 64 * t_a;                      // first position of the piece
+    const int rows = g.nt * G;
+
+    // ---- page numbers: lane i < 4 looks up the page of 16 positions i of a tile ----
+    bool bad = false;
+    const int32_t* table = a.pg.tables + (size_t)g.s * a.pg.max_pages;
+    auto look_up = [&](int t) {                           // raw entry, -2: no row sees it
+      int id = -2;
+      const int key = k0 + 64 * t + 16 * lane;
+      if (lane < 4 && t < n && key <= g.hi && key + 15 >= g.lo) id = __ldg(table + (key >> sh));
+      return id;
+    };
+    auto checked = [&](int id) {
+      if (id == -2) return -1;
+      if ((unsigned)id < (unsigned)a.pg.n_pages) return id;
+      bad = true;
+      return -1;
+    };
+    // ---- copies of group j: K and the scales of tile j, V of tile j - 1 ----
+    auto issue = [&](int j, int pid_k, int pid_v) {
+      const uint32_t st = sbase + (j % NS) * S::STAGE;
+      if (j < n) {
+        const int id = __shfl_sync(0xffffffffu, pid_k, warp);
+        const size_t ph = (size_t)max(id, 0) * n_kv + h;
+        const int key0 = k0 + 64 * j + 16 * warp;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int key = key0 + 8 * jj + rr;
+          const uint32_t bytes = id >= 0 && key >= g.lo && key <= g.hi ? 16u : 0u;
+          const uint8_t* src = a.pg.k_codes + ((ph << sh) + (key & (P - 1))) * D + 16 * cc;
+#pragma unroll
+          for (int b = 0; b < KB; ++b) cp16(st + ((jj * KB + b) * kPdThreads + tid) * 16, src + 64 * b, bytes);
+        }
+        if (lane < 2)
+          cp4(st + S::S_OFF + warp * 8 + lane * 4, (lane == 0 ? a.pg.k_scales : a.pg.v_scales) + ph, id >= 0 ? 4u : 0u);
+      }
+      if (j >= 1 && j <= n) {
+#pragma unroll
+        for (int kb = 0; kb < WD; ++kb) {
+          const int sub = team * WD + kb;
+          const int id = __shfl_sync(0xffffffffu, pid_v, sub);
+          const size_t ph = (size_t)max(id, 0) * n_kv + h;
+          const int key0 = k0 + 64 * (j - 1) + 16 * sub + 2 * cc;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {                   // keys 2c, 2c+1, 2c+8, 2c+9
+            const int key = key0 + (e & 1) + 8 * (e >> 1);
+            const uint32_t bytes = id >= 0 && key >= g.lo && key <= g.hi ? (uint32_t)VB : 0u;
+            const uint8_t* src = a.pg.v_codes + ((ph << sh) + (key & (P - 1))) * D + wd * S::DS + VB * rr;
+            const uint32_t dst = st + S::V_OFF + ((kb * 4 + e) * kPdThreads + tid) * VB;
+            if constexpr (VB == 16) cp16(dst, src, bytes); else cp8(dst, src, bytes);
+          }
+        }
+      }
+      cp_commit();
+    };
+    // page numbers of the tile that a group's K needs, of the one before, and of the next
+    int pid_prev = -1, pid_cur = checked(look_up(0)), raw_next = look_up(1);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      issue(j, pid_cur, pid_prev);
+      pid_prev = pid_cur;
+      pid_cur = checked(raw_next);
+      raw_next = look_up(j + 2);
+    }
+
+    // ---- q fragments of the unit: step 4 b + t takes dims 64 b + 16 c + 4 t .. +3 of lane column c ----
+    uint32_t qf[S::QREG ? KS : 1][4];
+    {
+      auto q_row = [&](int r) {
+        return q16 + ((size_t)(g.row0 + r / G) * a.L.n_q + h * G + r % G) * D;
+      };
+      if constexpr (S::QREG) {
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          uint4 v[2][2] = {};
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (rr + 8 * e < rows) {
+              const uint4* src = reinterpret_cast<const uint4*>(q_row(rr + 8 * e) + 64 * b + 16 * cc);
+              v[e][0] = src[0];
+              v[e][1] = src[1];
+            }
+          const uint32_t* w0 = reinterpret_cast<const uint32_t*>(v[0]);
+          const uint32_t* w1 = reinterpret_cast<const uint32_t*>(v[1]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            qf[4 * b + t][0] = w0[2 * t];
+            qf[4 * b + t][1] = w1[2 * t];
+            qf[4 * b + t][2] = w0[2 * t + 1];
+            qf[4 * b + t][3] = w1[2 * t + 1];
+          }
+        }
+      } else {
+        uint4* qs = reinterpret_cast<uint4*>(sm + S::Q_OFF);
+        for (int i = warp; i < KS; i += 4) {
+          const int d = 64 * (i >> 2) + 16 * cc + 4 * (i & 3);
+          uint2 v0 = {0, 0}, v1 = {0, 0};
+          if (rr < rows) v0 = *reinterpret_cast<const uint2*>(q_row(rr) + d);
+          if (rr + 8 < rows) v1 = *reinterpret_cast<const uint2*>(q_row(rr + 8) + d);
+          qs[i * 32 + lane] = make_uint4(v0.x, v1.x, v0.y, v1.y);
+        }
+        __syncthreads();
+      }
+    }
+
+    // what the thread's two rows see
+    const int pr0 = g.p0 + min(rr / G, g.nt - 1), pr1 = g.p0 + min((rr + 8) / G, g.nt - 1);
+    const int lo0 = W > 0 ? pr0 - W + 1 : 0, lo1 = W > 0 ? pr1 - W + 1 : 0;
+    const int p_last = g.hi, lo_last = W > 0 ? g.hi - W + 1 : 0;
+
+    float O[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) O[i][e] = 0.f;
+    float ref0 = -INFINITY, ref1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float sc[2][4];                                       // scores, then t = y + log2 sv
+
+    auto qk = [&](int j) {                                // raw scores of tile j into sc
+      constexpr int CH = D >= 256 ? 2 : 1;                // accumulation chains per 8 keys
+      float acc[CH][2][4];
+      const uint8_t* st = sm + (j % NS) * S::STAGE;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[c][e][i] = 0.f;
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        const uint4 ka = lds128(st + (b * kPdThreads + tid) * 16);
+        const uint4 kb = lds128(st + ((KB + b) * kPdThreads + tid) * 16);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          uint32_t q[4];
+          if constexpr (S::QREG) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = qf[4 * b + t][i];
+          } else {
+            const uint4 v = lds128(sm + S::Q_OFF + ((4 * b + t) * 32 + lane) * 16);
+            q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
+          }
+          uint32_t b0, b1;
+          codes_to_h2<E4M3>(wa[t], b0, b1);
+          mma_f16(acc[t % CH][0], q, b0, b1);
+          codes_to_h2<E4M3>(wb[t], b0, b1);
+          mma_f16(acc[t % CH][1], q, b0, b1);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sc[e][i] = acc[0][e][i];
+          if constexpr (CH == 2) sc[e][i] += acc[CH - 1][e][i];
+        }
+    };
+    // scores of tile j -> t, masked; the maxima of the thread's rows over the warp's 16 keys
+    float isv = 1.f;
+    auto scale_mask = [&](int j, float& m0, float& m1) {
+      const float2 s2 = *reinterpret_cast<const float2*>(sm + (j % NS) * S::STAGE + S::S_OFF + warp * 8);
+      const float sk = s2.x * L2E, sv = s2.y > 0.f ? s2.y : 1.f;
+      const float lsv = __log2f(sv);
+      isv = __fdividef(1.f, sv);
+      const int key0 = k0 + 64 * j + 16 * warp;
+      if (key0 >= lo_last && key0 + 15 <= g.p0) {         // every row sees all 16 keys
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[e][i] = fmaf(sc[e][i], sk, lsv);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = key0 + 8 * e + 2 * cc + (i & 1);
+            const bool see = (i >> 1) ? key <= pr1 && key >= lo1 : key <= pr0 && key >= lo0;
+            sc[e][i] = see ? fmaf(sc[e][i], sk, lsv) : -INFINITY;
+          }
+      }
+      m0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      m1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+#pragma unroll
+      for (int m = 1; m <= 2; m <<= 1) {
+        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, m));
+        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, m));
+      }
+    };
+    float* mbuf = reinterpret_cast<float*>(sm + S::M_OFF);
+    auto post_max = [&](int j, float m0, float m1) {
+      if (cc == 0) {
+        mbuf[((j & 1) * 4 + warp) * 16 + rr] = m0;
+        mbuf[((j & 1) * 4 + warp) * 16 + rr + 8] = m1;
+      }
+    };
+    auto team_sync = [&]() {
+      if constexpr (WD == 4) __syncthreads();
+      else if constexpr (WD == 2) named_bar(1 + team, 64);
+      else __syncwarp();
+    };
+
+    // ---- tile by tile ----
+    cp_wait<NS - 1>();                                    // group 0
+    __syncwarp();
+    qk(0);
+    float m0, m1;
+    scale_mask(0, m0, m1);
+    if constexpr (WD > 1) {
+      post_max(0, m0, m1);
+      team_sync();
+    }
+    (void)p_last;
+    for (int j = 0; j < n; ++j) {
+      if constexpr (WD > 1) {
+#pragma unroll
+        for (int w = 0; w < WD; ++w) {
+          m0 = fmaxf(m0, mbuf[((j & 1) * 4 + team * WD + w) * 16 + rr]);
+          m1 = fmaxf(m1, mbuf[((j & 1) * 4 + team * WD + w) * 16 + rr + 8]);
+        }
+      }
+      // a renewed reference: what was summed so far is rescaled
+      const bool new0 = m0 > ref0 + kSlack || (ref0 == -INFINITY && m0 > -INFINITY);
+      const bool new1 = m1 > ref1 + kSlack || (ref1 == -INFINITY && m1 > -INFINITY);
+      if (__any_sync(0xffffffffu, new0 || new1)) {
+        const float a0 = new0 ? ex2(ref0 - m0) : 1.f, a1 = new1 ? ex2(ref1 - m1) : 1.f;
+        if (new0) ref0 = m0;
+        if (new1) ref1 = m1;
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          O[i][0] *= a0;
+          O[i][1] *= a0;
+          O[i][2] *= a1;
+          O[i][3] *= a1;
+        }
+      }
+      uint32_t pf[4];
+      {
+        const float r0 = ref0 == -INFINITY ? 0.f : ref0 - kTop, r1 = ref1 == -INFINITY ? 0.f : ref1 - kTop;
+        float p[2][4];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          p[e][0] = ex2(sc[e][0] - r0);
+          p[e][1] = ex2(sc[e][1] - r0);
+          p[e][2] = ex2(sc[e][2] - r1);
+          p[e][3] = ex2(sc[e][3] - r1);
+          s0 += p[e][0] + p[e][1];
+          s1 += p[e][2] + p[e][3];
+          pf[2 * e] = pack_h2(p[e][0], p[e][1]);
+          pf[2 * e + 1] = pack_h2(p[e][2], p[e][3]);
+        }
+        l0 = fmaf(s0, isv, l0);
+        l1 = fmaf(s1, isv, l1);
+      }
+      if constexpr (WD > 1)
+        *reinterpret_cast<uint4*>(sm + S::P_OFF + ((j & 1) * 4 + warp) * 512 + lane * 16) =
+            make_uint4(pf[0], pf[1], pf[2], pf[3]);
+      // the stage of tile j's K and scales (and V of j - 1) is free: the next group's copies
+      __syncwarp();
+      issue(j + NS, pid_cur, pid_prev);
+      pid_prev = pid_cur;
+      pid_cur = checked(raw_next);
+      raw_next = look_up(j + NS + 2);
+      cp_wait<NS - 1>();                                  // group j + 1: K of the next tile, V of this one
+      __syncwarp();
+      if (j + 1 < n) {
+        qk(j + 1);
+        scale_mask(j + 1, m0, m1);
+        if constexpr (WD > 1) post_max(j + 1, m0, m1);
+      }
+      if constexpr (WD > 1) team_sync();
+      const uint8_t* st = sm + ((j + 1) % NS) * S::STAGE + S::V_OFF;
+#pragma unroll
+      for (int kb = 0; kb < WD; ++kb) {
+        if constexpr (WD > 1) {
+          const uint4 v = lds128(sm + S::P_OFF + ((j & 1) * 4 + team * WD + kb) * 512 + lane * 16);
+          pf[0] = v.x; pf[1] = v.y; pf[2] = v.z; pf[3] = v.w;
+        }
+        uint32_t vw[4][VB / 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint8_t* src = st + ((kb * 4 + e) * kPdThreads + tid) * VB;
+          if constexpr (VB == 16) {
+            const uint4 v = lds128(src);
+            vw[e][0] = v.x; vw[e][1] = v.y; vw[e][2] = v.z; vw[e][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            vw[e][0] = v.x; vw[e][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < VB / 4; ++w) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {                // dims 4 w + 2 hf, + 1 of the lane's
+            const uint32_t sel = hf ? 0x7362u : 0x5140u;  // bytes (key, next key) of two dims
+            uint32_t a0, a1, b0, b1;
+            codes_to_h2<E4M3>(prmt(vw[0][w], vw[1][w], sel), a0, a1);
+            codes_to_h2<E4M3>(prmt(vw[2][w], vw[3][w], sel), b0, b1);
+            mma_f16(O[4 * w + 2 * hf], pf, a0, b0);
+            mma_f16(O[4 * w + 2 * hf + 1], pf, a1, b1);
+          }
+        }
+      }
+    }
+
+    // ---- join the warps, in shared memory ----
+    cp_wait<0>();
+    bad = __syncthreads_or(bad);
+    if (bad && tid == 0) flag_error(status, KVQ_DEV_BADSEQ);
+#pragma unroll
+    for (int m = 1; m <= 2; m <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, m);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, m);
+    }
+    float* ob = reinterpret_cast<float*>(sm);             // [TEAMS][16][OSTR]
+    float* lb = ob + S::TEAMS * 16 * S::OSTR;             // [4 warps][16] l, then [4 warps][16] ref
+    if (cc == 0) {
+      lb[warp * 16 + rr] = l0;
+      lb[warp * 16 + rr + 8] = l1;
+      lb[64 + warp * 16 + rr] = ref0;
+      lb[64 + warp * 16 + rr + 8] = ref1;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (rr + 8 * e < rows) {
+#pragma unroll
+        for (int cn = 0; cn < 2; ++cn) {
+          float* dst = ob + (team * 16 + rr + 8 * e) * S::OSTR + wd * S::DS + VB * (2 * cc + cn);
+#pragma unroll
+          for (int i = 0; i < NT; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(O[i][2 * e + cn], O[i + 1][2 * e + cn],
+                                                              O[i + 2][2 * e + cn], O[i + 3][2 * e + cn]);
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = n == g.tiles;
+    const int slot = 2 * blockIdx.x + (x == x_begin ? 0 : 1);
+    for (int i = tid; i < rows * (D / 4); i += kPdThreads) {
+      const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+      float M = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, lb[64 + w * 16 + r]);
+      float4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < S::TEAMS; ++t) {
+        const float rf = lb[64 + t * WD * 16 + r], f = rf == -INFINITY ? 0.f : ex2(rf - M);
+        const float4 v = *reinterpret_cast<const float4*>(ob + (t * 16 + r) * S::OSTR + d);
+        o.x = fmaf(v.x, f, o.x);
+        o.y = fmaf(v.y, f, o.y);
+        o.z = fmaf(v.z, f, o.z);
+        o.w = fmaf(v.w, f, o.w);
+#pragma unroll
+        for (int w = 0; w < WD; ++w) l = fmaf(lb[(t * WD + w) * 16 + r], f, l);
+      }
+      if (bad) l = __int_as_float(0x7FC00000);
+      if (whole) {
+        const float inv = 1.f / l;
+        const size_t at = ((size_t)(g.row0 + r / G) * a.L.n_q + h * G + r % G) * D + d;
+        const float w[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (a.out_f32) reinterpret_cast<float*>(a.out)[at + e] = w[e];
+          else reinterpret_cast<uint16_t*>(a.out)[at + e] = f_to_bf16_rn(w[e]);
+        }
+      } else {
+        *reinterpret_cast<float4*>(part_o + ((size_t)slot * 16 + r) * D + d) = o;
+        if (d == 0) {
+          part_ml[(size_t)slot * 32 + r] = M;
+          part_ml[(size_t)slot * 32 + 16 + r] = l;
+        }
+      }
+    }
+    __syncthreads();                                      // the ring is free for the next piece
+    x += n;
+  }
+}
+
+// The units that were cut: one block per (unit, 512 outputs of it), each
+// thread four dims of one row over the unit's pieces in order.
+template <int D>
+__global__ void __launch_bounds__(128)
+paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, const int ctas, const long long* prefix,
+                   const float* part_o, const float* part_ml) {
+  pdl_launch();
+  pdl_wait();
+  const int n_kv = a.L.n_kv, G = a.L.G;
+  const int u = blockIdx.x / n_kv, h = blockIdx.x - u * n_kv;
+  const long long T = __ldg(prefix + n_groups) * n_kv;
+  const long long pu = __ldg(prefix + u);
+  const int tiles = (int)(__ldg(prefix + u + 1) - pu);
+  if (tiles == 0) return;
+  const PdShares shares = pd_shares(T, ctas);
+  const long long x0 = pu * n_kv + (long long)h * tiles, x1 = x0 + tiles;
+  const int c0 = shares.cta_of(x0), c1 = shares.cta_of(x1 - 1);
+  if (c0 == c1) return;                                   // one CTA had it whole
+  const PagedGroup g = paged_group(a.r, a.pg, a.L.window, TG, u);
+  const int i = blockIdx.y * 128 + threadIdx.x;
+  if (i >= g.nt * G * (D / 4)) return;
+  const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+  const int first = 2 * c0 + (shares.begin(c0) == x0 ? 0 : 1);
+  float M = -INFINITY;
+  for (int c = c0; c <= c1; ++c) {
+    const int slot = c == c0 ? first : 2 * c;
+    M = fmaxf(M, __ldg(part_ml + (size_t)slot * 32 + r));
+  }
+  float l = 0.f;
+  float4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const int slot = c == c0 ? first : 2 * c;
+    const float m = __ldg(part_ml + (size_t)slot * 32 + r), lp = __ldg(part_ml + (size_t)slot * 32 + 16 + r);
+    const float4 v = __ldg(reinterpret_cast<const float4*>(part_o + ((size_t)slot * 16 + r) * D + d));
+    const float f = m == -INFINITY ? 0.f : ex2(m - M);
+    l = fmaf(lp, f, l);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
+  }
+  const float inv = 1.f / l;
+  const size_t at = ((size_t)(g.row0 + r / G) * a.L.n_q + h * G + r % G) * D + d;
+  const float w[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (a.out_f32) reinterpret_cast<float*>(a.out)[at + e] = w[e];
+    else reinterpret_cast<uint16_t*>(a.out)[at + e] = f_to_bf16_rn(w[e]);
+  }
+}
+
+int pd_cps(int D) { return D == 64 ? Pd<64>::CPS : D == 128 ? Pd<128>::CPS : D == 256 ? Pd<256>::CPS : Pd<512>::CPS; }
+
+// rows of a group, groups and CTAs of a call
+struct PdPlan { int TG, n_groups, max_tiles, ctas; };
+PdPlan pd_plan(const LayerArgs& L, const PagedRows& r, int max_pos, int num_sms) {
+  PdPlan p;
+  p.TG = r.row_offsets ? std::max(1, 16 / L.G) : 1;
+  p.n_groups = paged_groups(r, p.TG);
+  // a group sees at most max_pos + 1 positions, or its window's
+  long long keys = (long long)max_pos + 1;
+  if (L.window > 0) keys = std::min<long long>(keys, (long long)L.window + p.TG - 1);
+  p.max_tiles = (int)((keys + 62) / 64 + 1);
+  if (keys == (long long)max_pos + 1) p.max_tiles = (int)((keys + 63) / 64);   // they begin at 0
+  const long long most = (long long)p.n_groups * L.n_kv * p.max_tiles;
+  p.ctas = (int)std::max(1ll, std::min<long long>((long long)num_sms * pd_cps(L.D), most));
+  return p;
+}
+
+// status (256 B), q16, prefix, part_o, part_ml
+struct PdWs { size_t q16, prefix, part_o, part_ml, total; };
+PdWs pd_ws(const LayerArgs& L, const PagedRows& r, const PdPlan& p) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  PdWs w;
+  w.q16 = 256;
+  w.prefix = up(w.q16 + (size_t)r.n_rows * L.n_q * L.D * 2);
+  w.part_o = up(w.prefix + ((size_t)p.n_groups + 1) * 8);
+  w.part_ml = up(w.part_o + (size_t)p.ctas * 2 * 16 * L.D * 4);
+  w.total = up(w.part_ml + (size_t)p.ctas * 2 * 32 * 4);
+  return w;
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, void* ws, int num_sms, cudaStream_t st) {
+  using S = Pd<D>;
+  const PdPlan p = pd_plan(a.L, a.r, max_pos, num_sms);
+  const PdWs w = pd_ws(a.L, a.r, p);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  uint32_t* status = reinterpret_cast<uint32_t*>(b);
+  uint16_t* q16 = reinterpret_cast<uint16_t*>(b + w.q16);
+  long long* prefix = reinterpret_cast<long long*>(b + w.prefix);
+  float* part_o = reinterpret_cast<float*>(b + w.part_o);
+  float* part_ml = reinterpret_cast<float*>(b + w.part_ml);
+  cudaError_t e = launch_paged_prep<D>(a, f, p.TG, p.n_groups, q16, prefix, status, status + 1, st);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(paged_decode_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+  if (e != cudaSuccess) return e;
+  if ((e = prof_before(st)) != cudaSuccess) return e;
+  e = launch_pdl(paged_decode_kernel<D, E4M3>, dim3(p.ctas), dim3(kPdThreads), S::BYTES, st, a, p.TG, p.n_groups, q16,
+                 prefix, part_o, part_ml, status);
+  if (e != cudaSuccess) return e;
+  if ((e = prof_after(st)) != cudaSuccess) return e;
+  if (p.max_tiles < 2) return cudaSuccess;                // a single tile is never cut
+  const long long units = (long long)p.n_groups * a.L.n_kv;
+  if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int slices = (p.TG * a.L.G * (D / 4) + 127) / 128;
+  return launch_pdl(paged_merge_kernel<D>, dim3((unsigned)units, slices), dim3(128), 0, st, a, p.TG, p.n_groups, p.ctas,
+                    prefix, part_o, part_ml);
+}
+
+template <int D>
+cudaError_t launch_d(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, void* ws, int num_sms, cudaStream_t st) {
+  return a.pg.e4m3 ? launch_t<D, true>(a, f, max_pos, ws, num_sms, st)
+                   : launch_t<D, false>(a, f, max_pos, ws, num_sms, st);
+}
+
+}  // namespace
+
+size_t paged_decode_ws_bytes(const LayerArgs& L, int n_seqs, int n_rows, int max_pos, int num_sms) {
+  // (a call of single tokens has no row offsets; windows may have more groups)
+  static const int32_t some = 0;
+  const PagedRows one = {nullptr, nullptr, n_seqs, n_rows}, many = {&some, nullptr, n_seqs, n_rows};
+  return std::max(pd_ws(L, one, pd_plan(L, one, max_pos, num_sms)).total,
+                  pd_ws(L, many, pd_plan(L, many, max_pos, num_sms)).total);
+}
+
+cudaError_t launch_paged_decode(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, void* ws, int num_sms,
+                                cudaStream_t st) {
+  switch (a.L.D) {
+    case 64: return launch_d<64>(a, f, max_pos, ws, num_sms, st);
+    case 128: return launch_d<128>(a, f, max_pos, ws, num_sms, st);
+    case 256: return launch_d<256>(a, f, max_pos, ws, num_sms, st);
+    default: return launch_d<512>(a, f, max_pos, ws, num_sms, st);
+  }
+}
+
+}  // namespace kvq
