@@ -21,7 +21,8 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvq.so")
 
 SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_decode.cu", "kvq_prefill.cu", "kvq_prompt.cu", "kvq_train.cu",
-           "kvq_train_bwd.cu", "kvq_prep_bwd.cu", "kvq_paged_append.cu", "kvq_paged_decode.cu", "kvq_pages.cu"]
+           "kvq_train_bwd.cu", "kvq_prep_bwd.cu", "kvq_paged_append.cu", "kvq_paged_decode.cu",
+           "kvq_paged_prefill.cu", "kvq_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE]
 

@@ -1166,7 +1166,9 @@ kvq_status paged_read(bool window, const kvq_layer* layer, const kvq_paged_cache
   if (q_prepped && !aligned(q_prepped, 2)) return fail(KVQ_EINVAL, "q_prepped is not 2-byte aligned");
   REQUIRE_PTR(workspace, "workspace", 256);
   const int sms = num_sms_current();
-  const size_t need = kvq::paged_decode_ws_bytes(a.L, n_seqs, n_rows, max_pos, sms);
+  const bool tc = window && kvq::paged_prefill_supported(a.L, max_rows_per_seq);
+  const size_t need = tc ? kvq::paged_prefill_ws_bytes(a.L, n_seqs, n_rows, max_pos, sms)
+                         : kvq::paged_decode_ws_bytes(a.L, n_seqs, n_rows, max_pos, sms);
   if (workspace_bytes < need)
     return fail(KVQ_EWORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
   a.q_raw = q_raw;
@@ -1175,7 +1177,9 @@ kvq_status paged_read(bool window, const kvq_layer* layer, const kvq_paged_cache
   a.out_f32 = out_is_f32;
   a.q_prepped = q_prepped;
   const kvq::RopeFreqs& f = rope_freqs(layer->rope_theta, a.L.D, a.L.rope_dims);
-  const cudaError_t e = kvq::launch_paged_decode(a, f, max_pos, workspace, sms, static_cast<cudaStream_t>(stream));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = tc ? kvq::launch_paged_prefill(a, f, max_pos, workspace, sms, cs)
+                           : kvq::launch_paged_decode(a, f, max_pos, workspace, sms, cs);
   if (e != cudaSuccess) return cuda_fail(e, window ? "attn_paged_prefill launch" : "attn_paged_decode launch");
   return KVQ_OK;
 }
@@ -1323,7 +1327,10 @@ size_t attn_paged_prefill_workspace_bytes(const kvq_layer* layer, const kvq_page
   if (check_paged(layer, cache, &L, &pg) != KVQ_OK || n_seqs < 0 || n_seqs >= (1 << 24) || n_rows < 0 ||
       n_rows >= (1 << 24) || max_rows_per_seq < 0 || !max_pos_ok(max_pos))
     return 0;
-  return kvq::paged_decode_ws_bytes(L, n_seqs, n_rows, max_pos, num_sms_current());
+  // (a call of fewer rows than it asked for may take either path)
+  const size_t rows = kvq::paged_decode_ws_bytes(L, n_seqs, n_rows, max_pos, num_sms_current());
+  if (!kvq::paged_prefill_supported(L, max_rows_per_seq)) return rows;
+  return std::max(rows, kvq::paged_prefill_ws_bytes(L, n_seqs, n_rows, max_pos, num_sms_current()));
 }
 
 kvq_status kvq_pages_free(const kvq_page_pool* pool, const int32_t* seqs, const int32_t* keep_tokens, int32_t n,

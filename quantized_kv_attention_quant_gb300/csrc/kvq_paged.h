@@ -62,6 +62,12 @@ size_t paged_decode_ws_bytes(const LayerArgs& L, int n_seqs, int n_rows, int max
 cudaError_t launch_paged_decode(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, void* ws, int num_sms,
                                 cudaStream_t st);
 
+// The read on tcgen05: prompt rows, G dividing 128, more than a few rows.
+bool paged_prefill_supported(const LayerArgs& L, int max_rows_per_seq);
+size_t paged_prefill_ws_bytes(const LayerArgs& L, int n_seqs, int n_rows, int max_pos, int num_sms);
+cudaError_t launch_paged_prefill(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, void* ws, int num_sms,
+                                 cudaStream_t st);
+
 // The pool of pages (kvq_page_pool) and the caches whose pages it manages.
 struct PoolArgs {
   int32_t* tables;

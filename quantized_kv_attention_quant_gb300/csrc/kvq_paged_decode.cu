@@ -611,7 +611,7 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   long long* prefix = reinterpret_cast<long long*>(b + w.prefix);
   float* part_o = reinterpret_cast<float*>(b + w.part_o);
   float* part_ml = reinterpret_cast<float*>(b + w.part_ml);
-  cudaError_t e = launch_paged_prep<D>(a, f, p.TG, p.n_groups, q16, prefix, status, status + 1, st);
+  cudaError_t e = launch_paged_prep<D>(a, f, p.TG, p.n_groups, q16, prefix, nullptr, status, status + 1, st);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(paged_decode_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (e != cudaSuccess) return e;

@@ -120,17 +120,64 @@ __device__ __forceinline__ void paged_plan_block(const PagedRows& r, const Paged
   }
 }
 
-// Block 0 makes the plan (prefix != nullptr) and writes the status word, the
-// others prep rb rows each.
+// order = the groups, those with the most key tiles first (one block): a
+// counting sort over the tile counts; the order of equal ones is open (it
+// decides only which CTA takes a group).
+constexpr int kOrderBins = 2048;
+__device__ __forceinline__ void paged_order_block(const PagedRows& r, const PagedArgs& pg, int window, int TG,
+                                                  int n_groups, int32_t* order, uint32_t* status) {
+  __shared__ int bins[kOrderBins];
+  __shared__ int wsum[kQrWarps];
+  constexpr int PER = kOrderBins / (kQrWarps * 32);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < kOrderBins; i += kQrWarps * 32) bins[i] = 0;
+  __syncthreads();
+  bool bad = false;
+  auto bin_of = [](int tiles) { return kOrderBins - 1 - min(tiles, kOrderBins - 1); };   // most first
+  for (int u = tid; u < n_groups; u += kQrWarps * 32) {
+    const PagedGroup g = paged_group(r, pg, window, TG, u);
+    bad |= g.bad > 0;
+    atomicAdd(&bins[bin_of(g.tiles)], 1);
+  }
+  __syncthreads();
+  int mine[PER], sum = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    mine[k] = sum;
+    sum += bins[PER * tid + k];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, m);
+    if (lane >= m) inc += o;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  int before = inc - sum;
+  for (int w = 0; w < warp; ++w) before += wsum[w];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) bins[PER * tid + k] = before + mine[k];
+  const bool any = __syncthreads_or(bad);
+  for (int u = tid; u < n_groups; u += kQrWarps * 32) {
+    const PagedGroup g = paged_group(r, pg, window, TG, u);
+    order[atomicAdd(&bins[bin_of(g.tiles)], 1)] = u;
+  }
+  if (tid == 0) *status = any ? (1u << KVQ_DEV_BADSEQ) : 0u;
+}
+
+// Block 0 makes the plan (the tile prefix, or the order of the groups) and
+// writes the status word, the others prep rb rows each.
 template <int D>
 __global__ void __launch_bounds__(kQrWarps * 32)
 paged_prep_kernel(const DecodeArgs a, const PagedArgs pg, const RopeFreqs freqs, const int rb, const int TG,
-                  const int n_groups, long long* prefix, uint32_t* status) {
+                  const int n_groups, long long* prefix, int32_t* order, uint32_t* status) {
   if (blockIdx.x == 0) {
     pdl_wait();
     pdl_launch();
     PagedRows r = {a.row_offsets, a.pos, a.n_seqs, a.n_rows};
-    paged_plan_block(r, pg, a.L.window, TG, n_groups, prefix, status);
+    if (prefix) paged_plan_block(r, pg, a.L.window, TG, n_groups, prefix, status);
+    else paged_order_block(r, pg, a.L.window, TG, n_groups, order, status);
   } else {
     qprep_rows_block<D>(a, freqs, rb, blockIdx.x - 1);
     paged_fill_rows<D>(a, pg, rb, blockIdx.x - 1);
@@ -141,7 +188,8 @@ paged_prep_kernel(const DecodeArgs a, const PagedArgs pg, const RopeFreqs freqs,
 // may clear in the place of a status word.
 template <int D>
 cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG, int n_groups, uint16_t* q16,
-                              long long* prefix, uint32_t* status, uint32_t* spare, cudaStream_t st) {
+                              long long* prefix, int32_t* order, uint32_t* status, uint32_t* spare,
+                              cudaStream_t st) {
   DecodeArgs d = {};
   d.L = a.L;
   d.n_seqs = a.r.n_seqs;
@@ -158,7 +206,7 @@ cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG
   const int rb = qprep_rows_rb(a.L);
   const int nq = (a.r.n_rows + rb - 1) / rb;
   return launch_pdl(paged_prep_kernel<D>, dim3(nq + 1), dim3(kQrWarps * 32), qprep_rows_smem(a.L, rb), st, d, a.pg, f,
-                    rb, TG, n_groups, prefix, status);
+                    rb, TG, n_groups, prefix, order, status);
 }
 
 }  // namespace
