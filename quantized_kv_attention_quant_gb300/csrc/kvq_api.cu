@@ -1099,6 +1099,8 @@ kvq_status check_paged_cache(const kvq_paged_cache* c, kvq::PagedArgs* out) {
   // a page's codes are addressed in 32 bits
   if ((long long)c->n_kv_heads * c->page_tokens * c->head_dim > 0x7fffffffLL)
     return fail(KVQ_EUNSUPPORTED, "a page of more than 2^31 codes");
+  if ((long long)c->n_pages * c->n_kv_heads > 0x7fffffffLL)
+    return fail(KVQ_EUNSUPPORTED, "n_pages * n_kv_heads is not below 2^31");
   REQUIRE_PTR(c->k_codes, "k_codes", 16);
   REQUIRE_PTR(c->v_codes, "v_codes", 16);
   REQUIRE_PTR(c->k_scales, "k_scales", 4);

@@ -43,28 +43,25 @@ __device__ __forceinline__ int paged_page(const PagedArgs& pg, int s, int p) {
   return (unsigned)id < (unsigned)pg.n_pages ? id : -1;
 }
 
-// Two f16 values from two int8 codes (bytes of x with the sign bit flipped,
-// i.e. code + 128): the byte under the exponent of 1024 is 1024 + 128 + code,
-// and the subtraction of 1152 is exact.
-__device__ __forceinline__ uint32_t i8_pair(uint32_t flipped, uint32_t sel) {
-  const uint32_t h = prmt(flipped, 0x64646464u, sel);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
+// Four codes (bytes 0..3 of w) as two pairs of f16: (0, 1) and (2, 3).
+//   int8: a code with its sign bit flipped under the exponent of 1024 is 1024 +
+//   128 + code; the subtraction of 1152 is exact.
+//   e4m3: the hardware's conversion (three logic operations a pair, which
+//   rebias the exponent, took 7 % longer in the decode read).
+__device__ __forceinline__ uint32_t h2_sub_1152(uint32_t x) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)r.x | ((uint32_t)r.y << 16);
-}
-// Four codes (bytes 0..3 of w) as two pairs: (0, 1) and (2, 3).
 template <bool E4M3>
 __device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (E4M3) {
-    lo = e4m3_pair(w & 0xFFFFu);
-    hi = e4m3_pair(w >> 16);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
   } else {
     w ^= 0x80808080u;
-    lo = i8_pair(w, 0x4140u);
-    hi = i8_pair(w, 0x4342u);
+    lo = h2_sub_1152(prmt(w, 0x64646464u, 0x4140u));
+    hi = h2_sub_1152(prmt(w, 0x64646464u, 0x4342u));
   }
 }
 

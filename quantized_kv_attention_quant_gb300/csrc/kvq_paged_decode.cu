@@ -19,60 +19,77 @@
 // 2^15 whatever the scales are (renewed when a tile exceeds it by 2^8).  A
 // scale of 0 (all codes 0) counts as 1.
 //
-// A CTA is four warps.  Warp w scores keys 16 w .. of a tile over all dims.
-// With D >= 256, WD = D / 128 warps share the output: each keeps 128 dims of O
-// (64 registers) for the keys of all of them, and they exchange P and the row
-// maxima through shared memory, one barrier a tile: the next tile's scores are
-// formed before it, so it also publishes their maxima.  Codes come by 16-byte
-// asynchronous copies into a ring that no other thread reads (thread i's
-// copies are thread i's fragments: the order of dims inside an MMA's k range
-// and of output columns is free, so a lane takes 16 consecutive bytes), which
-// needs no barrier and has no bank conflicts; positions that no row of the
-// group sees are filled with zeros and never read.  Page numbers are looked up
-// a tile ahead of the copies.
+// A CTA is four warps; with D >= 256, WD = D / 128 of them form a team that
+// shares the output: each keeps 128 dims of O (64 registers) for the keys of
+// all of them, and they exchange P and the row maxima through shared memory,
+// one barrier a tile (the next tile's scores are formed before it, so it also
+// publishes their maxima).  With D <= 128 a warp works alone, on 32 keys of a
+// tile of 128.
+//
+// Codes come by the tensor memory accelerator in boxes of 16 keys x 128 dims
+// (one page, one scale) into a ring that is the warp's own: no barrier between
+// warps, and a box is refilled as soon as the warp has read it.  The boxes are
+// 128-byte swizzled; which key an MMA column stands for is chosen (key_of) so
+// that neither the K reads (two keys, four 16-byte chunks a quarter warp) nor
+// the V reads (four keys, two chunks) meet a bank twice.  The order of dims
+// inside an MMA's k range and of output columns is free too, so a lane takes 16
+// consecutive bytes.  Page numbers are looked up a tile ahead of the copies.
+// (16-byte asynchronous copies by every lane, in the place of the accelerator,
+// spent a third of the instructions on addresses and bounds.)
 #include <algorithm>
 
 #include "kvq_paged.cuh"
 #include "kvq_paged_rows.cuh"
+#include "kvq_tc.cuh"
+#include "kvq_tma.cuh"
 
 namespace kvq {
 
 namespace {
 
 constexpr int kPdThreads = 128;
-constexpr int kPdMinTiles = 2;           // shortest share of a CTA, key tiles
+constexpr int kPdMinKeys = 128;          // shortest share of a CTA, keys
 
 template <int D>
 struct Pd {
   static constexpr int WD = D >= 128 ? D / 128 : 1;     // warps that share a tile's output dims
   static constexpr int TEAMS = 4 / WD;
+  static constexpr int SW = WD == 1 ? 2 : 1;            // 16-key subtiles per warp and tile
+  static constexpr int SUBS = 4 * SW;                   // per tile
+  static constexpr int KT = 16 * SUBS;                  // keys per tile
+  static constexpr int SV = SW * WD;                    // subtiles whose V a warp multiplies
   static constexpr int DS = D / WD;                     // output dims per warp
   static constexpr int NT = DS / 8;                     // 8-dim MMA columns per warp
   static constexpr int VB = DS / 8;                     // V bytes of a key per lane (8 or 16)
-  static constexpr int KB = D / 64;                     // 16-byte K chunks of a key per lane
   static constexpr int KS = D / 16;                     // MMA steps of QK
   static constexpr bool QREG = D <= 128;                // q fragments in registers
-  // ring: K chunks [2 KB][128 threads][16 B], V chunks [4 WD][128][VB], scales [4 warps][2]
-  static constexpr int V_OFF = 2 * KB * kPdThreads * 16;
-  static constexpr int S_OFF = V_OFF + 4 * WD * kPdThreads * VB;
-  static constexpr int STAGE = S_OFF + 64;
-  static constexpr int NS = D <= 128 ? 4 : 3;           // stages
-  static constexpr int CPS = D == 64 ? 4 : D == 128 ? 3 : D == 256 ? 2 : 1;   // CTAs per SM
-  static constexpr int RING = NS * STAGE;
+  // a warp's ring: boxes of 16 keys x ROW bytes; per tile NK of K, then SV of V
+  static constexpr int ROW = D < 128 ? D : 128;
+  static constexpr int BOX = 16 * ROW;
+  static constexpr int KBX = D < 128 ? 1 : D / 128;     // K boxes of a subtile
+  static constexpr int NK = SW * KBX;
+  static constexpr int NB = NK + SV;
+  static constexpr int DEP = D == 512 ? 1 : 2;          // tiles in the ring
+  static constexpr int CPS = D == 64 ? 4 : D == 128 ? 3 : 2;       // CTAs per SM
+  static constexpr int RING = 4 * DEP * NB * BOX;
   static constexpr int Q_OFF = RING;                    // q fragments [KS][32] x 16 B
   static constexpr int P_OFF = Q_OFF + (QREG ? 0 : KS * 512);      // P fragments [2][4 warps][32] x 16 B
   static constexpr int M_OFF = P_OFF + (WD > 1 ? 4096 : 0);        // row maxima [2][4 warps][16]
-  static constexpr int BYTES = M_OFF + 512;
+  static constexpr int S_OFF = M_OFF + 512;             // scales [4 warps][4 tiles][SW][2]
+  static constexpr int B_OFF = S_OFF + 4 * 4 * 2 * 2 * 4;          // barriers [4 warps][DEP][NB]
+  static constexpr int BYTES = B_OFF + 4 * DEP * NB * 8;
   static constexpr int OSTR = D + 4;                    // floats of a merged row (a row's start moves by 4 banks)
-  static_assert(TEAMS * 16 * OSTR * 4 + 4 * 16 * 8 <= RING, "the merge of a CTA's warps reuses the ring");
+  static_assert(TEAMS * 16 * OSTR * 4 + 128 * 4 <= RING, "the merge of a CTA's warps reuses the ring");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+// The key of a subtile's 8 that column i of an MMA stands for.
+__device__ __forceinline__ int key_of(int i) { return i & 1 ? (i - 1) ^ 5 : i; }
+// Byte offset of 16-byte chunk c of key k in a box (the accelerator's swizzle).
+template <int ROW>
+__device__ __forceinline__ uint32_t box_off(int k, int c) {
+  return ROW == 128 ? k * 128 + ((c ^ (k & 7)) << 4) : k * 64 + ((c ^ ((k >> 1) & 3)) << 4);
 }
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
-}
+
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -93,33 +110,51 @@ struct PdShares {
   __device__ long long begin(int c) const { return T * c / nc; }
   __device__ int cta_of(long long x) const { return (int)(((x + 1) * nc - 1) / T); }
 };
+template <int D>
 __device__ __forceinline__ PdShares pd_shares(long long T, int ctas) {
-  return {T, (int)max(1ll, min((long long)ctas, T / kPdMinTiles))};
+  return {T, (int)max(1ll, min((long long)ctas, T * Pd<D>::KT / kPdMinKeys))};
 }
 
 // part_o [2 ctas][16][D], part_ml [2 ctas][2][16]: slot 2 c of CTA c is the
 // piece that begins its share, 2 c + 1 the piece that ends it.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kPdThreads, Pd<D>::CPS)
-paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, const uint16_t* q16,
+paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap tmk,
+                    const __grid_constant__ CUtensorMap tmv, const int TG, const int n_groups, const uint16_t* q16,
                     const long long* prefix, float* part_o, float* part_ml, uint32_t* status) {
   using S = Pd<D>;
-  constexpr int WD = S::WD, KB = S::KB, NT = S::NT, VB = S::VB, NS = S::NS, KS = S::KS;
+  constexpr int WD = S::WD, NT = S::NT, VB = S::VB, KS = S::KS, SW = S::SW, SV = S::SV, NK = S::NK, NB = S::NB,
+                DEP = S::DEP, KT = S::KT;
   constexpr float L2E = 1.4426950408889634f;
   constexpr float kSlack = 8.f;      // how far a tile may exceed ref, log2
   constexpr float kTop = 7.f;        // p of a key at ref is 2^kTop
-  extern __shared__ __align__(128) uint8_t sm[];
+  extern __shared__ __align__(1024) uint8_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rr = lane >> 2, cc = lane & 3;
   const int team = warp / WD, wd = warp % WD;
   const int G = a.L.G, n_kv = a.L.n_kv, P = a.pg.P, sh = a.pg.p_shift, W = a.L.window;
-  const uint32_t sbase = smem_u32(sm);
+  uint8_t* ring = sm + warp * (DEP * NB * S::BOX);
+  float* scale = reinterpret_cast<float*>(sm + S::S_OFF) + warp * 4 * SW * 2;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::B_OFF) + warp * DEP * NB;
+  if (lane == 0) {
+    for (int i = 0; i < DEP * NB; ++i) mbar_init(full + i, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   pdl_launch();
   pdl_wait();                                             // q16, the plan and the status word are written
-  const PdShares shares = pd_shares(__ldg(prefix + n_groups) * n_kv, gridDim.x);
+  const PdShares shares = pd_shares<D>(__ldg(prefix + n_groups) * n_kv, gridDim.x);
   if (shares.T == 0 || (int)blockIdx.x >= shares.nc) return;
   long long x = shares.begin(blockIdx.x);
   const long long x_begin = x, x_end = shares.begin(blockIdx.x + 1);
+  int used = 0;                                           // tiles the ring has held
+  bool dead = false;
+  auto wait = [&](uint64_t* bar, int parity) {
+    if (!dead && !mbar_wait(bar, parity)) {
+      dead = true;
+      flag_error(status, KVQ_DEV_TIMEOUT);
+    }
+  };
 
   while (x < x_end) {
     // ---- the unit of tile x: group u, kv head h, tiles [t_a, t_b) of its `tiles` ----
@@ -132,20 +167,20 @@ paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, con
       }
       u = lo;
     }
-    const PagedGroup g = paged_group(a.r, a.pg, W, TG, u);
+    const PagedGroup g = paged_group(a.r, a.pg, W, TG, KT, u);
     const long long in_u = x - __ldg(prefix + u) * n_kv;
     const int h = (int)(in_u / g.tiles), t_a = (int)(in_u - (long long)h * g.tiles);
     const int n = (int)min((long long)(g.tiles - t_a), x_end - x);
-    const int k0 = g.kt0 + 64 * t_a;                      // first position of the piece
+    const int k0 = g.kt0 + KT * t_a;                      // first position of the piece
     const int rows = g.nt * G;
 
-    // ---- page numbers: lane i < 4 looks up the page of 16 positions i of a tile ----
+    // ---- page numbers: lane i < SUBS looks up the page of 16 positions i of a tile ----
     bool bad = false;
     const int32_t* table = a.pg.tables + (size_t)g.s * a.pg.max_pages;
     auto look_up = [&](int t) {                           // raw entry, -2: no row sees it
       int id = -2;
-      const int key = k0 + 64 * t + 16 * lane;
-      if (lane < 4 && t < n && key <= g.hi && key + 15 >= g.lo) id = __ldg(table + (key >> sh));
+      const int key = k0 + KT * t + 16 * lane;
+      if (lane < S::SUBS && t < n && key <= g.hi && key + 15 >= g.lo) id = __ldg(table + (key >> sh));
       return id;
     };
     auto checked = [&](int id) {
@@ -154,52 +189,61 @@ paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, con
       bad = true;
       return -1;
     };
-    // ---- copies of group j: K and the scales of tile j, V of tile j - 1 ----
-    auto issue = [&](int j, int pid_k, int pid_v) {
-      const uint32_t st = sbase + (j % NS) * S::STAGE;
-      if (j < n) {
-        const int id = __shfl_sync(0xffffffffu, pid_k, warp);
-        const size_t ph = (size_t)max(id, 0) * n_kv + h;
-        const int key0 = k0 + 64 * j + 16 * warp;
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          const int key = key0 + 8 * jj + rr;
-          const uint32_t bytes = id >= 0 && key >= g.lo && key <= g.hi ? 16u : 0u;
-          const uint8_t* src = a.pg.k_codes + ((ph << sh) + (key & (P - 1))) * D + 16 * cc;
-#pragma unroll
-          for (int b = 0; b < KB; ++b) cp16(st + ((jj * KB + b) * kPdThreads + tid) * 16, src + 64 * b, bytes);
-        }
-        if (lane < 2)
-          cp4(st + S::S_OFF + warp * 8 + lane * 4, (lane == 0 ? a.pg.k_scales : a.pg.v_scales) + ph, id >= 0 ? 4u : 0u);
-      }
-      if (j >= 1 && j <= n) {
-#pragma unroll
-        for (int kb = 0; kb < WD; ++kb) {
-          const int sub = team * WD + kb;
-          const int id = __shfl_sync(0xffffffffu, pid_v, sub);
-          const size_t ph = (size_t)max(id, 0) * n_kv + h;
-          const int key0 = k0 + 64 * (j - 1) + 16 * sub + 2 * cc;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {                   // keys 2c, 2c+1, 2c+8, 2c+9
-            const int key = key0 + (e & 1) + 8 * (e >> 1);
-            const uint32_t bytes = id >= 0 && key >= g.lo && key <= g.hi ? (uint32_t)VB : 0u;
-            const uint8_t* src = a.pg.v_codes + ((ph << sh) + (key & (P - 1))) * D + wd * S::DS + VB * rr;
-            const uint32_t dst = st + S::V_OFF + ((kb * 4 + e) * kPdThreads + tid) * VB;
-            if constexpr (VB == 16) cp16(dst, src, bytes); else cp8(dst, src, bytes);
-          }
-        }
-      }
-      cp_commit();
+    // copies of a box: 16 positions from key0, bytes x .. of their rows, of page id (page 0 where there is
+    // none: what no row sees is masked)
+    auto copy = [&](int box, const CUtensorMap* map, int id, int key0, int xb) {
+      mbar_arrive_expect_tx(full + box, S::BOX);
+      tc::tma_load_3d(smem_u32(ring + box * S::BOX), map, xb, key0 & (P - 1), max(id, 0) * n_kv + h,
+                      smem_u32(full + box));
     };
-    // page numbers of the tile that a group's K needs, of the one before, and of the next
-    int pid_prev = -1, pid_cur = checked(look_up(0)), raw_next = look_up(1);
+    auto issue_k = [&](int t, int pid) {                  // K and the scales of tile t
+      const int slot = (used + t) % DEP;
+      int ids[SW];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      issue(j, pid_cur, pid_prev);
-      pid_prev = pid_cur;
-      pid_cur = checked(raw_next);
-      raw_next = look_up(j + 2);
+      for (int e = 0; e < SW; ++e) ids[e] = __shfl_sync(0xffffffffu, pid, SW * warp + e);
+      const int key0 = k0 + KT * t + 16 * SW * warp;
+      if (lane == 0) {
+#pragma unroll
+        for (int e = 0; e < SW; ++e)
+#pragma unroll
+          for (int b = 0; b < S::KBX; ++b) copy(slot * NB + e * S::KBX + b, &tmk, ids[e], key0 + 16 * e, 128 * b);
+      }
+      if (lane < 2 * SW) {
+        const int id = SW == 2 && lane >= 2 ? ids[SW - 1] : ids[0];
+        cp4(smem_u32(scale + ((used + t) & 3) * SW * 2 + lane),
+            (lane & 1 ? a.pg.v_scales : a.pg.k_scales) + (size_t)max(id, 0) * n_kv + h, id >= 0 ? 4u : 0u);
+      }
+    };
+    auto issue_v = [&](int t, int pid) {                  // V of tile t: the team's keys, the warp's dims
+      const int slot = (used + t) % DEP;
+#pragma unroll
+      for (int e = 0; e < SV; ++e) {
+        const int sub = team * SV + e, id = __shfl_sync(0xffffffffu, pid, sub);
+        if (lane == 0) copy(slot * NB + NK + e, &tmv, id, k0 + KT * t + 16 * sub, wd * S::DS);
+      }
+    };
+    // pages of tile j + DEP (V comes next) and j + DEP + 1 (K)
+    int pid_v = checked(look_up(0)), pid_k, raw;
+    if (DEP == 2) {
+      pid_k = checked(look_up(1));
+      raw = look_up(2);
+      issue_k(0, pid_v);
+      cp_commit();
+      issue_v(0, pid_v);
+      if (n > 1) issue_k(1, pid_k);
+      cp_commit();
+      if (n > 1) issue_v(1, pid_k);
+      pid_v = checked(raw);
+      raw = look_up(3);
+    } else {
+      raw = look_up(1);
+      issue_k(0, pid_v);
+      cp_commit();
+      issue_v(0, pid_v);
+      pid_v = checked(raw);
+      raw = look_up(2);
     }
+    pid_k = pid_v;
 
     // ---- q fragments of the unit: step 4 b + t takes dims 64 b + 16 c + 4 t .. +3 of lane column c ----
     uint32_t qf[S::QREG ? KS : 1][4];
@@ -209,7 +253,7 @@ paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, con
       };
       if constexpr (S::QREG) {
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
+        for (int b = 0; b < D / 64; ++b) {
           uint4 v[2][2] = {};
 #pragma unroll
           for (int e = 0; e < 2; ++e)
@@ -241,10 +285,11 @@ paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, con
       }
     }
 
-    // what the thread's two rows see
+    // what the thread's two rows see, and what all of them do
     const int pr0 = g.p0 + min(rr / G, g.nt - 1), pr1 = g.p0 + min((rr + 8) / G, g.nt - 1);
     const int lo0 = W > 0 ? pr0 - W + 1 : 0, lo1 = W > 0 ? pr1 - W + 1 : 0;
-    const int p_last = g.hi, lo_last = W > 0 ? g.hi - W + 1 : 0;
+    const int lo_last = W > 0 ? g.hi - W + 1 : 0;
+    const int kc0 = key_of(2 * cc), kc1 = key_of(2 * cc + 1);      // keys of the thread's columns
 
     float O[NT][4];
 #pragma unroll
@@ -252,73 +297,77 @@ paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, con
 #pragma unroll
       for (int e = 0; e < 4; ++e) O[i][e] = 0.f;
     float ref0 = -INFINITY, ref1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float sc[2][4];                                       // scores, then t = y + log2 sv
+    float sc[SW][2][4];                                   // raw scores of the tile to come: subtile, 8 keys, MMA element
+    float sk[SW], lsv[SW], isv[SW];
 
-    auto qk = [&](int j) {                                // raw scores of tile j into sc
-      constexpr int CH = D >= 256 ? 2 : 1;                // accumulation chains per 8 keys
-      float acc[CH][2][4];
-      const uint8_t* st = sm + (j % NS) * S::STAGE;
+    // scores of tile j, its boxes refilled, its scales; the maxima of the thread's rows over the warp's keys
+    auto scores = [&](int j, float& m0, float& m1) {
+      const int tt = used + j, slot = tt % DEP, par = (tt / DEP) & 1;
+      m0 = m1 = -INFINITY;
+      cp_wait<DEP - 1>();
+      __syncwarp();
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
+      for (int e = 0; e < SW; ++e) {
+        constexpr int CH = D >= 256 ? 2 : 1;              // accumulation chains per 8 keys
+        float acc[CH][2][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[c][e][i] = 0.f;
+          for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const uint4 ka = lds128(st + (b * kPdThreads + tid) * 16);
-        const uint4 kb = lds128(st + ((KB + b) * kPdThreads + tid) * 16);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+            for (int i = 0; i < 4; ++i) acc[c][f][i] = 0.f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          uint32_t q[4];
-          if constexpr (S::QREG) {
+        for (int b = 0; b < D / 64; ++b) {
+          const int box = slot * NB + e * S::KBX + b / 2;
+          if (b % 2 == 0) wait(full + box, par);
+          const uint8_t* bx = ring + box * S::BOX;
+          const uint4 ka = lds128(bx + box_off<S::ROW>(key_of(rr), 4 * (b & 1) + cc));
+          const uint4 kb = lds128(bx + box_off<S::ROW>(8 + key_of(rr), 4 * (b & 1) + cc));
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = qf[4 * b + t][i];
-          } else {
-            const uint4 v = lds128(sm + S::Q_OFF + ((4 * b + t) * 32 + lane) * 16);
-            q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
+          for (int t = 0; t < 4; ++t) {
+            uint32_t q[4];
+            if constexpr (S::QREG) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) q[i] = qf[4 * b + t][i];
+            } else {
+              const uint4 v = lds128(sm + S::Q_OFF + ((4 * b + t) * 32 + lane) * 16);
+              q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
+            }
+            uint32_t b0, b1;
+            codes_to_h2<E4M3>(wa[t], b0, b1);
+            mma_f16(acc[t % CH][0], q, b0, b1);
+            codes_to_h2<E4M3>(wb[t], b0, b1);
+            mma_f16(acc[t % CH][1], q, b0, b1);
           }
-          uint32_t b0, b1;
-          codes_to_h2<E4M3>(wa[t], b0, b1);
-          mma_f16(acc[t % CH][0], q, b0, b1);
-          codes_to_h2<E4M3>(wb[t], b0, b1);
-          mma_f16(acc[t % CH][1], q, b0, b1);
         }
-      }
+        const float2 s2 = *reinterpret_cast<const float2*>(scale + ((tt & 3) * SW + e) * 2);
+        // (a scale of 0 stands for codes of 0; the smallest float keeps a masked -inf what it is)
+        sk[e] = fmaxf(s2.x * L2E, 1e-30f);
+        const float sv = s2.y > 0.f ? s2.y : 1.f;
+        lsv[e] = __log2f(sv);
+        isv[e] = __fdividef(1.f, sv);
+        const int key0 = k0 + KT * j + 16 * (SW * warp + e);
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+        for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc[e][i] = acc[0][e][i];
-          if constexpr (CH == 2) sc[e][i] += acc[CH - 1][e][i];
+          for (int i = 0; i < 4; ++i) sc[e][f][i] = CH == 2 ? acc[0][f][i] + acc[CH - 1][f][i] : acc[0][f][i];
+        if (key0 < lo_last || key0 + 15 > g.p0) {         // a row does not see all 16 keys
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = key0 + 8 * f + (i & 1 ? kc1 : kc0);
+              const bool see = (i >> 1) ? key <= pr1 && key >= lo1 : key <= pr0 && key >= lo0;
+              sc[e][f][i] = see ? sc[e][f][i] : -INFINITY;
+            }
         }
-    };
-    // scores of tile j -> t, masked; the maxima of the thread's rows over the warp's 16 keys
-    float isv = 1.f;
-    auto scale_mask = [&](int j, float& m0, float& m1) {
-      const float2 s2 = *reinterpret_cast<const float2*>(sm + (j % NS) * S::STAGE + S::S_OFF + warp * 8);
-      const float sk = s2.x * L2E, sv = s2.y > 0.f ? s2.y : 1.f;
-      const float lsv = __log2f(sv);
-      isv = __fdividef(1.f, sv);
-      const int key0 = k0 + 64 * j + 16 * warp;
-      if (key0 >= lo_last && key0 + 15 <= g.p0) {         // every row sees all 16 keys
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[e][i] = fmaf(sc[e][i], sk, lsv);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = key0 + 8 * e + 2 * cc + (i & 1);
-            const bool see = (i >> 1) ? key <= pr1 && key >= lo1 : key <= pr0 && key >= lo0;
-            sc[e][i] = see ? fmaf(sc[e][i], sk, lsv) : -INFINITY;
-          }
+        m0 = fmaxf(m0, fmaf(fmaxf(fmaxf(sc[e][0][0], sc[e][0][1]), fmaxf(sc[e][1][0], sc[e][1][1])), sk[e], lsv[e]));
+        m1 = fmaxf(m1, fmaf(fmaxf(fmaxf(sc[e][0][2], sc[e][0][3]), fmaxf(sc[e][1][2], sc[e][1][3])), sk[e], lsv[e]));
       }
-      m0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      m1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+      __syncwarp();                                       // the boxes and scales are read
+      if (j + DEP < n) issue_k(j + DEP, pid_k);
+      cp_commit();
 #pragma unroll
       for (int m = 1; m <= 2; m <<= 1) {
         m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, m));
@@ -335,21 +384,20 @@ paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, con
     auto team_sync = [&]() {
       if constexpr (WD == 4) __syncthreads();
       else if constexpr (WD == 2) named_bar(1 + team, 64);
-      else __syncwarp();
     };
 
     // ---- tile by tile ----
-    cp_wait<NS - 1>();                                    // group 0
-    __syncwarp();
-    qk(0);
     float m0, m1;
-    scale_mask(0, m0, m1);
+    scores(0, m0, m1);
     if constexpr (WD > 1) {
       post_max(0, m0, m1);
       team_sync();
     }
-    (void)p_last;
     for (int j = 0; j < n; ++j) {
+      // (pid_k served K of tile j + DEP: the same pages hold its V)
+      pid_v = pid_k;
+      pid_k = checked(raw);
+      raw = look_up(j + DEP + 2);
       if constexpr (WD > 1) {
 #pragma unroll
         for (int w = 0; w < WD; ++w) {
@@ -374,59 +422,69 @@ paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, con
           O[i][3] *= a1;
         }
       }
-      uint32_t pf[4];
-      {
-        const float r0 = ref0 == -INFINITY ? 0.f : ref0 - kTop, r1 = ref1 == -INFINITY ? 0.f : ref1 - kTop;
-        float p[2][4];
+      uint32_t pf[SW][4];
+      const float r0 = ref0 == -INFINITY ? 0.f : ref0 - kTop, r1 = ref1 == -INFINITY ? 0.f : ref1 - kTop;
+#pragma unroll
+      for (int e = 0; e < SW; ++e) {
+        const float c0 = lsv[e] - r0, c1 = lsv[e] - r1;
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          p[e][0] = ex2(sc[e][0] - r0);
-          p[e][1] = ex2(sc[e][1] - r0);
-          p[e][2] = ex2(sc[e][2] - r1);
-          p[e][3] = ex2(sc[e][3] - r1);
-          s0 += p[e][0] + p[e][1];
-          s1 += p[e][2] + p[e][3];
-          pf[2 * e] = pack_h2(p[e][0], p[e][1]);
-          pf[2 * e + 1] = pack_h2(p[e][2], p[e][3]);
+        for (int f = 0; f < 2; ++f) {
+          const float p0 = ex2(fmaf(sc[e][f][0], sk[e], c0)), p1 = ex2(fmaf(sc[e][f][1], sk[e], c0));
+          const float p2 = ex2(fmaf(sc[e][f][2], sk[e], c1)), p3 = ex2(fmaf(sc[e][f][3], sk[e], c1));
+          s0 += p0 + p1;
+          s1 += p2 + p3;
+          pf[e][2 * f] = pack_h2(p0, p1);
+          pf[e][2 * f + 1] = pack_h2(p2, p3);
         }
-        l0 = fmaf(s0, isv, l0);
-        l1 = fmaf(s1, isv, l1);
+        l0 = fmaf(s0, isv[e], l0);
+        l1 = fmaf(s1, isv[e], l1);
       }
       if constexpr (WD > 1)
         *reinterpret_cast<uint4*>(sm + S::P_OFF + ((j & 1) * 4 + warp) * 512 + lane * 16) =
-            make_uint4(pf[0], pf[1], pf[2], pf[3]);
-      // the stage of tile j's K and scales (and V of j - 1) is free: the next group's copies
-      __syncwarp();
-      issue(j + NS, pid_cur, pid_prev);
-      pid_prev = pid_cur;
-      pid_cur = checked(raw_next);
-      raw_next = look_up(j + NS + 2);
-      cp_wait<NS - 1>();                                  // group j + 1: K of the next tile, V of this one
-      __syncwarp();
+            make_uint4(pf[0][0], pf[0][1], pf[0][2], pf[0][3]);
       if (j + 1 < n) {
-        qk(j + 1);
-        scale_mask(j + 1, m0, m1);
+        scores(j + 1, m0, m1);
         if constexpr (WD > 1) post_max(j + 1, m0, m1);
       }
-      if constexpr (WD > 1) team_sync();
-      const uint8_t* st = sm + ((j + 1) % NS) * S::STAGE + S::V_OFF;
+      team_sync();
+      const int slot = (used + j) % DEP, par = ((used + j) / DEP) & 1;
 #pragma unroll
-      for (int kb = 0; kb < WD; ++kb) {
+      for (int e = 0; e < SV; ++e) {
+        uint32_t p[4];
         if constexpr (WD > 1) {
-          const uint4 v = lds128(sm + S::P_OFF + ((j & 1) * 4 + team * WD + kb) * 512 + lane * 16);
-          pf[0] = v.x; pf[1] = v.y; pf[2] = v.z; pf[3] = v.w;
+          const uint4 v = lds128(sm + S::P_OFF + ((j & 1) * 4 + team * WD + e) * 512 + lane * 16);
+          p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = pf[e][i];
         }
+        const int box = slot * NB + NK + e;
+        wait(full + box, par);
+        const uint8_t* bx = ring + box * S::BOX;
         uint32_t vw[4][VB / 4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint8_t* src = st + ((kb * 4 + e) * kPdThreads + tid) * VB;
+        for (int f = 0; f < 4; ++f) {                     // the keys of P's columns
+          const int k = (f & 1 ? kc1 : kc0) + 8 * (f >> 1);
           if constexpr (VB == 16) {
-            const uint4 v = lds128(src);
-            vw[e][0] = v.x; vw[e][1] = v.y; vw[e][2] = v.z; vw[e][3] = v.w;
+            const uint4 v = lds128(bx + box_off<S::ROW>(k, rr));
+            vw[f][0] = v.x; vw[f][1] = v.y; vw[f][2] = v.z; vw[f][3] = v.w;
           } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(src);
-            vw[e][0] = v.x; vw[e][1] = v.y;
+            const uint2 v = *reinterpret_cast<const uint2*>(bx + box_off<S::ROW>(k, rr >> 1) + 8 * (rr & 1));
+            vw[f][0] = v.x; vw[f][1] = v.y;
+          }
+        }
+        if constexpr (E4M3) {
+          // bytes that no row sees may read as NaN, which a weight of 0 does not hide
+          const int key0 = k0 + KT * j + 16 * (team * SV + e);
+          if (key0 < g.lo || key0 + 15 > g.hi) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const int key = key0 + (f & 1 ? kc1 : kc0) + 8 * (f >> 1);
+              if (key < g.lo || key > g.hi)
+#pragma unroll
+                for (int w = 0; w < VB / 4; ++w) vw[f][w] = 0u;
+            }
           }
         }
 #pragma unroll
@@ -437,12 +495,15 @@ paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, con
             uint32_t a0, a1, b0, b1;
             codes_to_h2<E4M3>(prmt(vw[0][w], vw[1][w], sel), a0, a1);
             codes_to_h2<E4M3>(prmt(vw[2][w], vw[3][w], sel), b0, b1);
-            mma_f16(O[4 * w + 2 * hf], pf, a0, b0);
-            mma_f16(O[4 * w + 2 * hf + 1], pf, a1, b1);
+            mma_f16(O[4 * w + 2 * hf], p, a0, b0);
+            mma_f16(O[4 * w + 2 * hf + 1], p, a1, b1);
           }
         }
       }
+      __syncwarp();                                       // V is read
+      if (j + DEP < n) issue_v(j + DEP, pid_v);
     }
+    used += n;
 
     // ---- join the warps, in shared memory ----
     cp_wait<0>();
@@ -512,7 +573,8 @@ paged_decode_kernel(const PagedReadArgs a, const int TG, const int n_groups, con
         }
       }
     }
-    __syncthreads();                                      // the ring is free for the next piece
+    fence_proxy_async();                                  // (the accelerator writes there next)
+    __syncthreads();
     x += n;
   }
 }
@@ -531,11 +593,11 @@ paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, cons
   const long long pu = __ldg(prefix + u);
   const int tiles = (int)(__ldg(prefix + u + 1) - pu);
   if (tiles == 0) return;
-  const PdShares shares = pd_shares(T, ctas);
+  const PdShares shares = pd_shares<D>(T, ctas);
   const long long x0 = pu * n_kv + (long long)h * tiles, x1 = x0 + tiles;
   const int c0 = shares.cta_of(x0), c1 = shares.cta_of(x1 - 1);
   if (c0 == c1) return;                                   // one CTA had it whole
-  const PagedGroup g = paged_group(a.r, a.pg, a.L.window, TG, u);
+  const PagedGroup g = paged_group(a.r, a.pg, a.L.window, TG, Pd<D>::KT, u);
   const int i = blockIdx.y * 128 + threadIdx.x;
   if (i >= g.nt * G * (D / 4)) return;
   const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
@@ -569,6 +631,7 @@ paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, cons
   }
 }
 
+int pd_kt(int D) { return D <= 128 ? Pd<128>::KT : Pd<256>::KT; }
 int pd_cps(int D) { return D == 64 ? Pd<64>::CPS : D == 128 ? Pd<128>::CPS : D == 256 ? Pd<256>::CPS : Pd<512>::CPS; }
 
 // rows of a group, groups and CTAs of a call
@@ -580,8 +643,9 @@ PdPlan pd_plan(const LayerArgs& L, const PagedRows& r, int max_pos, int num_sms)
   // a group sees at most max_pos + 1 positions, or its window's
   long long keys = (long long)max_pos + 1;
   if (L.window > 0) keys = std::min<long long>(keys, (long long)L.window + p.TG - 1);
-  p.max_tiles = (int)((keys + 62) / 64 + 1);
-  if (keys == (long long)max_pos + 1) p.max_tiles = (int)((keys + 63) / 64);   // they begin at 0
+  // (a window's keys begin anywhere in a tile, a whole sequence's at 0)
+  const int kt = pd_kt(L.D);
+  p.max_tiles = (int)(keys == (long long)max_pos + 1 ? (keys + kt - 1) / kt : (keys + kt + 62) / kt + 1);
   const long long most = (long long)p.n_groups * L.n_kv * p.max_tiles;
   p.ctas = (int)std::max(1ll, std::min<long long>((long long)num_sms * pd_cps(L.D), most));
   return p;
@@ -611,13 +675,17 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   long long* prefix = reinterpret_cast<long long*>(b + w.prefix);
   float* part_o = reinterpret_cast<float*>(b + w.part_o);
   float* part_ml = reinterpret_cast<float*>(b + w.part_ml);
-  cudaError_t e = launch_paged_prep<D>(a, f, p.TG, p.n_groups, q16, prefix, nullptr, status, status + 1, st);
+  cudaError_t e = launch_paged_prep<D>(a, f, p.TG, S::KT, p.n_groups, q16, prefix, nullptr, status, status + 1, st);
   if (e != cudaSuccess) return e;
+  CUtensorMap tmk, tmv;
+  if (!pages_map(&tmk, a.pg.k_codes, D, a.pg.P, (long long)a.pg.n_pages * a.L.n_kv) ||
+      !pages_map(&tmv, a.pg.v_codes, D, a.pg.P, (long long)a.pg.n_pages * a.L.n_kv))
+    return cudaErrorInvalidValue;
   e = cudaFuncSetAttribute(paged_decode_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (e != cudaSuccess) return e;
   if ((e = prof_before(st)) != cudaSuccess) return e;
-  e = launch_pdl(paged_decode_kernel<D, E4M3>, dim3(p.ctas), dim3(kPdThreads), S::BYTES, st, a, p.TG, p.n_groups, q16,
-                 prefix, part_o, part_ml, status);
+  e = launch_pdl(paged_decode_kernel<D, E4M3>, dim3(p.ctas), dim3(kPdThreads), S::BYTES, st, a, tmk, tmv, p.TG, p.n_groups,
+                 q16, prefix, part_o, part_ml, status);
   if (e != cudaSuccess) return e;
   if ((e = prof_after(st)) != cudaSuccess) return e;
   if (p.max_tiles < 2) return cudaSuccess;                // a single tile is never cut

@@ -130,9 +130,9 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   const int per = n_kv * S::NSPLIT, z = blockIdx.y;
   const int rank = blockIdx.x / per, hx = blockIdx.x - rank * per;
   const int u = __ldg(order + rank), h = hx / S::NSPLIT, d_base = (hx % S::NSPLIT) * DO;
-  const PagedGroup g = paged_group(a.r, a.pg, W, TQ, u);
+  const PagedGroup g = paged_group(a.r, a.pg, W, TQ, KT, u);
   if (g.tiles == 0) return;
-  const int n_all = (g.hi - g.kt0) / KT + 1;
+  const int n_all = g.tiles;
   const int pieces = pf_pieces(n_all, splits);
   if (z >= pieces) return;
   const int t_a = pf_tile0(n_all, pieces, z), n = pf_tile0(n_all, pieces, z + 1) - t_a;
@@ -559,9 +559,9 @@ paged_join_kernel(const PagedReadArgs a, const int TQ, const int splits, const f
   pdl_wait();
   const int per = a.L.n_kv * S::NSPLIT, G = a.L.G;
   const int u = blockIdx.x / per, hx = blockIdx.x - u * per;
-  const PagedGroup g = paged_group(a.r, a.pg, a.L.window, TQ, u);
+  const PagedGroup g = paged_group(a.r, a.pg, a.L.window, TQ, S::KT, u);
   if (g.tiles == 0) return;
-  const int pieces = pf_pieces((g.hi - g.kt0) / S::KT + 1, splits);
+  const int pieces = pf_pieces(g.tiles, splits);
   if (pieces == 1) return;
   const int i = blockIdx.y * 256 + threadIdx.x;
   const int r = i / (DO / 4), d = (i - r * (DO / 4)) * 4;
@@ -641,7 +641,7 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   int32_t* order = reinterpret_cast<int32_t*>(b + w.order);
   float* part_o = reinterpret_cast<float*>(b + w.part_o);
   float* part_ml = reinterpret_cast<float*>(b + w.part_ml);
-  cudaError_t e = launch_paged_prep<D>(a, f, p.TQ, p.n_groups, q16, nullptr, order, status, status + 1, st);
+  cudaError_t e = launch_paged_prep<D>(a, f, p.TQ, S::KT, p.n_groups, q16, nullptr, order, status, status + 1, st);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(paged_prefill_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (e != cudaSuccess) return e;

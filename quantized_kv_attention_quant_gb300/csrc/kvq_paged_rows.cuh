@@ -18,11 +18,12 @@ struct PagedGroup {
   int bad;      // rows past it
   int p0;       // position of the first row
   int lo, hi;   // oldest and newest position that a row of the group sees
-  int kt0;      // lo rounded down to a key tile
-  int tiles;    // key tiles (0: nothing to read)
+  int kt0;      // lo rounded down to 64
+  int tiles;    // key tiles of KT from there (0: nothing to read)
 };
 
-__device__ __forceinline__ PagedGroup paged_group(const PagedRows& r, const PagedArgs& pg, int window, int TG, int u) {
+__device__ __forceinline__ PagedGroup paged_group(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
+                                                  int u) {
   PagedGroup g;
   int t0 = 0, take;
   if (r.row_offsets == nullptr) {
@@ -48,8 +49,8 @@ __device__ __forceinline__ PagedGroup paged_group(const PagedRows& r, const Page
   g.bad = take - g.nt;
   g.hi = g.p0 + g.nt - 1;
   g.lo = window > 0 ? max(0, g.p0 - window + 1) : 0;
-  g.kt0 = g.lo & ~(kTileKeys - 1);
-  g.tiles = g.nt > 0 ? (g.hi - g.kt0) / kTileKeys + 1 : 0;
+  g.kt0 = g.lo & ~63;
+  g.tiles = g.nt > 0 ? (g.hi - g.kt0) / KT + 1 : 0;
   return g;
 }
 
@@ -82,7 +83,7 @@ __device__ __forceinline__ void paged_fill_rows(const DecodeArgs& a, const Paged
 
 // prefix[u] = key tiles of the groups before u (one block), and the call's
 // status word.
-__device__ __forceinline__ void paged_plan_block(const PagedRows& r, const PagedArgs& pg, int window, int TG,
+__device__ __forceinline__ void paged_plan_block(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
                                                  int n_groups, long long* prefix, uint32_t* status) {
   __shared__ int wsum[kQrWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -92,7 +93,7 @@ __device__ __forceinline__ void paged_plan_block(const PagedRows& r, const Paged
     const int u = u0 + tid;
     int t = 0;
     if (u < n_groups) {
-      const PagedGroup g = paged_group(r, pg, window, TG, u);
+      const PagedGroup g = paged_group(r, pg, window, TG, KT, u);
       t = g.tiles;
       bad |= g.bad > 0;
     }
@@ -124,7 +125,7 @@ __device__ __forceinline__ void paged_plan_block(const PagedRows& r, const Paged
 // counting sort over the tile counts; the order of equal ones is open (it
 // decides only which CTA takes a group).
 constexpr int kOrderBins = 2048;
-__device__ __forceinline__ void paged_order_block(const PagedRows& r, const PagedArgs& pg, int window, int TG,
+__device__ __forceinline__ void paged_order_block(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
                                                   int n_groups, int32_t* order, uint32_t* status) {
   __shared__ int bins[kOrderBins];
   __shared__ int wsum[kQrWarps];
@@ -135,7 +136,7 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
   bool bad = false;
   auto bin_of = [](int tiles) { return kOrderBins - 1 - min(tiles, kOrderBins - 1); };   // most first
   for (int u = tid; u < n_groups; u += kQrWarps * 32) {
-    const PagedGroup g = paged_group(r, pg, window, TG, u);
+    const PagedGroup g = paged_group(r, pg, window, TG, KT, u);
     bad |= g.bad > 0;
     atomicAdd(&bins[bin_of(g.tiles)], 1);
   }
@@ -160,7 +161,7 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
   for (int k = 0; k < PER; ++k) bins[PER * tid + k] = before + mine[k];
   const bool any = __syncthreads_or(bad);
   for (int u = tid; u < n_groups; u += kQrWarps * 32) {
-    const PagedGroup g = paged_group(r, pg, window, TG, u);
+    const PagedGroup g = paged_group(r, pg, window, TG, KT, u);
     order[atomicAdd(&bins[bin_of(g.tiles)], 1)] = u;
   }
   if (tid == 0) *status = any ? (1u << KVQ_DEV_BADSEQ) : 0u;
@@ -171,13 +172,13 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
 template <int D>
 __global__ void __launch_bounds__(kQrWarps * 32)
 paged_prep_kernel(const DecodeArgs a, const PagedArgs pg, const RopeFreqs freqs, const int rb, const int TG,
-                  const int n_groups, long long* prefix, int32_t* order, uint32_t* status) {
+                  const int KT, const int n_groups, long long* prefix, int32_t* order, uint32_t* status) {
   if (blockIdx.x == 0) {
     pdl_wait();
     pdl_launch();
     PagedRows r = {a.row_offsets, a.pos, a.n_seqs, a.n_rows};
-    if (prefix) paged_plan_block(r, pg, a.L.window, TG, n_groups, prefix, status);
-    else paged_order_block(r, pg, a.L.window, TG, n_groups, order, status);
+    if (prefix) paged_plan_block(r, pg, a.L.window, TG, KT, n_groups, prefix, status);
+    else paged_order_block(r, pg, a.L.window, TG, KT, n_groups, order, status);
   } else {
     qprep_rows_block<D>(a, freqs, rb, blockIdx.x - 1);
     paged_fill_rows<D>(a, pg, rb, blockIdx.x - 1);
@@ -187,7 +188,7 @@ paged_prep_kernel(const DecodeArgs a, const PagedArgs pg, const RopeFreqs freqs,
 // q_hat as f16 to q16 [n_rows][n_q][D]; `spare`: a word that qprep_rows_block
 // may clear in the place of a status word.
 template <int D>
-cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG, int n_groups, uint16_t* q16,
+cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG, int KT, int n_groups, uint16_t* q16,
                               long long* prefix, int32_t* order, uint32_t* status, uint32_t* spare,
                               cudaStream_t st) {
   DecodeArgs d = {};
@@ -206,7 +207,7 @@ cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG
   const int rb = qprep_rows_rb(a.L);
   const int nq = (a.r.n_rows + rb - 1) / rb;
   return launch_pdl(paged_prep_kernel<D>, dim3(nq + 1), dim3(kQrWarps * 32), qprep_rows_smem(a.L, rb), st, d, a.pg, f,
-                    rb, TG, n_groups, prefix, order, status);
+                    rb, TG, KT, n_groups, prefix, order, status);
 }
 
 }  // namespace

@@ -46,6 +46,20 @@ inline bool rows_map(CUtensorMap* m, CUtensorMapDataType type, const void* base,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Pages of 8-bit codes [pages * heads][page_tokens][D], read in boxes of 16
+// rows of 128 bytes (D = 64: 64), swizzled.  The base must be 16-byte aligned.
+inline bool pages_map(CUtensorMap* m, const void* base, int D, int page_tokens, long long pages) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page_tokens, (cuuint64_t)pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)page_tokens * D};
+  const cuuint32_t box[3] = {D < 128 ? (cuuint32_t)D : 128u, 16u, 1u};
+  const cuuint32_t es[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Runs of 1024 contiguous bytes, [n3][n2][n1][1024 bytes] packed, read in
 // boxes of (one run, b1, b2, 1), not swizzled.  The base must be 16-byte aligned.
 inline bool runs_map(CUtensorMap* m, const void* base, int n1, int n2, int n3, int b1, int b2) {
