@@ -25,7 +25,7 @@
 
 #include "kvq_append.cuh"
 #include "kvq_paged.cuh"
-#include "kvq_qrows.cuh"
+#include "kvq_paged_prep.cuh"
 
 namespace kvq {
 
@@ -58,7 +58,7 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
   const int R = kind == 0 ? a.L.rope_dims : 0, half = R >> 1, n_kv = a.L.n_kv;
   const PaSmem m = pa_smem(D, a.L.rope_dims >> 1, hb, cap, rb);
   uint16_t* rows = reinterpret_cast<uint16_t*>(pa_buf);   // [hb][cap][D]
-  float4* cs = reinterpret_cast<float4*>(pa_buf + m.cs);
+  const Angles ang = {reinterpret_cast<float2*>(pa_buf + m.cs), reinterpret_cast<float2*>(pa_buf + m.cs) + rb * half};
   float (*freq)[3] = reinterpret_cast<float (*)[3]>(pa_buf + m.freq);
   uint16_t* nr = reinterpret_cast<uint16_t*>(pa_buf + m.nrm) + warp * 2 * D;
   if (R > 0) stage_freqs(freqs.f, half, freq);
@@ -98,9 +98,7 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
       __syncthreads();                                    // the frequencies; the last rows' angles are read
       for (int idx = tid; idx < cnt * half; idx += kPaWarps * 32) {
         const int r = idx / half, j = idx - r * half;
-        ff cc, sn;
-        rope_cos_sin(p_lo + c0 + r, freq[j][0], freq[j][1], freq[j][2], cc, sn);
-        cs[R == D ? r * half + (j % E) * 16 + j / E : idx] = make_float4(cc.hi, cc.lo, sn.hi, sn.lo);
+        put_angle<D>(ang, r, R, j, p_lo + c0 + r, freq[j]);
       }
     }
     __syncthreads();
@@ -108,29 +106,27 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
       const int r = it / nh, hh = it - r * nh;
       const size_t row = (size_t)(row0 + c0 + r);
       const uint32_t* src = reinterpret_cast<const uint32_t*>(raw + (row * n_kv + h0 + hh) * D + lane * E);
-      float x[E];
+      uint32_t x[E / 2], y[E / 2];
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const uint32_t v = __ldg(src + i / 2);
-        x[i] = bf16lo_to_f(v);
-        x[i + 1] = bf16hi_to_f(v);
-      }
-      uint16_t y[E];
-      uint32_t yw[E / 2];
-      prep_row_warp<D>(x, w, a.L.eps, R, cs + r * half, nr, nr + D, y, yw);
+      for (int i = 0; i < E / 2; ++i) x[i] = __ldg(src + i);
+      prep_row<D>(x, w, a.L.eps, R, ang, r, nr, y);
       uint32_t* dst = reinterpret_cast<uint32_t*>(rows + ((size_t)hh * cap + c0 + r) * D + lane * E);
       float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < E; ++i) top = fmaxf(top, fabsf(bf16_to_f(y[i])));
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) dst[i] = yw[i];
+      for (int i = 0; i < E / 2; ++i) {
+        top = fmaxf(top, fmaxf(fabsf(bf16lo_to_f(y[i])), fabsf(bf16hi_to_f(y[i]))));
+        dst[i] = y[i];
+      }
 #pragma unroll
       for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
       if (lane == 0) atomicMax(&amax[hh], __float_as_uint(top));   // (of magnitudes: ordered as their bits)
       if (a.prepped) {
         uint16_t* d = a.prepped + (((size_t)kind * a.r.n_rows + row) * n_kv + h0 + hh) * D + lane * E;
 #pragma unroll
-        for (int i = 0; i < E; ++i) d[i] = y[i];
+        for (int i = 0; i < E / 2; ++i) {
+          d[2 * i] = (uint16_t)(y[i] & 0xFFFFu);
+          d[2 * i + 1] = (uint16_t)(y[i] >> 16);
+        }
       }
     }
   }
@@ -252,10 +248,11 @@ cudaError_t launch_append_t(const PagedAppendArgs& a, const RopeFreqs& f, int nu
   const int P = a.pg.P, half = a.L.rope_dims / 2, n_kv = a.L.n_kv;
   const int cap = std::min(P, a.r.n_rows);
   const int rb = half > 0 ? std::max(1, std::min(16, 1024 / half)) : 16;
-  // as many heads as 64 KB of rows hold, fewer while blocks are short
-  int hb = std::max(1, std::min({n_kv, kPaMaxHeads, 65536 / (cap * D * 2)}));
+  // the heads of a block share its angles; as many as 32 KB of rows hold, fewer
+  // while there are less than eight blocks per SM
+  int hb = std::max(1, std::min({n_kv, kPaMaxHeads, 32768 / (cap * D * 2)}));
   const long long pages = (long long)a.r.n_rows / P + a.r.n_seqs;
-  while (hb > 1 && pages * ((n_kv + hb - 1) / hb) * 2 < 2ll * num_sms) hb = (hb + 1) / 2;
+  while (hb > 1 && pages * ((n_kv + hb - 1) / hb) * 2 < 8ll * num_sms) hb = (hb + 1) / 2;
   const size_t smem = pa_smem(D, half, hb, cap, rb).total;
   cudaError_t e = cudaFuncSetAttribute(paged_append_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);

@@ -641,7 +641,7 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   int32_t* order = reinterpret_cast<int32_t*>(b + w.order);
   float* part_o = reinterpret_cast<float*>(b + w.part_o);
   float* part_ml = reinterpret_cast<float*>(b + w.part_ml);
-  cudaError_t e = launch_paged_prep<D>(a, f, p.TQ, S::KT, p.n_groups, q16, nullptr, order, status, status + 1, st);
+  cudaError_t e = launch_paged_prep<D>(a, f, p.TQ, S::KT, p.n_groups, q16, nullptr, order, status, num_sms, st);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(paged_prefill_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (e != cudaSuccess) return e;

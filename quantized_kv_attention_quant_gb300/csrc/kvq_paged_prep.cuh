@@ -1,0 +1,159 @@
+// The rows' prep of the paged calls: RMSNorm and RoPE of one row by one warp,
+// D/32 consecutive elements a lane, each rounded to the bf16 nearest to the
+// exact result (the precision contract of kvq_common.cuh).
+//
+// The float-float arithmetic that decides every rounding is needed only where
+// a plain fp32 result lies near a tie.  So the row is formed in fp32 with a
+// bound on its error, rounded from both ends of the interval, and only where
+// the two differ in bf16 is the exact form taken: for the norm the whole row
+// (its sum of squares), for the rotation the element.
+//   Norm.  x^2 is exact; a lane's D/32 squares are summed in two chains, so that
+//   at most D/64 + 1 + 5 (warp) additions and one of eps round: <= 15 * 2^-24 of
+//   the sum, half of it in 1/sqrt, plus the rounded sqrt and division and the
+//   product with x w (exact) at 2^-24 each: below 11 * 2^-24; 16 * 2^-24 are taken.
+//   Rotation.  r = fl(x c - fl(y s)) with c, s the leading floats of the angle:
+//   within 2^-22 (|x c| + |y s|) of the exact value (kvq_common.cuh, rot_bf16);
+//   1.5 times that is taken, which covers the rounding of the two ends.
+// 2^-140 more on each side covers what underflows; it also sends exact zeros to
+// the exact forms, which keep their sign.
+// About 1 row in 10 of 128 dims takes the norm's exact form, and an element in
+// some 2000 the rotation's.
+#pragma once
+#include "kvq_common.cuh"
+
+namespace kvq {
+namespace {
+
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Angles of a block's rows: the leading floats (cos, sin) and the rest apart.
+// Pair j of a row is entry angle_at(j) of its half: under full rotation the
+// 16 lanes of a half row read consecutive entries.
+struct Angles {
+  float2* hi;
+  float2* lo;
+};
+template <int D>
+__device__ __forceinline__ int angle_at(int R, int j) {
+  constexpr int E = D / 32;
+  return R == D ? (j % E) * 16 + j / E : j;
+}
+template <int D>
+__device__ __forceinline__ void put_angle(const Angles& t, int row, int R, int j, int p, const float (&f)[3]) {
+  ff c, s;
+  rope_cos_sin(p, f[0], f[1], f[2], c, s);
+  const int at = row * (R >> 1) + angle_at<D>(R, j);
+  t.hi[at] = make_float2(c.hi, s.hi);
+  t.lo[at] = make_float2(c.lo, s.lo);
+}
+
+constexpr float kUnder = 7.17464813734306e-43f;           // 2^-140
+
+// x c + y s (s negated by the caller for the lower half), nearest bf16 bits.
+// True when the fp32 ends agree.
+__device__ __forceinline__ bool rot_ends(float x, float y, float c, float s, uint32_t& bits) {
+  const float ys = __fmul_rn(y, s);
+  const float r = __fmaf_rn(x, c, ys);
+  const float b = __fmaf_rn(__fmaf_rn(fabsf(x), fabsf(c), fabsf(ys)), 3.5762786865234375e-7f, kUnder);   // 1.5 * 2^-22
+  const uint32_t two = bf16x2_rn(__fadd_rn(r, b), __fsub_rn(r, b));
+  bits = two & 0xFFFFu;
+  return bits == two >> 16;
+}
+
+// raw: the lane's D/32 bf16 in pairs; w: its weights; row: the row's place in
+// the angles; nr: two shared rows [D] of the warp's own (0 < R < D).  Returns the
+// prepped elements in pairs.
+template <int D>
+__device__ __forceinline__ void prep_row(const uint32_t (&raw)[D / 64], const float (&w)[D / 32], const float eps,
+                                         const int R, const Angles& ang, const int row, uint16_t* nr,
+                                         uint32_t (&y)[D / 64]) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, half = R >> 1;
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    s0 = __fmaf_rn(bf16lo_to_f(raw[i]), bf16lo_to_f(raw[i]), s0);
+    s1 = __fmaf_rn(bf16hi_to_f(raw[i]), bf16hi_to_f(raw[i]), s1);
+  }
+  float ss = s0 + s1;
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+  const float ms = __fadd_rn(__fmul_rn(ss, 1.f / D), eps);
+  const float inv = __fdiv_rn(1.f, __fsqrt_rn(ms));
+  const float eb = inv * (16.f / 16777216.f);
+  bool same = ms > 1e-30f && ms < 1e30f;                  // (no subnormals, no overflow in the bound)
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float a = __fmul_rn(bf16lo_to_f(raw[i]), w[2 * i]), b = __fmul_rn(bf16hi_to_f(raw[i]), w[2 * i + 1]);
+    const float da = __fmaf_rn(fabsf(a), eb, kUnder), db = __fmaf_rn(fabsf(b), eb, kUnder);
+    y[i] = bf16x2_rn(__fmaf_rn(a, inv, da), __fmaf_rn(b, inv, db));
+    same &= y[i] == bf16x2_rn(__fmaf_rn(a, inv, -da), __fmaf_rn(b, inv, -db));
+  }
+  if (!__all_sync(0xffffffffu, same)) {
+    ff t0 = {0.f, 0.f}, t1 = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      ff_acc_sq(t0, bf16lo_to_f(raw[i]));
+      ff_acc_sq(t1, bf16hi_to_f(raw[i]));
+    }
+    const ff ex = rms_inv(ff_warp_sum(ff_add(t0, t1)), D, eps);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
+      y[i] = (uint32_t)norm_scale_bf16(bf16lo_to_f(raw[i]), w[2 * i], ex) |
+             ((uint32_t)norm_scale_bf16(bf16hi_to_f(raw[i]), w[2 * i + 1], ex) << 16);
+  }
+  if (R == D) {
+    // x_e c - x_(e+D/2) s in lanes 0..15, x_e c + x_(e-D/2) s in lanes 16..31
+    const float2* t = ang.hi + row * half + (lane & 15);
+    const float sign = lane < 16 ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, y[i], 16);
+      const float2 a0 = t[32 * i], a1 = t[32 * i + 16];
+      uint32_t lo, hi;
+      const bool k0 = rot_ends(bf16lo_to_f(y[i]), bf16lo_to_f(o), a0.x, sign * a0.y, lo);
+      const bool k1 = rot_ends(bf16hi_to_f(y[i]), bf16hi_to_f(o), a1.x, sign * a1.y, hi);
+      if (!(k0 && k1)) {
+        const float2* l = ang.lo + row * half + (lane & 15);
+        const float2 b0 = l[32 * i], b1 = l[32 * i + 16];
+        lo = rot_bf16(bf16lo_to_f(y[i]), bf16lo_to_f(o), ff{a0.x, b0.x}, ff{-sign * a0.y, -sign * b0.y});
+        hi = rot_bf16(bf16hi_to_f(y[i]), bf16hi_to_f(o), ff{a1.x, b1.x}, ff{-sign * a1.y, -sign * b1.y});
+      }
+      y[i] = lo | (hi << 16);
+    }
+  } else if (R > 0) {
+    // the normed row to shared memory; the rotated dims are then spread over
+    // all lanes (dim e = lane + 32 k), whatever share of the row they are
+    uint32_t* nw = reinterpret_cast<uint32_t*>(nr) + lane * (E / 2);
+    uint16_t* rt = nr + D;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) nw[i] = y[i];
+    __syncwarp();
+    for (int e = lane; e < R; e += 32) {
+      const bool low = e < half;
+      const int j = low ? e : e - half;
+      const float2 a = ang.hi[row * half + j];
+      const float xe = bf16_to_f(nr[e]), xp = bf16_to_f(nr[low ? e + half : j]);
+      uint32_t r;
+      if (!rot_ends(xe, xp, a.x, low ? -a.y : a.y, r)) {
+        const float2 b = ang.lo[row * half + j];
+        r = rot_bf16(xe, xp, ff{a.x, b.x}, low ? ff{a.y, b.y} : ff{-a.y, -b.y});
+      }
+      rt[e] = (uint16_t)r;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const int e = lane * E + 2 * i;                     // R is even: e and e + 1 on the same side
+      if (e < R) y[i] = *reinterpret_cast<const uint32_t*>(rt + e);
+    }
+    __syncwarp();                                         // both rows read before the next item writes them
+  }
+}
+
+}  // namespace
+}  // namespace kvq

@@ -2,11 +2,15 @@
 // rows that read nothing, and the plan of the calls that cut their keys into
 // equal shares.
 #pragma once
+#include <algorithm>
+
 #include "kvq_paged.cuh"
-#include "kvq_qrows.cuh"
+#include "kvq_paged_prep.cuh"
 
 namespace kvq {
 namespace {
+
+constexpr int kPrWarps = 8;           // of the prep kernel's blocks
 
 // Rows of a read are taken in groups of at most TG consecutive rows of one
 // sequence.  Group u of sequence s with base(s) = floor(row_offsets[s] / TG) + s
@@ -58,38 +62,15 @@ inline int paged_groups(const PagedRows& r, int TG) {
   return r.row_offsets ? r.n_rows / TG + r.n_seqs : r.n_rows;
 }
 
-// Rows without keys: an idle sequence's are zeros, those past the table NaN.
-template <int D>
-__device__ __forceinline__ void paged_fill_rows(const DecodeArgs& a, const PagedArgs& pg, int rb, int bx) {
-  const int limit = pg.limit;
-  for (int row = bx * rb; row < min(a.n_rows, bx * rb + rb); ++row) {
-    int p, start;
-    if (a.row_offsets == nullptr) {
-      start = p = __ldg(a.pos + row);
-    } else {
-      const RowInfo ri = row_info(a, row);
-      start = __ldg(a.pos + ri.s);
-      p = ri.p;
-    }
-    if (start >= 0 && p >= 0 && p < limit) continue;
-    const float v = start < 0 ? 0.f : __int_as_float(0x7FC00000);
-    const size_t n = (size_t)a.L.n_q * D, at = (size_t)row * n;
-    for (size_t i = threadIdx.x; i < n; i += kQrWarps * 32) {
-      if (a.out_f32) reinterpret_cast<float*>(a.out)[at + i] = v;
-      else reinterpret_cast<uint16_t*>(a.out)[at + i] = start < 0 ? 0 : 0x7FC0;
-    }
-  }
-}
-
 // prefix[u] = key tiles of the groups before u (one block), and the call's
 // status word.
 __device__ __forceinline__ void paged_plan_block(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
                                                  int n_groups, long long* prefix, uint32_t* status) {
-  __shared__ int wsum[kQrWarps];
+  __shared__ int wsum[kPrWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long long base = 0;
   bool bad = false;
-  for (int u0 = 0; u0 < n_groups; u0 += kQrWarps * 32) {
+  for (int u0 = 0; u0 < n_groups; u0 += kPrWarps * 32) {
     const int u = u0 + tid;
     int t = 0;
     if (u < n_groups) {
@@ -106,7 +87,7 @@ __device__ __forceinline__ void paged_plan_block(const PagedRows& r, const Paged
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
     long long before = base, total = 0;
-    for (int w = 0; w < kQrWarps; ++w) {
+    for (int w = 0; w < kPrWarps; ++w) {
       if (w < warp) before += wsum[w];
       total += wsum[w];
     }
@@ -128,14 +109,14 @@ constexpr int kOrderBins = 2048;
 __device__ __forceinline__ void paged_order_block(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
                                                   int n_groups, int32_t* order, uint32_t* status) {
   __shared__ int bins[kOrderBins];
-  __shared__ int wsum[kQrWarps];
-  constexpr int PER = kOrderBins / (kQrWarps * 32);
+  __shared__ int wsum[kPrWarps];
+  constexpr int PER = kOrderBins / (kPrWarps * 32);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < kOrderBins; i += kQrWarps * 32) bins[i] = 0;
+  for (int i = tid; i < kOrderBins; i += kPrWarps * 32) bins[i] = 0;
   __syncthreads();
   bool bad = false;
   auto bin_of = [](int tiles) { return kOrderBins - 1 - min(tiles, kOrderBins - 1); };   // most first
-  for (int u = tid; u < n_groups; u += kQrWarps * 32) {
+  for (int u = tid; u < n_groups; u += kPrWarps * 32) {
     const PagedGroup g = paged_group(r, pg, window, TG, KT, u);
     bad |= g.bad > 0;
     atomicAdd(&bins[bin_of(g.tiles)], 1);
@@ -160,7 +141,7 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
 #pragma unroll
   for (int k = 0; k < PER; ++k) bins[PER * tid + k] = before + mine[k];
   const bool any = __syncthreads_or(bad);
-  for (int u = tid; u < n_groups; u += kQrWarps * 32) {
+  for (int u = tid; u < n_groups; u += kPrWarps * 32) {
     const PagedGroup g = paged_group(r, pg, window, TG, KT, u);
     order[atomicAdd(&bins[bin_of(g.tiles)], 1)] = u;
   }
@@ -168,46 +149,109 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
 }
 
 // Block 0 makes the plan (the tile prefix, or the order of the groups) and
-// writes the status word, the others prep rb rows each.
+// writes the status word; the others each prep rb rows of hpb heads, a warp a
+// (row, head) at a time: q_hat as f16 to q16 [n_rows][n_q][D] (exact for bf16 in
+// f16's normal range) and as bf16 to q_prepped.  Rows that read nothing get
+// their outputs here: zeros for an idle sequence, NaN past the table.
 template <int D>
-__global__ void __launch_bounds__(kQrWarps * 32)
-paged_prep_kernel(const DecodeArgs a, const PagedArgs pg, const RopeFreqs freqs, const int rb, const int TG,
-                  const int KT, const int n_groups, long long* prefix, int32_t* order, uint32_t* status) {
+__global__ void __launch_bounds__(kPrWarps * 32)
+paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, const int hpb, const int TG, const int KT,
+                  const int n_groups, uint16_t* q16, long long* prefix, int32_t* order, uint32_t* status) {
+  constexpr int E = D / 32;
+  extern __shared__ __align__(16) uint8_t pr_buf[];
+  __shared__ int rpos[16], rstart[16];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (blockIdx.x == 0) {
     pdl_wait();
     pdl_launch();
-    PagedRows r = {a.row_offsets, a.pos, a.n_seqs, a.n_rows};
-    if (prefix) paged_plan_block(r, pg, a.L.window, TG, KT, n_groups, prefix, status);
-    else paged_order_block(r, pg, a.L.window, TG, KT, n_groups, order, status);
-  } else {
-    qprep_rows_block<D>(a, freqs, rb, blockIdx.x - 1);
-    paged_fill_rows<D>(a, pg, rb, blockIdx.x - 1);
+    if (prefix) paged_plan_block(a.r, a.pg, a.L.window, TG, KT, n_groups, prefix, status);
+    else paged_order_block(a.r, a.pg, a.L.window, TG, KT, n_groups, order, status);
+    return;
+  }
+  const int R = a.L.rope_dims, half = R >> 1, n_q = a.L.n_q;
+  Angles ang = {reinterpret_cast<float2*>(pr_buf), reinterpret_cast<float2*>(pr_buf) + rb * half};
+  float (*freq)[3] = reinterpret_cast<float (*)[3]>(pr_buf + (size_t)rb * half * 16);
+  uint16_t* nr = reinterpret_cast<uint16_t*>(pr_buf + (size_t)rb * half * 16 + 16 * ((3 * half + 3) / 4)) + warp * 2 * D;
+  const int hb = (n_q + hpb - 1) / hpb;
+  const int row0 = (blockIdx.x - 1) / hb * rb, h0 = (blockIdx.x - 1) % hb * hpb;
+  const int n = min(rb, a.r.n_rows - row0), nh = min(hpb, n_q - h0);
+  // until the stream's previous kernel is complete only the frequency table is read
+  if (R > 0) stage_freqs(freqs.f, half, freq);
+  pdl_wait();
+  pdl_launch();
+  const auto source = [&](int it) {
+    const int r = it / nh;
+    return reinterpret_cast<const uint32_t*>(a.q_raw + ((size_t)(row0 + r) * n_q + h0 + it - r * nh) * D + lane * E);
+  };
+  uint32_t nx[E / 2];
+  if (warp < n * nh) {
+    const uint32_t* src = source(warp);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) nx[i] = src[i];
+  }
+  float w[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) w[i] = bf16_to_f(__ldg(a.q_w + lane * E + i));
+  if (tid < n) {
+    const int row = row0 + tid, s = paged_seq_of(a.r, row);
+    const SeqRows sr = paged_seq_rows(a.r, s);
+    rstart[tid] = sr.start;
+    rpos[tid] = sr.start < 0 ? 0 : sr.start + (row - sr.off);
+  }
+  __syncthreads();
+  for (int idx = tid; idx < n * half; idx += kPrWarps * 32) {
+    const int r = idx / half, j = idx - r * half;
+    put_angle<D>(ang, r, R, j, min(max(rpos[r], 0), (1 << 24) - 1), freq[j]);
+  }
+  __syncthreads();
+  for (int it = warp; it < n * nh; it += kPrWarps) {
+    const int r = it / nh, h = h0 + it - r * nh;
+    uint32_t raw[E / 2], y[E / 2];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) raw[i] = nx[i];
+    if (it + kPrWarps < n * nh) {
+      const uint32_t* src = source(it + kPrWarps);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) nx[i] = src[i];
+    }
+    prep_row<D>(raw, w, a.L.eps, R, ang, r, nr, y);
+    const size_t at = ((size_t)(row0 + r) * n_q + h) * D + lane * E;
+    uint32_t* d = reinterpret_cast<uint32_t*>(q16 + at);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) d[i] = pack_h2(bf16lo_to_f(y[i]), bf16hi_to_f(y[i]));
+    if (a.q_prepped) {                                    // (only 2-byte alignment is asked of it)
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        a.q_prepped[at + 2 * i] = (uint16_t)(y[i] & 0xFFFFu);
+        a.q_prepped[at + 2 * i + 1] = (uint16_t)(y[i] >> 16);
+      }
+    }
+    if (rstart[r] < 0 || rpos[r] < 0 || rpos[r] >= a.pg.limit) {
+      const bool idle = rstart[r] < 0;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (a.out_f32) reinterpret_cast<float*>(a.out)[at + i] = idle ? 0.f : __int_as_float(0x7FC00000);
+        else reinterpret_cast<uint16_t*>(a.out)[at + i] = idle ? 0 : 0x7FC0;
+      }
+    }
   }
 }
 
-// q_hat as f16 to q16 [n_rows][n_q][D]; `spare`: a word that qprep_rows_block
-// may clear in the place of a status word.
 template <int D>
 cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG, int KT, int n_groups, uint16_t* q16,
-                              long long* prefix, int32_t* order, uint32_t* status, uint32_t* spare,
-                              cudaStream_t st) {
-  DecodeArgs d = {};
-  d.L = a.L;
-  d.n_seqs = a.r.n_seqs;
-  d.n_rows = a.r.n_rows;
-  d.row_offsets = a.r.row_offsets;
-  d.pos = a.r.start;
-  d.q_raw = a.q_raw;
-  d.q_w = a.q_w;
-  d.out = a.out;
-  d.out_f32 = a.out_f32;
-  d.q_prepped = a.q_prepped;
-  d.ws.status = spare;
-  d.ws.q16 = q16;
-  const int rb = qprep_rows_rb(a.L);
-  const int nq = (a.r.n_rows + rb - 1) / rb;
-  return launch_pdl(paged_prep_kernel<D>, dim3(nq + 1), dim3(kQrWarps * 32), qprep_rows_smem(a.L, rb), st, d, a.pg, f,
-                    rb, TG, KT, n_groups, prefix, order, status);
+                              long long* prefix, int32_t* order, uint32_t* status, int num_sms, cudaStream_t st) {
+  // few rows: a head a warp, eight heads a block (latency); many: all heads of
+  // up to 16 rows, which share their angles (16 KB of them at most)
+  const int n_q = a.L.n_q, half = a.L.rope_dims / 2;
+  const bool few = (long long)a.r.n_rows * n_q <= 16ll * num_sms;
+  const int hpb = few ? std::min(n_q, kPrWarps) : n_q;
+  int rb = few ? std::max(1, kPrWarps / hpb) : std::max(1, std::min(16, a.r.n_rows / (6 * num_sms)));
+  if (half > 0) rb = std::max(1, std::min(rb, 1024 / half));
+  const size_t smem = (size_t)rb * half * 16 + 16 * ((3 * half + 3) / 4) + (size_t)kPrWarps * 2 * D * 2;
+  const long long blocks = (long long)((a.r.n_rows + rb - 1) / rb) * ((n_q + hpb - 1) / hpb) + 1;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_pdl(paged_prep_kernel<D>, dim3((unsigned)blocks), dim3(kPrWarps * 32), smem, st, a, f, rb, hpb, TG, KT,
+                    n_groups, q16, prefix, order, status);
 }
 
 }  // namespace

@@ -27,80 +27,6 @@ namespace {
 
 constexpr int kQrWarps = 8;
 
-// One row by one warp, D/32 elements per lane: RMSNorm of x with weight w,
-// then RoPE over the first R dims with the row's angles csr (R == D: pair j at
-// 16 * (j % E) + j / E, else pair j at j).  nr, rt: a shared row each of the
-// warp's own (R < D).  y and yw receive the bf16 row, as values and in pairs.
-template <int D>
-__device__ __forceinline__ void prep_row_warp(const float (&x)[D / 32], const float (&w)[D / 32], const float eps,
-                                              const int R, const float4* csr, uint16_t* nr, uint16_t* rt,
-                                              uint16_t (&y)[D / 32], uint32_t (&yw)[D / 64]) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, half = R >> 1;
-  // sum of squares in two independent float-float chains (more work in
-  // flight per warp), joined before the warp reduction
-  ff s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < E; i += 2) {
-    ff_acc_sq(s0, x[i]);
-    ff_acc_sq(s1, x[i + 1]);
-  }
-  const ff ss = ff_warp_sum(ff_add(s0, s1));
-  const ff inv = rms_inv(ss, D, eps);
-#pragma unroll
-  for (int i = 0; i < E; ++i) y[i] = norm_scale_bf16(x[i], w[i], inv);
-#pragma unroll
-  for (int i = 0; i < E; i += 2) yw[i / 2] = (uint32_t)y[i] | ((uint32_t)y[i + 1] << 16);
-  if (R == D) {
-    // x_e c - x_(e+D/2) s in lanes 0..15, x_e c + x_(e-D/2) s in lanes 16..31
-    const float4* csf = csr + (lane & 15);
-    const bool upper = lane >= 16;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float xe = bf16_to_f(y[i]);
-      const float xp = __shfl_xor_sync(0xffffffffu, xe, 16);
-      const float4 cv = csf[i * 16];
-      y[i] = rot_bf16(xe, xp, ff{cv.x, cv.y}, upper ? ff{-cv.z, -cv.w} : ff{cv.z, cv.w});
-    }
-#pragma unroll
-    for (int i = 0; i < E; i += 2) yw[i / 2] = (uint32_t)y[i] | ((uint32_t)y[i + 1] << 16);
-  } else if (R > 0) {
-    // the normed row to shared memory; the rotated dims are then spread over
-    // all lanes (dim e = lane + 32 k), whatever share of the row they are
-    uint32_t* nw = reinterpret_cast<uint32_t*>(nr) + lane * (E / 2);
-    if constexpr (E % 8 == 0) {
-#pragma unroll
-      for (int i = 0; i < E / 2; i += 4)
-        *reinterpret_cast<uint4*>(nw + i) = make_uint4(yw[i], yw[i + 1], yw[i + 2], yw[i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) nw[i] = yw[i];
-    }
-    __syncwarp();
-    for (int e = lane; e < R; e += 32) {
-      const bool lo = e < half;
-      const int j = lo ? e : e - half;
-      const float4 cv = csr[j];
-      rt[e] = rot_bf16(bf16_to_f(nr[e]), bf16_to_f(nr[lo ? e + half : j]), ff{cv.x, cv.y},
-                       lo ? ff{cv.z, cv.w} : ff{-cv.z, -cv.w});
-    }
-    __syncwarp();
-    if (lane * E < R) {                               // this lane holds rotated dims
-#pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const int e = lane * E + i;                   // R is even: e and e + 1 on the same side
-        if (e < R) yw[i / 2] = (uint32_t)rt[e] | ((uint32_t)rt[e + 1] << 16);
-      }
-#pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        y[i] = uint16_t(yw[i / 2] & 0xFFFFu);
-        y[i + 1] = uint16_t(yw[i / 2] >> 16);
-      }
-    }
-    __syncwarp();                                     // both rows read before the next item writes them
-  }
-}
-
 // One block: rows bx*rb .. bx*rb + rb - 1 of the call `a`.
 template <int D>
 __device__ __forceinline__ void qprep_rows_block(const DecodeArgs& a, const RopeFreqs& freqs, const int rb,
@@ -160,9 +86,71 @@ __device__ __forceinline__ void qprep_rows_block(const DecodeArgs& a, const Rope
       x[i] = bf16lo_to_f(u);
       x[i + 1] = bf16hi_to_f(u);
     }
+    // sum of squares in two independent float-float chains (more work in
+    // flight per warp), joined before the warp reduction
+    ff s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      ff_acc_sq(s0, x[i]);
+      ff_acc_sq(s1, x[i + 1]);
+    }
+    const ff ss = ff_warp_sum(ff_add(s0, s1));
+    const ff inv = rms_inv(ss, D, a.L.eps);
     uint16_t y[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] = norm_scale_bf16(x[i], wq[i], inv);
     uint32_t yw[E / 2];
-    prep_row_warp<D>(x, wq, a.L.eps, R, cs + r * half, nr, rt, y, yw);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) yw[i / 2] = (uint32_t)y[i] | ((uint32_t)y[i + 1] << 16);
+    if (R == D) {
+      // x_e c - x_(e+D/2) s in lanes 0..15, x_e c + x_(e-D/2) s in lanes 16..31
+      const float4* csr = cs + r * half + (lane & 15);
+      const bool upper = lane >= 16;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float xe = bf16_to_f(y[i]);
+        const float xp = __shfl_xor_sync(0xffffffffu, xe, 16);
+        const float4 cv = csr[i * 16];
+        y[i] = rot_bf16(xe, xp, ff{cv.x, cv.y}, upper ? ff{-cv.z, -cv.w} : ff{cv.z, cv.w});
+      }
+#pragma unroll
+      for (int i = 0; i < E; i += 2) yw[i / 2] = (uint32_t)y[i] | ((uint32_t)y[i + 1] << 16);
+    } else if (R > 0) {
+      // the normed row to shared memory; the rotated dims are then spread over
+      // all lanes (dim e = lane + 32 k), whatever share of the row they are
+      uint32_t* nw = reinterpret_cast<uint32_t*>(nr) + lane * (E / 2);
+      if constexpr (E % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < E / 2; i += 4)
+          *reinterpret_cast<uint4*>(nw + i) = make_uint4(yw[i], yw[i + 1], yw[i + 2], yw[i + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) nw[i] = yw[i];
+      }
+      __syncwarp();
+      const float4* csr = cs + r * half;
+      for (int e = lane; e < R; e += 32) {
+        const bool lo = e < half;
+        const int j = lo ? e : e - half;
+        const float4 cv = csr[j];
+        rt[e] = rot_bf16(bf16_to_f(nr[e]), bf16_to_f(nr[lo ? e + half : j]), ff{cv.x, cv.y},
+                         lo ? ff{cv.z, cv.w} : ff{-cv.z, -cv.w});
+      }
+      __syncwarp();
+      if (lane * E < R) {                               // this lane holds rotated dims
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          const int e = lane * E + i;                   // R is even: e and e + 1 on the same side
+          if (e < R) yw[i / 2] = (uint32_t)rt[e] | ((uint32_t)rt[e + 1] << 16);
+        }
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          y[i] = uint16_t(yw[i / 2] & 0xFFFFu);
+          y[i + 1] = uint16_t(yw[i / 2] >> 16);
+        }
+      }
+      __syncwarp();                                     // both rows read before the next item writes them
+    }
     if (a.q_prepped) {                                  // (only 2-byte alignment is asked of it)
       if ((reinterpret_cast<uintptr_t>(a.q_prepped) & 3u) == 0) {
         uint32_t* d = reinterpret_cast<uint32_t*>(a.q_prepped + base);
