@@ -10,11 +10,14 @@
 // so codes enter both products as the exact f16 values they stand for.
 //
 // Roles (one barrier pair per buffer, no block barrier in the loop):
-//   - converters: 16-byte loads of codes (the next tile's K or V in flight in
-//     registers while this one is converted), code pairs to f16, stored to the
-//     128-byte-swizzled rows of 64 dims that the MMA reads: K as a K-major
+//   - converters: a unit of work is 16 keys (one page, one scale) x up to 256 dims
+//     of K or V; the tiles' units are dealt over seven warps.  16-byte loads of codes,
+//     two or three units in flight per warp in registers, code pairs to f16, stored to
+//     the 128-byte-swizzled rows of 64 dims that the MMA reads: K as a K-major
 //     operand, V as an MN-major one (rows are keys in both, so one layout serves
-//     both).  Positions that no row sees are stored as zeros and not read.
+//     both).  Eight lanes take four chunks of two neighbouring rows, whose
+//     swizzles meet all banks.  Positions that no row sees are stored as zeros and
+//     not read.
 //   - one MMA thread: S = q K^T into a score slot of tensor memory, O += P V with
 //     P from tensor memory.  MT = 2 (head_dim <= 128): the two row tiles
 //     alternate, one's products run under the other's softmax.  MT = 1: two score
@@ -50,8 +53,12 @@ struct Pf {
   static constexpr int KT = D == 512 ? 64 : 128;        // keys per tile
   static constexpr int SUB = KT / 16;                   // scales per tile
   static constexpr int KST = D <= 128 ? 2 : 1;          // K and V stages
-  static constexpr int NC = 224;                        // converter threads
-  static constexpr int THREADS = 256 + NC + 32;         // 512: 128 registers each
+  static constexpr int CW = 7;                          // converter warps
+  static constexpr int THREADS = 256 + 32 * CW + 32;    // 512: 128 registers each
+  // a converter's unit: 16 keys x UD dims, UJ 16-byte loads per lane
+  static constexpr int UD = D < 256 ? D : 256, UJ = UD / 32;
+  static constexpr int UK = SUB * (D / UD), UV = SUB * (DO / UD);          // units of a tile
+  static constexpr int RING = D < 256 ? 3 : 2;          // units in flight per converter warp
   static constexpr int Q_BYTES = 128 * D * 2;           // of a row tile
   static constexpr int K_BYTES = KT * D * 2, V_BYTES = KT * DO * 2;
   static constexpr int K_OFF = MT * Q_BYTES;
@@ -62,8 +69,6 @@ struct Pf {
   static constexpr int USED = B_OFF + 160;
   // (one CTA per SM: each takes all of tensor memory)
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
-  static constexpr int KN = KT * D / 16, VN = KT * DO / 16;        // 16-byte loads of a tile
-  static constexpr int KV = (KN + NC - 1) / NC, VV = (VN + NC - 1) / NC;   // per converter thread
   static constexpr int C_S = MT * DO;                   // tensor-memory columns: O, then two score slots
   static_assert(C_S + 2 * KT <= 512, "tensor memory");
   static_assert(BYTES <= 227 * 1024, "shared memory");
@@ -72,6 +77,26 @@ struct Pf {
 __device__ __forceinline__ float pf_ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// pairs of floats in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ uint4 ldg_codes(const uint8_t* p) {
@@ -87,8 +112,7 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t lbo, u
 }
 constexpr uint32_t kMnMajorB = 1u << 16;                // instruction descriptor: B is MN-major
 
-__device__ __forceinline__ void pf_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
+__device__ __forceinline__ void pf_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
                "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -98,8 +122,15 @@ __device__ __forceinline__ void pf_ld32(uint32_t taddr, float (&v)[32]) {
                  "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
                  "=r"(r[30]), "=r"(r[31])
                : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// the loads of r are complete (its uses stay behind the wait)
+__device__ __forceinline__ void pf_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 __device__ __forceinline__ void pf_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -118,7 +149,7 @@ __global__ void __launch_bounds__(Pf<D>::THREADS, 1)
 paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, const int32_t* order, const uint16_t* q16,
                      float* part_o, float* part_ml, uint32_t* status) {
   using S = Pf<D>;
-  constexpr int MT = S::MT, DO = S::DO, KT = S::KT, SUB = S::SUB, KST = S::KST, NC = S::NC;
+  constexpr int MT = S::MT, DO = S::DO, KT = S::KT, SUB = S::SUB, KST = S::KST;
   constexpr float L2E = 1.4426950408889634f;
   constexpr float kSlack = 8.f, kTop = 7.f;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -140,7 +171,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   const int rows = g.nt * G;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::B_OFF);
-  uint64_t* k_full = bars;                                // [2] (converter warps)
+  uint64_t* k_full = bars;                                // [2] (converters' units)
   uint64_t* k_empty = bars + 2;                           // [2]
   uint64_t* v_full = bars + 4;                            // [2]
   uint64_t* v_empty = bars + 6;                           // [2]
@@ -151,8 +182,8 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   const uint32_t sb = smem_u32(sm);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, NC / 32);
-      mbar_init(v_full + i, NC / 32);
+      mbar_init(k_full + i, S::UK);
+      mbar_init(v_full + i, S::UV);
       mbar_init(k_empty + i, 1);
       mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
@@ -186,19 +217,21 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     }
   };
 
-  if (warp == 8 + NC / 32) {
+  if (warp == 8 + S::CW) {
     // ================= products =================
     constexpr uint32_t ID_QK = tc::idesc_f16_f32(128, KT), ID_PV = tc::idesc_f16_f32(128, DO) | kMnMajorB;
     const bool leader = lane == 0;
+    // descriptors of the first steps; an address step of b bytes adds b / 16
+    const uint64_t q_desc = tc::desc_kmajor_sw128(sb, 1024), k_desc = tc::desc_kmajor_sw128(sb + S::K_OFF, 1024),
+                   v_desc = desc_mn_sw128(sb + S::V_OFF, KT * 128, 1024);
     auto qk = [&](int m, int i) {                         // slot: MT == 2: m, else i & 1
       const int slot = MT == 2 ? m : i & 1, st = i % KST;
       if (leader) {
+        const uint64_t qd = q_desc + m * (S::Q_BYTES / 16), kd = k_desc + st * (S::K_BYTES / 16);
+        const uint32_t d = tmem + S::C_S + KT * slot;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
-          tc::mma_f16(tmem + S::C_S + KT * slot,
-                      tc::desc_kmajor_sw128(sb + m * S::Q_BYTES + (s >> 2) * 16384 + 32 * (s & 3), 1024),
-                      tc::desc_kmajor_sw128(sb + S::K_OFF + st * S::K_BYTES + (s >> 2) * (KT * 128) + 32 * (s & 3), 1024),
-                      ID_QK, s != 0);
+          tc::mma_f16(d, qd + (s >> 2) * 1024 + 2 * (s & 3), kd + (s >> 2) * (KT * 8) + 2 * (s & 3), ID_QK, s != 0);
         tc::commit(s_full + slot);
       }
       __syncwarp();
@@ -206,12 +239,12 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     auto pv = [&](int m, int i) {
       const int slot = MT == 2 ? m : i & 1, st = i % KST;
       if (leader) {
+        const uint64_t vd = v_desc + st * (S::V_BYTES / 16);
+        const uint32_t p = tmem + S::C_S + KT * slot;
 #pragma unroll
         for (int s = 0; s < KT / 16; ++s) {
           const int col = MT == 2 ? 8 * s : (s / (KT / 32)) * (KT / 2) + 8 * (s % (KT / 32));
-          tc::mma_f16_ts(tmem + m * DO, tmem + S::C_S + KT * slot + col,
-                         desc_mn_sw128(sb + S::V_OFF + st * S::V_BYTES + 2048 * s, KT * 128, 1024), ID_PV,
-                         i > 0 || s > 0);
+          tc::mma_f16_ts(tmem + m * DO, p + col, vd + 128 * s, ID_PV, i > 0 || s > 0);
         }
       }
       __syncwarp();
@@ -247,111 +280,122 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     done(o_full);
   } else if (warp >= 8) {
     // ================= converters =================
-    const int ct = tid - 256, cw = warp - 8;
-    constexpr int CK = D / 16, CV = DO / 16;              // 16-byte chunks of a key
+    constexpr int UK = S::UK, UV = S::UV, UJ = S::UJ, RING = S::RING;
     const int32_t* table = a.pg.tables + (size_t)g.s * a.pg.max_pages;
-    // lane s < SUB: the page of 16 positions s of tile t (-2: none is seen)
-    auto look_up = [&](int t) {
-      const int key = k0 + KT * t + 16 * lane;
-      int id = -2;
-      if (lane < SUB && t < n && key <= g.hi && key + 15 >= g.lo) id = __ldg(table + (key >> sh));
-      return id;
-    };
-    auto checked = [&](int id) {
-      if (id == -2) return -1;
-      if ((unsigned)id < (unsigned)a.pg.n_pages) return id;
-      ctl[1] = 1;
-      return -1;
-    };
-    auto load = [&](const uint8_t* codes, int t, int pid, int key_l, int c) {   // chunk c of key key_l of tile t
-      const int id = __shfl_sync(0xffffffffu, pid, key_l >> 4);
-      const int key = k0 + KT * t + key_l;
-      uint4 v = {0u, 0u, 0u, 0u};
-      if (id >= 0 && key >= g.lo && key <= g.hi)
-        v = ldg_codes(codes + ((((size_t)id * n_kv + h) << sh) + (key & (P - 1))) * D + 16 * c);
-      return v;
-    };
-    // chunk c (16 dims) of row key_l: two swizzled 16-byte chunks of f16; odd
-    // 64-dim blocks write theirs in the other order, so that the lanes of a key
-    // meet all banks
-    auto store = [&](uint32_t base, int key_l, int c, uint4 v) {
-      uint32_t o[8];
-      codes_to_h2<E4M3>(v.x, o[0], o[1]);
-      codes_to_h2<E4M3>(v.y, o[2], o[3]);
-      codes_to_h2<E4M3>(v.z, o[4], o[5]);
-      codes_to_h2<E4M3>(v.w, o[6], o[7]);
-      uint8_t* row = sm + base + (c >> 2) * (KT * 128);
-      const int c0 = 2 * (c & 3), odd = (c >> 2) & 1;
-      const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-      *reinterpret_cast<uint4*>(row + tc::sw128_off(key_l, c0 + odd)) = odd ? hi : lo;
-      *reinterpret_cast<uint4*>(row + tc::sw128_off(key_l, c0 + 1 - odd)) = odd ? lo : hi;
-    };
-    uint4 ka[S::KV], va[S::VV];
-    float sk = 0.f, sv = 0.f;
-    auto load_k = [&](int t, int pid) {
-#pragma unroll
-      for (int j = 0; j < S::KV; ++j) {
-        const int x = min(j * NC + ct, S::KN - 1);
-        ka[j] = load(a.pg.k_codes, t, pid, x / CK, x % CK);
-      }
-      if (cw == 0) {                                      // lane s: the scales of its 16 positions
-        sk = sv = 0.f;
-        if (lane < SUB && pid >= 0) {
-          sk = __ldg(a.pg.k_scales + (size_t)pid * n_kv + h);
-          sv = __ldg(a.pg.v_scales + (size_t)pid * n_kv + h);
+    const size_t page_bytes = ((size_t)n_kv << sh) * D;
+    // the lane's first row of a unit and 16-dim chunk of its 64-dim blocks
+    const int r0 = 2 * (lane >> 3) + ((lane >> 2) & 1), c0 = lane & 3;
+    const uint32_t s_lane = tc::sw128_off(r0, 2 * c0);
+    const size_t head = ((size_t)h << sh) * D + r0 * D + 16 * c0;
+    // the CTA's units: K(0), then K(i + 1) and V(i) for each tile i (K runs a
+    // tile ahead); each warp takes every CW-th, and walks them three times:
+    // pages, loads, stores
+    struct Walk {
+      int i, in;                                          // tile, unit of K(i + 1) and V(i); i = -1: K(0)
+      __device__ explicit Walk(int first) : i(-1), in(first) {
+        if (in >= UK) {
+          in -= UK;
+          i = 0;
         }
       }
+      __device__ void next() {
+        in += S::CW;
+        const int all = i < 0 ? UK : UK + UV;
+        if (in >= all) {
+          in -= all;
+          ++i;
+        }
+      }
+      __device__ bool v() const { return in >= UK; }
+      __device__ int tile() const { return v() ? i : i + 1; }
+      __device__ int sub() const { return (v() ? in - UK : in) % SUB; }
+      __device__ int blk() const { return (v() ? in - UK : in) / SUB; }
     };
-    auto load_v = [&](int t, int pid) {
+    // page of a unit (raw entry; -2: no row sees it)
+    auto look_up = [&](const Walk& x) {
+      int id = -2;
+      const int key = k0 + KT * x.tile() + 16 * x.sub();
+      if (x.tile() < n && key <= g.hi && key + 15 >= g.lo) id = __ldg(table + (key >> sh));
+      return id;
+    };
+    uint4 buf[RING][UJ];
+    float2 scl[RING];
+    auto load = [&](uint4 (&v)[UJ], float2& sc2, const Walk& x, int raw) {
 #pragma unroll
-      for (int j = 0; j < S::VV; ++j) {
-        const int x = min(j * NC + ct, S::VN - 1);
-        va[j] = load(a.pg.v_codes, t, pid, x / CV, d_base / 16 + x % CV);
+      for (int j = 0; j < UJ; ++j) v[j] = make_uint4(0u, 0u, 0u, 0u);
+      sc2 = make_float2(0.f, 1.f);
+      if (raw == -2) return;
+      if ((unsigned)raw >= (unsigned)a.pg.n_pages) {
+        ctl[1] = 1;
+        return;
+      }
+      const int key = k0 + KT * x.tile() + 16 * x.sub();
+      const uint8_t* src = (x.v() ? a.pg.v_codes + d_base : a.pg.k_codes) + head + raw * page_bytes +
+                           (key & (P - 1)) * D + x.blk() * S::UD;
+      constexpr int NBK = S::UD / 64;                     // 64-dim blocks of a unit
+#pragma unroll
+      for (int j = 0; j < UJ; ++j) {
+        const int dr = 8 * (j / NBK), k = key + r0 + dr;
+        if (k >= g.lo && k <= g.hi) v[j] = ldg_codes(src + dr * D + 64 * (j % NBK));
+      }
+      if (!x.v() && x.blk() == 0) {
+        sc2.x = __ldg(a.pg.k_scales + (size_t)raw * n_kv + h);
+        sc2.y = __ldg(a.pg.v_scales + (size_t)raw * n_kv + h);
       }
     };
-    auto store_k = [&](int t) {
-      const int st = t % KST;
-      wait(k_empty + st, ((t / KST) & 1) ^ 1);
-      if (cw == 0 && lane < SUB) {
-        const float one = sv > 0.f ? sv : 1.f;
-        *reinterpret_cast<float4*>(sm + S::SC_OFF + ((t & 3) * SUB + lane) * 16) =
-            make_float4(sk * L2E, __log2f(one), __fdividef(1.f, one), 0.f);
+    auto put = [&](const uint4 (&v)[UJ], float2 sc2, const Walk& x) {
+      const int t = x.tile(), st = t % KST;
+      if (t >= n) return;                                 // (there is no K behind the last tile)
+      wait((x.v() ? v_empty : k_empty) + st, ((t / KST) & 1) ^ 1);
+      if (!x.v() && x.blk() == 0 && lane == 0) {
+        const float one = sc2.y > 0.f ? sc2.y : 1.f;
+        *reinterpret_cast<float4*>(sm + S::SC_OFF + ((t & 3) * SUB + x.sub()) * 16) =
+            make_float4(fmaxf(sc2.x * L2E, 1e-30f), __log2f(one), __fdividef(1.f, one), 0.f);
       }
+      constexpr int NBK = S::UD / 64;
+      uint8_t* at = sm + (x.v() ? S::V_OFF + st * S::V_BYTES : S::K_OFF + st * S::K_BYTES) +
+                    x.blk() * NBK * (KT * 128) + x.sub() * 2048;
 #pragma unroll
-      for (int j = 0; j < S::KV; ++j) {
-        const int x = j * NC + ct;
-        if (x < S::KN) store(S::K_OFF + st * S::K_BYTES, x / CK, x % CK, ka[j]);
+      for (int j = 0; j < UJ; ++j) {
+        uint32_t o[8];
+        codes_to_h2<E4M3>(v[j].x, o[0], o[1]);
+        codes_to_h2<E4M3>(v[j].y, o[2], o[3]);
+        codes_to_h2<E4M3>(v[j].z, o[4], o[5]);
+        codes_to_h2<E4M3>(v[j].w, o[6], o[7]);
+        uint8_t* d = at + 1024 * (j / NBK) + (KT * 128) * (j % NBK);
+        *reinterpret_cast<uint4*>(d + s_lane) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(d + (s_lane ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(k_full + st);
+      if (lane == 0) mbar_arrive((x.v() ? v_full : k_full) + st);
     };
-    // K runs a tile ahead of V: K(0), K(1), V(0), K(2), V(1), .., each loaded
-    // while the one before it waits or is stored
-    int pid1 = checked(look_up(0)), raw = look_up(1);
-    load_k(0, pid1);
-    load_v(0, pid1);
-    store_k(0);
-    pid1 = checked(raw);
-    raw = look_up(2);
-    if (n > 1) load_k(1, pid1);
-    for (int i = 0; i < n; ++i) {
-      const int st = i % KST;
-      const int pid2 = checked(raw);                      // of tile i + 2 (pid1: of i + 1)
-      raw = look_up(i + 3);
-      if (i + 1 < n) store_k(i + 1);
-      if (i + 2 < n) load_k(i + 2, pid2);
-      wait(v_empty + st, ((i / KST) & 1) ^ 1);
+    Walk page(warp - 8), ahead = page, now = page;
+    int raw[RING];
 #pragma unroll
-      for (int j = 0; j < S::VV; ++j) {
-        const int x = j * NC + ct;
-        if (x < S::VN) store(S::V_OFF + st * S::V_BYTES, x / CV, x % CV, va[j]);
+    for (int b = 0; b < RING; ++b) {
+      raw[b] = look_up(page);
+      page.next();
+    }
+#pragma unroll
+    for (int b = 0; b < RING; ++b) {
+      load(buf[b], scl[b], ahead, raw[b]);
+      ahead.next();
+      raw[b] = look_up(page);
+      page.next();
+    }
+    while (now.i < n) {
+#pragma unroll
+      for (int b = 0; b < RING; ++b) {
+        if (now.i < n) {
+          put(buf[b], scl[b], now);
+          now.next();
+          load(buf[b], scl[b], ahead, raw[b]);
+          ahead.next();
+          raw[b] = look_up(page);
+          page.next();
+        }
       }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_full + st);
-      if (i + 1 < n) load_v(i + 1, pid1);
-      pid1 = pid2;
     }
   } else {
     // ================= softmax =================
@@ -380,27 +424,35 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       const int key0 = k0 + KT * i + (MT == 2 ? 0 : (KT / 2) * wg);
       const bool whole = key0 >= lo_max && key0 + NK - 1 <= p_min;
       // ---- the tile's largest t ----
+      // (a masked score is -inf; the scales in shared memory are above 0)
+      auto hide = [&](uint32_t (&v)[32], int c) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int key = key0 + 32 * c + e;
+          v[e] = key <= p_r && key >= lo_r ? v[e] : 0xFF800000u;
+        }
+      };
+      // (a chunk of 32 scores is loaded while the one before it is worked on)
+      uint32_t vb[2][32];
       float top = -INFINITY;
+      pf_ld32(t_s, vb[0]);
 #pragma unroll
       for (int c = 0; c < NK / 32; ++c) {
-        float v[32];
-        pf_ld32(t_s + 32 * c, v);
-        tc::wait_ld();
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int key = key0 + 32 * c + e;
-            v[e] = key <= p_r && key >= lo_r ? v[e] : -INFINITY;
-          }
-        }
+        uint32_t (&v)[32] = vb[c & 1];
+        pf_wait(v);
+        pf_ld32(t_s + (c + 1 < NK / 32 ? 32 * (c + 1) : 0), vb[(c + 1) & 1]);   // (the last: the first again)
+        if (!whole) hide(v, c);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          float x = v[16 * b];
+          float x0 = __uint_as_float(v[16 * b]), x1 = __uint_as_float(v[16 * b + 1]);
 #pragma unroll
-          for (int e = 1; e < 16; ++e) x = fmaxf(x, v[16 * b + e]);
+          for (int e = 2; e < 14; e += 4) {
+            x0 = max3(x0, __uint_as_float(v[16 * b + e]), __uint_as_float(v[16 * b + e + 1]));
+            x1 = max3(x1, __uint_as_float(v[16 * b + e + 2]), __uint_as_float(v[16 * b + e + 3]));
+          }
+          x0 = max3(x0, __uint_as_float(v[16 * b + 14]), __uint_as_float(v[16 * b + 15]));
           const float4 f = sc[2 * c + b];
-          // (a masked subtile of scale 0 would read -inf * 0)
-          top = fmaxf(top, x == -INFINITY ? x : fmaf(x, f.x, f.y));
+          top = fmaxf(top, fmaf(fmaxf(x0, x1), f.x, f.y));
         }
       }
       if constexpr (MT == 1) {                            // the other half's
@@ -438,35 +490,31 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       const float base = ref == -INFINITY ? 0.f : ref - kTop;
 #pragma unroll
       for (int c = 0; c < NK / 32; ++c) {
-        float v[32];
-        pf_ld32(t_s + 32 * c, v);
-        tc::wait_ld();
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int key = key0 + 32 * c + e;
-            v[e] = key <= p_r && key >= lo_r ? v[e] : -INFINITY;
-          }
-        }
+        uint32_t (&v)[32] = vb[c & 1];
+        pf_wait(v);
+        if (c + 1 < NK / 32) pf_ld32(t_s + 32 * (c + 1), vb[(c + 1) & 1]);
+        if (!whole) hide(v, c);
         uint32_t pw[16];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const float4 f = sc[2 * c + b];
           const float off = f.y - base;
-          float s0 = 0.f, s1 = 0.f;
+          float2 s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float x0 = fmaf(v[16 * b + e], f.x, off), x1 = fmaf(v[16 * b + e + 1], f.x, off);
-            if (!whole) {                                 // (-inf * 0)
-              x0 = v[16 * b + e] == -INFINITY ? -INFINITY : x0;
-              x1 = v[16 * b + e + 1] == -INFINITY ? -INFINITY : x1;
-            }
-            const float p0 = pf_ex2(x0), p1 = pf_ex2(x1);
-            s0 += p0;
-            s1 += p1;
-            pw[8 * b + e / 2] = pack_h2(p0, p1);
+          for (int e = 0; e < 16; e += 4) {
+            float2 x = fma2(make_float2(__uint_as_float(v[16 * b + e]), __uint_as_float(v[16 * b + e + 1])),
+                            make_float2(f.x, f.x), make_float2(off, off));
+            float2 y = fma2(make_float2(__uint_as_float(v[16 * b + e + 2]), __uint_as_float(v[16 * b + e + 3])),
+                            make_float2(f.x, f.x), make_float2(off, off));
+            x = make_float2(pf_ex2(x.x), pf_ex2(x.y));
+            y = make_float2(pf_ex2(y.x), pf_ex2(y.y));
+            s0 = add2(s0, x);
+            s1 = add2(s1, y);
+            pw[8 * b + e / 2] = pack_h2(x.x, x.y);
+            pw[8 * b + e / 2 + 1] = pack_h2(y.x, y.y);
           }
-          l = fmaf(s0 + s1, f.z, l);
+          s0 = add2(s0, s1);
+          l = fmaf(s0.x + s0.y, f.z, l);
         }
         pf_st16(t_s + 16 * c, pw);
       }
