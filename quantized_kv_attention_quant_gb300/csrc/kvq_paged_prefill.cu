@@ -36,6 +36,7 @@
 // the keys when there are too few of them to fill the GPU; paged_join_kernel
 // joins the pieces in order.
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_paged.cuh"
 #include "kvq_paged_rows.cuh"
@@ -217,7 +218,11 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     }
   };
 
-  if (warp == 8 + S::CW) {
+  // MT == 2: a row of 128 scores stays in registers: 168 for the softmax threads,
+  // 88 for the others (256 threads each of the launch's 512 x 128)
+  if (warp >= 8) {
+   if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+   if (warp == 8 + S::CW) {
     // ================= products =================
     constexpr uint32_t ID_QK = tc::idesc_f16_f32(128, KT), ID_PV = tc::idesc_f16_f32(128, DO) | kMnMajorB;
     const bool leader = lane == 0;
@@ -278,7 +283,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       if (MT == 2 && nx < n) done(k_empty + nx % KST);
     }
     done(o_full);
-  } else if (warp >= 8) {
+   } else {
     // ================= converters =================
     constexpr int UK = S::UK, UV = S::UV, UJ = S::UJ, RING = S::RING;
     const int32_t* table = a.pg.tables + (size_t)g.s * a.pg.max_pages;
@@ -397,8 +402,10 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
         }
       }
     }
+   }
   } else {
     // ================= softmax =================
+    if constexpr (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     constexpr int NK = MT == 2 ? KT : KT / 2;             // keys of a tile per thread
     const int wg = warp >> 2;                             // row tile, or half of the keys
     const int m = MT == 2 ? wg : 0;
@@ -423,34 +430,35 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       const float4* sc = reinterpret_cast<const float4*>(sm + S::SC_OFF) + (i & 3) * SUB + (MT == 2 ? 0 : (SUB / 2) * wg);
       const int key0 = k0 + KT * i + (MT == 2 ? 0 : (KT / 2) * wg);
       const bool whole = key0 >= lo_max && key0 + NK - 1 <= p_min;
-      // ---- the tile's largest t ----
+      // ---- the scores, and the tile's largest t ----
       // (a masked score is -inf; the scales in shared memory are above 0)
-      auto hide = [&](uint32_t (&v)[32], int c) {
+      constexpr int NCH = NK / 32;
+      uint32_t v[NCH][32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int key = key0 + 32 * c + e;
-          v[e] = key <= p_r && key >= lo_r ? v[e] : 0xFF800000u;
-        }
-      };
-      // (a chunk of 32 scores is loaded while the one before it is worked on)
-      uint32_t vb[2][32];
+      for (int c = 0; c < NCH; ++c) pf_ld32(t_s + 32 * c, v[c]);
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) pf_wait(v[c]);
+      if (!whole) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int key = key0 + 32 * c + e;
+            v[c][e] = key <= p_r && key >= lo_r ? v[c][e] : 0xFF800000u;
+          }
+      }
       float top = -INFINITY;
-      pf_ld32(t_s, vb[0]);
 #pragma unroll
-      for (int c = 0; c < NK / 32; ++c) {
-        uint32_t (&v)[32] = vb[c & 1];
-        pf_wait(v);
-        pf_ld32(t_s + (c + 1 < NK / 32 ? 32 * (c + 1) : 0), vb[(c + 1) & 1]);   // (the last: the first again)
-        if (!whole) hide(v, c);
+      for (int c = 0; c < NCH; ++c) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          float x0 = __uint_as_float(v[16 * b]), x1 = __uint_as_float(v[16 * b + 1]);
+          float x0 = __uint_as_float(v[c][16 * b]), x1 = __uint_as_float(v[c][16 * b + 1]);
 #pragma unroll
           for (int e = 2; e < 14; e += 4) {
-            x0 = max3(x0, __uint_as_float(v[16 * b + e]), __uint_as_float(v[16 * b + e + 1]));
-            x1 = max3(x1, __uint_as_float(v[16 * b + e + 2]), __uint_as_float(v[16 * b + e + 3]));
+            x0 = max3(x0, __uint_as_float(v[c][16 * b + e]), __uint_as_float(v[c][16 * b + e + 1]));
+            x1 = max3(x1, __uint_as_float(v[c][16 * b + e + 2]), __uint_as_float(v[c][16 * b + e + 3]));
           }
-          x0 = max3(x0, __uint_as_float(v[16 * b + 14]), __uint_as_float(v[16 * b + 15]));
+          x0 = max3(x0, __uint_as_float(v[c][16 * b + 14]), __uint_as_float(v[c][16 * b + 15]));
           const float4 f = sc[2 * c + b];
           top = fmaxf(top, fmaf(fmaxf(x0, x1), f.x, f.y));
         }
@@ -489,11 +497,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       // ---- P ----
       const float base = ref == -INFINITY ? 0.f : ref - kTop;
 #pragma unroll
-      for (int c = 0; c < NK / 32; ++c) {
-        uint32_t (&v)[32] = vb[c & 1];
-        pf_wait(v);
-        if (c + 1 < NK / 32) pf_ld32(t_s + 32 * (c + 1), vb[(c + 1) & 1]);
-        if (!whole) hide(v, c);
+      for (int c = 0; c < NCH; ++c) {
         uint32_t pw[16];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -502,9 +506,9 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
           float2 s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            float2 x = fma2(make_float2(__uint_as_float(v[16 * b + e]), __uint_as_float(v[16 * b + e + 1])),
+            float2 x = fma2(make_float2(__uint_as_float(v[c][16 * b + e]), __uint_as_float(v[c][16 * b + e + 1])),
                             make_float2(f.x, f.x), make_float2(off, off));
-            float2 y = fma2(make_float2(__uint_as_float(v[16 * b + e + 2]), __uint_as_float(v[16 * b + e + 3])),
+            float2 y = fma2(make_float2(__uint_as_float(v[c][16 * b + e + 2]), __uint_as_float(v[c][16 * b + e + 3])),
                             make_float2(f.x, f.x), make_float2(off, off));
             x = make_float2(pf_ex2(x.x), pf_ex2(x.y));
             y = make_float2(pf_ex2(y.x), pf_ex2(y.y));
@@ -642,6 +646,21 @@ paged_join_kernel(const PagedReadArgs a, const int TQ, const int splits, const f
   }
 }
 
+// setmaxnreg hands out the registers that the block was launched with: a build
+// that needs fewer than 128 a thread would wait forever, so it is refused.
+template <int D, bool E4M3>
+cudaError_t check_registers() {
+  if (Pf<D>::MT != 2) return cudaSuccess;
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, paged_prefill_kernel<D, E4M3>);
+    if (e != cudaSuccess) return e;
+    regs.store(at.numRegs, std::memory_order_relaxed);
+  }
+  return regs.load(std::memory_order_relaxed) == 128 ? cudaSuccess : cudaErrorLaunchOutOfResources;
+}
+
 struct PfPlan { int TQ, n_groups, splits; long long units; };
 template <int D>
 PfPlan pf_plan(const LayerArgs& L, int n_seqs, int n_rows, int max_pos, int num_sms) {
@@ -689,7 +708,9 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   int32_t* order = reinterpret_cast<int32_t*>(b + w.order);
   float* part_o = reinterpret_cast<float*>(b + w.part_o);
   float* part_ml = reinterpret_cast<float*>(b + w.part_ml);
-  cudaError_t e = launch_paged_prep<D>(a, f, p.TQ, S::KT, p.n_groups, q16, nullptr, order, status, num_sms, st);
+  cudaError_t e = check_registers<D, E4M3>();
+  if (e != cudaSuccess) return e;
+  e = launch_paged_prep<D>(a, f, p.TQ, S::KT, p.n_groups, q16, nullptr, order, status, num_sms, st);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(paged_prefill_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (e != cudaSuccess) return e;
