@@ -9,9 +9,9 @@
 //   s_new = largest / 127 (int8) or / 448 (e4m3), 0 below 2^-40,
 //   s     = max(s_new, s_old) if the page already holds rows, else s_new,
 // writes code = round(x / s) for the new rows; where s grew, the rows that
-// were there become round(code * s_old / s).  All in IEEE fp32 (a multiply by
-// the reciprocal decides where it is clear of a rounding boundary, else a
-// division).  Units: rows row_offsets[s] .. of sequence s touch at most
+// were there become round(code * s_old / s).  All in IEEE fp32 (products with
+// the reciprocal, a little more and a little less, decide where they round to
+// the same code, else a division).  Units: rows row_offsets[s] .. of sequence s touch at most
 // floor(rows / P) + 2 pages, so unit u of sequence s with base(s) =
 // floor(row_offsets[s] / P) + 2 s is its page number u - base(s); units past
 // the sequence's last page leave at once.  One warp preps a row (an element
@@ -23,7 +23,6 @@
 // against blocks enough to fill the GPU.
 #include <algorithm>
 
-#include "kvq_append.cuh"
 #include "kvq_paged.cuh"
 #include "kvq_paged_prep.cuh"
 
@@ -44,6 +43,42 @@ __host__ __device__ inline PaSmem pa_smem(int D, int half, int hb, int cap, int 
   m.nrm = m.freq + 16 * (size_t)((3 * half + 3) / 4);
   m.total = m.nrm + (size_t)kPaWarps * 2 * D * 2;
   return m;
+}
+
+// Codes of E bf16 values (pairs in src) at scale s.  x times the rounded
+// reciprocal is within 2^-23 of x / s, and fl32(x / s) within 2^-24: where both
+// ends of 2^-21 around the product give one code, that is round(fl32(x / s)).
+template <int E, bool E4M3>
+__device__ __forceinline__ void encode_row(const uint32_t (&src)[E / 2], float s, uint32_t (&o)[(E + 3) / 4]) {
+  constexpr float kRound = 12582912.f;                    // 1.5 * 2^23: the sum's last bit is 1
+#pragma unroll
+  for (int i = 0; i < (E + 3) / 4; ++i) o[i] = 0u;
+  if (!(s > 0.f)) return;
+  const float rcp = __frcp_rn(s), up = rcp * (1.f + 4.76837158203125e-7f), dn = rcp * (1.f - 4.76837158203125e-7f);
+  bool same = true;
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float x0 = bf16lo_to_f(src[i]), x1 = bf16hi_to_f(src[i]);
+    uint32_t two;
+    if constexpr (E4M3) {
+      uint16_t a, b;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x1 * up), "f"(x0 * up));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(x1 * dn), "f"(x0 * dn));
+      same &= a == b;
+      two = a;
+    } else {
+      const uint32_t a0 = __float_as_uint(__fmaf_rn(x0, up, kRound)), a1 = __float_as_uint(__fmaf_rn(x1, up, kRound));
+      same &= a0 == __float_as_uint(__fmaf_rn(x0, dn, kRound)) && a1 == __float_as_uint(__fmaf_rn(x1, dn, kRound));
+      two = prmt(a0, a1, 0x4440u) & 0xFFFFu;              // (|x / s| < 127.5: no code leaves its byte)
+    }
+    o[i / 2] |= two << (16 * (i & 1));
+  }
+  if (same) return;
+#pragma unroll
+  for (int i = 0; i < (E + 3) / 4; ++i) o[i] = 0u;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    o[i / 4] |= encode_q<E4M3>(__fdiv_rn((i & 1) ? bf16hi_to_f(src[i / 2]) : bf16lo_to_f(src[i / 2]), s)) << (8 * (i & 3));
 }
 
 template <int D, bool E4M3>
@@ -91,6 +126,15 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
   for (int i = 0; i < E; ++i) w[i] = kind == 0 ? bf16_to_f(__ldg(a.k_w + lane * E + i)) : 1.f;
   const uint16_t* raw = (kind == 0 || a.L.k_eq_v) ? a.k_raw : a.v_raw;
 
+  // (row, head) items of the warp
+  struct Item { int r, h; };
+  const auto step = [&](Item& it) {
+    it.h += kPaWarps;
+    while (it.h >= nh) {
+      it.h -= nh;
+      ++it.r;
+    }
+  };
   // ---- prep, rb rows at a time ----
   for (int c0 = 0; c0 < n; c0 += rb) {
     const int cnt = min(rb, n - c0);
@@ -102,26 +146,31 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
       }
     }
     __syncthreads();
-    for (int it = warp; it < cnt * nh; it += kPaWarps) {
-      const int r = it / nh, hh = it - r * nh;
-      const size_t row = (size_t)(row0 + c0 + r);
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(raw + (row * n_kv + h0 + hh) * D + lane * E);
+    Item at = {warp / nh, warp % nh}, ahead = at;
+    uint32_t nx[E / 2] = {};
+    const auto fetch = [&](const Item& it) {
+      if (it.r < cnt) load_pairs<E>(nx, raw + ((size_t)(row0 + c0 + it.r) * n_kv + h0 + it.h) * D + lane * E);
+    };
+    fetch(ahead);
+    step(ahead);
+    for (; at.r < cnt; step(at)) {
+      const int r = at.r, hh = at.h;
       uint32_t x[E / 2], y[E / 2];
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) x[i] = __ldg(src + i);
+      for (int i = 0; i < E / 2; ++i) x[i] = nx[i];
+      fetch(ahead);
+      step(ahead);
       prep_row<D>(x, w, a.L.eps, R, ang, r, nr, y);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(rows + ((size_t)hh * cap + c0 + r) * D + lane * E);
+      store_pairs<E>(rows + (hh * cap + c0 + r) * D + lane * E, y);
       float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
+      for (int i = 0; i < E / 2; ++i)
         top = fmaxf(top, fmaxf(fabsf(bf16lo_to_f(y[i])), fabsf(bf16hi_to_f(y[i]))));
-        dst[i] = y[i];
-      }
 #pragma unroll
       for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
       if (lane == 0) atomicMax(&amax[hh], __float_as_uint(top));   // (of magnitudes: ordered as their bits)
       if (a.prepped) {
-        uint16_t* d = a.prepped + (((size_t)kind * a.r.n_rows + row) * n_kv + h0 + hh) * D + lane * E;
+        uint16_t* d = a.prepped + (((size_t)kind * a.r.n_rows + row0 + c0 + r) * n_kv + h0 + hh) * D + lane * E;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
           d[2 * i] = (uint16_t)(y[i] & 0xFFFFu);
@@ -172,33 +221,17 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
   }
 
   // ---- the new rows' codes ----
-  for (int it = warp; it < n * nh; it += kPaWarps) {
-    const int r = it / nh, hh = it - r * nh;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(rows + ((size_t)hh * cap + r) * D + lane * E);
-    const float s = s_now[hh], rcp = s > 0.f ? __frcp_rn(s) : 0.f;
-    uint32_t code[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const uint32_t u2 = src[i / 2];
-      const float x = (i & 1) ? bf16hi_to_f(u2) : bf16lo_to_f(u2);
-      if constexpr (E4M3) {
-        code[i] = s > 0.f ? encode_q<true>(__fdiv_rn(x, s)) : 0u;
-      } else {
-        code[i] = s > 0.f ? (uint32_t)min(max(quant_code(x, s, rcp), -127), 127) & 0xFFu : 0u;
-      }
-    }
+  for (Item at = {warp / nh, warp % nh}; at.r < n; step(at)) {
+    const int r = at.r, hh = at.h;
+    uint32_t src[E / 2];
+    load_pairs<E>(src, rows + (hh * cap + r) * D + lane * E);
+    uint32_t o[(E + 3) / 4];
+    encode_row<E, E4M3>(src, s_now[hh], o);
     uint8_t* dst = codes + ((((size_t)hh) << sh) + slot0 + r) * D + lane * E;
-    if constexpr (E == 2) {
-      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)(code[0] | (code[1] << 8));
-    } else {
-      uint32_t o[E / 4];
-#pragma unroll
-      for (int i = 0; i < E / 4; ++i)
-        o[i] = code[4 * i] | (code[4 * i + 1] << 8) | (code[4 * i + 2] << 16) | (code[4 * i + 3] << 24);
-      if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst) = o[0];
-      if constexpr (E == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
-      if constexpr (E == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    if constexpr (E == 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)o[0];
+    if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst) = o[0];
+    if constexpr (E == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+    if constexpr (E == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 

@@ -9,8 +9,9 @@
 // (its sum of squares), for the rotation the element.
 //   Norm.  x^2 is exact; a lane's D/32 squares are summed in two chains, so that
 //   at most D/64 + 1 + 5 (warp) additions and one of eps round: <= 15 * 2^-24 of
-//   the sum, half of it in 1/sqrt, plus the rounded sqrt and division and the
-//   product with x w (exact) at 2^-24 each: below 11 * 2^-24; 16 * 2^-24 are taken.
+//   the sum, half of it in 1/sqrt, whose approximation is within 2^-22 (at most
+//   2 units in the last place), and the product with x w (exact) rounds once:
+//   below 13 * 2^-24; 16 * 2^-24 are taken.
 //   Rotation.  r = fl(x c - fl(y s)) with c, s the leading floats of the angle:
 //   within 2^-22 (|x c| + |y s|) of the exact value (kvq_common.cuh, rot_bf16);
 //   1.5 times that is taken, which covers the rounding of the two ends.
@@ -28,6 +29,37 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// E 16-bit values as pairs, in the widest accesses (16-byte aligned rows).
+template <int E>
+__device__ __forceinline__ void load_pairs(uint32_t (&v)[E / 2], const uint16_t* p) {
+  if constexpr (E == 2) v[0] = *reinterpret_cast<const uint32_t*>(p);
+  if constexpr (E == 4) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    v[0] = x.x;
+    v[1] = x.y;
+  }
+  if constexpr (E >= 8) {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+      v[4 * i] = x.x;
+      v[4 * i + 1] = x.y;
+      v[4 * i + 2] = x.z;
+      v[4 * i + 3] = x.w;
+    }
+  }
+}
+template <int E>
+__device__ __forceinline__ void store_pairs(uint16_t* p, const uint32_t (&v)[E / 2]) {
+  if constexpr (E == 2) *reinterpret_cast<uint32_t*>(p) = v[0];
+  if constexpr (E == 4) *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
+  if constexpr (E >= 8) {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i)
+      reinterpret_cast<uint4*>(p)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
 }
 
 // Angles of a block's rows: the leading floats (cos, sin) and the rest apart.
@@ -83,7 +115,7 @@ __device__ __forceinline__ void prep_row(const uint32_t (&raw)[D / 64], const fl
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
   const float ms = __fadd_rn(__fmul_rn(ss, 1.f / D), eps);
-  const float inv = __fdiv_rn(1.f, __fsqrt_rn(ms));
+  const float inv = rsqrtf(ms);
   const float eb = inv * (16.f / 16777216.f);
   bool same = ms > 1e-30f && ms < 1e30f;                  // (no subnormals, no overflow in the bound)
 #pragma unroll

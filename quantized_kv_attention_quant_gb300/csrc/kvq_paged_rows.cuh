@@ -179,16 +179,23 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
   if (R > 0) stage_freqs(freqs.f, half, freq);
   pdl_wait();
   pdl_launch();
-  const auto source = [&](int it) {
-    const int r = it / nh;
-    return reinterpret_cast<const uint32_t*>(a.q_raw + ((size_t)(row0 + r) * n_q + h0 + it - r * nh) * D + lane * E);
+  // (row, head) items of the warp, one ahead of the other
+  struct Item { int r, h; };
+  const auto step = [&](Item& it) {
+    it.h += kPrWarps;
+    while (it.h >= nh) {
+      it.h -= nh;
+      ++it.r;
+    }
   };
-  uint32_t nx[E / 2];
-  if (warp < n * nh) {
-    const uint32_t* src = source(warp);
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) nx[i] = src[i];
-  }
+  Item at = {warp / nh, warp % nh}, ahead = at;
+  const uint16_t* base = a.q_raw + ((size_t)row0 * n_q + h0) * D + lane * E;
+  uint32_t nx[E / 2] = {};
+  const auto fetch = [&](const Item& it) {
+    if (it.r < n) load_pairs<E>(nx, base + ((size_t)it.r * n_q + it.h) * D);
+  };
+  fetch(ahead);
+  step(ahead);
   float w[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) w[i] = bf16_to_f(__ldg(a.q_w + lane * E + i));
@@ -204,34 +211,32 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
     put_angle<D>(ang, r, R, j, min(max(rpos[r], 0), (1 << 24) - 1), freq[j]);
   }
   __syncthreads();
-  for (int it = warp; it < n * nh; it += kPrWarps) {
-    const int r = it / nh, h = h0 + it - r * nh;
+  for (; at.r < n; step(at)) {
+    const int r = at.r;
     uint32_t raw[E / 2], y[E / 2];
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) raw[i] = nx[i];
-    if (it + kPrWarps < n * nh) {
-      const uint32_t* src = source(it + kPrWarps);
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) nx[i] = src[i];
-    }
+    fetch(ahead);
+    step(ahead);
     prep_row<D>(raw, w, a.L.eps, R, ang, r, nr, y);
-    const size_t at = ((size_t)(row0 + r) * n_q + h) * D + lane * E;
-    uint32_t* d = reinterpret_cast<uint32_t*>(q16 + at);
+    const size_t o = ((size_t)(row0 + r) * n_q + h0 + at.h) * D + lane * E;
+    uint32_t f[E / 2];
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) d[i] = pack_h2(bf16lo_to_f(y[i]), bf16hi_to_f(y[i]));
+    for (int i = 0; i < E / 2; ++i) f[i] = pack_h2(bf16lo_to_f(y[i]), bf16hi_to_f(y[i]));
+    store_pairs<E>(q16 + o, f);
     if (a.q_prepped) {                                    // (only 2-byte alignment is asked of it)
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
-        a.q_prepped[at + 2 * i] = (uint16_t)(y[i] & 0xFFFFu);
-        a.q_prepped[at + 2 * i + 1] = (uint16_t)(y[i] >> 16);
+        a.q_prepped[o + 2 * i] = (uint16_t)(y[i] & 0xFFFFu);
+        a.q_prepped[o + 2 * i + 1] = (uint16_t)(y[i] >> 16);
       }
     }
     if (rstart[r] < 0 || rpos[r] < 0 || rpos[r] >= a.pg.limit) {
       const bool idle = rstart[r] < 0;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        if (a.out_f32) reinterpret_cast<float*>(a.out)[at + i] = idle ? 0.f : __int_as_float(0x7FC00000);
-        else reinterpret_cast<uint16_t*>(a.out)[at + i] = idle ? 0 : 0x7FC0;
+        if (a.out_f32) reinterpret_cast<float*>(a.out)[o + i] = idle ? 0.f : __int_as_float(0x7FC00000);
+        else reinterpret_cast<uint16_t*>(a.out)[o + i] = idle ? 0 : 0x7FC0;
       }
     }
   }
