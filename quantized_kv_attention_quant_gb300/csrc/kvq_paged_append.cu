@@ -282,10 +282,10 @@ cudaError_t launch_append_t(const PagedAppendArgs& a, const RopeFreqs& f, int nu
   const int cap = std::min(P, a.r.n_rows);
   const int rb = half > 0 ? std::max(1, std::min(16, 1024 / half)) : 16;
   // the heads of a block share its angles; as many as 32 KB of rows hold, fewer
-  // while there are less than eight blocks per SM
+  // while there are less than four blocks per SM
   int hb = std::max(1, std::min({n_kv, kPaMaxHeads, 32768 / (cap * D * 2)}));
   const long long pages = (long long)a.r.n_rows / P + a.r.n_seqs;
-  while (hb > 1 && pages * ((n_kv + hb - 1) / hb) * 2 < 8ll * num_sms) hb = (hb + 1) / 2;
+  while (hb > 1 && pages * ((n_kv + hb - 1) / hb) * 2 < 4ll * num_sms) hb = (hb + 1) / 2;
   const size_t smem = pa_smem(D, half, hb, cap, rb).total;
   cudaError_t e = cudaFuncSetAttribute(paged_append_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);

@@ -9,16 +9,17 @@
 // (its sum of squares), for the rotation the element.
 //   Norm.  x^2 is exact; a lane's D/32 squares are summed in two chains, so that
 //   at most D/64 + 1 + 5 (warp) additions and one of eps round: <= 15 * 2^-24 of
-//   the sum, half of it in 1/sqrt, whose approximation is within 2^-22 (at most
-//   2 units in the last place), and the product with x w (exact) rounds once:
-//   below 13 * 2^-24; 16 * 2^-24 are taken.
-//   Rotation.  r = fl(x c - fl(y s)) with c, s the leading floats of the angle:
-//   within 2^-22 (|x c| + |y s|) of the exact value (kvq_common.cuh, rot_bf16);
-//   1.5 times that is taken, which covers the rounding of the two ends.
+//   the sum, half of it in 1/sqrt, whose approximation is within 2^-22.9 (2.2 *
+//   2^-24), and the product with x w (exact) rounds once: below 11 * 2^-24; 12 *
+//   2^-24 are taken.
+//   Rotation.  r = fl(x c + fl(y s)) with c, s the leading floats of the angle.
+//   What they leave out is at most 2^-25 each, the product rounds by 2^-24 |y|, r
+//   and the two ends by 2^-24 |r| each, and |r| <= |x| + |y|: 3.5 * 2^-24 (|x| +
+//   |y|) in all; 2^-22 are taken.
 // 2^-140 more on each side covers what underflows; it also sends exact zeros to
 // the exact forms, which keep their sign.
-// About 1 row in 10 of 128 dims takes the norm's exact form, and an element in
-// some 2000 the rotation's.
+// About 1 row in 30 of 128 dims takes the norm's exact form, and an element in
+// some 1000 the rotation's.
 #pragma once
 #include "kvq_common.cuh"
 
@@ -62,9 +63,10 @@ __device__ __forceinline__ void store_pairs(uint16_t* p, const uint32_t (&v)[E /
   }
 }
 
-// Angles of a block's rows: the leading floats (cos, sin) and the rest apart.
-// Pair j of a row is entry angle_at(j) of its half: under full rotation the
-// 16 lanes of a half row read consecutive entries.
+// Angles of a block's rows: the leading floats (cos, sin) and the rest apart,
+// R/2 pairs a row.  Under full rotation lane l and l + 16 rotate elements
+// l E .. with the pairs l E .., two of them 16 bytes apart from the next lane's:
+// pair j = l E + 2 i + e is entry 32 i + 2 l + e.
 struct Angles {
   float2* hi;
   float2* lo;
@@ -72,7 +74,7 @@ struct Angles {
 template <int D>
 __device__ __forceinline__ int angle_at(int R, int j) {
   constexpr int E = D / 32;
-  return R == D ? (j % E) * 16 + j / E : j;
+  return R == D ? (j % E / 2) * 32 + j / E * 2 + (j & 1) : j;
 }
 template <int D>
 __device__ __forceinline__ void put_angle(const Angles& t, int row, int R, int j, int p, const float (&f)[3]) {
@@ -84,16 +86,12 @@ __device__ __forceinline__ void put_angle(const Angles& t, int row, int R, int j
 }
 
 constexpr float kUnder = 7.17464813734306e-43f;           // 2^-140
+constexpr float kRotEnds = 2.384185791015625e-7f;         // 2^-22
 
-// x c + y s (s negated by the caller for the lower half), nearest bf16 bits.
-// True when the fp32 ends agree.
-__device__ __forceinline__ bool rot_ends(float x, float y, float c, float s, uint32_t& bits) {
-  const float ys = __fmul_rn(y, s);
-  const float r = __fmaf_rn(x, c, ys);
-  const float b = __fmaf_rn(__fmaf_rn(fabsf(x), fabsf(c), fabsf(ys)), 3.5762786865234375e-7f, kUnder);   // 1.5 * 2^-22
-  const uint32_t two = bf16x2_rn(__fadd_rn(r, b), __fsub_rn(r, b));
-  bits = two & 0xFFFFu;
-  return bits == two >> 16;
+// The two ends of x c + y s.
+__device__ __forceinline__ float2 rot_ends(float x, float y, float c, float s) {
+  const float r = __fmaf_rn(x, c, __fmul_rn(y, s)), b = fabsf(x) + fabsf(y);
+  return make_float2(__fmaf_rn(b, kRotEnds, r) + kUnder, __fmaf_rn(b, -kRotEnds, r) - kUnder);
 }
 
 // raw: the lane's D/32 bf16 in pairs; w: its weights; row: the row's place in
@@ -115,8 +113,9 @@ __device__ __forceinline__ void prep_row(const uint32_t (&raw)[D / 64], const fl
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
   const float ms = __fadd_rn(__fmul_rn(ss, 1.f / D), eps);
-  const float inv = rsqrtf(ms);
-  const float eb = inv * (16.f / 16777216.f);
+  float inv;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ms));
+  const float eb = inv * (12.f / 16777216.f);
   bool same = ms > 1e-30f && ms < 1e30f;                  // (no subnormals, no overflow in the bound)
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) {
@@ -140,22 +139,21 @@ __device__ __forceinline__ void prep_row(const uint32_t (&raw)[D / 64], const fl
   }
   if (R == D) {
     // x_e c - x_(e+D/2) s in lanes 0..15, x_e c + x_(e-D/2) s in lanes 16..31
-    const float2* t = ang.hi + row * half + (lane & 15);
-    const float sign = lane < 16 ? -1.f : 1.f;
+    const float4* t = reinterpret_cast<const float4*>(ang.hi + row * half) + (lane & 15);
+    const uint32_t flip = lane < 16 ? 0x80008000u : 0u;
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
-      const uint32_t o = __shfl_xor_sync(0xffffffffu, y[i], 16);
-      const float2 a0 = t[32 * i], a1 = t[32 * i + 16];
-      uint32_t lo, hi;
-      const bool k0 = rot_ends(bf16lo_to_f(y[i]), bf16lo_to_f(o), a0.x, sign * a0.y, lo);
-      const bool k1 = rot_ends(bf16hi_to_f(y[i]), bf16hi_to_f(o), a1.x, sign * a1.y, hi);
-      if (!(k0 && k1)) {
-        const float2* l = ang.lo + row * half + (lane & 15);
-        const float2 b0 = l[32 * i], b1 = l[32 * i + 16];
-        lo = rot_bf16(bf16lo_to_f(y[i]), bf16lo_to_f(o), ff{a0.x, b0.x}, ff{-sign * a0.y, -sign * b0.y});
-        hi = rot_bf16(bf16hi_to_f(y[i]), bf16hi_to_f(o), ff{a1.x, b1.x}, ff{-sign * a1.y, -sign * b1.y});
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, y[i], 16) ^ flip;
+      const float4 a = t[16 * i];                         // (cos, sin) of both elements
+      const float2 r0 = rot_ends(bf16lo_to_f(y[i]), bf16lo_to_f(o), a.x, a.y);
+      const float2 r1 = rot_ends(bf16hi_to_f(y[i]), bf16hi_to_f(o), a.z, a.w);
+      uint32_t r = bf16x2_rn(r0.x, r1.x);
+      if (r != bf16x2_rn(r0.y, r1.y)) {
+        const float4 b = (reinterpret_cast<const float4*>(ang.lo + row * half) + (lane & 15))[16 * i];
+        r = (uint32_t)rot_bf16(bf16lo_to_f(y[i]), bf16lo_to_f(o), ff{a.x, b.x}, ff{-a.y, -b.y}) |
+            ((uint32_t)rot_bf16(bf16hi_to_f(y[i]), bf16hi_to_f(o), ff{a.z, b.z}, ff{-a.w, -b.w}) << 16);
       }
-      y[i] = lo | (hi << 16);
+      y[i] = r;
     }
   } else if (R > 0) {
     // the normed row to shared memory; the rotated dims are then spread over
@@ -170,8 +168,10 @@ __device__ __forceinline__ void prep_row(const uint32_t (&raw)[D / 64], const fl
       const int j = low ? e : e - half;
       const float2 a = ang.hi[row * half + j];
       const float xe = bf16_to_f(nr[e]), xp = bf16_to_f(nr[low ? e + half : j]);
-      uint32_t r;
-      if (!rot_ends(xe, xp, a.x, low ? -a.y : a.y, r)) {
+      const float2 ends = rot_ends(xe, xp, a.x, low ? -a.y : a.y);
+      const uint32_t two = bf16x2_rn(ends.x, ends.y);
+      uint32_t r = two & 0xFFFFu;
+      if (r != two >> 16) {
         const float2 b = ang.lo[row * half + j];
         r = rot_bf16(xe, xp, ff{a.x, b.x}, low ? ff{a.y, b.y} : ff{-a.y, -b.y});
       }
