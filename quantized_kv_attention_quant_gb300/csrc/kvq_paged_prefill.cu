@@ -1,35 +1,39 @@
 // attn_paged_prefill on the tensor cores (tcgen05): prompt rows over pages of
 // 8-bit codes.
 //
-// One CTA takes MT tiles of 128 (token, q head) rows of one sequence and kv
-// head (row r = token r / G, head r % G) and walks the keys they see in tiles
-// of KT.  Mathematics as in kvq_paged_decode.cu: products of f16 q and codes
-// are exact, the value scale goes into the probability,
+// A pair of CTAs (a cluster of two, cta_group::2 MMAs) takes 2 MT tiles of 128
+// (token, q head) rows of one sequence and kv head (row r = token r / G, head r %
+// G), CTA c the rows 128 MT c .., and walks the keys they see in tiles of KT.
+// Mathematics as in kvq_paged_decode.cu: products of f16 q and codes are exact,
+// the value scale goes into the probability,
 //   t_j = (q . ck_j) sk log2 e + log2 sv,  p_j = 2^(t_j - ref) as f16,
 //   O += p_j cv_j,  l += p_j / sv,  out = O / l,
-// so codes enter both products as the exact f16 values they stand for.
+// so codes enter both products as the exact f16 values they stand for.  An MMA
+// of the pair reads half of its B operand from each CTA's shared memory: CTA c
+// converts the keys KT / 2 c .. of K and the output dims DO / 2 c .. of V, so the
+// codes are converted once for twice the rows (a CTA for itself spent as long
+// on the conversion as on everything else).
 //
 // Roles (one barrier pair per buffer, no block barrier in the loop):
-//   - converters: a unit of work is 16 keys (one page, one scale) x up to 256 dims
-//     of K or V; the tiles' units are dealt over seven warps.  16-byte loads of codes,
-//     two or three units in flight per warp in registers, code pairs to f16, stored to
-//     the 128-byte-swizzled rows of 64 dims that the MMA reads: K as a K-major
-//     operand, V as an MN-major one (rows are keys in both, so one layout serves
-//     both).  Eight lanes take four chunks of two neighbouring rows, whose
-//     swizzles meet all banks.  Positions that no row sees are stored as zeros and
-//     not read.
-//   - one MMA thread: S = q K^T into a score slot of tensor memory, O += P V with
-//     P from tensor memory.  MT = 2 (head_dim <= 128): the two row tiles
-//     alternate, one's products run under the other's softmax.  MT = 1: two score
-//     slots, the next tile's S runs under this one's softmax.
-//   - softmax: MT = 2: a thread per row; MT = 1: two threads per row, each half
-//     of the tile's keys, which exchange the row maximum through shared memory.
-//     P (f16) overwrites the scores it comes from.  ref is renewed (and O
-//     rescaled) only where a tile exceeds it by 2^8.
+//   - four converter warps: 16-byte loads of codes, a tile ahead in registers, code
+//     pairs to f16, stored to the swizzled rows that the MMA reads: K as a K-major
+//     operand, V as an MN-major one (rows are keys in both).  A warp's keys lie 16
+//     by 16 in one page.  Eight lanes take four chunks of two neighbouring rows,
+//     whose swizzles meet all banks.  Positions that no row sees are stored as
+//     zeros and not read.  K runs a tile ahead of V.
+//   - one MMA warp of CTA 0, for both: S = q K^T into a score slot of tensor memory,
+//     O += P V with P from tensor memory.
+//   - eight softmax warps.  MT = 2 (head_dim <= 128): a thread per row, four warps
+//     per row tile; the two row tiles take turns on the tensor cores, one's products
+//     under the other's softmax.  MT = 1: two threads per row, each half of the
+//     tile's keys, which exchange the row maximum through shared memory; two score
+//     slots, the next tile's S runs under this one's softmax.  P (f16) overwrites
+//     the scores it comes from.  ref is renewed (and O rescaled) only where a tile
+//     exceeds it by 2^8.
 // MMAs of one thread execute in issue order, so S of the next tile may be
 // issued right behind the P V that reads the slot it overwrites.
 //
-// head_dim 512: two CTAs per row tile, each 256 of the output dims (tensor
+// head_dim 512: two pairs per row tile, each 256 of the output dims (tensor
 // memory holds 512 columns: 256 of O, 2 KT of scores).
 //
 // Row tiles are taken longest first (sorted by the prep kernel), and cut along
@@ -49,25 +53,28 @@ namespace {
 template <int D>
 struct Pf {
   static constexpr int MT = D <= 128 ? 2 : 1;           // row tiles per CTA
-  static constexpr int DO = D > 256 ? 256 : D;          // output dims per CTA
+  static constexpr int ROWS = 2 * MT * 128;             // rows of a pair
+  static constexpr int DO = D > 256 ? 256 : D;          // output dims per pair
   static constexpr int NSPLIT = D / DO;
   static constexpr int KT = D == 512 ? 64 : 128;        // keys per tile
   static constexpr int SUB = KT / 16;                   // scales per tile
-  static constexpr int KST = D <= 128 ? 2 : 1;          // K and V stages
-  static constexpr int CW = 7;                          // converter warps
-  static constexpr int THREADS = 256 + 32 * CW + 32;    // 512: 128 registers each
-  // a converter's unit: 16 keys x UD dims, UJ 16-byte loads per lane
-  static constexpr int UD = D < 256 ? D : 256, UJ = UD / 32;
-  static constexpr int UK = SUB * (D / UD), UV = SUB * (DO / UD);          // units of a tile
-  static constexpr int RING = D < 256 ? 3 : 2;          // units in flight per converter warp
+  static constexpr int KST = D <= 128 ? 3 : 2;          // K and V stages
+  static constexpr int THREADS = 512;                   // 8 softmax, 4 converter, 1 MMA warp (and 3 to fill a warpgroup)
+  // a converter warp per tile: 16 keys x KD dims of K, VU times 16 keys x VD dims of V
+  static constexpr int KHALVES = 8 / SUB;               // warps that share 16 keys of K (halves of the dims)
+  static constexpr int KD = D / KHALVES, KJ = KD / 32;  // KJ 16-byte loads per lane
+  static constexpr int VU = SUB / 4, VD = DO / 2, VJ = VD / 32;
   static constexpr int Q_BYTES = 128 * D * 2;           // of a row tile
-  static constexpr int K_BYTES = KT * D * 2, V_BYTES = KT * DO * 2;
+  static constexpr int K_BYTES = KT / 2 * D * 2, V_BYTES = KT * VD * 2;    // of a CTA's half tile
+  static constexpr int K_BLK = KT / 2 * 128;            // 64 dims of K
+  static constexpr int V_ROW = VD < 64 ? VD * 2 : 128;  // bytes of a key in a block of V
+  static constexpr int V_BLK = KT * V_ROW;
   static constexpr int K_OFF = MT * Q_BYTES;
   static constexpr int V_OFF = K_OFF + KST * K_BYTES;
   static constexpr int SC_OFF = V_OFF + KST * V_BYTES;  // float4 [4][SUB]: sk log2 e, log2 sv, 1 / sv
   static constexpr int X_OFF = SC_OFF + 4 * SUB * 16;   // MT == 1: row maxima [2][2][128]
   static constexpr int B_OFF = X_OFF + (MT == 1 ? 2048 : 0);
-  static constexpr int USED = B_OFF + 160;
+  static constexpr int USED = B_OFF + 200;
   // (one CTA per SM: each takes all of tensor memory)
   static constexpr int BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
   static constexpr int C_S = MT * DO;                   // tensor-memory columns: O, then two score slots
@@ -106,10 +113,23 @@ __device__ __forceinline__ uint4 ldg_codes(const uint8_t* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
-// MN-major operand, 128-byte swizzle: lbo to the next 64 elements of N, sbo to the next 8 of K
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+// MN-major operand, rows of 128 or 64 swizzled bytes: lbo to the next row's worth of N, sbo to the next 8 of K
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo, uint32_t sbo, int row) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+         ((uint64_t)1 << 46) | ((uint64_t)(row == 128 ? 2 : 4) << 61);
+}
+// D (+)= A[tmem of both CTAs] * B[half of N in each CTA's smem]
+__device__ __forceinline__ void mma2_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+               :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u) : "memory");
+}
+// An arrival at CTA 0's barrier after this CTA's shared memory was written and
+// fenced for the tensor cores, which read it where it is: a release within the
+// CTA (one over the cluster took 1000 cycles).
+__device__ __forceinline__ void arrive_pair(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(tc::in_cta0(bar)) : "memory");
 }
 constexpr uint32_t kMnMajorB = 1u << 16;                // instruction descriptor: B is MN-major
 
@@ -146,7 +166,7 @@ __device__ __forceinline__ int pf_pieces(int n, int splits) { return min(n, spli
 __device__ __forceinline__ int pf_tile0(int n, int pieces, int z) { return (int)((long long)n * z / pieces); }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(Pf<D>::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pf<D>::THREADS, 1)
 paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, const int32_t* order, const uint16_t* q16,
                      float* part_o, float* part_ml, uint32_t* status) {
   using S = Pf<D>;
@@ -160,7 +180,8 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   pdl_wait();                                             // q16, the order and the status word are written
   // ---- the CTA's rows and keys ----
   const int per = n_kv * S::NSPLIT, z = blockIdx.y;
-  const int rank = blockIdx.x / per, hx = blockIdx.x - rank * per;
+  const int cta = (int)tc::cta_rank();                    // of the pair
+  const int rank = (blockIdx.x >> 1) / per, hx = (blockIdx.x >> 1) - rank * per;
   const int u = __ldg(order + rank), h = hx / S::NSPLIT, d_base = (hx % S::NSPLIT) * DO;
   const PagedGroup g = paged_group(a.r, a.pg, W, TQ, KT, u);
   if (g.tiles == 0) return;
@@ -169,45 +190,52 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   if (z >= pieces) return;
   const int t_a = pf_tile0(n_all, pieces, z), n = pf_tile0(n_all, pieces, z + 1) - t_a;
   const int k0 = g.kt0 + KT * t_a;
-  const int rows = g.nt * G;
+  const int rows = g.nt * G, row0 = cta * MT * 128;       // of the pair; the CTA's first
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::B_OFF);
-  uint64_t* k_full = bars;                                // [2] (converters' units)
-  uint64_t* k_empty = bars + 2;                           // [2]
-  uint64_t* v_full = bars + 4;                            // [2]
-  uint64_t* v_empty = bars + 6;                           // [2]
-  uint64_t* s_full = bars + 8;                            // [2] scores of a slot written
-  uint64_t* p_full = bars + 10;                           // [2] P of a slot written (softmax warps)
-  uint64_t* o_full = bars + 12;                           // [1]
-  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 14);   // tensor memory, bad page
+  // in CTA 0: K, V converted and P written in both CTAs; in each CTA: the rest
+  uint64_t* k_full = bars;                                // [3] (converter warps of both)
+  uint64_t* v_full = bars + 3;                            // [3]
+  uint64_t* p_full = bars + 6;                            // [2] (softmax warps of both)
+  uint64_t* k_empty = bars + 8;                           // [3] (the MMA warp)
+  uint64_t* v_empty = bars + 11;                          // [3]
+  uint64_t* s_full = bars + 14;                           // [2] scores of a slot written
+  uint64_t* o_full = bars + 16;                           // [2] a row tile's last product
+  uint64_t* sc_full = bars + 18;                          // [4] a tile's scales (the CTA's converter warps)
+  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 22);   // tensor memory, bad page
   const uint32_t sb = smem_u32(sm);
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, S::UK);
-      mbar_init(v_full + i, S::UV);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(k_full + i, 8);
+      mbar_init(v_full + i, 8);
       mbar_init(k_empty + i, 1);
       mbar_init(v_empty + i, 1);
-      mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, MT == 2 ? 4 : 8);
     }
-    mbar_init(o_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(p_full + i, MT == 2 ? 8 : 16);
+      mbar_init(s_full + i, 1);
+      mbar_init(o_full + i, 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(sc_full + i, 4);
     fence_mbar_init();
     ctl[1] = 0;
   }
   if (warp == 0) {
-    tc::tmem_alloc(const_cast<uint32_t*>(ctl), 512);
-    tc::tmem_relinquish();
+    tc::tmem_alloc2(const_cast<uint32_t*>(ctl), 512);
+    tc::tmem_relinquish2();
   }
   // ---- q into shared memory: blocks of 64 dims [128 rows x 128 B], swizzled ----
   for (int i = tid; i < MT * 128 * (D / 8); i += S::THREADS) {
     const int r = i / (D / 8), c = i - r * (D / 8);       // row, 16-byte chunk of it
     uint4 v = {0u, 0u, 0u, 0u};
-    if (r < rows) v = *reinterpret_cast<const uint4*>(q16 + ((size_t)(g.row0 + r / G) * a.L.n_q + h * G + r % G) * D + 8 * c);
+    const int rg = row0 + r;
+    if (rg < rows) v = *reinterpret_cast<const uint4*>(q16 + ((size_t)(g.row0 + rg / G) * a.L.n_q + h * G + rg % G) * D + 8 * c);
     *reinterpret_cast<uint4*>(sm + (r >> 7) * S::Q_BYTES + (c >> 3) * 16384 + tc::sw128_off(r & 127, c & 7)) = v;
   }
   fence_proxy_async();
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();                                     // barriers, tensor memory and q of both CTAs
   tc::fence_after_sync();
   const uint32_t tmem = ctl[0];
   bool dead = false;
@@ -221,200 +249,210 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   // MT == 2: a row of 128 scores stays in registers: 168 for the softmax threads,
   // 88 for the others (256 threads each of the launch's 512 x 128)
   if (warp >= 8) {
-   if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-   if (warp == 8 + S::CW) {
-    // ================= products =================
-    constexpr uint32_t ID_QK = tc::idesc_f16_f32(128, KT), ID_PV = tc::idesc_f16_f32(128, DO) | kMnMajorB;
-    const bool leader = lane == 0;
-    // descriptors of the first steps; an address step of b bytes adds b / 16
-    const uint64_t q_desc = tc::desc_kmajor_sw128(sb, 1024), k_desc = tc::desc_kmajor_sw128(sb + S::K_OFF, 1024),
-                   v_desc = desc_mn_sw128(sb + S::V_OFF, KT * 128, 1024);
-    auto qk = [&](int m, int i) {                         // slot: MT == 2: m, else i & 1
-      const int slot = MT == 2 ? m : i & 1, st = i % KST;
-      if (leader) {
-        const uint64_t qd = q_desc + m * (S::Q_BYTES / 16), kd = k_desc + st * (S::K_BYTES / 16);
-        const uint32_t d = tmem + S::C_S + KT * slot;
+    if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp >= 12) {
+      // ================= products of both CTAs (CTA 0) =================
+      if (cta == 0 && warp == 12) {
+        constexpr uint32_t ID_QK = tc::idesc_f16_f32(256, KT), ID_PV = tc::idesc_f16_f32(256, DO) | kMnMajorB;
+        // descriptors of the first steps; an address step of b bytes adds b / 16
+        const uint64_t q_desc = tc::desc_kmajor_sw128(sb, 1024), k_desc = tc::desc_kmajor_sw128(sb + S::K_OFF, 1024),
+                       v_desc = desc_mn(sb + S::V_OFF, S::V_BLK, 8 * S::V_ROW, S::V_ROW);
+        auto qk = [&](int m, int i) {                     // scores of tile i
+          const int slot = MT == 2 ? m : i & 1, st = i % KST;
+          if (lane == 0) {
+            const uint64_t qd = q_desc + m * (S::Q_BYTES / 16), kd = k_desc + st * (S::K_BYTES / 16);
+            const uint32_t d = tmem + S::C_S + KT * slot;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          tc::mma_f16(d, qd + (s >> 2) * 1024 + 2 * (s & 3), kd + (s >> 2) * (KT * 8) + 2 * (s & 3), ID_QK, s != 0);
-        tc::commit(s_full + slot);
-      }
-      __syncwarp();
-    };
-    auto pv = [&](int m, int i) {
-      const int slot = MT == 2 ? m : i & 1, st = i % KST;
-      if (leader) {
-        const uint64_t vd = v_desc + st * (S::V_BYTES / 16);
-        const uint32_t p = tmem + S::C_S + KT * slot;
+            for (int s = 0; s < D / 16; ++s)
+              tc::mma2_f16(d, qd + (s >> 2) * 1024 + 2 * (s & 3), kd + (s >> 2) * (S::K_BLK / 16) + 2 * (s & 3), ID_QK,
+                           s != 0);
+            tc::commit2(s_full + slot);
+            if (m == MT - 1) tc::commit2(k_empty + st);
+          }
+          __syncwarp();
+        };
+        auto pv = [&](int m, int i) {                     // O += P V of tile i
+          const int slot = MT == 2 ? m : i & 1, st = i % KST;
+          wait(p_full + slot, MT == 2 ? i & 1 : (i >> 1) & 1);
+          tc::fence_after_sync();
+          if (lane == 0) {
+            const uint64_t vd = v_desc + st * (S::V_BYTES / 16);
+            const uint32_t p = tmem + S::C_S + KT * slot, d = tmem + m * DO;
 #pragma unroll
-        for (int s = 0; s < KT / 16; ++s) {
-          const int col = MT == 2 ? 8 * s : (s / (KT / 32)) * (KT / 2) + 8 * (s % (KT / 32));
-          tc::mma_f16_ts(tmem + m * DO, p + col, vd + 128 * s, ID_PV, i > 0 || s > 0);
-        }
-      }
-      __syncwarp();
-    };
-    auto done = [&](uint64_t* bar) {
-      if (leader) tc::commit(bar);
-      __syncwarp();
-    };
-    wait(k_full, 0);
-    tc::fence_after_sync();
-    for (int m = 0; m < MT; ++m) qk(m, 0);
-    done(k_empty);
-    for (int i = 0; i < n; ++i) {
-      const int nx = i + 1;
-      if (MT == 1 && nx < n) {                            // the next scores before this P V
-        wait(k_full + nx % KST, (nx / KST) & 1);
+            for (int s = 0; s < KT / 16; ++s) {
+              const int col = MT == 2 ? 8 * s : (s / (KT / 32)) * (KT / 2) + 8 * (s % (KT / 32));
+              mma2_f16_ts(d, p + col, vd + s * S::V_ROW, ID_PV, i > 0 || s > 0);
+            }
+            if (m == MT - 1) tc::commit2(v_empty + st);
+            if (i == n - 1) tc::commit2(o_full + m);
+          }
+          __syncwarp();
+        };
+        wait(k_full, 0);
         tc::fence_after_sync();
-        qk(0, nx);
-        done(k_empty + nx % KST);
-      }
-      wait(v_full + i % KST, (i / KST) & 1);
-      if (MT == 2 && nx < n) wait(k_full + nx % KST, (nx / KST) & 1);
-      for (int m = 0; m < MT; ++m) {
-        if (MT == 2) wait(p_full + m, i & 1);
-        else wait(p_full + (i & 1), (i >> 1) & 1);
-        tc::fence_after_sync();
-        pv(m, i);
-        if (m == MT - 1) done(v_empty + i % KST);
-        if (MT == 2 && nx < n) qk(m, nx);
-      }
-      if (MT == 2 && nx < n) done(k_empty + nx % KST);
-    }
-    done(o_full);
-   } else {
-    // ================= converters =================
-    constexpr int UK = S::UK, UV = S::UV, UJ = S::UJ, RING = S::RING;
-    const int32_t* table = a.pg.tables + (size_t)g.s * a.pg.max_pages;
-    const size_t page_bytes = ((size_t)n_kv << sh) * D;
-    // the lane's first row of a unit and 16-dim chunk of its 64-dim blocks
-    const int r0 = 2 * (lane >> 3) + ((lane >> 2) & 1), c0 = lane & 3;
-    const uint32_t s_lane = tc::sw128_off(r0, 2 * c0);
-    const size_t head = ((size_t)h << sh) * D + r0 * D + 16 * c0;
-    // the CTA's units: K(0), then K(i + 1) and V(i) for each tile i (K runs a
-    // tile ahead); each warp takes every CW-th, and walks them three times:
-    // pages, loads, stores
-    struct Walk {
-      int i, in;                                          // tile, unit of K(i + 1) and V(i); i = -1: K(0)
-      __device__ explicit Walk(int first) : i(-1), in(first) {
-        if (in >= UK) {
-          in -= UK;
-          i = 0;
+        for (int m = 0; m < MT; ++m) qk(m, 0);
+        for (int i = 0; i < n; ++i) {
+          const int nx = i + 1;
+          // MT == 1: the next scores under this tile's softmax; MT == 2: each row tile's right behind its P V, in
+          // turn, so that one row tile's products run under the other's softmax
+          if (MT == 1 && nx < n) {
+            wait(k_full + nx % KST, (nx / KST) & 1);
+            tc::fence_after_sync();
+            qk(0, nx);
+          }
+          wait(v_full + i % KST, (i / KST) & 1);
+          if (MT == 2 && nx < n) wait(k_full + nx % KST, (nx / KST) & 1);
+          for (int m = 0; m < MT; ++m) {
+            pv(m, i);
+            if (MT == 2 && nx < n) qk(m, nx);
+          }
         }
       }
-      __device__ void next() {
-        in += S::CW;
-        const int all = i < 0 ? UK : UK + UV;
-        if (in >= all) {
-          in -= all;
-          ++i;
-        }
-      }
-      __device__ bool v() const { return in >= UK; }
-      __device__ int tile() const { return v() ? i : i + 1; }
-      __device__ int sub() const { return (v() ? in - UK : in) % SUB; }
-      __device__ int blk() const { return (v() ? in - UK : in) / SUB; }
-    };
-    // page of a unit (raw entry; -2: no row sees it)
-    auto look_up = [&](const Walk& x) {
-      int id = -2;
-      const int key = k0 + KT * x.tile() + 16 * x.sub();
-      if (x.tile() < n && key <= g.hi && key + 15 >= g.lo) id = __ldg(table + (key >> sh));
-      return id;
-    };
-    uint4 buf[RING][UJ];
-    float2 scl[RING];
-    auto load = [&](uint4 (&v)[UJ], float2& sc2, const Walk& x, int raw) {
-#pragma unroll
-      for (int j = 0; j < UJ; ++j) v[j] = make_uint4(0u, 0u, 0u, 0u);
-      sc2 = make_float2(0.f, 1.f);
-      if (raw == -2) return;
-      if ((unsigned)raw >= (unsigned)a.pg.n_pages) {
+    } else {
+      // ================= converters =================
+      constexpr int KJ = S::KJ, VJ = S::VJ, VU = S::VU, NKW = SUB / 2;   // K's 16-key runs of this CTA
+      const int cw = warp - 8;
+      // the warp's 16 keys of K (16-key run cta * NKW + cw % NKW of a tile, half cw / NKW of the dims) and its
+      // runs cw, cw + 4 .. of V; with VU == 2 the K run is one of them
+      const int run_k = cta * NKW + cw % NKW, half = cw / NKW;
+      const int32_t* table = a.pg.tables + (size_t)g.s * a.pg.max_pages;
+      const size_t page_bytes = ((size_t)n_kv << sh) * D;
+      // the lane's first row and 16-dim chunk of 64 dims; load j: row + 8 (j / blocks), block j % blocks
+      // (32 dims of V: one chunk of one row)
+      const int r0 = 2 * (lane >> 3) + ((lane >> 2) & 1), c0 = lane & 3;
+      const uint32_t s_lane = tc::sw128_off(r0, 2 * c0);
+      const int rv = S::VD < 64 ? lane >> 1 : r0, cv = S::VD < 64 ? lane & 1 : c0;
+      const uint32_t v_at = S::VD < 64 ? rv * 64 + ((2 * cv ^ ((rv >> 1) & 3)) << 4) : s_lane;
+      const uint8_t* k_lane = a.pg.k_codes + ((size_t)h << sh) * D + r0 * D + 16 * c0 + half * S::KD;
+      const uint8_t* v_lane = a.pg.v_codes + ((size_t)h << sh) * D + rv * D + 16 * cv + d_base + cta * S::VD;
+      auto look_up = [&](int t, int run) {                // raw table entry, -2: no row sees the keys
+        const int key = k0 + KT * t + 16 * run;
+        return t < n && key <= g.hi && key + 15 >= g.lo ? __ldg(table + (key >> sh)) : -2;
+      };
+      auto checked = [&](int id) {
+        if (id == -2) return -1;
+        if ((unsigned)id < (unsigned)a.pg.n_pages) return id;
         ctl[1] = 1;
-        return;
-      }
-      const int key = k0 + KT * x.tile() + 16 * x.sub();
-      const uint8_t* src = (x.v() ? a.pg.v_codes + d_base : a.pg.k_codes) + head + raw * page_bytes +
-                           (key & (P - 1)) * D + x.blk() * S::UD;
-      constexpr int NBK = S::UD / 64;                     // 64-dim blocks of a unit
+        return -1;
+      };
+      // J loads of run `run` of tile t, rows r + 8 (j / nb)
+      auto load = [&](auto& v, const uint8_t* codes, int nb, int r, int t, int run, int id) {
+        constexpr int J = sizeof(v) / 16;
+        const int key = k0 + KT * t + 16 * run;
+        const uint8_t* src = codes + max(id, 0) * page_bytes + (key & (P - 1)) * D;
+        if (id >= 0 && key >= g.lo && key + 15 <= g.hi) {
 #pragma unroll
-      for (int j = 0; j < UJ; ++j) {
-        const int dr = 8 * (j / NBK), k = key + r0 + dr;
-        if (k >= g.lo && k <= g.hi) v[j] = ldg_codes(src + dr * D + 64 * (j % NBK));
-      }
-      if (!x.v() && x.blk() == 0) {
-        sc2.x = __ldg(a.pg.k_scales + (size_t)raw * n_kv + h);
-        sc2.y = __ldg(a.pg.v_scales + (size_t)raw * n_kv + h);
-      }
-    };
-    auto put = [&](const uint4 (&v)[UJ], float2 sc2, const Walk& x) {
-      const int t = x.tile(), st = t % KST;
-      if (t >= n) return;                                 // (there is no K behind the last tile)
-      wait((x.v() ? v_empty : k_empty) + st, ((t / KST) & 1) ^ 1);
-      if (!x.v() && x.blk() == 0 && lane == 0) {
-        const float one = sc2.y > 0.f ? sc2.y : 1.f;
-        *reinterpret_cast<float4*>(sm + S::SC_OFF + ((t & 3) * SUB + x.sub()) * 16) =
-            make_float4(fmaxf(sc2.x * L2E, 1e-30f), __log2f(one), __fdividef(1.f, one), 0.f);
-      }
-      constexpr int NBK = S::UD / 64;
-      uint8_t* at = sm + (x.v() ? S::V_OFF + st * S::V_BYTES : S::K_OFF + st * S::K_BYTES) +
-                    x.blk() * NBK * (KT * 128) + x.sub() * 2048;
+          for (int j = 0; j < J; ++j) v[j] = ldg_codes(src + 8 * (j / nb) * D + 64 * (j % nb));
+        } else {
 #pragma unroll
-      for (int j = 0; j < UJ; ++j) {
-        uint32_t o[8];
-        codes_to_h2<E4M3>(v[j].x, o[0], o[1]);
-        codes_to_h2<E4M3>(v[j].y, o[2], o[3]);
-        codes_to_h2<E4M3>(v[j].z, o[4], o[5]);
-        codes_to_h2<E4M3>(v[j].w, o[6], o[7]);
-        uint8_t* d = at + 1024 * (j / NBK) + (KT * 128) * (j % NBK);
-        *reinterpret_cast<uint4*>(d + s_lane) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(d + (s_lane ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
+          for (int j = 0; j < J; ++j) {
+            const int k = key + r + 8 * (j / nb);
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (id >= 0 && k >= g.lo && k <= g.hi) v[j] = ldg_codes(src + 8 * (j / nb) * D + 64 * (j % nb));
+          }
+        }
+      };
+      auto put = [&](const auto& v, uint32_t at, uint32_t at1, int nb, uint32_t blk) {
+        constexpr int J = sizeof(v) / 16;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          uint32_t o[8];
+          codes_to_h2<E4M3>(v[j].x, o[0], o[1]);
+          codes_to_h2<E4M3>(v[j].y, o[2], o[3]);
+          codes_to_h2<E4M3>(v[j].z, o[4], o[5]);
+          codes_to_h2<E4M3>(v[j].w, o[6], o[7]);
+          const uint32_t d = 1024 * (j / nb) + blk * (j % nb);
+          *reinterpret_cast<uint4*>(sm + at + d) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(sm + at1 + d) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      };
+      auto full = [&](uint64_t* bar) {                    // (in CTA 0)
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_pair(bar);
+      };
+      uint4 kb[KJ], vb[VU][VJ];
+      float sk[VU], sv[VU];
+      auto load_k = [&](int t, const int (&id)[VU], int idk) {
+        load(kb, k_lane, S::KD / 64, r0, t, run_k, idk);
+#pragma unroll
+        for (int e = 0; e < VU; ++e) {
+          sk[e] = id[e] >= 0 ? __ldg(a.pg.k_scales + (size_t)id[e] * n_kv + h) : 0.f;
+          sv[e] = id[e] >= 0 ? __ldg(a.pg.v_scales + (size_t)id[e] * n_kv + h) : 0.f;
+        }
+      };
+      auto load_v = [&](int t, const int (&id)[VU]) {
+#pragma unroll
+        for (int e = 0; e < VU; ++e) load(vb[e], v_lane, S::VD < 64 ? 1 : S::VD / 64, rv, t, cw + 4 * e, id[e]);
+      };
+      auto put_k = [&](int t) {
+        const int st = t % KST;
+        wait(k_empty + st, ((t / KST) & 1) ^ 1);
+        if (lane == 0) {
+#pragma unroll
+          for (int e = 0; e < VU; ++e) {
+            const float one = sv[e] > 0.f ? sv[e] : 1.f;
+            *reinterpret_cast<float4*>(sm + S::SC_OFF + ((t & 3) * SUB + cw + 4 * e) * 16) =
+                make_float4(fmaxf(sk[e] * L2E, 1e-30f), __log2f(one), __fdividef(1.f, one), 0.f);
+          }
+          mbar_arrive(sc_full + (t & 3));
+        }
+        const uint32_t at = S::K_OFF + st * S::K_BYTES + half * (S::KD / 64) * S::K_BLK + (cw % NKW) * 2048;
+        put(kb, at + s_lane, at + (s_lane ^ 16u), S::KD / 64, S::K_BLK);
+        full(k_full + st);
+      };
+      // page numbers of tiles: id0 of i (V), id1 of i + 1 (K comes next), raw ahead
+      int id0[VU], id1[VU], raw[VU];
+      auto idk_of = [&](const int (&id)[VU], int t) {     // the K run's
+        return VU == 2 ? (run_k < 4 ? id[0] : id[VU - 1]) : checked(look_up(t, run_k));
+      };
+#pragma unroll
+      for (int e = 0; e < VU; ++e) {
+        id0[e] = checked(look_up(0, cw + 4 * e));
+        id1[e] = checked(look_up(1, cw + 4 * e));
+        raw[e] = look_up(2, cw + 4 * e);
       }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive((x.v() ? v_full : k_full) + st);
-    };
-    Walk page(warp - 8), ahead = page, now = page;
-    int raw[RING];
+      load_k(0, id0, idk_of(id0, 0));
+      load_v(0, id0);
+      put_k(0);
+      load_k(1, id1, idk_of(id1, 1));
+      for (int i = 0; i < n; ++i) {
+        const int st = i % KST;
+        int id2[VU];
 #pragma unroll
-    for (int b = 0; b < RING; ++b) {
-      raw[b] = look_up(page);
-      page.next();
-    }
+        for (int e = 0; e < VU; ++e) {
+          id2[e] = checked(raw[e]);
+          raw[e] = look_up(i + 3, cw + 4 * e);
+        }
+        if (i + 1 < n) put_k(i + 1);
+        load_k(i + 2, id2, idk_of(id2, i + 2));
+        wait(v_empty + st, ((i / KST) & 1) ^ 1);
 #pragma unroll
-    for (int b = 0; b < RING; ++b) {
-      load(buf[b], scl[b], ahead, raw[b]);
-      ahead.next();
-      raw[b] = look_up(page);
-      page.next();
-    }
-    while (now.i < n) {
+        for (int e = 0; e < VU; ++e) {
+          const uint32_t at = S::V_OFF + st * S::V_BYTES + (cw + 4 * e) * 16 * S::V_ROW;
+          put(vb[e], at + v_at, at + (v_at ^ 16u), S::VD < 64 ? 1 : S::VD / 64, S::V_BLK);
+        }
+        full(v_full + st);
+        load_v(i + 1, id1);
 #pragma unroll
-      for (int b = 0; b < RING; ++b) {
-        if (now.i < n) {
-          put(buf[b], scl[b], now);
-          now.next();
-          load(buf[b], scl[b], ahead, raw[b]);
-          ahead.next();
-          raw[b] = look_up(page);
-          page.next();
+        for (int e = 0; e < VU; ++e) {
+          id0[e] = id1[e];
+          id1[e] = id2[e];
         }
       }
     }
-   }
   } else {
     // ================= softmax =================
     if constexpr (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     constexpr int NK = MT == 2 ? KT : KT / 2;             // keys of a tile per thread
     const int wg = warp >> 2;                             // row tile, or half of the keys
     const int m = MT == 2 ? wg : 0;
-    const int r = 32 * (warp & 3) + lane, rg = 128 * m + r;
+    const int r = 32 * (warp & 3) + lane, rg = row0 + 128 * m + r;
     const int t_r = min(rg / G, g.nt - 1);
     const int p_r = g.p0 + t_r, lo_r = W > 0 ? p_r - W + 1 : 0;
     const bool valid = rg < rows;
     // what every row of the row tile sees
-    const int t_first = min(128 * m / G, g.nt - 1), t_last = min((128 * m + 127) / G, g.nt - 1);
+    const int t_first = min((row0 + 128 * m) / G, g.nt - 1), t_last = min((row0 + 128 * m + 127) / G, g.nt - 1);
     const int p_min = g.p0 + t_first, lo_max = W > 0 ? g.p0 + t_last - W + 1 : 0;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t t_o = lanes + m * DO;
@@ -423,6 +461,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     for (int i = 0; i < n; ++i) {
       const int slot = MT == 2 ? m : i & 1;
       const uint32_t t_s = lanes + S::C_S + KT * slot + (MT == 2 ? 0 : (KT / 2) * wg);
+      wait(sc_full + (i & 3), (i >> 2) & 1);
       if (MT == 2) wait(s_full + m, i & 1);
       else wait(s_full + slot, (i >> 1) & 1);
       tc::fence_after_sync();
@@ -525,7 +564,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + slot);
+      if (lane == 0) tc::arrive_cta0(p_full + slot);   // (only tensor memory is passed on)
     }
     // ---- out ----
     if constexpr (MT == 1) {                              // l of both halves
@@ -534,7 +573,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       named_bar(1, 256);
       l += xm[(wg ^ 1) * 128 + r];
     }
-    wait(o_full, 0);
+    wait(o_full + m, 0);
     tc::fence_after_sync();
     __syncwarp();
     if (ctl[1]) {
@@ -545,7 +584,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     constexpr int OC = MT == 2 ? DO : DO / 2;
     const int o0 = MT == 2 ? 0 : OC * wg;
     const size_t unit = (size_t)u * per + hx;
-    const size_t prow = (unit * splits + z) * (MT * 128) + rg;
+    const size_t prow = (unit * splits + z) * S::ROWS + rg;
     const size_t at = ((size_t)(g.row0 + rg / G) * a.L.n_q + h * G + rg % G) * D + d_base + o0;
     const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
 #pragma unroll 1
@@ -594,9 +633,10 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   }
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();                                     // neither CTA's memory is used any more
   if (warp == 0) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc2(tmem, 512);
   }
 }
 
@@ -606,7 +646,7 @@ template <int D>
 __global__ void __launch_bounds__(256)
 paged_join_kernel(const PagedReadArgs a, const int TQ, const int splits, const float* part_o, const float* part_ml) {
   using S = Pf<D>;
-  constexpr int DO = S::DO, ROWS = S::MT * 128;
+  constexpr int DO = S::DO, ROWS = S::ROWS;
   pdl_launch();
   pdl_wait();
   const int per = a.L.n_kv * S::NSPLIT, G = a.L.G;
@@ -666,17 +706,17 @@ template <int D>
 PfPlan pf_plan(const LayerArgs& L, int n_seqs, int n_rows, int max_pos, int num_sms) {
   using S = Pf<D>;
   PfPlan p;
-  p.TQ = S::MT * 128 / L.G;
+  p.TQ = S::ROWS / L.G;
   static const int32_t some = 0;
   p.n_groups = paged_groups(PagedRows{&some, nullptr, n_seqs, n_rows}, p.TQ);
   p.units = (long long)p.n_groups * L.n_kv * S::NSPLIT;
-  // as many pieces as fill the GPU once (one CTA per SM), of at least two tiles
+  // as many pieces as fill the GPU once (one pair per two SMs), of at least two tiles
   long long keys = (long long)max_pos + 1;
   if (L.window > 0) keys = std::min<long long>(keys, (long long)L.window + p.TQ);
   const long long tiles = (keys + S::KT - 1) / S::KT;
   // (groups are counted with room for one short one per sequence)
   const long long real = std::max(1ll, ((long long)n_rows / p.TQ + (n_rows % p.TQ != 0)) * L.n_kv * S::NSPLIT);
-  p.splits = (int)std::max(1ll, std::min<long long>({num_sms / real, tiles / 2, 64ll}));
+  p.splits = (int)std::max(1ll, std::min<long long>({num_sms / 2 / real, tiles / 2, 64ll}));
   return p;
 }
 
@@ -686,7 +726,7 @@ template <int D>
 PfWs pf_ws(const LayerArgs& L, int n_rows, const PfPlan& p) {
   using S = Pf<D>;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t prows = p.splits > 1 ? (size_t)p.units * p.splits * S::MT * 128 : 0;
+  const size_t prows = p.splits > 1 ? (size_t)p.units * p.splits * S::ROWS : 0;
   PfWs w;
   w.q16 = 256;
   w.order = up(w.q16 + (size_t)n_rows * L.n_q * D * 2);
@@ -701,7 +741,7 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   using S = Pf<D>;
   const PfPlan p = pf_plan<D>(a.L, a.r.n_seqs, a.r.n_rows, max_pos, num_sms);
   const PfWs w = pf_ws<D>(a.L, a.r.n_rows, p);
-  if (p.units > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (p.units > 0x3fffffffLL) return cudaErrorInvalidValue;
   uint8_t* b = static_cast<uint8_t*>(ws);
   uint32_t* status = reinterpret_cast<uint32_t*>(b);
   uint16_t* q16 = reinterpret_cast<uint16_t*>(b + w.q16);
@@ -715,11 +755,11 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   e = cudaFuncSetAttribute(paged_prefill_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (e != cudaSuccess) return e;
   if ((e = prof_before(st)) != cudaSuccess) return e;
-  e = launch_pdl(paged_prefill_kernel<D, E4M3>, dim3((unsigned)p.units, p.splits), dim3(S::THREADS), S::BYTES, st, a,
+  e = launch_pdl(paged_prefill_kernel<D, E4M3>, dim3((unsigned)p.units * 2, p.splits), dim3(S::THREADS), S::BYTES, st, a,
                  p.TQ, p.splits, order, q16, part_o, part_ml, status);
   if (e != cudaSuccess) return e;
   if ((e = prof_after(st)) != cudaSuccess || p.splits == 1) return e;
-  return launch_pdl(paged_join_kernel<D>, dim3((unsigned)p.units, S::MT * 128 * (S::DO / 4) / 256), dim3(256), 0, st, a,
+  return launch_pdl(paged_join_kernel<D>, dim3((unsigned)p.units, S::ROWS * (S::DO / 4) / 256), dim3(256), 0, st, a,
                     p.TQ, p.splits, part_o, part_ml);
 }
 
