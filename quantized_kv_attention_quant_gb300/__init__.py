@@ -175,10 +175,12 @@ def header_functions() -> list:
 def _ptr(x):
     if x is None:
         return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if isinstance(x, ctypes.Array):
         return ctypes.addressof(x)
     raise TypeError(f"cannot pass {type(x)} as a device pointer")

@@ -2,9 +2,25 @@
 // over pages, and the pages' upkeep (kvq_paged_append.cu, kvq_paged_decode.cu,
 // kvq_paged_prefill.cu, kvq_pages.cu).
 #pragma once
+#include <atomic>
+
 #include "kvq_internal.h"
 
 namespace kvq {
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device (`done`:
+// the kernel's own, a bit per device).
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // One layer's pages (kvq_paged_cache) with the table of a call's sequences.
 struct PagedArgs {

@@ -102,11 +102,7 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
 
   // ---- the block's page: its sequence, positions and rows ----
   const int u = blockIdx.x, P = a.pg.P, sh = a.pg.p_shift;
-  int lo = 0, hi = a.r.n_seqs - 1;                        // the largest s with base(s) <= u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((__ldg(a.r.row_offsets + mid) >> sh) + 2 * mid <= u) lo = mid; else hi = mid - 1;
-  }
+  const int lo = warp_search(a.r.n_seqs, u, [&](int s) { return (__ldg(a.r.row_offsets + s) >> sh) + 2 * s; });
   const SeqRows sr = paged_seq_rows(a.r, lo);
   if (sr.rows <= 0 || sr.start < 0 || sr.off < 0 || sr.off + sr.rows > a.r.n_rows) return;
   const int page_i = (sr.start >> sh) + u - ((sr.off >> sh) + 2 * lo);
@@ -276,6 +272,9 @@ paged_gather_kernel(const PagedGatherArgs a, const long long items) {
   }
 }
 
+// a head's rows of the largest page, angles of 1024 pairs, frequencies, the warps' rows
+constexpr size_t kPaMostSmem = 128 * 512 * 2 + 1024 * 16 + 256 * 12 + kPaWarps * 2 * 512 * 2 + 64;
+
 template <int D, bool E4M3>
 cudaError_t launch_append_t(const PagedAppendArgs& a, const RopeFreqs& f, int num_sms, cudaStream_t st) {
   const int P = a.pg.P, half = a.L.rope_dims / 2, n_kv = a.L.n_kv;
@@ -287,8 +286,8 @@ cudaError_t launch_append_t(const PagedAppendArgs& a, const RopeFreqs& f, int nu
   const long long pages = (long long)a.r.n_rows / P + a.r.n_seqs;
   while (hb > 1 && pages * ((n_kv + hb - 1) / hb) * 2 < 4ll * num_sms) hb = (hb + 1) / 2;
   const size_t smem = pa_smem(D, half, hb, cap, rb).total;
-  cudaError_t e = cudaFuncSetAttribute(paged_append_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(paged_append_kernel<D, E4M3>, (int)kPaMostSmem, allowed);
   if (e != cudaSuccess) return e;
   const long long units = (long long)(a.r.n_rows >> a.pg.p_shift) + 2ll * a.r.n_seqs;
   if (units > 0x7fffffffLL) return cudaErrorInvalidValue;

@@ -158,16 +158,9 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
 
   while (x < x_end) {
     // ---- the unit of tile x: group u, kv head h, tiles [t_a, t_b) of its `tiles` ----
-    int u;
-    {
-      int lo = 0, hi = n_groups - 1;                      // the largest u with prefix[u] n_kv <= x
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(prefix + mid) * n_kv <= x) lo = mid; else hi = mid - 1;
-      }
-      u = lo;
-    }
-    const PagedGroup g = paged_group(a.r, a.pg, W, TG, KT, u);
+    const auto first_tile = [=](int i) { return __ldg(prefix + i) * n_kv; };
+    const int u = warp_search(n_groups, x, first_tile);
+    const PagedGroup g = paged_group<true>(a.r, a.pg, W, TG, KT, u);
     const long long in_u = x - __ldg(prefix + u) * n_kv;
     const int h = (int)(in_u / g.tiles), t_a = (int)(in_u - (long long)h * g.tiles);
     const int n = (int)min((long long)(g.tiles - t_a), x_end - x);
@@ -579,10 +572,12 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
   }
 }
 
-// The units that were cut: one block per (unit, 512 outputs of it), each
-// thread four dims of one row over the unit's pieces in order.
+// The units that were cut: one block per (unit, 128 outputs of it); eight
+// threads share four dims of one row, each every eighth piece (a unit may have
+// dozens), and add up in a fixed order.
+constexpr int kMergeWays = 8;
 template <int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(256)
 paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, const int ctas, const long long* prefix,
                    const float* part_o, const float* part_ml) {
   pdl_launch();
@@ -597,25 +592,47 @@ paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, cons
   const long long x0 = pu * n_kv + (long long)h * tiles, x1 = x0 + tiles;
   const int c0 = shares.cta_of(x0), c1 = shares.cta_of(x1 - 1);
   if (c0 == c1) return;                                   // one CTA had it whole
-  const PagedGroup g = paged_group(a.r, a.pg, a.L.window, TG, Pd<D>::KT, u);
-  const int i = blockIdx.y * 128 + threadIdx.x;
-  if (i >= g.nt * G * (D / 4)) return;
-  const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+  const PagedGroup g = paged_group<true>(a.r, a.pg, a.L.window, TG, Pd<D>::KT, u);
+  __shared__ float4 so[kMergeWays][32];
+  __shared__ float2 sl[kMergeWays][32];
+  const int way = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = blockIdx.y * 32 + lane, r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+  const bool valid = r < g.nt * G;
   const int first = 2 * c0 + (shares.begin(c0) == x0 ? 0 : 1);
-  float M = -INFINITY;
-  for (int c = c0; c <= c1; ++c) {
-    const int slot = c == c0 ? first : 2 * c;
-    M = fmaxf(M, __ldg(part_ml + (size_t)slot * 32 + r));
-  }
-  float l = 0.f;
+  // the way's pieces relative to their largest reference
+  float M = -INFINITY, l = 0.f;
   float4 o = {0.f, 0.f, 0.f, 0.f};
+  if (valid) {
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const int slot = c == c0 ? first : 2 * c;
-    const float m = __ldg(part_ml + (size_t)slot * 32 + r), lp = __ldg(part_ml + (size_t)slot * 32 + 16 + r);
-    const float4 v = __ldg(reinterpret_cast<const float4*>(part_o + ((size_t)slot * 16 + r) * D + d));
-    const float f = m == -INFINITY ? 0.f : ex2(m - M);
-    l = fmaf(lp, f, l);
+    for (int c = c0 + way; c <= c1; c += kMergeWays)
+      M = fmaxf(M, __ldg(part_ml + (size_t)(c == c0 ? first : 2 * c) * 32 + r));
+#pragma unroll 4
+    for (int c = c0 + way; c <= c1; c += kMergeWays) {
+      const int slot = c == c0 ? first : 2 * c;
+      const float m = __ldg(part_ml + (size_t)slot * 32 + r), lp = __ldg(part_ml + (size_t)slot * 32 + 16 + r);
+      const float4 v = __ldg(reinterpret_cast<const float4*>(part_o + ((size_t)slot * 16 + r) * D + d));
+      const float f = m == -INFINITY ? 0.f : ex2(m - M);
+      l = fmaf(lp, f, l);
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  so[way][lane] = o;
+  sl[way][lane] = make_float2(M, l);
+  __syncthreads();
+  if (way != 0 || !valid) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWays; ++w) M = fmaxf(M, sl[w][lane].x);
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kMergeWays; ++w) {
+    const float2 ml = sl[w][lane];
+    const float4 v = so[w][lane];
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+    l = fmaf(ml.y, f, l);
     o.x = fmaf(v.x, f, o.x);
     o.y = fmaf(v.y, f, o.y);
     o.z = fmaf(v.z, f, o.z);
@@ -681,7 +698,8 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   if (!pages_map(&tmk, a.pg.k_codes, D, a.pg.P, (long long)a.pg.n_pages * a.L.n_kv) ||
       !pages_map(&tmv, a.pg.v_codes, D, a.pg.P, (long long)a.pg.n_pages * a.L.n_kv))
     return cudaErrorInvalidValue;
-  e = cudaFuncSetAttribute(paged_decode_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+  static std::atomic<uint64_t> allowed{0};
+  e = allow_smem(paged_decode_kernel<D, E4M3>, S::BYTES, allowed);
   if (e != cudaSuccess) return e;
   if ((e = prof_before(st)) != cudaSuccess) return e;
   e = launch_pdl(paged_decode_kernel<D, E4M3>, dim3(p.ctas), dim3(kPdThreads), S::BYTES, st, a, tmk, tmv, p.TG, p.n_groups,
@@ -691,8 +709,8 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   if (p.max_tiles < 2) return cudaSuccess;                // a single tile is never cut
   const long long units = (long long)p.n_groups * a.L.n_kv;
   if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const int slices = (p.TG * a.L.G * (D / 4) + 127) / 128;
-  return launch_pdl(paged_merge_kernel<D>, dim3((unsigned)units, slices), dim3(128), 0, st, a, p.TG, p.n_groups, p.ctas,
+  const int slices = (p.TG * a.L.G * (D / 4) + 31) / 32;
+  return launch_pdl(paged_merge_kernel<D>, dim3((unsigned)units, slices), dim3(32 * kMergeWays), 0, st, a, p.TG, p.n_groups, p.ctas,
                     prefix, part_o, part_ml);
 }
 

@@ -183,7 +183,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   const int cta = (int)tc::cta_rank();                    // of the pair
   const int rank = (blockIdx.x >> 1) / per, hx = (blockIdx.x >> 1) - rank * per;
   const int u = __ldg(order + rank), h = hx / S::NSPLIT, d_base = (hx % S::NSPLIT) * DO;
-  const PagedGroup g = paged_group(a.r, a.pg, W, TQ, KT, u);
+  const PagedGroup g = paged_group<true>(a.r, a.pg, W, TQ, KT, u);
   if (g.tiles == 0) return;
   const int n_all = g.tiles;
   const int pieces = pf_pieces(n_all, splits);
@@ -651,7 +651,7 @@ paged_join_kernel(const PagedReadArgs a, const int TQ, const int splits, const f
   pdl_wait();
   const int per = a.L.n_kv * S::NSPLIT, G = a.L.G;
   const int u = blockIdx.x / per, hx = blockIdx.x - u * per;
-  const PagedGroup g = paged_group(a.r, a.pg, a.L.window, TQ, S::KT, u);
+  const PagedGroup g = paged_group<true>(a.r, a.pg, a.L.window, TQ, S::KT, u);
   if (g.tiles == 0) return;
   const int pieces = pf_pieces(g.tiles, splits);
   if (pieces == 1) return;
@@ -752,7 +752,8 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   if (e != cudaSuccess) return e;
   e = launch_paged_prep<D>(a, f, p.TQ, S::KT, p.n_groups, q16, nullptr, order, status, num_sms, st);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(paged_prefill_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+  static std::atomic<uint64_t> allowed{0};
+  e = allow_smem(paged_prefill_kernel<D, E4M3>, S::BYTES, allowed);
   if (e != cudaSuccess) return e;
   if ((e = prof_before(st)) != cudaSuccess) return e;
   e = launch_pdl(paged_prefill_kernel<D, E4M3>, dim3((unsigned)p.units * 2, p.splits), dim3(S::THREADS), S::BYTES, st, a,

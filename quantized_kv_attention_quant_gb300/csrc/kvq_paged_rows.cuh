@@ -26,6 +26,8 @@ struct PagedGroup {
   int tiles;    // key tiles of KT from there (0: nothing to read)
 };
 
+// WARP: u is the same in all lanes, which search together.
+template <bool WARP>
 __device__ __forceinline__ PagedGroup paged_group(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
                                                   int u) {
   PagedGroup g;
@@ -36,10 +38,16 @@ __device__ __forceinline__ PagedGroup paged_group(const PagedRows& r, const Page
     g.p0 = __ldg(r.start + u);
     take = 1;
   } else {
-    int lo = 0, hi = r.n_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(r.row_offsets + mid) / TG + mid <= u) lo = mid; else hi = mid - 1;
+    const auto base = [&](int s) { return __ldg(r.row_offsets + s) / TG + s; };
+    int lo = 0;
+    if constexpr (WARP) {
+      lo = warp_search(r.n_seqs, u, base);
+    } else {
+      int hi = r.n_seqs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (base(mid) <= u) lo = mid; else hi = mid - 1;
+      }
     }
     const SeqRows sr = paged_seq_rows(r, lo);
     g.s = lo;
@@ -74,7 +82,7 @@ __device__ __forceinline__ void paged_plan_block(const PagedRows& r, const Paged
     const int u = u0 + tid;
     int t = 0;
     if (u < n_groups) {
-      const PagedGroup g = paged_group(r, pg, window, TG, KT, u);
+      const PagedGroup g = paged_group<false>(r, pg, window, TG, KT, u);
       t = g.tiles;
       bad |= g.bad > 0;
     }
@@ -117,7 +125,7 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
   bool bad = false;
   auto bin_of = [](int tiles) { return kOrderBins - 1 - min(tiles, kOrderBins - 1); };   // most first
   for (int u = tid; u < n_groups; u += kPrWarps * 32) {
-    const PagedGroup g = paged_group(r, pg, window, TG, KT, u);
+    const PagedGroup g = paged_group<false>(r, pg, window, TG, KT, u);
     bad |= g.bad > 0;
     atomicAdd(&bins[bin_of(g.tiles)], 1);
   }
@@ -142,7 +150,7 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
   for (int k = 0; k < PER; ++k) bins[PER * tid + k] = before + mine[k];
   const bool any = __syncthreads_or(bad);
   for (int u = tid; u < n_groups; u += kPrWarps * 32) {
-    const PagedGroup g = paged_group(r, pg, window, TG, KT, u);
+    const PagedGroup g = paged_group<false>(r, pg, window, TG, KT, u);
     order[atomicAdd(&bins[bin_of(g.tiles)], 1)] = u;
   }
   if (tid == 0) *status = any ? (1u << KVQ_DEV_BADSEQ) : 0u;
