@@ -49,6 +49,7 @@ namespace {
 
 constexpr int kPdThreads = 128;
 constexpr int kPdMinKeys = 128;          // shortest share of a CTA, keys
+constexpr int kPdPlan = 1024;            // groups that a CTA plans itself
 
 template <int D>
 struct Pd {
@@ -77,7 +78,8 @@ struct Pd {
   static constexpr int M_OFF = P_OFF + (WD > 1 ? 4096 : 0);        // row maxima [2][4 warps][16]
   static constexpr int S_OFF = M_OFF + 512;             // scales [4 warps][4 tiles][SW][2]
   static constexpr int B_OFF = S_OFF + 4 * 4 * 2 * 2 * 4;          // barriers [4 warps][DEP][NB]
-  static constexpr int BYTES = B_OFF + 4 * DEP * NB * 8;
+  static constexpr int PLAN_OFF = B_OFF + 4 * DEP * NB * 8;       // a small call's plan, and 4 sums
+  static constexpr int BYTES = PLAN_OFF + (kPdPlan + 1 + 4) * 4;
   static constexpr int OSTR = D + 4;                    // floats of a merged row (a row's start moves by 4 banks)
   static_assert(TEAMS * 16 * OSTR * 4 + 128 * 4 <= RING, "the merge of a CTA's warps reuses the ring");
 };
@@ -101,14 +103,19 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
 __device__ __forceinline__ uint4 lds128(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// The shares of a call: T tiles over nc CTAs, CTA c taking [T c / nc, T (c+1) / nc).
+// The shares of a call: a line of T places (a unit has one for what it costs at
+// all, then one per key tile) over nc CTAs, CTA c taking those from
+// ceil(T c / nc) to before ceil(T (c + 1) / nc).
 struct PdShares {
   long long T;
   int nc;
-  __device__ long long begin(int c) const { return T * c / nc; }
-  __device__ int cta_of(long long x) const { return (int)(((x + 1) * nc - 1) / T); }
+  __device__ long long begin(int c) const { return (T * c + nc - 1) / nc; }
+  __device__ int cta_of(long long x) const { return (int)(x * nc / T); }
 };
 template <int D>
 __device__ __forceinline__ PdShares pd_shares(long long T, int ctas) {
@@ -137,14 +144,27 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
   float* scale = reinterpret_cast<float*>(sm + S::S_OFF) + warp * 4 * SW * 2;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::B_OFF) + warp * DEP * NB;
   if (lane == 0) {
+    prefetch_map(&tmk);
+    prefetch_map(&tmv);
     for (int i = 0; i < DEP * NB; ++i) mbar_init(full + i, 1);
     fence_mbar_init();
   }
   __syncwarp();
   pdl_launch();
-  pdl_wait();                                             // q16, the plan and the status word are written
-  const PdShares shares = pd_shares<D>(__ldg(prefix + n_groups) * n_kv, gridDim.x);
-  if (shares.T == 0 || (int)blockIdx.x >= shares.nc) return;
+  // The prep kernel lets this one start when the kernels before both are
+  // complete, so up to kPdPlan groups are planned here, and the first keys asked
+  // for, while it runs; q16 and the status word are waited for before their use.
+  const bool own = n_groups <= kPdPlan;
+  int* const plan = reinterpret_cast<int*>(sm + S::PLAN_OFF);
+  if (own) paged_plan<4>(a.r, a.pg, W, TG, KT, n_groups, plan, plan + kPdPlan + 1);
+  else pdl_wait();
+  bool waited = !own;
+  const auto width_before = [=](int i) { return own ? (long long)plan[i] : __ldg(prefix + i); };
+  const PdShares shares = pd_shares<D>(width_before(n_groups) * n_kv, gridDim.x);
+  if (shares.T == 0 || (int)blockIdx.x >= shares.nc) {
+    if (own) pdl_wait();                                  // (whoever waits for this kernel waits for that one)
+    return;
+  }
   long long x = shares.begin(blockIdx.x);
   const long long x_begin = x, x_end = shares.begin(blockIdx.x + 1);
   int used = 0;                                           // tiles the ring has held
@@ -157,13 +177,21 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
   };
 
   while (x < x_end) {
-    // ---- the unit of tile x: group u, kv head h, tiles [t_a, t_b) of its `tiles` ----
-    const auto first_tile = [=](int i) { return __ldg(prefix + i) * n_kv; };
-    const int u = warp_search(n_groups, x, first_tile);
+    // ---- the unit of place x: group u, kv head h, n of its key tiles from t_a ----
+    const auto first_place = [=](int i) { return width_before(i) * n_kv; };
+    const int u = warp_search(n_groups, x, first_place);
+    const long long w0 = width_before(u);
+    const int width = (int)(width_before(u + 1) - w0);
     const PagedGroup g = paged_group<true>(a.r, a.pg, W, TG, KT, u);
-    const long long in_u = x - __ldg(prefix + u) * n_kv;
-    const int h = (int)(in_u / g.tiles), t_a = (int)(in_u - (long long)h * g.tiles);
-    const int n = (int)min((long long)(g.tiles - t_a), x_end - x);
+    const int in_u = (int)(x - w0 * n_kv);
+    const int h = in_u / width, at = in_u - h * width;
+    const int t_a = max(at - 1, 0);
+    const int places = (int)min((long long)(width - at), x_end - x);
+    const int n = places - (at == 0 ? 1 : 0);
+    if (n == 0) {                                         // the share ends before the unit's first tile
+      x += places;
+      continue;
+    }
     const int k0 = g.kt0 + KT * t_a;                      // first position of the piece
     const int rows = g.nt * G;
 
@@ -237,6 +265,11 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
       raw = look_up(2);
     }
     pid_k = pid_v;
+
+    if (!waited) {
+      pdl_wait();
+      waited = true;
+    }
 
     // ---- q fragments of the unit: step 4 b + t takes dims 64 b + 16 c + 4 t .. +3 of lane column c ----
     uint32_t qf[S::QREG ? KS : 1][4];
@@ -529,7 +562,7 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
       }
     }
     __syncthreads();
-    const bool whole = n == g.tiles;
+    const bool whole = n == width - 1;
     const int slot = 2 * blockIdx.x + (x == x_begin ? 0 : 1);
     for (int i = tid; i < rows * (D / 4); i += kPdThreads) {
       const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
@@ -568,8 +601,9 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
     }
     fence_proxy_async();                                  // (the accelerator writes there next)
     __syncthreads();
-    x += n;
+    x += places;
   }
+  if (!waited) pdl_wait();
 }
 
 // The units that were cut: one block per (unit, 128 outputs of it); eight
@@ -586,11 +620,11 @@ paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, cons
   const int u = blockIdx.x / n_kv, h = blockIdx.x - u * n_kv;
   const long long T = __ldg(prefix + n_groups) * n_kv;
   const long long pu = __ldg(prefix + u);
-  const int tiles = (int)(__ldg(prefix + u + 1) - pu);
-  if (tiles == 0) return;
+  const int width = (int)(__ldg(prefix + u + 1) - pu);
+  if (width == 0) return;
   const PdShares shares = pd_shares<D>(T, ctas);
-  const long long x0 = pu * n_kv + (long long)h * tiles, x1 = x0 + tiles;
-  const int c0 = shares.cta_of(x0), c1 = shares.cta_of(x1 - 1);
+  const long long x0 = pu * n_kv + (long long)h * width, x1 = x0 + width;
+  const int c0 = shares.cta_of(x0 + 1), c1 = shares.cta_of(x1 - 1);
   if (c0 == c1) return;                                   // one CTA had it whole
   const PagedGroup g = paged_group<true>(a.r, a.pg, a.L.window, TG, Pd<D>::KT, u);
   __shared__ float4 so[kMergeWays][32];
@@ -598,7 +632,7 @@ paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, cons
   const int way = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = blockIdx.y * 32 + lane, r = i / (D / 4), d = (i - r * (D / 4)) * 4;
   const bool valid = r < g.nt * G;
-  const int first = 2 * c0 + (shares.begin(c0) == x0 ? 0 : 1);
+  const int first = 2 * c0 + (shares.begin(c0) >= x0 ? 0 : 1);
   // the way's pieces relative to their largest reference
   float M = -INFINITY, l = 0.f;
   float4 o = {0.f, 0.f, 0.f, 0.f};

@@ -70,20 +70,26 @@ inline int paged_groups(const PagedRows& r, int TG) {
   return r.row_offsets ? r.n_rows / TG + r.n_seqs : r.n_rows;
 }
 
-// prefix[u] = key tiles of the groups before u (one block), and the call's
-// status word.
-__device__ __forceinline__ void paged_plan_block(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
-                                                 int n_groups, long long* prefix, uint32_t* status) {
-  __shared__ int wsum[kPrWarps];
+// The width of a group in a call's shares of work: its key tiles, and one more
+// for what a unit costs however short it is (look-ups, its first copies, its
+// results).  Without it a CTA with ten short units of a ragged batch ended
+// 27 us after one with a single long one (of 115).
+__device__ __forceinline__ int paged_width(int tiles) { return tiles > 0 ? tiles + 1 : 0; }
+
+// prefix[u] = widths of the groups before u, by a block of WARPS warps (wsum:
+// WARPS ints of shared memory); true in every thread if a row is past its table.
+template <int WARPS, typename T>
+__device__ __forceinline__ bool paged_plan(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
+                                           int n_groups, T* prefix, int* wsum) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  long long base = 0;
+  T base = 0;
   bool bad = false;
-  for (int u0 = 0; u0 < n_groups; u0 += kPrWarps * 32) {
+  for (int u0 = 0; u0 < n_groups; u0 += WARPS * 32) {
     const int u = u0 + tid;
     int t = 0;
     if (u < n_groups) {
       const PagedGroup g = paged_group<false>(r, pg, window, TG, KT, u);
-      t = g.tiles;
+      t = paged_width(g.tiles);
       bad |= g.bad > 0;
     }
     int inc = t;
@@ -94,8 +100,8 @@ __device__ __forceinline__ void paged_plan_block(const PagedRows& r, const Paged
     }
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    long long before = base, total = 0;
-    for (int w = 0; w < kPrWarps; ++w) {
+    T before = base, total = 0;
+    for (int w = 0; w < WARPS; ++w) {
       if (w < warp) before += wsum[w];
       total += wsum[w];
     }
@@ -103,11 +109,8 @@ __device__ __forceinline__ void paged_plan_block(const PagedRows& r, const Paged
     base += total;
     __syncthreads();
   }
-  const bool any = __syncthreads_or(bad);
-  if (tid == 0) {
-    prefix[n_groups] = base;
-    *status = any ? (1u << KVQ_DEV_BADSEQ) : 0u;
-  }
+  if (tid == 0) prefix[n_groups] = base;
+  return __syncthreads_or(bad);
 }
 
 // order = the groups, those with the most key tiles first (one block): a
@@ -156,7 +159,7 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
   if (tid == 0) *status = any ? (1u << KVQ_DEV_BADSEQ) : 0u;
 }
 
-// Block 0 makes the plan (the tile prefix, or the order of the groups) and
+// Block 0 makes the plan (the groups' widths added up, or the order of the groups) and
 // writes the status word; the others each prep rb rows of hpb heads, a warp a
 // (row, head) at a time: q_hat as f16 to q16 [n_rows][n_q][D] (exact for bf16 in
 // f16's normal range) and as bf16 to q_prepped.  Rows that read nothing get
@@ -172,8 +175,11 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
   if (blockIdx.x == 0) {
     pdl_wait();
     pdl_launch();
-    if (prefix) paged_plan_block(a.r, a.pg, a.L.window, TG, KT, n_groups, prefix, status);
-    else paged_order_block(a.r, a.pg, a.L.window, TG, KT, n_groups, order, status);
+    if (prefix) {
+      __shared__ int wsum[kPrWarps];
+      const bool bad = paged_plan<kPrWarps>(a.r, a.pg, a.L.window, TG, KT, n_groups, prefix, wsum);
+      if (tid == 0) *status = bad ? (1u << KVQ_DEV_BADSEQ) : 0u;
+    } else paged_order_block(a.r, a.pg, a.L.window, TG, KT, n_groups, order, status);
     return;
   }
   const int R = a.L.rope_dims, half = R >> 1, n_q = a.L.n_q;
