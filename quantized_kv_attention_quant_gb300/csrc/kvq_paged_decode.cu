@@ -277,38 +277,39 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
       auto q_row = [&](int r) {
         return q16 + ((size_t)(g.row0 + r / G) * a.L.n_q + h * G + r % G) * D;
       };
-      if constexpr (S::QREG) {
+      // (a team's warps fill the fragments that all of them read, every fourth block of 64 dims each)
+      constexpr int STEP = S::QREG ? 1 : 4, NBL = D / 64 / STEP;
+      const int b0 = S::QREG ? 0 : warp;
+      uint4 v[NBL][2][2];
 #pragma unroll
-        for (int b = 0; b < D / 64; ++b) {
-          uint4 v[2][2] = {};
+      for (int i = 0; i < NBL; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (rr + 8 * e < rows) {
-              const uint4* src = reinterpret_cast<const uint4*>(q_row(rr + 8 * e) + 64 * b + 16 * cc);
-              v[e][0] = src[0];
-              v[e][1] = src[1];
-            }
-          const uint32_t* w0 = reinterpret_cast<const uint32_t*>(v[0]);
-          const uint32_t* w1 = reinterpret_cast<const uint32_t*>(v[1]);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            qf[4 * b + t][0] = w0[2 * t];
-            qf[4 * b + t][1] = w1[2 * t];
-            qf[4 * b + t][2] = w0[2 * t + 1];
-            qf[4 * b + t][3] = w1[2 * t + 1];
+        for (int e = 0; e < 2; ++e) {
+          v[i][e][0] = v[i][e][1] = make_uint4(0, 0, 0, 0);
+          if (rr + 8 * e < rows) {
+            const uint4* src = reinterpret_cast<const uint4*>(q_row(rr + 8 * e) + 64 * (b0 + STEP * i) + 16 * cc);
+            v[i][e][0] = src[0];
+            v[i][e][1] = src[1];
           }
         }
-      } else {
-        uint4* qs = reinterpret_cast<uint4*>(sm + S::Q_OFF);
-        for (int i = warp; i < KS; i += 4) {
-          const int d = 64 * (i >> 2) + 16 * cc + 4 * (i & 3);
-          uint2 v0 = {0, 0}, v1 = {0, 0};
-          if (rr < rows) v0 = *reinterpret_cast<const uint2*>(q_row(rr) + d);
-          if (rr + 8 < rows) v1 = *reinterpret_cast<const uint2*>(q_row(rr + 8) + d);
-          qs[i * 32 + lane] = make_uint4(v0.x, v1.x, v0.y, v1.y);
+#pragma unroll
+      for (int i = 0; i < NBL; ++i) {
+        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(v[i][0]);
+        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(v[i][1]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          if constexpr (S::QREG) {
+            qf[4 * i + t][0] = w0[2 * t];
+            qf[4 * i + t][1] = w1[2 * t];
+            qf[4 * i + t][2] = w0[2 * t + 1];
+            qf[4 * i + t][3] = w1[2 * t + 1];
+          } else {
+            reinterpret_cast<uint4*>(sm + S::Q_OFF)[(4 * (b0 + STEP * i) + t) * 32 + lane] =
+                make_uint4(w0[2 * t], w1[2 * t], w0[2 * t + 1], w1[2 * t + 1]);
+          }
         }
-        __syncthreads();
       }
+      if constexpr (!S::QREG) __syncthreads();
     }
 
     // what the thread's two rows see, and what all of them do
@@ -615,9 +616,10 @@ __global__ void __launch_bounds__(256)
 paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, const int ctas, const long long* prefix,
                    const float* part_o, const float* part_ml) {
   pdl_launch();
-  pdl_wait();
   const int n_kv = a.L.n_kv, G = a.L.G;
   const int u = blockIdx.x / n_kv, h = blockIdx.x - u * n_kv;
+  const PagedGroup g = paged_group<true>(a.r, a.pg, a.L.window, TG, Pd<D>::KT, u);   // (of the call's inputs alone)
+  pdl_wait();
   const long long T = __ldg(prefix + n_groups) * n_kv;
   const long long pu = __ldg(prefix + u);
   const int width = (int)(__ldg(prefix + u + 1) - pu);
@@ -626,31 +628,49 @@ paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, cons
   const long long x0 = pu * n_kv + (long long)h * width, x1 = x0 + width;
   const int c0 = shares.cta_of(x0 + 1), c1 = shares.cta_of(x1 - 1);
   if (c0 == c1) return;                                   // one CTA had it whole
-  const PagedGroup g = paged_group<true>(a.r, a.pg, a.L.window, TG, Pd<D>::KT, u);
   __shared__ float4 so[kMergeWays][32];
   __shared__ float2 sl[kMergeWays][32];
   const int way = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = blockIdx.y * 32 + lane, r = i / (D / 4), d = (i - r * (D / 4)) * 4;
   const bool valid = r < g.nt * G;
   const int first = 2 * c0 + (shares.begin(c0) >= x0 ? 0 : 1);
-  // the way's pieces relative to their largest reference
+  // the way's pieces, four at a time, relative to the largest reference so far
   float M = -INFINITY, l = 0.f;
   float4 o = {0.f, 0.f, 0.f, 0.f};
   if (valid) {
-#pragma unroll 4
-    for (int c = c0 + way; c <= c1; c += kMergeWays)
-      M = fmaxf(M, __ldg(part_ml + (size_t)(c == c0 ? first : 2 * c) * 32 + r));
-#pragma unroll 4
-    for (int c = c0 + way; c <= c1; c += kMergeWays) {
-      const int slot = c == c0 ? first : 2 * c;
-      const float m = __ldg(part_ml + (size_t)slot * 32 + r), lp = __ldg(part_ml + (size_t)slot * 32 + 16 + r);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(part_o + ((size_t)slot * 16 + r) * D + d));
-      const float f = m == -INFINITY ? 0.f : ex2(m - M);
-      l = fmaf(lp, f, l);
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
+    for (int c = c0 + way; c <= c1; c += 4 * kMergeWays) {
+      float m[4], lp[4];
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at = c + k * kMergeWays;
+        m[k] = -INFINITY;
+        if (at <= c1) {
+          const size_t slot = at == c0 ? first : 2 * at;
+          m[k] = __ldg(part_ml + slot * 32 + r);
+          lp[k] = __ldg(part_ml + slot * 32 + 16 + r);
+          v[k] = __ldg(reinterpret_cast<const float4*>(part_o + (slot * 16 + r) * D + d));
+        }
+      }
+      const float M1 = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), M);
+      const float f0 = M == -INFINITY ? 0.f : ex2(M - M1);
+      M = M1;
+      l *= f0;
+      o.x *= f0;
+      o.y *= f0;
+      o.z *= f0;
+      o.w *= f0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (c + k * kMergeWays <= c1) {
+          const float f = m[k] == -INFINITY ? 0.f : ex2(m[k] - M);
+          l = fmaf(lp[k], f, l);
+          o.x = fmaf(v[k].x, f, o.x);
+          o.y = fmaf(v[k].y, f, o.y);
+          o.z = fmaf(v[k].z, f, o.z);
+          o.w = fmaf(v[k].w, f, o.w);
+        }
+      }
     }
   }
   so[way][lane] = o;
