@@ -14,8 +14,8 @@
 // the same code, else a division).  Units: rows row_offsets[s] .. of sequence s touch at most
 // floor(rows / P) + 2 pages, so unit u of sequence s with base(s) =
 // floor(row_offsets[s] / P) + 2 s is its page number u - base(s); units past
-// the sequence's last page leave at once.  One warp preps a row (an element
-// count of D/32 per lane), with the rotation angles of up to rb rows at a time
+// the sequence's last page leave at once.  One warp preps 256 / D rows at a
+// time (one of 256 or 512), with the rotation angles of up to rb rows at a time
 // computed once for all heads of the block.
 //
 // What bounds it: the float-float prep arithmetic (the angles above all), not
@@ -41,7 +41,7 @@ __host__ __device__ inline PaSmem pa_smem(int D, int half, int hb, int cap, int 
   m.cs = ((size_t)hb * cap * D * 2 + 15) / 16 * 16;
   m.freq = m.cs + (size_t)rb * half * 16;
   m.nrm = m.freq + 16 * (size_t)((3 * half + 3) / 4);
-  m.total = m.nrm + (size_t)kPaWarps * 2 * D * 2;
+  m.total = m.nrm + (size_t)kPaWarps * 2 * (D < 256 ? 256 : D) * 2;
   return m;
 }
 
@@ -49,10 +49,10 @@ __host__ __device__ inline PaSmem pa_smem(int D, int half, int hb, int cap, int 
 // reciprocal is within 2^-23 of x / s, and fl32(x / s) within 2^-24: where both
 // ends of 2^-21 around the product give one code, that is round(fl32(x / s)).
 template <int E, bool E4M3>
-__device__ __forceinline__ void encode_row(const uint32_t (&src)[E / 2], float s, uint32_t (&o)[(E + 3) / 4]) {
+__device__ __forceinline__ void encode_row(const uint32_t (&src)[E / 2], float s, uint32_t (&o)[E / 4]) {
   constexpr float kRound = 12582912.f;                    // 1.5 * 2^23: the sum's last bit is 1
 #pragma unroll
-  for (int i = 0; i < (E + 3) / 4; ++i) o[i] = 0u;
+  for (int i = 0; i < E / 4; ++i) o[i] = 0u;
   if (!(s > 0.f)) return;
   const float rcp = __frcp_rn(s), up = rcp * (1.f + 4.76837158203125e-7f), dn = rcp * (1.f - 4.76837158203125e-7f);
   bool same = true;
@@ -75,7 +75,7 @@ __device__ __forceinline__ void encode_row(const uint32_t (&src)[E / 2], float s
   }
   if (same) return;
 #pragma unroll
-  for (int i = 0; i < (E + 3) / 4; ++i) o[i] = 0u;
+  for (int i = 0; i < E / 4; ++i) o[i] = 0u;
 #pragma unroll
   for (int i = 0; i < E; ++i)
     o[i / 4] |= encode_q<E4M3>(__fdiv_rn((i & 1) ? bf16hi_to_f(src[i / 2]) : bf16lo_to_f(src[i / 2]), s)) << (8 * (i & 3));
@@ -84,18 +84,19 @@ __device__ __forceinline__ void encode_row(const uint32_t (&src)[E / 2], float s
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kPaWarps * 32)
 paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb, const int cap, const int rb) {
-  constexpr int E = D / 32;
+  using PL = PrepLanes<D>;
+  constexpr int E = PL::E, ROUND = kPaWarps * PL::ROWS;   // items of a round
   extern __shared__ __align__(16) uint8_t pa_buf[];
   __shared__ uint32_t amax[kPaMaxHeads];
   __shared__ float s_was[kPaMaxHeads], s_now[kPaMaxHeads];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, sub = tid / PL::N, lane = tid & (PL::N - 1);   // (sub: the row's lanes in the block)
   const int kind = blockIdx.z;                            // 0: K, 1: V
   const int R = kind == 0 ? a.L.rope_dims : 0, half = R >> 1, n_kv = a.L.n_kv;
   const PaSmem m = pa_smem(D, a.L.rope_dims >> 1, hb, cap, rb);
   uint16_t* rows = reinterpret_cast<uint16_t*>(pa_buf);   // [hb][cap][D]
   const Angles ang = {reinterpret_cast<float2*>(pa_buf + m.cs), reinterpret_cast<float2*>(pa_buf + m.cs) + rb * half};
   float (*freq)[3] = reinterpret_cast<float (*)[3]>(pa_buf + m.freq);
-  uint16_t* nr = reinterpret_cast<uint16_t*>(pa_buf + m.nrm) + warp * 2 * D;
+  uint16_t* nr = reinterpret_cast<uint16_t*>(pa_buf + m.nrm) + sub * 2 * D;
   if (R > 0) stage_freqs(freqs.f, half, freq);
   pdl_wait();
   pdl_launch();
@@ -122,15 +123,8 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
   for (int i = 0; i < E; ++i) w[i] = kind == 0 ? bf16_to_f(__ldg(a.k_w + lane * E + i)) : 1.f;
   const uint16_t* raw = (kind == 0 || a.L.k_eq_v) ? a.k_raw : a.v_raw;
 
-  // (row, head) items of the warp
-  struct Item { int r, h; };
-  const auto step = [&](Item& it) {
-    it.h += kPaWarps;
-    while (it.h >= nh) {
-      it.h -= nh;
-      ++it.r;
-    }
-  };
+  const uint32_t inv = prep_inv(nh);
+  const int sub0 = sub & ~(PL::ROWS - 1), in_warp = sub & (PL::ROWS - 1);
   // ---- prep, rb rows at a time ----
   for (int c0 = 0; c0 < n; c0 += rb) {
     const int cnt = min(rb, n - c0);
@@ -142,20 +136,21 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
       }
     }
     __syncthreads();
-    Item at = {warp / nh, warp % nh}, ahead = at;
+    // (row, head) items, one round ahead (past the last: the last again)
+    const int items = cnt * nh;
     uint32_t nx[E / 2] = {};
-    const auto fetch = [&](const Item& it) {
-      if (it.r < cnt) load_pairs<E>(nx, raw + ((size_t)(row0 + c0 + it.r) * n_kv + h0 + it.h) * D + lane * E);
+    const auto fetch = [&](int i) {
+      const PrepItem it = prep_item(min(i, items - 1), nh, inv);
+      load_pairs<E>(nx, raw + ((size_t)(row0 + c0 + it.r) * n_kv + h0 + it.h) * D + lane * E);
     };
-    fetch(ahead);
-    step(ahead);
-    for (; at.r < cnt; step(at)) {
+    fetch(sub);
+    for (int i0 = sub0; i0 < items; i0 += ROUND) {
+      const PrepItem at = prep_item(min(i0 + in_warp, items - 1), nh, inv);
       const int r = at.r, hh = at.h;
       uint32_t x[E / 2], y[E / 2];
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) x[i] = nx[i];
-      fetch(ahead);
-      step(ahead);
+      if (i0 + ROUND < items) fetch(i0 + ROUND + in_warp);
       prep_row<D>(x, w, a.L.eps, R, ang, r, nr, y);
       store_pairs<E>(rows + (hh * cap + c0 + r) * D + lane * E, y);
       float top = 0.f;
@@ -163,7 +158,7 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
       for (int i = 0; i < E / 2; ++i)
         top = fmaxf(top, fmaxf(fabsf(bf16lo_to_f(y[i])), fabsf(bf16hi_to_f(y[i]))));
 #pragma unroll
-      for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      for (int k = PL::N / 2; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
       if (lane == 0) atomicMax(&amax[hh], __float_as_uint(top));   // (of magnitudes: ordered as their bits)
       if (a.prepped) {
         uint16_t* d = a.prepped + (((size_t)kind * a.r.n_rows + row0 + c0 + r) * n_kv + h0 + hh) * D + lane * E;
@@ -217,15 +212,14 @@ paged_append_kernel(const PagedAppendArgs a, const RopeFreqs freqs, const int hb
   }
 
   // ---- the new rows' codes ----
-  for (Item at = {warp / nh, warp % nh}; at.r < n; step(at)) {
+  for (int i = sub; i < n * nh; i += ROUND) {
+    const PrepItem at = prep_item(i, nh, inv);
     const int r = at.r, hh = at.h;
     uint32_t src[E / 2];
     load_pairs<E>(src, rows + (hh * cap + r) * D + lane * E);
-    uint32_t o[(E + 3) / 4];
+    uint32_t o[E / 4];
     encode_row<E, E4M3>(src, s_now[hh], o);
     uint8_t* dst = codes + ((((size_t)hh) << sh) + slot0 + r) * D + lane * E;
-    if constexpr (E == 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)o[0];
-    if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst) = o[0];
     if constexpr (E == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
     if constexpr (E == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
   }

@@ -1,15 +1,16 @@
-// The rows' prep of the paged calls: RMSNorm and RoPE of one row by one warp,
-// D/32 consecutive elements a lane, each rounded to the bf16 nearest to the
-// exact result (the precision contract of kvq_common.cuh).
+// The rows' prep of the paged calls: RMSNorm and RoPE of 256 / D rows (one of
+// 256 or 512) at a time by one warp, at least 8 consecutive elements a lane, each
+// rounded to the bf16 nearest to the exact result (the precision contract of
+// kvq_common.cuh).
 //
 // The float-float arithmetic that decides every rounding is needed only where
 // a plain fp32 result lies near a tie.  So the row is formed in fp32 with a
 // bound on its error, rounded from both ends of the interval, and only where
 // the two differ in bf16 is the exact form taken: for the norm the whole row
 // (its sum of squares), for the rotation the element.
-//   Norm.  x^2 is exact; a lane's D/32 squares are summed in two chains, so that
-//   at most D/64 + 1 + 5 (warp) additions and one of eps round: <= 15 * 2^-24 of
-//   the sum, half of it in 1/sqrt, whose approximation is within 2^-22.9 (2.2 *
+//   Norm.  x^2 is exact; a lane's 8 or 16 squares are summed in two chains, so
+//   that at most 8 + 1 + 5 (lanes) additions and one of eps round: <= 15 * 2^-24
+//   of the sum, half of it in 1/sqrt, whose approximation is within 2^-22.9 (2.2 *
 //   2^-24), and the product with x w (exact) rounds once: below 11 * 2^-24; 12 *
 //   2^-24 are taken.
 //   Rotation.  r = fl(x c + fl(y s)) with c, s the leading floats of the angle.
@@ -32,49 +33,55 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   return r;
 }
 
-// E 16-bit values as pairs, in the widest accesses (16-byte aligned rows).
+// E 16-bit values as pairs, 16 bytes an access.
 template <int E>
 __device__ __forceinline__ void load_pairs(uint32_t (&v)[E / 2], const uint16_t* p) {
-  if constexpr (E == 2) v[0] = *reinterpret_cast<const uint32_t*>(p);
-  if constexpr (E == 4) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    v[0] = x.x;
-    v[1] = x.y;
-  }
-  if constexpr (E >= 8) {
 #pragma unroll
-    for (int i = 0; i < E / 8; ++i) {
-      const uint4 x = reinterpret_cast<const uint4*>(p)[i];
-      v[4 * i] = x.x;
-      v[4 * i + 1] = x.y;
-      v[4 * i + 2] = x.z;
-      v[4 * i + 3] = x.w;
-    }
+  for (int i = 0; i < E / 8; ++i) {
+    const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+    v[4 * i] = x.x;
+    v[4 * i + 1] = x.y;
+    v[4 * i + 2] = x.z;
+    v[4 * i + 3] = x.w;
   }
 }
 template <int E>
 __device__ __forceinline__ void store_pairs(uint16_t* p, const uint32_t (&v)[E / 2]) {
-  if constexpr (E == 2) *reinterpret_cast<uint32_t*>(p) = v[0];
-  if constexpr (E == 4) *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
-  if constexpr (E >= 8) {
 #pragma unroll
-    for (int i = 0; i < E / 8; ++i)
-      reinterpret_cast<uint4*>(p)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  }
+  for (int i = 0; i < E / 8; ++i)
+    reinterpret_cast<uint4*>(p)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// A row's lanes, and rows of a warp.
+template <int D>
+struct PrepLanes {
+  static constexpr int E = D < 256 ? 8 : D / 32;          // elements a lane
+  static constexpr int N = D / E;                         // lanes a row
+  static constexpr int ROWS = 32 / N;                     // rows a warp
+};
+
+// Item i of n rows (r) by heads (h), i < 2^16; inv = ceil(2^32 / heads) gives
+// i / heads exactly (for one head it passes 32 bits).
+struct PrepItem { int r, h; };
+__device__ __forceinline__ uint32_t prep_inv(int heads) { return 0xFFFFFFFFu / (uint32_t)heads + 1u; }
+__device__ __forceinline__ PrepItem prep_item(int i, int heads, uint32_t inv) {
+  const int r = heads == 1 ? i : (int)__umulhi((uint32_t)i, inv);
+  return {r, i - r * heads};
 }
 
 // Angles of a block's rows: the leading floats (cos, sin) and the rest apart,
-// R/2 pairs a row.  Under full rotation lane l and l + 16 rotate elements
-// l E .. with the pairs l E .., two of them 16 bytes apart from the next lane's:
-// pair j = l E + 2 i + e is entry 32 i + 2 l + e.
+// R/2 pairs a row.  Under full rotation lane l of a row's first half and its
+// partner in the second rotate elements l E .. with the pairs l E .., two of them
+// 16 bytes apart from the next lane's: pair j = l E + 2 i + e is entry
+// N i + 2 l + e.
 struct Angles {
   float2* hi;
   float2* lo;
 };
 template <int D>
 __device__ __forceinline__ int angle_at(int R, int j) {
-  constexpr int E = D / 32;
-  return R == D ? (j % E / 2) * 32 + j / E * 2 + (j & 1) : j;
+  constexpr int E = PrepLanes<D>::E;
+  return R == D ? (j % E / 2) * PrepLanes<D>::N + j / E * 2 + (j & 1) : j;
 }
 template <int D>
 __device__ __forceinline__ void put_angle(const Angles& t, int row, int R, int j, int p, const float (&f)[3]) {
@@ -94,15 +101,15 @@ __device__ __forceinline__ float2 rot_ends(float x, float y, float c, float s) {
   return make_float2(__fmaf_rn(b, kRotEnds, r) + kUnder, __fmaf_rn(b, -kRotEnds, r) - kUnder);
 }
 
-// raw: the lane's D/32 bf16 in pairs; w: its weights; row: the row's place in
-// the angles; nr: two shared rows [D] of the warp's own (0 < R < D).  Returns the
-// prepped elements in pairs.
-template <int D>
-__device__ __forceinline__ void prep_row(const uint32_t (&raw)[D / 64], const float (&w)[D / 32], const float eps,
+// raw: the lane's E bf16 in pairs; w: its weights; row: the row's place in the
+// angles; nr: two shared rows [D] of the row's own (0 < R < D).  Returns the
+// prepped elements in pairs.  All lanes of the warp call it.
+template <int D, int E = PrepLanes<D>::E>
+__device__ __forceinline__ void prep_row(const uint32_t (&raw)[E / 2], const float (&w)[E], const float eps,
                                          const int R, const Angles& ang, const int row, uint16_t* nr,
-                                         uint32_t (&y)[D / 64]) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, half = R >> 1;
+                                         uint32_t (&y)[E / 2]) {
+  constexpr int N = PrepLanes<D>::N;
+  const int lane = threadIdx.x & (N - 1), half = R >> 1;
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) {
@@ -111,7 +118,7 @@ __device__ __forceinline__ void prep_row(const uint32_t (&raw)[D / 64], const fl
   }
   float ss = s0 + s1;
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+  for (int m = N / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
   const float ms = __fadd_rn(__fmul_rn(ss, 1.f / D), eps);
   float inv;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ms));
@@ -131,25 +138,29 @@ __device__ __forceinline__ void prep_row(const uint32_t (&raw)[D / 64], const fl
       ff_acc_sq(t0, bf16lo_to_f(raw[i]));
       ff_acc_sq(t1, bf16hi_to_f(raw[i]));
     }
-    const ff ex = rms_inv(ff_warp_sum(ff_add(t0, t1)), D, eps);
+    t0 = ff_add(t0, t1);
+#pragma unroll
+    for (int m = N / 2; m >= 1; m >>= 1)
+      t0 = ff_add(t0, ff{__shfl_xor_sync(0xffffffffu, t0.hi, m), __shfl_xor_sync(0xffffffffu, t0.lo, m)});
+    const ff ex = rms_inv(t0, D, eps);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i)
       y[i] = (uint32_t)norm_scale_bf16(bf16lo_to_f(raw[i]), w[2 * i], ex) |
              ((uint32_t)norm_scale_bf16(bf16hi_to_f(raw[i]), w[2 * i + 1], ex) << 16);
   }
   if (R == D) {
-    // x_e c - x_(e+D/2) s in lanes 0..15, x_e c + x_(e-D/2) s in lanes 16..31
-    const float4* t = reinterpret_cast<const float4*>(ang.hi + row * half) + (lane & 15);
-    const uint32_t flip = lane < 16 ? 0x80008000u : 0u;
+    // x_e c - x_(e+D/2) s in the row's first lanes, x_e c + x_(e-D/2) s in the others
+    const float4* t = reinterpret_cast<const float4*>(ang.hi + row * half) + (lane & (N / 2 - 1));
+    const uint32_t flip = lane < N / 2 ? 0x80008000u : 0u;
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
-      const uint32_t o = __shfl_xor_sync(0xffffffffu, y[i], 16) ^ flip;
-      const float4 a = t[16 * i];                         // (cos, sin) of both elements
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, y[i], N / 2) ^ flip;
+      const float4 a = t[N / 2 * i];                        // (cos, sin) of both elements
       const float2 r0 = rot_ends(bf16lo_to_f(y[i]), bf16lo_to_f(o), a.x, a.y);
       const float2 r1 = rot_ends(bf16hi_to_f(y[i]), bf16hi_to_f(o), a.z, a.w);
       uint32_t r = bf16x2_rn(r0.x, r1.x);
       if (r != bf16x2_rn(r0.y, r1.y)) {
-        const float4 b = (reinterpret_cast<const float4*>(ang.lo + row * half) + (lane & 15))[16 * i];
+        const float4 b = (reinterpret_cast<const float4*>(ang.lo + row * half) + (lane & (N / 2 - 1)))[N / 2 * i];
         r = (uint32_t)rot_bf16(bf16lo_to_f(y[i]), bf16lo_to_f(o), ff{a.x, b.x}, ff{-a.y, -b.y}) |
             ((uint32_t)rot_bf16(bf16hi_to_f(y[i]), bf16hi_to_f(o), ff{a.z, b.z}, ff{-a.w, -b.w}) << 16);
       }
@@ -157,13 +168,13 @@ __device__ __forceinline__ void prep_row(const uint32_t (&raw)[D / 64], const fl
     }
   } else if (R > 0) {
     // the normed row to shared memory; the rotated dims are then spread over
-    // all lanes (dim e = lane + 32 k), whatever share of the row they are
+    // all its lanes (dim e = lane + N k), whatever share of the row they are
     uint32_t* nw = reinterpret_cast<uint32_t*>(nr) + lane * (E / 2);
     uint16_t* rt = nr + D;
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) nw[i] = y[i];
     __syncwarp();
-    for (int e = lane; e < R; e += 32) {
+    for (int e = lane; e < R; e += N) {
       const bool low = e < half;
       const int j = low ? e : e - half;
       const float2 a = ang.hi[row * half + j];

@@ -160,18 +160,18 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
 }
 
 // Block 0 makes the plan (the groups' widths added up, or the order of the groups) and
-// writes the status word; the others each prep rb rows of hpb heads, a warp a
-// (row, head) at a time: q_hat as f16 to q16 [n_rows][n_q][D] (exact for bf16 in
+// writes the status word; the others each prep rb rows of hpb heads: q_hat as f16 to q16 [n_rows][n_q][D] (exact for bf16 in
 // f16's normal range) and as bf16 to q_prepped.  Rows that read nothing get
 // their outputs here: zeros for an idle sequence, NaN past the table.
 template <int D>
 __global__ void __launch_bounds__(kPrWarps * 32)
 paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, const int hpb, const int TG, const int KT,
                   const int n_groups, uint16_t* q16, long long* prefix, int32_t* order, uint32_t* status) {
-  constexpr int E = D / 32;
+  using PL = PrepLanes<D>;
+  constexpr int E = PL::E;
   extern __shared__ __align__(16) uint8_t pr_buf[];
   __shared__ int rpos[16], rstart[16];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, sub = tid / PL::N, lane = tid & (PL::N - 1);   // (sub: the row's lanes in the block)
   if (blockIdx.x == 0) {
     pdl_wait();
     pdl_launch();
@@ -185,7 +185,7 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
   const int R = a.L.rope_dims, half = R >> 1, n_q = a.L.n_q;
   Angles ang = {reinterpret_cast<float2*>(pr_buf), reinterpret_cast<float2*>(pr_buf) + rb * half};
   float (*freq)[3] = reinterpret_cast<float (*)[3]>(pr_buf + (size_t)rb * half * 16);
-  uint16_t* nr = reinterpret_cast<uint16_t*>(pr_buf + (size_t)rb * half * 16 + 16 * ((3 * half + 3) / 4)) + warp * 2 * D;
+  uint16_t* nr = reinterpret_cast<uint16_t*>(pr_buf + (size_t)rb * half * 16 + 16 * ((3 * half + 3) / 4)) + sub * 2 * D;
   const int hb = (n_q + hpb - 1) / hpb;
   const int row0 = (blockIdx.x - 1) / hb * rb, h0 = (blockIdx.x - 1) % hb * hpb;
   const int n = min(rb, a.r.n_rows - row0), nh = min(hpb, n_q - h0);
@@ -193,31 +193,29 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
   if (R > 0) stage_freqs(freqs.f, half, freq);
   pdl_wait();
   pdl_launch();
-  // (row, head) items of the warp, one ahead of the other
-  struct Item { int r, h; };
-  const auto step = [&](Item& it) {
-    it.h += kPrWarps;
-    while (it.h >= nh) {
-      it.h -= nh;
-      ++it.r;
-    }
-  };
-  Item at = {warp / nh, warp % nh}, ahead = at;
+  // (row, head) items, kPrWarps PL::ROWS of them at a time, one round ahead (past the last: the last again)
+  const int items = n * nh;
+  const uint32_t inv = prep_inv(nh);
   const uint16_t* base = a.q_raw + ((size_t)row0 * n_q + h0) * D + lane * E;
   uint32_t nx[E / 2] = {};
-  const auto fetch = [&](const Item& it) {
-    if (it.r < n) load_pairs<E>(nx, base + ((size_t)it.r * n_q + it.h) * D);
+  const auto fetch = [&](int i) {
+    const PrepItem it = prep_item(min(i, items - 1), nh, inv);
+    load_pairs<E>(nx, base + ((size_t)it.r * n_q + it.h) * D);
   };
-  fetch(ahead);
-  step(ahead);
+  fetch(sub);
   float w[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) w[i] = bf16_to_f(__ldg(a.q_w + lane * E + i));
-  if (tid < n) {
-    const int row = row0 + tid, s = paged_seq_of(a.r, row);
+  for (int r = tid >> 5; r < n; r += kPrWarps) {
+    const int row = row0 + r;
+    const int s = a.r.row_offsets == nullptr
+                      ? row
+                      : warp_search(a.r.n_seqs, row, [&](int i) { return __ldg(a.r.row_offsets + i); });
     const SeqRows sr = paged_seq_rows(a.r, s);
-    rstart[tid] = sr.start;
-    rpos[tid] = sr.start < 0 ? 0 : sr.start + (row - sr.off);
+    if ((tid & 31) == 0) {
+      rstart[r] = sr.start;
+      rpos[r] = sr.start < 0 ? 0 : sr.start + (row - sr.off);
+    }
   }
   __syncthreads();
   for (int idx = tid; idx < n * half; idx += kPrWarps * 32) {
@@ -225,13 +223,15 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
     put_angle<D>(ang, r, R, j, min(max(rpos[r], 0), (1 << 24) - 1), freq[j]);
   }
   __syncthreads();
-  for (; at.r < n; step(at)) {
+  // (the rounds of a warp: it has PL::ROWS items in each)
+  for (int i0 = sub & ~(PL::ROWS - 1); i0 < items; i0 += kPrWarps * PL::ROWS) {
+    const int ii = i0 + (sub & (PL::ROWS - 1));
+    const PrepItem at = prep_item(min(ii, items - 1), nh, inv);
     const int r = at.r;
     uint32_t raw[E / 2], y[E / 2];
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) raw[i] = nx[i];
-    fetch(ahead);
-    step(ahead);
+    if (i0 + kPrWarps * PL::ROWS < items) fetch(ii + kPrWarps * PL::ROWS);
     prep_row<D>(raw, w, a.L.eps, R, ang, r, nr, y);
     const size_t o = ((size_t)(row0 + r) * n_q + h0 + at.h) * D + lane * E;
     uint32_t f[E / 2];
@@ -259,14 +259,15 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
 template <int D>
 cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG, int KT, int n_groups, uint16_t* q16,
                               long long* prefix, int32_t* order, uint32_t* status, int num_sms, cudaStream_t st) {
-  // few rows: a head a warp, eight heads a block (latency); many: all heads of
+  // few rows: a block takes what its warps prep at once (latency); many: all heads of
   // up to 16 rows, which share their angles (16 KB of them at most)
   const int n_q = a.L.n_q, half = a.L.rope_dims / 2;
   const bool few = (long long)a.r.n_rows * n_q <= 16ll * num_sms;
-  const int hpb = few ? std::min(n_q, kPrWarps) : n_q;
-  int rb = few ? std::max(1, kPrWarps / hpb) : std::max(1, std::min(16, a.r.n_rows / (6 * num_sms)));
+  const int at_once = kPrWarps * PrepLanes<D>::ROWS;
+  const int hpb = few ? std::min(n_q, at_once) : n_q;
+  int rb = few ? std::max(1, std::min(16, at_once / hpb)) : std::max(1, std::min(16, a.r.n_rows / (6 * num_sms)));
   if (half > 0) rb = std::max(1, std::min(rb, 1024 / half));
-  const size_t smem = (size_t)rb * half * 16 + 16 * ((3 * half + 3) / 4) + (size_t)kPrWarps * 2 * D * 2;
+  const size_t smem = (size_t)rb * half * 16 + 16 * ((3 * half + 3) / 4) + (size_t)at_once * 2 * D * 2;
   const long long blocks = (long long)((a.r.n_rows + rb - 1) / rb) * ((n_q + hpb - 1) / hpb) + 1;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_pdl(paged_prep_kernel<D>, dim3((unsigned)blocks), dim3(kPrWarps * 32), smem, st, a, f, rb, hpb, TG, KT,
