@@ -167,7 +167,7 @@ __device__ __forceinline__ int pf_tile0(int n, int pieces, int z) { return (int)
 
 template <int D, bool E4M3>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pf<D>::THREADS, 1)
-paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, const int32_t* order, const uint16_t* q16,
+paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, const int2* order, const uint16_t* q16,
                      float* part_o, float* part_ml, uint32_t* status) {
   using S = Pf<D>;
   constexpr int MT = S::MT, DO = S::DO, KT = S::KT, SUB = S::SUB, KST = S::KST;
@@ -182,8 +182,9 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   const int per = n_kv * S::NSPLIT, z = blockIdx.y;
   const int cta = (int)tc::cta_rank();                    // of the pair
   const int rank = (blockIdx.x >> 1) / per, hx = (blockIdx.x >> 1) - rank * per;
-  const int u = __ldg(order + rank), h = hx / S::NSPLIT, d_base = (hx % S::NSPLIT) * DO;
-  const PagedGroup g = paged_group<true>(a.r, a.pg, W, TQ, KT, u);
+  const int2 us = __ldg(order + rank);
+  const int u = us.x, h = hx / S::NSPLIT, d_base = (hx % S::NSPLIT) * DO;
+  const PagedGroup g = paged_group_of(a.r, a.pg, W, TQ, KT, u, us.y);
   if (g.tiles == 0) return;
   const int n_all = g.tiles;
   const int pieces = pf_pieces(n_all, splits);
@@ -224,20 +225,37 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     tc::tmem_alloc2(const_cast<uint32_t*>(ctl), 512);
     tc::tmem_relinquish2();
   }
-  // ---- q into shared memory: blocks of 64 dims [128 rows x 128 B], swizzled ----
-  for (int i = tid; i < MT * 128 * (D / 8); i += S::THREADS) {
-    const int r = i / (D / 8), c = i - r * (D / 8);       // row, 16-byte chunk of it
-    uint4 v = {0u, 0u, 0u, 0u};
-    const int rg = row0 + r;
-    if (rg < rows) v = *reinterpret_cast<const uint4*>(q16 + ((size_t)(g.row0 + rg / G) * a.L.n_q + h * G + rg % G) * D + 8 * c);
-    *reinterpret_cast<uint4*>(sm + (r >> 7) * S::Q_BYTES + (c >> 3) * 16384 + tc::sw128_off(r & 127, c & 7)) = v;
+  // ---- q into shared memory: blocks of 64 dims [128 rows x 128 B], swizzled; the converter warps fetch their
+  // first codes meanwhile ----
+  constexpr int QT = S::THREADS - 128, QN = MT * 128 * (D / 8);
+  if (warp < 8 || warp >= 12) {
+    const int g_shift = __ffs(G) - 1;                     // (G divides 128)
+    for (int i0 = warp < 8 ? tid : tid - 128; i0 < QN; i0 += 4 * QT) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * QT, r = i / (D / 8), c = i - r * (D / 8), rg = row0 + r;   // row, 16-byte chunk of it
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < QN && rg < rows)
+          v[k] = __ldg(reinterpret_cast<const uint4*>(
+              q16 + ((size_t)(g.row0 + (rg >> g_shift)) * a.L.n_q + h * G + (rg & (G - 1))) * D + 8 * c));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * QT, r = i / (D / 8), c = i - r * (D / 8);
+        if (i < QN)
+          *reinterpret_cast<uint4*>(sm + (r >> 7) * S::Q_BYTES + (c >> 3) * 16384 + tc::sw128_off(r & 127, c & 7)) = v[k];
+      }
+    }
   }
-  fence_proxy_async();
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::cluster_sync();                                     // barriers, tensor memory and q of both CTAs
-  tc::fence_after_sync();
-  const uint32_t tmem = ctl[0];
+  auto meet = [&]() {                                     // barriers, tensor memory and q of both CTAs
+    fence_proxy_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after_sync();
+    return ctl[0];
+  };
   bool dead = false;
   auto wait = [&](uint64_t* bar, int parity) {
     if (!dead && !mbar_wait(bar, parity)) {
@@ -251,6 +269,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   if (warp >= 8) {
     if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp >= 12) {
+      const uint32_t tmem = meet();
       // ================= products of both CTAs (CTA 0) =================
       if (cta == 0 && warp == 12) {
         constexpr uint32_t ID_QK = tc::idesc_f16_f32(256, KT), ID_PV = tc::idesc_f16_f32(256, DO) | kMnMajorB;
@@ -329,10 +348,11 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
         const int key = k0 + KT * t + 16 * run;
         return t < n && key <= g.hi && key + 15 >= g.lo ? __ldg(table + (key >> sh)) : -2;
       };
+      bool bad = false;
       auto checked = [&](int id) {
         if (id == -2) return -1;
         if ((unsigned)id < (unsigned)a.pg.n_pages) return id;
-        ctl[1] = 1;
+        bad = true;
         return -1;
       };
       // J loads of run `run` of tile t, rows r + 8 (j / nb)
@@ -414,6 +434,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       }
       load_k(0, id0, idk_of(id0, 0));
       load_v(0, id0);
+      meet();
       put_k(0);
       load_k(1, id1, idk_of(id1, 1));
       for (int i = 0; i < n; ++i) {
@@ -432,6 +453,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
           const uint32_t at = S::V_OFF + st * S::V_BYTES + (cw + 4 * e) * 16 * S::V_ROW;
           put(vb[e], at + v_at, at + (v_at ^ 16u), S::VD < 64 ? 1 : S::VD / 64, S::V_BLK);
         }
+        if (bad) ctl[1] = 1;
         full(v_full + st);
         load_v(i + 1, id1);
 #pragma unroll
@@ -443,6 +465,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     }
   } else {
     // ================= softmax =================
+    const uint32_t tmem = meet();
     if constexpr (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     constexpr int NK = MT == 2 ? KT : KT / 2;             // keys of a tile per thread
     const int wg = warp >> 2;                             // row tile, or half of the keys
@@ -636,7 +659,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   tc::cluster_sync();                                     // neither CTA's memory is used any more
   if (warp == 0) {
     tc::fence_after_sync();
-    tc::tmem_dealloc2(tmem, 512);
+    tc::tmem_dealloc2(ctl[0], 512);
   }
 }
 
@@ -730,7 +753,7 @@ PfWs pf_ws(const LayerArgs& L, int n_rows, const PfPlan& p) {
   PfWs w;
   w.q16 = 256;
   w.order = up(w.q16 + (size_t)n_rows * L.n_q * D * 2);
-  w.part_o = up(w.order + (size_t)p.n_groups * 4);
+  w.part_o = up(w.order + (size_t)p.n_groups * 8);
   w.part_ml = up(w.part_o + prows * S::DO * 4);
   w.total = up(w.part_ml + prows * 8);
   return w;
@@ -745,7 +768,7 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   uint8_t* b = static_cast<uint8_t*>(ws);
   uint32_t* status = reinterpret_cast<uint32_t*>(b);
   uint16_t* q16 = reinterpret_cast<uint16_t*>(b + w.q16);
-  int32_t* order = reinterpret_cast<int32_t*>(b + w.order);
+  int2* order = reinterpret_cast<int2*>(b + w.order);
   float* part_o = reinterpret_cast<float*>(b + w.part_o);
   float* part_ml = reinterpret_cast<float*>(b + w.part_ml);
   cudaError_t e = check_registers<D, E4M3>();

@@ -26,32 +26,19 @@ struct PagedGroup {
   int tiles;    // key tiles of KT from there (0: nothing to read)
 };
 
-// WARP: u is the same in all lanes, which search together.
-template <bool WARP>
-__device__ __forceinline__ PagedGroup paged_group(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
-                                                  int u) {
+// Group u, which belongs to sequence s.
+__device__ __forceinline__ PagedGroup paged_group_of(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
+                                                     int u, int s) {
   PagedGroup g;
   int t0 = 0, take;
+  g.s = s;
   if (r.row_offsets == nullptr) {
-    g.s = u;
     g.row0 = u;
     g.p0 = __ldg(r.start + u);
     take = 1;
   } else {
-    const auto base = [&](int s) { return __ldg(r.row_offsets + s) / TG + s; };
-    int lo = 0;
-    if constexpr (WARP) {
-      lo = warp_search(r.n_seqs, u, base);
-    } else {
-      int hi = r.n_seqs - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (base(mid) <= u) lo = mid; else hi = mid - 1;
-      }
-    }
-    const SeqRows sr = paged_seq_rows(r, lo);
-    g.s = lo;
-    t0 = (u - (sr.off / TG + lo)) * TG;
+    const SeqRows sr = paged_seq_rows(r, s);
+    t0 = (u - (sr.off / TG + s)) * TG;
     take = sr.off >= 0 && sr.off + sr.rows <= r.n_rows ? max(0, min(TG, sr.rows - t0)) : 0;
     g.row0 = sr.off + t0;
     g.p0 = sr.start >= 0 ? sr.start + t0 : -1;
@@ -64,6 +51,27 @@ __device__ __forceinline__ PagedGroup paged_group(const PagedRows& r, const Page
   g.kt0 = g.lo & ~63;
   g.tiles = g.nt > 0 ? (g.hi - g.kt0) / KT + 1 : 0;
   return g;
+}
+
+// Group u; WARP: u is the same in all lanes, which search its sequence together.
+template <bool WARP>
+__device__ __forceinline__ PagedGroup paged_group(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
+                                                  int u) {
+  int s = u;
+  if (r.row_offsets != nullptr) {
+    const auto base = [&](int i) { return __ldg(r.row_offsets + i) / TG + i; };
+    s = 0;
+    if constexpr (WARP) {
+      s = warp_search(r.n_seqs, u, base);
+    } else {
+      int hi = r.n_seqs - 1;
+      while (s < hi) {
+        const int mid = (s + hi + 1) >> 1;
+        if (base(mid) <= u) s = mid; else hi = mid - 1;
+      }
+    }
+  }
+  return paged_group_of(r, pg, window, TG, KT, u, s);
 }
 
 inline int paged_groups(const PagedRows& r, int TG) {
@@ -113,12 +121,12 @@ __device__ __forceinline__ bool paged_plan(const PagedRows& r, const PagedArgs& 
   return __syncthreads_or(bad);
 }
 
-// order = the groups, those with the most key tiles first (one block): a
+// order = the groups (and their sequences), those with the most key tiles first (one block): a
 // counting sort over the tile counts; the order of equal ones is open (it
 // decides only which CTA takes a group).
 constexpr int kOrderBins = 2048;
 __device__ __forceinline__ void paged_order_block(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
-                                                  int n_groups, int32_t* order, uint32_t* status) {
+                                                  int n_groups, int2* order, uint32_t* status) {
   __shared__ int bins[kOrderBins];
   __shared__ int wsum[kPrWarps];
   constexpr int PER = kOrderBins / (kPrWarps * 32);
@@ -154,7 +162,7 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
   const bool any = __syncthreads_or(bad);
   for (int u = tid; u < n_groups; u += kPrWarps * 32) {
     const PagedGroup g = paged_group<false>(r, pg, window, TG, KT, u);
-    order[atomicAdd(&bins[bin_of(g.tiles)], 1)] = u;
+    order[atomicAdd(&bins[bin_of(g.tiles)], 1)] = make_int2(u, g.s);
   }
   if (tid == 0) *status = any ? (1u << KVQ_DEV_BADSEQ) : 0u;
 }
@@ -166,7 +174,7 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
 template <int D>
 __global__ void __launch_bounds__(kPrWarps * 32)
 paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, const int hpb, const int TG, const int KT,
-                  const int n_groups, uint16_t* q16, long long* prefix, int32_t* order, uint32_t* status) {
+                  const int n_groups, uint16_t* q16, long long* prefix, int2* order, uint32_t* status) {
   using PL = PrepLanes<D>;
   constexpr int E = PL::E;
   extern __shared__ __align__(16) uint8_t pr_buf[];
@@ -258,7 +266,7 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
 
 template <int D>
 cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG, int KT, int n_groups, uint16_t* q16,
-                              long long* prefix, int32_t* order, uint32_t* status, int num_sms, cudaStream_t st) {
+                              long long* prefix, int2* order, uint32_t* status, int num_sms, cudaStream_t st) {
   // few rows: a block takes what its warps prep at once (latency); many: all heads of
   // up to 16 rows, which share their angles (16 KB of them at most)
   const int n_q = a.L.n_q, half = a.L.rope_dims / 2;
