@@ -131,6 +131,14 @@ __device__ __forceinline__ void mma2_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 __device__ __forceinline__ void arrive_pair(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(tc::in_cta0(bar)) : "memory");
 }
+// One thread of the warp, always the same, known to the compiler as one: the
+// operands of what it issues stay in uniform registers (27 cycles an MMA; 65, more
+// than the MMA takes, under a test of the lane number).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 constexpr uint32_t kMnMajorB = 1u << 16;                // instruction descriptor: B is MN-major
 
 __device__ __forceinline__ void pf_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -269,7 +277,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   if (warp >= 8) {
     if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp >= 12) {
-      const uint32_t tmem = meet();
+      const uint32_t tmem = __shfl_sync(0xffffffffu, meet(), 0);
       // ================= products of both CTAs (CTA 0) =================
       if (cta == 0 && warp == 12) {
         constexpr uint32_t ID_QK = tc::idesc_f16_f32(256, KT), ID_PV = tc::idesc_f16_f32(256, DO) | kMnMajorB;
@@ -278,7 +286,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
                        v_desc = desc_mn(sb + S::V_OFF, S::V_BLK, 8 * S::V_ROW, S::V_ROW);
         auto qk = [&](int m, int i) {                     // scores of tile i
           const int slot = MT == 2 ? m : i & 1, st = i % KST;
-          if (lane == 0) {
+          if (elect_one()) {
             const uint64_t qd = q_desc + m * (S::Q_BYTES / 16), kd = k_desc + st * (S::K_BYTES / 16);
             const uint32_t d = tmem + S::C_S + KT * slot;
 #pragma unroll
@@ -294,7 +302,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
           const int slot = MT == 2 ? m : i & 1, st = i % KST;
           wait(p_full + slot, MT == 2 ? i & 1 : (i >> 1) & 1);
           tc::fence_after_sync();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint64_t vd = v_desc + st * (S::V_BYTES / 16);
             const uint32_t p = tmem + S::C_S + KT * slot, d = tmem + m * DO;
 #pragma unroll
@@ -307,23 +315,24 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
           }
           __syncwarp();
         };
+        const int n_u = __shfl_sync(0xffffffffu, n, 0);
         wait(k_full, 0);
         tc::fence_after_sync();
         for (int m = 0; m < MT; ++m) qk(m, 0);
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < n_u; ++i) {
           const int nx = i + 1;
           // MT == 1: the next scores under this tile's softmax; MT == 2: each row tile's right behind its P V, in
           // turn, so that one row tile's products run under the other's softmax
-          if (MT == 1 && nx < n) {
+          if (MT == 1 && nx < n_u) {
             wait(k_full + nx % KST, (nx / KST) & 1);
             tc::fence_after_sync();
             qk(0, nx);
           }
           wait(v_full + i % KST, (i / KST) & 1);
-          if (MT == 2 && nx < n) wait(k_full + nx % KST, (nx / KST) & 1);
+          if (MT == 2 && nx < n_u) wait(k_full + nx % KST, (nx / KST) & 1);
           for (int m = 0; m < MT; ++m) {
             pv(m, i);
-            if (MT == 2 && nx < n) qk(m, nx);
+            if (MT == 2 && nx < n_u) qk(m, nx);
           }
         }
       }
