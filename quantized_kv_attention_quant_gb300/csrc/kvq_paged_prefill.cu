@@ -235,13 +235,13 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   }
   // ---- q into shared memory: blocks of 64 dims [128 rows x 128 B], swizzled; the converter warps fetch their
   // first codes meanwhile ----
-  constexpr int QT = S::THREADS - 128, QN = MT * 128 * (D / 8);
+  constexpr int QT = S::THREADS - 128, QN = MT * 128 * (D / 8), QB = 11;   // (QB loads in flight)
   if (warp < 8 || warp >= 12) {
     const int g_shift = __ffs(G) - 1;                     // (G divides 128)
-    for (int i0 = warp < 8 ? tid : tid - 128; i0 < QN; i0 += 4 * QT) {
-      uint4 v[4];
+    for (int i0 = warp < 8 ? tid : tid - 128; i0 < QN; i0 += QB * QT) {
+      uint4 v[QB];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < QB; ++k) {
         const int i = i0 + k * QT, r = i / (D / 8), c = i - r * (D / 8), rg = row0 + r;   // row, 16-byte chunk of it
         v[k] = make_uint4(0u, 0u, 0u, 0u);
         if (i < QN && rg < rows)
@@ -249,7 +249,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
               q16 + ((size_t)(g.row0 + (rg >> g_shift)) * a.L.n_q + h * G + (rg & (G - 1))) * D + 8 * c));
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < QB; ++k) {
         const int i = i0 + k * QT, r = i / (D / 8), c = i - r * (D / 8);
         if (i < QN)
           *reinterpret_cast<uint4*>(sm + (r >> 7) * S::Q_BYTES + (c >> 3) * 16384 + tc::sw128_off(r & 127, c & 7)) = v[k];
@@ -620,41 +620,43 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     const size_t at = ((size_t)(g.row0 + rg / G) * a.L.n_q + h * G + rg % G) * D + d_base + o0;
     const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
 #pragma unroll 1
-    for (int c = 0; c < OC / 16; ++c) {
-      float v[16];
-      tc::ld_x16(t_o + o0 + 16 * c, v);
-      tc::wait_ld();
+    for (int c = 0; c < OC / 32; ++c) {
+      uint32_t w[32];
+      pf_ld32(t_o + o0 + 32 * c, w);
+      pf_wait(w);
       if (!valid) continue;
       if (pieces > 1) {
-        float4* d = reinterpret_cast<float4*>(part_o + prow * DO + o0 + 16 * c);
+        uint4* d = reinterpret_cast<uint4*>(part_o + prow * DO + o0 + 32 * c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        for (int e = 0; e < 8; ++e) d[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         continue;
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] *= inv;
+      for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * inv);
       if (a.out_f32) {
-        float* d = reinterpret_cast<float*>(a.out) + at + 16 * c;
+        uint32_t* d = reinterpret_cast<uint32_t*>(a.out) + at + 32 * c;
+        if (vec) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(d)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) d[e] = w[e];
+        }
+      } else {
+        uint16_t* d = reinterpret_cast<uint16_t*>(a.out) + at + 32 * c;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = bf16x2_rn(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
         if (vec) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            reinterpret_cast<float4*>(d)[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            reinterpret_cast<uint4*>(d)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) d[e] = v[e];
-        }
-      } else {
-        uint16_t* d = reinterpret_cast<uint16_t*>(a.out) + at + 16 * c;
-        if (vec) {
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[e] = (uint32_t)f_to_bf16_rn(v[2 * e]) | ((uint32_t)f_to_bf16_rn(v[2 * e + 1]) << 16);
-          reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) d[e] = f_to_bf16_rn(v[e]);
+          for (int e = 0; e < 16; ++e) {
+            d[2 * e] = (uint16_t)(w[e] & 0xFFFFu);
+            d[2 * e + 1] = (uint16_t)(w[e] >> 16);
+          }
         }
       }
     }
