@@ -25,7 +25,8 @@
 //     O += P V with P from tensor memory.
 //   - eight softmax warps.  MT = 2 (head_dim <= 128): a thread per row, four warps
 //     per row tile; the two row tiles take turns on the tensor cores, one's products
-//     under the other's softmax.  MT = 1: two threads per row, each half of the
+//     under the other's softmax, and P V begins with the first half of the keys while
+//     the second is formed.  MT = 1: two threads per row, each half of the
 //     tile's keys, which exchange the row maximum through shared memory; two score
 //     slots, the next tile's S runs under this one's softmax.  P (f16) overwrites
 //     the scores it comes from.  ref is renewed (and O rescaled) only where a tile
@@ -39,6 +40,18 @@
 // Row tiles are taken longest first (sorted by the prep kernel), and cut along
 // the keys when there are too few of them to fill the GPU; paged_join_kernel
 // joins the pieces in order.
+//
+// Measured (8 q heads a pair of CTAs, GB300): 6374 packed rows of 32 q heads on 8
+// kv heads, D 128, 161 GFLOP: this kernel 172 us alone (0.48 of the measured bf16
+// rate), its prep 45; 500 rows behind 16300 keys, 8 q heads on 2, D 256, 68 GFLOP:
+// 67 us (0.52), join 7.  What bounds it: at D <= 128 the chain of a row tile (scores
+// loaded 110, maxima 670, P 1200, its products and the next scores some 1000 of
+// about 4200 cycles; the tensor cores take 2048 of them for both row tiles), and a
+// CTA's ends, some 9 us of its 40: q and the first keys 4, the first scores 1, the
+// results 2, the next CTA's start 2.  Left out, as measured (us, the first case):
+// P through shared memory, which frees the score slot at once (226 against 226,
+// 78.5 against 75.2 at D 256, which has two slots anyway); one MMA warp per row
+// tile (the two fall into step); a CTA for itself instead of a pair (276 / 103).
 #include <algorithm>
 #include <atomic>
 
@@ -211,7 +224,8 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   uint64_t* s_full = bars + 14;                           // [2] scores of a slot written
   uint64_t* o_full = bars + 16;                           // [2] a row tile's last product
   uint64_t* sc_full = bars + 18;                          // [4] a tile's scales (the CTA's converter warps)
-  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 22);   // tensor memory, bad page
+  uint64_t* p_half = bars + 22;                           // [2] as p_full, MT == 2: the first half of the keys
+  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 24);   // tensor memory, bad page
   const uint32_t sb = smem_u32(sm);
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) {
@@ -222,6 +236,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(p_full + i, MT == 2 ? 8 : 16);
+      mbar_init(p_half + i, 8);
       mbar_init(s_full + i, 1);
       mbar_init(o_full + i, 1);
     }
@@ -300,13 +315,22 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
         };
         auto pv = [&](int m, int i) {                     // O += P V of tile i
           const int slot = MT == 2 ? m : i & 1, st = i % KST;
+          const uint64_t vd = v_desc + st * (S::V_BYTES / 16);
+          const uint32_t p = tmem + S::C_S + KT * slot, d = tmem + m * DO;
+          if constexpr (MT == 2) {
+            wait(p_half + m, i & 1);
+            tc::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+              for (int s = 0; s < KT / 32; ++s) mma2_f16_ts(d, p + 8 * s, vd + s * S::V_ROW, ID_PV, i > 0 || s > 0);
+            }
+            __syncwarp();
+          }
           wait(p_full + slot, MT == 2 ? i & 1 : (i >> 1) & 1);
           tc::fence_after_sync();
           if (elect_one()) {
-            const uint64_t vd = v_desc + st * (S::V_BYTES / 16);
-            const uint32_t p = tmem + S::C_S + KT * slot, d = tmem + m * DO;
 #pragma unroll
-            for (int s = 0; s < KT / 16; ++s) {
+            for (int s = MT == 2 ? KT / 32 : 0; s < KT / 16; ++s) {
               const int col = MT == 2 ? 8 * s : (s / (KT / 32)) * (KT / 2) + 8 * (s % (KT / 32));
               mma2_f16_ts(d, p + col, vd + s * S::V_ROW, ID_PV, i > 0 || s > 0);
             }
@@ -592,6 +616,12 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
           l = fmaf(s0.x + s0.y, f.z, l);
         }
         pf_st16(t_s + 16 * c, pw);
+        if (MT == 2 && c == NCH / 2 - 1) {
+          tc::wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::arrive_cta0(p_half + m);
+        }
       }
       tc::wait_st();
       tc::fence_before_sync();
