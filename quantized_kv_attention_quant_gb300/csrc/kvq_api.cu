@@ -1426,6 +1426,6 @@ const char* kvq_status_string(kvq_status s) {
 
 const char* kvq_last_error(void) { return g_last_error.c_str(); }
 
-int32_t kvq_version(void) { return 140; }
+int32_t kvq_version(void) { return 150; }
 
 }  // extern "C"
