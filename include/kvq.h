@@ -605,7 +605,9 @@ typedef struct {
  *   tables         device int32[n_seqs][max_pages]
  *   row_offsets, start_pos, n_rows, k_raw, v_raw, k_norm_w, kv_prepped
  *                  as for kv_quant_append, with n_seqs and n_rows below 2^24; a
- *                  sequence with a negative start_pos is idle
+ *                  sequence with a negative start_pos is idle; n_rows may be more
+ *                  than row_offsets[n_seqs] (a batch padded to a captured size): here
+ *                  and below the rows behind the last sequence are left as they are
  * Rows of idle sequences, past the table, or whose page the table does not
  * name are not written (to kv_prepped neither).  All inputs must be finite.
  */
@@ -635,7 +637,10 @@ kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t* tables,
  *               batch, whose output is zeros
  *   max_pos     host upper bound of pos[], 0 <= max_pos < 2^24 (sizes the
  *               workspace and the shares of the work)
- *   q_raw, q_norm_w, out, out_is_f32, q_prepped   as for attn_decode
+ *   q_raw, q_norm_w, out, out_is_f32, q_prepped   as for attn_decode; q_hat enters
+ *               its product as f16, so its elements may be up to 65504 (a row with
+ *               a larger one is NaN) and below 2^-14 are rounded to a multiple of
+ *               2^-24
  *   workspace   at least attn_paged_decode_workspace_bytes(...) bytes; its first
  *               4 bytes receive the status word
  * A row whose position is above max_pos or past the table, or one of whose

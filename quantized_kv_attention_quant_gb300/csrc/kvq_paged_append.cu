@@ -240,6 +240,7 @@ paged_gather_kernel(const PagedGatherArgs a, const long long items) {
     const int row = (int)(it / per), in = (int)(it - (long long)row * per);
     const int h = in / (a.D / 16), d0 = (in - h * (a.D / 16)) * 16;
     const SeqRows sr = paged_seq_rows(a.r, paged_seq_of(a.r, row));
+    if (row - sr.off >= sr.rows) continue;                // behind the last sequence
     const int p = sr.start + (row - sr.off);
     const int page = sr.start >= 0 && p >= 0 && p < limit ? paged_page(a.pg, sr.s, p) : -1;
     uint32_t o[8];

@@ -11,6 +11,7 @@ namespace kvq {
 namespace {
 
 constexpr int kPrWarps = 8;           // of the prep kernel's blocks
+constexpr int kNoSeq = -2;            // in the place of a start: the row lies behind the last sequence
 
 // Rows of a read are taken in groups of at most TG consecutive rows of one
 // sequence.  Group u of sequence s with base(s) = floor(row_offsets[s] / TG) + s
@@ -170,7 +171,8 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
 // Block 0 makes the plan (the groups' widths added up, or the order of the groups) and
 // writes the status word; the others each prep rb rows of hpb heads: q_hat as f16 to q16 [n_rows][n_q][D] (exact for bf16 in
 // f16's normal range) and as bf16 to q_prepped.  Rows that read nothing get
-// their outputs here: zeros for an idle sequence, NaN past the table.
+// their outputs here: zeros for an idle sequence, NaN past the table; rows behind
+// the last sequence get none.
 template <int D>
 __global__ void __launch_bounds__(kPrWarps * 32)
 paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, const int hpb, const int TG, const int KT,
@@ -221,7 +223,7 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
                       : warp_search(a.r.n_seqs, row, [&](int i) { return __ldg(a.r.row_offsets + i); });
     const SeqRows sr = paged_seq_rows(a.r, s);
     if ((tid & 31) == 0) {
-      rstart[r] = sr.start;
+      rstart[r] = row - sr.off < sr.rows ? max(sr.start, -1) : kNoSeq;
       rpos[r] = sr.start < 0 ? 0 : sr.start + (row - sr.off);
     }
   }
@@ -246,14 +248,14 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) f[i] = pack_h2(bf16lo_to_f(y[i]), bf16hi_to_f(y[i]));
     store_pairs<E>(q16 + o, f);
-    if (a.q_prepped) {                                    // (only 2-byte alignment is asked of it)
+    if (a.q_prepped && rstart[r] != kNoSeq) {             // (only 2-byte alignment is asked of it)
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
         a.q_prepped[o + 2 * i] = (uint16_t)(y[i] & 0xFFFFu);
         a.q_prepped[o + 2 * i + 1] = (uint16_t)(y[i] >> 16);
       }
     }
-    if (rstart[r] < 0 || rpos[r] < 0 || rpos[r] >= a.pg.limit) {
+    if (rstart[r] != kNoSeq && (rstart[r] < 0 || rpos[r] < 0 || rpos[r] >= a.pg.limit)) {
       const bool idle = rstart[r] < 0;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
@@ -274,6 +276,7 @@ cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG
   const int at_once = kPrWarps * PrepLanes<D>::ROWS;
   const int hpb = few ? std::min(n_q, at_once) : n_q;
   int rb = few ? std::max(1, std::min(16, at_once / hpb)) : std::max(1, std::min(16, a.r.n_rows / (6 * num_sms)));
+  rb = std::max(1, std::min(rb, 32768 / n_q));            // (items of a block: prep_item)
   if (half > 0) rb = std::max(1, std::min(rb, 1024 / half));
   const size_t smem = (size_t)rb * half * 16 + 16 * ((3 * half + 3) / 4) + (size_t)at_once * 2 * D * 2;
   const long long blocks = (long long)((a.r.n_rows + rb - 1) / rb) * ((n_q + hpb - 1) / hpb) + 1;
