@@ -15,6 +15,10 @@
 // of whole pages (codes and scales of every cache) follow in a grid over the
 // GPU, warp by warp in runs of 8 KB, the pairs read from the workspace; they are
 // bound by memory traffic (each byte read and written once).
+//
+// Measured: free and fork of 48 sequences 3.5 us each, reserve 9 (half of it the
+// two passes' loads, half barriers and the cluster), compact's marking 7, the copies
+// of 295 MB of pages (900 pages, 20 layers) 91 us of a call's 102, 6.5 TB/s.
 #include <algorithm>
 
 #include "kvq_common.cuh"
