@@ -21,7 +21,7 @@
 // What bounds it: instructions, of the prep (two thirds) and the codes, not the
 // few bytes per row.  The heads of a block share a row's angles; more heads a
 // block mean fewer angles, fewer blocks and more shared memory.  Measured: 8008
-// rows of 8 kv heads of 128, 52 us (33 MB in, 16 out; issue 67 %); 64 rows of 2
+// rows of 8 kv heads of 128, 50 us (33 MB in, 16 out; issue 67 %); 64 rows of 2
 // heads of 256 in 64 sequences 8.4 us (latency).
 //
 // Gather.  A thread takes 16 codes of one row; 8008 rows of 8 kv heads of 128 in
@@ -272,14 +272,14 @@ paged_gather_kernel(const PagedGatherArgs a, const long long items) {
   }
 }
 
-// a head's rows of the largest page, angles of 1024 pairs, frequencies, the warps' rows
-constexpr size_t kPaMostSmem = 128 * 512 * 2 + 1024 * 16 + 256 * 12 + kPaWarps * 2 * 512 * 2 + 64;
+// a head's rows of the largest page, angles of 512 pairs, frequencies, the warps' rows
+constexpr size_t kPaMostSmem = 128 * 512 * 2 + 512 * 16 + 256 * 12 + kPaWarps * 2 * 512 * 2 + 64;
 
 template <int D, bool E4M3>
 cudaError_t launch_append_t(const PagedAppendArgs& a, const RopeFreqs& f, int num_sms, cudaStream_t st) {
   const int P = a.pg.P, half = a.L.rope_dims / 2, n_kv = a.L.n_kv;
   const int cap = std::min(P, a.r.n_rows);
-  const int rb = half > 0 ? std::max(1, std::min(16, 1024 / half)) : 16;
+  const int rb = half > 0 ? std::max(1, std::min(8, 512 / half)) : 8;     // (16 and 1024: 61.6 us for 59.4)
   // the heads of a block share its angles; as many as 32 KB of rows hold, fewer
   // while there are less than four blocks per SM
   int hb = std::max(1, std::min({n_kv, kPaMaxHeads, 32768 / (cap * D * 2)}));

@@ -57,7 +57,10 @@ namespace {
 
 constexpr int kPdThreads = 128;
 constexpr int kPdMinKeys = 128;          // shortest share of a CTA, keys
-constexpr int kPdPlan = 1024;            // groups that a CTA plans itself
+// Groups that a CTA plans itself, one a thread, in the place of waiting for the
+// prep kernel's plan: 16 single rows 10.5 us a call for 12.5, 64 14.8 for 15.6; beyond
+// that it costs more than the wait (600 rows 52.7 for 51.7, 400 groups of windows 63 for 60).
+constexpr int kPdPlan = kPdThreads;
 
 template <int D>
 struct Pd {
@@ -615,29 +618,44 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
   if (!waited) pdl_wait();
 }
 
-// The units that were cut: one block per (unit, 128 outputs of it); eight
+// The units that were cut: one block per (unit, 128 outputs of it), or, where
+// there are more units than twice the shares, per (cut between two shares, 128
+// outputs); eight
 // threads share four dims of one row, each every eighth piece (a unit may have
 // dozens), and add up in a fixed order.  38 pieces a unit (D 512): 6.4 us, the
 // latency of a few dependent loads (with one thread for all of a unit's pieces,
 // and look-ups by single threads, that call took 93 us in the place of 76).
 constexpr int kMergeWays = 8;
-template <int D>
+template <int D, bool BY_CUT>
 __global__ void __launch_bounds__(256)
 paged_merge_kernel(const PagedReadArgs a, const int TG, const int n_groups, const int ctas, const long long* prefix,
                    const float* part_o, const float* part_ml) {
   pdl_launch();
   const int n_kv = a.L.n_kv, G = a.L.G;
-  const int u = blockIdx.x / n_kv, h = blockIdx.x - u * n_kv;
-  const PagedGroup g = paged_group<true>(a.r, a.pg, a.L.window, TG, Pd<D>::KT, u);   // (of the call's inputs alone)
+  int u = blockIdx.x / n_kv, h = blockIdx.x - u * n_kv;
+  PagedGroup g;
+  if constexpr (!BY_CUT)                                  // (of the call's inputs alone)
+    g = paged_group<true>(a.r, a.pg, a.L.window, TG, Pd<D>::KT, u);
   pdl_wait();
   const long long T = __ldg(prefix + n_groups) * n_kv;
+  const PdShares shares = pd_shares<D>(T, ctas);
+  const int cut = blockIdx.x + 1;
+  if constexpr (BY_CUT) {
+    if (T == 0 || cut >= shares.nc) return;
+    const auto first_place = [=](int i) { return __ldg(prefix + i) * n_kv; };
+    u = warp_search(n_groups, shares.begin(cut), first_place);
+  }
   const long long pu = __ldg(prefix + u);
   const int width = (int)(__ldg(prefix + u + 1) - pu);
   if (width == 0) return;
-  const PdShares shares = pd_shares<D>(T, ctas);
+  if constexpr (BY_CUT) h = (int)((shares.begin(cut) - pu * n_kv) / width);
   const long long x0 = pu * n_kv + (long long)h * width, x1 = x0 + width;
   const int c0 = shares.cta_of(x0 + 1), c1 = shares.cta_of(x1 - 1);
   if (c0 == c1) return;                                   // one CTA had it whole
+  if constexpr (BY_CUT) {
+    if (cut != c0 + 1) return;                            // not the unit's first cut
+    g = paged_group<true>(a.r, a.pg, a.L.window, TG, Pd<D>::KT, u);
+  }
   __shared__ float4 so[kMergeWays][32];
   __shared__ float2 sl[kMergeWays][32];
   const int way = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -772,10 +790,13 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   if ((e = prof_after(st)) != cudaSuccess) return e;
   if (p.max_tiles < 2) return cudaSuccess;                // a single tile is never cut
   const long long units = (long long)p.n_groups * a.L.n_kv;
-  if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // (finding a cut's unit takes two loads more, 256 rows of 2 kv heads 31.8 us a call for 28.7; but most of many
+  // units are not cut: 480 windows of 4 rows, 1920 units, 76 for 128, 1000 rows 77 for 84)
+  const bool by_cut = units > 2ll * p.ctas;
   const int slices = (p.TG * a.L.G * (D / 4) + 31) / 32;
-  return launch_pdl(paged_merge_kernel<D>, dim3((unsigned)units, slices), dim3(32 * kMergeWays), 0, st, a, p.TG, p.n_groups, p.ctas,
-                    prefix, part_o, part_ml);
+  return launch_pdl(by_cut ? paged_merge_kernel<D, true> : paged_merge_kernel<D, false>,
+                    dim3((unsigned)(by_cut ? std::max(1, p.ctas - 1) : units), slices), dim3(32 * kMergeWays), 0, st, a,
+                    p.TG, p.n_groups, p.ctas, prefix, part_o, part_ml);
 }
 
 template <int D>
