@@ -11,12 +11,12 @@
 // writes code = round(x / s) for the new rows; where s grew, the rows that
 // were there become round(code * s_old / s).  All in IEEE fp32 (products with
 // the reciprocal, a little more and a little less, decide where they round to
-// the same code, else a division).  Units: rows row_offsets[s] .. of sequence s touch at most
-// floor(rows / P) + 2 pages, so unit u of sequence s with base(s) =
-// floor(row_offsets[s] / P) + 2 s is its page number u - base(s); units past
-// the sequence's last page leave at once.  One warp preps 256 / D rows at a
-// time (one of 256 or 512), with the rotation angles of up to rb rows at a time
-// computed once for all heads of the block.
+// the same code, else a division).  Units: rows row_offsets[s] .. of sequence s
+// touch at most floor(rows / P) + 2 pages, so unit u of sequence s with base(s) =
+// floor(row_offsets[s] / P) + 2 s is its page number u - base(s); units past the
+// sequence's last page leave at once.  One warp preps 256 / D rows at a time (one
+// of 256 or 512), with the rotation angles of up to rb rows at a time computed
+// once for all heads of the block.
 //
 // What bounds it: instructions, of the prep (two thirds) and the codes, not the
 // few bytes per row.  The heads of a block share a row's angles; more heads a

@@ -620,11 +620,10 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
 
 // The units that were cut: one block per (unit, 128 outputs of it), or, where
 // there are more units than twice the shares, per (cut between two shares, 128
-// outputs); eight
-// threads share four dims of one row, each every eighth piece (a unit may have
-// dozens), and add up in a fixed order.  38 pieces a unit (D 512): 6.4 us, the
-// latency of a few dependent loads (with one thread for all of a unit's pieces,
-// and look-ups by single threads, that call took 93 us in the place of 76).
+// outputs); eight threads share four dims of one row, each every eighth piece (a
+// unit may have dozens), and add up in a fixed order.  38 pieces a unit (D 512):
+// 6.4 us, the latency of a few dependent loads (with one thread for all of a unit's
+// pieces, and look-ups by single threads, that call took 93 us in the place of 76).
 constexpr int kMergeWays = 8;
 template <int D, bool BY_CUT>
 __global__ void __launch_bounds__(256)

@@ -168,13 +168,14 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
   if (tid == 0) *status = any ? (1u << KVQ_DEV_BADSEQ) : 0u;
 }
 
-// Block 0 makes the plan (the groups' widths added up, or the order of the groups) and
-// writes the status word; the others each prep rb rows of hpb heads: q_hat as f16 to q16 [n_rows][n_q][D] (exact for bf16 in
-// f16's normal range) and as bf16 to q_prepped.  Rows that read nothing get
-// their outputs here: zeros for an idle sequence, NaN past the table; rows behind
-// the last sequence get none.  6374 rows of 32 heads of 128: 45 us, instructions (384
-// for two rows of a warp, issue 76 %; the bytes would take 15); one token of 64
-// sequences 5, of 8 sequences with heads of 512 7: angles, norm and rotation in turn.
+// Block 0 makes the plan (the groups' widths added up, or the order of the
+// groups) and writes the status word; the others each prep rb rows of hpb heads:
+// q_hat as f16 to q16 [n_rows][n_q][D] (exact for bf16 in f16's normal range) and
+// as bf16 to q_prepped.  Rows that read nothing get their outputs here: zeros for
+// an idle sequence, NaN past the table; rows behind the last sequence get none.
+// 6374 rows of 32 heads of 128: 45 us, instructions (384 for two rows of a warp,
+// issue 76 %; the bytes would take 15); one token of 64 sequences 5, of 8
+// sequences with heads of 512 7: angles, norm and rotation in turn.
 template <int D>
 __global__ void __launch_bounds__(kPrWarps * 32)
 paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, const int hpb, const int TG, const int KT,
