@@ -21,7 +21,7 @@
 // What bounds it: instructions, of the prep (two thirds) and the codes, not the
 // few bytes per row.  The heads of a block share a row's angles; more heads a
 // block mean fewer angles, fewer blocks and more shared memory.  Measured: 8008
-// rows of 8 kv heads of 128, 50 us (33 MB in, 16 out; issue 67 %); 64 rows of 2
+// rows of 8 kv heads of 128, 50 us (33 MB in, 16 out; issue 71 %); 64 rows of 2
 // heads of 256 in 64 sequences 8.4 us (latency).
 //
 // Gather.  A thread takes 16 codes of one row; 8008 rows of 8 kv heads of 128 in
