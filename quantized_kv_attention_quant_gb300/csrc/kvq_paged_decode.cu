@@ -209,14 +209,14 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
     // ---- page numbers: lane i < SUBS looks up the page of 16 positions i of a tile ----
     bool bad = false;
     const int32_t* table = a.pg.tables + (size_t)g.s * a.pg.max_pages;
-    auto look_up = [&](int t) {                           // raw entry, -2: no row sees it
-      int id = -2;
+    auto seen = [&](int t) {
       const int key = k0 + KT * t + 16 * lane;
-      if (lane < S::SUBS && t < n && key <= g.hi && key + 15 >= g.lo) id = __ldg(table + (key >> sh));
-      return id;
+      return lane < S::SUBS && t < n && key <= g.hi && key + 15 >= g.lo;
     };
-    auto checked = [&](int id) {
-      if (id == -2) return -1;
+    auto look_up = [&](int t) { return seen(t) ? __ldg(table + ((k0 + KT * t + 16 * lane) >> sh)) : -1; };
+    // the page of a looked-up entry of tile t (which may hold any number), or -1
+    auto checked = [&](int t, int id) {
+      if (!seen(t)) return -1;
       if ((unsigned)id < (unsigned)a.pg.n_pages) return id;
       bad = true;
       return -1;
@@ -255,9 +255,9 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
       }
     };
     // pages of tile j + DEP (V comes next) and j + DEP + 1 (K)
-    int pid_v = checked(look_up(0)), pid_k, raw;
+    int pid_v = checked(0, look_up(0)), pid_k, raw;
     if (DEP == 2) {
-      pid_k = checked(look_up(1));
+      pid_k = checked(1, look_up(1));
       raw = look_up(2);
       issue_k(0, pid_v);
       cp_commit();
@@ -265,14 +265,14 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
       if (n > 1) issue_k(1, pid_k);
       cp_commit();
       if (n > 1) issue_v(1, pid_k);
-      pid_v = checked(raw);
+      pid_v = checked(2, raw);
       raw = look_up(3);
     } else {
       raw = look_up(1);
       issue_k(0, pid_v);
       cp_commit();
       issue_v(0, pid_v);
-      pid_v = checked(raw);
+      pid_v = checked(1, raw);
       raw = look_up(2);
     }
     pid_k = pid_v;
@@ -434,7 +434,7 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
     for (int j = 0; j < n; ++j) {
       // (pid_k served K of tile j + DEP: the same pages hold its V)
       pid_v = pid_k;
-      pid_k = checked(raw);
+      pid_k = checked(j + DEP + 1, raw);
       raw = look_up(j + DEP + 2);
       if constexpr (WD > 1) {
 #pragma unroll

@@ -377,13 +377,17 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       const uint32_t v_at = S::VD < 64 ? rv * 64 + ((2 * cv ^ ((rv >> 1) & 3)) << 4) : s_lane;
       const uint8_t* k_lane = a.pg.k_codes + ((size_t)h << sh) * D + r0 * D + 16 * c0 + half * S::KD;
       const uint8_t* v_lane = a.pg.v_codes + ((size_t)h << sh) * D + rv * D + 16 * cv + d_base + cta * S::VD;
-      auto look_up = [&](int t, int run) {                // raw table entry, -2: no row sees the keys
+      auto seen = [&](int t, int run) {
         const int key = k0 + KT * t + 16 * run;
-        return t < n && key <= g.hi && key + 15 >= g.lo ? __ldg(table + (key >> sh)) : -2;
+        return t < n && key <= g.hi && key + 15 >= g.lo;
+      };
+      auto look_up = [&](int t, int run) {
+        return seen(t, run) ? __ldg(table + ((k0 + KT * t + 16 * run) >> sh)) : -1;
       };
       bool bad = false;
-      auto checked = [&](int id) {
-        if (id == -2) return -1;
+      // the page of a looked-up entry of tile t (which may hold any number), or -1
+      auto checked = [&](int t, int run, int id) {
+        if (!seen(t, run)) return -1;
         if ((unsigned)id < (unsigned)a.pg.n_pages) return id;
         bad = true;
         return -1;
@@ -457,12 +461,12 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       // page numbers of tiles: id0 of i (V), id1 of i + 1 (K comes next), raw ahead
       int id0[VU], id1[VU], raw[VU];
       auto idk_of = [&](const int (&id)[VU], int t) {     // the K run's
-        return VU == 2 ? (run_k < 4 ? id[0] : id[VU - 1]) : checked(look_up(t, run_k));
+        return VU == 2 ? (run_k < 4 ? id[0] : id[VU - 1]) : checked(t, run_k, look_up(t, run_k));
       };
 #pragma unroll
       for (int e = 0; e < VU; ++e) {
-        id0[e] = checked(look_up(0, cw + 4 * e));
-        id1[e] = checked(look_up(1, cw + 4 * e));
+        id0[e] = checked(0, cw + 4 * e, look_up(0, cw + 4 * e));
+        id1[e] = checked(1, cw + 4 * e, look_up(1, cw + 4 * e));
         raw[e] = look_up(2, cw + 4 * e);
       }
       load_k(0, id0, idk_of(id0, 0));
@@ -475,7 +479,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
         int id2[VU];
 #pragma unroll
         for (int e = 0; e < VU; ++e) {
-          id2[e] = checked(raw[e]);
+          id2[e] = checked(i + 2, cw + 4 * e, raw[e]);
           raw[e] = look_up(i + 3, cw + 4 * e);
         }
         if (i + 1 < n) put_k(i + 1);
