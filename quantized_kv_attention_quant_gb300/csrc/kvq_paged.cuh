@@ -19,6 +19,13 @@ namespace {
 // log2 and the reciprocal of every other scale.
 constexpr float kSmallestScale = 9.094947017729282e-13f;   // 2^-40
 
+// A V scale of 0 counts as this in a read's reference and sum: 2^20 below the
+// smallest scale, so that a page of zeros sets the reference only where its keys
+// weigh 2^20 times the others' (counted as 1, it pushed the others' probabilities
+// below f16's range); and not so small that a weight of 2^-30 beside values of
+// scale 2^40 leaves fp32's range before it is summed (2^(-30 - 60 - 40)).
+constexpr float kZeroScale = 8.673617379884035e-19f;       // 2^-60
+
 // The largest i in [0, n) with key(i) <= x, for non-decreasing keys with key(0)
 // <= x, by a whole warp: 32 keys at a time, so that up to 1024 take two loads one
 // after the other in the place of ten.

@@ -17,8 +17,9 @@
 //   O += p_j cv_j,   l += p_j / sv      out = O / l
 // The value scale goes into the probability, not the codes, so both products
 // take codes as exact f16 values, and ref follows the largest t_j, so p_j <=
-// 2^15 whatever the scales are (renewed when a tile exceeds it by 2^8).  A
-// scale of 0 (all codes 0) counts as 1.
+// 2^15 whatever the scales are (renewed when a tile exceeds it by 2^8).  A value
+// scale of 0 (rows of zeros, whatever the codes) counts as kZeroScale in t and l,
+// and its p enters the product as 0.
 //
 // A CTA is four warps; with D >= 256, WD = D / 128 of them form a team that
 // shares the output: each keeps 128 dims of O (64 registers) for the keys of
@@ -337,6 +338,7 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
     float ref0 = -INFINITY, ref1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float sc[SW][2][4];                                   // raw scores of the tile to come: subtile, 8 keys, MMA element
     float sk[SW], lsv[SW], isv[SW];
+    uint32_t pm[SW];                                      // 0: values of scale 0
 
     // scores of tile j, its boxes refilled, its scales; the maxima of the thread's rows over the warp's keys
     auto scores = [&](int j, float& m0, float& m1) {
@@ -380,9 +382,10 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
           }
         }
         const float2 s2 = *reinterpret_cast<const float2*>(scale + ((tt & 3) * SW + e) * 2);
-        // (a scale of 0 stands for codes of 0; the smallest float keeps a masked -inf what it is)
+        // (a K scale of 0: scores of 0, by a factor that keeps a masked -inf what it is)
         sk[e] = fmaxf(s2.x * L2E, 1e-30f);
-        const float sv = s2.y > 0.f ? s2.y : 1.f;
+        const float sv = s2.y > 0.f ? s2.y : kZeroScale;
+        pm[e] = s2.y > 0.f ? 0xFFFFFFFFu : 0u;
         lsv[e] = __log2f(sv);
         isv[e] = __fdividef(1.f, sv);
         const int key0 = k0 + KT * j + 16 * (SW * warp + e);
@@ -472,8 +475,8 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
           const float p2 = ex2(fmaf(sc[e][f][2], sk[e], c1)), p3 = ex2(fmaf(sc[e][f][3], sk[e], c1));
           s0 += p0 + p1;
           s1 += p2 + p3;
-          pf[e][2 * f] = pack_h2(p0, p1);
-          pf[e][2 * f + 1] = pack_h2(p2, p3);
+          pf[e][2 * f] = pack_h2(p0, p1) & pm[e];
+          pf[e][2 * f + 1] = pack_h2(p2, p3) & pm[e];
         }
         l0 = fmaf(s0, isv[e], l0);
         l1 = fmaf(s1, isv[e], l1);

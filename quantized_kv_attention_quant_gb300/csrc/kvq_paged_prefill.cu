@@ -7,8 +7,8 @@
 // Mathematics as in kvq_paged_decode.cu: products of f16 q and codes are exact,
 // the value scale goes into the probability,
 //   t_j = (q . ck_j) sk log2 e + log2 sv,  p_j = 2^(t_j - ref) as f16,
-//   O += p_j cv_j,  l += p_j / sv,  out = O / l,
-// so codes enter both products as the exact f16 values they stand for.  An MMA
+//   O += p_j cv_j,  l += p_j / sv,  out = O / l
+// (sv = 0: kZeroScale in t and l, the codes as zeros), so codes enter both products as the exact f16 values they stand for.  An MMA
 // of the pair reads half of its B operand from each CTA's shared memory: CTA c
 // converts the keys KT / 2 c .. of K and the output dims DO / 2 c .. of V, so the
 // codes are converted once for twice the rows (a CTA for itself spent as long
@@ -448,9 +448,9 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
         if (lane == 0) {
 #pragma unroll
           for (int e = 0; e < VU; ++e) {
-            const float one = sv[e] > 0.f ? sv[e] : 1.f;
+            const float s = sv[e] > 0.f ? sv[e] : kZeroScale;
             *reinterpret_cast<float4*>(sm + S::SC_OFF + ((t & 3) * SUB + cw + 4 * e) * 16) =
-                make_float4(fmaxf(sk[e] * L2E, 1e-30f), __log2f(one), __fdividef(1.f, one), 0.f);
+                make_float4(fmaxf(sk[e] * L2E, 1e-30f), __log2f(s), __fdividef(1.f, s), 0.f);
           }
           mbar_arrive(sc_full + (t & 3));
         }
@@ -458,7 +458,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
         put(kb, at + s_lane, at + (s_lane ^ 16u), S::KD / 64, S::K_BLK);
         full(k_full + st);
       };
-      // page numbers of tiles: id0 of i (V), id1 of i + 1 (K comes next), raw ahead
+      // page numbers of tiles: id0 of the first, id1 of i + 1 (its V comes next), raw ahead
       int id0[VU], id1[VU], raw[VU];
       auto idk_of = [&](const int (&id)[VU], int t) {     // the K run's
         return VU == 2 ? (run_k < 4 ? id[0] : id[VU - 1]) : checked(t, run_k, look_up(t, run_k));
@@ -472,6 +472,12 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
       load_k(0, id0, idk_of(id0, 0));
       load_v(0, id0);
       meet();
+      // (values of scale 0 are stored as zeros: here, and below by not reading them)
+#pragma unroll
+      for (int e = 0; e < VU; ++e)
+        if (!(sv[e] > 0.f))
+#pragma unroll
+          for (int j = 0; j < VJ; ++j) vb[e][j] = make_uint4(0u, 0u, 0u, 0u);
       put_k(0);
       load_k(1, id1, idk_of(id1, 1));
       for (int i = 0; i < n; ++i) {
@@ -483,6 +489,9 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
           raw[e] = look_up(i + 3, cw + 4 * e);
         }
         if (i + 1 < n) put_k(i + 1);
+#pragma unroll
+        for (int e = 0; e < VU; ++e)
+          if (!(sv[e] > 0.f)) id1[e] = -1;
         load_k(i + 2, id2, idk_of(id2, i + 2));
         wait(v_empty + st, ((i / KST) & 1) ^ 1);
 #pragma unroll
@@ -494,10 +503,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
         full(v_full + st);
         load_v(i + 1, id1);
 #pragma unroll
-        for (int e = 0; e < VU; ++e) {
-          id0[e] = id1[e];
-          id1[e] = id2[e];
-        }
+        for (int e = 0; e < VU; ++e) id1[e] = id2[e];
       }
     }
   } else {

@@ -28,3 +28,38 @@ def test_no_number_outside_the_pool_is_a_page(m, D, kind, rows, entry):
     got = r.run()
     assert r.status() == m.KVQ_STATUS_SEQ_SKIPPED
     assert np.isnan(got[:rows]).all() and np.array_equal(got[rows:], want[rows:])
+
+
+@pytest.mark.parametrize("sharp", [2.0, 6.0])
+@pytest.mark.parametrize("rows", [1, 4, 150])
+@pytest.mark.parametrize("D,kind", [(64, "i8"), (128, "e4m3"), (256, "i8"), (512, "e4m3")])
+def test_zero_scales_beside_the_smallest(m, D, kind, rows, sharp):
+    """Value scales 0, 2^-40 and 2^-33: a page of zeros takes its weight and leaves the others' values their bits."""
+    layer = spec(16, 4, D, rope_dims=0)
+    gpu, tables, g = filled(m, layer, 16, kind, [300], 78)
+    for i, page in enumerate(tables[0]):
+        gpu.p.scales["v"][page] = [0.0, 2.0 ** -40, 2.0 ** -33][i % 3]
+    gpu = Gpu(m, gpu.p)                                        # (the codes of the zero pages stay: their rows read as zeros)
+    q, w = ask(g, layer, rows, sharp)
+    r = Read(m, layer, gpu, tables, [300 - rows], [rows], q, w, True, offsets([rows]) if rows > 1 else None)
+    got = r.run()
+    assert r.status() == 0
+    check(layer, gpu, tables, q, w, got, [(t, 0, 300 - rows + t) for t in range(0, rows, 7)], True)
+
+
+@pytest.mark.parametrize("rows", [1, 60])
+@pytest.mark.parametrize("D,kind", [(64, "i8"), (128, "e4m3"), (256, "i8"), (512, "e4m3")])
+def test_scales_of_zero_read_as_zeros(m, D, kind, rows):
+    """Whatever the codes: keys of scale 0 score 0, values of scale 0 add nothing, and with nothing else the output is 0."""
+    layer = spec(4, 1, D, rope_dims=0)
+    gpu, tables, g = filled(m, layer, 16, kind, [200, 90], 79)
+    gpu.p.scales["k"][tables[0][::2]] = 0.0
+    gpu.p.scales["v"][tables[0][1::3]] = 0.0
+    gpu.p.scales["v"][tables[1][:6]] = 0.0
+    gpu = Gpu(m, gpu.p)
+    q, w = ask(g, layer, 2 * rows, 2.0)
+    r = Read(m, layer, gpu, tables, [200 - rows, 90 - rows], [rows] * 2, q, w, True,
+             offsets([rows] * 2) if rows > 1 else None)
+    got = r.run()
+    assert r.status() == 0 and not got[rows:].any()
+    check(layer, gpu, tables, q, w, got, [(t, 0, 200 - rows + t) for t in range(0, rows, 7)], True)
