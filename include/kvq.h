@@ -643,8 +643,9 @@ kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t* tables,
  *               2^-24
  *   workspace   at least attn_paged_decode_workspace_bytes(...) bytes; its first
  *               4 bytes receive the status word
- * A row whose position is above max_pos or past the table, or one of whose
- * pages the table does not name, is NaN and sets KVQ_STATUS_SEQ_SKIPPED.
+ * A row whose position is above max_pos or past the table, or that sees a
+ * position whose page the table does not name, is NaN and sets
+ * KVQ_STATUS_SEQ_SKIPPED; the other rows of the call are as they are without it.
  */
 kvq_status attn_paged_decode(const kvq_layer* layer, const kvq_paged_cache* cache, const int32_t* tables,
                              int32_t max_pages, int32_t n_seqs, const int32_t* pos, int32_t max_pos,

@@ -61,6 +61,8 @@ __device__ __forceinline__ SeqRows paged_seq_rows(const PagedRows& r, int s) {
   return {s, o, __ldg(r.row_offsets + s + 1) - o, __ldg(r.start + s)};
 }
 
+constexpr int kNoPage = -2;          // of a read, in the place of a page: rows see the keys, but the table names no page
+
 // The page of position p of sequence s, or -1 when the table names none.
 __device__ __forceinline__ int paged_page(const PagedArgs& pg, int s, int p) {
   const int id = __ldg(pg.tables + (size_t)s * pg.max_pages + (p >> pg.p_shift));

@@ -18,8 +18,9 @@
 // The value scale goes into the probability, not the codes, so both products
 // take codes as exact f16 values, and ref follows the largest t_j, so p_j <=
 // 2^15 whatever the scales are (renewed when a tile exceeds it by 2^8).  A value
-// scale of 0 (rows of zeros, whatever the codes) counts as kZeroScale in t and l,
-// and its p enters the product as 0.
+// scale of 0 (rows of zeros, whatever numbers the codes are) counts as kZeroScale
+// in t and l, and its p enters the product as 0.  Keys whose page is not named have
+// a K scale of NaN: so have the scores of the rows that see them, and those rows alone.
 //
 // A CTA is four warps; with D >= 256, WD = D / 128 of them form a team that
 // shares the output: each keeps 128 dims of O (64 registers) for the keys of
@@ -215,18 +216,19 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
       return lane < S::SUBS && t < n && key <= g.hi && key + 15 >= g.lo;
     };
     auto look_up = [&](int t) { return seen(t) ? __ldg(table + ((k0 + KT * t + 16 * lane) >> sh)) : -1; };
-    // the page of a looked-up entry of tile t (which may hold any number), or -1
+    // the page of a looked-up entry of tile t (which may hold any number), -1 where no row sees it, kNoPage where the
+    // entry names none
     auto checked = [&](int t, int id) {
       if (!seen(t)) return -1;
       if ((unsigned)id < (unsigned)a.pg.n_pages) return id;
       bad = true;
-      return -1;
+      return kNoPage;
     };
-    // copies of a box: 16 positions from key0, bytes x .. of their rows, of page id (page 0 where there is
-    // none: what no row sees is masked)
+    // copies of a box: 16 positions from key0, bytes x .. of their rows, of page id (zeros, from outside the pages,
+    // where there is none)
     auto copy = [&](int box, const CUtensorMap* map, int id, int key0, int xb) {
       mbar_arrive_expect_tx(full + box, S::BOX);
-      tc::tma_load_3d(smem_u32(ring + box * S::BOX), map, xb, key0 & (P - 1), max(id, 0) * n_kv + h,
+      tc::tma_load_3d(smem_u32(ring + box * S::BOX), map, xb, key0 & (P - 1), id < 0 ? -1 : id * n_kv + h,
                       smem_u32(full + box));
     };
     auto issue_k = [&](int t, int pid) {                  // K and the scales of tile t
@@ -242,9 +244,12 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
           for (int b = 0; b < S::KBX; ++b) copy(slot * NB + e * S::KBX + b, &tmk, ids[e], key0 + 16 * e, 128 * b);
       }
       if (lane < 2 * SW) {
+        // (keys without a page: a K scale of NaN)
         const int id = SW == 2 && lane >= 2 ? ids[SW - 1] : ids[0];
-        cp4(smem_u32(scale + ((used + t) & 3) * SW * 2 + lane),
-            (lane & 1 ? a.pg.v_scales : a.pg.k_scales) + (size_t)max(id, 0) * n_kv + h, id >= 0 ? 4u : 0u);
+        float* at = scale + ((used + t) & 3) * SW * 2 + lane;
+        if (id == kNoPage) *at = lane & 1 ? 0.f : __int_as_float(0x7FC00000);
+        else cp4(smem_u32(at), (lane & 1 ? a.pg.v_scales : a.pg.k_scales) + (size_t)max(id, 0) * n_kv + h,
+                 id >= 0 ? 4u : 0u);
       }
     };
     auto issue_v = [&](int t, int pid) {                  // V of tile t: the team's keys, the warp's dims
@@ -338,7 +343,6 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
     float ref0 = -INFINITY, ref1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float sc[SW][2][4];                                   // raw scores of the tile to come: subtile, 8 keys, MMA element
     float sk[SW], lsv[SW], isv[SW];
-    uint32_t pm[SW];                                      // 0: values of scale 0
 
     // scores of tile j, its boxes refilled, its scales; the maxima of the thread's rows over the warp's keys
     auto scores = [&](int j, float& m0, float& m1) {
@@ -385,7 +389,6 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
         // (a K scale of 0: scores of 0, by a factor that keeps a masked -inf what it is)
         sk[e] = fmaxf(s2.x * L2E, 1e-30f);
         const float sv = s2.y > 0.f ? s2.y : kZeroScale;
-        pm[e] = s2.y > 0.f ? 0xFFFFFFFFu : 0u;
         lsv[e] = __log2f(sv);
         isv[e] = __fdividef(1.f, sv);
         const int key0 = k0 + KT * j + 16 * (SW * warp + e);
@@ -393,14 +396,16 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
         for (int f = 0; f < 2; ++f)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[e][f][i] = CH == 2 ? acc[0][f][i] + acc[CH - 1][f][i] : acc[0][f][i];
-        if (key0 < lo_last || key0 + 15 > g.p0) {         // a row does not see all 16 keys
+        // a row does not see all 16 keys, or they have no page (NaN for the rows that see one)
+        if (key0 < lo_last || key0 + 15 > g.p0 || s2.x != s2.x) {
+          const float add = s2.x - s2.x;
 #pragma unroll
           for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int key = key0 + 8 * f + (i & 1 ? kc1 : kc0);
               const bool see = (i >> 1) ? key <= pr1 && key >= lo1 : key <= pr0 && key >= lo0;
-              sc[e][f][i] = see ? sc[e][f][i] : -INFINITY;
+              sc[e][f][i] = see ? sc[e][f][i] + add : -INFINITY;
             }
         }
         m0 = fmaxf(m0, fmaf(fmaxf(fmaxf(sc[e][0][0], sc[e][0][1]), fmaxf(sc[e][1][0], sc[e][1][1])), sk[e], lsv[e]));
@@ -475,11 +480,15 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
           const float p2 = ex2(fmaf(sc[e][f][2], sk[e], c1)), p3 = ex2(fmaf(sc[e][f][3], sk[e], c1));
           s0 += p0 + p1;
           s1 += p2 + p3;
-          pf[e][2 * f] = pack_h2(p0, p1) & pm[e];
-          pf[e][2 * f + 1] = pack_h2(p2, p3) & pm[e];
+          pf[e][2 * f] = pack_h2(p0, p1);
+          pf[e][2 * f + 1] = pack_h2(p2, p3);
         }
         l0 = fmaf(s0, isv[e], l0);
         l1 = fmaf(s1, isv[e], l1);
+        if (lsv[e] < -50.f) {                             // values of scale 0 (the smallest other: -40)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pf[e][i] = 0u;
+        }
       }
       if constexpr (WD > 1)
         *reinterpret_cast<uint4*>(sm + S::P_OFF + ((j & 1) * 4 + warp) * 512 + lane * 16) =
@@ -596,7 +605,6 @@ paged_decode_kernel(const PagedReadArgs a, const __grid_constant__ CUtensorMap t
 #pragma unroll
         for (int w = 0; w < WD; ++w) l = fmaf(lb[(t * WD + w) * 16 + r], f, l);
       }
-      if (bad) l = __int_as_float(0x7FC00000);
       if (whole) {
         const float inv = 1.f / l;
         const size_t at = ((size_t)(g.row0 + r / G) * a.L.n_q + h * G + r % G) * D + d;

@@ -8,7 +8,9 @@
 // the value scale goes into the probability,
 //   t_j = (q . ck_j) sk log2 e + log2 sv,  p_j = 2^(t_j - ref) as f16,
 //   O += p_j cv_j,  l += p_j / sv,  out = O / l
-// (sv = 0: kZeroScale in t and l, the codes as zeros), so codes enter both products as the exact f16 values they stand for.  An MMA
+// (sv = 0: kZeroScale in t and l, the codes as zeros; keys whose page is not
+// named: scores of 0 at sk = infinity, NaN for the rows that see them and -inf for
+// the others), so codes enter both products as the exact f16 values they stand for.  An MMA
 // of the pair reads half of its B operand from each CTA's shared memory: CTA c
 // converts the keys KT / 2 c .. of K and the output dims DO / 2 c .. of V, so the
 // codes are converted once for twice the rows (a CTA for itself spent as long
@@ -225,7 +227,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   uint64_t* o_full = bars + 16;                           // [2] a row tile's last product
   uint64_t* sc_full = bars + 18;                          // [4] a tile's scales (the CTA's converter warps)
   uint64_t* p_half = bars + 22;                           // [2] as p_full, MT == 2: the first half of the keys
-  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 24);   // tensor memory, bad page
+  volatile uint32_t* ctl = reinterpret_cast<volatile uint32_t*>(bars + 24);   // tensor memory
   const uint32_t sb = smem_u32(sm);
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) {
@@ -242,7 +244,6 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     }
     for (int i = 0; i < 4; ++i) mbar_init(sc_full + i, 4);
     fence_mbar_init();
-    ctl[1] = 0;
   }
   if (warp == 0) {
     tc::tmem_alloc2(const_cast<uint32_t*>(ctl), 512);
@@ -385,12 +386,13 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
         return seen(t, run) ? __ldg(table + ((k0 + KT * t + 16 * run) >> sh)) : -1;
       };
       bool bad = false;
-      // the page of a looked-up entry of tile t (which may hold any number), or -1
+      // the page of a looked-up entry of tile t (which may hold any number), -1 where no row sees the keys, kNoPage
+      // where the entry names none
       auto checked = [&](int t, int run, int id) {
         if (!seen(t, run)) return -1;
         if ((unsigned)id < (unsigned)a.pg.n_pages) return id;
         bad = true;
-        return -1;
+        return kNoPage;
       };
       // J loads of run `run` of tile t, rows r + 8 (j / nb)
       auto load = [&](auto& v, const uint8_t* codes, int nb, int r, int t, int run, int id) {
@@ -434,7 +436,8 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
         load(kb, k_lane, S::KD / 64, r0, t, run_k, idk);
 #pragma unroll
         for (int e = 0; e < VU; ++e) {
-          sk[e] = id[e] >= 0 ? __ldg(a.pg.k_scales + (size_t)id[e] * n_kv + h) : 0.f;
+          sk[e] = id[e] == kNoPage ? INFINITY : 0.f;
+          if (id[e] >= 0) sk[e] = __ldg(a.pg.k_scales + (size_t)id[e] * n_kv + h);
           sv[e] = id[e] >= 0 ? __ldg(a.pg.v_scales + (size_t)id[e] * n_kv + h) : 0.f;
         }
       };
@@ -499,12 +502,12 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
           const uint32_t at = S::V_OFF + st * S::V_BYTES + (cw + 4 * e) * 16 * S::V_ROW;
           put(vb[e], at + v_at, at + (v_at ^ 16u), S::VD < 64 ? 1 : S::VD / 64, S::V_BLK);
         }
-        if (bad) ctl[1] = 1;
         full(v_full + st);
         load_v(i + 1, id1);
 #pragma unroll
         for (int e = 0; e < VU; ++e) id1[e] = id2[e];
       }
+      if (bad && lane == 0) flag_error(status, KVQ_DEV_BADSEQ);
     }
   } else {
     // ================= softmax =================
@@ -648,10 +651,6 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     wait(o_full + m, 0);
     tc::fence_after_sync();
     __syncwarp();
-    if (ctl[1]) {
-      l = __int_as_float(0x7FC00000);
-      if (tid == 0) flag_error(status, KVQ_DEV_BADSEQ);
-    }
     const float inv = 1.f / l;
     constexpr int OC = MT == 2 ? DO : DO / 2;
     const int o0 = MT == 2 ? 0 : OC * wg;

@@ -63,3 +63,44 @@ def test_scales_of_zero_read_as_zeros(m, D, kind, rows):
     got = r.run()
     assert r.status() == 0 and not got[rows:].any()
     check(layer, gpu, tables, q, w, got, [(t, 0, 200 - rows + t) for t in range(0, rows, 7)], True)
+
+
+# n_q, n_kv, D, window, first position, rows, places of the table that name no page (of 16 positions), codes
+MISSING = [(8, 2, 128, 0, 200, 40, [14], "i8"), (8, 2, 128, 20, 200, 40, [12], "e4m3"), (8, 2, 128, 8, 200, 64, [12, 15], "i8"),
+           (4, 1, 64, 0, 0, 300, [9, 11], "e4m3"), (4, 4, 64, 33, 100, 200, [6, 13], "i8"),
+           (8, 2, 256, 0, 100, 120, [12], "i8"), (8, 2, 256, 50, 90, 150, [5, 13], "e4m3"),
+           (16, 1, 512, 0, 60, 70, [7], "i8"), (16, 1, 512, 30, 60, 70, [4], "e4m3"),
+           (8, 2, 128, 0, 5000, 100, [316], "i8"), (8, 2, 256, 0, 4990, 100, [317], "e4m3"), (4, 4, 128, 0, 0, 400, [20], "i8"),
+           # windows of few rows, and ratios that take 16 rows at a time
+           (8, 2, 128, 0, 220, 6, [14], "i8"), (4, 1, 64, 9, 230, 8, [13], "e4m3"), (8, 2, 256, 10, 230, 8, [13], "i8"),
+           (16, 1, 512, 0, 223, 2, [14], "i8"), (6, 2, 128, 0, 200, 40, [14], "e4m3"), (6, 2, 256, 20, 200, 40, [12], "i8"),
+           (8, 2, 128, 0, 4990, 8, [312], "e4m3")]
+
+
+@pytest.mark.parametrize("n_q,n_kv,D,window,start,rows,places,kind", MISSING)
+def test_only_rows_that_see_a_missing_page(m, n_q, n_kv, D, window, start, rows, places, kind):
+    """A chunk or window with pages missing among its keys: the rows before them (or, under a window, past them) are as
+    with all pages, bit for bit."""
+    layer = spec(n_q, n_kv, D, window)
+    gpu, tables, g = filled(m, layer, 16, kind, [start + rows], D + rows, fill=0x7F)
+    p, spare = gpu.p, min(set(range(gpu.p.n_pages)) - set(tables[0]))
+    for x in (p.codes["k"], p.codes["v"], p.scales["k"], p.scales["v"]):
+        x[[0, spare]] = x[[spare, 0]]                          # (page 0 holds bytes that read as NaN)
+    tables[tables == 0] = spare
+    gpu = Gpu(m, p)
+    q, w = ask(g, layer, rows, 3.0)
+    off = offsets([rows])
+    want = Read(m, layer, gpu, tables, [start], [rows], q, w, True, off).run()
+    bad = tables.copy()
+    bad[0, places] = [-1, gpu.p.n_pages][:len(places)]
+    r = Read(m, layer, gpu, bad, [start], [rows], q, w, True, off)
+    got = r.run()
+    pos = start + np.arange(rows)
+    first = np.maximum(0, pos - window + 1) if window else np.zeros_like(pos)
+    sees = np.zeros(rows, bool)
+    for i in places:
+        sees |= (first <= 16 * i + 15) & (pos >= 16 * i)
+    assert sees.any() and not sees.all() and r.status() == m.KVQ_STATUS_SEQ_SKIPPED
+    assert np.isnan(got[sees]).all()
+    assert np.array_equal(got[~sees], want[~sees])
+    check(layer, gpu, tables, q, w, got, [(int(t), 0, int(pos[t])) for t in np.flatnonzero(~sees)[::9]], True)
