@@ -661,6 +661,9 @@ size_t attn_paged_decode_workspace_bytes(const kvq_layer* layer, const kvq_paged
  * the rows' keys and values.  Arguments as for attn_prefill_chunk and
  * attn_paged_decode; max_pos bounds the position of every row.  A sequence
  * with a negative start_pos is idle: its rows are zeros.
+ * A workspace that attn_paged_prefill_workspace_bytes asks for serves every call
+ * of no larger n_seqs, n_rows, max_rows_per_seq and max_pos (the last chunk of a
+ * prompt in the workspace of the others).
  */
 kvq_status attn_paged_prefill(const kvq_layer* layer, const kvq_paged_cache* cache, const int32_t* tables,
                               int32_t max_pages, int32_t n_seqs, const int32_t* row_offsets, const int32_t* start_pos,

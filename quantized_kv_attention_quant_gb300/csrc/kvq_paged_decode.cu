@@ -784,7 +784,7 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   long long* prefix = reinterpret_cast<long long*>(b + w.prefix);
   float* part_o = reinterpret_cast<float*>(b + w.part_o);
   float* part_ml = reinterpret_cast<float*>(b + w.part_ml);
-  cudaError_t e = launch_paged_prep<D>(a, f, p.TG, S::KT, p.n_groups, q16, prefix, nullptr, status, num_sms, st);
+  cudaError_t e = launch_paged_prep<D>(a, f, p.TG, S::KT, p.n_groups, q16, prefix, PagedOrder{}, status, num_sms, st);
   if (e != cudaSuccess) return e;
   CUtensorMap tmk, tmv;
   if (!pages_map(&tmk, a.pg.k_codes, D, a.pg.P, (long long)a.pg.n_pages * a.L.n_kv) ||

@@ -184,14 +184,13 @@ __device__ __forceinline__ void pf_st16(uint32_t taddr, const uint32_t (&v)[16])
                : "memory");
 }
 
-// The pieces that a unit of n key tiles is cut into, and piece z's tiles.
-__device__ __forceinline__ int pf_pieces(int n, int splits) { return min(n, splits); }
+// The first tile of piece z of a unit of n key tiles.
 __device__ __forceinline__ int pf_tile0(int n, int pieces, int z) { return (int)((long long)n * z / pieces); }
 
 template <int D, bool E4M3>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pf<D>::THREADS, 1)
-paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, const int2* order, const uint16_t* q16,
-                     float* part_o, float* part_ml, uint32_t* status) {
+paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int4* order, const uint16_t* q16, float* part_o,
+                     float* part_ml, uint32_t* status) {
   using S = Pf<D>;
   constexpr int MT = S::MT, DO = S::DO, KT = S::KT, SUB = S::SUB, KST = S::KST;
   constexpr float L2E = 1.4426950408889634f;
@@ -205,12 +204,12 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
   const int per = n_kv * S::NSPLIT, z = blockIdx.y;
   const int cta = (int)tc::cta_rank();                    // of the pair
   const int rank = (blockIdx.x >> 1) / per, hx = (blockIdx.x >> 1) - rank * per;
-  const int2 us = __ldg(order + rank);
+  const int4 us = __ldg(order + rank);
   const int u = us.x, h = hx / S::NSPLIT, d_base = (hx % S::NSPLIT) * DO;
   const PagedGroup g = paged_group_of(a.r, a.pg, W, TQ, KT, u, us.y);
   if (g.tiles == 0) return;
   const int n_all = g.tiles;
-  const int pieces = pf_pieces(n_all, splits);
+  const int pieces = us.w;
   if (z >= pieces) return;
   const int t_a = pf_tile0(n_all, pieces, z), n = pf_tile0(n_all, pieces, z + 1) - t_a;
   const int k0 = g.kt0 + KT * t_a;
@@ -654,8 +653,7 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
     const float inv = 1.f / l;
     constexpr int OC = MT == 2 ? DO : DO / 2;
     const int o0 = MT == 2 ? 0 : OC * wg;
-    const size_t unit = (size_t)u * per + hx;
-    const size_t prow = (unit * splits + z) * S::ROWS + rg;
+    const size_t prow = ((size_t)__ldg(order + rank).z * per + hx * pieces + z) * S::ROWS + rg;
     const size_t at = ((size_t)(g.row0 + rg / G) * a.L.n_q + h * G + rg % G) * D + d_base + o0;
     const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
 #pragma unroll 1
@@ -717,21 +715,21 @@ paged_prefill_kernel(const PagedReadArgs a, const int TQ, const int splits, cons
 // over its pieces, in order.
 template <int D>
 __global__ void __launch_bounds__(256)
-paged_join_kernel(const PagedReadArgs a, const int TQ, const int splits, const float* part_o, const float* part_ml) {
+paged_join_kernel(const PagedReadArgs a, const int TQ, const int4* order, const float* part_o, const float* part_ml) {
   using S = Pf<D>;
   constexpr int DO = S::DO, ROWS = S::ROWS;
   pdl_launch();
   pdl_wait();
   const int per = a.L.n_kv * S::NSPLIT, G = a.L.G;
-  const int u = blockIdx.x / per, hx = blockIdx.x - u * per;
-  const PagedGroup g = paged_group<true>(a.r, a.pg, a.L.window, TQ, S::KT, u);
-  if (g.tiles == 0) return;
-  const int pieces = pf_pieces(g.tiles, splits);
-  if (pieces == 1) return;
+  const int rank = blockIdx.x / per, hx = blockIdx.x - rank * per;
+  const int4 us = __ldg(order + rank);
+  const int pieces = us.w;
+  if (pieces < 2) return;
+  const PagedGroup g = paged_group_of(a.r, a.pg, a.L.window, TQ, S::KT, us.x, us.y);
   const int i = blockIdx.y * 256 + threadIdx.x;
   const int r = i / (DO / 4), d = (i - r * (DO / 4)) * 4;
   if (r >= g.nt * G) return;
-  const size_t row0 = ((size_t)blockIdx.x * splits) * ROWS + r;
+  const size_t row0 = ((size_t)us.z * per + hx * pieces) * ROWS + r;
   float M = -INFINITY;
   for (int z = 0; z < pieces; ++z) M = fmaxf(M, __ldg(part_ml + (row0 + (size_t)z * ROWS) * 2));
   float l = 0.f;
@@ -774,7 +772,9 @@ cudaError_t check_registers() {
   return regs.load(std::memory_order_relaxed) == 128 ? cudaSuccess : cudaErrorLaunchOutOfResources;
 }
 
-struct PfPlan { int TQ, n_groups, splits; long long units; };
+// most: pieces of a unit; places: for the pieces of units that are cut (of this
+// call or any of fewer rows, which may cut more)
+struct PfPlan { int TQ, n_groups, most; long long units, places; };
 template <int D>
 PfPlan pf_plan(const LayerArgs& L, int n_seqs, int n_rows, int max_pos, int num_sms) {
   using S = Pf<D>;
@@ -783,13 +783,16 @@ PfPlan pf_plan(const LayerArgs& L, int n_seqs, int n_rows, int max_pos, int num_
   static const int32_t some = 0;
   p.n_groups = paged_groups(PagedRows{&some, nullptr, n_seqs, n_rows}, p.TQ);
   p.units = (long long)p.n_groups * L.n_kv * S::NSPLIT;
-  // as many pieces as fill the GPU once (one pair per two SMs), of at least two tiles
+  // as many pieces as fill the GPU once (one pair per two SMs), of at least two tiles; units of ragged
+  // batches that are more than the rows need get places for pieces that fill it twice
   long long keys = (long long)max_pos + 1;
   if (L.window > 0) keys = std::min<long long>(keys, (long long)L.window + p.TQ);
   const long long tiles = (keys + S::KT - 1) / S::KT;
   // (groups are counted with room for one short one per sequence)
   const long long real = std::max(1ll, ((long long)n_rows / p.TQ + (n_rows % p.TQ != 0)) * L.n_kv * S::NSPLIT);
-  p.splits = (int)std::max(1ll, std::min<long long>({num_sms / 2 / real, tiles / 2, 64ll}));
+  const long long cut = std::max(1ll, std::min<long long>(tiles / 2, kMostPieces));
+  p.most = (int)std::max(1ll, std::min<long long>(num_sms / 2 / real, cut));
+  p.places = cut > 1 ? std::min<long long>(num_sms / 2 * 2, p.units * cut) : 0;
   return p;
 }
 
@@ -799,11 +802,11 @@ template <int D>
 PfWs pf_ws(const LayerArgs& L, int n_rows, const PfPlan& p) {
   using S = Pf<D>;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t prows = p.splits > 1 ? (size_t)p.units * p.splits * S::ROWS : 0;
+  const size_t prows = (size_t)p.places * S::ROWS;
   PfWs w;
   w.q16 = 256;
   w.order = up(w.q16 + (size_t)n_rows * L.n_q * D * 2);
-  w.part_o = up(w.order + (size_t)p.n_groups * 8);
+  w.part_o = up(w.order + (size_t)p.n_groups * 16);
   w.part_ml = up(w.part_o + prows * S::DO * 4);
   w.total = up(w.part_ml + prows * 8);
   return w;
@@ -818,23 +821,26 @@ cudaError_t launch_t(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
   uint8_t* b = static_cast<uint8_t*>(ws);
   uint32_t* status = reinterpret_cast<uint32_t*>(b);
   uint16_t* q16 = reinterpret_cast<uint16_t*>(b + w.q16);
-  int2* order = reinterpret_cast<int2*>(b + w.order);
+  int4* order = reinterpret_cast<int4*>(b + w.order);
   float* part_o = reinterpret_cast<float*>(b + w.part_o);
   float* part_ml = reinterpret_cast<float*>(b + w.part_ml);
   cudaError_t e = check_registers<D, E4M3>();
   if (e != cudaSuccess) return e;
-  e = launch_paged_prep<D>(a, f, p.TQ, S::KT, p.n_groups, q16, nullptr, order, status, num_sms, st);
+  const PagedOrder po = {order, a.L.n_kv * S::NSPLIT, p.most, (int)p.places};
+  e = launch_paged_prep<D>(a, f, p.TQ, S::KT, p.n_groups, q16, nullptr, po, status, num_sms, st);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> allowed{0};
   e = allow_smem(paged_prefill_kernel<D, E4M3>, S::BYTES, allowed);
   if (e != cudaSuccess) return e;
   if ((e = prof_before(st)) != cudaSuccess) return e;
-  e = launch_pdl(paged_prefill_kernel<D, E4M3>, dim3((unsigned)p.units * 2, p.splits), dim3(S::THREADS), S::BYTES, st, a,
-                 p.TQ, p.splits, order, q16, part_o, part_ml, status);
+  e = launch_pdl(paged_prefill_kernel<D, E4M3>, dim3((unsigned)p.units * 2, p.most), dim3(S::THREADS), S::BYTES, st, a,
+                 p.TQ, order, q16, part_o, part_ml, status);
   if (e != cudaSuccess) return e;
-  if ((e = prof_after(st)) != cudaSuccess || p.splits == 1) return e;
-  return launch_pdl(paged_join_kernel<D>, dim3((unsigned)p.units, S::ROWS * (S::DO / 4) / 256), dim3(256), 0, st, a,
-                    p.TQ, p.splits, part_o, part_ml);
+  if ((e = prof_after(st)) != cudaSuccess || p.most == 1) return e;
+  // (units that are cut are the first of the order, and have two places at least)
+  const long long cut = std::min(p.units, p.places / 2);
+  return launch_pdl(paged_join_kernel<D>, dim3((unsigned)cut, S::ROWS * (S::DO / 4) / 256), dim3(256), 0, st, a, p.TQ,
+                    order, part_o, part_ml);
 }
 
 template <int D>

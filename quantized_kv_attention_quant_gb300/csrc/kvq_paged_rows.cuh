@@ -122,14 +122,27 @@ __device__ __forceinline__ bool paged_plan(const PagedRows& r, const PagedArgs& 
   return __syncthreads_or(bad);
 }
 
-// order = the groups (and their sequences), those with the most key tiles first (one block): a
+// order[rank] = the groups, those with the most key tiles first (one block): a
 // counting sort over the tile counts; the order of equal ones is open (it
-// decides only which CTA takes a group).
+// decides only which CTA takes a group).  A group of t tiles is cut into min(t, s)
+// pieces along its keys, and those of more than one piece get places for their
+// results, one behind the other.  s is the largest number up to `most` whose pieces,
+// `per` places each, fit `places`: with ge(x) groups of at least x tiles, the groups
+// of more than one tile have ge(2) - ge(1) + sum of ge(1 .. s) pieces, and those before rank r, which
+// has m = min(t, s) itself, r m + sum of ge(m + 1 .. s).
+struct PagedOrder {
+  int4* order;     // group, sequence, first piece, pieces
+  int per, most, places;
+};
 constexpr int kOrderBins = 2048;
+constexpr int kMostPieces = 64;       // of a group
 __device__ __forceinline__ void paged_order_block(const PagedRows& r, const PagedArgs& pg, int window, int TG, int KT,
-                                                  int n_groups, int2* order, uint32_t* status) {
+                                                  int n_groups, const PagedOrder& o, uint32_t* status) {
   __shared__ int bins[kOrderBins];
   __shared__ int wsum[kPrWarps];
+  __shared__ int ge[kMostPieces + 1];
+  __shared__ long long upto[kMostPieces + 1];             // sum of ge(1 .. x)
+  __shared__ int s_sh;
   constexpr int PER = kOrderBins / (kPrWarps * 32);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int i = tid; i < kOrderBins; i += kPrWarps * 32) bins[i] = 0;
@@ -159,11 +172,37 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
   int before = inc - sum;
   for (int w = 0; w < warp; ++w) before += wsum[w];
 #pragma unroll
-  for (int k = 0; k < PER; ++k) bins[PER * tid + k] = before + mine[k];
+  for (int k = 0; k < PER; ++k) {
+    bins[PER * tid + k] = before + mine[k];
+    const int x = kOrderBins - (PER * tid + k);           // these have at least x tiles
+    if (x <= kMostPieces) ge[x] = before + mine[k];
+  }
   const bool any = __syncthreads_or(bad);
+  if (warp == 0) {
+    long long a = ge[lane + 1], b = ge[lane + 33];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, a, m), y = __shfl_up_sync(0xffffffffu, b, m);
+      if (lane >= m) {
+        a += x;
+        b += y;
+      }
+    }
+    b += __shfl_sync(0xffffffffu, a, 31);
+    upto[lane + 1] = a;
+    upto[lane + 33] = b;
+    const long long more = (long long)ge[2] - ge[1];
+    const bool fit_a = lane + 1 <= o.most && (lane == 0 || (a + more) * o.per <= o.places);
+    const bool fit_b = lane + 33 <= o.most && (b + more) * o.per <= o.places;
+    const int fit = __popc(__ballot_sync(0xffffffffu, fit_a)) + __popc(__ballot_sync(0xffffffffu, fit_b));
+    if (lane == 0) s_sh = max(1, fit);
+  }
+  __syncthreads();
+  const int s = s_sh;
   for (int u = tid; u < n_groups; u += kPrWarps * 32) {
     const PagedGroup g = paged_group<false>(r, pg, window, TG, KT, u);
-    order[atomicAdd(&bins[bin_of(g.tiles)], 1)] = make_int2(u, g.s);
+    const int rank = atomicAdd(&bins[bin_of(g.tiles)], 1), m = min(g.tiles, s);
+    o.order[rank] = make_int4(u, g.s, m > 1 ? (int)((long long)rank * m + upto[s] - upto[m]) : 0, m);
   }
   if (tid == 0) *status = any ? (1u << KVQ_DEV_BADSEQ) : 0u;
 }
@@ -179,7 +218,7 @@ __device__ __forceinline__ void paged_order_block(const PagedRows& r, const Page
 template <int D>
 __global__ void __launch_bounds__(kPrWarps * 32)
 paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, const int hpb, const int TG, const int KT,
-                  const int n_groups, uint16_t* q16, long long* prefix, int2* order, uint32_t* status) {
+                  const int n_groups, uint16_t* q16, long long* prefix, const PagedOrder order, uint32_t* status) {
   using PL = PrepLanes<D>;
   constexpr int E = PL::E;
   extern __shared__ __align__(16) uint8_t pr_buf[];
@@ -271,7 +310,8 @@ paged_prep_kernel(const PagedReadArgs a, const RopeFreqs freqs, const int rb, co
 
 template <int D>
 cudaError_t launch_paged_prep(const PagedReadArgs& a, const RopeFreqs& f, int TG, int KT, int n_groups, uint16_t* q16,
-                              long long* prefix, int2* order, uint32_t* status, int num_sms, cudaStream_t st) {
+                              long long* prefix, const PagedOrder& order, uint32_t* status, int num_sms,
+                              cudaStream_t st) {
   // few rows: a block takes what its warps prep at once (latency); many: all heads of
   // up to 16 rows, which share their angles (16 KB of them at most)
   const int n_q = a.L.n_q, half = a.L.rope_dims / 2;

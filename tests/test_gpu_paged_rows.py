@@ -1,5 +1,5 @@
 """The paged reads row by row: table entries that name no page whatever number they hold, value scales of 0 beside
-small ones, and rows that are NaN only where they themselves see a position without a page."""
+small ones, rows that are NaN only where they themselves see a position without a page, and chunks cut along their keys."""
 import numpy as np
 import pytest
 
@@ -104,3 +104,41 @@ def test_only_rows_that_see_a_missing_page(m, n_q, n_kv, D, window, start, rows,
     assert np.isnan(got[sees]).all()
     assert np.array_equal(got[~sees], want[~sees])
     check(layer, gpu, tables, q, w, got, [(int(t), 0, int(pos[t])) for t in np.flatnonzero(~sees)[::9]], True)
+
+
+@pytest.mark.parametrize("n_q,n_kv,D,kind,copies", [(8, 2, 256, "i8", 1), (8, 2, 256, "e4m3", 5), (16, 1, 512, "i8", 2),
+                                                    (16, 4, 128, "e4m3", 2), (4, 1, 64, "i8", 9)])
+def test_short_chunks_cut_along_their_keys(m, n_q, n_kv, D, kind, copies):
+    """Chunks of few rows behind keys from one tile to dozens: pieces whose places lie one behind the other, more than
+    there are places for (5 and 9 copies) or fewer."""
+    layer = spec(n_q, n_kv, D)
+    lens = [40, 2600, 90, 1500, 130, 700, 300, 200] * copies
+    rows = [10, 33, 9, 12, 11, 10, 17, 10] * copies
+    gpu, tables, g = filled(m, layer, 64, kind, lens, D + copies)
+    start, off = [n - r for n, r in zip(lens, rows)], offsets(rows)
+    q, w = ask(g, layer, int(off[-1]), 3.0)
+    r = Read(m, layer, gpu, tables, start, rows, q, w, True, off)
+    got = r.run()
+    assert r.status() == 0 and np.array_equal(got, r.run())
+    at = [(int(off[s]) + t, s, start[s] + t) for s in range(len(lens)) for t in (0, rows[s] - 1)]
+    check(layer, gpu, tables, q, w, got, at if copies < 3 else at[::3], True)
+
+
+def test_one_workspace_for_a_chunked_prompt(m):
+    """Chunks of 500 rows and the rest, all in the workspace of the first."""
+    layer = spec(8, 2, 256)
+    total, most = 1064, 500
+    gpu, tables, g = filled(m, layer, 64, "i8", [total], 6)
+    q, w = ask(g, layer, total, 3.0)
+    L, dq, dw, t = lay(m, layer), dev(q), dev(w), dev(tables)
+    need = m.attn_paged_prefill_workspace_bytes(L, gpu.cache, 1, most, most, total - 1)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out = torch.empty((total, 8, 256), dtype=torch.float32, device="cuda")
+    for at in range(0, total, most):
+        n = min(most, total - at)
+        m.attn_paged_prefill(L, gpu.cache, t, tables.shape[1], 1, dev(offsets([n])), dev(np.int32([at])), n, n,
+                             total - 1, dq[at:at + n], dw, out[at:at + n], True, None, ws, need)
+        torch.cuda.synchronize()
+        assert int(ws[:4].cpu().numpy().view(np.uint32)[0]) == 0
+    check(layer, gpu, tables, q, w, out.cpu().numpy().astype(np.float64),
+          [(p, 0, p) for p in (0, 1, 499, 500, 777, 999, 1000, 1063)], True)
