@@ -852,7 +852,7 @@ cudaError_t launch_d(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
 }  // namespace
 
 bool paged_prefill_supported(const LayerArgs& L, int max_rows_per_seq) {
-  return 128 % L.G == 0 && max_rows_per_seq * L.G > 32;
+  return 128 % L.G == 0 && max_rows_per_seq > 32 / L.G;   // (their product may pass 32 bits)
 }
 
 size_t paged_prefill_ws_bytes(const LayerArgs& L, int n_seqs, int n_rows, int max_pos, int num_sms) {

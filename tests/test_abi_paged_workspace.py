@@ -58,3 +58,11 @@ def test_a_smaller_decode_fits(m, shape):
     sizes = [(n, p) for n in (1, 2, 3, 7, 16, 64, 300, 5000) for p in (0, 1, 63, 64, 500, 511, 512, 4095, 100000)]
     got = {x: m.attn_paged_decode_workspace_bytes(lay, c, *x) for x in sizes}
     assert all(got[a] <= got[b] for a in sizes for b in sizes if a[0] <= b[0] and a[1] <= b[1])
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_rows_of_a_sequence_without_a_bound(m, shape):
+    """max_rows_per_seq may be far above the rows of the call."""
+    want = need(m, shape, 3, 500, 500, 9000)
+    for most in (1 << 20, 1 << 28, 1 << 29, 1 << 30, (1 << 31) - 1):
+        assert need(m, shape, 3, 500, most, 9000) == want
