@@ -591,7 +591,7 @@ typedef struct {
   float* v_scales;
   int32_t n_pages;
   int32_t page_tokens;   /* 16, 32, 64 or 128 */
-  int32_t n_kv_heads;    /* the layer's */
+  int32_t n_kv_heads;    /* the layer's (which has at most 65535 q heads) */
   int32_t head_dim;
   int32_t code_type;     /* KVQ_CODE_I8 or KVQ_CODE_E4M3 */
 } kvq_paged_cache;

@@ -1126,6 +1126,8 @@ kvq_status check_paged(const kvq_layer* layer, const kvq_paged_cache* cache, kvq
   if (cache->n_kv_heads != L->n_kv || cache->head_dim != L->D)
     return fail(KVQ_EINVAL, "the cache's n_kv_heads (%d) and head_dim (%d) are not the layer's (%d, %d)",
                 cache->n_kv_heads, cache->head_dim, L->n_kv, L->D);
+  // (the prep's items of a row: prep_item)
+  if (L->n_q > 65535) return fail(KVQ_EUNSUPPORTED, "n_q_heads %d of a paged layer exceeds 65535", L->n_q);
   return KVQ_OK;
 }
 
