@@ -1131,6 +1131,16 @@ kvq_status check_paged(const kvq_layer* layer, const kvq_paged_cache* cache, kvq
   return KVQ_OK;
 }
 
+// The row kernel cuts (group of rows, kv head, key tile) places into shares in
+// 64 bits times the CTAs, and counts a group's in 32: groups of one row at
+// least, tiles of 64 positions at least, two places more for where they begin and for the group.
+bool paged_places_ok(const kvq::LayerArgs& L, int n_seqs, int n_rows, int max_pos) {
+  long long keys = (long long)max_pos + 1;
+  if (L.window > 0) keys = std::min<long long>(keys, (long long)L.window + 16);
+  const long long places = (keys / 64 + 3) * L.n_kv;
+  return places < (1ll << 31) && places <= (1ll << 52) / ((long long)n_rows + n_seqs);
+}
+
 kvq_status check_paged_rows(const int32_t* tables, int32_t max_pages, int32_t n_seqs, const int32_t* row_offsets,
                             const int32_t* start_pos, int32_t n_rows, int32_t max_pos, kvq::PagedArgs* pg,
                             kvq::PagedRows* r) {
@@ -1159,6 +1169,9 @@ kvq_status paged_read(bool window, const kvq_layer* layer, const kvq_paged_cache
   if (n_rows >= (1 << 24) || n_seqs >= (1 << 24)) return fail(KVQ_EINVAL, "n_rows or n_seqs not below 2^24");
   if ((st = check_paged_rows(tables, max_pages, n_seqs, row_offsets, pos, n_rows, max_pos, &a.pg, &a.r)) != KVQ_OK)
     return st;
+  if (!paged_places_ok(a.L, n_seqs, n_rows, max_pos))
+    return fail(KVQ_EUNSUPPORTED, "%d rows of %d kv heads at positions up to %d are too many for one call", n_rows,
+                a.L.n_kv, max_pos);
   if (window) {
     REQUIRE_PTR(row_offsets, "row_offsets", 4);
     if (max_rows_per_seq < 1) return fail(KVQ_EINVAL, "max_rows_per_seq < 1");
@@ -1312,6 +1325,7 @@ size_t attn_paged_decode_workspace_bytes(const kvq_layer* layer, const kvq_paged
   kvq::LayerArgs L;
   kvq::PagedArgs pg;
   if (check_paged(layer, cache, &L, &pg) != KVQ_OK || n_seqs < 0 || n_seqs >= (1 << 24) || !max_pos_ok(max_pos)) return 0;
+  if (n_seqs > 0 && !paged_places_ok(L, n_seqs, n_seqs, max_pos)) return 0;
   return kvq::paged_decode_ws_bytes(L, n_seqs, n_seqs, max_pos, num_sms_current());
 }
 
@@ -1331,6 +1345,7 @@ size_t attn_paged_prefill_workspace_bytes(const kvq_layer* layer, const kvq_page
   if (check_paged(layer, cache, &L, &pg) != KVQ_OK || n_seqs < 0 || n_seqs >= (1 << 24) || n_rows < 0 ||
       n_rows >= (1 << 24) || max_rows_per_seq < 0 || !max_pos_ok(max_pos))
     return 0;
+  if (n_rows > 0 && !paged_places_ok(L, n_seqs, n_rows, max_pos)) return 0;
   // (a call of fewer rows than it asked for may take either path)
   const size_t rows = kvq::paged_decode_ws_bytes(L, n_seqs, n_rows, max_pos, num_sms_current());
   if (!kvq::paged_prefill_supported(L, max_rows_per_seq)) return rows;
