@@ -41,9 +41,9 @@
 // spent a third of the instructions on addresses and bounds.)
 //
 // What bounds it, measured on GB300: 64 ragged sequences of up to 16,000 keys, 32 q
-// heads on 8 of 128, e4m3 (577 MB): 112 us with prep and merge, 86 of them the walk
+// heads on 8 of 128, e4m3 (577 MB): 113 us with prep and merge, 86 of them the walk
 // at the copy rate, 5 until the first tile is there, 9 until the last CTA ends;
-// 8 x 32,700 keys, 16 q heads on one of 512, int8 (268 MB): 68 us, the walk 46 (0.87 of
+// 8 x 32,700 keys, 16 q heads on one of 512, int8 (268 MB): 69 us, the walk 46 (0.87 of
 // the copy rate), the prep before it 7, results and merge 9.  Rings of K and V
 // apart, q in shared memory at D 128 and a fourth CTA per SM gained nothing.
 #include <algorithm>

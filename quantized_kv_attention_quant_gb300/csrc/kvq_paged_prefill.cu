@@ -783,8 +783,10 @@ PfPlan pf_plan(const LayerArgs& L, int n_seqs, int n_rows, int max_pos, int num_
   static const int32_t some = 0;
   p.n_groups = paged_groups(PagedRows{&some, nullptr, n_seqs, n_rows}, p.TQ);
   p.units = (long long)p.n_groups * L.n_kv * S::NSPLIT;
-  // as many pieces as fill the GPU once (one pair per two SMs), of at least two tiles; units of ragged
-  // batches that are more than the rows need get places for pieces that fill it twice
+  // as many pieces as fill the GPU once (one pair per two SMs), of at least two tiles; where the units are
+  // more than their rows would fill, as many as fit places for twice the pairs (once: 2 chunks of 40 rows
+  // behind 16,000 keys with 3 behind 2,000, 32q/8kv D 128, 202 us for 101; 32 windows of 32 rows, 8q/2kv
+  // D 256, window 512, 32 for 51)
   long long keys = (long long)max_pos + 1;
   if (L.window > 0) keys = std::min<long long>(keys, (long long)L.window + p.TQ);
   const long long tiles = (keys + S::KT - 1) / S::KT;
@@ -851,6 +853,21 @@ cudaError_t launch_d(const PagedReadArgs& a, const RopeFreqs& f, int max_pos, vo
 
 }  // namespace
 
+// The rows of a call go to one kernel, by those of its longest sequence.  32 (token, head) rows, two units
+// of the row kernel, for which it walks the keys twice, is where the two cross at the latest when the GPU is
+// full: us a call of this kernel / the row kernel, 64 sequences behind 4000 keys (one behind 16,000):
+//   (token, head) rows        16             32             64             128            256
+//   D 64, 8q/2kv      125 / 35       113 / 58       115 / 98       116 / 181      117 / 410
+//                    (28 / 13)      (30 / 14)      (31 / 17)      (33 / 20)      (34 / 27)
+//   D 128, 32q/8kv    401 / 143      393 / 238      401 / 425      410 / 792      436 / 1513
+//                    (39 / 23)      (40 / 27)      (41 / 36)      (43 / 59)      (46 / 104)
+//   D 256, 8q/2kv     124 / 86       125 / 149      130 / 254      130 / 443      138 / 817
+//                    (32 / 18)      (33 / 22)      (34 / 27)      (37 / 38)      (40 / 61)
+//   D 512, 16q/1kv    208 / 93       210 / 149      214 / 261      222 / 472      234 / 796
+//                    (44 / 21)      (46 / 24)      (48 / 31)      (52 / 39)      (49 / 60)
+//   D 256, window 512, 32 sequences: 34 / 30   36 / 41   40 / 62   51 / 100   32 / 131
+// G = 3, 5, 6, .. rows of a token do not divide a row tile, whose places are formed by shifts: such layers
+// take the row kernel at any length (6374 prompt rows of 24q/8kv D 128 1170 us, of 32q/8kv 206 here).
 bool paged_prefill_supported(const LayerArgs& L, int max_rows_per_seq) {
   return 128 % L.G == 0 && max_rows_per_seq > 32 / L.G;   // (their product may pass 32 bits)
 }

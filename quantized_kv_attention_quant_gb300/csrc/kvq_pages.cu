@@ -313,7 +313,7 @@ struct CopyPlan {
 };
 
 // Runs of the page pairs, a warp each; `renumber`: also the tables, by the
-// pages' new numbers.  `back`: pair k's source is src[n - 1 - k].
+// pages' new numbers, and pair k's source is src[n - 1 - k].
 __global__ void __launch_bounds__(256)
 pages_copy_kernel(const PoolArgs p, const __grid_constant__ CopyPlan plan, const PagesWs w, const int renumber) {
   pdl_wait();
